@@ -474,6 +474,64 @@ moe_status_t moe_forward_host_stream(const moe_bf16 *X_host, moe_bf16 *Y_host, i
                                      int renorm, void *ws, size_t ws_bytes, void *stream,
                                      void *h2d_stream, void *d2h_stream);
 
+/* ---- The rest of a feed-forward sub-block around the layer: the norm in front
+ * of it, the residual dropout behind it, and a dense gated feed-forward block
+ * beside (a shared expert) or instead of it. Element types of these calls: */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype_t;
+
+/* Layer norm of the rows of x [T,d] (row stride ldx >= d elements; any
+ * alignment of a whole element):
+ *   y[t,c] = gamma[c] (x[t,c] - m) r + beta[c],  m = mean of x[t,:],
+ *   r = 1 / sqrt(var + eps), var the mean of (x[t,c] - m)^2
+ * gamma, beta [d] of wtype (x's type or MOE_DTYPE_F32) or NULL (1 and 0); y [T,d]
+ * of x's type, row stride ldy; mean, rstd [T] fp32 or NULL (the backward takes
+ * them). Statistics and arithmetic in fp32, y rounded once. y may be x (same
+ * stride). T >= 0 (0: nothing is enqueued), d >= 1, eps >= 0. One kernel. */
+moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma,
+                                   const void *beta, int64_t T, int d, float eps,
+                                   moe_dtype_t type, moe_dtype_t wtype, void *y, int64_t ldy,
+                                   float *mean, float *rstd, void *stream);
+
+/* Its backward: with xh = (x - m) r and g = gamma dy,
+ *   dx     = r (g - mean(g) - xh mean(g xh))  [+ dres]     per row, rounded once
+ *   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+ * dy, x, dx [T,d] of `type` with their row strides; dres [T,d] or NULL: a gradient
+ * that reaches x by another branch (the residual), added to dx. dx may be dy or
+ * dres. dgamma, dbeta [d] of wtype, each may be NULL; summed in fp32 in a fixed
+ * order (deterministic), 0 for T = 0. scratch: moe_layernorm_scratch_bytes(T, d)
+ * bytes, 256-byte aligned, needed with dgamma or dbeta; its content on entry does
+ * not matter. Two kernels (one without dgamma and dbeta; d > 8192: one more). */
+size_t moe_layernorm_scratch_bytes(int64_t T, int d);
+moe_status_t moe_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                    const void *gamma, const float *mean, const float *rstd,
+                                    const void *dres, int64_t lddres, int64_t T, int d,
+                                    moe_dtype_t type, moe_dtype_t wtype, void *dx, int64_t lddx,
+                                    void *dgamma, void *dbeta, void *scratch,
+                                    size_t scratch_bytes, void *stream);
+
+/* Residual dropout: y = residual + (kept ? x * 65536 / (65536 - thr) : 0) with
+ * thr = floor(65536 p + 0.5), so p is taken to a multiple of 2^-16 and the
+ * scaling is the inverse of that; residual NULL: no sum. Element i = t * d + c
+ * (whatever the row strides) is kept where 16 bits of the counter-based generator
+ * Philox 4x32-10 (Salmon et al., SC11), key = seed, counter words (i / 8, offset)
+ * low words first, are >= thr: the half (i % 2, low first) of output word
+ * (i % 8) / 2. The same seed and offset give the same mask for every type and
+ * layout; calls that are to differ take another offset. offset_dev: a device
+ * counter that the kernel adds to `offset`, or NULL (a captured graph draws anew
+ * in each replay when the caller advances it). The mask is stored nowhere: the
+ * backward draws it again. x, residual, y [T,d] of `type`, row strides in
+ * elements; y may be x or residual. A dropped element does not read into y
+ * whatever x holds (infinities and NaN too). T >= 0, 0 <= p <= 1. One kernel. */
+moe_status_t moe_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                         int64_t T, int d, double p, uint64_t seed, uint64_t offset,
+                         const uint64_t *offset_dev, moe_dtype_t type, void *y, int64_t ldy,
+                         void *stream);
+/* dx = kept ? dy * 65536 / (65536 - thr) : 0 for the same p, seed and offset (the
+ * residual's gradient is dy itself). dx may be dy. One kernel. */
+moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d, double p,
+                                  uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
+                                  moe_dtype_t type, void *dx, int64_t lddx, void *stream);
+
 /* Failure-detection self-test: enqueues one CTA that waits, through the same
  * bounded wait as the GEMM pipelines, on a barrier nothing arrives at. After
  * the wait limit (about 1 s) it sets MOE_DEVERR_TIMEOUT in the workspace's

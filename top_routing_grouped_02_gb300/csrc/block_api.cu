@@ -1,0 +1,130 @@
+// C ABI of the sub-block operators around the layer (layer norm, residual
+// dropout): argument checks and launches. Errors are returned before anything
+// is enqueued.
+#include <math.h>
+
+#include "common.cuh"
+
+using namespace moe;
+
+namespace {
+
+bool valid_type(moe_dtype_t t) {
+    return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F16 || t == MOE_DTYPE_F32;
+}
+int size_of(moe_dtype_t t) { return t == MOE_DTYPE_F32 ? 4 : 2; }
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
+moe_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// A [T,d] matrix of the operators: whole elements, rows that do not overlap, and
+// offsets that 64 bits hold.
+moe_status_t check_matrix(const void *p, int64_t ld, int64_t T, int d, moe_dtype_t t) {
+    if (p == nullptr || !aligned(p, size_of(t))) return MOE_ERR_INVALID_ARG;
+    if (ld < d && T > 1) return MOE_ERR_INVALID_ARG;
+    if (T > 1 && ld > (1ll << 58) / T) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+moe_status_t check_shape(int64_t T, int d, moe_dtype_t t) {
+    if (T < 0 || d < 1 || !valid_type(t)) return MOE_ERR_INVALID_ARG;
+    if (T > (1ll << 58) / d) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+moe_status_t drop(const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t T, int d,
+                  double p, uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
+                  moe_dtype_t type, void *y, int64_t ldy, void *stream) {
+    moe_status_t st = check_shape(T, d, type);
+    if (st != MOE_OK) return st;
+    if (!(p >= 0.0 && p <= 1.0) || !aligned(offset_dev, 8)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
+    if ((st = check_matrix(y, ldy, T, d, type)) != MOE_OK) return st;
+    if (res != nullptr && (st = check_matrix(res, ldr, T, d, type)) != MOE_OK) return st;
+    if ((st = check_arch()) != MOE_OK) return st;
+    const uint32_t thr = (uint32_t)floor(p * 65536.0 + 0.5);
+    return from_cuda(launch_dropout(x, ldx, res, ldr, y, ldy, T, d, thr, seed, offset, offset_dev,
+                                    type, as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma,
+                                   const void *beta, int64_t T, int d, float eps,
+                                   moe_dtype_t type, moe_dtype_t wtype, void *y, int64_t ldy,
+                                   float *mean, float *rstd, void *stream) {
+    moe_status_t st = check_shape(T, d, type);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.f) || (wtype != type && wtype != MOE_DTYPE_F32)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(gamma, size_of(wtype)) || !aligned(beta, size_of(wtype)) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
+    if ((st = check_matrix(y, ldy, T, d, type)) != MOE_OK) return st;
+    if (x == y && ldx != ldy && T > 1) return MOE_ERR_INVALID_ARG;
+    if ((st = check_arch()) != MOE_OK) return st;
+    return from_cuda(launch_layernorm_forward(x, ldx, gamma, beta, y, ldy, mean, rstd, T, d, eps,
+                                              type, wtype == MOE_DTYPE_F32, as_stream(stream)));
+}
+
+size_t moe_layernorm_scratch_bytes(int64_t T, int d) {
+    if (T < 0 || d < 1) return 0;
+    return ((size_t)ln_partials(T) * 2 * (size_t)d * sizeof(float) + 255) / 256 * 256;
+}
+
+moe_status_t moe_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                    const void *gamma, const float *mean, const float *rstd,
+                                    const void *dres, int64_t lddres, int64_t T, int d,
+                                    moe_dtype_t type, moe_dtype_t wtype, void *dx, int64_t lddx,
+                                    void *dgamma, void *dbeta, void *scratch,
+                                    size_t scratch_bytes, void *stream) {
+    moe_status_t st = check_shape(T, d, type);
+    if (st != MOE_OK) return st;
+    if (wtype != type && wtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+    const int ws = size_of(wtype);
+    if (!aligned(gamma, ws) || !aligned(dgamma, ws) || !aligned(dbeta, ws))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (mean == nullptr || rstd == nullptr || !aligned(mean, 4) || !aligned(rstd, 4))
+            return MOE_ERR_INVALID_ARG;
+        if ((st = check_matrix(dy, lddy, T, d, type)) != MOE_OK) return st;
+        if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
+        if ((st = check_matrix(dx, lddx, T, d, type)) != MOE_OK) return st;
+        if (dres != nullptr && (st = check_matrix(dres, lddres, T, d, type)) != MOE_OK) return st;
+        if (dgamma != nullptr || dbeta != nullptr) {
+            if (scratch == nullptr || !aligned(scratch, 256)) return MOE_ERR_INVALID_ARG;
+            if (scratch_bytes < moe_layernorm_scratch_bytes(T, d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+        }
+    }
+    if ((st = check_arch()) != MOE_OK) return st;
+    if (T == 0) {  // sums over no rows
+        cudaError_t e = cudaSuccess;
+        if (dgamma != nullptr) e = cudaMemsetAsync(dgamma, 0, (size_t)d * ws, as_stream(stream));
+        if (e == cudaSuccess && dbeta != nullptr)
+            e = cudaMemsetAsync(dbeta, 0, (size_t)d * ws, as_stream(stream));
+        return from_cuda(e);
+    }
+    return from_cuda(launch_layernorm_backward(dy, lddy, x, ldx, gamma, mean, rstd, dres, lddres,
+                                               dx, lddx, dgamma, dbeta, T, d, type,
+                                               wtype == MOE_DTYPE_F32,
+                                               static_cast<float *>(scratch), as_stream(stream)));
+}
+
+moe_status_t moe_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                         int64_t T, int d, double p, uint64_t seed, uint64_t offset,
+                         const uint64_t *offset_dev, moe_dtype_t type, void *y, int64_t ldy,
+                         void *stream) {
+    return drop(x, ldx, residual, ldr, T, d, p, seed, offset, offset_dev, type, y, ldy, stream);
+}
+
+moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d, double p,
+                                  uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
+                                  moe_dtype_t type, void *dx, int64_t lddx, void *stream) {
+    return drop(dy, lddy, nullptr, 0, T, d, p, seed, offset, offset_dev, type, dx, lddx, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,619 @@
+// Layer norm, forward and backward.
+//
+//   y = gamma (x - m) r + beta,  m = mean of the row, r = 1 / sqrt(var + eps)
+//   g = gamma dy,  xh = (x - m) r
+//   dx = r (g - mean(g) - xh mean(g xh))  (+ dres)
+//   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+//
+// Both are bound by HBM: the forward reads x and writes y once, the backward
+// reads x, dy (and dres) and writes dx once. A row lives in the registers of a
+// group of warps (8 elements a thread, 4 or 8 in 32 bits), so nothing is read
+// twice. The groups loop over rows with a stride and fetch the next row before
+// they work on the current one. Row statistics: each warp takes the mean and
+// the squared deviations from its own mean of its elements, and the warps'
+// pairs are joined by
+//   m = sum n_w m_w / d,  M2 = sum (M2_w + n_w (m_w - m)^2),
+// one exchange through shared memory a row, with no subtraction of large equal
+// numbers: a row whose offset is far larger than its spread keeps its variance.
+//
+// Weight gradients: each thread owns its columns and sums them over the rows of
+// its group in fp32 registers; the groups of a block are added in a fixed order
+// through shared memory, each block writes one partial row per array, and a
+// second kernel adds the blocks' partials in a fixed order. No atomics: the
+// result does not depend on timing.
+//
+// Rows too wide for the registers (see reg_width) take kernels that read the
+// row again from L2 for each pass.
+#include <algorithm>
+
+#include "common.cuh"
+#include "elem.cuh"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+struct LnArgs {
+    const void *x, *gamma, *beta;
+    void *y;
+    float *mean, *rstd;
+    int64_t ldx, ldy;
+    int64_t T;
+    int d;
+    int w32;  // gamma, beta (and their gradients) are fp32, else x's type
+    float eps;
+    int wpr;  // warps per row
+    // backward
+    const void *dy, *dres;
+    void *dx;
+    int64_t lddy, lddres, lddx;
+    float *part;       // [blocks][2][d] partial sums (dgamma, dbeta), or NULL
+};
+
+template <typename T>
+__device__ __forceinline__ float load_w(const void *w, int w32, int c, float none) {
+    if (w == nullptr) return none;
+    return w32 ? static_cast<const float *>(w)[c] : load_f32(static_cast<const T *>(w) + c);
+}
+
+// Elements of a row that warp w of `tpr` threads holds.
+template <int V, int NV>
+__device__ __forceinline__ int warp_count(int w, int nvec, int tpr) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) n += min(max(nvec - (i * tpr + w * 32), 0), 32);
+    return n * V;
+}
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(1024, 1) ln_forward_kernel(const LnArgs a) {
+    __shared__ float2 sh[2][32];
+    pdl_wait();
+    pdl_trigger();
+    constexpr int EPT = V * NV;
+    const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+    const int w0 = group * a.wpr, wg = warp - w0;
+    const int groups = blockDim.x / tpr;
+    const int nvec = a.d / V;
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    if (row >= a.T) return;
+
+    bool ok[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
+    Raw<T, V> cur[NV];
+    auto fetch = [&](int64_t r, Raw<T, V>(&v)[NV]) {
+        const T *p = static_cast<const T *>(a.x) + r * a.ldx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) v[i] = reinterpret_cast<const Raw<T, V> *>(p)[i * tpr + t];
+    };
+    fetch(row, cur);
+    float gm[EPT], bt[EPT];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (i * tpr + t) * V + j;
+            gm[i * V + j] = ok[i] ? load_w<T>(a.gamma, a.w32, c, 1.f) : 0.f;
+            bt[i * V + j] = ok[i] ? load_w<T>(a.beta, a.w32, c, 0.f) : 0.f;
+        }
+    const float inv_d = 1.f / (float)a.d;
+    const int n_own = warp_count<V, NV>(wg, nvec, tpr);
+    const float inv_own = n_own > 0 ? 1.f / (float)n_own : 0.f;
+    const float n_lane = lane < a.wpr ? (float)warp_count<V, NV>(lane, nvec, tpr) : 0.f;
+
+    for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
+        float f[EPT];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (ok[i]) {
+                to_f32<T, V>(cur[i], f + i * V);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[i * V + j] = 0.f;
+            }
+        }
+        if (row + stride < a.T) fetch(row + stride, cur);
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) s += f[e];
+        float mean = warp_sum(s) * inv_own;
+        float m2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float c = f[i * V + j] - mean;
+                    m2 = fmaf(c, c, m2);
+                }
+            }
+        m2 = warp_sum(m2);
+        if (a.wpr > 1) {
+            if (lane == 0) sh[buf][warp] = make_float2(mean, m2);
+            group_sync(1 + group, tpr);
+            const float2 o = lane < a.wpr ? sh[buf][w0 + lane] : make_float2(0.f, 0.f);
+            mean = warp_sum(n_lane * o.x) * inv_d;
+            const float c = o.x - mean;
+            m2 = warp_sum(lane < a.wpr && n_lane > 0.f ? fmaf(n_lane * c, c, o.y) : 0.f);
+        }
+        const float rstd = __frsqrt_rn(fmaf(m2, inv_d, a.eps));
+        T *yp = static_cast<T *>(a.y) + row * a.ldy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+                float o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    o[j] = fmaf((f[i * V + j] - mean) * rstd, gm[i * V + j], bt[i * V + j]);
+                reinterpret_cast<Raw<T, V> *>(yp)[i * tpr + t] = from_f32<T, V>(o);
+            }
+        if (t == 0) {
+            if (a.mean != nullptr) a.mean[row] = mean;
+            if (a.rstd != nullptr) a.rstd[row] = rstd;
+        }
+    }
+}
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(1024, 1) ln_backward_kernel(const LnArgs a) {
+    extern __shared__ float acc_sh[];  // [2][d], used when a block has several groups
+    __shared__ float2 sh[2][32];
+    pdl_wait();
+    pdl_trigger();
+    constexpr int EPT = V * NV;
+    const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+    const int w0 = group * a.wpr;
+    const int groups = blockDim.x / tpr;
+    const int nvec = a.d / V;
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+
+    bool ok[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
+    Raw<T, V> xr[NV], yr[NV], rr[NV];
+    float m_next = 0.f, r_next = 0.f;
+    const bool has_res = a.dres != nullptr;
+    auto fetch = [&](int64_t r) {
+        const T *px = static_cast<const T *>(a.x) + r * a.ldx;
+        const T *py = static_cast<const T *>(a.dy) + r * a.lddy;
+        const T *pr = static_cast<const T *>(a.dres) + r * a.lddres;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+                xr[i] = reinterpret_cast<const Raw<T, V> *>(px)[i * tpr + t];
+                yr[i] = reinterpret_cast<const Raw<T, V> *>(py)[i * tpr + t];
+                if (has_res) rr[i] = reinterpret_cast<const Raw<T, V> *>(pr)[i * tpr + t];
+            }
+        m_next = a.mean[r];
+        r_next = a.rstd[r];
+    };
+    if (row < a.T) fetch(row);
+    float gm[EPT], dg[EPT], db[EPT];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (i * tpr + t) * V + j;
+            gm[i * V + j] = ok[i] ? load_w<T>(a.gamma, a.w32, c, 1.f) : 0.f;
+            dg[i * V + j] = db[i * V + j] = 0.f;
+        }
+    const float inv_d = 1.f / (float)a.d;
+
+    for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
+        const float mean = m_next, rstd = r_next;
+        float xh[EPT], g[EPT];
+        Raw<T, V> res[NV];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (has_res) res[i] = rr[i];
+            if (ok[i]) {
+                to_f32<T, V>(xr[i], xh + i * V);
+                to_f32<T, V>(yr[i], g + i * V);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int e = i * V + j;
+                    xh[e] = (xh[e] - mean) * rstd;
+                    db[e] += g[e];
+                    dg[e] = fmaf(g[e], xh[e], dg[e]);
+                    g[e] *= gm[e];
+                    s2 += g[e];
+                    s1 = fmaf(g[e], xh[e], s1);
+                }
+            }
+        }
+        if (row + stride < a.T) fetch(row + stride);
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (a.wpr > 1) {
+            if (lane == 0) sh[buf][warp] = make_float2(s1, s2);
+            group_sync(1 + group, tpr);
+            const float2 o = lane < a.wpr ? sh[buf][w0 + lane] : make_float2(0.f, 0.f);
+            s1 = warp_sum(o.x);
+            s2 = warp_sum(o.y);
+        }
+        const float c1 = s1 * inv_d, c2 = s2 * inv_d;
+        T *px = static_cast<T *>(a.dx) + row * a.lddx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+                float o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    o[j] = rstd * (fmaf(-c1, xh[i * V + j], g[i * V + j]) - c2);
+                if (has_res) {
+                    float q[V];
+                    to_f32<T, V>(res[i], q);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] += q[j];
+                }
+                reinterpret_cast<Raw<T, V> *>(px)[i * tpr + t] = from_f32<T, V>(o);
+            }
+    }
+    if (a.part == nullptr) return;
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+    if (groups == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i])
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int c = (i * tpr + t) * V + j;
+                    part[c] = dg[i * V + j];
+                    part[a.d + c] = db[i * V + j];
+                }
+        return;
+    }
+    for (int k = 0; k < groups; ++k) {
+        if (group == k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (ok[i])
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int c = (i * tpr + t) * V + j;
+                        acc_sh[c] = (k ? acc_sh[c] : 0.f) + dg[i * V + j];
+                        acc_sh[a.d + c] = (k ? acc_sh[a.d + c] : 0.f) + db[i * V + j];
+                    }
+        }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) part[c] = acc_sh[c];
+}
+
+// dgamma[c], dbeta[c] = the sum of P partial rows, each thread row q of the block
+// adding rows q, q + 8, ... and thread row 0 the eight sums, in that order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ln_weight_reduce_kernel(const float *__restrict__ part, int P, int d, int w32, void *dgamma,
+                        void *dbeta) {
+    __shared__ float sh[8][33];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < 2 * (int64_t)d) {
+        const float *p = part + c;
+#pragma unroll 8
+        for (int k = q; k < P; k += 8) s += p[(int64_t)k * 2 * d];
+    }
+    sh[q][lane] = s;
+    __syncthreads();
+    if (q != 0 || c >= 2 * (int64_t)d) return;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += sh[k][lane];
+    void *out = c < d ? dgamma : dbeta;
+    if (out == nullptr) return;
+    const int64_t i = c < d ? c : c - d;
+    if (w32) static_cast<float *>(out)[i] = s;
+    else store_f32(static_cast<T *>(out) + i, s);
+}
+
+// ---- rows too wide for the registers ----------------------------------------
+
+// Sum over the block, in a fixed order.
+__device__ __forceinline__ float block_sum(float v, float *sh) {
+    v = warp_sum(v);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) sh[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < (int)(blockDim.x >> 5) ? sh[lane] : 0.f);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) ln_forward_wide_kernel(const LnArgs a) {
+    __shared__ float sh[32];
+    pdl_wait();
+    pdl_trigger();
+    const int nvec = a.d / V;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const Raw<T, V> *xp =
+            reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.x) + row * a.ldx);
+        Raw<T, V> *yp = reinterpret_cast<Raw<T, V> *>(static_cast<T *>(a.y) + row * a.ldy);
+        float s = 0.f, f[V];
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            to_f32<T, V>(xp[v], f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s += f[j];
+        }
+        const float mean = block_sum(s, sh) / (float)a.d;
+        s = 0.f;
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            to_f32<T, V>(xp[v], f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s = fmaf(f[j] - mean, f[j] - mean, s);
+        }
+        const float rstd = __frsqrt_rn(block_sum(s, sh) / (float)a.d + a.eps);
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            to_f32<T, V>(xp[v], f);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                f[j] = fmaf((f[j] - mean) * rstd, load_w<T>(a.gamma, a.w32, v * V + j, 1.f),
+                            load_w<T>(a.beta, a.w32, v * V + j, 0.f));
+            yp[v] = from_f32<T, V>(f);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean != nullptr) a.mean[row] = mean;
+            if (a.rstd != nullptr) a.rstd[row] = rstd;
+        }
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) ln_backward_wide_kernel(const LnArgs a) {
+    __shared__ float sh[32];
+    pdl_wait();
+    pdl_trigger();
+    const int nvec = a.d / V;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const Raw<T, V> *xp =
+            reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.x) + row * a.ldx);
+        const Raw<T, V> *yp =
+            reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.dy) + row * a.lddy);
+        const Raw<T, V> *rp =
+            reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.dres) + row * a.lddres);
+        Raw<T, V> *op = reinterpret_cast<Raw<T, V> *>(static_cast<T *>(a.dx) + row * a.lddx);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float s1 = 0.f, s2 = 0.f, x[V], g[V];
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            to_f32<T, V>(xp[v], x);
+            to_f32<T, V>(yp[v], g);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float gj = g[j] * load_w<T>(a.gamma, a.w32, v * V + j, 1.f);
+                s2 += gj;
+                s1 = fmaf(gj, (x[j] - mean) * rstd, s1);
+            }
+        }
+        const float c1 = block_sum(s1, sh) / (float)a.d;
+        const float c2 = block_sum(s2, sh) / (float)a.d;
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            to_f32<T, V>(xp[v], x);
+            to_f32<T, V>(yp[v], g);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float gj = g[j] * load_w<T>(a.gamma, a.w32, v * V + j, 1.f);
+                x[j] = rstd * (fmaf(-c1, (x[j] - mean) * rstd, gj) - c2);
+            }
+            if (a.dres != nullptr) {
+                to_f32<T, V>(rp[v], g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[j] += g[j];
+            }
+            op[v] = from_f32<T, V>(x);
+        }
+    }
+}
+
+// Partial weight gradients of a wide row: a thread per V columns, block row
+// blockIdx.y adding rows blockIdx.y, blockIdx.y + gridDim.y, ...
+template <typename T, int V>
+__global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int v = blockIdx.x * 256 + threadIdx.x;
+    if (v >= a.d / V) return;
+    float dg[V], db[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) dg[j] = db[j] = 0.f;
+    for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
+        float x[V], g[V];
+        to_f32<T, V>(reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.x) + row * a.ldx)[v], x);
+        to_f32<T, V>(reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.dy) + row * a.lddy)[v], g);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            db[j] += g[j];
+            dg[j] = fmaf(g[j], (x[j] - mean) * rstd, dg[j]);
+        }
+    }
+    float *part = a.part + (int64_t)blockIdx.y * 2 * a.d;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        part[v * V + j] = dg[j];
+        part[a.d + v * V + j] = db[j];
+    }
+}
+
+// ------------------------------------------------------------ host side --
+
+// Widest row of the register kernels: 32 warps of 8 elements a thread.
+constexpr int kRegWidth = 8192;
+// Threads of a backward block: as many row groups as fit, so that there is one
+// partial row of weight gradients per SM.
+constexpr int kBwdThreads = 1024;
+
+// Vector length (elements) that divides d and every row stride and suits the
+// pointers' alignment.
+struct Align {
+    uint64_t bits = 0;
+    void add(const void *p, int64_t ld, int d, int esize, int64_t T) {
+        if (p == nullptr) return;
+        bits |= reinterpret_cast<uintptr_t>(p) | (uint64_t)d * esize;
+        if (T > 1) bits |= (uint64_t)ld * esize;
+    }
+    bool fits(int bytes) const { return (bits & (bytes - 1)) == 0; }
+};
+
+int row_groups(int wpr, int threads) { return std::max(1, threads / (32 * wpr)); }
+
+template <typename T, int V, int NV>
+cudaError_t forward_regs(LnArgs a, cudaStream_t s) {
+    a.wpr = (a.d / V + 32 * NV - 1) / (32 * NV);
+    const int groups = row_groups(a.wpr, 256), threads = groups * a.wpr * 32;
+    const int64_t want = (a.T + groups - 1) / groups;
+    const int grid = (int)std::min<int64_t>(want, (int64_t)sm_count() * std::max(1, 1024 / threads));
+    return launch_k(ln_forward_kernel<T, V, NV>, dim3(grid), dim3(threads), 0, s, a);
+}
+
+template <typename T, int V, int NV>
+cudaError_t backward_regs(LnArgs a, int *P, cudaStream_t s) {
+    a.wpr = (a.d / V + 32 * NV - 1) / (32 * NV);
+    // at most 15 groups: each has a barrier of its own (barrier 0 is the block's)
+    int groups = row_groups(a.wpr, kBwdThreads);
+    if (a.wpr > 1) groups = std::min(groups, 15);
+    groups = (int)std::min<int64_t>(groups, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
+    const int threads = groups * a.wpr * 32;
+    const int64_t want = (a.T + groups - 1) / groups;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count()));
+    *P = grid;
+    const size_t smem = groups > 1 && a.part != nullptr ? (size_t)2 * a.d * sizeof(float) : 0;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = ensure_dynamic_smem(
+            reinterpret_cast<const void *>(ln_backward_kernel<T, V, NV>), (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_k(ln_backward_kernel<T, V, NV>, dim3(grid), dim3(threads), smem, s, a);
+}
+
+template <typename T>
+cudaError_t forward_type(const LnArgs &a, const Align &al, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);  // elements of a 16-byte vector
+    if (a.d > kRegWidth) {
+        const int grid = (int)std::min<int64_t>(a.T, 2 * sm_count());
+        return al.fits(16) ? launch_k(ln_forward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
+                           : launch_k(ln_forward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
+    }
+    if constexpr (sizeof(T) == 4) {
+        if (a.d <= kRegWidth / 2)
+            return al.fits(16) ? forward_regs<T, 4, 1>(a, s) : forward_regs<T, 1, 4>(a, s);
+        return al.fits(16) ? forward_regs<T, 4, 2>(a, s) : forward_regs<T, 1, 8>(a, s);
+    } else {
+        if (al.fits(16)) return forward_regs<T, 8, 1>(a, s);
+        return al.fits(4) ? forward_regs<T, 2, 4>(a, s) : forward_regs<T, 1, 8>(a, s);
+    }
+}
+
+template <typename T>
+cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *dbeta,
+                          cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    cudaError_t e;
+    int P = 0;
+    if (a.d > kRegWidth) {
+        const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.T, 2 * sm_count()));
+        e = al.fits(16) ? launch_k(ln_backward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
+                        : launch_k(ln_backward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
+        if (e != cudaSuccess || a.part == nullptr) return e;
+        P = ln_partials(a.T);
+        const int v = al.fits(16) ? W : 1;
+        const dim3 g((a.d / v + 255) / 256, P);
+        e = al.fits(16) ? launch_k(ln_weight_wide_kernel<T, W>, g, dim3(256), 0, s, a)
+                        : launch_k(ln_weight_wide_kernel<T, 1>, g, dim3(256), 0, s, a);
+    } else if constexpr (sizeof(T) == 4) {
+        if (a.d <= kRegWidth / 2)
+            e = al.fits(16) ? backward_regs<T, 4, 1>(a, &P, s) : backward_regs<T, 1, 4>(a, &P, s);
+        else
+            e = al.fits(16) ? backward_regs<T, 4, 2>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
+    } else {
+        if (al.fits(16)) e = backward_regs<T, 8, 1>(a, &P, s);
+        else e = al.fits(4) ? backward_regs<T, 2, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
+    }
+    if (e != cudaSuccess || a.part == nullptr) return e;
+    return launch_k(ln_weight_reduce_kernel<T>, dim3((2 * a.d + 31) / 32), dim3(256), 0, s,
+                    static_cast<const float *>(a.part), P, a.d, a.w32, dgamma, dbeta);
+}
+
+}  // namespace
+
+int ln_partials(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(T, kLnPartials)); }
+
+cudaError_t launch_layernorm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta,
+                                     void *y, int64_t ldy, float *mean, float *rstd, int64_t T,
+                                     int d, float eps, moe_dtype_t type, bool w32, cudaStream_t s) {
+    LnArgs a{};
+    a.x = x;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.T = T;
+    a.d = d;
+    a.w32 = w32;
+    a.eps = eps;
+    const int es = type == MOE_DTYPE_F32 ? 4 : 2;
+    Align al;
+    al.add(x, ldx, d, es, T);
+    al.add(y, ldy, d, es, T);
+    switch (type) {
+        case MOE_DTYPE_BF16: return forward_type<__nv_bfloat16>(a, al, s);
+        case MOE_DTYPE_F16: return forward_type<__half>(a, al, s);
+        default: return forward_type<float>(a, al, s);
+    }
+}
+
+cudaError_t launch_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                      const void *gamma, const float *mean, const float *rstd,
+                                      const void *dres, int64_t lddres, void *dx, int64_t lddx,
+                                      void *dgamma, void *dbeta, int64_t T, int d,
+                                      moe_dtype_t type, bool w32, float *part, cudaStream_t s) {
+    LnArgs a{};
+    a.x = x;
+    a.gamma = gamma;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.dy = dy;
+    a.dres = dres;
+    a.dx = dx;
+    a.ldx = ldx;
+    a.lddy = lddy;
+    a.lddres = lddres;
+    a.lddx = lddx;
+    a.T = T;
+    a.d = d;
+    a.w32 = w32;
+    a.part = dgamma != nullptr || dbeta != nullptr ? part : nullptr;
+    const int es = type == MOE_DTYPE_F32 ? 4 : 2;
+    Align al;
+    al.add(dy, lddy, d, es, T);
+    al.add(x, ldx, d, es, T);
+    al.add(dres, lddres, d, es, T);
+    al.add(dx, lddx, d, es, T);
+    switch (type) {
+        case MOE_DTYPE_BF16: return backward_type<__nv_bfloat16>(a, al, dgamma, dbeta, s);
+        case MOE_DTYPE_F16: return backward_type<__half>(a, al, dgamma, dbeta, s);
+        default: return backward_type<float>(a, al, dgamma, dbeta, s);
+    }
+}
+
+}  // namespace moe

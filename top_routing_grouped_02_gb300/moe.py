@@ -30,7 +30,9 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
 LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_gate_up": 1,
             "moe_gemm_gate_up_train": 1, "moe_backward_dh": 2, "moe_backward_dx": 2,
             "moe_backward_router": 5, "moe_backward_dw": 5,
-            "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1}
+            "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1,
+            "moe_layernorm": 1, "moe_layernorm_backward": 2, "moe_dropout": 1,
+            "moe_dropout_backward": 1}
 TILE_M = 128
 
 
@@ -45,6 +47,10 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
+_U = ctypes.c_uint64
+_F = ctypes.c_float
+_D = ctypes.c_double
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_abi_version": (_I, []),
@@ -81,6 +87,12 @@ _SIGS = {
     "moe_selftest_wait_timeout": (_I, [_P, _SZ, _P]),
     "moe_forward_host_stream": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                      _I, _P, _SZ, _P, _P, _P]),
+    "moe_layernorm_forward": (_I, [_P, _L, _P, _P, _L, _I, _F, _I, _I, _P, _L, _P, _P, _P]),
+    "moe_layernorm_scratch_bytes": (_SZ, [_L, _I]),
+    "moe_layernorm_backward": (_I, [_P, _L, _P, _L, _P, _P, _P, _P, _L, _L, _I, _I, _I, _P, _L, _P,
+                                    _P, _P, _SZ, _P]),
+    "moe_dropout": (_I, [_P, _L, _P, _L, _L, _I, _D, _U, _U, _P, _I, _P, _L, _P]),
+    "moe_dropout_backward": (_I, [_P, _L, _L, _I, _D, _U, _U, _P, _I, _P, _L, _P]),
     "moe_round_capacity": (ctypes.c_int64, [_I, _I, _I, _I]),
     "moe_round_workspace_bytes": (_SZ, [_I, _I]),
     "moe_round_routing": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
@@ -554,3 +566,141 @@ def moe_forward_rounded(X, Wr, W1, W3, W2, K: int, bias=None, renorm: bool = Tru
     else:
         _check("moe_forward_rounded", lib().moe_forward_rounded(*args))
     return Y
+
+
+# ------------------------------------- layer norm, residual dropout, dense block
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
+    """(pointer, row stride, rows, row length) of a CUDA tensor seen as a matrix of
+    rows along its last dimension: contiguous, or 2-D with unit inner stride."""
+    if not t.is_cuda or t.dtype not in _DTYPES or t.dim() < 1:
+        raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} and type {like.dtype}")
+    d = t.shape[-1]
+    if d == 0:
+        raise ValueError(f"{name} has rows of length 0")
+    if t.is_contiguous():
+        return t.data_ptr(), d, t.numel() // d, d
+    if t.dim() != 2 or (d > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < d):
+        raise ValueError(f"{name} must be contiguous or a matrix of non-overlapping rows")
+    return t.data_ptr(), t.stride(0), t.shape[0], d
+
+
+def _vec(t: torch.Tensor | None, d: int, dtypes, name: str):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dim() != 1 or t.shape[0] != d or (d > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous CUDA vector of {d}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be of type {dtypes}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _wtype(x: torch.Tensor, gamma, beta):
+    w = gamma if gamma is not None else beta
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have one type")
+    return x.dtype if w is None else w.dtype
+
+
+def moe_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False, y=None,
+                  stream=None):
+    """y = layer norm of x along its last dimension (gamma, beta: [d] of x's type or
+    fp32, or None); stats=True: (y, mean, rstd), the fp32 row statistics that the
+    backward takes."""
+    px, ldx, T, d = _rows(x, "x")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    py, ldy, _, _ = _rows(y, "y", x)
+    wt = _wtype(x, gamma, beta)
+    kinds = (x.dtype, torch.float32)
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    st = lib().moe_layernorm_forward(
+        px, ldx, _vec(gamma, d, kinds, "gamma"), _vec(beta, d, kinds, "beta"), T, d, eps,
+        _DTYPES[x.dtype], _DTYPES[wt], py, ldy, mean.data_ptr() if stats else None,
+        rstd.data_ptr() if stats else None, _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeError("moe_layernorm_forward", st)
+    return (y, mean, rstd) if stats else y
+
+
+def moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=None, wdtype=None, dx=None, scratch=None,
+                           stream=None):
+    """(dx, dgamma, dbeta) of moe_layernorm, with `dres` (the gradient that reaches
+    x by the residual branch) added to dx when given. dgamma and dbeta have gamma's
+    type, or wdtype (default fp32) without gamma."""
+    px, ldx, T, d = _rows(x, "x")
+    pdy, lddy, _, _ = _rows(dy, "dy", x)
+    pres, ldres = (None, 0) if dres is None else _rows(dres, "dres", x)[:2]
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    pdx, lddx, _, _ = _rows(dx, "dx", x)
+    wt = gamma.dtype if gamma is not None else wdtype or torch.float32
+    if wt not in (x.dtype, torch.float32):
+        raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wt}")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != T:
+            raise ValueError(f"{name} must hold {T} contiguous fp32 values")
+    grads = torch.empty((2, d), dtype=wt, device=x.device)
+    if scratch is None:
+        scratch = torch.empty(lib().moe_layernorm_scratch_bytes(T, d), dtype=torch.uint8,
+                              device=x.device)
+    st = lib().moe_layernorm_backward(
+        pdy, lddy, px, ldx, _vec(gamma, d, (x.dtype, torch.float32), "gamma"), mean.data_ptr(),
+        rstd.data_ptr(), pres, ldres, T, d, _DTYPES[x.dtype], _DTYPES[wt], pdx, lddx,
+        grads.data_ptr(), grads.data_ptr() + d * grads.element_size(), scratch.data_ptr(),
+        scratch.numel(), _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeError("moe_layernorm_backward", st)
+    return dx, grads[0], grads[1]
+
+
+def moe_dropout(x, p: float, seed: int, offset: int = 0, residual=None, offset_dev=None, y=None,
+                stream=None):
+    """residual + dropout(x): the mask is a function of (seed, offset, element), see
+    moe.h; offset_dev: a one-element int64 CUDA tensor added to offset."""
+    px, ldx, T, d = _rows(x, "x")
+    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", x)[:2]
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    py, ldy, _, _ = _rows(y, "y", x)
+    st = lib().moe_dropout(px, ldx, pr, ldr, T, d, p, seed, offset, _counter(offset_dev),
+                           _DTYPES[x.dtype], py, ldy, _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeError("moe_dropout", st)
+    return y
+
+
+def moe_dropout_backward(dy, p: float, seed: int, offset: int = 0, offset_dev=None, dx=None,
+                         stream=None):
+    """The gradient of moe_dropout with respect to x (the residual's is dy)."""
+    pdy, lddy, T, d = _rows(dy, "dy")
+    if dx is None:
+        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    pdx, lddx, _, _ = _rows(dx, "dx", dy)
+    st = lib().moe_dropout_backward(pdy, lddy, T, d, p, seed, offset, _counter(offset_dev),
+                                    _DTYPES[dy.dtype], pdx, lddx, _raw_stream(stream, dy.device))
+    if st != MOE_OK:
+        raise MoeError("moe_dropout_backward", st)
+    return dx
+
+
+def _counter(t):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != torch.int64 or t.numel() != 1:
+        raise ValueError("offset_dev must be a one-element int64 CUDA tensor")
+    return t.data_ptr()
