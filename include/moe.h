@@ -532,6 +532,51 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
                                   uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                                   moe_dtype_t type, void *dx, int64_t lddx, void *stream);
 
+/* Dense gated feed-forward block (a shared expert, or a layer without experts):
+ *   A1 = X W1, A3 = X W3, H = act(A1) * A3, Y = H W2
+ * X, Y [T,d], W1, W3 [d,n], W2 [n,d], all of `type` (MOE_DTYPE_BF16 or
+ * MOE_DTYPE_F16), dense, row-major and 16-byte aligned; d and n multiples of 8 up
+ * to 2^20, any T >= 0 (0: nothing is enqueued). Sums in fp32; H is rounded to
+ * `type` between the two products, Y once. act: */
+typedef enum {
+    MOE_ACT_SILU = 0,      /* a sigmoid(a) */
+    MOE_ACT_GELU_TANH = 1  /* 0.5 a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) */
+} moe_act_t;
+
+/* Workspace of the calls below for T tokens (train: of the backward too), 256-byte
+ * aligned; 0 for an invalid shape. Its control words (the device error word of
+ * moe_sync_check and join counters) start at zero, once before the first use
+ * (moe_ffn_workspace_init), and every call leaves the counters so. It serves any
+ * shape that needs no more bytes. Calls that overlap on the GPU need one each. */
+size_t moe_ffn_workspace_bytes(int T, int d, int n, int train);
+moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream);
+
+/* Y. Two kernels: gate and up projections, activation and product in one, the
+ * down projection in the other. Up to 128 tokens on kernels that stream the
+ * weights, each SM an equal share of them. */
+moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, const void *W2, int T,
+                             int d, int n, moe_act_t act, moe_dtype_t type, void *Y, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/* Y and what the backward takes: H [T,n] of `type` and the pre-activations A1, A3
+ * [T,n] fp32 (16-byte aligned). Two kernels. */
+moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
+                                   int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
+                                   void *H, float *A1, float *A3, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/* The gradients, with G = dY W2^T, dA1 = G A3 act'(A1), dA3 = G act(A1):
+ *   dX = dA1 W1^T + dA3 W3^T, dW1 = X^T dA1, dW3 = X^T dA3, dW2 = H^T dY
+ * all of `type`, each rounded once after an fp32 sum (dA1 and dA3 are rounded to
+ * `type` as operands). dX may be NULL; dW1, dW3 and dW2 are all given or all NULL.
+ * T = 0 gives zero weight gradients. ws: a workspace for training. Three kernels
+ * (one fewer without dX, or without the weight gradients). Deterministic. */
+moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
+                              const void *W2, const void *H, const float *A1, const float *A3,
+                              int T, int d, int n, moe_act_t act, moe_dtype_t type, void *dX,
+                              void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
+                              void *stream);
+
 /* Failure-detection self-test: enqueues one CTA that waits, through the same
  * bounded wait as the GEMM pipelines, on a barrier nothing arrives at. After
  * the wait limit (about 1 s) it sets MOE_DEVERR_TIMEOUT in the workspace's

@@ -73,3 +73,63 @@ def matrix(T, d, dtype, gen, ld=None, scale=1.0, shift=0.0, device="cuda"):
     """[T, d] view of a [T, ld] buffer of normal values."""
     v = torch.randn(max(T, 1), ld or d, generator=gen, dtype=torch.float64) * scale + shift
     return v.to(dtype).to(device)[:T, :d]
+
+
+def _act(a, act):
+    """The activation, its derivative (64 bits)."""
+    if act == "silu":
+        sg = torch.sigmoid(a)
+        return a * sg, sg * (1 + a * (1 - sg))
+    c = math.sqrt(2 / math.pi)
+    t = torch.tanh(c * (a + 0.044715 * a ** 3))
+    return 0.5 * a * (1 + t), 0.5 * (1 + t) + 0.5 * a * (1 - t * t) * c * (1 + 3 * 0.044715 * a * a)
+
+
+def ffn(x, W1, W3, W2, act, dY=None):
+    """{name: (value, slack)}: the block's outputs in 64 bits, and for each element a
+    bound on the error in front of its final rounding. Counted: one rounding (u) of
+    H, dA1 and dA3 to 16 bits, K accumulations of at most 2^-23 of the sum of
+    absolute terms each, and 2^-19 for the activation's approximate exponential and
+    division. |act'| <= 1.2 and |act''| <= 1.2."""
+    u, e32 = HALF[x.dtype], 2.0 ** -23
+    x, W1, W3, W2 = (t.double() for t in (x, W1, W3, W2))
+    d, n = W1.shape
+    a1, a3 = x @ W1, x @ W3
+    e1, e3 = (d * e32 * (x.abs() @ w.abs()) for w in (W1, W3))
+    f, df = _act(a1, act)
+    H = f * a3
+    eH = 1.2 * e1 * (a3.abs() + e3) + f.abs() * e3 + 2.0 ** -19 * H.abs()
+    eH = eH + u * (H.abs() + eH)
+    out = {"Y": (H @ W2, eH @ W2.abs() + n * e32 * ((H.abs() + eH) @ W2.abs()))}
+    if dY is None:
+        return out
+    dY = dY.double()
+    T = x.shape[0]
+    G, eG = dY @ W2.T, d * e32 * (dY.abs() @ W2.abs().T)
+    dA1, dA3 = G * a3 * df, G * f
+    eA1 = eG * (a3 * df).abs() + (G.abs() + eG) * (1.2 * e3 + 1.2 * a3.abs() * e1) + 2.0 ** -19 * (G * a3).abs()
+    eA3 = eG * f.abs() + (G.abs() + eG) * 1.2 * e1 + 2.0 ** -19 * dA3.abs()
+    eA1, eA3 = eA1 + u * (dA1.abs() + eA1), eA3 + u * (dA3.abs() + eA3)
+    xa, ya = x.abs(), dY.abs()
+    b1, b3 = dA1.abs() + eA1, dA3.abs() + eA3
+    out["dX"] = (dA1 @ W1.T + dA3 @ W3.T, eA1 @ W1.abs().T + eA3 @ W3.abs().T
+                 + 2 * n * e32 * (b1 @ W1.abs().T + b3 @ W3.abs().T))
+    out["dW1"] = (x.T @ dA1, xa.T @ eA1 + T * e32 * (xa.T @ b1))
+    out["dW3"] = (x.T @ dA3, xa.T @ eA3 + T * e32 * (xa.T @ b3))
+    out["dW2"] = (H.T @ dY, eH.T @ ya + T * e32 * ((H.abs() + eH).T @ ya))
+    return out
+
+
+def check_ffn(got, ref, name):
+    """Every element within its bound, and the whole within 1.5 u in the 2-norm (two
+    independent roundings of at most u each give sqrt(2) u)."""
+    want, slack = ref
+    u = HALF[got.dtype]
+    g = got.double()
+    assert torch.isfinite(g).all(), f"{name}: not finite"
+    bound = u * (want.abs() + slack) + slack + TINY[got.dtype]
+    err = (g - want).abs()
+    assert (err <= bound).all(), f"{name}: worst {float((err / bound).max()):.3f} of its bound"
+    if want.numel() >= 64:  # a norm over a few elements says no more than they do
+        rel = float(err.norm() / want.norm())
+        assert rel <= 1.5 * u, f"{name}: 2-norm error {rel:.2e} of u {u:.2e}"

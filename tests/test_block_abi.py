@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from block_common import keep_mask, layernorm, layernorm_backward
+from block_common import ffn, keep_mask, layernorm, layernorm_backward
 from top_routing_grouped_02_gb300 import _build, moe
 
 INVALID, SHAPE, SMALL = 1, 2, 3
@@ -69,6 +69,60 @@ def test_dropout_refusals(lib):
     assert drop(lib, T=1 << 56, d=64) == SHAPE
     assert drop(lib, T=0, x=None, y=None) == 0
     assert lib.moe_dropout_backward(None, 64, 4, 64, 0.1, 1, 2, None, 0, P, 64, None) == INVALID
+
+
+def ffn_fwd(lib, X=P, W1=P, W3=P, W2=P, T=4, d=64, n=128, act=0, t=0, Y=P, ws=P, nbytes=1 << 40):
+    return lib.moe_ffn_forward(X, W1, W3, W2, T, d, n, act, t, Y, ws, nbytes, None)
+
+
+def ffn_train(lib, T=4, d=64, n=128, H=P, A1=P, A3=P, ws=P, nbytes=1 << 40):
+    return lib.moe_ffn_forward_train(P, P, P, P, T, d, n, 0, 0, P, H, A1, A3, ws, nbytes, None)
+
+
+def ffn_bwd(lib, dY=P, A1=P, T=4, d=64, n=128, act=0, t=0, dX=P, dW1=P, dW3=P, dW2=P, ws=P, nbytes=1 << 40):
+    return lib.moe_ffn_backward(dY, P, P, P, P, P, A1, P, T, d, n, act, t, dX, dW1, dW3, dW2, ws, nbytes, None)
+
+
+def test_ffn_refusals(lib):
+    passed = ffn_fwd(lib)
+    assert passed not in (INVALID, SHAPE, SMALL)
+    for bad in (dict(X=None), dict(W1=None), dict(W3=P + 8), dict(W2=None), dict(Y=None), dict(T=-1),
+                dict(d=0), dict(n=-8), dict(act=2), dict(t=5), dict(ws=None), dict(ws=P + 16)):
+        assert ffn_fwd(lib, **bad) == INVALID, bad
+    for bad in (dict(d=12), dict(n=4), dict(t=2), dict(d=(1 << 20) + 8)):
+        assert ffn_fwd(lib, **bad) == SHAPE, bad
+    for T in (1, 128, 129):
+        need = lib.moe_ffn_workspace_bytes(T, 64, 128, 0)
+        assert ffn_fwd(lib, T=T, nbytes=need - 1) == SMALL
+        assert ffn_fwd(lib, T=T, nbytes=need) == passed
+        assert lib.moe_ffn_workspace_bytes(T, 64, 128, 1) >= need
+    assert ffn_fwd(lib, T=0, X=None) == 0
+    assert ffn_train(lib) == passed
+    for bad in (dict(H=None), dict(A1=None), dict(A3=P + 4)):
+        assert ffn_train(lib, **bad) == INVALID, bad
+    assert ffn_bwd(lib) == passed
+    assert ffn_bwd(lib, dX=None) == passed
+    assert ffn_bwd(lib, dW1=None, dW3=None, dW2=None) == passed
+    for bad in (dict(dY=None), dict(A1=None), dict(dX=P + 8), dict(dW1=None), dict(dW2=None),
+                dict(dW3=P + 2), dict(act=-1), dict(ws=None)):
+        assert ffn_bwd(lib, **bad) == INVALID, bad
+    assert ffn_bwd(lib, T=300, nbytes=lib.moe_ffn_workspace_bytes(300, 64, 128, 1) - 1) == SMALL
+    assert lib.moe_ffn_workspace_bytes(4, 60, 128, 0) == 0
+    assert lib.moe_ffn_workspace_init(P, 64, None) == SMALL
+
+
+def test_plain_ffn_against_autograd():
+    g = torch.Generator().manual_seed(1)
+    for act in ("silu", "gelu"):
+        x, W1, W3 = (torch.randn(*s, generator=g).bfloat16() for s in ((5, 12), (12, 9), (12, 9)))
+        W2, dY = torch.randn(9, 12, generator=g).bfloat16(), torch.randn(5, 12, generator=g).bfloat16()
+        leaves = [t.double().requires_grad_() for t in (x, W1, W3, W2)]
+        f = torch.nn.functional.silu if act == "silu" else lambda a: torch.nn.functional.gelu(a, approximate="tanh")
+        y = (f(leaves[0] @ leaves[1]) * (leaves[0] @ leaves[2])) @ leaves[3]
+        y.backward(dY.double())
+        ref = ffn(x, W1, W3, W2, act, dY)
+        for name, want in zip(("Y", "dX", "dW1", "dW3", "dW2"), [y.detach()] + [t.grad for t in leaves]):
+            torch.testing.assert_close(ref[name][0], want)
 
 
 def test_binding_refusals():

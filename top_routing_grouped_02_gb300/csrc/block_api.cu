@@ -1,7 +1,9 @@
 // C ABI of the sub-block operators around the layer (layer norm, residual
-// dropout): argument checks and launches. Errors are returned before anything
+// dropout, dense gated feed-forward block): argument checks and launches. Errors are returned before anything
 // is enqueued.
 #include <math.h>
+
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -46,6 +48,50 @@ moe_status_t drop(const void *x, int64_t ldx, const void *res, int64_t ldr, int6
     const uint32_t thr = (uint32_t)floor(p * 65536.0 + 0.5);
     return from_cuda(launch_dropout(x, ldx, res, ldr, y, ldy, T, d, thr, seed, offset, offset_dev,
                                     type, as_stream(stream)));
+}
+
+// ---- dense feed-forward block
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+moe_status_t check_ffn(int T, int d, int n, moe_act_t act, moe_dtype_t type) {
+    if (T < 0 || d < 1 || n < 1 || !valid_type(type) ||
+        (act != MOE_ACT_SILU && act != MOE_ACT_GELU_TANH))
+        return MOE_ERR_INVALID_ARG;
+    if (d % 8 != 0 || n % 8 != 0 || d > kFfnMaxWidth || n > kFfnMaxWidth || type == MOE_DTYPE_F32)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    // row tiles and columns of every product stay within 32-bit indices
+    if (T > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+// Regions behind the control words: the backward's dA1, dA3, or H of a forward
+// without saved tensors and the parts of the weight-streaming kernels.
+struct FfnWs {
+    size_t h, part, da1, da3, total;
+};
+FfnWs ffn_ws(int T, int n, bool train) {
+    FfnWs w;
+    const size_t act = align256((size_t)T * n * 2);
+    w.h = w.da1 = align256(kFfnControlBytes);
+    w.da3 = w.da1 + act;
+    w.part = w.h + act;
+    w.total = w.part + (T <= kFfnStreamTokens ? align256(ffn_stream_part_bytes(T)) : 0);
+    if (train && w.da3 + act > w.total) w.total = w.da3 + act;
+    return w;
+}
+
+char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
+
+bool all_aligned16(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (p == nullptr || !aligned(p, 16)) return false;
+    return true;
+}
+
+moe_status_t check_ffn_ws(void *ws, size_t ws_bytes, int T, int n, bool train) {
+    if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    return ws_bytes < ffn_ws(T, n, train).total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
 }  // namespace
@@ -125,6 +171,86 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
                                   uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                                   moe_dtype_t type, void *dx, int64_t lddx, void *stream) {
     return drop(dy, lddy, nullptr, 0, T, d, p, seed, offset, offset_dev, type, dx, lddx, stream);
+}
+
+size_t moe_ffn_workspace_bytes(int T, int d, int n, int train) {
+    if (check_ffn(T, d, n, MOE_ACT_SILU, MOE_DTYPE_BF16) != MOE_OK) return 0;
+    return ffn_ws(T, n, train != 0).total;
+}
+
+moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream) {
+    if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kFfnControlBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const moe_status_t st = check_arch();
+    if (st != MOE_OK) return st;
+    return from_cuda(cudaMemsetAsync(ws, 0, kFfnControlBytes, as_stream(stream)));
+}
+
+moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, const void *W2, int T,
+                             int d, int n, moe_act_t act, moe_dtype_t type, void *Y, void *ws,
+                             size_t ws_bytes, void *stream) {
+    moe_status_t st = check_ffn(T, d, n, act, type);
+    if (st != MOE_OK || T == 0) return st;
+    if (!all_aligned16({X, W1, W3, W2, Y})) return MOE_ERR_INVALID_ARG;
+    if ((st = check_ffn_ws(ws, ws_bytes, T, n, false)) != MOE_OK) return st;
+    if ((st = check_arch()) != MOE_OK) return st;
+    const FfnWs w = ffn_ws(T, n, false);
+    uint32_t *err = static_cast<uint32_t *>(ws);
+    const bool f16 = type == MOE_DTYPE_F16;
+    cudaStream_t s = as_stream(stream);
+    if (T <= kFfnStreamTokens)
+        return from_cuda(launch_ffn_stream(X, W1, W3, W2, T, d, n, act, f16, at(ws, w.h), Y,
+                                           reinterpret_cast<float *>(at(ws, w.part)),
+                                           reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),
+                                           err, s));
+    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, at(ws, w.h), nullptr, nullptr, err, s);
+    if (e == cudaSuccess) e = launch_ffn_down(at(ws, w.h), W2, T, d, n, f16, Y, err, s);
+    return from_cuda(e);
+}
+
+moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
+                                   int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
+                                   void *H, float *A1, float *A3, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    moe_status_t st = check_ffn(T, d, n, act, type);
+    if (st != MOE_OK || T == 0) return st;
+    if (!all_aligned16({X, W1, W3, W2, Y, H, A1, A3})) return MOE_ERR_INVALID_ARG;
+    if ((st = check_ffn_ws(ws, ws_bytes, T, n, false)) != MOE_OK) return st;
+    if ((st = check_arch()) != MOE_OK) return st;
+    uint32_t *err = static_cast<uint32_t *>(ws);
+    const bool f16 = type == MOE_DTYPE_F16;
+    cudaStream_t s = as_stream(stream);
+    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, H, A1, A3, err, s);
+    if (e == cudaSuccess) e = launch_ffn_down(H, W2, T, d, n, f16, Y, err, s);
+    return from_cuda(e);
+}
+
+moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
+                              const void *W2, const void *H, const float *A1, const float *A3,
+                              int T, int d, int n, moe_act_t act, moe_dtype_t type, void *dX,
+                              void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
+                              void *stream) {
+    moe_status_t st = check_ffn(T, d, n, act, type);
+    if (st != MOE_OK) return st;
+    const int given = (dW1 != nullptr) + (dW3 != nullptr) + (dW2 != nullptr);
+    if (given != 0 && (given != 3 || !all_aligned16({dW1, dW3, dW2}))) return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!all_aligned16({dY, X, W1, W3, W2, H, A1, A3}) || !aligned(dX, 16))
+            return MOE_ERR_INVALID_ARG;
+        if ((st = check_ffn_ws(ws, ws_bytes, T, n, true)) != MOE_OK) return st;
+    }
+    if ((st = check_arch()) != MOE_OK) return st;
+    cudaStream_t s = as_stream(stream);
+    if (T == 0) {  // sums over no tokens
+        cudaError_t e = cudaSuccess;
+        for (void *p : {dW1, dW3, dW2})
+            if (p != nullptr && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)d * n * 2, s);
+        return from_cuda(e);
+    }
+    const FfnWs w = ffn_ws(T, n, true);
+    return from_cuda(launch_ffn_backward(dY, X, W1, W3, W2, H, A1, A3, T, d, n, act,
+                                         type == MOE_DTYPE_F16, at(ws, w.da1), at(ws, w.da3), dX,
+                                         dW1, dW3, dW2, static_cast<uint32_t *>(ws), s));
 }
 
 }  // extern "C"

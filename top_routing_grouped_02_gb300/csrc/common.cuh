@@ -226,6 +226,29 @@ cudaError_t launch_dropout(const void *x, int64_t ldx, const void *res, int64_t 
                            uint64_t offset, const uint64_t *offset_dev, moe_dtype_t type,
                            cudaStream_t s);
 
+// Dense gated feed-forward block (ffn.cu: large products; ffn_small.cu: up to
+// kFfnStreamTokens tokens, which stream the weights). f16: fp16, else bf16. A1,
+// A3 of the gate product may be NULL; dX may be NULL, and dW1, dW3, dW2 together.
+constexpr int kFfnStreamTokens = 128;
+constexpr int kFfnMaxCtas = 192;       // of one weight-streaming launch
+constexpr int kFfnMaxWidth = 1 << 20;  // of d and n
+constexpr size_t kFfnTicketOffset = 256;  // workspace: control words, then tickets
+constexpr size_t kFfnControlBytes = kFfnTicketOffset + (size_t)(kFfnMaxWidth / 128) * 4 * sizeof(uint32_t);
+size_t ffn_stream_part_bytes(int T);
+cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, const void *W2, int T,
+                              int d, int n, int act, bool f16, void *H, void *Y, float *part,
+                              uint32_t *ticket, uint32_t *err, cudaStream_t s);
+cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
+                            int act, bool f16, void *H, float *A1, float *A3, uint32_t *err,
+                            cudaStream_t s);
+cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, bool f16, void *Y,
+                            uint32_t *err, cudaStream_t s);
+cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
+                                const void *W2, const void *H, const float *A1, const float *A3,
+                                int T, int d, int n, int act, bool f16, void *dA1, void *dA3,
+                                void *dX, void *dW1, void *dW3, void *dW2, uint32_t *err,
+                                cudaStream_t s);
+
 // One CTA whose pipeline wait on a barrier nothing arrives at runs out after the
 // wait limit (about 1 s) and sets MOE_DEVERR_TIMEOUT in *err.
 cudaError_t launch_wait_timeout_selftest(uint32_t *err, cudaStream_t s);

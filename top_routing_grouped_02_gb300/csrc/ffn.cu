@@ -1,0 +1,535 @@
+// Dense gated feed-forward block on the 5th-generation tensor cores, forward and
+// backward:
+//   A1 = X W1, A3 = X W3, H = act(A1) * A3, Y = H W2
+//   G = dY W2^T, dA1 = G A3 act'(A1), dA3 = G act(A1)
+//   dX = dA1 W1^T + dA3 W3^T, dW1 = X^T dA1, dW3 = X^T dA3, dW2 = H^T dY
+// X, Y [T,d], W1, W3 [d,n], W2 [n,d], all 16 bits; accumulation in fp32.
+//
+// One persistent kernel template runs all five products (Mode). Each is bound by
+// the tensor cores once T is a few hundred; few tokens take the weight-streaming
+// kernel of ffn_small.cu instead. A CTA pair (tcgen05 cta_group::2) owns a tile
+// of 256 rows x BN columns: each CTA holds its 128 rows of A and half of the
+// columns of B per 64-deep stage, the even CTA issues the MMAs over both. Two
+// accumulators in TMEM: the epilogue of one tile runs while the MMAs fill the
+// other. gate/up: the even CTA's half of B is W1's columns and the odd CTA's W3's,
+// so a thread finds a1 and a3 of one element in its own TMEM lane and H leaves in
+// the epilogue; neither A1 nor A3 is read back from memory in the forward.
+// All tails (T, d, n need not be multiples of a tile) are left to TMA: loads
+// outside a tensor give zeros, which add nothing, and stores outside write nothing.
+//
+// The backward's operands dA1, dA3 and the forward's H are rounded to 16 bits
+// because the tensor cores multiply 16-bit operands; A1 and A3 are kept in fp32
+// for the backward so that dA1 and dA3 carry one rounding each and not three.
+//
+// Warps: 0 TMA producer, 1 MMA issuer (even CTA), 2 TMEM allocation, 4-11 epilogue
+// (two warps per quadrant of 32 TMEM lanes, splitting the columns). Waits are
+// bounded; a wait that gives up flags the error word, its role stops, and loads and
+// MMAs in flight are drained before the CTA leaves.
+#include <algorithm>
+
+#include "ffn.cuh"
+
+namespace moe {
+namespace ffn {
+namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+}  // namespace
+
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+              uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return nullptr;
+    }();
+    if (fn == nullptr) return false;
+    const uint64_t es = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols * es};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+// kGate: H (and, for training, A1, A3) from X, W1, W3. kDown: Y from H, W2.
+// kDHid: dA1, dA3 from dY, W2 (K-major: its rows are the output columns) and A1,
+// A3. kDX: dX, one reduction over dA1 W1^T then dA3 W3^T (K-major weights).
+// kWGrad: dW1, dW3, dW2 in one launch, both operands MN-major, reduction over T.
+enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4 };
+
+constexpr int BM = 128;  // rows per CTA
+constexpr int BK = 64;   // reduction depth per stage: 128 bytes of 16-bit elements
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr uint32_t kABytes = BM * BK * 2;  // 16 KB
+constexpr uint32_t kBox = 64 * 64 * 2;     // 8 KB: 64 x 64 elements
+constexpr uint32_t kEpiBuf = 32 * 64;      // 32 rows of 64 bytes
+constexpr int kEpiBufs = 2;                // per epilogue warp
+// Row-tile pairs that take every column block before the next group starts: the
+// 76 pairs at work then cover about 8 x 10 tiles and share their operands in L2.
+constexpr int kGroup = 8;
+
+template <int BN>
+struct Geo {
+    static constexpr int kBoxes = BN / 128;  // 64-column boxes of B per CTA
+    static constexpr uint32_t kStageBytes = kABytes + kBoxes * kBox;
+    static constexpr int kStages = BN == 256 ? 6 : 8;  // 192 KB
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes +
+                                    (size_t)kEpiWarps * kEpiBufs * kEpiBuf + 256;
+};
+
+struct Maps {
+    CUtensorMap a[3], b[3], o[3];
+};
+
+struct Args {
+    int units;           // tiles of all problems
+    int first[3];        // first unit of each problem (kWGrad: three, else one)
+    int mt[3], nb[3];    // row-tile pairs, column blocks
+    int rows[3], cols[3];// of the outputs
+    int kb, kb_half;     // k-blocks; kDX: those of its first half
+    uint32_t idesc;
+    int f16, act;
+    int pre;             // kGate: store A1, A3
+    const float *a1, *a3;// kDHid
+    uint32_t *err;
+};
+
+struct Ctl {
+    uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+};
+static_assert(sizeof(Ctl) <= 256, "control block");
+
+template <int MODE, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
+    using G = Geo<BN>;
+    constexpr int S = G::kStages;
+    constexpr bool A_MN = MODE == kWGrad;
+    constexpr bool B_K = MODE == kDHid || MODE == kDX;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + (size_t)S * G::kStageBytes +
+                                       (size_t)kEpiWarps * kEpiBufs * kEpiBuf);
+    const uint32_t base = ptx::smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->tfull[a]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->tempty[a]), 2 * kEpiWarps);
+        }
+        ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
+        ptx::fence_barrier_init();
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base), 2 * BN);
+        ptx::tmem_relinquish_pair();
+    }
+    pdl_wait();
+    pdl_trigger();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+
+    struct Unit {
+        int p, m, nb, row0;  // problem, row-tile pair, column block, this CTA's first row
+    };
+    auto unit_at = [&](int u) {
+        Unit x;
+        x.p = 0;
+        if (MODE == kWGrad) x.p = u >= args.first[2] ? 2 : u >= args.first[1] ? 1 : 0;
+        u -= args.first[x.p];
+        const int mt = args.mt[x.p], per = kGroup * args.nb[x.p];
+        const int k = u / per, gs = min(kGroup, mt - k * kGroup), r = u - k * per;
+        x.nb = r / gs;
+        x.m = k * kGroup + r - x.nb * gs;
+        x.row0 = (2 * x.m + (int)rank) * BM;
+        return x;
+    };
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------ producer --
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = pair; u < args.units && ok; u += pairs) {
+            const Unit un = unit_at(u);
+            for (int kb = 0; kb < args.kb; ++kb, ++it) {
+                const uint32_t s = it % S;
+                if (!bounded_wait(ptx::smem_addr(&ctl->empty[s]), ((it / S) & 1u) ^ 1u, args.err)) {
+                    ok = false;
+                    break;
+                }
+                // both CTAs' loads complete on the even CTA's barrier
+                const uint32_t full = ptx::smem_addr(&ctl->full[s]);
+                if (leader) ptx::mbar_arrive_expect_tx(full, 2 * G::kStageBytes);
+                const uint32_t bar = ptx::mapa(full, 0);
+                const uint32_t sA = base + s * G::kStageBytes, sB = sA + kABytes;
+                const bool second = MODE == kDX && kb >= args.kb_half;
+                const int k0 = (second ? kb - args.kb_half : kb) * BK;
+                const int ai = MODE == kWGrad ? un.p : second ? 1 : 0;
+                const int bi = MODE == kWGrad ? un.p
+                               : MODE == kGate ? (int)rank
+                               : second ? 1 : 0;
+                if (A_MN) {
+                    ptx::tma_load_2d_pair(sA, &maps.a[ai], bar, un.row0, k0);
+                    ptx::tma_load_2d_pair(sA + kBox, &maps.a[ai], bar, un.row0 + 64, k0);
+                } else {
+                    ptx::tma_load_2d_pair(sA, &maps.a[ai], bar, k0, un.row0);
+                }
+                // this CTA's half of the tile's columns of B
+                const int c0 = MODE == kGate ? un.nb * (BN / 2) : un.nb * BN + (int)rank * (BN / 2);
+#pragma unroll
+                for (int q = 0; q < G::kBoxes; ++q) {
+                    if (B_K) ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, k0, c0 + q * 64);
+                    else ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, c0 + q * 64, k0);
+                }
+            }
+        }
+        if (!ok && leader) {
+            const uint32_t first = it > (uint32_t)S ? it - S : 0u;
+            for (uint32_t j = first; j < it; ++j)
+                bounded_wait(ptx::smem_addr(&ctl->full[j % S]), (j / S) & 1u, args.err);
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ---------------------------------------------------- MMA issuer --
+        uint32_t it = 0, uc = 0;
+        bool ok = true;
+        for (int u = pair; u < args.units && ok; u += pairs, ++uc) {
+            const uint32_t a = uc & 1u;
+            if (!bounded_wait(ptx::smem_addr(&ctl->tempty[a]), ((uc >> 1) & 1u) ^ 1u, args.err)) break;
+            ptx::tc_fence_after();
+            for (int kb = 0; kb < args.kb; ++kb, ++it) {
+                const uint32_t s = it % S;
+                if (!bounded_wait(ptx::smem_addr(&ctl->full[s]), (it / S) & 1u, args.err)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t sA = base + s * G::kStageBytes, sB = sA + kABytes;
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k) {
+                    // K-major: the next 16 of the reduction are 32 bytes on; MN-major:
+                    // 16 rows of 128 bytes, 64-column slabs 8 KB apart
+                    const uint64_t ad = A_MN ? ptx::desc_sw128(sA + k * 2048, kBox, 1024)
+                                             : ptx::desc_sw128(sA + k * 32, 16, 1024);
+                    const uint64_t bd = B_K ? ptx::desc_sw128(sB + k * 32, 16, 1024)
+                                            : ptx::desc_sw128(sB + k * 2048, kBox, 1024);
+                    ptx::tc_mma_f16_pair(tmem_base + a * BN, ad, bd, args.idesc, (kb | k) != 0);
+                }
+                ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[s]), 0x3);
+            }
+            if (!ok) break;
+            ptx::tc_commit_pair(ptx::smem_addr(&ctl->tfull[a]), 0x3);
+        }
+        ptx::tc_commit_pair(ptx::smem_addr(&ctl->drain), 0x1);
+        bounded_wait(ptx::smem_addr(&ctl->drain), 0, args.err);
+    } else if (warp >= 4) {
+        // ------------------------------------------------------ epilogue --
+        const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+        const uint32_t buf0 = base + (uint32_t)S * G::kStageBytes + (uint32_t)ew * kEpiBufs * kEpiBuf;
+        const uint32_t tempty0 = ptx::mapa(ptx::smem_addr(&ctl->tempty[0]), 0);
+        const bool f16 = args.f16 != 0;
+        uint32_t groups = 0, uc = 0;
+        // 32 rows x 64 bytes through a staging buffer (64-byte swizzle) and a TMA
+        // store at (x, y), skipped where the whole box lies outside
+        auto store_box = [&](const uint32_t (&v)[16], int x, int y, const CUtensorMap *map) {
+            const uint32_t buf = buf0 + (groups % kEpiBufs) * kEpiBuf;
+            if (lane == 0 && groups >= (uint32_t)kEpiBufs) ptx::bulk_wait_group_read<kEpiBufs - 1>();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ptx::st_shared_v4(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), v[4 * i],
+                                  v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::tma_store_2d(map, buf, x, y);
+                ptx::bulk_commit_group();
+            }
+            ++groups;
+        };
+        for (int u = pair; u < args.units; u += pairs, ++uc) {
+            const Unit un = unit_at(u);
+            const int rows = args.rows[un.p], cols = args.cols[un.p];
+            const int y0 = un.row0 + q * 32;
+            const uint32_t a = uc & 1u;
+            constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // output columns of the tile
+            const int c_lo = half * (kCols / 64), c_hi = c_lo + kCols / 64;
+            // kDHid: this row's A1, A3 of a 32-column chunk, loaded one chunk ahead
+            float4 x1[8], x3[8];
+            auto load_pre = [&](int c, float4 (&l1)[8], float4 (&l3)[8]) {
+                const int row = y0 + lane, col = un.nb * kCols + c * 32;
+                const int64_t off = (int64_t)row * cols + col;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = row < rows && col + 4 * i < cols;
+                    l1[i] = in ? __ldg(reinterpret_cast<const float4 *>(args.a1 + off) + i)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                    l3[i] = in ? __ldg(reinterpret_cast<const float4 *>(args.a3 + off) + i)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            };
+            if constexpr (MODE == kDHid) load_pre(c_lo, x1, x3);
+            if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (uc >> 1) & 1u, args.err)) break;
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * BN;
+#pragma unroll 1
+            for (int c = c_lo; c < c_hi; ++c) {
+                const int x0 = un.nb * kCols + c * 32;
+                const bool in = y0 < rows && x0 < cols;
+                if constexpr (MODE == kGate) {
+                    uint32_t g[32], v[32], o[16];
+                    ptx::tmem_ld32(taddr + c * 32, g);
+                    ptx::tmem_ld32(taddr + BN / 2 + c * 32, v);
+                    if (!in) continue;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float h[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float ga = __uint_as_float(g[2 * i + j]);
+                            h[j] = ga * act_sigmoid(ga, args.act) * __uint_as_float(v[2 * i + j]);
+                        }
+                        o[i] = pack(h[0], h[1], f16);
+                    }
+                    store_box(o, x0, y0, &maps.o[0]);
+                    if (args.pre) {
+                        // fp32: two boxes of 16 columns each
+                        const bool in2 = x0 + 16 < cols;
+                        uint32_t lo[16], hi[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            lo[i] = g[i];
+                            hi[i] = g[16 + i];
+                        }
+                        store_box(lo, x0, y0, &maps.o[1]);
+                        if (in2) store_box(hi, x0 + 16, y0, &maps.o[1]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            lo[i] = v[i];
+                            hi[i] = v[16 + i];
+                        }
+                        store_box(lo, x0, y0, &maps.o[2]);
+                        if (in2) store_box(hi, x0 + 16, y0, &maps.o[2]);
+                    }
+                } else if constexpr (MODE == kDHid) {
+                    float4 n1[8], n3[8];
+                    if (c + 1 < c_hi) load_pre(c + 1, n1, n3);
+                    uint32_t g[32], o1[16], o3[16];
+                    ptx::tmem_ld32(taddr + c * 32, g);
+                    if (in) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float r1[2], r3[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float a1 = (&x1[i >> 1].x)[2 * (i & 1) + j];
+                                const float a3 = (&x3[i >> 1].x)[2 * (i & 1) + j];
+                                const float gv = __uint_as_float(g[2 * i + j]);
+                                const float sg = act_sigmoid(a1, args.act);
+                                r1[j] = gv * a3 * act_grad(a1, sg, args.act);
+                                r3[j] = gv * (a1 * sg);
+                            }
+                            o1[i] = pack(r1[0], r1[1], f16);
+                            o3[i] = pack(r3[0], r3[1], f16);
+                        }
+                        store_box(o1, x0, y0, &maps.o[0]);
+                        store_box(o3, x0, y0, &maps.o[1]);
+                    }
+                    if (c + 1 < c_hi) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            x1[i] = n1[i];
+                            x3[i] = n3[i];
+                        }
+                    }
+                } else {
+                    uint32_t v[32], o[16];
+                    ptx::tmem_ld32(taddr + c * 32, v);
+                    if (!in) continue;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
+                    store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
+        }
+        if (lane == 0) ptx::bulk_wait_group<0>();
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // no arrival or MMA of the pair is outstanding
+    ptx::tc_fence_after();
+    if (warp == 2) ptx::tmem_dealloc_pair(tmem_base, 2 * BN);
+}
+
+// ------------------------------------------------------------ host side --
+
+template <int MODE, int BN>
+cudaError_t launch_bn(const Maps &maps, Args args, cudaStream_t s) {
+    const int problems = MODE == kWGrad ? 3 : 1;
+    args.units = 0;
+    for (int p = 0; p < 3; ++p) {
+        args.first[p] = args.units;
+        if (p >= problems) continue;
+        constexpr int kCols = MODE == kGate ? BN / 2 : BN;
+        args.mt[p] = (args.rows[p] + 2 * BM - 1) / (2 * BM);
+        args.nb[p] = (args.cols[p] + kCols - 1) / kCols;
+        args.units += args.mt[p] * args.nb[p];
+    }
+    args.idesc = idesc(args.f16 != 0, 2 * BM, BN, MODE == kWGrad, !(MODE == kDHid || MODE == kDX));
+    constexpr size_t kSmem = Geo<BN>::kSmem;
+    const cudaError_t e = ensure_dynamic_smem(
+        reinterpret_cast<const void *>(dense_gemm_kernel<MODE, BN>), (int)kSmem);
+    if (e != cudaSuccess) return e;
+    const int pairs = std::max(1, std::min(sm_count() / 2, args.units));
+    return launch_k(dense_gemm_kernel<MODE, BN>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
+}
+
+// 256-column tiles, or 128-column tiles where they leave fewer SMs idle: the
+// waves of tiles over the SM pairs times the tile's width, 128-column tiles
+// counted an eighth dearer (they load twice the A bytes per MMA).
+template <int MODE>
+cudaError_t launch(const Maps &maps, const Args &args, cudaStream_t s) {
+    const int pairs = std::max(1, sm_count() / 2);
+    int64_t u[2] = {0, 0};
+    for (int p = 0; p < (MODE == kWGrad ? 3 : 1); ++p) {
+        const int64_t mt = (args.rows[p] + 2 * BM - 1) / (2 * BM);
+        const int64_t cols = (int64_t)args.cols[p] * (MODE == kGate ? 2 : 1);
+        u[0] += mt * ((cols + 255) / 256);
+        u[1] += mt * ((cols + 127) / 128);
+    }
+    const int64_t wide = (u[0] + pairs - 1) / pairs * 16, narrow = (u[1] + pairs - 1) / pairs * 9;
+    return narrow < wide ? launch_bn<MODE, 128>(maps, args, s) : launch_bn<MODE, 256>(maps, args, s);
+}
+
+constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B, kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+
+// Operand maps: K-major A rows (64 x 128 boxes) and 64 x 64 boxes for the rest.
+bool map_a(CUtensorMap *m, bool f16, const void *p, int cols, int rows) {
+    return make_map(m, map_type(f16), p, cols, rows, 64, BM, kSw128);
+}
+bool map_64(CUtensorMap *m, bool f16, const void *p, int cols, int rows) {
+    return make_map(m, map_type(f16), p, cols, rows, 64, 64, kSw128);
+}
+bool map_out(CUtensorMap *m, bool f16, const void *p, int cols, int rows) {
+    return make_map(m, map_type(f16), p, cols, rows, 32, 32, kSw64);
+}
+bool map_out32(CUtensorMap *m, const void *p, int cols, int rows) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p, cols, rows, 16, 32, kSw64);
+}
+
+}  // namespace
+}  // namespace ffn
+
+using namespace ffn;
+
+cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
+                            int act, bool f16, void *H, float *A1, float *A3, uint32_t *err,
+                            cudaStream_t s) {
+    Maps m{};
+    if (!map_a(&m.a[0], f16, X, d, T) || !map_64(&m.b[0], f16, W1, n, d) ||
+        !map_64(&m.b[1], f16, W3, n, d) || !map_out(&m.o[0], f16, H, n, T))
+        return cudaErrorInvalidValue;
+    if (A1 != nullptr && (!map_out32(&m.o[1], A1, n, T) || !map_out32(&m.o[2], A3, n, T)))
+        return cudaErrorInvalidValue;
+    Args a{};
+    a.rows[0] = T;
+    a.cols[0] = n;
+    a.kb = (d + BK - 1) / BK;
+    a.f16 = f16;
+    a.act = act;
+    a.pre = A1 != nullptr;
+    a.err = err;
+    return launch<kGate>(m, a, s);
+}
+
+cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, bool f16, void *Y,
+                            uint32_t *err, cudaStream_t s) {
+    Maps m{};
+    if (!map_a(&m.a[0], f16, H, n, T) || !map_64(&m.b[0], f16, W2, d, n) ||
+        !map_out(&m.o[0], f16, Y, d, T))
+        return cudaErrorInvalidValue;
+    Args a{};
+    a.rows[0] = T;
+    a.cols[0] = d;
+    a.kb = (n + BK - 1) / BK;
+    a.f16 = f16;
+    a.err = err;
+    return launch<kDown>(m, a, s);
+}
+
+cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
+                                const void *W2, const void *H, const float *A1, const float *A3,
+                                int T, int d, int n, int act, bool f16, void *dA1, void *dA3,
+                                void *dX, void *dW1, void *dW3, void *dW2, uint32_t *err,
+                                cudaStream_t s) {
+    Maps m{};
+    if (!map_a(&m.a[0], f16, dY, d, T) || !map_64(&m.b[0], f16, W2, d, n) ||
+        !map_out(&m.o[0], f16, dA1, n, T) || !map_out(&m.o[1], f16, dA3, n, T))
+        return cudaErrorInvalidValue;
+    Args a{};
+    a.rows[0] = T;
+    a.cols[0] = n;
+    a.kb = (d + BK - 1) / BK;
+    a.f16 = f16;
+    a.act = act;
+    a.a1 = A1;
+    a.a3 = A3;
+    a.err = err;
+    cudaError_t e = launch<kDHid>(m, a, s);
+    if (e != cudaSuccess) return e;
+    if (dX != nullptr) {
+        if (!map_a(&m.a[0], f16, dA1, n, T) || !map_a(&m.a[1], f16, dA3, n, T) ||
+            !map_64(&m.b[0], f16, W1, n, d) || !map_64(&m.b[1], f16, W3, n, d) ||
+            !map_out(&m.o[0], f16, dX, d, T))
+            return cudaErrorInvalidValue;
+        a.cols[0] = d;
+        a.kb_half = (n + BK - 1) / BK;
+        a.kb = 2 * a.kb_half;
+        if ((e = launch<kDX>(m, a, s)) != cudaSuccess) return e;
+    }
+    if (dW1 == nullptr) return cudaSuccess;
+    if (!map_64(&m.a[0], f16, X, d, T) || !map_64(&m.a[1], f16, X, d, T) ||
+        !map_64(&m.a[2], f16, H, n, T) || !map_64(&m.b[0], f16, dA1, n, T) ||
+        !map_64(&m.b[1], f16, dA3, n, T) || !map_64(&m.b[2], f16, dY, d, T) ||
+        !map_out(&m.o[0], f16, dW1, n, d) || !map_out(&m.o[1], f16, dW3, n, d) ||
+        !map_out(&m.o[2], f16, dW2, d, n))
+        return cudaErrorInvalidValue;
+    a.rows[0] = a.rows[1] = a.cols[2] = d;
+    a.cols[0] = a.cols[1] = a.rows[2] = n;
+    a.kb = (T + BK - 1) / BK;
+    return launch<kWGrad>(m, a, s);
+}
+
+}  // namespace moe

@@ -32,7 +32,7 @@ LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_g
             "moe_backward_router": 5, "moe_backward_dw": 5,
             "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1,
             "moe_layernorm": 1, "moe_layernorm_backward": 2, "moe_dropout": 1,
-            "moe_dropout_backward": 1}
+            "moe_dropout_backward": 1, "moe_ffn": 2, "moe_ffn_train": 2, "moe_ffn_backward": 3}
 TILE_M = 128
 
 
@@ -93,6 +93,13 @@ _SIGS = {
                                     _P, _P, _SZ, _P]),
     "moe_dropout": (_I, [_P, _L, _P, _L, _L, _I, _D, _U, _U, _P, _I, _P, _L, _P]),
     "moe_dropout_backward": (_I, [_P, _L, _L, _I, _D, _U, _U, _P, _I, _P, _L, _P]),
+    "moe_ffn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_ffn_workspace_init": (_I, [_P, _SZ, _P]),
+    "moe_ffn_forward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_ffn_forward_train": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ,
+                                   _P]),
+    "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
+                              _P, _SZ, _P]),
     "moe_round_capacity": (ctypes.c_int64, [_I, _I, _I, _I]),
     "moe_round_workspace_bytes": (_SZ, [_I, _I]),
     "moe_round_routing": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
@@ -704,3 +711,101 @@ def _counter(t):
     if not t.is_cuda or t.dtype != torch.int64 or t.numel() != 1:
         raise ValueError("offset_dev must be a one-element int64 CUDA tensor")
     return t.data_ptr()
+
+
+ACTS = {"silu": 0, "gelu": 1}
+
+
+def ffn_workspace(T: int, d: int, n: int, train: bool = False, device=None, stream=None):
+    """A workspace (uint8, control words zeroed) of the dense block's calls for up to
+    T tokens; train: of moe_ffn_backward too."""
+    nbytes = int(lib().moe_ffn_workspace_bytes(T, d, n, int(train)))
+    if nbytes == 0:
+        raise ValueError("invalid feed-forward shape")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    _check("moe_ffn_workspace_init", lib().moe_ffn_workspace_init(
+        ws.data_ptr(), nbytes, _raw_stream(stream, ws.device)))
+    return ws
+
+
+def _ffn_shape(x, W1, W3, W2, act):
+    if x.dim() < 1 or W1.dim() != 2 or x.shape[-1] != W1.shape[0]:
+        raise ValueError("x must be [..., d] and W1 [d, n]")
+    d, n = W1.shape
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"the feed-forward block takes bf16 or fp16, got {x.dtype}")
+    T = x.numel() // d if d else 0
+    _dense(x, x.shape, x.dtype, "x")
+    _dense(W1, (d, n), x.dtype, "W1")
+    _dense(W3, (d, n), x.dtype, "W3")
+    _dense(W2, (n, d), x.dtype, "W2")
+    return T, d, n
+
+
+def _dense(t, shape, dtype, name):
+    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {tuple(shape)} of {dtype}")
+    return t.data_ptr()
+
+
+def moe_ffn(x, W1, W3, W2, act: str = "silu", ws=None, Y=None, stream=None):
+    """Y = (act(x W1) * (x W3)) W2 of x [..., d] (bf16 or fp16); act "silu" or "gelu"
+    (the tanh form). ws: ffn_workspace, kept between calls."""
+    T, d, n = _ffn_shape(x, W1, W3, W2, act)
+    if ws is None:
+        ws = ffn_workspace(T, d, n, device=x.device, stream=stream)
+    if Y is None:
+        Y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    st = lib().moe_ffn_forward(
+        x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), T, d, n, ACTS[act],
+        _DTYPES[x.dtype], _dense(Y, x.shape, x.dtype, "Y"), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeError("moe_ffn_forward", st)
+    return Y
+
+
+def moe_ffn_train(x, W1, W3, W2, act: str = "silu", ws=None, stream=None):
+    """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3 fp32)."""
+    T, d, n = _ffn_shape(x, W1, W3, W2, act)
+    if ws is None:
+        ws = ffn_workspace(T, d, n, device=x.device, stream=stream)
+    Y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    H = torch.empty((T, n), dtype=x.dtype, device=x.device)
+    A1, A3 = (torch.empty((T, n), dtype=torch.float32, device=x.device) for _ in range(2))
+    st = lib().moe_ffn_forward_train(
+        x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), T, d, n, ACTS[act],
+        _DTYPES[x.dtype], Y.data_ptr(), H.data_ptr(), A1.data_ptr(), A3.data_ptr(), ws.data_ptr(),
+        ws.numel(), _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeError("moe_ffn_forward_train", st)
+    return Y, H, A1, A3
+
+
+def moe_ffn_backward(dY, x, W1, W3, W2, H, A1, A3, act: str = "silu", need_dx: bool = True,
+                     need_dw: bool = True, ws=None, stream=None):
+    """(dX, dW1, dW3, dW2) of moe_ffn_train, all of x's type (None where not asked
+    for). ws: ffn_workspace(..., train=True)."""
+    T, d, n = _ffn_shape(x, W1, W3, W2, act)
+    _dense(dY, x.shape, x.dtype, "dY")
+    _dense(H, (T, n), x.dtype, "H")
+    _dense(A1, (T, n), torch.float32, "A1")
+    _dense(A3, (T, n), torch.float32, "A3")
+    if ws is None:
+        ws = ffn_workspace(T, d, n, train=True, device=x.device, stream=stream)
+    dX = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dW1 = dW3 = dW2 = None
+    if need_dw:
+        dW1, dW3 = (torch.empty((d, n), dtype=x.dtype, device=x.device) for _ in range(2))
+        dW2 = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    st = lib().moe_ffn_backward(
+        dY.data_ptr(), x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), H.data_ptr(),
+        A1.data_ptr(), A3.data_ptr(), T, d, n, ACTS[act], _DTYPES[x.dtype],
+        dX.data_ptr() if need_dx else None, dW1.data_ptr() if need_dw else None,
+        dW3.data_ptr() if need_dw else None, dW2.data_ptr() if need_dw else None, ws.data_ptr(),
+        ws.numel(), _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeError("moe_ffn_backward", st)
+    return dX, dW1, dW3, dW2
