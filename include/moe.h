@@ -543,8 +543,8 @@ typedef enum {
     MOE_ACT_GELU_TANH = 1  /* 0.5 a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) */
 } moe_act_t;
 
-/* Workspace of the calls below for T tokens (train: of the backward too), 256-byte
- * aligned; 0 for an invalid shape. Its control words (the device error word of
+/* Workspace of the calls below for up to T tokens (train: of the backward too),
+ * 256-byte aligned; 0 for an invalid shape. Its control words (the device error word of
  * moe_sync_check and join counters) start at zero, once before the first use
  * (moe_ffn_workspace_init), and every call leaves the counters so. It serves any
  * shape that needs no more bytes. Calls that overlap on the GPU need one each. */

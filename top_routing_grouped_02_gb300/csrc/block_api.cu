@@ -3,6 +3,7 @@
 // is enqueued.
 #include <math.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "common.cuh"
@@ -70,13 +71,16 @@ moe_status_t check_ffn(int T, int d, int n, moe_act_t act, moe_dtype_t type) {
 struct FfnWs {
     size_t h, part, da1, da3, total;
 };
-FfnWs ffn_ws(int T, int n, bool train) {
+FfnWs ffn_ws(int T, int d, int n, bool train) {
     FfnWs w;
     const size_t act = align256((size_t)T * n * 2);
     w.h = w.da1 = align256(kFfnControlBytes);
     w.da3 = w.da1 + act;
     w.part = w.h + act;
-    w.total = w.part + (T <= kFfnStreamTokens ? align256(ffn_stream_part_bytes(T)) : 0);
+    // a workspace for T tokens serves fewer: the most that T or fewer need
+    const int few = std::min(T, kFfnStreamTokens);
+    w.total = std::max(w.part, w.h + align256((size_t)few * n * 2) +
+                                   align256(ffn_stream_part_bytes(few, d, n)));
     if (train && w.da3 + act > w.total) w.total = w.da3 + act;
     return w;
 }
@@ -89,9 +93,9 @@ bool all_aligned16(std::initializer_list<const void *> ps) {
     return true;
 }
 
-moe_status_t check_ffn_ws(void *ws, size_t ws_bytes, int T, int n, bool train) {
+moe_status_t check_ffn_ws(void *ws, size_t ws_bytes, int T, int d, int n, bool train) {
     if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
-    return ws_bytes < ffn_ws(T, n, train).total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+    return ws_bytes < ffn_ws(T, d, n, train).total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
 }  // namespace
@@ -175,7 +179,7 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
 
 size_t moe_ffn_workspace_bytes(int T, int d, int n, int train) {
     if (check_ffn(T, d, n, MOE_ACT_SILU, MOE_DTYPE_BF16) != MOE_OK) return 0;
-    return ffn_ws(T, n, train != 0).total;
+    return ffn_ws(T, d, n, train != 0).total;
 }
 
 moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream) {
@@ -192,9 +196,9 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
     moe_status_t st = check_ffn(T, d, n, act, type);
     if (st != MOE_OK || T == 0) return st;
     if (!all_aligned16({X, W1, W3, W2, Y})) return MOE_ERR_INVALID_ARG;
-    if ((st = check_ffn_ws(ws, ws_bytes, T, n, false)) != MOE_OK) return st;
+    if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, false)) != MOE_OK) return st;
     if ((st = check_arch()) != MOE_OK) return st;
-    const FfnWs w = ffn_ws(T, n, false);
+    const FfnWs w = ffn_ws(T, d, n, false);
     uint32_t *err = static_cast<uint32_t *>(ws);
     const bool f16 = type == MOE_DTYPE_F16;
     cudaStream_t s = as_stream(stream);
@@ -215,7 +219,7 @@ moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3
     moe_status_t st = check_ffn(T, d, n, act, type);
     if (st != MOE_OK || T == 0) return st;
     if (!all_aligned16({X, W1, W3, W2, Y, H, A1, A3})) return MOE_ERR_INVALID_ARG;
-    if ((st = check_ffn_ws(ws, ws_bytes, T, n, false)) != MOE_OK) return st;
+    if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, false)) != MOE_OK) return st;
     if ((st = check_arch()) != MOE_OK) return st;
     uint32_t *err = static_cast<uint32_t *>(ws);
     const bool f16 = type == MOE_DTYPE_F16;
@@ -237,7 +241,7 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
     if (T > 0) {
         if (!all_aligned16({dY, X, W1, W3, W2, H, A1, A3}) || !aligned(dX, 16))
             return MOE_ERR_INVALID_ARG;
-        if ((st = check_ffn_ws(ws, ws_bytes, T, n, true)) != MOE_OK) return st;
+        if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, true)) != MOE_OK) return st;
     }
     if ((st = check_arch()) != MOE_OK) return st;
     cudaStream_t s = as_stream(stream);
@@ -247,7 +251,7 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
             if (p != nullptr && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)d * n * 2, s);
         return from_cuda(e);
     }
-    const FfnWs w = ffn_ws(T, n, true);
+    const FfnWs w = ffn_ws(T, d, n, true);
     return from_cuda(launch_ffn_backward(dY, X, W1, W3, W2, H, A1, A3, T, d, n, act,
                                          type == MOE_DTYPE_F16, at(ws, w.da1), at(ws, w.da3), dX,
                                          dW1, dW3, dW2, static_cast<uint32_t *>(ws), s));

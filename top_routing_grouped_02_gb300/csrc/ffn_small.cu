@@ -326,9 +326,9 @@ int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 1
 
 // CTAs of one product: one per SM, fewer where a run would be under four k-blocks
 // (then the joining costs more than the shorter runs save).
-int stream_grid(int cols, int K) {
+int stream_grid(int cols, int K, int sms) {
     const int64_t tiles = (cols + 127) / 128, W = tiles * ((K + BK - 1) / BK);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count(), kFfnMaxCtas), std::max(tiles, W / 4)));
+    return (int)std::min<int64_t>(std::min(sms, kFfnMaxCtas), std::max(tiles, W / 4));
 }
 
 cudaError_t launch_stream(int mats, const void *w0, const void *w1, const void *x, int T, int K,
@@ -353,7 +353,7 @@ cudaError_t launch_stream(int mats, const void *w0, const void *w1, const void *
     a.part = part;
     a.ticket = ticket;
     a.err = err;
-    const int grid = stream_grid(cols, K);
+    const int grid = stream_grid(cols, K, sm_count());
 #define MOE_CASE(N)                                                      \
     case N:                                                              \
         return mats == 2 ? launch_nt<2, N>(m, a, grid, s) : launch_nt<1, N>(m, a, grid, s)
@@ -372,9 +372,10 @@ cudaError_t launch_stream(int mats, const void *w0, const void *w1, const void *
 
 using namespace ffn;
 
-size_t ffn_stream_part_bytes(int T) {
-    // two parts of two matrices for each CTA
-    return (size_t)kFfnMaxCtas * 2 * 2 * T * 128 * sizeof(float);
+size_t ffn_stream_part_bytes(int T, int d, int n) {
+    // two parts for each CTA, of two matrices in the first product
+    const size_t ctas = std::max(2 * stream_grid(n, d, kFfnMaxCtas), stream_grid(d, n, kFfnMaxCtas));
+    return ctas * 2 * T * 128 * sizeof(float);
 }
 
 cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, const void *W2, int T,
