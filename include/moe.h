@@ -551,9 +551,11 @@ typedef enum {
 size_t moe_ffn_workspace_bytes(int T, int d, int n, int train);
 moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream);
 
-/* Y. Two kernels: gate and up projections, activation and product in one, the
- * down projection in the other. Up to 128 tokens on kernels that stream the
- * weights, each SM an equal share of them. */
+/* Y. Up to 128 tokens one kernel, which streams the weights, each SM an equal share
+ * of them, with H complete on all SMs before the down projection (bounded waits: a
+ * CTA that never gets an SM sets MOE_DEVERR_TIMEOUT; initialise the workspace again
+ * after that). Otherwise two: gate and up projections, activation and product in
+ * one, the down projection in the other. */
 moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, const void *W2, int T,
                              int d, int n, moe_act_t act, moe_dtype_t type, void *Y, void *ws,
                              size_t ws_bytes, void *stream);

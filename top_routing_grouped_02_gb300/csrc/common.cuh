@@ -233,7 +233,8 @@ constexpr int kFfnStreamTokens = 128;
 constexpr int kFfnMaxCtas = 192;       // of one weight-streaming launch
 constexpr int kFfnMaxWidth = 1 << 20;  // of d and n
 constexpr size_t kFfnTicketOffset = 256;  // workspace: control words, then tickets
-constexpr size_t kFfnControlBytes = kFfnTicketOffset + (size_t)(kFfnMaxWidth / 128) * 4 * sizeof(uint32_t);
+constexpr size_t kFfnControlBytes =  // a ticket for each warp of each tile of two products
+    kFfnTicketOffset + 2 * (size_t)(kFfnMaxWidth / 128) * 4 * sizeof(uint32_t);
 size_t ffn_stream_part_bytes(int T, int d, int n);
 cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, const void *W2, int T,
                               int d, int n, int act, bool f16, void *H, void *Y, float *part,

@@ -1,6 +1,6 @@
-// Dense gated feed-forward block for few tokens (decoding): the weights are
-// streamed once and nothing else is large, so HBM bounds it: 2 d n weights for
-// H = act(X W1) * (X W3), d n for Y = H W2.
+// Dense gated feed-forward block for few tokens (decoding), one persistent launch:
+//   H = act(X W1) * (X W3), Y = H W2.
+// The weights are streamed once and nothing else is large, so HBM bounds it.
 //
 // The tensor cores take the weights as the 128-row operand: a tile is 128 columns
 // of W (TMA boxes of 64 columns x 64 rows, MN-major) against NT tokens (16 .. 128,
@@ -8,18 +8,19 @@
 // weight column per TMEM lane and one token per TMEM column, and one token costs
 // no more MMA time than its share of the weight traffic.
 //
-// All tiles' k-blocks (64 rows of W) form one sequence, cut into equal runs, one
-// per CTA, whatever the number of tiles: every SM reads the same number of bytes.
-// A tile that is cut is joined by its parts: each warp writes its part (fp32) to
-// the workspace and takes a ticket; the last to arrive adds all parts in the order
-// of the runs (so the result does not depend on who is last), applies the
-// activation and stores. Nobody waits. Tickets return to zero with the last
-// arrival.
+// Each product is a sequence of units of 32 KB of weights (gate and up: 64 rows of
+// both matrices; down: 128 rows), cut into equal runs, one per CTA and SM,
+// whatever the number of tiles: every SM reads the same number of bytes. A tile
+// that is cut is joined by the CTAs that hold its parts: each writes its part (fp32)
+// to the workspace, and once all have, each adds all parts of its share of the
+// tokens, in the order of the runs, so the result does not depend on timing.
 //
-// The second product is launched to overlap the first (programmatic dependent
-// launch): its CTAs fill their weight stages, which do not depend on H, and only
-// then wait for the first kernel. Both kernels' shared memory and TMEM fit one SM
-// together for up to 32 tokens.
+// The down projection needs all of H: a grid-wide counter separates the products.
+// The rings of all SMs (about 200 KB each) meanwhile fill with W2, which does not
+// depend on H, so HBM stays busy through the joins and the barrier (asking for more
+// of it into L2 measured no faster). All CTAs are
+// resident together (one per SM); every wait is bounded. The counters return to
+// zero with the launch.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 TMEM allocation, 4-7 epilogue.
 #include <algorithm>
@@ -32,38 +33,38 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int BK = 64;
-constexpr uint32_t kBox = 64 * 64 * 2;  // 8 KB: 64 columns x 64 rows of W
-constexpr uint32_t kMat = 2 * kBox;     // 128 columns
-constexpr int kMaxStages = 8;
+constexpr uint32_t kBox = 64 * 64 * 2;    // 8 KB: 64 columns x 64 rows of W
+constexpr uint32_t kMat = 2 * kBox;       // 128 columns
+constexpr uint32_t kWBytes = 2 * kMat;    // weights of one unit
+constexpr int kMaxStages = 6;
+// control words (behind the error word): grid arrivals, exits
+constexpr int kWordGrid = 8, kWordExit = 9;
 
-// MATS weight matrices (2: gate and up; 1: down), NT tokens.
-template <int MATS, int NT>
+template <int NT>
 struct Geo {
-    static constexpr uint32_t kTok = NT * BK * 2;
-    static constexpr uint32_t kStageBytes = MATS * kMat + kTok;
-    // half an SM's shared memory for up to 32 tokens, else all of it
-    static constexpr uint32_t kBudget = NT <= 32 ? 108 * 1024 : 216 * 1024;
-    static constexpr int kStages =
-        kBudget / kStageBytes < kMaxStages ? kBudget / kStageBytes : kMaxStages;
+    static constexpr uint32_t kTok = NT * BK * 2;  // 64 of the reduction of all tokens
+    static constexpr uint32_t kStageBytes = kWBytes + 2 * kTok;
+    static constexpr int kStages = std::min<int>(kMaxStages, 216 * 1024 / kStageBytes);
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
-    // two accumulators of MATS * NT columns
-    static constexpr uint32_t kTmem = 2 * MATS * NT < 32 ? 32 : 2 * MATS * NT;
+    static constexpr uint32_t kTmem = 4 * NT;  // two accumulators of two matrices
+};
+
+// One product: out[T, cols] from the reduction over K.
+struct Product {
+    int cols, kbs, tiles, ctas;  // kbs: units per tile
+    void *out;
 };
 
 struct SmallMaps {
-    CUtensorMap w[2], x;
+    CUtensorMap w[3], x, h;
 };
 
 struct SmallArgs {
-    int T, cols;   // tokens, output columns
-    int kbs;       // k-blocks per tile
-    int tiles;
-    int act, f16;
+    Product p[2];
+    int T, act, f16;
     uint32_t idesc;
-    int early;     // weights may be read before the previous kernel has finished
-    void *out;     // [T, cols], 16 bits
-    float *part;   // [CTA][2][MATS][T][128]
-    uint32_t *ticket;  // [tiles][4]
+    float *part;       // [CTA][2][matrices][T / 4][128][4]
+    uint32_t *ticket;  // [tiles of both products][4]
     uint32_t *err;
 };
 
@@ -73,8 +74,22 @@ struct SmallCtl {
 };
 static_assert(sizeof(SmallCtl) <= 256, "control block");
 
-// First k-block of CTA c's run among W of them.
-__device__ __forceinline__ int64_t run_start(int64_t W, int c) { return W * c / (int)gridDim.x; }
+// A CTA's run of a product's units.
+struct Run {
+    int64_t W;
+    int ctas, kbs;
+    __device__ __forceinline__ Run(const Product &p)
+        : W((int64_t)p.tiles * p.kbs), ctas(p.ctas), kbs(p.kbs) {}
+    __device__ __forceinline__ int64_t start(int c) const { return c >= ctas ? W : quot(W * c, ctas); }
+    // the CTA whose run holds unit u
+    __device__ __forceinline__ int owner(int64_t u) const { return (int)quot((u + 1) * ctas - 1, W); }
+    // quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division
+    // costs some 0.3 us here)
+    static __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+        if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+        return a / b;
+    }
+};
 
 // TMEM: 16 consecutive columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -89,10 +104,178 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-template <int MATS, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1)
-stream_gemm_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs args) {
-    using G = Geo<MATS, NT>;
+// Polls a word in global memory (acquire) until (word & mask) == want.
+__device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint32_t want,
+                                          uint32_t *err) {
+    if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        __nanosleep(32);
+        if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
+        if ((spin & 15u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, MOE_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Epilogue of one product (warps 4-7): the CTA's segments, then the joins of its cut
+// tiles. MATS accumulators per segment: 2 (gate, up) or 1. seg: segments so far
+// in the launch. False when a wait gave up.
+//
+// A part is [matrix][T / 4][128 columns] vectors of four tokens, so that a lane
+// writes and reads 16 bytes at a time.
+// joined() is called once the CTA's outputs are stored, before the tickets are
+// released.
+template <int MATS, int NT, typename Joined>
+__device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p, uint32_t *ticket,
+                                         SmallCtl *ctl, uint32_t tmem_base, int &seg, Joined joined) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, T = args.T;
+    const Run run(p);
+    const int64_t begin = run.start(blockIdx.x), end = run.start(blockIdx.x + 1);
+    if (begin == end) return true;
+    const bool f16 = args.f16 != 0;
+    uint16_t *out = static_cast<uint16_t *>(p.out);
+    const int TG = (T + 3) / 4;
+    const int64_t part_ld = (int64_t)MATS * TG * 128;  // vectors of one part
+    const int first_tile = (int)(begin / p.kbs), last_tile = (int)((end - 1) / p.kbs);
+    auto emit = [&](int tile, int t, float s0, float s1) {
+        const int col = tile * 128 + q * 32 + lane;
+        const float v = MATS == 2 ? s0 * act_sigmoid(s0, args.act) * s1 : s0;
+        if (col < p.cols) out[(int64_t)t * p.cols + col] = round16(v, f16);
+    };
+    auto is_cut = [&](int tile) {
+        return begin > (int64_t)tile * p.kbs || end < (int64_t)(tile + 1) * p.kbs;
+    };
+    // a run's first tile goes to slot 0 of its CTA, a later one (its last) to slot 1
+    auto slot = [&](int c, int which) {
+        return reinterpret_cast<float4 *>(args.part) + ((int64_t)c * 2 + which) * part_ld + q * 32 + lane;
+    };
+    // the two tiles that may be cut: the runs [c0, c0 + P) that hold their units, the
+    // vectors [lo, hi) of tokens that this CTA joins, and where c0's part lies
+    struct Cut {
+        int tile, c0, P, lo, hi;
+        const float4 *first;
+    } cuts[2];
+    int ncuts = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int tile = i == 0 ? first_tile : last_tile;
+        Cut &x = cuts[i];
+        x.tile = -1;
+        if ((i == 1 && tile == first_tile) || !is_cut(tile)) continue;
+        const int64_t t0 = (int64_t)tile * p.kbs;
+        x.tile = tile;
+        x.c0 = run.owner(t0);
+        x.P = run.owner(t0 + p.kbs - 1) - x.c0 + 1;
+        const int k = blockIdx.x - x.c0;
+        x.lo = TG * k / x.P;
+        x.hi = TG * (k + 1) / x.P;
+        x.first = slot(x.c0, run.start(x.c0) == t0 ? 0 : 1);
+        ++ncuts;
+    }
+
+    for (int tile = first_tile; tile <= last_tile; ++tile, ++seg) {
+        const bool cut = is_cut(tile);
+        const int a = seg & 1;
+        if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (seg >> 1) & 1, args.err)) return false;
+        ptx::tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 2 * NT;
+        float4 *mine = cut ? slot(blockIdx.x, tile == first_tile ? 0 : 1) : nullptr;
+#pragma unroll 1
+        for (int c = 0; c < NT && c < T; c += 16) {
+            uint32_t r[MATS][16];
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) tmem_ld16(taddr + m * NT + c, r[m]);
+            if (!cut) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < T)
+                        emit(tile, c + j, __uint_as_float(r[0][j]), __uint_as_float(r[MATS - 1][j]));
+                continue;
+            }
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                    if (c + j < T)
+                        __stcg(mine + (int64_t)(m * TG + (c + j) / 4) * 128,
+                               make_float4(__uint_as_float(r[m][j]), __uint_as_float(r[m][j + 1]),
+                                           __uint_as_float(r[m][j + 2]), __uint_as_float(r[m][j + 3])));
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->tempty[a]));
+        if (cut) {
+            // low half: parts written; high half: holders that need them no more
+            const Cut &x = tile == first_tile ? cuts[0] : cuts[1];
+            __threadfence();
+            __syncwarp();
+            // (a holder with no share of the tokens needs none of them)
+            if (lane == 0) atomicAdd(ticket + tile * 4 + q, x.hi > x.lo ? 1u : 0x10001u);
+        }
+    }
+    if (ncuts == 0) return true;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Cut &x = cuts[i];
+        if (x.tile < 0 || x.lo == x.hi) continue;
+        bool ok = true;
+        if (lane == 0) ok = word_wait(ticket + x.tile * 4 + q, 0xffffu, (uint32_t)x.P, args.err);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    }
+    constexpr int kBatch = MATS == 2 ? 10 : 16;  // parts in flight
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const Cut x = i == 0 ? cuts[0] : cuts[1];
+        if (x.tile < 0) continue;
+#pragma unroll 1
+        for (int g = x.lo; g < x.hi; ++g) {
+            float sum[MATS][4] = {};
+#pragma unroll 1
+            for (int c = 0; c < x.P; c += kBatch) {
+                float4 v[MATS][kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m)
+                        v[m][j] = c + j < x.P ? __ldcg((c + j == 0 ? x.first : slot(x.c0 + c + j, 0)) +
+                                                       (int64_t)(m * TG + g) * 128)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m) {
+                        sum[m][0] += v[m][j].x;
+                        sum[m][1] += v[m][j].y;
+                        sum[m][2] += v[m][j].z;
+                        sum[m][3] += v[m][j].w;
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * g + j < T) emit(x.tile, 4 * g + j, sum[0][j], sum[MATS - 1][j]);
+        }
+    }
+    __syncwarp();  // every lane has its parts
+    // this CTA's shares are done; the last holder of a tile returns its ticket to zero
+    auto release = [&](const Cut &x) {
+        if (x.tile < 0 || x.lo == x.hi) return;
+        uint32_t *w = ticket + x.tile * 4 + q;
+        if (atomicAdd(w, 0x10000u) >> 16 == (uint32_t)(x.P - 1)) *w = 0;
+    };
+    joined();
+    if (lane == 0) {
+        release(cuts[0]);
+        release(cuts[1]);
+    }
+    return true;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant__ SmallArgs args) {
+    using G = Geo<NT>;
     constexpr int S = G::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -117,254 +300,197 @@ stream_gemm_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs args)
         ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), G::kTmem);
         ptx::tmem_relinquish();
     }
-    if (!args.early) {
-        pdl_wait();
-        pdl_trigger();
-    }
+    pdl_wait();
+    pdl_trigger();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
 
-    const int64_t W = (int64_t)args.tiles * args.kbs;
-    const int64_t begin = run_start(W, blockIdx.x), end = run_start(W, blockIdx.x + 1);
-    const int count = (int)(end - begin);
-
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------------ producer --
-        auto load_w = [&](int64_t i, uint32_t s) {
-            const int tile = (int)(i / args.kbs), kb = (int)(i - (int64_t)tile * args.kbs);
-            const uint32_t full = ptx::smem_addr(&ctl->full[s]), dst = base + s * G::kStageBytes;
-            ptx::mbar_arrive_expect_tx(full, G::kStageBytes);
-#pragma unroll
-            for (int m = 0; m < MATS; ++m) {
-                ptx::tma_load_2d(dst + m * kMat, &maps.w[m], full, tile * 128, kb * BK);
-                ptx::tma_load_2d(dst + m * kMat + kBox, &maps.w[m], full, tile * 128 + 64, kb * BK);
-            }
-        };
-        auto load_x = [&](int64_t i, uint32_t s) {
-            const int kb = (int)(i % args.kbs);
-            ptx::tma_load_2d(base + s * G::kStageBytes + MATS * kMat, &maps.x,
-                             ptx::smem_addr(&ctl->full[s]), kb * BK, 0);
-        };
-        int it = 0;
+        uint32_t it = 0;
         bool ok = true;
-        if (args.early) {
-            // the stages' weights, then (once the previous kernel has finished) its output
-            const int ahead = min(count, S);
-            for (int j = 0; j < ahead; ++j) load_w(begin + j, j);
-            pdl_wait();
-            ptx::fence_proxy_async_global();
-            for (int j = 0; j < ahead; ++j) load_x(begin + j, j);
-            it = ahead;
-        }
-        for (; it < count; ++it) {
-            const uint32_t s = it % S;
-            if (!bounded_wait(ptx::smem_addr(&ctl->empty[s]), ((it / S) & 1u) ^ 1u, args.err)) {
-                ok = false;
-                break;
+#pragma unroll
+        for (int ph = 0; ph < 2; ++ph) {
+            const Product &p = args.p[ph];
+            const Run run(p);
+            const int64_t begin = run.start(blockIdx.x);
+            const int count = (int)(run.start(blockIdx.x + 1) - begin);
+            int tile = (int)(begin / p.kbs), kb = (int)(begin - (int64_t)tile * p.kbs);
+            auto load_w = [&](uint32_t s, int tl, int k) {
+                const uint32_t full = ptx::smem_addr(&ctl->full[s]), dst = base + s * G::kStageBytes;
+                ptx::mbar_arrive_expect_tx(full, kWBytes + (ph + 1) * G::kTok);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const CUtensorMap *w = &maps.w[ph == 0 ? m : 2];
+                    const int y = ph == 0 ? k * BK : (2 * k + m) * BK;
+                    ptx::tma_load_2d(dst + m * kMat, w, full, tl * 128, y);
+                    ptx::tma_load_2d(dst + m * kMat + kBox, w, full, tl * 128 + 64, y);
+                }
+            };
+            auto load_x = [&](uint32_t s, int k) {
+                const uint32_t full = ptx::smem_addr(&ctl->full[s]);
+                const uint32_t dst = base + s * G::kStageBytes + kWBytes;
+                if (ph == 0) {
+                    ptx::tma_load_2d(dst, &maps.x, full, k * BK, 0);
+                } else {
+                    ptx::tma_load_2d(dst, &maps.h, full, 2 * k * BK, 0);
+                    ptx::tma_load_2d(dst + G::kTok, &maps.h, full, (2 * k + 1) * BK, 0);
+                }
+            };
+            auto next = [&](int &tl, int &k) {
+                if (++k == p.kbs) {
+                    k = 0;
+                    ++tl;
+                }
+            };
+            auto wait_empty = [&](uint32_t i) {
+                return bounded_wait(ptx::smem_addr(&ctl->empty[i % S]), ((i / S) & 1u) ^ 1u, args.err);
+            };
+            int done = 0;
+            if (ph == 1 && ok && count > 0) {
+                // a ring full of weights, then (once H is complete) its rows
+                const int ahead = min(count, S);
+                const uint32_t it0 = it;
+                const int kb0 = kb;
+                for (int j = 0; j < ahead && ok; ++j) {
+                    ok = wait_empty(it0 + j);
+                    if (!ok) break;
+                    load_w((it0 + j) % S, tile, kb);
+                    next(tile, kb);
+                    ++it;
+                }
+                ok = ok && word_wait(args.err + kWordGrid, 0xffffffffu, gridDim.x, args.err);
+                ptx::fence_proxy_async_global();
+                // (after a wait that gave up too: every announced byte arrives)
+                int tl = 0, k = kb0;
+                for (uint32_t i = it0; i < it; ++i) {
+                    load_x(i % S, k);
+                    next(tl, k);
+                }
+                done = ahead;
             }
-            load_w(begin + it, s);
-            load_x(begin + it, s);
+            for (int j = done; j < count && ok; ++j) {
+                ok = wait_empty(it);
+                if (!ok) break;
+                load_w(it % S, tile, kb);
+                load_x(it % S, kb);
+                next(tile, kb);
+                ++it;
+            }
         }
-        if (!ok)
-            for (int j = max(0, it - S); j < it; ++j)
+        if (!ok) {
+            // drain the loads that may still be landing in shared memory
+            const uint32_t first = it > (uint32_t)S ? it - S : 0u;
+            for (uint32_t j = first; j < it; ++j)
                 bounded_wait(ptx::smem_addr(&ctl->full[j % S]), (j / S) & 1u, args.err);
+        }
     } else if (warp == 1 && lane == 0) {
         // ---------------------------------------------------- MMA issuer --
-        int seg = -1;
-        int64_t seg_tile = -1;
+        uint32_t it = 0;
+        int seg = 0;
         bool ok = true;
-        for (int it = 0; it < count; ++it) {
-            const int64_t tile = (begin + it) / args.kbs;
-            const bool first = tile != seg_tile;
-            if (first) {
-                if (seg >= 0) ptx::tc_commit(ptx::smem_addr(&ctl->tfull[seg & 1]));
-                ++seg;
-                seg_tile = tile;
-                if (!bounded_wait(ptx::smem_addr(&ctl->tempty[seg & 1]), ((seg >> 1) & 1) ^ 1, args.err)) {
-                    ok = false;
-                    break;
+#pragma unroll
+        for (int ph = 0; ph < 2; ++ph) {
+            const Product &p = args.p[ph];
+            const Run run(p);
+            const int64_t begin = run.start(blockIdx.x);
+            const int count = (int)(run.start(blockIdx.x + 1) - begin);
+            int kb = (int)(begin % p.kbs);
+            bool first = true;
+            for (int j = 0; j < count && ok; ++j, ++it) {
+                const uint32_t s = it % S, a = seg & 1;
+                if (first) {
+                    ok = bounded_wait(ptx::smem_addr(&ctl->tempty[a]), ((seg >> 1) & 1) ^ 1, args.err);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
                 }
+                ok = bounded_wait(ptx::smem_addr(&ctl->full[s]), (it / S) & 1u, args.err);
+                if (!ok) break;
                 ptx::tc_fence_after();
-            }
-            const uint32_t s = it % S;
-            if (!bounded_wait(ptx::smem_addr(&ctl->full[s]), (it / S) & 1u, args.err)) {
-                ok = false;
-                break;
-            }
-            ptx::tc_fence_after();
-            const uint32_t sW = base + s * G::kStageBytes, sX = sW + MATS * kMat;
+                const uint32_t sW = base + s * G::kStageBytes, sX = sW + kWBytes;
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-                const uint64_t bd = ptx::desc_sw128(sX + k * 32, 16, 1024);
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m < MATS; ++m)
-                    ptx::tc_mma_f16(tmem_base + ((seg & 1) * MATS + m) * NT,
-                                    ptx::desc_sw128(sW + m * kMat + k * 2048, kBox, 1024), bd,
-                                    args.idesc, !first || k != 0);
+                    for (int k = 0; k < BK / 16; ++k) {
+                        // gate/up: two matrices, two accumulators, the same tokens; down:
+                        // two successive halves of the reduction, one accumulator
+                        const uint64_t bd =
+                            ptx::desc_sw128(sX + (ph == 0 ? 0 : m * G::kTok) + k * 32, 16, 1024);
+                        ptx::tc_mma_f16(tmem_base + a * 2 * NT + (ph == 0 ? m * NT : 0),
+                                        ptx::desc_sw128(sW + m * kMat + k * 2048, kBox, 1024), bd,
+                                        args.idesc, !first || k != 0 || (ph == 1 && m != 0));
+                    }
+                ptx::tc_commit(ptx::smem_addr(&ctl->empty[s]));
+                first = false;
+                if (++kb == p.kbs || j == count - 1) {
+                    ptx::tc_commit(ptx::smem_addr(&ctl->tfull[a]));
+                    ++seg;
+                    kb = 0;
+                    first = true;
+                }
             }
-            ptx::tc_commit(ptx::smem_addr(&ctl->empty[s]));
         }
-        if (ok && seg >= 0) ptx::tc_commit(ptx::smem_addr(&ctl->tfull[seg & 1]));
         ptx::tc_commit(ptx::smem_addr(&ctl->drain));
         bounded_wait(ptx::smem_addr(&ctl->drain), 0, args.err);
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
-        const int q = warp & 3, T = args.T;
-        const bool f16 = args.f16 != 0;
-        uint16_t *out = static_cast<uint16_t *>(args.out);
-        if (args.early) pdl_wait();  // the previous kernel's tickets and parts, and H's readers
-        const int64_t part_ld = (int64_t)MATS * T * 128;  // floats of one part
-        int64_t i = begin;
-        for (int seg = 0; i < end; ++seg) {
-            const int tile = (int)(i / args.kbs);
-            const int64_t t0 = (int64_t)tile * args.kbs, t1 = t0 + args.kbs;
-            const bool whole = i == t0 && end >= t1;
-            const int a = seg & 1;
-            if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (seg >> 1) & 1, args.err)) break;
-            ptx::tc_fence_after();
-            const uint32_t taddr =
-                tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * MATS * NT;
-            const int col = tile * 128 + q * 32 + lane;
-            // the result of one token from its sums
-            auto emit = [&](int t, float s0, float s1) {
-                const float v = MATS == 2 ? s0 * act_sigmoid(s0, args.act) * s1 : s0;
-                if (col < args.cols) out[(int64_t)t * args.cols + col] = round16(v, f16);
-            };
-            // part of CTA c for this tile: a run's first tile goes to slot 0, a
-            // later one (its last) to slot 1
-            auto slot = [&](int c) {
-                const int64_t b = run_start(W, c);
-                return args.part + ((int64_t)c * 2 + (b / args.kbs == tile ? 0 : 1)) * part_ld +
-                       q * 32 + lane;
-            };
-            float *mine = whole ? nullptr : slot(blockIdx.x);
-#pragma unroll 1
-            for (int c = 0; c < NT && c < T; c += 16) {
-                uint32_t r[MATS][16];
-#pragma unroll
-                for (int m = 0; m < MATS; ++m) tmem_ld16(taddr + m * NT + c, r[m]);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (c + j >= T) break;
-                    if (whole) {
-                        emit(c + j, __uint_as_float(r[0][j]), __uint_as_float(r[MATS - 1][j]));
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < MATS; ++m)
-                            __stcg(mine + (int64_t)(m * T + c + j) * 128, __uint_as_float(r[m][j]));
-                    }
-                }
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->tempty[a]));
-            if (!whole) {
-                // the runs that hold k-blocks of this tile
-                int c0 = (int)(t0 * (int)gridDim.x / W), c1;
-                while (run_start(W, c0 + 1) <= t0) ++c0;
-                c1 = c0;
-                while (run_start(W, c1 + 1) < t1) ++c1;
-                __threadfence();
-                __syncwarp();
-                uint32_t arrived = 0;
-                uint32_t *ticket = args.ticket + tile * 4 + q;
-                if (lane == 0) arrived = atomicAdd(ticket, 1u);
-                arrived = __shfl_sync(0xffffffffu, arrived, 0);
-                if (arrived == (uint32_t)(c1 - c0)) {  // the last part
-                    __threadfence();
-#pragma unroll 1
-                    for (int t = 0; t < T; t += 16) {
-                        float sum[MATS][16];
-#pragma unroll
-                        for (int m = 0; m < MATS; ++m)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) sum[m][j] = 0.f;
-#pragma unroll 2
-                        for (int c = c0; c <= c1; ++c) {
-                            const float *p = slot(c) + (int64_t)t * 128;
-#pragma unroll
-                            for (int m = 0; m < MATS; ++m)
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (t + j < T) sum[m][j] += __ldcg(p + (int64_t)(m * T + j) * 128);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (t + j < T) emit(t + j, sum[0][j], sum[MATS - 1][j]);
-                    }
-                    if (lane == 0) *ticket = 0;
-                }
-            }
-            i = min(end, t1);
-        }
-    }
-    // the next kernel may start its own loads once this one is past its main loop
-    if (args.early) {
-        if (warp != 0 && warp < 4) pdl_wait();
-        pdl_trigger();
+        int seg = 0;
+        bool arrived = false;
+        auto arrive = [&] {
+            if (arrived) return;
+            arrived = true;
+            // this CTA's part of H is complete and visible to the loads of all SMs
+            ptx::fence_proxy_async_global();
+            __threadfence();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (warp == 4 && lane == 0) atomicAdd(args.err + kWordGrid, 1u);
+        };
+        const bool ok = epilogue<2, NT>(args, args.p[0], args.ticket, ctl, tmem_base, seg, arrive);
+        arrive();  // (without a cut tile, or after a wait that gave up)
+        if (ok)
+            epilogue<1, NT>(args, args.p[1], args.ticket + 4 * args.p[0].tiles, ctl, tmem_base, seg,
+                            [] {});
     }
 
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 2) ptx::tmem_dealloc(tmem_base, G::kTmem);
+    if (tid == 0) {
+        // the last CTA to leave returns the grid's counters to zero
+        __threadfence();
+        if (atomicAdd(args.err + kWordExit, 1u) == gridDim.x - 1) {
+            args.err[kWordGrid] = 0;
+            args.err[kWordExit] = 0;
+        }
+    }
 }
 
-template <int MATS, int NT>
+template <int NT>
 cudaError_t launch_nt(const SmallMaps &maps, SmallArgs args, int grid, cudaStream_t s) {
-    constexpr size_t kSmem = Geo<MATS, NT>::kSmem;
+    constexpr size_t kSmem = Geo<NT>::kSmem;
     args.idesc = idesc(args.f16 != 0, 128, NT, true, false);
-    const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(stream_gemm_kernel<MATS, NT>), (int)kSmem);
+    const cudaError_t e =
+        ensure_dynamic_smem(reinterpret_cast<const void *>(stream_ffn_kernel<NT>), (int)kSmem);
     if (e != cudaSuccess) return e;
-    return launch_k(stream_gemm_kernel<MATS, NT>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
+    return launch_k(stream_ffn_kernel<NT>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
 }
 
 int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
-// CTAs of one product: one per SM, fewer where a run would be under four k-blocks
-// (then the joining costs more than the shorter runs save).
-int stream_grid(int cols, int K, int sms) {
-    const int64_t tiles = (cols + 127) / 128, W = tiles * ((K + BK - 1) / BK);
-    return (int)std::min<int64_t>(std::min(sms, kFfnMaxCtas), std::max(tiles, W / 4));
-}
-
-cudaError_t launch_stream(int mats, const void *w0, const void *w1, const void *x, int T, int K,
-                          int cols, int act, bool f16, bool early, void *out, float *part,
-                          uint32_t *ticket, uint32_t *err, cudaStream_t s) {
-    const int nt = padded_tokens(T);
-    SmallMaps m{};
-    const CUtensorMapDataType ty = map_type(f16);
-    if (!make_map(&m.w[0], ty, w0, cols, K, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&m.w[1], ty, w1, cols, K, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&m.x, ty, x, K, T, 64, nt, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    SmallArgs a{};
-    a.T = T;
-    a.cols = cols;
-    a.kbs = (K + BK - 1) / BK;
-    a.tiles = (cols + 127) / 128;
-    a.act = act;
-    a.f16 = f16;
-    a.early = early;
-    a.out = out;
-    a.part = part;
-    a.ticket = ticket;
-    a.err = err;
-    const int grid = stream_grid(cols, K, sm_count());
-#define MOE_CASE(N)                                                      \
-    case N:                                                              \
-        return mats == 2 ? launch_nt<2, N>(m, a, grid, s) : launch_nt<1, N>(m, a, grid, s)
-    switch (nt) {
-        MOE_CASE(16);
-        MOE_CASE(32);
-        MOE_CASE(64);
-        default:
-            MOE_CASE(128);
-    }
-#undef MOE_CASE
+// A product whose units are 32 KB of weights, on one CTA per SM, fewer where a run
+// would be under two units (then the joining costs more than the shorter runs save).
+Product make_product(int cols, int K, int depth, int sms, void *out) {
+    Product p;
+    p.cols = cols;
+    p.kbs = (K + depth - 1) / depth;
+    p.tiles = (cols + 127) / 128;
+    p.ctas = (int)std::min<int64_t>(std::min(sms, kFfnMaxCtas),
+                                    std::max<int64_t>(p.tiles, (int64_t)p.tiles * p.kbs / 2));
+    p.out = out;
+    return p;
 }
 
 }  // namespace
@@ -374,17 +500,38 @@ using namespace ffn;
 
 size_t ffn_stream_part_bytes(int T, int d, int n) {
     // two parts for each CTA, of two matrices in the first product
-    const size_t ctas = std::max(2 * stream_grid(n, d, kFfnMaxCtas), stream_grid(d, n, kFfnMaxCtas));
-    return ctas * 2 * T * 128 * sizeof(float);
+    const size_t ctas = std::max(2 * make_product(n, d, BK, kFfnMaxCtas, nullptr).ctas,
+                                 make_product(d, n, 2 * BK, kFfnMaxCtas, nullptr).ctas);
+    return ctas * 2 * ((T + 3) / 4) * 128 * 4 * sizeof(float);
 }
 
 cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, const void *W2, int T,
                               int d, int n, int act, bool f16, void *H, void *Y, float *part,
                               uint32_t *ticket, uint32_t *err, cudaStream_t s) {
-    cudaError_t e = launch_stream(2, W1, W3, X, T, d, n, act, f16, false, H, part, ticket, err, s);
-    if (e != cudaSuccess) return e;
-    // the second product touches the parts and tickets only after the first is done
-    return launch_stream(1, W2, W2, H, T, n, d, act, f16, true, Y, part, ticket, err, s);
+    const int nt = padded_tokens(T);
+    SmallMaps m{};
+    const CUtensorMapDataType ty = map_type(f16);
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_map(&m.w[0], ty, W1, n, d, 64, BK, sw) || !make_map(&m.w[1], ty, W3, n, d, 64, BK, sw) ||
+        !make_map(&m.w[2], ty, W2, d, n, 64, BK, sw) || !make_map(&m.x, ty, X, d, T, 64, nt, sw) ||
+        !make_map(&m.h, ty, H, n, T, 64, nt, sw))
+        return cudaErrorInvalidValue;
+    SmallArgs a{};
+    a.p[0] = make_product(n, d, BK, sm_count(), H);
+    a.p[1] = make_product(d, n, 2 * BK, sm_count(), Y);
+    a.T = T;
+    a.act = act;
+    a.f16 = f16;
+    a.part = part;
+    a.ticket = ticket;
+    a.err = err;
+    const int grid = std::max(a.p[0].ctas, a.p[1].ctas);
+    switch (nt) {
+        case 16: return launch_nt<16>(m, a, grid, s);
+        case 32: return launch_nt<32>(m, a, grid, s);
+        case 64: return launch_nt<64>(m, a, grid, s);
+        default: return launch_nt<128>(m, a, grid, s);
+    }
 }
 
 }  // namespace moe
