@@ -14,7 +14,10 @@ EPS = 1e-5
 SHAPES = [(1, 1, 1), (3, 2, 2), (5, 7, 9), (2, 8, 8), (33, 33, 33), (4, 64, 72), (9, 256, 256),
           (1000, 264, 264), (7, 1000, 1003), (257, 1023, 1023), (3, 1536, 1536), (700, 2048, 2048),
           (5, 4095, 4098), (2, 4096, 4096), (310, 4104, 4104), (3, 8191, 8191), (3, 8192, 8192),
-          (2, 8193, 8200), (5, 12288, 12288)]
+          (2, 8193, 8200), (5, 12288, 12288),
+          # several rows a group, past the ring's length
+          (9000, 264, 264), (3000, 1000, 1024), (1500, 2048, 2048), (1300, 4104, 4104),
+          (1000, 7168, 7168), (330, 12288, 12296), (2000, 999, 999)]
 TYPES = [(BF, BF), (BF, FP), (HF, HF), (HF, FP), (FP, FP)]
 
 

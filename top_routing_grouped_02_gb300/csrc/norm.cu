@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "elem.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -51,6 +52,7 @@ struct LnArgs {
     int w32;  // gamma, beta (and their gradients) are fp32, else x's type
     float eps;
     int wpr;  // warps per row
+    int stages;  // ring stages per row group
     // backward
     const void *dy, *dres;
     void *dx;
@@ -71,6 +73,43 @@ __device__ __forceinline__ int warp_count(int w, int nvec, int tpr) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) n += min(max(nvec - (i * tpr + w * 32), 0), 32);
     return n * V;
+}
+
+// A block's partial sums dgamma, dbeta: each thread's columns, the groups added in
+// order through acc ([2][d] in shared memory, used with several groups).
+template <int V, int NV>
+__device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int group, int tpr, int t,
+                                               const bool (&ok)[NV], const float (&dg)[V * NV],
+                                               const float (&db)[V * NV], float *acc) {
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+    if (groups == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i])
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int c = (i * tpr + t) * V + j;
+                    part[c] = dg[i * V + j];
+                    part[a.d + c] = db[i * V + j];
+                }
+        return;
+    }
+    __syncthreads();
+    for (int k = 0; k < groups; ++k) {
+        if (group == k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (ok[i])
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int c = (i * tpr + t) * V + j;
+                        acc[c] = (k ? acc[c] : 0.f) + dg[i * V + j];
+                        acc[a.d + c] = (k ? acc[a.d + c] : 0.f) + db[i * V + j];
+                    }
+        }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) part[c] = acc[c];
 }
 
 template <typename T, int V, int NV>
@@ -265,34 +304,286 @@ __global__ void __launch_bounds__(1024, 1) ln_backward_kernel(const LnArgs a) {
             }
     }
     if (a.part == nullptr) return;
-    float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
-    if (groups == 1) {
+    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, acc_sh);
+}
+
+// ---- rows on 16-byte boundaries: a ring of rows in shared memory -----------------
+//
+// Each row group keeps a ring of its next rows in shared memory, filled by bulk
+// copies (cp.async.bulk, one thread of the group, completion on an mbarrier), so
+// that the loads in flight do not depend on how far the group's arithmetic is and
+// take no registers. A stage is refilled after the group's next barrier: by then
+// every thread has read it.
+
+// Bytes of the control block in front of the rings: barriers and statistics.
+constexpr int kRingStages = 8;  // most
+constexpr int kMaxGroups = 28;
+struct RingCtl {
+    uint64_t full[kMaxGroups][kRingStages];
+    float2 stat[2][32];
+};
+constexpr int kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+// Waits for a stage; gives up after about a second (the copies were issued by this
+// block, so only a device that has stopped would get there).
+__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) return;
+}
+
+template <typename T, int V, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a) {
+    extern __shared__ __align__(128) uint8_t ring_sh[];
+    RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
+    constexpr int EPT = V * NV;
+    const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+    const int w0 = group * a.wpr, wg = warp - w0;
+    const int groups = blockDim.x / tpr, S = a.stages;
+    const int nvec = a.d / V;
+    const uint32_t row_bytes = (uint32_t)a.d * sizeof(T);
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    uint8_t *ring = ring_sh + kRingCtl + (size_t)group * S * row_bytes;
+    const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
+        ptx::fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    auto fetch = [&](int64_t r, int s) {
+        ptx::mbar_arrive_expect_tx(bar0 + 8 * s, row_bytes);
+        ptx::bulk_load(ptx::smem_addr(ring + (size_t)s * row_bytes),
+                       static_cast<const T *>(a.x) + r * a.ldx, row_bytes, bar0 + 8 * s);
+    };
+    if (t == 0)
+        for (int s = 0; s < S && row + s * stride < a.T; ++s) fetch(row + s * stride, s);
+
+    bool ok[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
+    float gm[EPT], bt[EPT];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (i * tpr + t) * V + j;
+            gm[i * V + j] = ok[i] ? load_w<T>(a.gamma, a.w32, c, 1.f) : 0.f;
+            bt[i * V + j] = ok[i] ? load_w<T>(a.beta, a.w32, c, 0.f) : 0.f;
+        }
+    const float inv_d = 1.f / (float)a.d;
+    const int n_own = warp_count<V, NV>(wg, nvec, tpr);
+    const float inv_own = n_own > 0 ? 1.f / (float)n_own : 0.f;
+    const float n_lane = lane < a.wpr ? (float)warp_count<V, NV>(lane, nvec, tpr) : 0.f;
+
+    int s = 0;
+    uint32_t ph = 0;
+    for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
+        ring_wait(bar0 + 8 * s, ph);
+        const Raw<T, V> *src = reinterpret_cast<const Raw<T, V> *>(ring + (size_t)s * row_bytes);
+        float f[EPT];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (ok[i]) {
+                to_f32<T, V>(src[i * tpr + t], f + i * V);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[i * V + j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += f[i * V + j];
+        }
+        float mean = warp_sum(sum) * inv_own;
+        float m2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (ok[i])
+            if (ok[i]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const int c = (i * tpr + t) * V + j;
-                    part[c] = dg[i * V + j];
-                    part[a.d + c] = db[i * V + j];
+                    const float c = f[i * V + j] - mean;
+                    m2 = fmaf(c, c, m2);
                 }
-        return;
-    }
-    for (int k = 0; k < groups; ++k) {
-        if (group == k) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (ok[i])
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const int c = (i * tpr + t) * V + j;
-                        acc_sh[c] = (k ? acc_sh[c] : 0.f) + dg[i * V + j];
-                        acc_sh[a.d + c] = (k ? acc_sh[a.d + c] : 0.f) + db[i * V + j];
-                    }
+            }
+        m2 = warp_sum(m2);
+        if (a.wpr > 1) {
+            if (lane == 0) ctl->stat[buf][warp] = make_float2(mean, m2);
+            group_sync(1 + group, tpr);
+        } else {
+            __syncwarp();
         }
-        __syncthreads();
+        // every thread of the group has read the stage
+        if (t == 0 && row + S * stride < a.T) fetch(row + S * stride, s);
+        if (++s == S) {
+            s = 0;
+            ph ^= 1;
+        }
+        if (a.wpr > 1) {
+            const float2 o = lane < a.wpr ? ctl->stat[buf][w0 + lane] : make_float2(0.f, 0.f);
+            mean = warp_sum(n_lane * o.x) * inv_d;
+            const float c = o.x - mean;
+            m2 = warp_sum(lane < a.wpr && n_lane > 0.f ? fmaf(n_lane * c, c, o.y) : 0.f);
+        }
+        const float rstd = __frsqrt_rn(fmaf(m2, inv_d, a.eps));
+        T *yp = static_cast<T *>(a.y) + row * a.ldy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+                float o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    o[j] = fmaf((f[i * V + j] - mean) * rstd, gm[i * V + j], bt[i * V + j]);
+                reinterpret_cast<Raw<T, V> *>(yp)[i * tpr + t] = from_f32<T, V>(o);
+            }
+        if (t == 0) {
+            if (a.mean != nullptr) a.mean[row] = mean;
+            if (a.rstd != nullptr) a.rstd[row] = rstd;
+        }
     }
-    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) part[c] = acc_sh[c];
+}
+
+template <typename T, int V, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs a) {
+    extern __shared__ __align__(128) uint8_t ring_sh[];
+    RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
+    constexpr int EPT = V * NV;
+    const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+    const int w0 = group * a.wpr;
+    const int groups = blockDim.x / tpr, S = a.stages;
+    const int nvec = a.d / V;
+    const uint32_t row_bytes = (uint32_t)a.d * sizeof(T);
+    const bool has_res = a.dres != nullptr;
+    const uint32_t stage_bytes = (has_res ? 3 : 2) * row_bytes;
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    // gamma in fp32 for all groups, then the rings; later the sums of the groups
+    float *gsh = reinterpret_cast<float *>(ring_sh + kRingCtl);
+    uint8_t *rings = ring_sh + kRingCtl + (size_t)a.d * sizeof(float);
+    uint8_t *ring = rings + (size_t)group * S * stage_bytes;
+    const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
+        ptx::fence_barrier_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) gsh[c] = load_w<T>(a.gamma, a.w32, c, 1.f);
+    __syncthreads();
+    auto fetch = [&](int64_t r, int s) {
+        const uint32_t dst = ptx::smem_addr(ring + (size_t)s * stage_bytes), bar = bar0 + 8 * s;
+        ptx::mbar_arrive_expect_tx(bar, stage_bytes);
+        ptx::bulk_load(dst, static_cast<const T *>(a.x) + r * a.ldx, row_bytes, bar);
+        ptx::bulk_load(dst + row_bytes, static_cast<const T *>(a.dy) + r * a.lddy, row_bytes, bar);
+        if (has_res)
+            ptx::bulk_load(dst + 2 * row_bytes, static_cast<const T *>(a.dres) + r * a.lddres, row_bytes, bar);
+    };
+    if (t == 0)
+        for (int s = 0; s < S && row + s * stride < a.T; ++s) fetch(row + s * stride, s);
+
+    bool ok[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
+    float dg[EPT], db[EPT];
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) dg[e] = db[e] = 0.f;
+    const float inv_d = 1.f / (float)a.d;
+    float m_next = 0.f, r_next = 0.f;
+    if (row < a.T) {
+        m_next = a.mean[row];
+        r_next = a.rstd[row];
+    }
+    auto gamma_of = [&](int i, float (&g)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(gsh + (i * tpr + t) * V + j);
+            g[j] = v.x;
+            g[j + 1] = v.y;
+            g[j + 2] = v.z;
+            g[j + 3] = v.w;
+        }
+    };
+
+    int s = 0, s_prev = -1;
+    uint32_t ph = 0;
+    for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
+        const float mean = m_next, rstd = r_next;
+        if (row + stride < a.T) {
+            m_next = a.mean[row + stride];
+            r_next = a.rstd[row + stride];
+        }
+        ring_wait(bar0 + 8 * s, ph);
+        const Raw<T, V> *px = reinterpret_cast<const Raw<T, V> *>(ring + (size_t)s * stage_bytes);
+        const Raw<T, V> *py = px + nvec, *pr = py + nvec;
+        const float shift = -mean * rstd;
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+                float x[V], y[V], g[V];
+                to_f32<T, V>(px[i * tpr + t], x);
+                to_f32<T, V>(py[i * tpr + t], y);
+                gamma_of(i, g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int e = i * V + j;
+                    const float xh = (x[j] - mean) * rstd;
+                    db[e] += y[j];
+                    dg[e] = fmaf(y[j], xh, dg[e]);
+                    const float gy = y[j] * g[j];
+                    s2 += gy;
+                    s1 = fmaf(gy, xh, s1);
+                }
+            }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (a.wpr > 1) {
+            if (lane == 0) ctl->stat[buf][warp] = make_float2(s1, s2);
+            group_sync(1 + group, tpr);
+        } else {
+            __syncwarp();
+        }
+        // every thread of the group is done with the previous row's stage
+        if (t == 0 && s_prev >= 0 && row + (S - 1) * stride < a.T) fetch(row + (S - 1) * stride, s_prev);
+        if (a.wpr > 1) {
+            const float2 o = lane < a.wpr ? ctl->stat[buf][w0 + lane] : make_float2(0.f, 0.f);
+            s1 = warp_sum(o.x);
+            s2 = warp_sum(o.y);
+        }
+        const float c1 = s1 * inv_d, c2 = s2 * inv_d;
+        T *pd = static_cast<T *>(a.dx) + row * a.lddx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i]) {
+                float x[V], y[V], g[V];
+                to_f32<T, V>(px[i * tpr + t], x);
+                to_f32<T, V>(py[i * tpr + t], y);
+                gamma_of(i, g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (x[j] - mean) * rstd;
+                    x[j] = rstd * (fmaf(-c1, xh, y[j] * g[j]) - c2);
+                }
+                if (has_res) {
+                    to_f32<T, V>(pr[i * tpr + t], y);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) x[j] += y[j];
+                }
+                reinterpret_cast<Raw<T, V> *>(pd)[i * tpr + t] = from_f32<T, V>(x);
+            }
+        s_prev = s;
+        if (++s == S) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+    if (a.part == nullptr) return;
+    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, reinterpret_cast<float *>(rings));
 }
 
 // dgamma[c], dbeta[c] = the sum of P partial rows, each thread row q of the block
@@ -456,6 +747,10 @@ __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
 
 // Widest row of the register kernels: 32 warps of 8 elements a thread.
 constexpr int kRegWidth = 8192;
+// Aligned rows: up to kNarrow elements 8 a thread, beyond 16 (fewer warps share a
+// row, so fewer shuffles and shorter barriers); widest row that 28 warps hold.
+constexpr int kNarrow = 1024;
+constexpr int kRingWidth = 28 * 32 * 16;
 // Threads of a backward block: as many row groups as fit, so that there is one
 // partial row of weight gradients per SM.
 constexpr int kBwdThreads = 1024;
@@ -503,22 +798,77 @@ cudaError_t backward_regs(LnArgs a, int *P, cudaStream_t s) {
     return launch_k(ln_backward_kernel<T, V, NV>, dim3(grid), dim3(threads), smem, s, a);
 }
 
+// Row groups and ring stages of a block of at most max_threads threads (one block
+// per SM), with at most T / SMs rounded up groups so that few rows spread over the
+// SMs. False where two stages of one group do not fit the shared memory.
+constexpr size_t kRingSmem = 224 * 1024;
+bool ring_shape(LnArgs &a, int per_row, int max_threads, size_t fixed, size_t stage, int *groups) {
+    a.wpr = (a.d + per_row * 32 - 1) / (per_row * 32);
+    if (a.wpr * 32 > max_threads) return false;
+    int g = std::min(row_groups(a.wpr, max_threads), a.wpr > 1 ? 15 : kMaxGroups);
+    g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
+    while (g > 1 && fixed + 2 * g * stage > kRingSmem) --g;
+    const int64_t s = (int64_t)(kRingSmem - std::min(fixed, kRingSmem)) / (int64_t)(g * stage);
+    if (s < 2) return false;
+    a.stages = (int)std::min<int64_t>(s, kRingStages);
+    *groups = g;
+    return true;
+}
+
+template <typename T, int V, int NV, int MAXT>
+cudaError_t forward_ring(LnArgs a, bool *fits, cudaStream_t s) {
+    int groups;
+    const size_t stage = (size_t)a.d * sizeof(T);
+    *fits = ring_shape(a, V * NV, MAXT, kRingCtl, stage, &groups);
+    if (!*fits) return cudaSuccess;
+    const size_t smem = kRingCtl + groups * a.stages * stage;
+    const cudaError_t e = ensure_dynamic_smem(
+        reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV, MAXT>), (int)kRingSmem);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, sm_count());
+    return launch_k(ln_forward_ring_kernel<T, V, NV, MAXT>, dim3(grid), dim3(groups * a.wpr * 32),
+                    smem, s, a);
+}
+
+template <typename T, int V, int NV, int MAXT>
+cudaError_t backward_ring(LnArgs a, int *P, bool *fits, cudaStream_t s) {
+    int groups;
+    const size_t stage = (size_t)a.d * sizeof(T) * (a.dres != nullptr ? 3 : 2);
+    const size_t fixed = kRingCtl + (size_t)a.d * sizeof(float);
+    *fits = ring_shape(a, V * NV, MAXT, fixed, stage, &groups);
+    if (!*fits) return cudaSuccess;
+    // (two stages of 16-bit x and dy hold the groups' [2][d] fp32 sums)
+    const size_t smem = fixed + groups * a.stages * stage;
+    const cudaError_t e = ensure_dynamic_smem(
+        reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV, MAXT>), (int)kRingSmem);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(sm_count(), kLnPartials));
+    *P = grid;
+    return launch_k(ln_backward_ring_kernel<T, V, NV, MAXT>, dim3(grid), dim3(groups * a.wpr * 32),
+                    smem, s, a);
+}
+
 template <typename T>
 cudaError_t forward_type(const LnArgs &a, const Align &al, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);  // elements of a 16-byte vector
-    if (a.d > kRegWidth) {
+    if (al.fits(16) && a.d <= kRingWidth) {
+        bool fits = false;
+        cudaError_t e;
+        if constexpr (sizeof(T) == 4)
+            e = a.d <= kNarrow ? forward_ring<T, 4, 2, 512>(a, &fits, s) : forward_ring<T, 4, 4, 512>(a, &fits, s);
+        else
+            e = a.d <= kNarrow ? forward_ring<T, 8, 1, 896>(a, &fits, s) : forward_ring<T, 8, 2, 896>(a, &fits, s);
+        if (e != cudaSuccess || fits) return e;
+    }
+    if (a.d > kRegWidth || al.fits(16)) {
         const int grid = (int)std::min<int64_t>(a.T, 2 * sm_count());
         return al.fits(16) ? launch_k(ln_forward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
                            : launch_k(ln_forward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
     }
-    if constexpr (sizeof(T) == 4) {
-        if (a.d <= kRegWidth / 2)
-            return al.fits(16) ? forward_regs<T, 4, 1>(a, s) : forward_regs<T, 1, 4>(a, s);
-        return al.fits(16) ? forward_regs<T, 4, 2>(a, s) : forward_regs<T, 1, 8>(a, s);
-    } else {
-        if (al.fits(16)) return forward_regs<T, 8, 1>(a, s);
+    if constexpr (sizeof(T) == 4)
+        return a.d <= kRegWidth / 2 ? forward_regs<T, 1, 4>(a, s) : forward_regs<T, 1, 8>(a, s);
+    else
         return al.fits(4) ? forward_regs<T, 2, 4>(a, s) : forward_regs<T, 1, 8>(a, s);
-    }
 }
 
 template <typename T>
@@ -527,7 +877,19 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
     constexpr int W = 16 / sizeof(T);
     cudaError_t e;
     int P = 0;
-    if (a.d > kRegWidth) {
+    bool fits = false;
+    if (al.fits(16) && a.d <= kRingWidth) {
+        if constexpr (sizeof(T) == 4)
+            e = a.d <= kNarrow ? backward_ring<T, 4, 2, 512>(a, &P, &fits, s)
+                               : backward_ring<T, 4, 4, 512>(a, &P, &fits, s);
+        else
+            e = a.d <= kNarrow ? backward_ring<T, 8, 1, 896>(a, &P, &fits, s)
+                               : backward_ring<T, 8, 2, 896>(a, &P, &fits, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (fits) {
+        e = cudaSuccess;
+    } else if (a.d > kRegWidth || al.fits(16)) {
         const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.T, 2 * sm_count()));
         e = al.fits(16) ? launch_k(ln_backward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
                         : launch_k(ln_backward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
@@ -538,13 +900,9 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
         e = al.fits(16) ? launch_k(ln_weight_wide_kernel<T, W>, g, dim3(256), 0, s, a)
                         : launch_k(ln_weight_wide_kernel<T, 1>, g, dim3(256), 0, s, a);
     } else if constexpr (sizeof(T) == 4) {
-        if (a.d <= kRegWidth / 2)
-            e = al.fits(16) ? backward_regs<T, 4, 1>(a, &P, s) : backward_regs<T, 1, 4>(a, &P, s);
-        else
-            e = al.fits(16) ? backward_regs<T, 4, 2>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
+        e = a.d <= kRegWidth / 2 ? backward_regs<T, 1, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
     } else {
-        if (al.fits(16)) e = backward_regs<T, 8, 1>(a, &P, s);
-        else e = al.fits(4) ? backward_regs<T, 2, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
+        e = al.fits(4) ? backward_regs<T, 2, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
     }
     if (e != cudaSuccess || a.part == nullptr) return e;
     return launch_k(ln_weight_reduce_kernel<T>, dim3((2 * a.d + 31) / 32), dim3(256), 0, s,

@@ -589,35 +589,39 @@ def _raw_stream(stream, device) -> int:
 def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
     """(pointer, row stride, rows, row length) of a CUDA tensor seen as a matrix of
     rows along its last dimension: contiguous, or 2-D with unit inner stride."""
-    if not t.is_cuda or t.dtype not in _DTYPES or t.dim() < 1:
+    if not t.is_cuda or t.dtype not in _DTYPES or not t.dim():
         raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+    shape = t.shape
+    if like is not None and (shape != like.shape or t.dtype != like.dtype):
         raise ValueError(f"{name} must have shape {tuple(like.shape)} and type {like.dtype}")
-    d = t.shape[-1]
+    d = shape[-1]
     if d == 0:
         raise ValueError(f"{name} has rows of length 0")
     if t.is_contiguous():
         return t.data_ptr(), d, t.numel() // d, d
-    if t.dim() != 2 or (d > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < d):
+    if t.dim() != 2 or (d > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < d):
         raise ValueError(f"{name} must be contiguous or a matrix of non-overlapping rows")
-    return t.data_ptr(), t.stride(0), t.shape[0], d
+    return t.data_ptr(), t.stride(0), shape[0], d
 
 
-def _vec(t: torch.Tensor | None, d: int, dtypes, name: str):
+def _out(t, like, d, name):
+    """(tensor, pointer, row stride) of an output: `t`, or a new contiguous tensor."""
+    if t is None:
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return t, t.data_ptr(), d
+    ptr, ld, _, _ = _rows(t, name, like)
+    return t, ptr, ld
+
+
+def _vec(t: torch.Tensor | None, d: int, dtype, name: str):
+    """Pointer of a contiguous vector of d elements of x's dtype or fp32."""
     if t is None:
         return None
-    if not t.is_cuda or t.dim() != 1 or t.shape[0] != d or (d > 1 and t.stride(0) != 1):
+    if not t.is_cuda or t.dim() != 1 or t.shape[0] != d or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA vector of {d}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be of type {dtypes}, got {t.dtype}")
+    if t.dtype != dtype and t.dtype != torch.float32:
+        raise TypeError(f"{name} must be {dtype} or fp32, got {t.dtype}")
     return t.data_ptr()
-
-
-def _wtype(x: torch.Tensor, gamma, beta):
-    w = gamma if gamma is not None else beta
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise TypeError("gamma and beta must have one type")
-    return x.dtype if w is None else w.dtype
 
 
 def moe_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False, y=None,
@@ -626,19 +630,21 @@ def moe_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = Fal
     fp32, or None); stats=True: (y, mean, rstd), the fp32 row statistics that the
     backward takes."""
     px, ldx, T, d = _rows(x, "x")
-    if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    py, ldy, _, _ = _rows(y, "y", x)
-    wt = _wtype(x, gamma, beta)
-    kinds = (x.dtype, torch.float32)
-    mean = rstd = None
+    dtype, device = x.dtype, x.device
+    pg, pb = _vec(gamma, d, dtype, "gamma"), _vec(beta, d, dtype, "beta")
+    w = gamma if gamma is not None else beta
+    if pg is not None and pb is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have one type")
+    y, py, ldy = _out(y, x, d, "y")
+    mean = rstd = pm = pr = None
     if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-    st = lib().moe_layernorm_forward(
-        px, ldx, _vec(gamma, d, kinds, "gamma"), _vec(beta, d, kinds, "beta"), T, d, eps,
-        _DTYPES[x.dtype], _DTYPES[wt], py, ldy, mean.data_ptr() if stats else None,
-        rstd.data_ptr() if stats else None, _raw_stream(stream, x.device))
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
+    ty = _DTYPES[dtype]
+    st = lib().moe_layernorm_forward(px, ldx, pg, pb, T, d, eps, ty,
+                                     ty if w is None else _DTYPES[w.dtype], py, ldy, pm, pr,
+                                     _raw_stream(stream, device))
     if st != MOE_OK:
         raise MoeError("moe_layernorm_forward", st)
     return (y, mean, rstd) if stats else y
@@ -652,9 +658,7 @@ def moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=None, wdtype=None, dx=
     px, ldx, T, d = _rows(x, "x")
     pdy, lddy, _, _ = _rows(dy, "dy", x)
     pres, ldres = (None, 0) if dres is None else _rows(dres, "dres", x)[:2]
-    if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    pdx, lddx, _, _ = _rows(dx, "dx", x)
+    dx, pdx, lddx = _out(dx, x, d, "dx")
     wt = gamma.dtype if gamma is not None else wdtype or torch.float32
     if wt not in (x.dtype, torch.float32):
         raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wt}")
@@ -666,7 +670,7 @@ def moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=None, wdtype=None, dx=
         scratch = torch.empty(lib().moe_layernorm_scratch_bytes(T, d), dtype=torch.uint8,
                               device=x.device)
     st = lib().moe_layernorm_backward(
-        pdy, lddy, px, ldx, _vec(gamma, d, (x.dtype, torch.float32), "gamma"), mean.data_ptr(),
+        pdy, lddy, px, ldx, _vec(gamma, d, x.dtype, "gamma"), mean.data_ptr(),
         rstd.data_ptr(), pres, ldres, T, d, _DTYPES[x.dtype], _DTYPES[wt], pdx, lddx,
         grads.data_ptr(), grads.data_ptr() + d * grads.element_size(), scratch.data_ptr(),
         scratch.numel(), _raw_stream(stream, x.device))
@@ -681,9 +685,7 @@ def moe_dropout(x, p: float, seed: int, offset: int = 0, residual=None, offset_d
     moe.h; offset_dev: a one-element int64 CUDA tensor added to offset."""
     px, ldx, T, d = _rows(x, "x")
     pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", x)[:2]
-    if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    py, ldy, _, _ = _rows(y, "y", x)
+    y, py, ldy = _out(y, x, d, "y")
     st = lib().moe_dropout(px, ldx, pr, ldr, T, d, p, seed, offset, _counter(offset_dev),
                            _DTYPES[x.dtype], py, ldy, _raw_stream(stream, x.device))
     if st != MOE_OK:
@@ -695,9 +697,7 @@ def moe_dropout_backward(dy, p: float, seed: int, offset: int = 0, offset_dev=No
                          stream=None):
     """The gradient of moe_dropout with respect to x (the residual's is dy)."""
     pdy, lddy, T, d = _rows(dy, "dy")
-    if dx is None:
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    pdx, lddx, _, _ = _rows(dx, "dx", dy)
+    dx, pdx, lddx = _out(dx, dy, d, "dx")
     st = lib().moe_dropout_backward(pdy, lddy, T, d, p, seed, offset, _counter(offset_dev),
                                     _DTYPES[dy.dtype], pdx, lddx, _raw_stream(stream, dy.device))
     if st != MOE_OK:
