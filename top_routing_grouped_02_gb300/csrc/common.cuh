@@ -210,7 +210,7 @@ cudaError_t launch_combine_rows(const __nv_bfloat16 *Z, const int32_t *row_map,
 
 // Layer norm (norm.cu); w32: gamma, beta and their gradients are fp32, else of
 // `type`. part: ln_partials(T) * 2 * d floats of scratch.
-constexpr int kLnPartials = 256;
+constexpr int kLnPartials = 384;
 int ln_partials(int64_t T);
 cudaError_t launch_layernorm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta,
                                      void *y, int64_t ldy, float *mean, float *rstd, int64_t T,

@@ -90,6 +90,54 @@ __device__ __forceinline__ Raw<T, V> from_f32(const float *f) {
     }
 }
 
+// Pairs of fp32 values in one 64-bit register: the packed arithmetic of sm_100 and
+// later does two operations an instruction.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ void unpair(f32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ float pair_sum(f32x2 v) {
+    float lo, hi;
+    unpair(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// A 16-byte vector of V elements as V / 2 pairs, and back.
+template <typename T, int V>
+__device__ __forceinline__ void to_pairs(const uint4 &r, f32x2 *p) {
+    float f[V];
+    to_f32<T, V>(r, f);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) p[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ uint4 from_pairs(const f32x2 *p) {
+    float f[V];
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) unpair(p[j], f[2 * j], f[2 * j + 1]);
+    return from_f32<T, V>(f);
+}
+
 template <typename T>
 __device__ __forceinline__ float load_f32(const T *p) { return (float)*p; }
 template <typename T>

@@ -42,6 +42,10 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Threads of a ring block: 72 registers a thread forward, 128 backward, where the
+// column sums take 64.
+constexpr int kFwdThreads = 896, kBwdRingThreads = 512;
+
 struct LnArgs {
     const void *x, *gamma, *beta;
     void *y;
@@ -312,15 +316,21 @@ __global__ void __launch_bounds__(1024, 1) ln_backward_kernel(const LnArgs a) {
 // Each row group keeps a ring of its next rows in shared memory, filled by bulk
 // copies (cp.async.bulk, one thread of the group, completion on an mbarrier), so
 // that the loads in flight do not depend on how far the group's arithmetic is and
-// take no registers. A stage is refilled after the group's next barrier: by then
-// every thread has read it.
+// take no registers. A stage is refilled after a barrier that every thread of the
+// group passes after its last read of the stage.
+//
+// With that the kernels are limited by instruction issue nearly as much as by HBM,
+// so a row is spread over few threads (V * NV = 32 elements of 16 bits each: the
+// shuffles, barrier and bookkeeping of a row are paid per warp), the arithmetic is
+// on packed pairs, and gamma and beta wait in shared memory in fp32, as planes of
+// four elements of every vector, which a warp reads without bank conflicts.
 
-// Bytes of the control block in front of the rings: barriers and statistics.
-constexpr int kRingStages = 8;  // most
+constexpr int kRingStages = 4;  // most
 constexpr int kMaxGroups = 28;
 struct RingCtl {
     uint64_t full[kMaxGroups][kRingStages];
     float2 stat[2][32];
+    uint4 zero;  // what a thread past the row's end reads
 };
 constexpr int kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -334,11 +344,92 @@ __device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity) {
         if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) return;
 }
 
-template <typename T, int V, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a) {
+// Weights of vector v from their planes.
+template <int V>
+__device__ __forceinline__ void plane_pairs(const float *planes, int nvec, int v, f32x2 (&g)[V / 2]) {
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(planes + (h * nvec + v) * 4);
+        g[2 * h] = q.x;
+        g[2 * h + 1] = q.y;
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void fill_planes(float *planes, const void *w, int w32, int d, float none) {
+    const int nvec = d / V;
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = load_w<T>(w, w32, v * V + j, none);
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h)
+            *reinterpret_cast<float4 *>(planes + (h * nvec + v) * 4) =
+                make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+    }
+}
+
+// A block's partial sums dgamma, dbeta, 16-byte vectors at a time: the groups are added
+// in order through acc (in planes, [2][d], used with several groups).
+template <int V, int NV>
+__device__ __forceinline__ void store_partial_vecs(const LnArgs &a, int groups, int group, int tpr,
+                                                   int t, const bool (&ok)[NV],
+                                                   const f32x2 (&dg)[NV][V / 2],
+                                                   const f32x2 (&db)[NV][V / 2], float *acc) {
+    float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * 2 * a.d);
+    float4 *sums = reinterpret_cast<float4 *>(acc);
+    const int nvec = a.d / V;
+    constexpr int H = V / 4;
+    auto quad = [&](const f32x2 *p) {
+        float4 q;
+        unpair(p[0], q.x, q.y);
+        unpair(p[1], q.z, q.w);
+        return q;
+    };
+    if (groups == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (ok[i])
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    part[(i * tpr + t) * H + h] = quad(&dg[i][2 * h]);
+                    part[(nvec + i * tpr + t) * H + h] = quad(&db[i][2 * h]);
+                }
+        return;
+    }
+    __syncthreads();
+    for (int k = 0; k < groups; ++k) {
+        if (group == k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (ok[i])
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            float4 q = quad(m == 0 ? &dg[i][2 * h] : &db[i][2 * h]);
+                            float4 &x = sums[(m * H + h) * nvec + i * tpr + t];
+                            if (k > 0) {
+                                q.x = x.x + q.x;
+                                q.y = x.y + q.y;
+                                q.z = x.z + q.z;
+                                q.w = x.w + q.w;
+                            }
+                            x = q;
+                        }
+        }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * H * nvec; c += blockDim.x) {
+        const int m = c / (H * nvec), r = c - m * H * nvec, v = r / H, h = r - v * H;
+        part[c] = sums[(m * H + h) * nvec + v];
+    }
+}
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const LnArgs a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
-    constexpr int EPT = V * NV;
+    constexpr int P2 = V / 2;
     const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
     const int w0 = group * a.wpr, wg = warp - w0;
@@ -347,13 +438,14 @@ __global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a
     const uint32_t row_bytes = (uint32_t)a.d * sizeof(T);
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + group;
-    uint8_t *ring = ring_sh + kRingCtl + (size_t)group * S * row_bytes;
+    float *gamma = reinterpret_cast<float *>(ring_sh + kRingCtl), *beta = gamma + a.d;
+    uint8_t *ring = ring_sh + kRingCtl + (size_t)2 * a.d * sizeof(float) + (size_t)group * S * row_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
         ptx::fence_barrier_init();
     }
-    __syncthreads();
+    if (threadIdx.x == 0) ctl->zero = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_trigger();
     auto fetch = [&](int64_t r, int s) {
@@ -363,19 +455,13 @@ __global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a
     };
     if (t == 0)
         for (int s = 0; s < S && row + s * stride < a.T; ++s) fetch(row + s * stride, s);
+    fill_planes<T, V>(gamma, a.gamma, a.w32, a.d, 1.f);
+    fill_planes<T, V>(beta, a.beta, a.w32, a.d, 0.f);
+    __syncthreads();
 
     bool ok[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
-    float gm[EPT], bt[EPT];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (i * tpr + t) * V + j;
-            gm[i * V + j] = ok[i] ? load_w<T>(a.gamma, a.w32, c, 1.f) : 0.f;
-            bt[i * V + j] = ok[i] ? load_w<T>(a.beta, a.w32, c, 0.f) : 0.f;
-        }
     const float inv_d = 1.f / (float)a.d;
     const int n_own = warp_count<V, NV>(wg, nvec, tpr);
     const float inv_own = n_own > 0 ? 1.f / (float)n_own : 0.f;
@@ -385,34 +471,30 @@ __global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a
     uint32_t ph = 0;
     for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
         ring_wait(bar0 + 8 * s, ph);
-        const Raw<T, V> *src = reinterpret_cast<const Raw<T, V> *>(ring + (size_t)s * row_bytes);
-        float f[EPT];
-        float sum = 0.f;
+        const uint4 *src = reinterpret_cast<const uint4 *>(ring + (size_t)s * row_bytes) + t;
+        // f: the elements, then their distances from the warp's own mean (a thread past
+        // the row's end holds zeros throughout)
+        f32x2 f[NV][P2], acc = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (ok[i]) {
-                to_f32<T, V>(src[i * tpr + t], f + i * V);
-            } else {
+            to_pairs<T, V>(ok[i] ? src[i * tpr] : ctl->zero, f[i]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) f[i * V + j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum += f[i * V + j];
+            for (int j = 0; j < P2; ++j) acc = add2(acc, f[i][j]);
         }
-        float mean = warp_sum(sum) * inv_own;
-        float m2 = 0.f;
+        const float own = warp_sum(pair_sum(acc)) * inv_own;
+        acc = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
+        for (int i = 0; i < NV; ++i) {
+            const f32x2 shift = both(ok[i] ? -own : 0.f);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float c = f[i * V + j] - mean;
-                    m2 = fmaf(c, c, m2);
-                }
+            for (int j = 0; j < P2; ++j) {
+                f[i][j] = add2(f[i][j], shift);
+                acc = fma2(f[i][j], f[i][j], acc);
             }
-        m2 = warp_sum(m2);
+        }
+        float mean = own, dev = warp_sum(pair_sum(acc));
         if (a.wpr > 1) {
-            if (lane == 0) ctl->stat[buf][warp] = make_float2(mean, m2);
+            if (lane == 0) ctl->stat[buf][warp] = make_float2(own, dev);
             group_sync(1 + group, tpr);
         } else {
             __syncwarp();
@@ -427,19 +509,21 @@ __global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a
             const float2 o = lane < a.wpr ? ctl->stat[buf][w0 + lane] : make_float2(0.f, 0.f);
             mean = warp_sum(n_lane * o.x) * inv_d;
             const float c = o.x - mean;
-            m2 = warp_sum(lane < a.wpr && n_lane > 0.f ? fmaf(n_lane * c, c, o.y) : 0.f);
+            dev = warp_sum(n_lane > 0.f ? fmaf(n_lane * c, c, o.y) : 0.f);
         }
-        const float rstd = __frsqrt_rn(fmaf(m2, inv_d, a.eps));
-        T *yp = static_cast<T *>(a.y) + row * a.ldy;
+        const float rstd = __frsqrt_rn(fmaf(dev, inv_d, a.eps));
+        const f32x2 r2 = both(rstd), off = both((own - mean) * rstd);
+        uint4 *yp = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.ldy) + t;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-                float o[V];
+        for (int i = 0; i < NV; ++i) {
+            if (!ok[i]) continue;
+            f32x2 g[P2], o[P2];
+            plane_pairs<V>(gamma, nvec, i * tpr + t, g);
+            plane_pairs<V>(beta, nvec, i * tpr + t, o);
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    o[j] = fmaf((f[i * V + j] - mean) * rstd, gm[i * V + j], bt[i * V + j]);
-                reinterpret_cast<Raw<T, V> *>(yp)[i * tpr + t] = from_f32<T, V>(o);
-            }
+            for (int j = 0; j < P2; ++j) o[j] = fma2(fma2(f[i][j], r2, off), g[j], o[j]);
+            yp[i * tpr] = from_pairs<T, V>(o);
+        }
         if (t == 0) {
             if (a.mean != nullptr) a.mean[row] = mean;
             if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -447,11 +531,11 @@ __global__ void __launch_bounds__(MAXT, 1) ln_forward_ring_kernel(const LnArgs a
     }
 }
 
-template <typename T, int V, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs a) {
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(const LnArgs a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
-    constexpr int EPT = V * NV;
+    constexpr int P2 = V / 2;
     const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
     const int w0 = group * a.wpr;
@@ -462,8 +546,8 @@ __global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs 
     const uint32_t stage_bytes = (has_res ? 3 : 2) * row_bytes;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + group;
-    // gamma in fp32 for all groups, then the rings; later the sums of the groups
-    float *gsh = reinterpret_cast<float *>(ring_sh + kRingCtl);
+    // gamma, then the rings; later the sums of the groups
+    float *gamma = reinterpret_cast<float *>(ring_sh + kRingCtl);
     uint8_t *rings = ring_sh + kRingCtl + (size_t)a.d * sizeof(float);
     uint8_t *ring = rings + (size_t)group * S * stage_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
@@ -471,10 +555,9 @@ __global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs 
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
         ptx::fence_barrier_init();
     }
+    if (threadIdx.x == 0) ctl->zero = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_trigger();
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) gsh[c] = load_w<T>(a.gamma, a.w32, c, 1.f);
-    __syncthreads();
     auto fetch = [&](int64_t r, int s) {
         const uint32_t dst = ptx::smem_addr(ring + (size_t)s * stage_bytes), bar = bar0 + 8 * s;
         ptx::mbar_arrive_expect_tx(bar, stage_bytes);
@@ -485,29 +568,23 @@ __global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs 
     };
     if (t == 0)
         for (int s = 0; s < S && row + s * stride < a.T; ++s) fetch(row + s * stride, s);
+    fill_planes<T, V>(gamma, a.gamma, a.w32, a.d, 1.f);
+    __syncthreads();
 
     bool ok[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
-    float dg[EPT], db[EPT];
+    f32x2 dg[NV][P2], db[NV][P2];
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) dg[e] = db[e] = 0.f;
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P2; ++j) dg[i][j] = db[i][j] = 0;
     const float inv_d = 1.f / (float)a.d;
     float m_next = 0.f, r_next = 0.f;
     if (row < a.T) {
         m_next = a.mean[row];
         r_next = a.rstd[row];
     }
-    auto gamma_of = [&](int i, float (&g)[V]) {
-#pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(gsh + (i * tpr + t) * V + j);
-            g[j] = v.x;
-            g[j + 1] = v.y;
-            g[j + 2] = v.z;
-            g[j + 3] = v.w;
-        }
-    };
 
     int s = 0, s_prev = -1;
     uint32_t ph = 0;
@@ -518,30 +595,28 @@ __global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs 
             r_next = a.rstd[row + stride];
         }
         ring_wait(bar0 + 8 * s, ph);
-        const Raw<T, V> *px = reinterpret_cast<const Raw<T, V> *>(ring + (size_t)s * stage_bytes);
-        const Raw<T, V> *py = px + nvec, *pr = py + nvec;
-        const float shift = -mean * rstd;
-        float s1 = 0.f, s2 = 0.f;
+        const uint4 *px = reinterpret_cast<const uint4 *>(ring + (size_t)s * stage_bytes) + t;
+        const uint4 *py = px + nvec, *pr = py + nvec;
+        // xh = x r - m r
+        const f32x2 r2 = both(rstd), shift = both(-mean * rstd);
+        f32x2 p1 = 0, p2 = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-                float x[V], y[V], g[V];
-                to_f32<T, V>(px[i * tpr + t], x);
-                to_f32<T, V>(py[i * tpr + t], y);
-                gamma_of(i, g);
+        for (int i = 0; i < NV; ++i) {
+            if (!ok[i]) continue;
+            f32x2 x[P2], y[P2], g[P2];
+            to_pairs<T, V>(px[i * tpr], x);
+            to_pairs<T, V>(py[i * tpr], y);
+            plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int e = i * V + j;
-                    const float xh = (x[j] - mean) * rstd;
-                    db[e] += y[j];
-                    dg[e] = fmaf(y[j], xh, dg[e]);
-                    const float gy = y[j] * g[j];
-                    s2 += gy;
-                    s1 = fmaf(gy, xh, s1);
-                }
+            for (int j = 0; j < P2; ++j) {
+                const f32x2 xh = fma2(x[j], r2, shift), gy = mul2(y[j], g[j]);
+                db[i][j] = add2(db[i][j], y[j]);
+                dg[i][j] = fma2(y[j], xh, dg[i][j]);
+                p2 = add2(p2, gy);
+                p1 = fma2(gy, xh, p1);
             }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
+        }
+        float s1 = warp_sum(pair_sum(p1)), s2 = warp_sum(pair_sum(p2));
         if (a.wpr > 1) {
             if (lane == 0) ctl->stat[buf][warp] = make_float2(s1, s2);
             group_sync(1 + group, tpr);
@@ -555,27 +630,26 @@ __global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs 
             s1 = warp_sum(o.x);
             s2 = warp_sum(o.y);
         }
-        const float c1 = s1 * inv_d, c2 = s2 * inv_d;
-        T *pd = static_cast<T *>(a.dx) + row * a.lddx;
+        // dx = gy r - xh (c1 r) - c2 r
+        const f32x2 k1 = both(-s1 * inv_d * rstd), k2 = both(-s2 * inv_d * rstd);
+        uint4 *pd = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.lddx) + t;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-                float x[V], y[V], g[V];
-                to_f32<T, V>(px[i * tpr + t], x);
-                to_f32<T, V>(py[i * tpr + t], y);
-                gamma_of(i, g);
+        for (int i = 0; i < NV; ++i) {
+            if (!ok[i]) continue;
+            f32x2 x[P2], y[P2], g[P2];
+            to_pairs<T, V>(px[i * tpr], x);
+            to_pairs<T, V>(py[i * tpr], y);
+            plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xh = (x[j] - mean) * rstd;
-                    x[j] = rstd * (fmaf(-c1, xh, y[j] * g[j]) - c2);
-                }
-                if (has_res) {
-                    to_f32<T, V>(pr[i * tpr + t], y);
+            for (int j = 0; j < P2; ++j)
+                x[j] = fma2(fma2(x[j], r2, shift), k1, fma2(mul2(y[j], g[j]), r2, k2));
+            if (has_res) {
+                to_pairs<T, V>(pr[i * tpr], y);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) x[j] += y[j];
-                }
-                reinterpret_cast<Raw<T, V> *>(pd)[i * tpr + t] = from_f32<T, V>(x);
+                for (int j = 0; j < P2; ++j) x[j] = add2(x[j], y[j]);
             }
+            pd[i * tpr] = from_pairs<T, V>(x);
+        }
         s_prev = s;
         if (++s == S) {
             s = 0;
@@ -583,16 +657,16 @@ __global__ void __launch_bounds__(MAXT, 1) ln_backward_ring_kernel(const LnArgs 
         }
     }
     if (a.part == nullptr) return;
-    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, reinterpret_cast<float *>(rings));
+    store_partial_vecs<V, NV>(a, groups, group, tpr, t, ok, dg, db, reinterpret_cast<float *>(rings));
 }
 
 // dgamma[c], dbeta[c] = the sum of P partial rows, each thread row q of the block
-// adding rows q, q + 8, ... and thread row 0 the eight sums, in that order.
+// adding rows q, q + 16, ... and thread row 0 the sixteen sums, in that order.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 ln_weight_reduce_kernel(const float *__restrict__ part, int P, int d, int w32, void *dgamma,
                         void *dbeta) {
-    __shared__ float sh[8][33];
+    __shared__ float sh[16][33];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
@@ -600,15 +674,15 @@ ln_weight_reduce_kernel(const float *__restrict__ part, int P, int d, int w32, v
     float s = 0.f;
     if (c < 2 * (int64_t)d) {
         const float *p = part + c;
-#pragma unroll 8
-        for (int k = q; k < P; k += 8) s += p[(int64_t)k * 2 * d];
+#pragma unroll 10
+        for (int k = q; k < P; k += 16) s += p[(int64_t)k * 2 * d];
     }
     sh[q][lane] = s;
     __syncthreads();
     if (q != 0 || c >= 2 * (int64_t)d) return;
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += sh[k][lane];
+    for (int k = 0; k < 16; ++k) s += sh[k][lane];
     void *out = c < d ? dgamma : dbeta;
     if (out == nullptr) return;
     const int64_t i = c < d ? c : c - d;
@@ -747,10 +821,6 @@ __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
 
 // Widest row of the register kernels: 32 warps of 8 elements a thread.
 constexpr int kRegWidth = 8192;
-// Aligned rows: up to kNarrow elements 8 a thread, beyond 16 (fewer warps share a
-// row, so fewer shuffles and shorter barriers); widest row that 28 warps hold.
-constexpr int kNarrow = 1024;
-constexpr int kRingWidth = 28 * 32 * 16;
 // Threads of a backward block: as many row groups as fit, so that there is one
 // partial row of weight gradients per SM.
 constexpr int kBwdThreads = 1024;
@@ -802,62 +872,71 @@ cudaError_t backward_regs(LnArgs a, int *P, cudaStream_t s) {
 // per SM), with at most T / SMs rounded up groups so that few rows spread over the
 // SMs. False where two stages of one group do not fit the shared memory.
 constexpr size_t kRingSmem = 224 * 1024;
-bool ring_shape(LnArgs &a, int per_row, int max_threads, size_t fixed, size_t stage, int *groups) {
-    a.wpr = (a.d + per_row * 32 - 1) / (per_row * 32);
+bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t stage, int *groups) {
+    a.wpr = (a.d + per_thread * 32 - 1) / (per_thread * 32);
     if (a.wpr * 32 > max_threads) return false;
     int g = std::min(row_groups(a.wpr, max_threads), a.wpr > 1 ? 15 : kMaxGroups);
     g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
     while (g > 1 && fixed + 2 * g * stage > kRingSmem) --g;
-    const int64_t s = (int64_t)(kRingSmem - std::min(fixed, kRingSmem)) / (int64_t)(g * stage);
-    if (s < 2) return false;
-    a.stages = (int)std::min<int64_t>(s, kRingStages);
+    if (fixed + 2 * g * stage > kRingSmem) return false;
+    a.stages = (int)std::min<size_t>((kRingSmem - fixed) / (g * stage), kRingStages);
     *groups = g;
     return true;
 }
 
-template <typename T, int V, int NV, int MAXT>
+template <typename T, int V, int NV>
 cudaError_t forward_ring(LnArgs a, bool *fits, cudaStream_t s) {
     int groups;
-    const size_t stage = (size_t)a.d * sizeof(T);
-    *fits = ring_shape(a, V * NV, MAXT, kRingCtl, stage, &groups);
+    const size_t stage = (size_t)a.d * sizeof(T), fixed = kRingCtl + (size_t)2 * a.d * sizeof(float);
+    *fits = ring_shape(a, V * NV, kFwdThreads, fixed, stage, &groups);
     if (!*fits) return cudaSuccess;
-    const size_t smem = kRingCtl + groups * a.stages * stage;
     const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV, MAXT>), (int)kRingSmem);
+        reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV>), (int)kRingSmem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, sm_count());
-    return launch_k(ln_forward_ring_kernel<T, V, NV, MAXT>, dim3(grid), dim3(groups * a.wpr * 32),
-                    smem, s, a);
+    return launch_k(ln_forward_ring_kernel<T, V, NV>, dim3(grid), dim3(groups * a.wpr * 32),
+                    fixed + groups * a.stages * stage, s, a);
 }
 
-template <typename T, int V, int NV, int MAXT>
+template <typename T, int V, int NV>
 cudaError_t backward_ring(LnArgs a, int *P, bool *fits, cudaStream_t s) {
     int groups;
     const size_t stage = (size_t)a.d * sizeof(T) * (a.dres != nullptr ? 3 : 2);
     const size_t fixed = kRingCtl + (size_t)a.d * sizeof(float);
-    *fits = ring_shape(a, V * NV, MAXT, fixed, stage, &groups);
+    *fits = ring_shape(a, V * NV, kBwdRingThreads, fixed, stage, &groups);
     if (!*fits) return cudaSuccess;
-    // (two stages of 16-bit x and dy hold the groups' [2][d] fp32 sums)
-    const size_t smem = fixed + groups * a.stages * stage;
     const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV, MAXT>), (int)kRingSmem);
+        reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV>), (int)kRingSmem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(sm_count(), kLnPartials));
     *P = grid;
-    return launch_k(ln_backward_ring_kernel<T, V, NV, MAXT>, dim3(grid), dim3(groups * a.wpr * 32),
-                    smem, s, a);
+    // (two stages of one group, 8 d bytes or more, hold the groups' [2][d] fp32 sums)
+    return launch_k(ln_backward_ring_kernel<T, V, NV>, dim3(grid), dim3(groups * a.wpr * 32),
+                    fixed + groups * a.stages * stage, s, a);
+}
+
+// Vectors a thread: one or two where a warp still holds the row, else four.
+template <typename T>
+cudaError_t forward_aligned(const LnArgs &a, bool *fits, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    if (a.d <= 32 * W) return forward_ring<T, W, 1>(a, fits, s);
+    if (a.d <= 64 * W) return forward_ring<T, W, 2>(a, fits, s);
+    return forward_ring<T, W, 4>(a, fits, s);
+}
+template <typename T>
+cudaError_t backward_aligned(const LnArgs &a, int *P, bool *fits, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    if (a.d <= 32 * W) return backward_ring<T, W, 1>(a, P, fits, s);
+    if (a.d <= 64 * W) return backward_ring<T, W, 2>(a, P, fits, s);
+    return backward_ring<T, W, 4>(a, P, fits, s);
 }
 
 template <typename T>
 cudaError_t forward_type(const LnArgs &a, const Align &al, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);  // elements of a 16-byte vector
-    if (al.fits(16) && a.d <= kRingWidth) {
+    if (al.fits(16)) {
         bool fits = false;
-        cudaError_t e;
-        if constexpr (sizeof(T) == 4)
-            e = a.d <= kNarrow ? forward_ring<T, 4, 2, 512>(a, &fits, s) : forward_ring<T, 4, 4, 512>(a, &fits, s);
-        else
-            e = a.d <= kNarrow ? forward_ring<T, 8, 1, 896>(a, &fits, s) : forward_ring<T, 8, 2, 896>(a, &fits, s);
+        const cudaError_t e = forward_aligned<T>(a, &fits, s);
         if (e != cudaSuccess || fits) return e;
     }
     if (a.d > kRegWidth || al.fits(16)) {
@@ -878,13 +957,8 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
     cudaError_t e;
     int P = 0;
     bool fits = false;
-    if (al.fits(16) && a.d <= kRingWidth) {
-        if constexpr (sizeof(T) == 4)
-            e = a.d <= kNarrow ? backward_ring<T, 4, 2, 512>(a, &P, &fits, s)
-                               : backward_ring<T, 4, 4, 512>(a, &P, &fits, s);
-        else
-            e = a.d <= kNarrow ? backward_ring<T, 8, 1, 896>(a, &P, &fits, s)
-                               : backward_ring<T, 8, 2, 896>(a, &P, &fits, s);
+    if (al.fits(16)) {
+        e = backward_aligned<T>(a, &P, &fits, s);
         if (e != cudaSuccess) return e;
     }
     if (fits) {
@@ -905,7 +979,7 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
         e = al.fits(4) ? backward_regs<T, 2, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
     }
     if (e != cudaSuccess || a.part == nullptr) return e;
-    return launch_k(ln_weight_reduce_kernel<T>, dim3((2 * a.d + 31) / 32), dim3(256), 0, s,
+    return launch_k(ln_weight_reduce_kernel<T>, dim3((2 * a.d + 31) / 32), dim3(512), 0, s,
                     static_cast<const float *>(a.part), P, a.d, a.w32, dgamma, dbeta);
 }
 
