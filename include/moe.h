@@ -543,8 +543,8 @@ typedef enum {
     MOE_ACT_GELU_TANH = 1  /* 0.5 a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) */
 } moe_act_t;
 
-/* Workspace of the calls below for up to T tokens (train: of the backward too),
- * 256-byte aligned; 0 for an invalid shape. Its control words (the device error word of
+/* Workspace of the calls below for up to T tokens (train: of the training forward
+ * and the backward too; else of moe_ffn_forward), 256-byte aligned; 0 for an invalid shape. Its control words (the device error word of
  * moe_sync_check and join counters) start at zero, once before the first use
  * (moe_ffn_workspace_init), and every call leaves the counters so. It serves any
  * shape that needs no more bytes. Calls that overlap on the GPU need one each. */
@@ -561,7 +561,7 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
                              size_t ws_bytes, void *stream);
 
 /* Y and what the backward takes: H [T,n] of `type` and the pre-activations A1, A3
- * [T,n] fp32 (16-byte aligned). Two kernels. */
+ * [T,n] fp32 (16-byte aligned). ws: a workspace for training. Two kernels. */
 moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
                                    int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
                                    void *H, float *A1, float *A3, void *ws, size_t ws_bytes,

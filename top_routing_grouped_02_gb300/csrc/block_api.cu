@@ -67,7 +67,7 @@ moe_status_t check_ffn(int T, int d, int n, moe_act_t act, moe_dtype_t type) {
 }
 
 // Regions behind the control words: the backward's dA1, dA3, or H of a forward
-// without saved tensors and the parts of the weight-streaming kernels.
+// without saved tensors; then the parts of cut tiles.
 struct FfnWs {
     size_t h, part, da1, da3, total;
 };
@@ -76,15 +76,15 @@ FfnWs ffn_ws(int T, int d, int n, bool train) {
     const size_t act = align256((size_t)T * n * 2);
     w.h = w.da1 = align256(kFfnControlBytes);
     w.da3 = w.da1 + act;
-    w.part = w.h + act;
-    // a workspace for T tokens serves fewer: the most that T or fewer need
+    w.part = train ? w.da3 + act : w.h + act;
+    const bool tiled = train || T > kFfnStreamTokens;
+    w.total = w.part + (tiled ? align256(ffn_dense_part_bytes(T, d, n, train)) : 0);
+    // a workspace for T tokens serves fewer on the weight-streaming kernel
     const int few = std::min(T, kFfnStreamTokens);
-    w.total = std::max(w.part, w.h + align256((size_t)few * n * 2) +
-                                   align256(ffn_stream_part_bytes(few, d, n)));
-    if (train && w.da3 + act > w.total) w.total = w.da3 + act;
+    w.total = std::max(w.total, w.h + align256((size_t)few * n * 2) +
+                                    align256(ffn_stream_part_bytes(few, d, n)));
     return w;
 }
-
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
 
 bool all_aligned16(std::initializer_list<const void *> ps) {
@@ -200,15 +200,16 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
     if ((st = check_arch()) != MOE_OK) return st;
     const FfnWs w = ffn_ws(T, d, n, false);
     uint32_t *err = static_cast<uint32_t *>(ws);
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset));
+    float4 *part = reinterpret_cast<float4 *>(at(ws, w.part));
     const bool f16 = type == MOE_DTYPE_F16;
     cudaStream_t s = as_stream(stream);
     if (T <= kFfnStreamTokens)
         return from_cuda(launch_ffn_stream(X, W1, W3, W2, T, d, n, act, f16, at(ws, w.h), Y,
-                                           reinterpret_cast<float *>(at(ws, w.part)),
-                                           reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),
-                                           err, s));
-    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, at(ws, w.h), nullptr, nullptr, err, s);
-    if (e == cudaSuccess) e = launch_ffn_down(at(ws, w.h), W2, T, d, n, f16, Y, err, s);
+                                           reinterpret_cast<float *>(part), ticket, err, s));
+    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, at(ws, w.h), nullptr, nullptr, part,
+                                    ticket, err, s);
+    if (e == cudaSuccess) e = launch_ffn_down(at(ws, w.h), W2, T, d, n, f16, Y, part, ticket, err, s);
     return from_cuda(e);
 }
 
@@ -219,13 +220,15 @@ moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3
     moe_status_t st = check_ffn(T, d, n, act, type);
     if (st != MOE_OK || T == 0) return st;
     if (!all_aligned16({X, W1, W3, W2, Y, H, A1, A3})) return MOE_ERR_INVALID_ARG;
-    if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, false)) != MOE_OK) return st;
+    if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, true)) != MOE_OK) return st;
     if ((st = check_arch()) != MOE_OK) return st;
     uint32_t *err = static_cast<uint32_t *>(ws);
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset));
+    float4 *part = reinterpret_cast<float4 *>(at(ws, ffn_ws(T, d, n, true).part));
     const bool f16 = type == MOE_DTYPE_F16;
     cudaStream_t s = as_stream(stream);
-    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, H, A1, A3, err, s);
-    if (e == cudaSuccess) e = launch_ffn_down(H, W2, T, d, n, f16, Y, err, s);
+    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, H, A1, A3, part, ticket, err, s);
+    if (e == cudaSuccess) e = launch_ffn_down(H, W2, T, d, n, f16, Y, part, ticket, err, s);
     return from_cuda(e);
 }
 
@@ -254,7 +257,9 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
     const FfnWs w = ffn_ws(T, d, n, true);
     return from_cuda(launch_ffn_backward(dY, X, W1, W3, W2, H, A1, A3, T, d, n, act,
                                          type == MOE_DTYPE_F16, at(ws, w.da1), at(ws, w.da3), dX,
-                                         dW1, dW3, dW2, static_cast<uint32_t *>(ws), s));
+                                         dW1, dW3, dW2, reinterpret_cast<float4 *>(at(ws, w.part)),
+                                         reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),
+                                         static_cast<uint32_t *>(ws), s));
 }
 
 }  // extern "C"

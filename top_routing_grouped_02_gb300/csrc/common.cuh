@@ -236,19 +236,22 @@ constexpr size_t kFfnTicketOffset = 256;  // workspace: control words, then tick
 constexpr size_t kFfnControlBytes =  // a ticket for each warp of each tile of two products
     kFfnTicketOffset + 2 * (size_t)(kFfnMaxWidth / 128) * 4 * sizeof(uint32_t);
 size_t ffn_stream_part_bytes(int T, int d, int n);
+// Scratch of the tiled products' joins (part; ticket: counters that are zero between
+// launches, 16 for each of up to kFfnMaxCtas cut tiles).
+size_t ffn_dense_part_bytes(int T, int d, int n, bool train);
 cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, const void *W2, int T,
                               int d, int n, int act, bool f16, void *H, void *Y, float *part,
                               uint32_t *ticket, uint32_t *err, cudaStream_t s);
 cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
-                            int act, bool f16, void *H, float *A1, float *A3, uint32_t *err,
-                            cudaStream_t s);
+                            int act, bool f16, void *H, float *A1, float *A3, float4 *part,
+                            uint32_t *ticket, uint32_t *err, cudaStream_t s);
 cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, bool f16, void *Y,
-                            uint32_t *err, cudaStream_t s);
+                            float4 *part, uint32_t *ticket, uint32_t *err, cudaStream_t s);
 cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
                                 const void *W2, const void *H, const float *A1, const float *A3,
                                 int T, int d, int n, int act, bool f16, void *dA1, void *dA3,
-                                void *dX, void *dW1, void *dW3, void *dW2, uint32_t *err,
-                                cudaStream_t s);
+                                void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
+                                uint32_t *ticket, uint32_t *err, cudaStream_t s);
 
 // One CTA whose pipeline wait on a barrier nothing arrives at runs out after the
 // wait limit (about 1 s) and sets MOE_DEVERR_TIMEOUT in *err.

@@ -8,12 +8,18 @@
 // One persistent kernel template runs all five products (Mode). Each is bound by
 // the tensor cores once T is a few hundred; few tokens take the weight-streaming
 // kernel of ffn_small.cu instead. A CTA pair (tcgen05 cta_group::2) owns a tile
-// of 256 rows x BN columns: each CTA holds its 128 rows of A and half of the
+// of 256 rows x 256 columns: each CTA holds its 128 rows of A and half of the
 // columns of B per 64-deep stage, the even CTA issues the MMAs over both. Two
 // accumulators in TMEM: the epilogue of one tile runs while the MMAs fill the
 // other. gate/up: the even CTA's half of B is W1's columns and the odd CTA's W3's,
 // so a thread finds a1 and a3 of one element in its own TMEM lane and H leaves in
 // the epilogue; neither A1 nor A3 is read back from memory in the forward.
+// Tiles rarely come out even over the SM pairs, so the last ones (up to two a pair) are
+// cut: their k-blocks form one sequence, split into equal runs, one per pair. A tile
+// that is cut is joined by the pairs that hold its parts: every epilogue warp writes
+// its part (fp32) to the workspace, and once all have, each adds all parts, in the order
+// of the runs, of its share of the columns: the result does not depend on timing. The
+// cut tiles come first in each pair's work, so that joining overlaps whole tiles.
 // All tails (T, d, n need not be multiples of a tile) are left to TMA: loads
 // outside a tensor give zeros, which add nothing, and stores outside write nothing.
 //
@@ -82,14 +88,17 @@ constexpr int kEpiBufs = 2;                // per epilogue warp
 // 76 pairs at work then cover about 8 x 10 tiles and share their operands in L2.
 constexpr int kGroup = 8;
 
-template <int BN>
-struct Geo {
-    static constexpr int kBoxes = BN / 128;  // 64-column boxes of B per CTA
-    static constexpr uint32_t kStageBytes = kABytes + kBoxes * kBox;
-    static constexpr int kStages = BN == 256 ? 6 : 8;  // 192 KB
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes +
-                                    (size_t)kEpiWarps * kEpiBufs * kEpiBuf + 256;
-};
+constexpr int BN = 256;                      // tile columns
+constexpr int kBoxes = BN / 128;             // 64-column boxes of B per CTA
+constexpr uint32_t kStageBytes = kABytes + kBoxes * kBox;
+constexpr int kStages = 6;                   // 192 KB
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes +
+                         (size_t)kEpiWarps * kEpiBufs * kEpiBuf + 256;
+// Shortest run of k-blocks worth a join (a part is written and read at the cost of
+// about four).
+constexpr int kMinRun = 8;
+// Vectors (float4) of one warp's part: BN / 2 columns of 32 rows.
+constexpr int kPartVecs = BN / 2 * 32 / 4;
 
 struct Maps {
     CUtensorMap a[3], b[3], o[3];
@@ -97,6 +106,8 @@ struct Maps {
 
 struct Args {
     int units;           // tiles of all problems
+    int cut;             // the first `cut` of them are split over the pairs' runs
+    int runs;            // pairs that have a run
     int first[3];        // first unit of each problem (kWGrad: three, else one)
     int mt[3], nb[3];    // row-tile pairs, column blocks
     int rows[3], cols[3];// of the outputs
@@ -105,6 +116,8 @@ struct Args {
     int f16, act;
     int pre;             // kGate: store A1, A3
     const float *a1, *a3;// kDHid
+    float4 *part;        // [pair][first / last tile of its run][CTA][warp][kPartVecs]
+    uint32_t *ticket;    // [cut][CTA][warp]
     uint32_t *err;
 };
 
@@ -114,17 +127,45 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 256, "control block");
 
-template <int MODE, int BN>
+// A pair's work: the segments of its run over the cut tiles, then whole tiles.
+struct Work {
+    int pair, pairs, units, cut, kb;
+    int64_t pos, end;  // rest of the run
+    int next;          // next whole tile
+    int u, kb0, kb1;   // current: tile, its k-blocks
+    __device__ __forceinline__ Work(const Args &a, int pair_, int pairs_)
+        : pair(pair_), pairs(pairs_), units(a.units), cut(a.cut), kb(a.kb), next(a.cut + pair_) {
+        const Runs runs{(int64_t)a.cut * a.kb, a.runs};
+        pos = runs.start(pair);
+        end = runs.start(pair + 1);
+    }
+    __device__ __forceinline__ bool step() {
+        if (pos < end) {
+            u = (int)Runs::quot(pos, kb);
+            kb0 = (int)(pos - (int64_t)u * kb);
+            kb1 = (int)min((int64_t)kb, kb0 + (end - pos));
+            pos += kb1 - kb0;
+            return true;
+        }
+        if (next >= units) return false;
+        u = next;
+        next += pairs;
+        kb0 = 0;
+        kb1 = kb;
+        return true;
+    }
+};
+
+template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
-    using G = Geo<BN>;
-    constexpr int S = G::kStages;
+dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args args) {
+    constexpr int S = kStages;
     constexpr bool A_MN = MODE == kWGrad;
     constexpr bool B_K = MODE == kDHid || MODE == kDX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + (size_t)S * G::kStageBytes +
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + (size_t)S * kStageBytes +
                                        (size_t)kEpiWarps * kEpiBufs * kEpiBuf);
     const uint32_t base = ptx::smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -176,9 +217,9 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
         // ------------------------------------------------------ producer --
         uint32_t it = 0;
         bool ok = true;
-        for (int u = pair; u < args.units && ok; u += pairs) {
-            const Unit un = unit_at(u);
-            for (int kb = 0; kb < args.kb; ++kb, ++it) {
+        for (Work w(args, pair, pairs); ok && w.step();) {
+            const Unit un = unit_at(w.u);
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const uint32_t s = it % S;
                 if (!bounded_wait(ptx::smem_addr(&ctl->empty[s]), ((it / S) & 1u) ^ 1u, args.err)) {
                     ok = false;
@@ -186,9 +227,9 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
                 }
                 // both CTAs' loads complete on the even CTA's barrier
                 const uint32_t full = ptx::smem_addr(&ctl->full[s]);
-                if (leader) ptx::mbar_arrive_expect_tx(full, 2 * G::kStageBytes);
+                if (leader) ptx::mbar_arrive_expect_tx(full, 2 * kStageBytes);
                 const uint32_t bar = ptx::mapa(full, 0);
-                const uint32_t sA = base + s * G::kStageBytes, sB = sA + kABytes;
+                const uint32_t sA = base + s * kStageBytes, sB = sA + kABytes;
                 const bool second = MODE == kDX && kb >= args.kb_half;
                 const int k0 = (second ? kb - args.kb_half : kb) * BK;
                 const int ai = MODE == kWGrad ? un.p : second ? 1 : 0;
@@ -204,7 +245,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
                 // this CTA's half of the tile's columns of B
                 const int c0 = MODE == kGate ? un.nb * (BN / 2) : un.nb * BN + (int)rank * (BN / 2);
 #pragma unroll
-                for (int q = 0; q < G::kBoxes; ++q) {
+                for (int q = 0; q < kBoxes; ++q) {
                     if (B_K) ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, k0, c0 + q * 64);
                     else ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, c0 + q * 64, k0);
                 }
@@ -219,18 +260,18 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
         // ---------------------------------------------------- MMA issuer --
         uint32_t it = 0, uc = 0;
         bool ok = true;
-        for (int u = pair; u < args.units && ok; u += pairs, ++uc) {
+        for (Work w(args, pair, pairs); ok && w.step(); ++uc) {
             const uint32_t a = uc & 1u;
             if (!bounded_wait(ptx::smem_addr(&ctl->tempty[a]), ((uc >> 1) & 1u) ^ 1u, args.err)) break;
             ptx::tc_fence_after();
-            for (int kb = 0; kb < args.kb; ++kb, ++it) {
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const uint32_t s = it % S;
                 if (!bounded_wait(ptx::smem_addr(&ctl->full[s]), (it / S) & 1u, args.err)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t sA = base + s * G::kStageBytes, sB = sA + kABytes;
+                const uint32_t sA = base + s * kStageBytes, sB = sA + kABytes;
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k) {
                     // K-major: the next 16 of the reduction are 32 bytes on; MN-major:
@@ -239,7 +280,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
                                              : ptx::desc_sw128(sA + k * 32, 16, 1024);
                     const uint64_t bd = B_K ? ptx::desc_sw128(sB + k * 32, 16, 1024)
                                             : ptx::desc_sw128(sB + k * 2048, kBox, 1024);
-                    ptx::tc_mma_f16_pair(tmem_base + a * BN, ad, bd, args.idesc, (kb | k) != 0);
+                    ptx::tc_mma_f16_pair(tmem_base + a * BN, ad, bd, args.idesc, kb != w.kb0 || k != 0);
                 }
                 ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[s]), 0x3);
             }
@@ -251,7 +292,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
         const int ew = warp - 4, q = warp & 3, half = ew >> 2;
-        const uint32_t buf0 = base + (uint32_t)S * G::kStageBytes + (uint32_t)ew * kEpiBufs * kEpiBuf;
+        const uint32_t buf0 = base + (uint32_t)S * kStageBytes + (uint32_t)ew * kEpiBufs * kEpiBuf;
         const uint32_t tempty0 = ptx::mapa(ptx::smem_addr(&ctl->tempty[0]), 0);
         const bool f16 = args.f16 != 0;
         uint32_t groups = 0, uc = 0;
@@ -273,39 +314,80 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
             }
             ++groups;
         };
-        for (int u = pair; u < args.units; u += pairs, ++uc) {
+        constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // output columns of a tile
+        constexpr int NC = kCols / 64;                      // 32-column chunks of a warp
+        const int c_lo = half * NC;
+        // part of pair p's first (0) or last (1) tile: this warp's, at this lane
+        auto part_of = [&](int p, int which) {
+            return args.part + ((((int64_t)p * 2 + which) * 2 + rank) * kEpiWarps + ew) * kPartVecs + lane;
+        };
+        // a part's vectors of 32 columns starting at block blk (of 32 columns)
+        auto put = [&](float4 *p, int blk, const uint32_t (&v)[32]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                __stcg(p + (blk * 8 + i) * 32,
+                       make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                   __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+        };
+        // a cut tile of this pair's run: the runs [p0, p0 + P) that hold it, the chunks
+        // [lo, hi) of this warp that this pair joins
+        struct Cut {
+            int u, p0, P, lo, hi;
+            const float4 *first;
+        };
+        const Runs runs{(int64_t)args.cut * args.kb, args.runs};
+        auto cut_of = [&](int u) {
+            Cut x;
+            x.u = u;
+            const int64_t t0 = (int64_t)u * args.kb;
+            x.p0 = runs.owner(t0);
+            x.P = runs.owner(t0 + args.kb - 1) - x.p0 + 1;
+            const int k = pair - x.p0;
+            x.lo = NC * k / x.P;
+            x.hi = NC * (k + 1) / x.P;
+            x.first = part_of(x.p0, runs.start(x.p0) == t0 ? 0 : 1);
+            return x;
+        };
+        // 32 columns of a cut tile from its parts, in the order of the runs
+        auto gather = [&](const Cut &x, int blk, uint32_t (&v)[32]) {
+            float s[32] = {};
+#pragma unroll 1
+            for (int p = 0; p < x.P; ++p) {
+                const float4 *src = p == 0 ? x.first : part_of(x.p0 + p, 0);
+                float4 q[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = __ldcg(src + (blk * 8 + i) * 32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[4 * i] += q[i].x;
+                    s[4 * i + 1] += q[i].y;
+                    s[4 * i + 2] += q[i].z;
+                    s[4 * i + 3] += q[i].w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(s[i]);
+        };
+        // The chunks [lo, hi) of this warp's columns of a tile to the outputs: from the
+        // accumulator at taddr, or from the parts of x where joined.
+        auto finish = [&](int u, int lo, int hi, uint32_t taddr, bool joined, const Cut &x, auto ready) {
             const Unit un = unit_at(u);
             const int rows = args.rows[un.p], cols = args.cols[un.p];
             const int y0 = un.row0 + q * 32;
-            const uint32_t a = uc & 1u;
-            constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // output columns of the tile
-            const int c_lo = half * (kCols / 64), c_hi = c_lo + kCols / 64;
-            // kDHid: this row's A1, A3 of a 32-column chunk, loaded one chunk ahead
-            float4 x1[8], x3[8];
-            auto load_pre = [&](int c, float4 (&l1)[8], float4 (&l3)[8]) {
-                const int row = y0 + lane, col = un.nb * kCols + c * 32;
-                const int64_t off = (int64_t)row * cols + col;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool in = row < rows && col + 4 * i < cols;
-                    l1[i] = in ? __ldg(reinterpret_cast<const float4 *>(args.a1 + off) + i)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-                    l3[i] = in ? __ldg(reinterpret_cast<const float4 *>(args.a3 + off) + i)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+            if (!ready()) return false;
+            // blk: 32-column block of the tile as the accumulator holds it
+            auto load = [&](int blk, int own, uint32_t (&v)[32]) {
+                if (joined) gather(x, own, v);
+                else ptx::tmem_ld32(taddr + blk * 32, v);
             };
-            if constexpr (MODE == kDHid) load_pre(c_lo, x1, x3);
-            if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (uc >> 1) & 1u, args.err)) break;
-            ptx::tc_fence_after();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * BN;
 #pragma unroll 1
-            for (int c = c_lo; c < c_hi; ++c) {
-                const int x0 = un.nb * kCols + c * 32;
+            for (int c = lo; c < hi; ++c) {
+                const int x0 = un.nb * kCols + c * 32, own = c - c_lo;
                 const bool in = y0 < rows && x0 < cols;
                 if constexpr (MODE == kGate) {
                     uint32_t g[32], v[32], o[16];
-                    ptx::tmem_ld32(taddr + c * 32, g);
-                    ptx::tmem_ld32(taddr + BN / 2 + c * 32, v);
+                    load(c, own, g);
+                    load(BN / 64 + c, NC + own, v);
                     if (!in) continue;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -321,56 +403,58 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
                     if (args.pre) {
                         // fp32: two boxes of 16 columns each
                         const bool in2 = x0 + 16 < cols;
-                        uint32_t lo[16], hi[16];
+                        uint32_t lo16[16], hi16[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            lo[i] = g[i];
-                            hi[i] = g[16 + i];
+                            lo16[i] = g[i];
+                            hi16[i] = g[16 + i];
                         }
-                        store_box(lo, x0, y0, &maps.o[1]);
-                        if (in2) store_box(hi, x0 + 16, y0, &maps.o[1]);
+                        store_box(lo16, x0, y0, &maps.o[1]);
+                        if (in2) store_box(hi16, x0 + 16, y0, &maps.o[1]);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            lo[i] = v[i];
-                            hi[i] = v[16 + i];
+                            lo16[i] = v[i];
+                            hi16[i] = v[16 + i];
                         }
-                        store_box(lo, x0, y0, &maps.o[2]);
-                        if (in2) store_box(hi, x0 + 16, y0, &maps.o[2]);
+                        store_box(lo16, x0, y0, &maps.o[2]);
+                        if (in2) store_box(hi16, x0 + 16, y0, &maps.o[2]);
                     }
                 } else if constexpr (MODE == kDHid) {
-                    float4 n1[8], n3[8];
-                    if (c + 1 < c_hi) load_pre(c + 1, n1, n3);
+                    // this row's A1, A3 of the chunk
+                    float4 x1[8], x3[8];
+                    const int row = y0 + lane;
+                    const int64_t off = (int64_t)row * cols + x0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const bool at = row < rows && x0 + 4 * i < cols;
+                        x1[i] = at ? __ldg(reinterpret_cast<const float4 *>(args.a1 + off) + i)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x3[i] = at ? __ldg(reinterpret_cast<const float4 *>(args.a3 + off) + i)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
                     uint32_t g[32], o1[16], o3[16];
-                    ptx::tmem_ld32(taddr + c * 32, g);
-                    if (in) {
+                    load(c, own, g);
+                    if (!in) continue;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float r1[2], r3[2];
+                    for (int i = 0; i < 16; ++i) {
+                        float r1[2], r3[2];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float a1 = (&x1[i >> 1].x)[2 * (i & 1) + j];
-                                const float a3 = (&x3[i >> 1].x)[2 * (i & 1) + j];
-                                const float gv = __uint_as_float(g[2 * i + j]);
-                                const float sg = act_sigmoid(a1, args.act);
-                                r1[j] = gv * a3 * act_grad(a1, sg, args.act);
-                                r3[j] = gv * (a1 * sg);
-                            }
-                            o1[i] = pack(r1[0], r1[1], f16);
-                            o3[i] = pack(r3[0], r3[1], f16);
+                        for (int j = 0; j < 2; ++j) {
+                            const float a1 = (&x1[i >> 1].x)[2 * (i & 1) + j];
+                            const float a3 = (&x3[i >> 1].x)[2 * (i & 1) + j];
+                            const float gv = __uint_as_float(g[2 * i + j]);
+                            const float sg = act_sigmoid(a1, args.act);
+                            r1[j] = gv * a3 * act_grad(a1, sg, args.act);
+                            r3[j] = gv * (a1 * sg);
                         }
-                        store_box(o1, x0, y0, &maps.o[0]);
-                        store_box(o3, x0, y0, &maps.o[1]);
+                        o1[i] = pack(r1[0], r1[1], f16);
+                        o3[i] = pack(r3[0], r3[1], f16);
                     }
-                    if (c + 1 < c_hi) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x1[i] = n1[i];
-                            x3[i] = n3[i];
-                        }
-                    }
+                    store_box(o1, x0, y0, &maps.o[0]);
+                    store_box(o3, x0, y0, &maps.o[1]);
                 } else {
                     uint32_t v[32], o[16];
-                    ptx::tmem_ld32(taddr + c * 32, v);
+                    load(c, own, v);
                     if (!in) continue;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -378,10 +462,78 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
                     store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
                 }
             }
+            return true;
+        };
+
+        Cut cuts[2];
+        int ncuts = 0;
+        bool joins = false;  // the cut tiles are joined
+        bool ok = true;
+        // the joins of this run's cut tiles, once its last segment is written
+        auto join = [&] {
+            joins = true;
+            for (int i = 0; i < 2 && ok; ++i) {
+                if (i >= ncuts) break;
+                const Cut x = i == 0 ? cuts[0] : cuts[1];
+                if (x.lo == x.hi) continue;
+                uint32_t *ticket = args.ticket + ((int64_t)x.u * 2 + rank) * kEpiWarps + ew;
+                auto ready = [&] {
+                    bool all = true;
+                    if (lane == 0) all = word_wait(ticket, 0xffffu, (uint32_t)x.P, args.err);
+                    return __shfl_sync(0xffffffffu, all, 0) != 0;
+                };
+                ok = finish(x.u, c_lo + x.lo, c_lo + x.hi, 0, true, x, ready);
+                __syncwarp();  // every lane has its parts
+                // the last holder of the tile returns its ticket to zero
+                if (ok && lane == 0 && atomicAdd(ticket, 0x10000u) >> 16 == (uint32_t)(x.P - 1)) *ticket = 0;
+            }
+        };
+        for (Work w(args, pair, pairs); ok && w.step(); ++uc) {
+            const uint32_t a = uc & 1u;
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * BN;
+            const bool cut = w.kb1 - w.kb0 < args.kb;
+            if (w.u >= args.cut && !joins) {
+                join();
+                if (!ok) break;
+            }
+            auto ready = [&] {
+                if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (uc >> 1) & 1u, args.err)) return false;
+                ptx::tc_fence_after();
+                return true;
+            };
+            if (!cut) {
+                const Cut none{};
+                ok = finish(w.u, c_lo, c_lo + NC, taddr, false, none, ready);
+                if (!ok) break;
+            } else {
+                if (!(ok = ready())) break;
+                float4 *p = part_of(pair, ncuts == 0 && w.pos - (w.kb1 - w.kb0) == runs.start(pair) ? 0 : 1);
+#pragma unroll 1
+                for (int c = 0; c < BN / 64; ++c) {
+                    uint32_t v[32];
+                    const int blk = MODE == kGate ? (c < NC ? c_lo + c : BN / 64 + c_lo + c - NC) : c_lo + c;
+                    ptx::tmem_ld32(taddr + blk * 32, v);
+                    put(p, c, v);
+                }
+            }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
+            if (cut) {
+                const Cut x = cut_of(w.u);
+                if (ncuts == 0) cuts[0] = x;
+                else cuts[1] = x;
+                ++ncuts;
+                __threadfence();
+                __syncwarp();
+                // low half: parts written; high half: holders that need them no more (one
+                // with no share of the columns needs none of them)
+                if (lane == 0)
+                    atomicAdd(args.ticket + ((int64_t)x.u * 2 + rank) * kEpiWarps + ew,
+                              x.hi > x.lo ? 1u : 0x10001u);
+            }
         }
+        if (ok && !joins) join();
         if (lane == 0) ptx::bulk_wait_group<0>();
         __syncwarp();
     }
@@ -395,42 +547,49 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
 
 // ------------------------------------------------------------ host side --
 
-template <int MODE, int BN>
-cudaError_t launch_bn(const Maps &maps, Args args, cudaStream_t s) {
+// How `units` tiles of kb k-blocks go over `pairs` SM pairs: the first `cut` of them are
+// split into `runs` equal runs (so that all pairs end together), the rest are whole.
+// With few tiles all are cut, into runs of kMinRun k-blocks at least.
+void split_work(int64_t units, int kb, int pairs, int *cut, int *runs) {
+    const int64_t waves = units / pairs;
+    if (waves > 0) {
+        *cut = units % pairs == 0 ? 0 : (int)(units - (waves - 1) * pairs);
+        *runs = pairs;
+    } else {
+        *cut = (int)units;
+        *runs = (int)std::max<int64_t>(units, std::min<int64_t>(pairs, units * kb / kMinRun));
+    }
+    // every run holds k-blocks
+    *runs = (int)std::max<int64_t>(1, std::min<int64_t>(*runs, (int64_t)*cut * kb));
+}
+
+int64_t tiles_of(int rows, int cols, bool gate) {
+    const int k = gate ? BN / 2 : BN;
+    return (int64_t)((rows + 2 * BM - 1) / (2 * BM)) * ((cols + k - 1) / k);
+}
+
+template <int MODE>
+cudaError_t launch(const Maps &maps, Args args, cudaStream_t s) {
     const int problems = MODE == kWGrad ? 3 : 1;
-    args.units = 0;
+    int64_t units = 0;
     for (int p = 0; p < 3; ++p) {
-        args.first[p] = args.units;
+        args.first[p] = (int)units;
         if (p >= problems) continue;
         constexpr int kCols = MODE == kGate ? BN / 2 : BN;
         args.mt[p] = (args.rows[p] + 2 * BM - 1) / (2 * BM);
         args.nb[p] = (args.cols[p] + kCols - 1) / kCols;
-        args.units += args.mt[p] * args.nb[p];
+        units += tiles_of(args.rows[p], args.cols[p], MODE == kGate);
     }
+    if (units > (1 << 30)) return cudaErrorInvalidValue;
+    args.units = (int)units;
+    const int all = std::max(1, std::min(sm_count(), kFfnMaxCtas) / 2);
+    split_work(units, args.kb, all, &args.cut, &args.runs);
+    const int pairs = units >= all ? all : args.runs;
     args.idesc = idesc(args.f16 != 0, 2 * BM, BN, MODE == kWGrad, !(MODE == kDHid || MODE == kDX));
-    constexpr size_t kSmem = Geo<BN>::kSmem;
-    const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(dense_gemm_kernel<MODE, BN>), (int)kSmem);
+    const cudaError_t e =
+        ensure_dynamic_smem(reinterpret_cast<const void *>(dense_gemm_kernel<MODE>), (int)kSmem);
     if (e != cudaSuccess) return e;
-    const int pairs = std::max(1, std::min(sm_count() / 2, args.units));
-    return launch_k(dense_gemm_kernel<MODE, BN>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
-}
-
-// 256-column tiles, or 128-column tiles where they leave fewer SMs idle: the
-// waves of tiles over the SM pairs times the tile's width, 128-column tiles
-// counted an eighth dearer (they load twice the A bytes per MMA).
-template <int MODE>
-cudaError_t launch(const Maps &maps, const Args &args, cudaStream_t s) {
-    const int pairs = std::max(1, sm_count() / 2);
-    int64_t u[2] = {0, 0};
-    for (int p = 0; p < (MODE == kWGrad ? 3 : 1); ++p) {
-        const int64_t mt = (args.rows[p] + 2 * BM - 1) / (2 * BM);
-        const int64_t cols = (int64_t)args.cols[p] * (MODE == kGate ? 2 : 1);
-        u[0] += mt * ((cols + 255) / 256);
-        u[1] += mt * ((cols + 127) / 128);
-    }
-    const int64_t wide = (u[0] + pairs - 1) / pairs * 16, narrow = (u[1] + pairs - 1) / pairs * 9;
-    return narrow < wide ? launch_bn<MODE, 128>(maps, args, s) : launch_bn<MODE, 256>(maps, args, s);
+    return launch_k(dense_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
 }
 
 constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B, kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;
@@ -454,9 +613,28 @@ bool map_out32(CUtensorMap *m, const void *p, int cols, int rows) {
 
 using namespace ffn;
 
+size_t ffn_dense_part_bytes(int T, int d, int n, bool train) {
+    // the most pairs that have a run in any of the products
+    const int kd = (d + BK - 1) / BK, kn = (n + BK - 1) / BK, kt = (T + BK - 1) / BK;
+    int64_t most = 1;
+    auto product = [&](int64_t units, int kb) {
+        int cut, runs;
+        split_work(units, kb, kFfnMaxCtas / 2, &cut, &runs);
+        most = std::max<int64_t>(most, runs);
+    };
+    product(tiles_of(T, n, true), kd);
+    product(tiles_of(T, d, false), kn);
+    if (train) {
+        product(tiles_of(T, n, false), kd);
+        product(tiles_of(T, d, false), 2 * kn);
+        product(2 * tiles_of(d, n, false) + tiles_of(n, d, false), kt);
+    }
+    return (size_t)most * 2 * 2 * kEpiWarps * kPartVecs * sizeof(float4);
+}
+
 cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
-                            int act, bool f16, void *H, float *A1, float *A3, uint32_t *err,
-                            cudaStream_t s) {
+                            int act, bool f16, void *H, float *A1, float *A3, float4 *part,
+                            uint32_t *ticket, uint32_t *err, cudaStream_t s) {
     Maps m{};
     if (!map_a(&m.a[0], f16, X, d, T) || !map_64(&m.b[0], f16, W1, n, d) ||
         !map_64(&m.b[1], f16, W3, n, d) || !map_out(&m.o[0], f16, H, n, T))
@@ -470,12 +648,14 @@ cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T
     a.f16 = f16;
     a.act = act;
     a.pre = A1 != nullptr;
+    a.part = part;
+    a.ticket = ticket;
     a.err = err;
     return launch<kGate>(m, a, s);
 }
 
 cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, bool f16, void *Y,
-                            uint32_t *err, cudaStream_t s) {
+                            float4 *part, uint32_t *ticket, uint32_t *err, cudaStream_t s) {
     Maps m{};
     if (!map_a(&m.a[0], f16, H, n, T) || !map_64(&m.b[0], f16, W2, d, n) ||
         !map_out(&m.o[0], f16, Y, d, T))
@@ -485,6 +665,8 @@ cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, 
     a.cols[0] = d;
     a.kb = (n + BK - 1) / BK;
     a.f16 = f16;
+    a.part = part;
+    a.ticket = ticket;
     a.err = err;
     return launch<kDown>(m, a, s);
 }
@@ -492,8 +674,8 @@ cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, 
 cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
                                 const void *W2, const void *H, const float *A1, const float *A3,
                                 int T, int d, int n, int act, bool f16, void *dA1, void *dA3,
-                                void *dX, void *dW1, void *dW3, void *dW2, uint32_t *err,
-                                cudaStream_t s) {
+                                void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
+                                uint32_t *ticket, uint32_t *err, cudaStream_t s) {
     Maps m{};
     if (!map_a(&m.a[0], f16, dY, d, T) || !map_64(&m.b[0], f16, W2, d, n) ||
         !map_out(&m.o[0], f16, dA1, n, T) || !map_out(&m.o[1], f16, dA3, n, T))
@@ -506,6 +688,8 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
     a.act = act;
     a.a1 = A1;
     a.a3 = A3;
+    a.part = part;
+    a.ticket = ticket;
     a.err = err;
     cudaError_t e = launch<kDHid>(m, a, s);
     if (e != cudaSuccess) return e;

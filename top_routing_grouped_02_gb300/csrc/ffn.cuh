@@ -35,6 +35,37 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
     }
 }
 
+// Polls a word in global memory (acquire) until (word & mask) == want, bounded like
+// bounded_wait.
+__device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint32_t want,
+                                          uint32_t *err) {
+    if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        __nanosleep(32);
+        if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
+        if ((spin & 15u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, MOE_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// W units of work cut into `parts` equal runs, whatever the tiles they belong to.
+struct Runs {
+    int64_t W;
+    int parts;
+    __device__ __forceinline__ int64_t start(int c) const { return c >= parts ? W : quot(W * c, parts); }
+    // the run that holds unit u
+    __device__ __forceinline__ int owner(int64_t u) const { return (int)quot((u + 1) * parts - 1, W); }
+    // quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division
+    // costs some 0.3 us here)
+    static __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+        if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+        return a / b;
+    }
+};
+
 // Both activations are a * sigmoid(z(a)): SiLU with z = a, GELU's tanh form
 // 0.5 a (1 + tanh(u)) = a sigmoid(2 u) with z = 2 u = k (a + 0.044715 a^3),
 // k = 2 sqrt(2 / pi). sg: the sigmoid.

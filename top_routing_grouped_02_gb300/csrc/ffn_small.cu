@@ -74,23 +74,6 @@ struct SmallCtl {
 };
 static_assert(sizeof(SmallCtl) <= 256, "control block");
 
-// A CTA's run of a product's units.
-struct Run {
-    int64_t W;
-    int ctas, kbs;
-    __device__ __forceinline__ Run(const Product &p)
-        : W((int64_t)p.tiles * p.kbs), ctas(p.ctas), kbs(p.kbs) {}
-    __device__ __forceinline__ int64_t start(int c) const { return c >= ctas ? W : quot(W * c, ctas); }
-    // the CTA whose run holds unit u
-    __device__ __forceinline__ int owner(int64_t u) const { return (int)quot((u + 1) * ctas - 1, W); }
-    // quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division
-    // costs some 0.3 us here)
-    static __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-        if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-        return a / b;
-    }
-};
-
 // TMEM: 16 consecutive columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -102,21 +85,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
-}
-
-// Polls a word in global memory (acquire) until (word & mask) == want.
-__device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint32_t want,
-                                          uint32_t *err) {
-    if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
-    const uint64_t t0 = ptx::globaltimer_ns();
-    for (uint32_t spin = 1;; ++spin) {
-        __nanosleep(32);
-        if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
-        if ((spin & 15u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, MOE_DEVERR_TIMEOUT);
-            return false;
-        }
-    }
 }
 
 // Epilogue of one product (warps 4-7): the CTA's segments, then the joins of its cut
@@ -131,7 +99,7 @@ template <int MATS, int NT, typename Joined>
 __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p, uint32_t *ticket,
                                          SmallCtl *ctl, uint32_t tmem_base, int &seg, Joined joined) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, T = args.T;
-    const Run run(p);
+    const Runs run{(int64_t)p.tiles * p.kbs, p.ctas};
     const int64_t begin = run.start(blockIdx.x), end = run.start(blockIdx.x + 1);
     if (begin == end) return true;
     const bool f16 = args.f16 != 0;
@@ -314,7 +282,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             const Product &p = args.p[ph];
-            const Run run(p);
+            const Runs run{(int64_t)p.tiles * p.kbs, p.ctas};
             const int64_t begin = run.start(blockIdx.x);
             const int count = (int)(run.start(blockIdx.x + 1) - begin);
             int tile = (int)(begin / p.kbs), kb = (int)(begin - (int64_t)tile * p.kbs);
@@ -394,7 +362,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             const Product &p = args.p[ph];
-            const Run run(p);
+            const Runs run{(int64_t)p.tiles * p.kbs, p.ctas};
             const int64_t begin = run.start(blockIdx.x);
             const int count = (int)(run.start(blockIdx.x + 1) - begin);
             int kb = (int)(begin % p.kbs);

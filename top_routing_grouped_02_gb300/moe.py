@@ -676,7 +676,8 @@ def moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=None, wdtype=None, dx=
         scratch.numel(), _raw_stream(stream, x.device))
     if st != MOE_OK:
         raise MoeError("moe_layernorm_backward", st)
-    return dx, grads[0], grads[1]
+    dgamma, dbeta = grads.unbind(0)
+    return dx, dgamma, dbeta
 
 
 def moe_dropout(x, p: float, seed: int, offset: int = 0, residual=None, offset_dev=None, y=None,
@@ -718,7 +719,7 @@ ACTS = {"silu": 0, "gelu": 1}
 
 def ffn_workspace(T: int, d: int, n: int, train: bool = False, device=None, stream=None):
     """A workspace (uint8, control words zeroed) of the dense block's calls for up to
-    T tokens; train: of moe_ffn_backward too."""
+    T tokens; train: of moe_ffn_train and moe_ffn_backward too."""
     nbytes = int(lib().moe_ffn_workspace_bytes(T, d, n, int(train)))
     if nbytes == 0:
         raise ValueError("invalid feed-forward shape")
@@ -768,10 +769,11 @@ def moe_ffn(x, W1, W3, W2, act: str = "silu", ws=None, Y=None, stream=None):
 
 
 def moe_ffn_train(x, W1, W3, W2, act: str = "silu", ws=None, stream=None):
-    """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3 fp32)."""
+    """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3 fp32). ws:
+    ffn_workspace(..., train=True)."""
     T, d, n = _ffn_shape(x, W1, W3, W2, act)
     if ws is None:
-        ws = ffn_workspace(T, d, n, device=x.device, stream=stream)
+        ws = ffn_workspace(T, d, n, train=True, device=x.device, stream=stream)
     Y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     H = torch.empty((T, n), dtype=x.dtype, device=x.device)
     A1, A3 = (torch.empty((T, n), dtype=torch.float32, device=x.device) for _ in range(2))
