@@ -78,7 +78,7 @@ FfnWs ffn_ws(int T, int d, int n, bool train) {
     w.da3 = w.da1 + act;
     w.part = train ? w.da3 + act : w.h + act;
     const bool tiled = train || T > kFfnStreamTokens;
-    w.total = w.part + (tiled ? align256(ffn_dense_part_bytes(T, d, n, train)) : 0);
+    w.total = w.part + (tiled ? align256(ffn_dense_part_bytes()) : 0);
     // a workspace for T tokens serves fewer on the weight-streaming kernel
     const int few = std::min(T, kFfnStreamTokens);
     w.total = std::max(w.total, w.h + align256((size_t)few * n * 2) +

@@ -238,7 +238,7 @@ constexpr size_t kFfnControlBytes =  // a ticket for each warp of each tile of t
 size_t ffn_stream_part_bytes(int T, int d, int n);
 // Scratch of the tiled products' joins (part; ticket: counters that are zero between
 // launches, 16 for each of up to kFfnMaxCtas cut tiles).
-size_t ffn_dense_part_bytes(int T, int d, int n, bool train);
+size_t ffn_dense_part_bytes();
 cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, const void *W2, int T,
                               int d, int n, int act, bool f16, void *H, void *Y, float *part,
                               uint32_t *ticket, uint32_t *err, cudaStream_t s);

@@ -14,12 +14,14 @@
 // other. gate/up: the even CTA's half of B is W1's columns and the odd CTA's W3's,
 // so a thread finds a1 and a3 of one element in its own TMEM lane and H leaves in
 // the epilogue; neither A1 nor A3 is read back from memory in the forward.
-// Tiles rarely come out even over the SM pairs, so the last ones (up to two a pair) are
-// cut: their k-blocks form one sequence, split into equal runs, one per pair. A tile
-// that is cut is joined by the pairs that hold its parts: every epilogue warp writes
-// its part (fp32) to the workspace, and once all have, each adds all parts, in the order
-// of the runs, of its share of the columns: the result does not depend on timing. The
-// cut tiles come first in each pair's work, so that joining overlaps whole tiles.
+// Tiles rarely come out even over the SM pairs. Where that idles the pairs for longer
+// than a join takes (split_work), tiles are cut along the reduction: few tiles each into
+// as many equal runs as there are pairs for it, or, of many, the last ones (up to two a
+// pair) into one equal run per pair. The pairs that hold parts of a tile join it: every
+// epilogue warp writes its part (fp32) to the workspace, but for its own share of the
+// columns where the accumulator can wait, and once all have, each adds the parts of its
+// share in the order of the runs: the result does not depend on timing. The cut tiles
+// come first in each pair's work, so that joining overlaps whole tiles.
 // All tails (T, d, n need not be multiples of a tile) are left to TMA: loads
 // outside a tensor give zeros, which add nothing, and stores outside write nothing.
 //
@@ -107,7 +109,7 @@ struct Maps {
 struct Args {
     int units;           // tiles of all problems
     int cut;             // the first `cut` of them are split over the pairs' runs
-    int runs;            // pairs that have a run
+    int runs, split;     // pairs that have a run; runs per cut tile, or 0 (see Runs)
     int first[3];        // first unit of each problem (kWGrad: three, else one)
     int mt[3], nb[3];    // row-tile pairs, column blocks
     int rows[3], cols[3];// of the outputs
@@ -135,7 +137,7 @@ struct Work {
     int u, kb0, kb1;   // current: tile, its k-blocks
     __device__ __forceinline__ Work(const Args &a, int pair_, int pairs_)
         : pair(pair_), pairs(pairs_), units(a.units), cut(a.cut), kb(a.kb), next(a.cut + pair_) {
-        const Runs runs{(int64_t)a.cut * a.kb, a.runs};
+        const Runs runs(a.cut, a.kb, a.runs, a.split);
         pos = runs.start(pair);
         end = runs.start(pair + 1);
     }
@@ -334,8 +336,11 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         struct Cut {
             int u, p0, P, lo, hi;
             const float4 *first;
+            // this pair's own part of its share waits in the accumulator `acc` (the run's
+            // last segment), else ~0
+            uint32_t acc, taddr;
         };
-        const Runs runs{(int64_t)args.cut * args.kb, args.runs};
+        const Runs runs(args.cut, args.kb, args.runs, args.split);
         auto cut_of = [&](int u) {
             Cut x;
             x.u = u;
@@ -348,11 +353,18 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             x.first = part_of(x.p0, runs.start(x.p0) == t0 ? 0 : 1);
             return x;
         };
-        // 32 columns of a cut tile from its parts, in the order of the runs
-        auto gather = [&](const Cut &x, int blk, uint32_t (&v)[32]) {
+        // 32 columns of a cut tile from its parts, in the order of the runs; blk: their
+        // block in the parts, col: in the accumulator
+        auto gather = [&](const Cut &x, int blk, int col, uint32_t (&v)[32]) {
             float s[32] = {};
 #pragma unroll 1
             for (int p = 0; p < x.P; ++p) {
+                if (x.p0 + p == pair && x.acc != ~0u) {
+                    ptx::tmem_ld32(x.taddr + col * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(v[i]);
+                    continue;
+                }
                 const float4 *src = p == 0 ? x.first : part_of(x.p0 + p, 0);
                 float4 q[8];
 #pragma unroll
@@ -377,7 +389,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             if (!ready()) return false;
             // blk: 32-column block of the tile as the accumulator holds it
             auto load = [&](int blk, int own, uint32_t (&v)[32]) {
-                if (joined) gather(x, own, v);
+                if (joined) gather(x, own, blk, v);
                 else ptx::tmem_ld32(taddr + blk * 32, v);
             };
 #pragma unroll 1
@@ -475,7 +487,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             for (int i = 0; i < 2 && ok; ++i) {
                 if (i >= ncuts) break;
                 const Cut x = i == 0 ? cuts[0] : cuts[1];
-                if (x.lo == x.hi) continue;
+                if (x.lo == x.hi) continue;  // (its accumulator was not kept)
                 uint32_t *ticket = args.ticket + ((int64_t)x.u * 2 + rank) * kEpiWarps + ew;
                 auto ready = [&] {
                     bool all = true;
@@ -483,7 +495,10 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     return __shfl_sync(0xffffffffu, all, 0) != 0;
                 };
                 ok = finish(x.u, c_lo + x.lo, c_lo + x.hi, 0, true, x, ready);
+                ptx::tc_fence_before();
                 __syncwarp();  // every lane has its parts
+                if (ok && x.acc != ~0u && lane == 0)
+                    ptx::mbar_arrive_cluster(tempty0 + x.acc * (uint32_t)sizeof(uint64_t));
                 // the last holder of the tile returns its ticket to zero
                 if (ok && lane == 0 && atomicAdd(ticket, 0x10000u) >> 16 == (uint32_t)(x.P - 1)) *ticket = 0;
             }
@@ -506,21 +521,22 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 ok = finish(w.u, c_lo, c_lo + NC, taddr, false, none, ready);
                 if (!ok) break;
             } else {
+                Cut x = cut_of(w.u);
+                const int64_t seg = (int64_t)w.u * args.kb + w.kb0;  // its first k-block
+                const bool keep = w.pos == w.end && x.hi > x.lo;
+                x.acc = keep ? a : ~0u;
+                x.taddr = taddr;
                 if (!(ok = ready())) break;
-                float4 *p = part_of(pair, ncuts == 0 && w.pos - (w.kb1 - w.kb0) == runs.start(pair) ? 0 : 1);
+                float4 *p = part_of(pair, seg == runs.start(pair) ? 0 : 1);
 #pragma unroll 1
                 for (int c = 0; c < BN / 64; ++c) {
+                    const int own = MODE == kGate && c >= NC ? c - NC : c;
+                    if (keep && own >= x.lo && own < x.hi) continue;
                     uint32_t v[32];
-                    const int blk = MODE == kGate ? (c < NC ? c_lo + c : BN / 64 + c_lo + c - NC) : c_lo + c;
+                    const int blk = (MODE == kGate && c >= NC ? BN / 64 : 0) + c_lo + own;
                     ptx::tmem_ld32(taddr + blk * 32, v);
                     put(p, c, v);
                 }
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
-            if (cut) {
-                const Cut x = cut_of(w.u);
                 if (ncuts == 0) cuts[0] = x;
                 else cuts[1] = x;
                 ++ncuts;
@@ -531,7 +547,11 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 if (lane == 0)
                     atomicAdd(args.ticket + ((int64_t)x.u * 2 + rank) * kEpiWarps + ew,
                               x.hi > x.lo ? 1u : 0x10001u);
+                if (keep) continue;
             }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
         }
         if (ok && !joins) join();
         if (lane == 0) ptx::bulk_wait_group<0>();
@@ -548,19 +568,26 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
 // ------------------------------------------------------------ host side --
 
 // How `units` tiles of kb k-blocks go over `pairs` SM pairs: the first `cut` of them are
-// split into `runs` equal runs (so that all pairs end together), the rest are whole.
-// With few tiles all are cut, into runs of kMinRun k-blocks at least.
-void split_work(int64_t units, int kb, int pairs, int *cut, int *runs) {
-    const int64_t waves = units / pairs;
-    if (waves > 0) {
-        *cut = units % pairs == 0 ? 0 : (int)(units - (waves - 1) * pairs);
-        *runs = pairs;
-    } else {
-        *cut = (int)units;
-        *runs = (int)std::max<int64_t>(units, std::min<int64_t>(pairs, units * kb / kMinRun));
+// split into `runs` runs (`split` a tile, or equal ones), the rest are whole. Costs in
+// k-blocks of a pair's time (about 0.37 us): whole tiles take whole waves; a join takes
+// kJoin where every pair has one part (about 5 us for the 256 x 256 sums of each pair to
+// go through L2) and kJoinTail where it has two.
+constexpr int kJoin = 14, kJoinTail = 27;
+struct Split {
+    int cut, runs, split;
+};
+Split split_work(int64_t units, int kb, int pairs) {
+    const int64_t whole = (units + pairs - 1) / pairs * kb;
+    const int64_t tail = (units * kb + pairs - 1) / pairs + kJoinTail;
+    const int s = (int)std::min<int64_t>(pairs / units, kb / kMinRun);
+    if (s >= 2) {
+        const int64_t apart = (kb + s - 1) / s + kJoin;
+        if (apart < whole) return {(int)units, (int)units * s, s};
+    } else if (tail < whole) {
+        const int64_t waves = units / pairs;
+        return {(int)(units - std::max<int64_t>(0, waves - 1) * pairs), pairs, 0};
     }
-    // every run holds k-blocks
-    *runs = (int)std::max<int64_t>(1, std::min<int64_t>(*runs, (int64_t)*cut * kb));
+    return {0, 1, 0};
 }
 
 int64_t tiles_of(int rows, int cols, bool gate) {
@@ -583,8 +610,11 @@ cudaError_t launch(const Maps &maps, Args args, cudaStream_t s) {
     if (units > (1 << 30)) return cudaErrorInvalidValue;
     args.units = (int)units;
     const int all = std::max(1, std::min(sm_count(), kFfnMaxCtas) / 2);
-    split_work(units, args.kb, all, &args.cut, &args.runs);
-    const int pairs = units >= all ? all : args.runs;
+    const Split sp = split_work(units, args.kb, all);
+    args.cut = sp.cut;
+    args.runs = sp.runs;
+    args.split = sp.split;
+    const int pairs = (int)std::min<int64_t>(all, std::max<int64_t>(units, sp.runs));
     args.idesc = idesc(args.f16 != 0, 2 * BM, BN, MODE == kWGrad, !(MODE == kDHid || MODE == kDX));
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(dense_gemm_kernel<MODE>), (int)kSmem);
@@ -613,23 +643,9 @@ bool map_out32(CUtensorMap *m, const void *p, int cols, int rows) {
 
 using namespace ffn;
 
-size_t ffn_dense_part_bytes(int T, int d, int n, bool train) {
-    // the most pairs that have a run in any of the products
-    const int kd = (d + BK - 1) / BK, kn = (n + BK - 1) / BK, kt = (T + BK - 1) / BK;
-    int64_t most = 1;
-    auto product = [&](int64_t units, int kb) {
-        int cut, runs;
-        split_work(units, kb, kFfnMaxCtas / 2, &cut, &runs);
-        most = std::max<int64_t>(most, runs);
-    };
-    product(tiles_of(T, n, true), kd);
-    product(tiles_of(T, d, false), kn);
-    if (train) {
-        product(tiles_of(T, n, false), kd);
-        product(tiles_of(T, d, false), 2 * kn);
-        product(2 * tiles_of(d, n, false) + tiles_of(n, d, false), kt);
-    }
-    return (size_t)most * 2 * 2 * kEpiWarps * kPartVecs * sizeof(float4);
+size_t ffn_dense_part_bytes() {
+    // two parts for each pair (which products are cut depends on the device's SMs)
+    return (size_t)(kFfnMaxCtas / 2) * 2 * 2 * kEpiWarps * kPartVecs * sizeof(float4);
 }
 
 cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,

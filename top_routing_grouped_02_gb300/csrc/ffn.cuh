@@ -51,13 +51,30 @@ __device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint
     }
 }
 
-// W units of work cut into `parts` equal runs, whatever the tiles they belong to.
+// The units of `tiles` tiles (kb each) cut into `parts` runs: equal ones, whatever the
+// tiles they belong to, or (split > 0, parts = tiles * split) `split` equal runs a
+// tile.
 struct Runs {
     int64_t W;
-    int parts;
-    __device__ __forceinline__ int64_t start(int c) const { return c >= parts ? W : quot(W * c, parts); }
+    int parts, kb, split;
+    __device__ __forceinline__ Runs(int tiles, int kb_, int parts_, int split_ = 0)
+        : W((int64_t)tiles * kb_), parts(parts_), kb(kb_), split(split_) {}
+    __device__ __forceinline__ int64_t start(int c) const {
+        if (c >= parts) return W;
+        if (split > 0) {
+            const int t = c / split;
+            return (int64_t)t * kb + (int)quot((int64_t)kb * (c - t * split), split);
+        }
+        return quot(W * c, parts);
+    }
     // the run that holds unit u
-    __device__ __forceinline__ int owner(int64_t u) const { return (int)quot((u + 1) * parts - 1, W); }
+    __device__ __forceinline__ int owner(int64_t u) const {
+        if (split > 0) {
+            const int t = (int)quot(u, kb);
+            return t * split + (int)quot((u - (int64_t)t * kb + 1) * split - 1, kb);
+        }
+        return (int)quot((u + 1) * parts - 1, W);
+    }
     // quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division
     // costs some 0.3 us here)
     static __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {

@@ -99,7 +99,7 @@ template <int MATS, int NT, typename Joined>
 __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p, uint32_t *ticket,
                                          SmallCtl *ctl, uint32_t tmem_base, int &seg, Joined joined) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, T = args.T;
-    const Runs run{(int64_t)p.tiles * p.kbs, p.ctas};
+    const Runs run(p.tiles, p.kbs, p.ctas);
     const int64_t begin = run.start(blockIdx.x), end = run.start(blockIdx.x + 1);
     if (begin == end) return true;
     const bool f16 = args.f16 != 0;
@@ -282,7 +282,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             const Product &p = args.p[ph];
-            const Runs run{(int64_t)p.tiles * p.kbs, p.ctas};
+            const Runs run(p.tiles, p.kbs, p.ctas);
             const int64_t begin = run.start(blockIdx.x);
             const int count = (int)(run.start(blockIdx.x + 1) - begin);
             int tile = (int)(begin / p.kbs), kb = (int)(begin - (int64_t)tile * p.kbs);
@@ -362,7 +362,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             const Product &p = args.p[ph];
-            const Runs run{(int64_t)p.tiles * p.kbs, p.ctas};
+            const Runs run(p.tiles, p.kbs, p.ctas);
             const int64_t begin = run.start(blockIdx.x);
             const int count = (int)(run.start(blockIdx.x + 1) - begin);
             int kb = (int)(begin % p.kbs);
