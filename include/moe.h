@@ -560,8 +560,13 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
                              int d, int n, moe_act_t act, moe_dtype_t type, void *Y, void *ws,
                              size_t ws_bytes, void *stream);
 
-/* Y and what the backward takes: H [T,n] of `type` and the pre-activations A1, A3
- * [T,n] fp32 (16-byte aligned). ws: a workspace for training. Two kernels. */
+/* Y and what the backward takes: H [T,n] of `type` and the pre-activations A1, A3 in
+ * fp32, each a buffer of moe_ffn_saved_floats(T, n) floats (16-byte aligned) in blocks
+ * of 32 tokens x 32 columns: element (t, j) lies at float
+ *   ((t / 32) * ceil(n / 32) + j / 32) * 1024 + (j % 32) / 4 * 128 + (t % 32) * 4 + j % 4
+ * (what lies in the blocks past T and n is not defined). ws: a workspace for training.
+ * Two kernels. */
+size_t moe_ffn_saved_floats(int T, int n);
 moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
                                    int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
                                    void *H, float *A1, float *A3, void *ws, size_t ws_bytes,

@@ -182,6 +182,11 @@ size_t moe_ffn_workspace_bytes(int T, int d, int n, int train) {
     return ffn_ws(T, d, n, train != 0).total;
 }
 
+size_t moe_ffn_saved_floats(int T, int n) {
+    if (T < 0 || n < 1) return 0;
+    return (size_t)((T + 31ll) / 32) * ((n + 31ll) / 32) * 1024;
+}
+
 moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream) {
     if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < kFfnControlBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;

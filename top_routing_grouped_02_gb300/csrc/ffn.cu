@@ -14,20 +14,22 @@
 // other. gate/up: the even CTA's half of B is W1's columns and the odd CTA's W3's,
 // so a thread finds a1 and a3 of one element in its own TMEM lane and H leaves in
 // the epilogue; neither A1 nor A3 is read back from memory in the forward.
-// Tiles rarely come out even over the SM pairs. Where that idles the pairs for longer
-// than a join takes (split_work), tiles are cut along the reduction: few tiles each into
-// as many equal runs as there are pairs for it, or, of many, the last ones (up to two a
-// pair) into one equal run per pair. The pairs that hold parts of a tile join it: every
-// epilogue warp writes its part (fp32) to the workspace, but for its own share of the
-// columns where the accumulator can wait, and once all have, each adds the parts of its
-// share in the order of the runs: the result does not depend on timing. The cut tiles
-// come first in each pair's work, so that joining overlaps whole tiles.
+// Tiles rarely come out even over the SM pairs. Where the tiles past the last whole wave
+// (or all, if they are few) leave half of the pairs idle or more, each is cut along the
+// reduction into as many equal segments as there are pairs for it (split_work). The
+// pairs that hold a tile's segments join them: every epilogue warp writes its sums
+// (fp32) to the workspace, but for its own share of the columns, and once all have, each
+// adds its share, in the order of the segments: the result does not depend on timing.
+// The cut tiles come first in each pair's work, so that joining overlaps whole tiles.
+// (Equal runs over all of the last tiles, cut anywhere, balance better and measured
+// slower: pairs that share operands then read them at different places of the
+// reduction, 746 against 571 us for dX of 4096 tokens, d = 4096, n = 14336.)
 // All tails (T, d, n need not be multiples of a tile) are left to TMA: loads
 // outside a tensor give zeros, which add nothing, and stores outside write nothing.
 //
 // The backward's operands dA1, dA3 and the forward's H are rounded to 16 bits
 // because the tensor cores multiply 16-bit operands; A1 and A3 are kept in fp32
-// for the backward so that dA1 and dA3 carry one rounding each and not three.
+// for the backward (in blocks, see pre_block) so that dA1 and dA3 carry one rounding each and not three.
 //
 // Warps: 0 TMA producer, 1 MMA issuer (even CTA), 2 TMEM allocation, 4-11 epilogue
 // (two warps per quadrant of 32 TMEM lanes, splitting the columns). Waits are
@@ -96,9 +98,6 @@ constexpr uint32_t kStageBytes = kABytes + kBoxes * kBox;
 constexpr int kStages = 6;                   // 192 KB
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes +
                          (size_t)kEpiWarps * kEpiBufs * kEpiBuf + 256;
-// Shortest run of k-blocks worth a join (a part is written and read at the cost of
-// about four).
-constexpr int kMinRun = 8;
 // Vectors (float4) of one warp's part: BN / 2 columns of 32 rows.
 constexpr int kPartVecs = BN / 2 * 32 / 4;
 
@@ -108,20 +107,29 @@ struct Maps {
 
 struct Args {
     int units;           // tiles of all problems
-    int cut;             // the first `cut` of them are split over the pairs' runs
-    int runs, split;     // pairs that have a run; runs per cut tile, or 0 (see Runs)
+    int cut, split;      // the first `cut` of them are cut into `split` segments each
     int first[3];        // first unit of each problem (kWGrad: three, else one)
     int mt[3], nb[3];    // row-tile pairs, column blocks
     int rows[3], cols[3];// of the outputs
     int kb, kb_half;     // k-blocks; kDX: those of its first half
     uint32_t idesc;
     int f16, act;
-    int pre;             // kGate: store A1, A3
-    const float *a1, *a3;// kDHid
-    float4 *part;        // [pair][first / last tile of its run][CTA][warp][kPartVecs]
+    float *a1, *a3;      // pre-activations in blocks (pre_block): kGate stores them, or
+                         // NULL; kDHid reads them
+    float4 *part;        // [segment][CTA][warp][kPartVecs]
     uint32_t *ticket;    // [cut][CTA][warp]
     uint32_t *err;
 };
+
+// The pre-activations A1, A3 [T, n] fp32 in blocks of 32 x 32: lane r of an epilogue
+// warp holds row r of a block, so that a block is 8 x 32 vectors of four columns, and
+// a warp stores and loads 512 consecutive bytes an instruction. (As rows, each
+// instruction touches 32 lines, and the 16 loads of a block took as long as the main
+// loop of a short reduction.)
+__device__ __forceinline__ float4 *pre_block(float *a, int n, int row, int col, int lane) {
+    const int64_t block = (int64_t)(row / 32) * ((n + 31) / 32) + col / 32;
+    return reinterpret_cast<float4 *>(a) + block * 256 + lane;
+}
 
 struct Ctl {
     uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
@@ -129,26 +137,26 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 256, "control block");
 
-// A pair's work: the segments of its run over the cut tiles, then whole tiles.
+// A pair's work: its segment of a cut tile, if it has one (pair = tile * split +
+// segment), then whole tiles.
 struct Work {
-    int pair, pairs, units, cut, kb;
-    int64_t pos, end;  // rest of the run
-    int next;          // next whole tile
-    int u, kb0, kb1;   // current: tile, its k-blocks
-    __device__ __forceinline__ Work(const Args &a, int pair_, int pairs_)
-        : pair(pair_), pairs(pairs_), units(a.units), cut(a.cut), kb(a.kb), next(a.cut + pair_) {
-        const Runs runs(a.cut, a.kb, a.runs, a.split);
-        pos = runs.start(pair);
-        end = runs.start(pair + 1);
-    }
-    __device__ __forceinline__ bool step() {
-        if (pos < end) {
-            u = (int)Runs::quot(pos, kb);
-            kb0 = (int)(pos - (int64_t)u * kb);
-            kb1 = (int)min((int64_t)kb, kb0 + (end - pos));
-            pos += kb1 - kb0;
-            return true;
+    int pairs, units, kb, next;
+    int u, kb0, kb1;  // current: tile, its k-blocks
+    bool cut;         // a segment
+    __device__ __forceinline__ Work(const Args &a, int pair, int pairs_)
+        : pairs(pairs_), units(a.units), kb(a.kb), next(a.cut + pair), cut(false) {
+        if (pair < a.cut * a.split) {
+            u = pair / a.split;
+            const int j = pair - u * a.split;
+            kb0 = (int)((int64_t)kb * j / a.split);
+            kb1 = (int)((int64_t)kb * (j + 1) / a.split);
+            cut = true;
         }
+    }
+    bool started = false;
+    __device__ __forceinline__ bool step() {
+        if (cut && !started) return started = true;
+        cut = false;
         if (next >= units) return false;
         u = next;
         next += pairs;
@@ -319,9 +327,9 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // output columns of a tile
         constexpr int NC = kCols / 64;                      // 32-column chunks of a warp
         const int c_lo = half * NC;
-        // part of pair p's first (0) or last (1) tile: this warp's, at this lane
-        auto part_of = [&](int p, int which) {
-            return args.part + ((((int64_t)p * 2 + which) * 2 + rank) * kEpiWarps + ew) * kPartVecs + lane;
+        // this warp's part of pair p's segment, at this lane
+        auto part_of = [&](int p) {
+            return args.part + (((int64_t)p * 2 + rank) * kEpiWarps + ew) * kPartVecs + lane;
         };
         // a part's vectors of 32 columns starting at block blk (of 32 columns)
         auto put = [&](float4 *p, int blk, const uint32_t (&v)[32]) {
@@ -331,41 +339,21 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                        make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                                    __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
         };
-        // a cut tile of this pair's run: the runs [p0, p0 + P) that hold it, the chunks
-        // [lo, hi) of this warp that this pair joins
-        struct Cut {
-            int u, p0, P, lo, hi;
-            const float4 *first;
-            // this pair's own part of its share waits in the accumulator `acc` (the run's
-            // last segment), else ~0
-            uint32_t acc, taddr;
-        };
-        const Runs runs(args.cut, args.kb, args.runs, args.split);
-        auto cut_of = [&](int u) {
-            Cut x;
-            x.u = u;
-            const int64_t t0 = (int64_t)u * args.kb;
-            x.p0 = runs.owner(t0);
-            x.P = runs.owner(t0 + args.kb - 1) - x.p0 + 1;
-            const int k = pair - x.p0;
-            x.lo = NC * k / x.P;
-            x.hi = NC * (k + 1) / x.P;
-            x.first = part_of(x.p0, runs.start(x.p0) == t0 ? 0 : 1);
-            return x;
-        };
-        // 32 columns of a cut tile from its parts, in the order of the runs; blk: their
-        // block in the parts, col: in the accumulator
-        auto gather = [&](const Cut &x, int blk, int col, uint32_t (&v)[32]) {
+        // 32 columns of this pair's cut tile from its segments, in their order, this
+        // pair's own from its accumulator; blk: their block in the parts, col: in the
+        // accumulator
+        auto gather = [&](int blk, uint32_t taddr, int col, uint32_t (&v)[32]) {
             float s[32] = {};
+            const int p0 = pair - pair % args.split;
 #pragma unroll 1
-            for (int p = 0; p < x.P; ++p) {
-                if (x.p0 + p == pair && x.acc != ~0u) {
-                    ptx::tmem_ld32(x.taddr + col * 32, v);
+            for (int p = p0; p < p0 + args.split; ++p) {
+                if (p == pair) {
+                    ptx::tmem_ld32(taddr + col * 32, v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(v[i]);
                     continue;
                 }
-                const float4 *src = p == 0 ? x.first : part_of(x.p0 + p, 0);
+                const float4 *src = part_of(p);
                 float4 q[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) q[i] = __ldcg(src + (blk * 8 + i) * 32);
@@ -381,15 +369,30 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(s[i]);
         };
         // The chunks [lo, hi) of this warp's columns of a tile to the outputs: from the
-        // accumulator at taddr, or from the parts of x where joined.
-        auto finish = [&](int u, int lo, int hi, uint32_t taddr, bool joined, const Cut &x, auto ready) {
+        // accumulator at taddr alone, or joined from the tile's segments. ready(): waits for
+        // either. False if that gave up.
+        auto finish = [&](int u, int lo, int hi, uint32_t taddr, bool joined, auto ready) {
             const Unit un = unit_at(u);
             const int rows = args.rows[un.p], cols = args.cols[un.p];
             const int y0 = un.row0 + q * 32;
+            // kDHid: this row's A1, A3 of a chunk, loaded while the one before is stored
+            float4 x1[8], x3[8];
+            auto load_pre = [&](int c) {
+                const int x0 = un.nb * kCols + c * 32;
+                if (c >= hi || y0 >= rows || x0 >= cols) return;
+                const float4 *p1 = pre_block(args.a1, cols, y0, x0, lane);
+                const float4 *p3 = pre_block(args.a3, cols, y0, x0, lane);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x1[i] = __ldg(p1 + i * 32);
+                    x3[i] = __ldg(p3 + i * 32);
+                }
+            };
+            if constexpr (MODE == kDHid) load_pre(lo);
             if (!ready()) return false;
             // blk: 32-column block of the tile as the accumulator holds it
             auto load = [&](int blk, int own, uint32_t (&v)[32]) {
-                if (joined) gather(x, own, blk, v);
+                if (joined) gather(own, taddr, blk, v);
                 else ptx::tmem_ld32(taddr + blk * 32, v);
             };
 #pragma unroll 1
@@ -412,38 +415,18 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         o[i] = pack(h[0], h[1], f16);
                     }
                     store_box(o, x0, y0, &maps.o[0]);
-                    if (args.pre) {
-                        // fp32: two boxes of 16 columns each
-                        const bool in2 = x0 + 16 < cols;
-                        uint32_t lo16[16], hi16[16];
+                    if (args.a1 != nullptr) {
+                        float4 *p1 = pre_block(args.a1, cols, y0, x0, lane);
+                        float4 *p3 = pre_block(args.a3, cols, y0, x0, lane);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            lo16[i] = g[i];
-                            hi16[i] = g[16 + i];
+                        for (int i = 0; i < 8; ++i) {
+                            p1[i * 32] = make_float4(__uint_as_float(g[4 * i]), __uint_as_float(g[4 * i + 1]),
+                                                     __uint_as_float(g[4 * i + 2]), __uint_as_float(g[4 * i + 3]));
+                            p3[i * 32] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                     __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
                         }
-                        store_box(lo16, x0, y0, &maps.o[1]);
-                        if (in2) store_box(hi16, x0 + 16, y0, &maps.o[1]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            lo16[i] = v[i];
-                            hi16[i] = v[16 + i];
-                        }
-                        store_box(lo16, x0, y0, &maps.o[2]);
-                        if (in2) store_box(hi16, x0 + 16, y0, &maps.o[2]);
                     }
                 } else if constexpr (MODE == kDHid) {
-                    // this row's A1, A3 of the chunk
-                    float4 x1[8], x3[8];
-                    const int row = y0 + lane;
-                    const int64_t off = (int64_t)row * cols + x0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const bool at = row < rows && x0 + 4 * i < cols;
-                        x1[i] = at ? __ldg(reinterpret_cast<const float4 *>(args.a1 + off) + i)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x3[i] = at ? __ldg(reinterpret_cast<const float4 *>(args.a3 + off) + i)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
                     uint32_t g[32], o1[16], o3[16];
                     load(c, own, g);
                     if (!in) continue;
@@ -462,6 +445,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         o1[i] = pack(r1[0], r1[1], f16);
                         o3[i] = pack(r3[0], r3[1], f16);
                     }
+                    load_pre(c + 1);
                     store_box(o1, x0, y0, &maps.o[0]);
                     store_box(o3, x0, y0, &maps.o[1]);
                 } else {
@@ -477,83 +461,61 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             return true;
         };
 
-        Cut cuts[2];
-        int ncuts = 0;
-        bool joins = false;  // the cut tiles are joined
-        bool ok = true;
-        // the joins of this run's cut tiles, once its last segment is written
-        auto join = [&] {
-            joins = true;
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (i >= ncuts) break;
-                const Cut x = i == 0 ? cuts[0] : cuts[1];
-                if (x.lo == x.hi) continue;  // (its accumulator was not kept)
-                uint32_t *ticket = args.ticket + ((int64_t)x.u * 2 + rank) * kEpiWarps + ew;
-                auto ready = [&] {
-                    bool all = true;
-                    if (lane == 0) all = word_wait(ticket, 0xffffu, (uint32_t)x.P, args.err);
-                    return __shfl_sync(0xffffffffu, all, 0) != 0;
-                };
-                ok = finish(x.u, c_lo + x.lo, c_lo + x.hi, 0, true, x, ready);
-                ptx::tc_fence_before();
-                __syncwarp();  // every lane has its parts
-                if (ok && x.acc != ~0u && lane == 0)
-                    ptx::mbar_arrive_cluster(tempty0 + x.acc * (uint32_t)sizeof(uint64_t));
-                // the last holder of the tile returns its ticket to zero
-                if (ok && lane == 0 && atomicAdd(ticket, 0x10000u) >> 16 == (uint32_t)(x.P - 1)) *ticket = 0;
-            }
-        };
-        for (Work w(args, pair, pairs); ok && w.step(); ++uc) {
+        // The pair's segment, its join, then the whole tiles; finish() stands in one place
+        // only, since its code comes cold from memory.
+        Work w(args, pair, pairs);
+        bool joining = false;
+        const int j = args.split > 0 ? pair % args.split : 0;
+        const int lo = args.split > 0 ? NC * j / args.split : 0;
+        const int hi = args.split > 0 ? NC * (j + 1) / args.split : 0;  // its share of a cut tile
+        while (w.step()) {
             const uint32_t a = uc & 1u;
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * BN;
-            const bool cut = w.kb1 - w.kb0 < args.kb;
-            if (w.u >= args.cut && !joins) {
-                join();
-                if (!ok) break;
-            }
-            auto ready = [&] {
+            uint32_t *ticket = args.ticket + ((int64_t)w.u * 2 + rank) * kEpiWarps + ew;
+            auto filled = [&] {
                 if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (uc >> 1) & 1u, args.err)) return false;
                 ptx::tc_fence_after();
                 return true;
             };
-            if (!cut) {
-                const Cut none{};
-                ok = finish(w.u, c_lo, c_lo + NC, taddr, false, none, ready);
-                if (!ok) break;
-            } else {
-                Cut x = cut_of(w.u);
-                const int64_t seg = (int64_t)w.u * args.kb + w.kb0;  // its first k-block
-                const bool keep = w.pos == w.end && x.hi > x.lo;
-                x.acc = keep ? a : ~0u;
-                x.taddr = taddr;
-                if (!(ok = ready())) break;
-                float4 *p = part_of(pair, seg == runs.start(pair) ? 0 : 1);
+            joining = w.cut;
+            if (joining) {
+                if (!filled()) break;
+                float4 *p = part_of(pair);
 #pragma unroll 1
                 for (int c = 0; c < BN / 64; ++c) {
                     const int own = MODE == kGate && c >= NC ? c - NC : c;
-                    if (keep && own >= x.lo && own < x.hi) continue;
+                    if (own >= lo && own < hi) continue;
                     uint32_t v[32];
-                    const int blk = (MODE == kGate && c >= NC ? BN / 64 : 0) + c_lo + own;
-                    ptx::tmem_ld32(taddr + blk * 32, v);
+                    ptx::tmem_ld32(taddr + ((MODE == kGate && c >= NC ? BN / 64 : 0) + c_lo + own) * 32, v);
                     put(p, c, v);
                 }
-                if (ncuts == 0) cuts[0] = x;
-                else cuts[1] = x;
-                ++ncuts;
                 __threadfence();
                 __syncwarp();
                 // low half: parts written; high half: holders that need them no more (one
                 // with no share of the columns needs none of them)
-                if (lane == 0)
-                    atomicAdd(args.ticket + ((int64_t)x.u * 2 + rank) * kEpiWarps + ew,
-                              x.hi > x.lo ? 1u : 0x10001u);
-                if (keep) continue;
+                if (lane == 0) atomicAdd(ticket, hi > lo ? 1u : 0x10001u);
+            }
+            if (!joining || hi > lo) {
+                auto ready = [&] {
+                    if (!joining) return filled();
+                    bool all = true;
+                    if (lane == 0) all = word_wait(ticket, 0xffffu, (uint32_t)args.split, args.err);
+                    return __shfl_sync(0xffffffffu, all, 0) != 0;
+                };
+                if (!finish(w.u, joining ? c_lo + lo : c_lo, joining ? c_lo + hi : c_lo + NC, taddr,
+                            joining, ready))
+                    break;
+                // every lane has its parts; the last holder returns the ticket to zero
+                __syncwarp();
+                if (joining && lane == 0 &&
+                    atomicAdd(ticket, 0x10000u) >> 16 == (uint32_t)(args.split - 1))
+                    *ticket = 0;
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
+            ++uc;
         }
-        if (ok && !joins) join();
         if (lane == 0) ptx::bulk_wait_group<0>();
         __syncwarp();
     }
@@ -567,27 +529,19 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
 
 // ------------------------------------------------------------ host side --
 
-// How `units` tiles of kb k-blocks go over `pairs` SM pairs: the first `cut` of them are
-// split into `runs` runs (`split` a tile, or equal ones), the rest are whole. Costs in
-// k-blocks of a pair's time (about 0.37 us): whole tiles take whole waves; a join takes
-// kJoin where every pair has one part (about 5 us for the 256 x 256 sums of each pair to
-// go through L2) and kJoinTail where it has two.
-constexpr int kJoin = 14, kJoinTail = 27;
-struct Split {
-    int cut, runs, split;
-};
-Split split_work(int64_t units, int kb, int pairs) {
-    const int64_t whole = (units + pairs - 1) / pairs * kb;
-    const int64_t tail = (units * kb + pairs - 1) / pairs + kJoinTail;
-    const int s = (int)std::min<int64_t>(pairs / units, kb / kMinRun);
-    if (s >= 2) {
-        const int64_t apart = (kb + s - 1) / s + kJoin;
-        if (apart < whole) return {(int)units, (int)units * s, s};
-    } else if (tail < whole) {
-        const int64_t waves = units / pairs;
-        return {(int)(units - std::max<int64_t>(0, waves - 1) * pairs), pairs, 0};
-    }
-    return {0, 1, 0};
+// Which of `units` tiles of kb k-blocks are cut over `pairs` SM pairs: those past the
+// last whole wave, where that is worth a join (about 5 us, the time of kJoin k-blocks,
+// for the 256 x 256 sums of each pair to go through L2). At least kMinRun k-blocks a
+// segment.
+constexpr int kJoin = 14, kMinRun = 8;
+void split_work(int64_t units, int kb, int pairs, int *cut, int *split) {
+    *cut = *split = 0;
+    const int64_t rest = units % pairs;
+    if (rest == 0) return;
+    const int s = (int)std::min<int64_t>(pairs / rest, kb / kMinRun);
+    if (s < 2 || (kb + s - 1) / s + kJoin >= kb) return;
+    *cut = (int)rest;
+    *split = s;
 }
 
 int64_t tiles_of(int rows, int cols, bool gate) {
@@ -610,11 +564,8 @@ cudaError_t launch(const Maps &maps, Args args, cudaStream_t s) {
     if (units > (1 << 30)) return cudaErrorInvalidValue;
     args.units = (int)units;
     const int all = std::max(1, std::min(sm_count(), kFfnMaxCtas) / 2);
-    const Split sp = split_work(units, args.kb, all);
-    args.cut = sp.cut;
-    args.runs = sp.runs;
-    args.split = sp.split;
-    const int pairs = (int)std::min<int64_t>(all, std::max<int64_t>(units, sp.runs));
+    split_work(units, args.kb, all, &args.cut, &args.split);
+    const int pairs = (int)std::min<int64_t>(all, std::max<int64_t>(units, args.cut * args.split));
     args.idesc = idesc(args.f16 != 0, 2 * BM, BN, MODE == kWGrad, !(MODE == kDHid || MODE == kDX));
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(dense_gemm_kernel<MODE>), (int)kSmem);
@@ -634,9 +585,6 @@ bool map_64(CUtensorMap *m, bool f16, const void *p, int cols, int rows) {
 bool map_out(CUtensorMap *m, bool f16, const void *p, int cols, int rows) {
     return make_map(m, map_type(f16), p, cols, rows, 32, 32, kSw64);
 }
-bool map_out32(CUtensorMap *m, const void *p, int cols, int rows) {
-    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p, cols, rows, 16, 32, kSw64);
-}
 
 }  // namespace
 }  // namespace ffn
@@ -644,8 +592,8 @@ bool map_out32(CUtensorMap *m, const void *p, int cols, int rows) {
 using namespace ffn;
 
 size_t ffn_dense_part_bytes() {
-    // two parts for each pair (which products are cut depends on the device's SMs)
-    return (size_t)(kFfnMaxCtas / 2) * 2 * 2 * kEpiWarps * kPartVecs * sizeof(float4);
+    // a segment for each pair (which products are cut depends on the device's SMs)
+    return (size_t)kFfnMaxCtas * kEpiWarps * kPartVecs * sizeof(float4);
 }
 
 cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
@@ -655,15 +603,14 @@ cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T
     if (!map_a(&m.a[0], f16, X, d, T) || !map_64(&m.b[0], f16, W1, n, d) ||
         !map_64(&m.b[1], f16, W3, n, d) || !map_out(&m.o[0], f16, H, n, T))
         return cudaErrorInvalidValue;
-    if (A1 != nullptr && (!map_out32(&m.o[1], A1, n, T) || !map_out32(&m.o[2], A3, n, T)))
-        return cudaErrorInvalidValue;
     Args a{};
     a.rows[0] = T;
     a.cols[0] = n;
     a.kb = (d + BK - 1) / BK;
     a.f16 = f16;
     a.act = act;
-    a.pre = A1 != nullptr;
+    a.a1 = A1;
+    a.a3 = A3;
     a.part = part;
     a.ticket = ticket;
     a.err = err;
@@ -702,8 +649,8 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
     a.kb = (d + BK - 1) / BK;
     a.f16 = f16;
     a.act = act;
-    a.a1 = A1;
-    a.a3 = A3;
+    a.a1 = const_cast<float *>(A1);
+    a.a3 = const_cast<float *>(A3);
     a.part = part;
     a.ticket = ticket;
     a.err = err;

@@ -51,38 +51,6 @@ __device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint
     }
 }
 
-// The units of `tiles` tiles (kb each) cut into `parts` runs: equal ones, whatever the
-// tiles they belong to, or (split > 0, parts = tiles * split) `split` equal runs a
-// tile.
-struct Runs {
-    int64_t W;
-    int parts, kb, split;
-    __device__ __forceinline__ Runs(int tiles, int kb_, int parts_, int split_ = 0)
-        : W((int64_t)tiles * kb_), parts(parts_), kb(kb_), split(split_) {}
-    __device__ __forceinline__ int64_t start(int c) const {
-        if (c >= parts) return W;
-        if (split > 0) {
-            const int t = c / split;
-            return (int64_t)t * kb + (int)quot((int64_t)kb * (c - t * split), split);
-        }
-        return quot(W * c, parts);
-    }
-    // the run that holds unit u
-    __device__ __forceinline__ int owner(int64_t u) const {
-        if (split > 0) {
-            const int t = (int)quot(u, kb);
-            return t * split + (int)quot((u - (int64_t)t * kb + 1) * split - 1, kb);
-        }
-        return (int)quot((u + 1) * parts - 1, W);
-    }
-    // quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division
-    // costs some 0.3 us here)
-    static __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-        if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-        return a / b;
-    }
-};
-
 // Both activations are a * sigmoid(z(a)): SiLU with z = a, GELU's tanh form
 // 0.5 a (1 + tanh(u)) = a sigmoid(2 u) with z = 2 u = k (a + 0.044715 a^3),
 // k = 2 sqrt(2 / pi). sg: the sigmoid.

@@ -74,6 +74,23 @@ struct SmallCtl {
 };
 static_assert(sizeof(SmallCtl) <= 256, "control block");
 
+// The units of a product cut into equal runs, one per CTA, whatever the tiles they
+// belong to.
+struct Runs {
+    int64_t W;
+    int parts;
+    __device__ __forceinline__ Runs(const Product &p) : W((int64_t)p.tiles * p.kbs), parts(p.ctas) {}
+    __device__ __forceinline__ int64_t start(int c) const { return c >= parts ? W : quot(W * c, parts); }
+    // the run that holds unit u
+    __device__ __forceinline__ int owner(int64_t u) const { return (int)quot((u + 1) * parts - 1, W); }
+    // quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division
+    // costs some 0.3 us here)
+    static __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+        if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+        return a / b;
+    }
+};
+
 // TMEM: 16 consecutive columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -99,7 +116,7 @@ template <int MATS, int NT, typename Joined>
 __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p, uint32_t *ticket,
                                          SmallCtl *ctl, uint32_t tmem_base, int &seg, Joined joined) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, T = args.T;
-    const Runs run(p.tiles, p.kbs, p.ctas);
+    const Runs run(p);
     const int64_t begin = run.start(blockIdx.x), end = run.start(blockIdx.x + 1);
     if (begin == end) return true;
     const bool f16 = args.f16 != 0;
@@ -282,7 +299,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             const Product &p = args.p[ph];
-            const Runs run(p.tiles, p.kbs, p.ctas);
+            const Runs run(p);
             const int64_t begin = run.start(blockIdx.x);
             const int count = (int)(run.start(blockIdx.x + 1) - begin);
             int tile = (int)(begin / p.kbs), kb = (int)(begin - (int64_t)tile * p.kbs);
@@ -362,7 +379,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             const Product &p = args.p[ph];
-            const Runs run(p.tiles, p.kbs, p.ctas);
+            const Runs run(p);
             const int64_t begin = run.start(blockIdx.x);
             const int count = (int)(run.start(blockIdx.x + 1) - begin);
             int kb = (int)(begin % p.kbs);

@@ -94,6 +94,7 @@ _SIGS = {
     "moe_dropout": (_I, [_P, _L, _P, _L, _L, _I, _D, _U, _U, _P, _I, _P, _L, _P]),
     "moe_dropout_backward": (_I, [_P, _L, _L, _I, _D, _U, _U, _P, _I, _P, _L, _P]),
     "moe_ffn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_ffn_saved_floats": (_SZ, [_I, _I]),
     "moe_ffn_workspace_init": (_I, [_P, _SZ, _P]),
     "moe_ffn_forward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "moe_ffn_forward_train": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ,
@@ -769,14 +770,16 @@ def moe_ffn(x, W1, W3, W2, act: str = "silu", ws=None, Y=None, stream=None):
 
 
 def moe_ffn_train(x, W1, W3, W2, act: str = "silu", ws=None, stream=None):
-    """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3 fp32). ws:
+    """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3: fp32 in the
+    blocks that moe.h describes). ws:
     ffn_workspace(..., train=True)."""
     T, d, n = _ffn_shape(x, W1, W3, W2, act)
     if ws is None:
         ws = ffn_workspace(T, d, n, train=True, device=x.device, stream=stream)
     Y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     H = torch.empty((T, n), dtype=x.dtype, device=x.device)
-    A1, A3 = (torch.empty((T, n), dtype=torch.float32, device=x.device) for _ in range(2))
+    size = lib().moe_ffn_saved_floats(T, n)
+    A1, A3 = (torch.empty(size, dtype=torch.float32, device=x.device) for _ in range(2))
     st = lib().moe_ffn_forward_train(
         x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), T, d, n, ACTS[act],
         _DTYPES[x.dtype], Y.data_ptr(), H.data_ptr(), A1.data_ptr(), A3.data_ptr(), ws.data_ptr(),
@@ -793,8 +796,9 @@ def moe_ffn_backward(dY, x, W1, W3, W2, H, A1, A3, act: str = "silu", need_dx: b
     T, d, n = _ffn_shape(x, W1, W3, W2, act)
     _dense(dY, x.shape, x.dtype, "dY")
     _dense(H, (T, n), x.dtype, "H")
-    _dense(A1, (T, n), torch.float32, "A1")
-    _dense(A3, (T, n), torch.float32, "A3")
+    size = lib().moe_ffn_saved_floats(T, n)
+    _dense(A1, (size,), torch.float32, "A1")
+    _dense(A3, (size,), torch.float32, "A3")
     if ws is None:
         ws = ffn_workspace(T, d, n, train=True, device=x.device, stream=stream)
     dX = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
