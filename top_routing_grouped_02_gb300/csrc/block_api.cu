@@ -77,9 +77,9 @@ FfnWs ffn_ws(int T, int d, int n, bool train) {
     w.h = w.da1 = align256(kFfnControlBytes);
     w.da3 = w.da1 + act;
     w.part = train ? w.da3 + act : w.h + act;
-    const bool tiled = train || T > kFfnStreamTokens;
+    const bool tiled = train || !ffn_streams(T, d, n);
     w.total = w.part + (tiled ? align256(ffn_dense_part_bytes()) : 0);
-    // a workspace for T tokens serves fewer on the weight-streaming kernel
+    // a workspace for T tokens serves fewer, whichever kernel they take
     const int few = std::min(T, kFfnStreamTokens);
     w.total = std::max(w.total, w.h + align256((size_t)few * n * 2) +
                                     align256(ffn_stream_part_bytes(few, d, n)));
@@ -209,7 +209,7 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
     float4 *part = reinterpret_cast<float4 *>(at(ws, w.part));
     const bool f16 = type == MOE_DTYPE_F16;
     cudaStream_t s = as_stream(stream);
-    if (T <= kFfnStreamTokens)
+    if (ffn_streams(T, d, n))
         return from_cuda(launch_ffn_stream(X, W1, W3, W2, T, d, n, act, f16, at(ws, w.h), Y,
                                            reinterpret_cast<float *>(part), ticket, err, s));
     cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, at(ws, w.h), nullptr, nullptr, part,

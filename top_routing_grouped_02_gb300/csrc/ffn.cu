@@ -195,6 +195,14 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
         ptx::fence_barrier_init();
     }
+    if (warp == 3 && lane < 9) {  // the descriptors of this mode's tensors
+        constexpr int nA = MODE == kWGrad ? 3 : MODE == kDX ? 2 : 1;
+        constexpr int nB = MODE == kWGrad ? 3 : MODE == kDX || MODE == kGate ? 2 : 1;
+        constexpr int nO = MODE == kWGrad ? 3 : MODE == kDHid ? 2 : 1;
+        const int k = lane % 3;
+        if (lane < 3 ? k < nA : lane < 6 ? k < nB : k < nO)
+            ptx::prefetch_tensormap(lane < 3 ? &maps.a[k] : lane < 6 ? &maps.b[k] : &maps.o[k]);
+    }
     if (warp == 2) {
         ptx::tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base), 2 * BN);
         ptx::tmem_relinquish_pair();
@@ -376,7 +384,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             const int rows = args.rows[un.p], cols = args.cols[un.p];
             const int y0 = un.row0 + q * 32;
             // kDHid: this row's A1, A3 of a chunk, loaded while the one before is stored
-            float4 x1[8], x3[8];
+            float4 x1[8] = {}, x3[8] = {};
             auto load_pre = [&](int c) {
                 const int x0 = un.nb * kCols + c * 32;
                 if (c >= hi || y0 >= rows || x0 >= cols) return;
@@ -403,7 +411,6 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     uint32_t g[32], v[32], o[16];
                     load(c, own, g);
                     load(BN / 64 + c, NC + own, v);
-                    if (!in) continue;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float h[2];
@@ -414,8 +421,8 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         }
                         o[i] = pack(h[0], h[1], f16);
                     }
-                    store_box(o, x0, y0, &maps.o[0]);
-                    if (args.a1 != nullptr) {
+                    if (in) store_box(o, x0, y0, &maps.o[0]);
+                    if (in && args.a1 != nullptr) {
                         float4 *p1 = pre_block(args.a1, cols, y0, x0, lane);
                         float4 *p3 = pre_block(args.a3, cols, y0, x0, lane);
 #pragma unroll
@@ -429,7 +436,6 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 } else if constexpr (MODE == kDHid) {
                     uint32_t g[32], o1[16], o3[16];
                     load(c, own, g);
-                    if (!in) continue;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float r1[2], r3[2];
@@ -446,25 +452,24 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         o3[i] = pack(r3[0], r3[1], f16);
                     }
                     load_pre(c + 1);
-                    store_box(o1, x0, y0, &maps.o[0]);
-                    store_box(o3, x0, y0, &maps.o[1]);
+                    if (in) {
+                        store_box(o1, x0, y0, &maps.o[0]);
+                        store_box(o3, x0, y0, &maps.o[1]);
+                    }
                 } else {
                     uint32_t v[32], o[16];
                     load(c, own, v);
-                    if (!in) continue;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         o[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
-                    store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
+                    if (in) store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
                 }
             }
             return true;
         };
 
-        // The pair's segment, its join, then the whole tiles; finish() stands in one place
-        // only, since its code comes cold from memory.
+        // the pair's segment and its join, then the whole tiles
         Work w(args, pair, pairs);
-        bool joining = false;
         const int j = args.split > 0 ? pair % args.split : 0;
         const int lo = args.split > 0 ? NC * j / args.split : 0;
         const int hi = args.split > 0 ? NC * (j + 1) / args.split : 0;  // its share of a cut tile
@@ -477,7 +482,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 ptx::tc_fence_after();
                 return true;
             };
-            joining = w.cut;
+            const bool joining = w.cut;
             if (joining) {
                 if (!filled()) break;
                 float4 *p = part_of(pair);

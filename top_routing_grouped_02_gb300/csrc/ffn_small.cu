@@ -3,7 +3,7 @@
 // The weights are streamed once and nothing else is large, so HBM bounds it.
 //
 // The tensor cores take the weights as the 128-row operand: a tile is 128 columns
-// of W (TMA boxes of 64 columns x 64 rows, MN-major) against NT tokens (16 .. 128,
+// of W (TMA boxes of 64 columns x 64 rows, MN-major) against NT tokens (16 .. 64,
 // padded with zeros by TMA), so the accumulator holds the transposed output, one
 // weight column per TMEM lane and one token per TMEM column, and one token costs
 // no more MMA time than its share of the weight traffic.
@@ -463,7 +463,7 @@ cudaError_t launch_nt(const SmallMaps &maps, SmallArgs args, int grid, cudaStrea
     return launch_k(stream_ffn_kernel<NT>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
 }
 
-int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 // A product whose units are 32 KB of weights, on one CTA per SM, fewer where a run
 // would be under two units (then the joining costs more than the shorter runs save).
@@ -514,8 +514,7 @@ cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, con
     switch (nt) {
         case 16: return launch_nt<16>(m, a, grid, s);
         case 32: return launch_nt<32>(m, a, grid, s);
-        case 64: return launch_nt<64>(m, a, grid, s);
-        default: return launch_nt<128>(m, a, grid, s);
+        default: return launch_nt<64>(m, a, grid, s);
     }
 }
 

@@ -24,7 +24,7 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
           6: "MOE_ERR_DEVICE_TIMEOUT", 7: "MOE_ERR_DEVICE_CHECK"}
 # Kernels each call enqueues; the gate/up GEMM launches one more (a row gather)
 # when it runs on CTA pairs, the router's backward one fewer when T is too
-# short to split into chunks, moe_ffn one for up to 128 tokens, moe_permute one kernel instead of three for
+# short to split into chunks, moe_ffn one for few tokens, moe_permute one kernel instead of three for
 # T <= 65536, and the whole-layer calls depend on the shape
 # (forward_launches).
 LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_gate_up": 1,
