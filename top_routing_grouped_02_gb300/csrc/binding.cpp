@@ -1,0 +1,362 @@
+// Python entry points of the sub-block calls (layer norm, residual dropout, dense
+// feed-forward block): argument checks, output allocation and one call into
+// libmoe.so each. They do what the ctypes functions of moe.py do for the other calls;
+// these run at sizes where a call's host time is several times its GPU time, and from
+// Python it was (12 us of host time for a 2 us kernel).
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "moe.h"
+
+namespace {
+
+PyObject *g_error = nullptr;  // moe.MoeError
+
+struct Refused {};  // a Python exception is set
+
+[[noreturn]] void refuse(PyObject *type, const char *format, const char *name) {
+    PyErr_Format(type, format, name);
+    throw Refused();
+}
+
+at::Tensor tensor(PyObject *o, const char *name) {
+    if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a tensor", name);
+    return THPVariable_Unpack(o);
+}
+at::Tensor optional_tensor(PyObject *o, const char *name) {
+    return o == Py_None ? at::Tensor() : tensor(o, name);
+}
+double number(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+long integer(PyObject *o) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+uint64_t word(PyObject *o) {
+    const uint64_t v = PyLong_AsUnsignedLongLongMask(o);
+    if (v == (uint64_t)-1 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+
+int type_of(const at::Tensor &t) {
+    switch (t.scalar_type()) {
+        case at::kBFloat16: return MOE_DTYPE_BF16;
+        case at::kHalf: return MOE_DTYPE_F16;
+        case at::kFloat: return MOE_DTYPE_F32;
+        default: return -1;
+    }
+}
+
+void *stream_of(PyObject *o, const at::Tensor &t) {
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+    PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
+    if (v == nullptr) throw Refused();
+    const uint64_t s = PyLong_AsUnsignedLongLongMask(v);
+    Py_DECREF(v);
+    if (PyErr_Occurred()) throw Refused();
+    return reinterpret_cast<void *>(s);
+}
+
+// A tensor seen as a matrix of rows along its last dimension: contiguous, or 2-D with
+// unit inner stride.
+struct Rows {
+    void *p;
+    int64_t ld, T, d;
+};
+Rows rows_of(const at::Tensor &t, const char *name, const at::Tensor *like = nullptr) {
+    if (!t.is_cuda() || type_of(t) < 0 || t.dim() < 1)
+        refuse(PyExc_ValueError, "%s must be a bf16, fp16 or fp32 CUDA tensor", name);
+    if (like != nullptr && (t.sizes() != like->sizes() || t.scalar_type() != like->scalar_type() ||
+                            t.get_device() != like->get_device()))
+        refuse(PyExc_ValueError, "%s must have the first tensor's shape, type and device", name);
+    Rows r;
+    r.p = t.data_ptr();
+    r.d = t.size(-1);
+    if (r.d == 0 || r.d > INT32_MAX) refuse(PyExc_ValueError, "%s has rows of an unsupported length", name);
+    if (t.is_contiguous()) {
+        r.ld = r.d;
+        r.T = t.numel() / r.d;
+        return r;
+    }
+    if (t.dim() != 2 || (r.d > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) < r.d))
+        refuse(PyExc_ValueError, "%s must be contiguous or a matrix of non-overlapping rows", name);
+    r.ld = t.stride(0);
+    r.T = t.size(0);
+    return r;
+}
+// An output: `o`, or a new contiguous tensor like x.
+at::Tensor output(PyObject *o, const at::Tensor &x, const char *name) {
+    return o == Py_None ? at::empty(x.sizes(), x.options()) : tensor(o, name);
+}
+void *vec_of(const at::Tensor &t, int64_t d, const at::Tensor &x, const char *name) {
+    if (!t.defined()) return nullptr;
+    if (!t.is_cuda() || t.dim() != 1 || t.size(0) != d || !t.is_contiguous())
+        refuse(PyExc_ValueError, "%s must be a contiguous CUDA vector of the rows' length", name);
+    if (t.scalar_type() != x.scalar_type() && t.scalar_type() != at::kFloat)
+        refuse(PyExc_TypeError, "%s must have the rows' type or be fp32", name);
+    return t.data_ptr();
+}
+float *stat_of(const at::Tensor &t, int64_t T, const char *name) {
+    if (!t.is_cuda() || t.scalar_type() != at::kFloat || !t.is_contiguous() || t.numel() != T)
+        refuse(PyExc_ValueError, "%s must hold one contiguous fp32 value a row", name);
+    return static_cast<float *>(t.data_ptr());
+}
+const uint64_t *counter_of(const at::Tensor &t) {
+    if (!t.defined()) return nullptr;
+    if (!t.is_cuda() || t.scalar_type() != at::kLong || t.numel() != 1)
+        refuse(PyExc_ValueError, "%s must be a one-element int64 CUDA tensor", "offset_dev");
+    return static_cast<const uint64_t *>(t.data_ptr());
+}
+void *dense(const at::Tensor &t, at::IntArrayRef sizes, at::ScalarType type, const char *name) {
+    if (!t.is_cuda() || !t.is_contiguous() || t.scalar_type() != type || t.sizes() != sizes)
+        refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor of the call's shape and type", name);
+    return t.data_ptr();
+}
+moe_dtype_t dtype(const at::Tensor &t) { return static_cast<moe_dtype_t>(type_of(t)); }
+
+void check(const char *fn, moe_status_t status) {
+    if (status == MOE_OK) return;
+    PyObject *e = PyObject_CallFunction(g_error, "si", fn, (int)status);
+    if (e != nullptr) {
+        PyErr_SetObject(g_error, e);
+        Py_DECREF(e);
+    }
+    throw Refused();
+}
+
+void expect(Py_ssize_t n, Py_ssize_t want) {
+    if (n == want) return;
+    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    throw Refused();
+}
+PyObject *wrap(const at::Tensor &t) {
+    if (!t.defined()) Py_RETURN_NONE;
+    return THPVariable_Wrap(t);
+}
+template <typename... Ts>
+PyObject *wrap_all(const Ts &...ts) {
+    PyObject *items[] = {wrap(ts)...};
+    PyObject *tuple = PyTuple_New(sizeof...(ts));
+    for (size_t i = 0; i < sizeof...(ts); ++i) PyTuple_SET_ITEM(tuple, i, items[i]);
+    return tuple;
+}
+
+// x, gamma, beta, eps, stats, y, stream
+PyObject *layernorm(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 7);
+    const at::Tensor x = tensor(a[0], "x");
+    const at::Tensor gamma = optional_tensor(a[1], "gamma"), beta = optional_tensor(a[2], "beta");
+    const Rows rx = rows_of(x, "x");
+    const double eps = number(a[3]);
+    const bool stats = PyObject_IsTrue(a[4]) == 1;
+    void *pg = vec_of(gamma, rx.d, x, "gamma"), *pb = vec_of(beta, rx.d, x, "beta");
+    if (pg != nullptr && pb != nullptr && gamma.scalar_type() != beta.scalar_type())
+        refuse(PyExc_TypeError, "gamma and %s must have one type", "beta");
+    const at::Tensor y = output(a[5], x, "y");
+    const Rows ry = rows_of(y, "y", &x);
+    at::Tensor mean, rstd;
+    if (stats) {
+        const auto sizes = x.sizes().slice(0, x.dim() - 1);
+        mean = at::empty(sizes, x.options().dtype(at::kFloat));
+        rstd = at::empty(sizes, x.options().dtype(at::kFloat));
+    }
+    check("moe_layernorm_forward",
+          moe_layernorm_forward(rx.p, rx.ld, pg, pb, rx.T, (int)rx.d, (float)eps, dtype(x),
+                                dtype(pg != nullptr ? gamma : pb != nullptr ? beta : x), ry.p, ry.ld,
+                                stats ? static_cast<float *>(mean.data_ptr()) : nullptr,
+                                stats ? static_cast<float *>(rstd.data_ptr()) : nullptr,
+                                stream_of(a[6], x)));
+    return stats ? wrap_all(y, mean, rstd) : wrap(y);
+}
+
+// dy, x, gamma, mean, rstd, dres, fp32 weight gradients without gamma, dx, scratch, stream
+PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 10);
+    const at::Tensor dy = tensor(a[0], "dy"), x = tensor(a[1], "x");
+    const at::Tensor gamma = optional_tensor(a[2], "gamma"), mean = tensor(a[3], "mean"),
+                     rstd = tensor(a[4], "rstd"), dres = optional_tensor(a[5], "dres");
+    const Rows rx = rows_of(x, "x"), rdy = rows_of(dy, "dy", &x);
+    Rows rr{};
+    if (dres.defined()) rr = rows_of(dres, "dres", &x);
+    void *pg = vec_of(gamma, rx.d, x, "gamma");
+    float *pm = stat_of(mean, rx.T, "mean"), *pr = stat_of(rstd, rx.T, "rstd");
+    const at::Tensor dx = output(a[7], x, "dx");
+    const Rows rdx = rows_of(dx, "dx", &x);
+    const at::ScalarType wt = gamma.defined()               ? gamma.scalar_type()
+                              : PyObject_IsTrue(a[6]) == 1 ? at::kFloat
+                                                            : x.scalar_type();
+    const at::Tensor dgamma = at::empty({rx.d}, x.options().dtype(wt));
+    const at::Tensor dbeta = at::empty({rx.d}, x.options().dtype(wt));
+    const at::Tensor scratch =
+        a[8] != Py_None ? tensor(a[8], "scratch")
+                        : at::empty({(int64_t)moe_layernorm_scratch_bytes(rx.T, (int)rx.d)},
+                                    x.options().dtype(at::kByte));
+    if (!scratch.is_cuda() || !scratch.is_contiguous())
+        refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor", "scratch");
+    check("moe_layernorm_backward",
+          moe_layernorm_backward(rdy.p, rdy.ld, rx.p, rx.ld, pg, pm, pr, rr.p, rr.ld, rx.T, (int)rx.d,
+                                 dtype(x), dtype(dgamma), rdx.p, rdx.ld, dgamma.data_ptr(),
+                                 dbeta.data_ptr(), scratch.data_ptr(), scratch.nbytes(),
+                                 stream_of(a[9], x)));
+    return wrap_all(dx, dgamma, dbeta);
+}
+
+// x, p, seed, offset, residual, offset_dev, y, stream
+PyObject *dropout(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 8);
+    const at::Tensor x = tensor(a[0], "x"), res = optional_tensor(a[4], "residual"),
+                     ctr = optional_tensor(a[5], "offset_dev");
+    const Rows rx = rows_of(x, "x");
+    const double p = number(a[1]);
+    const uint64_t seed = word(a[2]), offset = word(a[3]);
+    Rows rr{};
+    if (res.defined()) rr = rows_of(res, "residual", &x);
+    const uint64_t *pc = counter_of(ctr);
+    const at::Tensor y = output(a[6], x, "y");
+    const Rows ry = rows_of(y, "y", &x);
+    check("moe_dropout", moe_dropout(rx.p, rx.ld, rr.p, rr.ld, rx.T, (int)rx.d, p, seed, offset, pc,
+                                     dtype(x), ry.p, ry.ld, stream_of(a[7], x)));
+    return wrap(y);
+}
+
+// dy, p, seed, offset, offset_dev, dx, stream
+PyObject *dropout_backward(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 7);
+    const at::Tensor dy = tensor(a[0], "dy"), ctr = optional_tensor(a[4], "offset_dev");
+    const Rows r = rows_of(dy, "dy");
+    const double p = number(a[1]);
+    const uint64_t seed = word(a[2]), offset = word(a[3]);
+    const uint64_t *pc = counter_of(ctr);
+    const at::Tensor dx = output(a[5], dy, "dx");
+    const Rows rdx = rows_of(dx, "dx", &dy);
+    check("moe_dropout_backward",
+          moe_dropout_backward(r.p, r.ld, r.T, (int)r.d, p, seed, offset, pc, dtype(dy), rdx.p, rdx.ld,
+                               stream_of(a[6], dy)));
+    return wrap(dx);
+}
+
+// The feed-forward block's operands.
+struct Ffn {
+    at::Tensor x, W1, W3, W2, ws;
+    int T, d, n;
+    void *px, *p1, *p3, *p2, *pws;
+    at::ScalarType type;
+};
+Ffn ffn_args(PyObject *x, PyObject *W1, PyObject *W3, PyObject *W2, PyObject *ws) {
+    Ffn f{tensor(x, "x"), tensor(W1, "W1"), tensor(W3, "W3"), tensor(W2, "W2"), tensor(ws, "ws")};
+    if (f.x.dim() < 1 || f.W1.dim() != 2 || f.x.size(-1) != f.W1.size(0))
+        refuse(PyExc_ValueError, "%s must be [..., d] and W1 [d, n]", "x");
+    f.type = f.x.scalar_type();
+    if (f.type != at::kBFloat16 && f.type != at::kHalf)
+        refuse(PyExc_TypeError, "the feed-forward block takes bf16 or fp16 %s", "x");
+    const int64_t d = f.W1.size(0), n = f.W1.size(1), T = d > 0 ? f.x.numel() / d : 0;
+    if (T > INT32_MAX || d > INT32_MAX || n > INT32_MAX)
+        refuse(PyExc_ValueError, "%s is too large", "x");
+    f.px = dense(f.x, f.x.sizes(), f.type, "x");
+    f.p1 = dense(f.W1, {d, n}, f.type, "W1");
+    f.p3 = dense(f.W3, {d, n}, f.type, "W3");
+    f.p2 = dense(f.W2, {n, d}, f.type, "W2");
+    if (!f.ws.is_cuda() || !f.ws.is_contiguous())
+        refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor", "ws");
+    f.pws = f.ws.data_ptr();
+    f.T = (int)T;
+    f.d = (int)d;
+    f.n = (int)n;
+    return f;
+}
+
+// x, W1, W3, W2, act, ws, Y, stream
+PyObject *ffn(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 8);
+    const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5]);
+    const at::Tensor Y = output(a[6], f.x, "Y");
+    void *py = dense(Y, f.x.sizes(), f.type, "Y");
+    check("moe_ffn_forward",
+          moe_ffn_forward(f.px, f.p1, f.p3, f.p2, f.T, f.d, f.n, (moe_act_t)integer(a[4]), dtype(f.x), py,
+                          f.pws, f.ws.nbytes(), stream_of(a[7], f.x)));
+    return wrap(Y);
+}
+
+// x, W1, W3, W2, act, ws, stream
+PyObject *ffn_train(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 7);
+    const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5]);
+    const at::Tensor Y = at::empty(f.x.sizes(), f.x.options());
+    const at::Tensor H = at::empty({f.T, f.n}, f.x.options());
+    const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
+    const at::Tensor A1 = at::empty({saved}, f.x.options().dtype(at::kFloat));
+    const at::Tensor A3 = at::empty({saved}, f.x.options().dtype(at::kFloat));
+    check("moe_ffn_forward_train",
+          moe_ffn_forward_train(f.px, f.p1, f.p3, f.p2, f.T, f.d, f.n, (moe_act_t)integer(a[4]),
+                                dtype(f.x), Y.data_ptr(), H.data_ptr(),
+                                static_cast<float *>(A1.data_ptr()), static_cast<float *>(A3.data_ptr()),
+                                f.pws, f.ws.nbytes(), stream_of(a[6], f.x)));
+    return wrap_all(Y, H, A1, A3);
+}
+
+// dY, x, W1, W3, W2, H, A1, A3, act, need_dx, need_dw, ws, stream
+PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 13);
+    const Ffn f = ffn_args(a[1], a[2], a[3], a[4], a[11]);
+    const at::Tensor dY = tensor(a[0], "dY"), H = tensor(a[5], "H"), A1 = tensor(a[6], "A1"),
+                     A3 = tensor(a[7], "A3");
+    const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
+    void *pdy = dense(dY, f.x.sizes(), f.type, "dY"), *ph = dense(H, {f.T, f.n}, f.type, "H");
+    const float *pa1 = static_cast<float *>(dense(A1, {saved}, at::kFloat, "A1"));
+    const float *pa3 = static_cast<float *>(dense(A3, {saved}, at::kFloat, "A3"));
+    at::Tensor dX, dW1, dW3, dW2;
+    if (PyObject_IsTrue(a[9]) == 1) dX = at::empty(f.x.sizes(), f.x.options());
+    const bool dw = PyObject_IsTrue(a[10]) == 1;
+    if (dw) {
+        dW1 = at::empty({f.d, f.n}, f.x.options());
+        dW3 = at::empty({f.d, f.n}, f.x.options());
+        dW2 = at::empty({f.n, f.d}, f.x.options());
+    }
+    check("moe_ffn_backward",
+          moe_ffn_backward(pdy, f.px, f.p1, f.p3, f.p2, ph, pa1, pa3, f.T, f.d, f.n,
+                           (moe_act_t)integer(a[8]), dtype(f.x), dX.defined() ? dX.data_ptr() : nullptr,
+                           dw ? dW1.data_ptr() : nullptr, dw ? dW3.data_ptr() : nullptr,
+                           dw ? dW2.data_ptr() : nullptr, f.pws, f.ws.nbytes(), stream_of(a[12], f.x)));
+    return wrap_all(dX, dW1, dW3, dW2);
+}
+
+// error class
+PyObject *set_error(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 1);
+    Py_INCREF(a[0]);
+    Py_XSETREF(g_error, a[0]);
+    Py_RETURN_NONE;
+}
+
+// No C++ exception leaves an entry point: refusals have set theirs, torch's are
+// translated.
+template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
+PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    try {
+        return F(args, n);
+    } catch (const Refused &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+#define MOE_ENTRY(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F>)), METH_FASTCALL, nullptr}
+PyMethodDef g_methods[] = {MOE_ENTRY(layernorm), MOE_ENTRY(layernorm_backward), MOE_ENTRY(dropout),
+                           MOE_ENTRY(dropout_backward), MOE_ENTRY(ffn), MOE_ENTRY(ffn_train),
+                           MOE_ENTRY(ffn_backward), MOE_ENTRY(set_error),
+                           {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods,
+                        nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__native() { return PyModule_Create(&g_module); }

@@ -1,7 +1,7 @@
 """Thin ctypes binding over libmoe.so (include/moe.h).
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
-kernels. Tensors must be contiguous CUDA tensors of the dtype each call names;
+kernels. (The sub-block calls at the end of the file marshal in _native.so.) Tensors must be contiguous CUDA tensors of the dtype each call names;
 their ``data_ptr()`` and the current torch stream are passed straight through.
 There is no fallback: if libmoe.so is missing or a call fails, a ``MoeError``
 is raised.
@@ -578,51 +578,22 @@ def moe_forward_rounded(X, Wr, W1, W3, W2, K: int, bias=None, renorm: bool = Tru
 
 # ------------------------------------- layer norm, residual dropout, dense block
 
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_nat = None
 
 
-def _raw_stream(stream, device) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream
-
-
-def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
-    """(pointer, row stride, rows, row length) of a CUDA tensor seen as a matrix of
-    rows along its last dimension: contiguous, or 2-D with unit inner stride."""
-    if not t.is_cuda or t.dtype not in _DTYPES or not t.dim():
-        raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor")
-    shape = t.shape
-    if like is not None and (shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name} must have shape {tuple(like.shape)} and type {like.dtype}")
-    d = shape[-1]
-    if d == 0:
-        raise ValueError(f"{name} has rows of length 0")
-    if t.is_contiguous():
-        return t.data_ptr(), d, t.numel() // d, d
-    if t.dim() != 2 or (d > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < d):
-        raise ValueError(f"{name} must be contiguous or a matrix of non-overlapping rows")
-    return t.data_ptr(), t.stride(0), shape[0], d
-
-
-def _out(t, like, d, name):
-    """(tensor, pointer, row stride) of an output: `t`, or a new contiguous tensor."""
-    if t is None:
-        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-        return t, t.data_ptr(), d
-    ptr, ld, _, _ = _rows(t, name, like)
-    return t, ptr, ld
-
-
-def _vec(t: torch.Tensor | None, d: int, dtype, name: str):
-    """Pointer of a contiguous vector of d elements of x's dtype or fp32."""
-    if t is None:
-        return None
-    if not t.is_cuda or t.dim() != 1 or t.shape[0] != d or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA vector of {d}")
-    if t.dtype != dtype and t.dtype != torch.float32:
-        raise TypeError(f"{name} must be {dtype} or fp32, got {t.dtype}")
-    return t.data_ptr()
+def _native():
+    """The compiled entry points of the calls below (csrc/binding.cpp): checks,
+    allocation of outputs and the library call."""
+    global _nat
+    if _nat is None:
+        lib()
+        try:
+            from . import _native as nat
+        except ImportError as e:
+            raise RuntimeError("_native.so not built; run __graft_entry__.build()") from e
+        nat.set_error(MoeError)
+        _nat = nat
+    return _nat
 
 
 def moe_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False, y=None,
@@ -630,25 +601,7 @@ def moe_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = Fal
     """y = layer norm of x along its last dimension (gamma, beta: [d] of x's type or
     fp32, or None); stats=True: (y, mean, rstd), the fp32 row statistics that the
     backward takes."""
-    px, ldx, T, d = _rows(x, "x")
-    dtype, device = x.dtype, x.device
-    pg, pb = _vec(gamma, d, dtype, "gamma"), _vec(beta, d, dtype, "beta")
-    w = gamma if gamma is not None else beta
-    if pg is not None and pb is not None and gamma.dtype != beta.dtype:
-        raise TypeError("gamma and beta must have one type")
-    y, py, ldy = _out(y, x, d, "y")
-    mean = rstd = pm = pr = None
-    if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        pm, pr = mean.data_ptr(), rstd.data_ptr()
-    ty = _DTYPES[dtype]
-    st = lib().moe_layernorm_forward(px, ldx, pg, pb, T, d, eps, ty,
-                                     ty if w is None else _DTYPES[w.dtype], py, ldy, pm, pr,
-                                     _raw_stream(stream, device))
-    if st != MOE_OK:
-        raise MoeError("moe_layernorm_forward", st)
-    return (y, mean, rstd) if stats else y
+    return _native().layernorm(x, gamma, beta, eps, stats, y, stream)
 
 
 def moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=None, wdtype=None, dx=None, scratch=None,
@@ -656,63 +609,23 @@ def moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=None, wdtype=None, dx=
     """(dx, dgamma, dbeta) of moe_layernorm, with `dres` (the gradient that reaches
     x by the residual branch) added to dx when given. dgamma and dbeta have gamma's
     type, or wdtype (default fp32) without gamma."""
-    px, ldx, T, d = _rows(x, "x")
-    pdy, lddy, _, _ = _rows(dy, "dy", x)
-    pres, ldres = (None, 0) if dres is None else _rows(dres, "dres", x)[:2]
-    dx, pdx, lddx = _out(dx, x, d, "dx")
-    wt = gamma.dtype if gamma is not None else wdtype or torch.float32
-    if wt not in (x.dtype, torch.float32):
-        raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wt}")
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != T:
-            raise ValueError(f"{name} must hold {T} contiguous fp32 values")
-    grads = torch.empty((2, d), dtype=wt, device=x.device)
-    if scratch is None:
-        scratch = torch.empty(lib().moe_layernorm_scratch_bytes(T, d), dtype=torch.uint8,
-                              device=x.device)
-    st = lib().moe_layernorm_backward(
-        pdy, lddy, px, ldx, _vec(gamma, d, x.dtype, "gamma"), mean.data_ptr(),
-        rstd.data_ptr(), pres, ldres, T, d, _DTYPES[x.dtype], _DTYPES[wt], pdx, lddx,
-        grads.data_ptr(), grads.data_ptr() + d * grads.element_size(), scratch.data_ptr(),
-        scratch.numel(), _raw_stream(stream, x.device))
-    if st != MOE_OK:
-        raise MoeError("moe_layernorm_backward", st)
-    dgamma, dbeta = grads.unbind(0)
-    return dx, dgamma, dbeta
+    if gamma is None and wdtype not in (None, torch.float32, x.dtype):
+        raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wdtype}")
+    return _native().layernorm_backward(dy, x, gamma, mean, rstd, dres, wdtype is not x.dtype, dx,
+                                        scratch, stream)
 
 
 def moe_dropout(x, p: float, seed: int, offset: int = 0, residual=None, offset_dev=None, y=None,
                 stream=None):
     """residual + dropout(x): the mask is a function of (seed, offset, element), see
     moe.h; offset_dev: a one-element int64 CUDA tensor added to offset."""
-    px, ldx, T, d = _rows(x, "x")
-    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", x)[:2]
-    y, py, ldy = _out(y, x, d, "y")
-    st = lib().moe_dropout(px, ldx, pr, ldr, T, d, p, seed, offset, _counter(offset_dev),
-                           _DTYPES[x.dtype], py, ldy, _raw_stream(stream, x.device))
-    if st != MOE_OK:
-        raise MoeError("moe_dropout", st)
-    return y
+    return _native().dropout(x, p, seed, offset, residual, offset_dev, y, stream)
 
 
 def moe_dropout_backward(dy, p: float, seed: int, offset: int = 0, offset_dev=None, dx=None,
                          stream=None):
     """The gradient of moe_dropout with respect to x (the residual's is dy)."""
-    pdy, lddy, T, d = _rows(dy, "dy")
-    dx, pdx, lddx = _out(dx, dy, d, "dx")
-    st = lib().moe_dropout_backward(pdy, lddy, T, d, p, seed, offset, _counter(offset_dev),
-                                    _DTYPES[dy.dtype], pdx, lddx, _raw_stream(stream, dy.device))
-    if st != MOE_OK:
-        raise MoeError("moe_dropout_backward", st)
-    return dx
-
-
-def _counter(t):
-    if t is None:
-        return None
-    if not t.is_cuda or t.dtype != torch.int64 or t.numel() != 1:
-        raise ValueError("offset_dev must be a one-element int64 CUDA tensor")
-    return t.data_ptr()
+    return _native().dropout_backward(dy, p, seed, offset, offset_dev, dx, stream)
 
 
 ACTS = {"silu": 0, "gelu": 1}
@@ -724,94 +637,44 @@ def ffn_workspace(T: int, d: int, n: int, train: bool = False, device=None, stre
     nbytes = int(lib().moe_ffn_workspace_bytes(T, d, n, int(train)))
     if nbytes == 0:
         raise ValueError("invalid feed-forward shape")
+    if device is not None and torch.device(device).type != "cuda":
+        raise ValueError("the workspace lies on a CUDA device")
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
     _check("moe_ffn_workspace_init", lib().moe_ffn_workspace_init(
-        ws.data_ptr(), nbytes, _raw_stream(stream, ws.device)))
+        ws.data_ptr(), nbytes, _stream(stream)))
     return ws
 
 
-def _ffn_shape(x, W1, W3, W2, act):
-    if x.dim() < 1 or W1.dim() != 2 or x.shape[-1] != W1.shape[0]:
-        raise ValueError("x must be [..., d] and W1 [d, n]")
-    d, n = W1.shape
+def _act(act: str) -> int:
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"the feed-forward block takes bf16 or fp16, got {x.dtype}")
-    T = x.numel() // d if d else 0
-    _dense(x, x.shape, x.dtype, "x")
-    _dense(W1, (d, n), x.dtype, "W1")
-    _dense(W3, (d, n), x.dtype, "W3")
-    _dense(W2, (n, d), x.dtype, "W2")
-    return T, d, n
+    return ACTS[act]
 
 
-def _dense(t, shape, dtype, name):
-    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor {tuple(shape)} of {dtype}")
-    return t.data_ptr()
+def _ffn_ws(ws, x, W1, train, stream):
+    if ws is not None:
+        return ws
+    if not x.is_cuda or x.dim() < 1 or W1.dim() != 2 or W1.numel() == 0:
+        raise ValueError("x must be a CUDA tensor [..., d] and W1 [d, n]")
+    d, n = W1.shape
+    return ffn_workspace(x.numel() // d, d, n, train, x.device, stream)
 
 
 def moe_ffn(x, W1, W3, W2, act: str = "silu", ws=None, Y=None, stream=None):
     """Y = (act(x W1) * (x W3)) W2 of x [..., d] (bf16 or fp16); act "silu" or "gelu"
     (the tanh form). ws: ffn_workspace, kept between calls."""
-    T, d, n = _ffn_shape(x, W1, W3, W2, act)
-    if ws is None:
-        ws = ffn_workspace(T, d, n, device=x.device, stream=stream)
-    if Y is None:
-        Y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    st = lib().moe_ffn_forward(
-        x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), T, d, n, ACTS[act],
-        _DTYPES[x.dtype], _dense(Y, x.shape, x.dtype, "Y"), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, x.device))
-    if st != MOE_OK:
-        raise MoeError("moe_ffn_forward", st)
-    return Y
+    return _native().ffn(x, W1, W3, W2, _act(act), _ffn_ws(ws, x, W1, False, stream), Y, stream)
 
 
 def moe_ffn_train(x, W1, W3, W2, act: str = "silu", ws=None, stream=None):
     """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3: fp32 in the
-    blocks that moe.h describes). ws:
-    ffn_workspace(..., train=True)."""
-    T, d, n = _ffn_shape(x, W1, W3, W2, act)
-    if ws is None:
-        ws = ffn_workspace(T, d, n, train=True, device=x.device, stream=stream)
-    Y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    H = torch.empty((T, n), dtype=x.dtype, device=x.device)
-    size = lib().moe_ffn_saved_floats(T, n)
-    A1, A3 = (torch.empty(size, dtype=torch.float32, device=x.device) for _ in range(2))
-    st = lib().moe_ffn_forward_train(
-        x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), T, d, n, ACTS[act],
-        _DTYPES[x.dtype], Y.data_ptr(), H.data_ptr(), A1.data_ptr(), A3.data_ptr(), ws.data_ptr(),
-        ws.numel(), _raw_stream(stream, x.device))
-    if st != MOE_OK:
-        raise MoeError("moe_ffn_forward_train", st)
-    return Y, H, A1, A3
+    blocks that moe.h describes). ws: ffn_workspace(..., train=True)."""
+    return _native().ffn_train(x, W1, W3, W2, _act(act), _ffn_ws(ws, x, W1, True, stream), stream)
 
 
 def moe_ffn_backward(dY, x, W1, W3, W2, H, A1, A3, act: str = "silu", need_dx: bool = True,
                      need_dw: bool = True, ws=None, stream=None):
     """(dX, dW1, dW3, dW2) of moe_ffn_train, all of x's type (None where not asked
     for). ws: ffn_workspace(..., train=True)."""
-    T, d, n = _ffn_shape(x, W1, W3, W2, act)
-    _dense(dY, x.shape, x.dtype, "dY")
-    _dense(H, (T, n), x.dtype, "H")
-    size = lib().moe_ffn_saved_floats(T, n)
-    _dense(A1, (size,), torch.float32, "A1")
-    _dense(A3, (size,), torch.float32, "A3")
-    if ws is None:
-        ws = ffn_workspace(T, d, n, train=True, device=x.device, stream=stream)
-    dX = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
-    dW1 = dW3 = dW2 = None
-    if need_dw:
-        dW1, dW3 = (torch.empty((d, n), dtype=x.dtype, device=x.device) for _ in range(2))
-        dW2 = torch.empty((n, d), dtype=x.dtype, device=x.device)
-    st = lib().moe_ffn_backward(
-        dY.data_ptr(), x.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), H.data_ptr(),
-        A1.data_ptr(), A3.data_ptr(), T, d, n, ACTS[act], _DTYPES[x.dtype],
-        dX.data_ptr() if need_dx else None, dW1.data_ptr() if need_dw else None,
-        dW3.data_ptr() if need_dw else None, dW2.data_ptr() if need_dw else None, ws.data_ptr(),
-        ws.numel(), _raw_stream(stream, x.device))
-    if st != MOE_OK:
-        raise MoeError("moe_ffn_backward", st)
-    return dX, dW1, dW3, dW2
+    return _native().ffn_backward(dY, x, W1, W3, W2, H, A1, A3, _act(act), need_dx, need_dw,
+                                  _ffn_ws(ws, x, W1, True, stream), stream)
