@@ -48,11 +48,12 @@ def layernorm_backward(dy, x, gamma, eps, dres=None):
     return (dx if dres is None else dx + dres.double()), (dy * xh).sum(0), dy.sum(0)
 
 
-def keep_mask(n, p, seed, offset):
-    """[n] bool: the definition of the dropout mask, in Python integers."""
+def keep_mask(n, p, seed, offset, first=0):
+    """[n] bool: the definition of the dropout mask for elements first .. first + n - 1
+    (first a multiple of 8), in Python integers."""
     thr = math.floor(p * 65536 + 0.5)
     out = []
-    for block in range((n + 7) // 8):
+    for block in range(first // 8, first // 8 + (n + 7) // 8):
         c = [block & 0xFFFFFFFF, block >> 32, offset & 0xFFFFFFFF, offset >> 32]
         k = [seed & 0xFFFFFFFF, seed >> 32]
         for _ in range(10):

@@ -85,6 +85,16 @@ def test_statistics():
         assert abs(float((u * v).sum()) - q * q * n) < pair
 
 
+@pytest.mark.parametrize("ld", [65536, 65544, 65537])
+def test_elements_past_32_bits(ld):
+    T, d = 65600, 65536  # 4.3e9 elements
+    x = torch.ones(T, ld, dtype=BF, device="cuda")[:, :d]
+    y = moe.moe_dropout(x, 0.5, 1, 2)
+    for row in (1, T // 2 + 1, T - 1):
+        keep = keep_mask(512, 0.5, 1, 2, first=row * d)
+        assert torch.equal((y[row, :512] != 0).cpu(), keep)
+
+
 def test_in_place_streams_and_graph():
     g = torch.Generator().manual_seed(2)
     x, res = matrix(70, 520, BF, g), matrix(70, 520, BF, g)

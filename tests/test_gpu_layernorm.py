@@ -152,6 +152,30 @@ def test_in_place_and_other_stream():
     assert torch.equal(got[1], dgamma) and torch.equal(got[2], dbeta)
 
 
+@pytest.mark.parametrize("d,ld", [(300, 304), (333, 333), (2048, 2048), (8193, 8193), (12288, 12290)])
+def test_gradients_over_their_operands(d, ld):
+    # dx in the place of dy or of dres, on every kernel
+    x, gamma, beta, dy, dres = make(40, d, ld, BF, FP, 7)
+    _, mean, rstd = moe.moe_layernorm(x, gamma, beta, EPS, stats=True)
+    want = moe.moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=dres)
+    for k in (0, 1):
+        bufs = [torch.empty(40, ld, dtype=BF, device="cuda")[:, :d].copy_(t) for t in (dy, dres)]
+        got = moe.moe_layernorm_backward(bufs[0], x, gamma, mean, rstd, dres=bufs[1], dx=bufs[k])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_offsets_past_32_bits():
+    T, d = 270000, 8192  # 2.2e9 elements
+    x = torch.empty(T, d, dtype=BF, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(0))
+    gamma = torch.ones(d, device="cuda")
+    y, mean, rstd = moe.moe_layernorm(x, gamma, None, EPS, stats=True)
+    tail = slice(T - 64, T)
+    want = moe.moe_layernorm(x[tail], gamma, None, EPS, stats=True)
+    assert all(torch.equal(a[tail], b) for a, b in zip((y, mean, rstd), want))
+    dx = moe.moe_layernorm_backward(y, x, gamma, mean, rstd)[0]
+    assert torch.equal(dx[tail], moe.moe_layernorm_backward(y[tail], x[tail], gamma, mean[tail], rstd[tail])[0])
+
+
 def test_rows_of_a_higher_rank():
     x, gamma, beta, _, _ = make(24, 96, 96, FP, FP, 5)
     y, mean, _ = moe.moe_layernorm(x.view(2, 3, 4, 96), gamma, beta, EPS, stats=True)

@@ -297,6 +297,25 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A launch whose CTAs wait on one another: cooperative, so that they are resident
+// together or not launched at all, whatever else runs on the device. (It starts in
+// plain stream order: 2 us later than a programmatic dependent launch.)
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_together(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                   cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();
 // Unique id of the CUDA context current on this thread (never reused, unlike a

@@ -575,6 +575,8 @@ cudaError_t launch(const Maps &maps, Args args, cudaStream_t s) {
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(dense_gemm_kernel<MODE>), (int)kSmem);
     if (e != cudaSuccess) return e;
+    if (args.cut > 0)
+        return launch_together(dense_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
     return launch_k(dense_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
 }
 

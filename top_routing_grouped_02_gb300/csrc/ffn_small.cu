@@ -460,7 +460,7 @@ cudaError_t launch_nt(const SmallMaps &maps, SmallArgs args, int grid, cudaStrea
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(stream_ffn_kernel<NT>), (int)kSmem);
     if (e != cudaSuccess) return e;
-    return launch_k(stream_ffn_kernel<NT>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
+    return launch_together(stream_ffn_kernel<NT>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
 }
 
 int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }

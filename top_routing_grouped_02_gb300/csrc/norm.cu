@@ -964,15 +964,18 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
     if (fits) {
         e = cudaSuccess;
     } else if (a.d > kRegWidth || al.fits(16)) {
+        // the weights' sums first: dx may be written over dy
         const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.T, 2 * sm_count()));
+        if (a.part != nullptr) {
+            P = ln_partials(a.T);
+            const int v = al.fits(16) ? W : 1;
+            const dim3 g((a.d / v + 255) / 256, P);
+            e = al.fits(16) ? launch_k(ln_weight_wide_kernel<T, W>, g, dim3(256), 0, s, a)
+                            : launch_k(ln_weight_wide_kernel<T, 1>, g, dim3(256), 0, s, a);
+            if (e != cudaSuccess) return e;
+        }
         e = al.fits(16) ? launch_k(ln_backward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
                         : launch_k(ln_backward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
-        if (e != cudaSuccess || a.part == nullptr) return e;
-        P = ln_partials(a.T);
-        const int v = al.fits(16) ? W : 1;
-        const dim3 g((a.d / v + 255) / 256, P);
-        e = al.fits(16) ? launch_k(ln_weight_wide_kernel<T, W>, g, dim3(256), 0, s, a)
-                        : launch_k(ln_weight_wide_kernel<T, 1>, g, dim3(256), 0, s, a);
     } else if constexpr (sizeof(T) == 4) {
         e = a.d <= kRegWidth / 2 ? backward_regs<T, 1, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
     } else {
