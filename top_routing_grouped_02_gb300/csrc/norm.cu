@@ -6,10 +6,9 @@
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
 // Both are bound by HBM: the forward reads x and writes y once, the backward
-// reads x, dy (and dres) and writes dx once. A row lives in the registers of a
-// group of warps (8 elements a thread, 4 or 8 in 32 bits), so nothing is read
-// twice. The groups loop over rows with a stride and fetch the next row before
-// they work on the current one. Row statistics: each warp takes the mean and
+// reads x, dy (and dres) and writes dx once. A group of warps takes a row at a time
+// from a ring of rows in shared memory, which is filled asynchronously ahead of it.
+// Row statistics: each warp takes the mean and
 // the squared deviations from its own mean of its elements, and the warps'
 // pairs are joined by
 //   m = sum n_w m_w / d,  M2 = sum (M2_w + n_w (m_w - m)^2),
@@ -22,8 +21,8 @@
 // second kernel adds the blocks' partials in a fixed order. No atomics: the
 // result does not depend on timing.
 //
-// Rows too wide for the registers (see reg_width) take kernels that read the
-// row again from L2 for each pass.
+// Rows too wide for a ring take kernels that read the row again from L2 for each
+// pass.
 #include <algorithm>
 
 #include "common.cuh"
@@ -70,7 +69,7 @@ __device__ __forceinline__ float load_w(const void *w, int w32, int c, float non
     return w32 ? static_cast<const float *>(w)[c] : load_f32(static_cast<const T *>(w) + c);
 }
 
-// Elements of a row that warp w of `tpr` threads holds.
+// Elements of a row that warp w of `tpr` threads holds, NV vectors of V each thread.
 template <int V, int NV>
 __device__ __forceinline__ int warp_count(int w, int nvec, int tpr) {
     int n = 0;
@@ -79,239 +78,7 @@ __device__ __forceinline__ int warp_count(int w, int nvec, int tpr) {
     return n * V;
 }
 
-// A block's partial sums dgamma, dbeta: each thread's columns, the groups added in
-// order through acc ([2][d] in shared memory, used with several groups).
-template <int V, int NV>
-__device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int group, int tpr, int t,
-                                               const bool (&ok)[NV], const float (&dg)[V * NV],
-                                               const float (&db)[V * NV], float *acc) {
-    float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
-    if (groups == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i])
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int c = (i * tpr + t) * V + j;
-                    part[c] = dg[i * V + j];
-                    part[a.d + c] = db[i * V + j];
-                }
-        return;
-    }
-    __syncthreads();
-    for (int k = 0; k < groups; ++k) {
-        if (group == k) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (ok[i])
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const int c = (i * tpr + t) * V + j;
-                        acc[c] = (k ? acc[c] : 0.f) + dg[i * V + j];
-                        acc[a.d + c] = (k ? acc[a.d + c] : 0.f) + db[i * V + j];
-                    }
-        }
-        __syncthreads();
-    }
-    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) part[c] = acc[c];
-}
-
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(1024, 1) ln_forward_kernel(const LnArgs a) {
-    __shared__ float2 sh[2][32];
-    pdl_wait();
-    pdl_trigger();
-    constexpr int EPT = V * NV;
-    const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
-    const int w0 = group * a.wpr, wg = warp - w0;
-    const int groups = blockDim.x / tpr;
-    const int nvec = a.d / V;
-    const int64_t stride = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + group;
-    if (row >= a.T) return;
-
-    bool ok[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
-    Raw<T, V> cur[NV];
-    auto fetch = [&](int64_t r, Raw<T, V>(&v)[NV]) {
-        const T *p = static_cast<const T *>(a.x) + r * a.ldx;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) v[i] = reinterpret_cast<const Raw<T, V> *>(p)[i * tpr + t];
-    };
-    fetch(row, cur);
-    float gm[EPT], bt[EPT];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (i * tpr + t) * V + j;
-            gm[i * V + j] = ok[i] ? load_w<T>(a.gamma, a.w32, c, 1.f) : 0.f;
-            bt[i * V + j] = ok[i] ? load_w<T>(a.beta, a.w32, c, 0.f) : 0.f;
-        }
-    const float inv_d = 1.f / (float)a.d;
-    const int n_own = warp_count<V, NV>(wg, nvec, tpr);
-    const float inv_own = n_own > 0 ? 1.f / (float)n_own : 0.f;
-    const float n_lane = lane < a.wpr ? (float)warp_count<V, NV>(lane, nvec, tpr) : 0.f;
-
-    for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
-        float f[EPT];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (ok[i]) {
-                to_f32<T, V>(cur[i], f + i * V);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[i * V + j] = 0.f;
-            }
-        }
-        if (row + stride < a.T) fetch(row + stride, cur);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) s += f[e];
-        float mean = warp_sum(s) * inv_own;
-        float m2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float c = f[i * V + j] - mean;
-                    m2 = fmaf(c, c, m2);
-                }
-            }
-        m2 = warp_sum(m2);
-        if (a.wpr > 1) {
-            if (lane == 0) sh[buf][warp] = make_float2(mean, m2);
-            group_sync(1 + group, tpr);
-            const float2 o = lane < a.wpr ? sh[buf][w0 + lane] : make_float2(0.f, 0.f);
-            mean = warp_sum(n_lane * o.x) * inv_d;
-            const float c = o.x - mean;
-            m2 = warp_sum(lane < a.wpr && n_lane > 0.f ? fmaf(n_lane * c, c, o.y) : 0.f);
-        }
-        const float rstd = __frsqrt_rn(fmaf(m2, inv_d, a.eps));
-        T *yp = static_cast<T *>(a.y) + row * a.ldy;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-                float o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    o[j] = fmaf((f[i * V + j] - mean) * rstd, gm[i * V + j], bt[i * V + j]);
-                reinterpret_cast<Raw<T, V> *>(yp)[i * tpr + t] = from_f32<T, V>(o);
-            }
-        if (t == 0) {
-            if (a.mean != nullptr) a.mean[row] = mean;
-            if (a.rstd != nullptr) a.rstd[row] = rstd;
-        }
-    }
-}
-
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(1024, 1) ln_backward_kernel(const LnArgs a) {
-    extern __shared__ float acc_sh[];  // [2][d], used when a block has several groups
-    __shared__ float2 sh[2][32];
-    pdl_wait();
-    pdl_trigger();
-    constexpr int EPT = V * NV;
-    const int tpr = a.wpr * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
-    const int w0 = group * a.wpr;
-    const int groups = blockDim.x / tpr;
-    const int nvec = a.d / V;
-    const int64_t stride = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + group;
-
-    bool ok[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
-    Raw<T, V> xr[NV], yr[NV], rr[NV];
-    float m_next = 0.f, r_next = 0.f;
-    const bool has_res = a.dres != nullptr;
-    auto fetch = [&](int64_t r) {
-        const T *px = static_cast<const T *>(a.x) + r * a.ldx;
-        const T *py = static_cast<const T *>(a.dy) + r * a.lddy;
-        const T *pr = static_cast<const T *>(a.dres) + r * a.lddres;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-                xr[i] = reinterpret_cast<const Raw<T, V> *>(px)[i * tpr + t];
-                yr[i] = reinterpret_cast<const Raw<T, V> *>(py)[i * tpr + t];
-                if (has_res) rr[i] = reinterpret_cast<const Raw<T, V> *>(pr)[i * tpr + t];
-            }
-        m_next = a.mean[r];
-        r_next = a.rstd[r];
-    };
-    if (row < a.T) fetch(row);
-    float gm[EPT], dg[EPT], db[EPT];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (i * tpr + t) * V + j;
-            gm[i * V + j] = ok[i] ? load_w<T>(a.gamma, a.w32, c, 1.f) : 0.f;
-            dg[i * V + j] = db[i * V + j] = 0.f;
-        }
-    const float inv_d = 1.f / (float)a.d;
-
-    for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
-        const float mean = m_next, rstd = r_next;
-        float xh[EPT], g[EPT];
-        Raw<T, V> res[NV];
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (has_res) res[i] = rr[i];
-            if (ok[i]) {
-                to_f32<T, V>(xr[i], xh + i * V);
-                to_f32<T, V>(yr[i], g + i * V);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int e = i * V + j;
-                    xh[e] = (xh[e] - mean) * rstd;
-                    db[e] += g[e];
-                    dg[e] = fmaf(g[e], xh[e], dg[e]);
-                    g[e] *= gm[e];
-                    s2 += g[e];
-                    s1 = fmaf(g[e], xh[e], s1);
-                }
-            }
-        }
-        if (row + stride < a.T) fetch(row + stride);
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (a.wpr > 1) {
-            if (lane == 0) sh[buf][warp] = make_float2(s1, s2);
-            group_sync(1 + group, tpr);
-            const float2 o = lane < a.wpr ? sh[buf][w0 + lane] : make_float2(0.f, 0.f);
-            s1 = warp_sum(o.x);
-            s2 = warp_sum(o.y);
-        }
-        const float c1 = s1 * inv_d, c2 = s2 * inv_d;
-        T *px = static_cast<T *>(a.dx) + row * a.lddx;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i]) {
-                float o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    o[j] = rstd * (fmaf(-c1, xh[i * V + j], g[i * V + j]) - c2);
-                if (has_res) {
-                    float q[V];
-                    to_f32<T, V>(res[i], q);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] += q[j];
-                }
-                reinterpret_cast<Raw<T, V> *>(px)[i * tpr + t] = from_f32<T, V>(o);
-            }
-    }
-    if (a.part == nullptr) return;
-    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, acc_sh);
-}
-
-// ---- rows on 16-byte boundaries: a ring of rows in shared memory -----------------
+// ---- a ring of rows in shared memory ---------------------------------------------
 //
 // Each row group keeps a ring of its next rows in shared memory, filled by bulk
 // copies (cp.async.bulk, one thread of the group, completion on an mbarrier), so
@@ -324,6 +91,14 @@ __global__ void __launch_bounds__(1024, 1) ln_backward_kernel(const LnArgs a) {
 // shuffles, barrier and bookkeeping of a row are paid per warp), the arithmetic is
 // on packed pairs, and gamma and beta wait in shared memory in fp32, as planes of
 // four elements of every vector, which a warp reads without bank conflicts.
+//
+// SHIFT: rows that do not start on 16-byte boundaries (an odd length, a sliced
+// buffer). The bulk copies take the 16-byte blocks that hold a row, so its image starts
+// up to 15 bytes into the stage, and a thread shifts its vectors out of two
+// neighbouring ones; results go to an image of the output row in shared memory, which
+// leaves by a bulk copy of its whole blocks and by element at its ends. Nothing is
+// read before the first or after the last element of a tensor: there the row's ends
+// come by element too.
 
 constexpr int kRingStages = 4;  // most
 constexpr int kMaxGroups = 28;
@@ -356,11 +131,11 @@ __device__ __forceinline__ void plane_pairs(const float *planes, int nvec, int v
 }
 template <typename T, int V>
 __device__ __forceinline__ void fill_planes(float *planes, const void *w, int w32, int d, float none) {
-    const int nvec = d / V;
+    const int nvec = (d + V - 1) / V;
     for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
         float f[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = load_w<T>(w, w32, v * V + j, none);
+        for (int j = 0; j < V; ++j) f[j] = v * V + j < d ? load_w<T>(w, w32, v * V + j, none) : 0.f;
 #pragma unroll
         for (int h = 0; h < V / 4; ++h)
             *reinterpret_cast<float4 *>(planes + (h * nvec + v) * 4) =
@@ -368,34 +143,17 @@ __device__ __forceinline__ void fill_planes(float *planes, const void *w, int w3
     }
 }
 
-// A block's partial sums dgamma, dbeta, 16-byte vectors at a time: the groups are added
-// in order through acc (in planes, [2][d], used with several groups).
+// A block's partial sums dgamma, dbeta: the groups are added in order through acc (in
+// planes, [2][d rounded up to V]), 16 bytes at a time.
 template <int V, int NV>
-__device__ __forceinline__ void store_partial_vecs(const LnArgs &a, int groups, int group, int tpr,
-                                                   int t, const bool (&ok)[NV],
-                                                   const f32x2 (&dg)[NV][V / 2],
-                                                   const f32x2 (&db)[NV][V / 2], float *acc) {
-    float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * 2 * a.d);
+__device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int group, int tpr,
+                                               int t, const bool (&ok)[NV],
+                                               const f32x2 (&dg)[NV][V / 2],
+                                               const f32x2 (&db)[NV][V / 2], float *acc) {
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
     float4 *sums = reinterpret_cast<float4 *>(acc);
-    const int nvec = a.d / V;
+    const int nvec = (a.d + V - 1) / V;
     constexpr int H = V / 4;
-    auto quad = [&](const f32x2 *p) {
-        float4 q;
-        unpair(p[0], q.x, q.y);
-        unpair(p[1], q.z, q.w);
-        return q;
-    };
-    if (groups == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (ok[i])
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    part[(i * tpr + t) * H + h] = quad(&dg[i][2 * h]);
-                    part[(nvec + i * tpr + t) * H + h] = quad(&db[i][2 * h]);
-                }
-        return;
-    }
     __syncthreads();
     for (int k = 0; k < groups; ++k) {
         if (group == k) {
@@ -406,7 +164,10 @@ __device__ __forceinline__ void store_partial_vecs(const LnArgs &a, int groups, 
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int h = 0; h < H; ++h) {
-                            float4 q = quad(m == 0 ? &dg[i][2 * h] : &db[i][2 * h]);
+                            const f32x2 *p = m == 0 ? &dg[i][2 * h] : &db[i][2 * h];
+                            float4 q;
+                            unpair(p[0], q.x, q.y);
+                            unpair(p[1], q.z, q.w);
                             float4 &x = sums[(m * H + h) * nvec + i * tpr + t];
                             if (k > 0) {
                                 q.x = x.x + q.x;
@@ -419,13 +180,129 @@ __device__ __forceinline__ void store_partial_vecs(const LnArgs &a, int groups, 
         }
         __syncthreads();
     }
-    for (int c = threadIdx.x; c < 2 * H * nvec; c += blockDim.x) {
-        const int m = c / (H * nvec), r = c - m * H * nvec, v = r / H, h = r - v * H;
-        part[c] = sums[(m * H + h) * nvec + v];
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) {
+        const int m = c >= a.d, e = c - m * a.d, v = e / V, j = e - v * V;
+        part[c] = acc[((m * H + j / 4) * nvec + v) * 4 + (j & 3)];
     }
 }
 
-template <typename T, int V, int NV>
+// ---- SHIFT helpers
+
+// Bytes of the image of a row: its blocks, wherever it starts, and one more that the
+// last vector's shift reads.
+__host__ __device__ constexpr uint32_t image_bytes(int d, int esize) {
+    return ((uint32_t)d * esize + 15) / 16 * 16 + 32;
+}
+// One thread: the blocks of row r of a [T, d] tensor into img, announced on bar
+// (which the caller arrives on, with the bytes returned). Elements in blocks that reach
+// out of the tensor are copied one by one.
+template <typename T>
+__device__ __forceinline__ uint32_t fetch_image(uint8_t *img, const T *base, int64_t ld, int64_t r,
+                                                int64_t rows, int d, uint32_t bar) {
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(base);
+    const uintptr_t b1 = reinterpret_cast<uintptr_t>(base + (rows - 1) * ld + d);
+    const T *row = base + r * ld;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row), end = reinterpret_cast<uintptr_t>(row + d);
+    const uintptr_t origin = at & ~(uintptr_t)15;
+    uintptr_t lo = origin, hi = (end + 15) & ~(uintptr_t)15;
+    if (lo < b0) lo += 16;
+    if (hi > b1) hi -= 16;
+    uint32_t bytes = 0;
+    if (hi > lo) {
+        bytes = (uint32_t)(hi - lo);
+        ptx::bulk_load(ptx::smem_addr(img + (lo - origin)), reinterpret_cast<const void *>(lo), bytes, bar);
+    } else {
+        lo = hi = end;  // no whole block: every element by itself
+    }
+    T *to = reinterpret_cast<T *>(img + (at - origin));
+    for (const T *p = row; reinterpret_cast<uintptr_t>(p) < lo; ++p) to[p - row] = *p;
+    if (hi < end)
+        for (const T *p = reinterpret_cast<const T *>(hi); p < row + d; ++p) to[p - row] = *p;
+    return bytes;
+}
+// The 16 bytes of vector v of a row whose image starts `shift` bytes into img.
+__device__ __forceinline__ uint4 image_vec(const uint8_t *img, int v, uint32_t shift) {
+    const uint4 a = reinterpret_cast<const uint4 *>(img)[v], b = reinterpret_cast<const uint4 *>(img)[v + 1];
+    uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x;
+    if (shift & 8) {
+        w0 = a.z;
+        w1 = a.w;
+        w2 = b.x;
+        w3 = b.y;
+        w4 = b.z;
+    }
+    if (shift & 4) {
+        w0 = w1;
+        w1 = w2;
+        w2 = w3;
+        w3 = w4;
+        w4 = shift & 8 ? b.w : b.y;
+    }
+    const uint32_t bits = (shift & 2) * 8;
+    return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits),
+                      __funnelshift_r(w2, w3, bits), __funnelshift_r(w3, w4, bits));
+}
+// v's first n elements (of 16 bytes), zeros after them.
+template <typename T>
+__device__ __forceinline__ uint4 first_elems(uint4 v, int n) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int left = (int)(n * sizeof(T)) - 4 * j;  // bytes of this word
+        if (left <= 0) w[j] = 0;
+        else if (left == 2) w[j] &= 0xffffu;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Writes n elements of a vector into the image of an output row.
+template <typename T>
+__device__ __forceinline__ void put_image(uint8_t *img, int v, uint32_t shift, uint4 q, int n) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint8_t *p = img + shift + v * 16;
+    if (n * (int)sizeof(T) == 16) {
+        if (sizeof(T) == 4 || (shift & 2) == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t *>(p)[j] = w[j];
+        } else {
+            *reinterpret_cast<uint16_t *>(p) = (uint16_t)w[0];
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                *reinterpret_cast<uint32_t *>(p + 2 + 4 * j) = __funnelshift_r(w[j], w[j + 1], 16);
+            *reinterpret_cast<uint16_t *>(p + 14) = (uint16_t)(w[3] >> 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16 / (int)sizeof(T); ++e)
+        if (e < n) {
+            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(p)[e] = w[e];
+            else reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+}
+// An output row from its image: whole blocks by one bulk copy (thread 0), the
+// elements at its ends by the group's other threads.
+template <typename T>
+__device__ __forceinline__ void send_image(const uint8_t *img, T *row, int d, int t, int tpr) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row), end = reinterpret_cast<uintptr_t>(row + d);
+    const uintptr_t origin = at & ~(uintptr_t)15;
+    const uintptr_t lo = (at + 15) & ~(uintptr_t)15, hi = end & ~(uintptr_t)15;
+    const bool whole = hi > lo;
+    if (t == 0) {
+        if (whole)
+            ptx::bulk_store(reinterpret_cast<void *>(lo), ptx::smem_addr(img + (lo - origin)),
+                            (uint32_t)(hi - lo));
+        ptx::bulk_commit_group();
+    }
+    const T *from = reinterpret_cast<const T *>(img + (at - origin));
+    const int head = whole ? (int)((lo - at) / sizeof(T)) : d;
+    const int tail = whole ? (int)((end - hi) / sizeof(T)) : 0;
+    for (int i = t; i < head + tail; i += tpr) {
+        const int e = i < head ? i : d - tail + (i - head);
+        row[e] = from[e];
+    }
+}
+
+template <typename T, int V, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const LnArgs a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
@@ -434,12 +311,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
     const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
     const int w0 = group * a.wpr, wg = warp - w0;
     const int groups = blockDim.x / tpr, S = a.stages;
-    const int nvec = a.d / V;
-    const uint32_t row_bytes = (uint32_t)a.d * sizeof(T);
+    const int nvec = (a.d + V - 1) / V;
+    const uint32_t row_bytes = SHIFT ? image_bytes(a.d, sizeof(T)) : (uint32_t)a.d * sizeof(T);
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + group;
-    float *gamma = reinterpret_cast<float *>(ring_sh + kRingCtl), *beta = gamma + a.d;
-    uint8_t *ring = ring_sh + kRingCtl + (size_t)2 * a.d * sizeof(float) + (size_t)group * S * row_bytes;
+    float *gamma = reinterpret_cast<float *>(ring_sh + kRingCtl), *beta = gamma + nvec * V;
+    // a group's ring and (SHIFT) its output image
+    uint8_t *ring = ring_sh + kRingCtl + (size_t)2 * nvec * V * sizeof(float) +
+                    (size_t)group * (S + SHIFT) * row_bytes;
+    uint8_t *image = ring + (size_t)S * row_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
@@ -449,6 +329,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
     pdl_wait();
     pdl_trigger();
     auto fetch = [&](int64_t r, int s) {
+        if constexpr (SHIFT) {
+            const uint32_t bytes = fetch_image(ring + (size_t)s * row_bytes, static_cast<const T *>(a.x),
+                                               a.ldx, r, a.T, a.d, bar0 + 8 * s);
+            ptx::mbar_arrive_expect_tx(bar0 + 8 * s, bytes);
+            return;
+        }
         ptx::mbar_arrive_expect_tx(bar0 + 8 * s, row_bytes);
         ptx::bulk_load(ptx::smem_addr(ring + (size_t)s * row_bytes),
                        static_cast<const T *>(a.x) + r * a.ldx, row_bytes, bar0 + 8 * s);
@@ -463,21 +349,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
 #pragma unroll
     for (int i = 0; i < NV; ++i) ok[i] = i * tpr + t < nvec;
     const float inv_d = 1.f / (float)a.d;
-    const int n_own = warp_count<V, NV>(wg, nvec, tpr);
+    // elements of a warp: its vectors, less what the last one lacks
+    const int lacks = nvec * V - a.d, last = (nvec - 1) % tpr / 32;
+    const int n_own = warp_count<V, NV>(wg, nvec, tpr) - (wg == last ? lacks : 0);
     const float inv_own = n_own > 0 ? 1.f / (float)n_own : 0.f;
-    const float n_lane = lane < a.wpr ? (float)warp_count<V, NV>(lane, nvec, tpr) : 0.f;
+    const float n_lane =
+        lane < a.wpr ? (float)(warp_count<V, NV>(lane, nvec, tpr) - (lane == last ? lacks : 0)) : 0.f;
 
     int s = 0;
     uint32_t ph = 0;
     for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
         ring_wait(bar0 + 8 * s, ph);
-        const uint4 *src = reinterpret_cast<const uint4 *>(ring + (size_t)s * row_bytes) + t;
+        const uint8_t *stage = ring + (size_t)s * row_bytes;
+        const uint4 *src = reinterpret_cast<const uint4 *>(stage) + t;
+        const uint32_t sx = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const T *>(a.x) + row * a.ldx) & 15;
         // f: the elements, then their distances from the warp's own mean (a thread past
         // the row's end holds zeros throughout)
         f32x2 f[NV][P2], acc = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            to_pairs<T, V>(ok[i] ? src[i * tpr] : ctl->zero, f[i]);
+            if constexpr (SHIFT) {
+                const int v = i * tpr + t;
+                uint4 q = ok[i] ? image_vec(stage, v, sx) : make_uint4(0, 0, 0, 0);
+                if ((v + 1) * V > a.d) q = first_elems<T>(q, a.d - v * V);
+                to_pairs<T, V>(q, f[i]);
+            } else {
+                to_pairs<T, V>(ok[i] ? src[i * tpr] : ctl->zero, f[i]);
+            }
 #pragma unroll
             for (int j = 0; j < P2; ++j) acc = add2(acc, f[i][j]);
         }
@@ -486,6 +384,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const f32x2 shift = both(ok[i] ? -own : 0.f);
+            if (SHIFT && ok[i] && (i * tpr + t + 1) * V > a.d) {
+                // the last vector: what it lacks stays zero
+                const int n = a.d - (i * tpr + t) * V;
+#pragma unroll
+                for (int j = 0; j < P2; ++j) {
+                    f[i][j] = add2(f[i][j], pair(2 * j < n ? -own : 0.f, 2 * j + 1 < n ? -own : 0.f));
+                    acc = fma2(f[i][j], f[i][j], acc);
+                }
+                continue;
+            }
 #pragma unroll
             for (int j = 0; j < P2; ++j) {
                 f[i][j] = add2(f[i][j], shift);
@@ -493,6 +401,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
             }
         }
         float mean = own, dev = warp_sum(pair_sum(acc));
+        if (SHIFT && t == 0) ptx::bulk_wait_group_read<0>();  // the image may be written again
         if (a.wpr > 1) {
             if (lane == 0) ctl->stat[buf][warp] = make_float2(own, dev);
             group_sync(1 + group, tpr);
@@ -513,7 +422,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
         }
         const float rstd = __frsqrt_rn(fmaf(dev, inv_d, a.eps));
         const f32x2 r2 = both(rstd), off = both((own - mean) * rstd);
-        uint4 *yp = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.ldy) + t;
+        T *yrow = static_cast<T *>(a.y) + row * a.ldy;
+        uint4 *yp = reinterpret_cast<uint4 *>(yrow) + t;
+        const uint32_t sy = (uint32_t)reinterpret_cast<uintptr_t>(yrow) & 15;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!ok[i]) continue;
@@ -522,16 +433,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
             plane_pairs<V>(beta, nvec, i * tpr + t, o);
 #pragma unroll
             for (int j = 0; j < P2; ++j) o[j] = fma2(fma2(f[i][j], r2, off), g[j], o[j]);
-            yp[i * tpr] = from_pairs<T, V>(o);
+            const uint4 q = from_pairs<T, V>(o);
+            if constexpr (SHIFT) put_image<T>(image, i * tpr + t, sy, q, min(V, a.d - (i * tpr + t) * V));
+            else yp[i * tpr] = q;
+        }
+        if constexpr (SHIFT) {
+            ptx::fence_proxy_async_smem();
+            if (a.wpr > 1) group_sync(1 + group, tpr);
+            else __syncwarp();
+            send_image(image, yrow, a.d, t, tpr);
         }
         if (t == 0) {
             if (a.mean != nullptr) a.mean[row] = mean;
             if (a.rstd != nullptr) a.rstd[row] = rstd;
         }
-    }
+    }    if (SHIFT && t == 0) ptx::bulk_wait_group<0>();
 }
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(const LnArgs a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
@@ -540,16 +459,17 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
     const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
     const int w0 = group * a.wpr;
     const int groups = blockDim.x / tpr, S = a.stages;
-    const int nvec = a.d / V;
-    const uint32_t row_bytes = (uint32_t)a.d * sizeof(T);
+    const int nvec = (a.d + V - 1) / V;
+    const uint32_t row_bytes = SHIFT ? image_bytes(a.d, sizeof(T)) : (uint32_t)a.d * sizeof(T);
     const bool has_res = a.dres != nullptr;
     const uint32_t stage_bytes = (has_res ? 3 : 2) * row_bytes;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + group;
     // gamma, then the rings; later the sums of the groups
     float *gamma = reinterpret_cast<float *>(ring_sh + kRingCtl);
-    uint8_t *rings = ring_sh + kRingCtl + (size_t)a.d * sizeof(float);
-    uint8_t *ring = rings + (size_t)group * S * stage_bytes;
+    uint8_t *rings = ring_sh + kRingCtl + (size_t)nvec * V * sizeof(float);
+    uint8_t *ring = rings + (size_t)group * (S * stage_bytes + SHIFT * row_bytes);
+    uint8_t *image = ring + (size_t)S * stage_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
@@ -560,6 +480,16 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
     pdl_trigger();
     auto fetch = [&](int64_t r, int s) {
         const uint32_t dst = ptx::smem_addr(ring + (size_t)s * stage_bytes), bar = bar0 + 8 * s;
+        if constexpr (SHIFT) {
+            uint8_t *img = ring + (size_t)s * stage_bytes;
+            uint32_t bytes = fetch_image(img, static_cast<const T *>(a.x), a.ldx, r, a.T, a.d, bar) +
+                             fetch_image(img + row_bytes, static_cast<const T *>(a.dy), a.lddy, r, a.T, a.d, bar);
+            if (has_res)
+                bytes += fetch_image(img + 2 * row_bytes, static_cast<const T *>(a.dres), a.lddres, r, a.T,
+                                     a.d, bar);
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+            return;
+        }
         ptx::mbar_arrive_expect_tx(bar, stage_bytes);
         ptx::bulk_load(dst, static_cast<const T *>(a.x) + r * a.ldx, row_bytes, bar);
         ptx::bulk_load(dst + row_bytes, static_cast<const T *>(a.dy) + r * a.lddy, row_bytes, bar);
@@ -595,8 +525,17 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             r_next = a.rstd[row + stride];
         }
         ring_wait(bar0 + 8 * s, ph);
-        const uint4 *px = reinterpret_cast<const uint4 *>(ring + (size_t)s * stage_bytes) + t;
+        const uint8_t *stage = ring + (size_t)s * stage_bytes;
+        const uint4 *px = reinterpret_cast<const uint4 *>(stage) + t;
         const uint4 *py = px + nvec, *pr = py + nvec;
+        // vector i of x, dy, dres
+        auto shift_of = [&](const void *base, int64_t ld) {
+            return (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + row * ld) & 15;
+        };
+        const uint32_t sx = shift_of(a.x, a.ldx), sy = shift_of(a.dy, a.lddy), sr = shift_of(a.dres, a.lddres);
+        auto vec_x = [&](int i) { return SHIFT ? image_vec(stage, i * tpr + t, sx) : px[i * tpr]; };
+        auto vec_y = [&](int i) { return SHIFT ? image_vec(stage + row_bytes, i * tpr + t, sy) : py[i * tpr]; };
+        auto vec_r = [&](int i) { return SHIFT ? image_vec(stage + 2 * row_bytes, i * tpr + t, sr) : pr[i * tpr]; };
         // xh = x r - m r
         const f32x2 r2 = both(rstd), shift = both(-mean * rstd);
         f32x2 p1 = 0, p2 = 0;
@@ -604,8 +543,13 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
         for (int i = 0; i < NV; ++i) {
             if (!ok[i]) continue;
             f32x2 x[P2], y[P2], g[P2];
-            to_pairs<T, V>(px[i * tpr], x);
-            to_pairs<T, V>(py[i * tpr], y);
+            uint4 qx = vec_x(i), qy = vec_y(i);
+            if (SHIFT && (i * tpr + t + 1) * V > a.d) {  // what the last vector lacks adds nothing
+                qx = first_elems<T>(qx, a.d - (i * tpr + t) * V);
+                qy = first_elems<T>(qy, a.d - (i * tpr + t) * V);
+            }
+            to_pairs<T, V>(qx, x);
+            to_pairs<T, V>(qy, y);
             plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
             for (int j = 0; j < P2; ++j) {
@@ -617,6 +561,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             }
         }
         float s1 = warp_sum(pair_sum(p1)), s2 = warp_sum(pair_sum(p2));
+        if (SHIFT && t == 0) ptx::bulk_wait_group_read<0>();  // the image may be written again
         if (a.wpr > 1) {
             if (lane == 0) ctl->stat[buf][warp] = make_float2(s1, s2);
             group_sync(1 + group, tpr);
@@ -632,23 +577,33 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
         }
         // dx = gy r - xh (c1 r) - c2 r
         const f32x2 k1 = both(-s1 * inv_d * rstd), k2 = both(-s2 * inv_d * rstd);
-        uint4 *pd = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.lddx) + t;
+        T *drow = static_cast<T *>(a.dx) + row * a.lddx;
+        uint4 *pd = reinterpret_cast<uint4 *>(drow) + t;
+        const uint32_t sd = (uint32_t)reinterpret_cast<uintptr_t>(drow) & 15;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!ok[i]) continue;
             f32x2 x[P2], y[P2], g[P2];
-            to_pairs<T, V>(px[i * tpr], x);
-            to_pairs<T, V>(py[i * tpr], y);
+            to_pairs<T, V>(vec_x(i), x);
+            to_pairs<T, V>(vec_y(i), y);
             plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
             for (int j = 0; j < P2; ++j)
                 x[j] = fma2(fma2(x[j], r2, shift), k1, fma2(mul2(y[j], g[j]), r2, k2));
             if (has_res) {
-                to_pairs<T, V>(pr[i * tpr], y);
+                to_pairs<T, V>(vec_r(i), y);
 #pragma unroll
                 for (int j = 0; j < P2; ++j) x[j] = add2(x[j], y[j]);
             }
-            pd[i * tpr] = from_pairs<T, V>(x);
+            const uint4 q = from_pairs<T, V>(x);
+            if constexpr (SHIFT) put_image<T>(image, i * tpr + t, sd, q, min(V, a.d - (i * tpr + t) * V));
+            else pd[i * tpr] = q;
+        }
+        if constexpr (SHIFT) {
+            ptx::fence_proxy_async_smem();
+            if (a.wpr > 1) group_sync(1 + group, tpr);
+            else __syncwarp();
+            send_image(image, drow, a.d, t, tpr);
         }
         s_prev = s;
         if (++s == S) {
@@ -656,8 +611,9 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             ph ^= 1;
         }
     }
+    if (SHIFT && t == 0) ptx::bulk_wait_group<0>();
     if (a.part == nullptr) return;
-    store_partial_vecs<V, NV>(a, groups, group, tpr, t, ok, dg, db, reinterpret_cast<float *>(rings));
+    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, reinterpret_cast<float *>(rings));
 }
 
 // dgamma[c], dbeta[c] = the sum of P partial rows, each thread row q of the block
@@ -690,7 +646,7 @@ ln_weight_reduce_kernel(const float *__restrict__ part, int P, int d, int w32, v
     else store_f32(static_cast<T *>(out) + i, s);
 }
 
-// ---- rows too wide for the registers ----------------------------------------
+// ---- rows too wide for a ring ------------------------------------------------
 
 // Sum over the block, in a fixed order.
 __device__ __forceinline__ float block_sum(float v, float *sh) {
@@ -819,12 +775,6 @@ __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
 
 // ------------------------------------------------------------ host side --
 
-// Widest row of the register kernels: 32 warps of 8 elements a thread.
-constexpr int kRegWidth = 8192;
-// Threads of a backward block: as many row groups as fit, so that there is one
-// partial row of weight gradients per SM.
-constexpr int kBwdThreads = 1024;
-
 // Vector length (elements) that divides d and every row stride and suits the
 // pointers' alignment.
 struct Align {
@@ -839,131 +789,98 @@ struct Align {
 
 int row_groups(int wpr, int threads) { return std::max(1, threads / (32 * wpr)); }
 
-template <typename T, int V, int NV>
-cudaError_t forward_regs(LnArgs a, cudaStream_t s) {
-    a.wpr = (a.d / V + 32 * NV - 1) / (32 * NV);
-    const int groups = row_groups(a.wpr, 256), threads = groups * a.wpr * 32;
-    const int64_t want = (a.T + groups - 1) / groups;
-    const int grid = (int)std::min<int64_t>(want, (int64_t)sm_count() * std::max(1, 1024 / threads));
-    return launch_k(ln_forward_kernel<T, V, NV>, dim3(grid), dim3(threads), 0, s, a);
-}
-
-template <typename T, int V, int NV>
-cudaError_t backward_regs(LnArgs a, int *P, cudaStream_t s) {
-    a.wpr = (a.d / V + 32 * NV - 1) / (32 * NV);
-    // at most 15 groups: each has a barrier of its own (barrier 0 is the block's)
-    int groups = row_groups(a.wpr, kBwdThreads);
-    if (a.wpr > 1) groups = std::min(groups, 15);
-    groups = (int)std::min<int64_t>(groups, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
-    const int threads = groups * a.wpr * 32;
-    const int64_t want = (a.T + groups - 1) / groups;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count()));
-    *P = grid;
-    const size_t smem = groups > 1 && a.part != nullptr ? (size_t)2 * a.d * sizeof(float) : 0;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = ensure_dynamic_smem(
-            reinterpret_cast<const void *>(ln_backward_kernel<T, V, NV>), (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_k(ln_backward_kernel<T, V, NV>, dim3(grid), dim3(threads), smem, s, a);
-}
-
 // Row groups and ring stages of a block of at most max_threads threads (one block
 // per SM), with at most T / SMs rounded up groups so that few rows spread over the
 // SMs. False where two stages of one group do not fit the shared memory.
 constexpr size_t kRingSmem = 224 * 1024;
-bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t stage, int *groups) {
+// `fixed` bytes a block, `extra` a group, `stage` a stage.
+bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t extra, size_t stage,
+                int *groups) {
     a.wpr = (a.d + per_thread * 32 - 1) / (per_thread * 32);
     if (a.wpr * 32 > max_threads) return false;
     int g = std::min(row_groups(a.wpr, max_threads), a.wpr > 1 ? 15 : kMaxGroups);
     g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
-    while (g > 1 && fixed + 2 * g * stage > kRingSmem) --g;
-    if (fixed + 2 * g * stage > kRingSmem) return false;
-    a.stages = (int)std::min<size_t>((kRingSmem - fixed) / (g * stage), kRingStages);
+    while (g > 1 && fixed + g * (extra + 2 * stage) > kRingSmem) --g;
+    if (fixed + g * (extra + 2 * stage) > kRingSmem) return false;
+    a.stages = (int)std::min<size_t>(((kRingSmem - fixed) / g - extra) / stage, kRingStages);
     *groups = g;
     return true;
 }
 
-template <typename T, int V, int NV>
+// Bytes of the fp32 planes of one weight vector.
+template <int V>
+size_t plane_bytes(int d) { return (size_t)(d + V - 1) / V * V * sizeof(float); }
+
+template <typename T, int V, int NV, bool SHIFT>
 cudaError_t forward_ring(LnArgs a, bool *fits, cudaStream_t s) {
     int groups;
-    const size_t stage = (size_t)a.d * sizeof(T), fixed = kRingCtl + (size_t)2 * a.d * sizeof(float);
-    *fits = ring_shape(a, V * NV, kFwdThreads, fixed, stage, &groups);
+    const size_t stage = SHIFT ? image_bytes(a.d, sizeof(T)) : (size_t)a.d * sizeof(T);
+    const size_t fixed = kRingCtl + 2 * plane_bytes<V>(a.d);
+    *fits = ring_shape(a, V * NV, kFwdThreads, fixed, SHIFT ? stage : 0, stage, &groups);
     if (!*fits) return cudaSuccess;
     const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV>), (int)kRingSmem);
+        reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV, SHIFT>), (int)kRingSmem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, sm_count());
-    return launch_k(ln_forward_ring_kernel<T, V, NV>, dim3(grid), dim3(groups * a.wpr * 32),
-                    fixed + groups * a.stages * stage, s, a);
+    return launch_k(ln_forward_ring_kernel<T, V, NV, SHIFT>, dim3(grid), dim3(groups * a.wpr * 32),
+                    fixed + groups * (a.stages + SHIFT) * stage, s, a);
 }
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool SHIFT>
 cudaError_t backward_ring(LnArgs a, int *P, bool *fits, cudaStream_t s) {
     int groups;
-    const size_t stage = (size_t)a.d * sizeof(T) * (a.dres != nullptr ? 3 : 2);
-    const size_t fixed = kRingCtl + (size_t)a.d * sizeof(float);
-    *fits = ring_shape(a, V * NV, kBwdRingThreads, fixed, stage, &groups);
+    const size_t row = SHIFT ? image_bytes(a.d, sizeof(T)) : (size_t)a.d * sizeof(T);
+    const size_t stage = row * (a.dres != nullptr ? 3 : 2), fixed = kRingCtl + plane_bytes<V>(a.d);
+    *fits = ring_shape(a, V * NV, kBwdRingThreads, fixed, SHIFT ? row : 0, stage, &groups);
     if (!*fits) return cudaSuccess;
     const cudaError_t e = ensure_dynamic_smem(
-        reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV>), (int)kRingSmem);
+        reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV, SHIFT>), (int)kRingSmem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(sm_count(), kLnPartials));
     *P = grid;
-    // (two stages of one group, 8 d bytes or more, hold the groups' [2][d] fp32 sums)
-    return launch_k(ln_backward_ring_kernel<T, V, NV>, dim3(grid), dim3(groups * a.wpr * 32),
-                    fixed + groups * a.stages * stage, s, a);
+    // (two stages hold the groups' [2][d] fp32 sums)
+    return launch_k(ln_backward_ring_kernel<T, V, NV, SHIFT>, dim3(grid), dim3(groups * a.wpr * 32),
+                    fixed + groups * (a.stages * stage + SHIFT * row), s, a);
 }
 
 // Vectors a thread: one or two where a warp still holds the row, else four.
-template <typename T>
-cudaError_t forward_aligned(const LnArgs &a, bool *fits, cudaStream_t s) {
+template <typename T, bool SHIFT>
+cudaError_t forward_rows(const LnArgs &a, bool *fits, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
-    if (a.d <= 32 * W) return forward_ring<T, W, 1>(a, fits, s);
-    if (a.d <= 64 * W) return forward_ring<T, W, 2>(a, fits, s);
-    return forward_ring<T, W, 4>(a, fits, s);
+    if (a.d <= 32 * W) return forward_ring<T, W, 1, SHIFT>(a, fits, s);
+    if (a.d <= 64 * W) return forward_ring<T, W, 2, SHIFT>(a, fits, s);
+    return forward_ring<T, W, 4, SHIFT>(a, fits, s);
 }
-template <typename T>
-cudaError_t backward_aligned(const LnArgs &a, int *P, bool *fits, cudaStream_t s) {
+template <typename T, bool SHIFT>
+cudaError_t backward_rows(const LnArgs &a, int *P, bool *fits, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
-    if (a.d <= 32 * W) return backward_ring<T, W, 1>(a, P, fits, s);
-    if (a.d <= 64 * W) return backward_ring<T, W, 2>(a, P, fits, s);
-    return backward_ring<T, W, 4>(a, P, fits, s);
+    if (a.d <= 32 * W) return backward_ring<T, W, 1, SHIFT>(a, P, fits, s);
+    if (a.d <= 64 * W) return backward_ring<T, W, 2, SHIFT>(a, P, fits, s);
+    return backward_ring<T, W, 4, SHIFT>(a, P, fits, s);
 }
 
 template <typename T>
 cudaError_t forward_type(const LnArgs &a, const Align &al, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);  // elements of a 16-byte vector
-    if (al.fits(16)) {
-        bool fits = false;
-        const cudaError_t e = forward_aligned<T>(a, &fits, s);
-        if (e != cudaSuccess || fits) return e;
-    }
-    if (a.d > kRegWidth || al.fits(16)) {
-        const int grid = (int)std::min<int64_t>(a.T, 2 * sm_count());
-        return al.fits(16) ? launch_k(ln_forward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
-                           : launch_k(ln_forward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
-    }
-    if constexpr (sizeof(T) == 4)
-        return a.d <= kRegWidth / 2 ? forward_regs<T, 1, 4>(a, s) : forward_regs<T, 1, 8>(a, s);
-    else
-        return al.fits(4) ? forward_regs<T, 2, 4>(a, s) : forward_regs<T, 1, 8>(a, s);
+    bool fits = false;
+    const cudaError_t e =
+        al.fits(16) ? forward_rows<T, false>(a, &fits, s) : forward_rows<T, true>(a, &fits, s);
+    if (e != cudaSuccess || fits) return e;
+    const int grid = (int)std::min<int64_t>(a.T, 2 * sm_count());
+    return al.fits(16) ? launch_k(ln_forward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
+                       : launch_k(ln_forward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
 }
 
 template <typename T>
 cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *dbeta,
                           cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
-    cudaError_t e;
     int P = 0;
     bool fits = false;
-    if (al.fits(16)) {
-        e = backward_aligned<T>(a, &P, &fits, s);
-        if (e != cudaSuccess) return e;
-    }
-    if (fits) {
-        e = cudaSuccess;
-    } else if (a.d > kRegWidth || al.fits(16)) {
+    cudaError_t e =
+        al.fits(16) ? backward_rows<T, false>(a, &P, &fits, s) : backward_rows<T, true>(a, &P, &fits, s);
+    if (e != cudaSuccess) return e;
+    if (!fits) {
         // the weights' sums first: dx may be written over dy
         const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.T, 2 * sm_count()));
         if (a.part != nullptr) {
@@ -976,10 +893,6 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
         }
         e = al.fits(16) ? launch_k(ln_backward_wide_kernel<T, W>, dim3(grid), dim3(1024), 0, s, a)
                         : launch_k(ln_backward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
-    } else if constexpr (sizeof(T) == 4) {
-        e = a.d <= kRegWidth / 2 ? backward_regs<T, 1, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
-    } else {
-        e = al.fits(4) ? backward_regs<T, 2, 4>(a, &P, s) : backward_regs<T, 1, 8>(a, &P, s);
     }
     if (e != cudaSuccess || a.part == nullptr) return e;
     return launch_k(ln_weight_reduce_kernel<T>, dim3((2 * a.d + 31) / 32), dim3(512), 0, s,
