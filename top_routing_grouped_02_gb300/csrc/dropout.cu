@@ -18,8 +18,10 @@
 // Elements are taken in whole generator blocks of eight. Where eight elements
 // are 16-byte aligned in every tensor, a thread loads them as vectors; otherwise
 // a warp takes 32 blocks = 256 elements, each lane draws one block's eight
-// mask bits, and the lanes then walk the elements one by one, neighbouring lanes on
-// neighbouring elements, taking each bit from the lane that drew it.
+// mask bits, and the lanes then walk the elements by one or two, neighbouring lanes on
+// neighbouring elements, taking each bit from the lane that drew it. Measured with a
+// residual, bf16, 8192 rows: 7168 or 7167 contiguous 54 us (6.5 TB/s), 7166 in rows of
+// 7170 76 us, 7167 in rows of 7170 86 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -126,45 +128,81 @@ __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(const DropArgs a)
     }
 }
 
-// Element path: any strides and alignment.
-template <typename T>
+// Element path: any strides and alignment. W elements an access: 2 where every row of
+// 16-bit elements starts on a word and has an even length, else 1.
+template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) dropout_elem_kernel(const DropArgs a) {
     pdl_wait();
     pdl_trigger();
     const uint64_t offset = a.offset + (a.offset_dev != nullptr ? *a.offset_dev : 0ull);
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
     T *y = static_cast<T *>(a.y);
+    constexpr int N = 8 / W;  // accesses of a lane in a run of 256 elements
     const int lane = threadIdx.x & 31;
     const int64_t runs = (a.n + 255) / 256, step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t run = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); run < runs;
          run += step) {
+        const int64_t i0 = run * 256;
+        const int64_t row = a.n <= 0xffffff00ll ? (int64_t)((uint32_t)i0 / (uint32_t)a.d) : i0 / a.d;
+        const int64_t col0 = i0 - row * a.d;
         const uint32_t m = keep_bits(a, (uint64_t)run * 32 + lane, offset);
-        int64_t i = run * 256 + lane;
-        int64_t row = a.n <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)a.d) : i / a.d;
-        int64_t col = i - row * a.d;
-        float f[8], r[8];
-        int64_t iy[8];
+        // elements W (32 j + lane) .. of the run: bits W lane % 8 .. of the block that lane
+        // (32 j + lane) W / 8 drew
+        auto bits_of = [&](int j) {
+            return __shfl_sync(0xffffffffu, m, 4 * W * j + lane * W / 8) >> (lane * W & 7);
+        };
+        auto one = [&](Raw<T, W> qx, Raw<T, W> qr, uint32_t bits) {
+            float f[W], r[W];
+            to_f32<T, W>(qx, f);
+            to_f32<T, W>(qr, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] = r[j] = 0.f;
-            iy[j] = -1;
-            if (i < a.n) {
-                f[j] = load_f32(x + row * a.ldx + col);
-                if (res != nullptr) r[j] = load_f32(res + row * a.ldr + col);
-                iy[j] = row * a.ldy + col;
-            }
-            i += 32;
-            col += 32;
+            for (int e = 0; e < W; ++e) f[e] = apply(a, (bits >> e) & 1, f[e], r[e]);
+            return from_f32<T, W>(f);
+        };
+        Raw<T, W> fx[N], fr[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) fr[j] = 0;
+        if (col0 + 256 <= a.d) {
+            // the run lies in one row: accesses at fixed distances
+            const int64_t col = col0 + lane * W;
+            const Raw<T, W> *px = reinterpret_cast<const Raw<T, W> *>(x + row * a.ldx + col);
+            const Raw<T, W> *pr = reinterpret_cast<const Raw<T, W> *>(res + row * a.ldr + col);
+            Raw<T, W> *py = reinterpret_cast<Raw<T, W> *>(y + row * a.ldy + col);
+#pragma unroll
+            for (int j = 0; j < N; ++j) fx[j] = px[32 * j];
+            if (res != nullptr)
+#pragma unroll
+                for (int j = 0; j < N; ++j) fr[j] = pr[32 * j];
+#pragma unroll
+            for (int j = 0; j < N; ++j) py[32 * j] = one(fx[j], fr[j], bits_of(j));
+            continue;
+        }
+        int64_t i = i0 + lane * W, col = col0 + lane * W, at[N];
+        int64_t ix = row * a.ldx + col, ir = row * a.ldr + col, iy = row * a.ldy + col;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
             while (col >= a.d) {
                 col -= a.d;
-                ++row;
+                ix += a.ldx - a.d;
+                ir += a.ldr - a.d;
+                iy += a.ldy - a.d;
             }
+            at[j] = -1;
+            if (i < a.n) {
+                at[j] = iy;
+                fx[j] = *reinterpret_cast<const Raw<T, W> *>(x + ix);
+                if (res != nullptr) fr[j] = *reinterpret_cast<const Raw<T, W> *>(res + ir);
+            }
+            i += 32 * W;
+            col += 32 * W;
+            ix += 32 * W;
+            ir += 32 * W;
+            iy += 32 * W;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // element 32 j + lane of the run: bit lane % 8 of block 4 j + lane / 8
-            const uint32_t bits = __shfl_sync(0xffffffffu, m, 4 * j + (lane >> 3));
-            if (iy[j] >= 0) store_f32(y + iy[j], apply(a, (bits >> (lane & 7)) & 1, f[j], r[j]));
+        for (int j = 0; j < N; ++j) {
+            const uint32_t bits = bits_of(j);
+            if (at[j] >= 0) *reinterpret_cast<Raw<T, W> *>(y + at[j]) = one(fx[j], fr[j], bits);
         }
     }
 }
@@ -186,7 +224,10 @@ cudaError_t launch_type(DropArgs a, int64_t T_rows, cudaStream_t s) {
     }
     const int64_t blocks = ((a.n + 255) / 256 + kThreads / 32 - 1) / (kThreads / 32);
     const dim3 grid((unsigned)std::min<int64_t>(blocks, max_blocks));
-    return launch_k(dropout_elem_kernel<T>, grid, dim3(kThreads), 0, s, a);
+    if constexpr (sizeof(T) == 2)
+        if ((ptrs & 3) == 0 && a.d % 2 == 0 && (rows & 3) == 0)
+            return launch_k(dropout_elem_kernel<T, 2>, grid, dim3(kThreads), 0, s, a);
+    return launch_k(dropout_elem_kernel<T, 1>, grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
