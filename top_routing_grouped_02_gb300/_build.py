@@ -57,8 +57,8 @@ def _native_compile(src: str, obj: str) -> list[str]:
 
 def _native_link(obj: str, out: str) -> list[str]:
     _, lib = _torch_dirs()
-    return ["g++", "-shared", obj, "-o", out, f"-L{PKG}", "-l:libmoe.so", f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
-            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    return ["g++", "-shared", obj, "-o", out, f"-L{PKG}", "-l:libmoe.so", f"-L{lib}", "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

@@ -6,9 +6,12 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <c10/cuda/CUDAStream.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
 
 #include "moe.h"
 
@@ -55,14 +58,31 @@ int type_of(const at::Tensor &t) {
     }
 }
 
-void *stream_of(PyObject *o, const at::Tensor &t) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-    PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
-    if (v == nullptr) throw Refused();
-    const uint64_t s = PyLong_AsUnsignedLongLongMask(v);
-    Py_DECREF(v);
-    if (PyErr_Occurred()) throw Refused();
-    return reinterpret_cast<void *>(s);
+// The call's stream, and torch's current one while the call lasts: what the call
+// allocates (outputs, scratch) then comes from this stream's memory, which no pending
+// work of another stream still uses or will be given before the call's kernels are done.
+struct OnStream {
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    cudaStream_t s;
+    OnStream(PyObject *o, const at::Tensor &t) {
+        if (!t.is_cuda()) refuse(PyExc_ValueError, "%s must be a CUDA tensor", "the first tensor");
+        const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(t.get_device());
+        s = now.stream();
+        if (o == Py_None) return;
+        PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
+        if (v == nullptr) throw Refused();
+        const uint64_t h = PyLong_AsUnsignedLongLongMask(v);
+        Py_DECREF(v);
+        if (PyErr_Occurred()) throw Refused();
+        if (reinterpret_cast<cudaStream_t>(h) == s) return;
+        s = reinterpret_cast<cudaStream_t>(h);
+        guard.emplace(c10::cuda::getStreamFromExternal(s, t.get_device()));
+    }
+    operator void *() const { return s; }
+};
+
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor &like) {
+    return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
 // A tensor seen as a matrix of rows along its last dimension: contiguous, or 2-D with
@@ -94,7 +114,7 @@ Rows rows_of(const at::Tensor &t, const char *name, const at::Tensor *like = nul
 }
 // An output: `o`, or a new contiguous tensor like x.
 at::Tensor output(PyObject *o, const at::Tensor &x, const char *name) {
-    return o == Py_None ? at::empty(x.sizes(), x.options()) : tensor(o, name);
+    return o == Py_None ? fresh(x.sizes(), x.scalar_type(), x) : tensor(o, name);
 }
 void *vec_of(const at::Tensor &t, int64_t d, const at::Tensor &x, const char *name) {
     if (!t.defined()) return nullptr;
@@ -155,6 +175,7 @@ PyObject *layernorm(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor x = tensor(a[0], "x");
     const at::Tensor gamma = optional_tensor(a[1], "gamma"), beta = optional_tensor(a[2], "beta");
     const Rows rx = rows_of(x, "x");
+    const OnStream stream(a[6], x);
     const double eps = number(a[3]);
     const bool stats = PyObject_IsTrue(a[4]) == 1;
     void *pg = vec_of(gamma, rx.d, x, "gamma"), *pb = vec_of(beta, rx.d, x, "beta");
@@ -165,15 +186,15 @@ PyObject *layernorm(PyObject *const *a, Py_ssize_t n) {
     at::Tensor mean, rstd;
     if (stats) {
         const auto sizes = x.sizes().slice(0, x.dim() - 1);
-        mean = at::empty(sizes, x.options().dtype(at::kFloat));
-        rstd = at::empty(sizes, x.options().dtype(at::kFloat));
+        mean = fresh(sizes, at::kFloat, x);
+        rstd = fresh(sizes, at::kFloat, x);
     }
     check("moe_layernorm_forward",
           moe_layernorm_forward(rx.p, rx.ld, pg, pb, rx.T, (int)rx.d, (float)eps, dtype(x),
                                 dtype(pg != nullptr ? gamma : pb != nullptr ? beta : x), ry.p, ry.ld,
                                 stats ? static_cast<float *>(mean.data_ptr()) : nullptr,
                                 stats ? static_cast<float *>(rstd.data_ptr()) : nullptr,
-                                stream_of(a[6], x)));
+                                stream));
     return stats ? wrap_all(y, mean, rstd) : wrap(y);
 }
 
@@ -184,6 +205,7 @@ PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor gamma = optional_tensor(a[2], "gamma"), mean = tensor(a[3], "mean"),
                      rstd = tensor(a[4], "rstd"), dres = optional_tensor(a[5], "dres");
     const Rows rx = rows_of(x, "x"), rdy = rows_of(dy, "dy", &x);
+    const OnStream stream(a[9], x);
     Rows rr{};
     if (dres.defined()) rr = rows_of(dres, "dres", &x);
     void *pg = vec_of(gamma, rx.d, x, "gamma");
@@ -193,19 +215,18 @@ PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
     const at::ScalarType wt = gamma.defined()               ? gamma.scalar_type()
                               : PyObject_IsTrue(a[6]) == 1 ? at::kFloat
                                                             : x.scalar_type();
-    const at::Tensor dgamma = at::empty({rx.d}, x.options().dtype(wt));
-    const at::Tensor dbeta = at::empty({rx.d}, x.options().dtype(wt));
+    const at::Tensor dgamma = fresh({rx.d}, wt, x);
+    const at::Tensor dbeta = fresh({rx.d}, wt, x);
     const at::Tensor scratch =
         a[8] != Py_None ? tensor(a[8], "scratch")
-                        : at::empty({(int64_t)moe_layernorm_scratch_bytes(rx.T, (int)rx.d)},
-                                    x.options().dtype(at::kByte));
+                        : fresh({(int64_t)moe_layernorm_scratch_bytes(rx.T, (int)rx.d)}, at::kByte, x);
     if (!scratch.is_cuda() || !scratch.is_contiguous())
         refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor", "scratch");
     check("moe_layernorm_backward",
           moe_layernorm_backward(rdy.p, rdy.ld, rx.p, rx.ld, pg, pm, pr, rr.p, rr.ld, rx.T, (int)rx.d,
                                  dtype(x), dtype(dgamma), rdx.p, rdx.ld, dgamma.data_ptr(),
                                  dbeta.data_ptr(), scratch.data_ptr(), scratch.nbytes(),
-                                 stream_of(a[9], x)));
+                                 stream));
     return wrap_all(dx, dgamma, dbeta);
 }
 
@@ -215,6 +236,7 @@ PyObject *dropout(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor x = tensor(a[0], "x"), res = optional_tensor(a[4], "residual"),
                      ctr = optional_tensor(a[5], "offset_dev");
     const Rows rx = rows_of(x, "x");
+    const OnStream stream(a[7], x);
     const double p = number(a[1]);
     const uint64_t seed = word(a[2]), offset = word(a[3]);
     Rows rr{};
@@ -223,7 +245,7 @@ PyObject *dropout(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor y = output(a[6], x, "y");
     const Rows ry = rows_of(y, "y", &x);
     check("moe_dropout", moe_dropout(rx.p, rx.ld, rr.p, rr.ld, rx.T, (int)rx.d, p, seed, offset, pc,
-                                     dtype(x), ry.p, ry.ld, stream_of(a[7], x)));
+                                     dtype(x), ry.p, ry.ld, stream));
     return wrap(y);
 }
 
@@ -232,6 +254,7 @@ PyObject *dropout_backward(PyObject *const *a, Py_ssize_t n) {
     expect(n, 7);
     const at::Tensor dy = tensor(a[0], "dy"), ctr = optional_tensor(a[4], "offset_dev");
     const Rows r = rows_of(dy, "dy");
+    const OnStream stream(a[6], dy);
     const double p = number(a[1]);
     const uint64_t seed = word(a[2]), offset = word(a[3]);
     const uint64_t *pc = counter_of(ctr);
@@ -239,7 +262,7 @@ PyObject *dropout_backward(PyObject *const *a, Py_ssize_t n) {
     const Rows rdx = rows_of(dx, "dx", &dy);
     check("moe_dropout_backward",
           moe_dropout_backward(r.p, r.ld, r.T, (int)r.d, p, seed, offset, pc, dtype(dy), rdx.p, rdx.ld,
-                               stream_of(a[6], dy)));
+                               stream));
     return wrap(dx);
 }
 
@@ -277,11 +300,12 @@ Ffn ffn_args(PyObject *x, PyObject *W1, PyObject *W3, PyObject *W2, PyObject *ws
 PyObject *ffn(PyObject *const *a, Py_ssize_t n) {
     expect(n, 8);
     const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5]);
+    const OnStream stream(a[7], f.x);
     const at::Tensor Y = output(a[6], f.x, "Y");
     void *py = dense(Y, f.x.sizes(), f.type, "Y");
     check("moe_ffn_forward",
           moe_ffn_forward(f.px, f.p1, f.p3, f.p2, f.T, f.d, f.n, (moe_act_t)integer(a[4]), dtype(f.x), py,
-                          f.pws, f.ws.nbytes(), stream_of(a[7], f.x)));
+                          f.pws, f.ws.nbytes(), stream));
     return wrap(Y);
 }
 
@@ -289,16 +313,17 @@ PyObject *ffn(PyObject *const *a, Py_ssize_t n) {
 PyObject *ffn_train(PyObject *const *a, Py_ssize_t n) {
     expect(n, 7);
     const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5]);
-    const at::Tensor Y = at::empty(f.x.sizes(), f.x.options());
-    const at::Tensor H = at::empty({f.T, f.n}, f.x.options());
+    const OnStream stream(a[6], f.x);
+    const at::Tensor Y = fresh(f.x.sizes(), f.type, f.x);
+    const at::Tensor H = fresh({f.T, f.n}, f.type, f.x);
     const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
-    const at::Tensor A1 = at::empty({saved}, f.x.options().dtype(at::kFloat));
-    const at::Tensor A3 = at::empty({saved}, f.x.options().dtype(at::kFloat));
+    const at::Tensor A1 = fresh({saved}, at::kFloat, f.x);
+    const at::Tensor A3 = fresh({saved}, at::kFloat, f.x);
     check("moe_ffn_forward_train",
           moe_ffn_forward_train(f.px, f.p1, f.p3, f.p2, f.T, f.d, f.n, (moe_act_t)integer(a[4]),
                                 dtype(f.x), Y.data_ptr(), H.data_ptr(),
                                 static_cast<float *>(A1.data_ptr()), static_cast<float *>(A3.data_ptr()),
-                                f.pws, f.ws.nbytes(), stream_of(a[6], f.x)));
+                                f.pws, f.ws.nbytes(), stream));
     return wrap_all(Y, H, A1, A3);
 }
 
@@ -306,6 +331,7 @@ PyObject *ffn_train(PyObject *const *a, Py_ssize_t n) {
 PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
     expect(n, 13);
     const Ffn f = ffn_args(a[1], a[2], a[3], a[4], a[11]);
+    const OnStream stream(a[12], f.x);
     const at::Tensor dY = tensor(a[0], "dY"), H = tensor(a[5], "H"), A1 = tensor(a[6], "A1"),
                      A3 = tensor(a[7], "A3");
     const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
@@ -313,18 +339,18 @@ PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
     const float *pa1 = static_cast<float *>(dense(A1, {saved}, at::kFloat, "A1"));
     const float *pa3 = static_cast<float *>(dense(A3, {saved}, at::kFloat, "A3"));
     at::Tensor dX, dW1, dW3, dW2;
-    if (PyObject_IsTrue(a[9]) == 1) dX = at::empty(f.x.sizes(), f.x.options());
+    if (PyObject_IsTrue(a[9]) == 1) dX = fresh(f.x.sizes(), f.type, f.x);
     const bool dw = PyObject_IsTrue(a[10]) == 1;
     if (dw) {
-        dW1 = at::empty({f.d, f.n}, f.x.options());
-        dW3 = at::empty({f.d, f.n}, f.x.options());
-        dW2 = at::empty({f.n, f.d}, f.x.options());
+        dW1 = fresh({f.d, f.n}, f.type, f.x);
+        dW3 = fresh({f.d, f.n}, f.type, f.x);
+        dW2 = fresh({f.n, f.d}, f.type, f.x);
     }
     check("moe_ffn_backward",
           moe_ffn_backward(pdy, f.px, f.p1, f.p3, f.p2, ph, pa1, pa3, f.T, f.d, f.n,
                            (moe_act_t)integer(a[8]), dtype(f.x), dX.defined() ? dX.data_ptr() : nullptr,
                            dw ? dW1.data_ptr() : nullptr, dw ? dW3.data_ptr() : nullptr,
-                           dw ? dW2.data_ptr() : nullptr, f.pws, f.ws.nbytes(), stream_of(a[12], f.x)));
+                           dw ? dW2.data_ptr() : nullptr, f.pws, f.ws.nbytes(), stream));
     return wrap_all(dX, dW1, dW3, dW2);
 }
 

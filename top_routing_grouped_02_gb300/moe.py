@@ -639,7 +639,8 @@ def ffn_workspace(T: int, d: int, n: int, train: bool = False, device=None, stre
         raise ValueError("invalid feed-forward shape")
     if device is not None and torch.device(device).type != "cuda":
         raise ValueError("the workspace lies on a CUDA device")
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    with torch.cuda.stream(stream):  # its memory, as a temporary's reuse follows that order
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
     _check("moe_ffn_workspace_init", lib().moe_ffn_workspace_init(
         ws.data_ptr(), nbytes, _stream(stream)))
     return ws
