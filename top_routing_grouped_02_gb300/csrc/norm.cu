@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
             if (a.mean != nullptr) a.mean[row] = mean;
             if (a.rstd != nullptr) a.rstd[row] = rstd;
         }
-    }    if (SHIFT && t == 0) ptx::bulk_wait_group<0>();
+    }
+    if (SHIFT && t == 0) ptx::bulk_wait_group<0>();
 }
 
 template <typename T, int V, int NV, bool SHIFT>
