@@ -57,11 +57,11 @@ def forward(h, p, K, drop, seed, step, ws):
                                            ws=ws["moe"])
     Z = moe.moe_gemm_down(H, p["W2"], w.view(-1), g["perm_slot"], g["offsets"], T, K, ws=ws["moe"])
     routed = moe.moe_combine(Z, g["row_of_slot"], K)
-    shared, S, B1, B3 = moe.moe_ffn_train(u, p["V1"], p["V3"], p["V2"], ws=ws["ffn"])
+    shared, S, F1, F3 = moe.moe_ffn_train(u, p["V1"], p["V3"], p["V2"], ws=ws["ffn"])
     y = moe.moe_dropout(routed, drop, seed, 2 * step, residual=h)
     y = moe.moe_dropout(shared, drop, seed, 2 * step + 1, residual=y, y=y)
     return y, dict(h=h, u=u, mean=mean, rstd=rstd, logits=logits, idx=idx, w=w, g=g, H=H, A1=A1,
-                   A3=A3, S=S, B1=B1, B3=B3)
+                   A3=A3, S=S, F1=F1, F3=F3)
 
 
 def backward(dy, s, p, K, drop, seed, step, ws):
@@ -69,8 +69,8 @@ def backward(dy, s, p, K, drop, seed, step, ws):
     g, u = s["g"], s["u"]
     drouted = moe.moe_dropout_backward(dy, drop, seed, 2 * step)
     dshared = moe.moe_dropout_backward(dy, drop, seed, 2 * step + 1)
-    du_s, dV1, dV3, dV2 = moe.moe_ffn_backward(dshared, u, p["V1"], p["V3"], p["V2"], s["S"], s["B1"],
-                                               s["B3"], ws=ws["ffn"])
+    du_s, dV1, dV3, dV2 = moe.moe_ffn_backward(dshared, u, p["V1"], p["V3"], p["V2"], s["S"], s["F1"],
+                                               s["F3"], ws=ws["ffn"])
     w = s["w"].view(-1)
     dA1, dA3, dS = moe.moe_backward_dh(drouted, p["W2"], s["A1"], s["A3"], w, g["perm_token"],
                                        g["perm_slot"], g["offsets"], K, ws=ws["moe"])

@@ -560,26 +560,26 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
                              int d, int n, moe_act_t act, moe_dtype_t type, void *Y, void *ws,
                              size_t ws_bytes, void *stream);
 
-/* Y and what the backward takes: H [T,n] of `type` and the pre-activations A1, A3 in
- * fp32, each a buffer of moe_ffn_saved_floats(T, n) floats (16-byte aligned) in blocks
- * of 32 tokens x 32 columns: element (t, j) lies at float
+/* Y and what the backward takes: H [T,n] of `type` and the factors
+ * F1 = A3 act'(A1) and F3 = act(A1) in fp32, each a buffer of moe_ffn_saved_floats(T, n)
+ * floats (16-byte aligned) in blocks of 32 tokens x 32 columns: element (t, j) lies at float
  *   ((t / 32) * ceil(n / 32) + j / 32) * 1024 + (j % 32) / 4 * 128 + (t % 32) * 4 + j % 4
  * (what lies in the blocks past T and n is not defined). ws: a workspace for training.
  * Two kernels. */
 size_t moe_ffn_saved_floats(int T, int n);
 moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
                                    int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
-                                   void *H, float *A1, float *A3, void *ws, size_t ws_bytes,
+                                   void *H, float *F1, float *F3, void *ws, size_t ws_bytes,
                                    void *stream);
 
-/* The gradients, with G = dY W2^T, dA1 = G A3 act'(A1), dA3 = G act(A1):
+/* The gradients, with G = dY W2^T, dA1 = G F1, dA3 = G F3:
  *   dX = dA1 W1^T + dA3 W3^T, dW1 = X^T dA1, dW3 = X^T dA3, dW2 = H^T dY
  * all of `type`, each rounded once after an fp32 sum (dA1 and dA3 are rounded to
  * `type` as operands). dX may be NULL; dW1, dW3 and dW2 are all given or all NULL.
- * T = 0 gives zero weight gradients. ws: a workspace for training. Three kernels
+ * act: the forward's (F1 and F3 hold it). T = 0 gives zero weight gradients. ws: a workspace for training. Three kernels
  * (one fewer without dX, or without the weight gradients). Deterministic. */
 moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
-                              const void *W2, const void *H, const float *A1, const float *A3,
+                              const void *W2, const void *H, const float *F1, const float *F3,
                               int T, int d, int n, moe_act_t act, moe_dtype_t type, void *dX,
                               void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
                               void *stream);

@@ -317,27 +317,27 @@ PyObject *ffn_train(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor Y = fresh(f.x.sizes(), f.type, f.x);
     const at::Tensor H = fresh({f.T, f.n}, f.type, f.x);
     const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
-    const at::Tensor A1 = fresh({saved}, at::kFloat, f.x);
-    const at::Tensor A3 = fresh({saved}, at::kFloat, f.x);
+    const at::Tensor F1 = fresh({saved}, at::kFloat, f.x);
+    const at::Tensor F3 = fresh({saved}, at::kFloat, f.x);
     check("moe_ffn_forward_train",
           moe_ffn_forward_train(f.px, f.p1, f.p3, f.p2, f.T, f.d, f.n, (moe_act_t)integer(a[4]),
                                 dtype(f.x), Y.data_ptr(), H.data_ptr(),
-                                static_cast<float *>(A1.data_ptr()), static_cast<float *>(A3.data_ptr()),
+                                static_cast<float *>(F1.data_ptr()), static_cast<float *>(F3.data_ptr()),
                                 f.pws, f.ws.nbytes(), stream));
-    return wrap_all(Y, H, A1, A3);
+    return wrap_all(Y, H, F1, F3);
 }
 
-// dY, x, W1, W3, W2, H, A1, A3, act, need_dx, need_dw, ws, stream
+// dY, x, W1, W3, W2, H, F1, F3, act, need_dx, need_dw, ws, stream
 PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
     expect(n, 13);
     const Ffn f = ffn_args(a[1], a[2], a[3], a[4], a[11]);
     const OnStream stream(a[12], f.x);
-    const at::Tensor dY = tensor(a[0], "dY"), H = tensor(a[5], "H"), A1 = tensor(a[6], "A1"),
-                     A3 = tensor(a[7], "A3");
+    const at::Tensor dY = tensor(a[0], "dY"), H = tensor(a[5], "H"), F1 = tensor(a[6], "F1"),
+                     F3 = tensor(a[7], "F3");
     const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
     void *pdy = dense(dY, f.x.sizes(), f.type, "dY"), *ph = dense(H, {f.T, f.n}, f.type, "H");
-    const float *pa1 = static_cast<float *>(dense(A1, {saved}, at::kFloat, "A1"));
-    const float *pa3 = static_cast<float *>(dense(A3, {saved}, at::kFloat, "A3"));
+    const float *pf1 = static_cast<float *>(dense(F1, {saved}, at::kFloat, "F1"));
+    const float *pf3 = static_cast<float *>(dense(F3, {saved}, at::kFloat, "F3"));
     at::Tensor dX, dW1, dW3, dW2;
     if (PyObject_IsTrue(a[9]) == 1) dX = fresh(f.x.sizes(), f.type, f.x);
     const bool dw = PyObject_IsTrue(a[10]) == 1;
@@ -347,7 +347,7 @@ PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
         dW2 = fresh({f.n, f.d}, f.type, f.x);
     }
     check("moe_ffn_backward",
-          moe_ffn_backward(pdy, f.px, f.p1, f.p3, f.p2, ph, pa1, pa3, f.T, f.d, f.n,
+          moe_ffn_backward(pdy, f.px, f.p1, f.p3, f.p2, ph, pf1, pf3, f.T, f.d, f.n,
                            (moe_act_t)integer(a[8]), dtype(f.x), dX.defined() ? dX.data_ptr() : nullptr,
                            dw ? dW1.data_ptr() : nullptr, dw ? dW3.data_ptr() : nullptr,
                            dw ? dW2.data_ptr() : nullptr, f.pws, f.ws.nbytes(), stream));

@@ -220,11 +220,11 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
 
 moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
                                    int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
-                                   void *H, float *A1, float *A3, void *ws, size_t ws_bytes,
+                                   void *H, float *F1, float *F3, void *ws, size_t ws_bytes,
                                    void *stream) {
     moe_status_t st = check_ffn(T, d, n, act, type);
     if (st != MOE_OK || T == 0) return st;
-    if (!all_aligned16({X, W1, W3, W2, Y, H, A1, A3})) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({X, W1, W3, W2, Y, H, F1, F3})) return MOE_ERR_INVALID_ARG;
     if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, true)) != MOE_OK) return st;
     if ((st = check_arch()) != MOE_OK) return st;
     uint32_t *err = static_cast<uint32_t *>(ws);
@@ -232,13 +232,13 @@ moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3
     float4 *part = reinterpret_cast<float4 *>(at(ws, ffn_ws(T, d, n, true).part));
     const bool f16 = type == MOE_DTYPE_F16;
     cudaStream_t s = as_stream(stream);
-    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, H, A1, A3, part, ticket, err, s);
+    cudaError_t e = launch_ffn_gate(X, W1, W3, T, d, n, act, f16, H, F1, F3, part, ticket, err, s);
     if (e == cudaSuccess) e = launch_ffn_down(H, W2, T, d, n, f16, Y, part, ticket, err, s);
     return from_cuda(e);
 }
 
 moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
-                              const void *W2, const void *H, const float *A1, const float *A3,
+                              const void *W2, const void *H, const float *F1, const float *F3,
                               int T, int d, int n, moe_act_t act, moe_dtype_t type, void *dX,
                               void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
                               void *stream) {
@@ -247,7 +247,7 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
     const int given = (dW1 != nullptr) + (dW3 != nullptr) + (dW2 != nullptr);
     if (given != 0 && (given != 3 || !all_aligned16({dW1, dW3, dW2}))) return MOE_ERR_INVALID_ARG;
     if (T > 0) {
-        if (!all_aligned16({dY, X, W1, W3, W2, H, A1, A3}) || !aligned(dX, 16))
+        if (!all_aligned16({dY, X, W1, W3, W2, H, F1, F3}) || !aligned(dX, 16))
             return MOE_ERR_INVALID_ARG;
         if ((st = check_ffn_ws(ws, ws_bytes, T, d, n, true)) != MOE_OK) return st;
     }
@@ -260,7 +260,7 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
         return from_cuda(e);
     }
     const FfnWs w = ffn_ws(T, d, n, true);
-    return from_cuda(launch_ffn_backward(dY, X, W1, W3, W2, H, A1, A3, T, d, n, act,
+    return from_cuda(launch_ffn_backward(dY, X, W1, W3, W2, H, F1, F3, T, d, n,
                                          type == MOE_DTYPE_F16, at(ws, w.da1), at(ws, w.da3), dX,
                                          dW1, dW3, dW2, reinterpret_cast<float4 *>(at(ws, w.part)),
                                          reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),

@@ -227,8 +227,8 @@ cudaError_t launch_dropout(const void *x, int64_t ldx, const void *res, int64_t 
                            cudaStream_t s);
 
 // Dense gated feed-forward block (ffn.cu: tiled products; ffn_small.cu: few tokens,
-// which stream the weights). f16: fp16, else bf16. A1,
-// A3 of the gate product may be NULL; dX may be NULL, and dW1, dW3, dW2 together.
+// which stream the weights). f16: fp16, else bf16. The factors F1, F3 of the gate product
+// may be NULL; dX may be NULL, and dW1, dW3, dW2 together.
 // The weight-streaming kernel takes up to 32 tokens, and up to 64 where the weights are
 // at most 2^26: it reads each token's values with every 128 columns of weights, which
 // costs large weights more of the SMs' intake than the tiled products' wider tiles.
@@ -252,13 +252,13 @@ cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, con
                               int d, int n, int act, bool f16, void *H, void *Y, float *part,
                               uint32_t *ticket, uint32_t *err, cudaStream_t s);
 cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
-                            int act, bool f16, void *H, float *A1, float *A3, float4 *part,
+                            int act, bool f16, void *H, float *F1, float *F3, float4 *part,
                             uint32_t *ticket, uint32_t *err, cudaStream_t s);
 cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, bool f16, void *Y,
                             float4 *part, uint32_t *ticket, uint32_t *err, cudaStream_t s);
 cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
-                                const void *W2, const void *H, const float *A1, const float *A3,
-                                int T, int d, int n, int act, bool f16, void *dA1, void *dA3,
+                                const void *W2, const void *H, const float *F1, const float *F3,
+                                int T, int d, int n, bool f16, void *dA1, void *dA3,
                                 void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
                                 uint32_t *ticket, uint32_t *err, cudaStream_t s);
 

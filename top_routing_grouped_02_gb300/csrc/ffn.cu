@@ -1,7 +1,7 @@
 // Dense gated feed-forward block on the 5th-generation tensor cores, forward and
 // backward:
 //   A1 = X W1, A3 = X W3, H = act(A1) * A3, Y = H W2
-//   G = dY W2^T, dA1 = G A3 act'(A1), dA3 = G act(A1)
+//   G = dY W2^T, dA1 = G F1, dA3 = G F3, where F1 = A3 act'(A1), F3 = act(A1)
 //   dX = dA1 W1^T + dA3 W3^T, dW1 = X^T dA1, dW3 = X^T dA3, dW2 = H^T dY
 // X, Y [T,d], W1, W3 [d,n], W2 [n,d], all 16 bits; accumulation in fp32.
 //
@@ -28,8 +28,9 @@
 // outside a tensor give zeros, which add nothing, and stores outside write nothing.
 //
 // The backward's operands dA1, dA3 and the forward's H are rounded to 16 bits
-// because the tensor cores multiply 16-bit operands; A1 and A3 are kept in fp32
-// for the backward (in blocks, see pre_block) so that dA1 and dA3 carry one rounding each and not three.
+// because the tensor cores multiply 16-bit operands. The factors F1 and F3 are made by
+// the forward, where the sigmoid is at hand, and kept in fp32 (in blocks, see
+// saved_block), so that dA1 and dA3 carry one rounding each and not three.
 //
 // Warps: 0 TMA producer, 1 MMA issuer (even CTA), 2 TMEM allocation, 4-11 epilogue
 // (two warps per quadrant of 32 TMEM lanes, splitting the columns). Waits are
@@ -74,9 +75,9 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint
 
 namespace {
 
-// kGate: H (and, for training, A1, A3) from X, W1, W3. kDown: Y from H, W2.
-// kDHid: dA1, dA3 from dY, W2 (K-major: its rows are the output columns) and A1,
-// A3. kDX: dX, one reduction over dA1 W1^T then dA3 W3^T (K-major weights).
+// kGate: H (and, for training, F1, F3) from X, W1, W3. kDown: Y from H, W2.
+// kDHid: dA1, dA3 from dY, W2 (K-major: its rows are the output columns) and F1,
+// F3. kDX: dX, one reduction over dA1 W1^T then dA3 W3^T (K-major weights).
 // kWGrad: dW1, dW3, dW2 in one launch, both operands MN-major, reduction over T.
 enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4 };
 
@@ -114,19 +115,19 @@ struct Args {
     int kb, kb_half;     // k-blocks; kDX: those of its first half
     uint32_t idesc;
     int f16, act;
-    float *a1, *a3;      // pre-activations in blocks (pre_block): kGate stores them, or
+    float *f1, *f3;      // the factors in blocks (saved_block): kGate stores them, or
                          // NULL; kDHid reads them
     float4 *part;        // [segment][CTA][warp][kPartVecs]
     uint32_t *ticket;    // [cut][CTA][warp]
     uint32_t *err;
 };
 
-// The pre-activations A1, A3 [T, n] fp32 in blocks of 32 x 32: lane r of an epilogue
+// The factors F1, F3 [T, n] fp32 in blocks of 32 x 32: lane r of an epilogue
 // warp holds row r of a block, so that a block is 8 x 32 vectors of four columns, and
 // a warp stores and loads 512 consecutive bytes an instruction. (As rows, each
 // instruction touches 32 lines, and the 16 loads of a block took as long as the main
 // loop of a short reduction.)
-__device__ __forceinline__ float4 *pre_block(float *a, int n, int row, int col, int lane) {
+__device__ __forceinline__ float4 *saved_block(float *a, int n, int row, int col, int lane) {
     const int64_t block = (int64_t)(row / 32) * ((n + 31) / 32) + col / 32;
     return reinterpret_cast<float4 *>(a) + block * 256 + lane;
 }
@@ -383,20 +384,20 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             const Unit un = unit_at(u);
             const int rows = args.rows[un.p], cols = args.cols[un.p];
             const int y0 = un.row0 + q * 32;
-            // kDHid: this row's A1, A3 of a chunk, loaded while the one before is stored
+            // kDHid: this row's factors of a chunk, loaded while the one before is stored
             float4 x1[8] = {}, x3[8] = {};
-            auto load_pre = [&](int c) {
+            auto load_factors = [&](int c) {
                 const int x0 = un.nb * kCols + c * 32;
                 if (c >= hi || y0 >= rows || x0 >= cols) return;
-                const float4 *p1 = pre_block(args.a1, cols, y0, x0, lane);
-                const float4 *p3 = pre_block(args.a3, cols, y0, x0, lane);
+                const float4 *p1 = saved_block(args.f1, cols, y0, x0, lane);
+                const float4 *p3 = saved_block(args.f3, cols, y0, x0, lane);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     x1[i] = __ldg(p1 + i * 32);
                     x3[i] = __ldg(p3 + i * 32);
                 }
             };
-            if constexpr (MODE == kDHid) load_pre(lo);
+            if constexpr (MODE == kDHid) load_factors(lo);
             if (!ready()) return false;
             // blk: 32-column block of the tile as the accumulator holds it
             auto load = [&](int blk, int own, uint32_t (&v)[32]) {
@@ -411,26 +412,33 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     uint32_t g[32], v[32], o[16];
                     load(c, own, g);
                     load(BN / 64 + c, NC + own, v);
+                    const bool train = args.f1 != nullptr;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float h[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const float ga = __uint_as_float(g[2 * i + j]);
-                            h[j] = ga * act_sigmoid(ga, args.act) * __uint_as_float(v[2 * i + j]);
+                            const float a1 = __uint_as_float(g[2 * i + j]);
+                            const float a3 = __uint_as_float(v[2 * i + j]);
+                            const float sg = act_sigmoid(a1, args.act);
+                            h[j] = a1 * sg * a3;
+                            if (train) {  // v: F1, g: F3
+                                v[2 * i + j] = __float_as_uint(a3 * act_grad(a1, sg, args.act));
+                                g[2 * i + j] = __float_as_uint(a1 * sg);
+                            }
                         }
                         o[i] = pack(h[0], h[1], f16);
                     }
                     if (in) store_box(o, x0, y0, &maps.o[0]);
-                    if (in && args.a1 != nullptr) {
-                        float4 *p1 = pre_block(args.a1, cols, y0, x0, lane);
-                        float4 *p3 = pre_block(args.a3, cols, y0, x0, lane);
+                    if (in && train) {
+                        float4 *p1 = saved_block(args.f1, cols, y0, x0, lane);
+                        float4 *p3 = saved_block(args.f3, cols, y0, x0, lane);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            p1[i * 32] = make_float4(__uint_as_float(g[4 * i]), __uint_as_float(g[4 * i + 1]),
-                                                     __uint_as_float(g[4 * i + 2]), __uint_as_float(g[4 * i + 3]));
-                            p3[i * 32] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                            p1[i * 32] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                                                      __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                            p3[i * 32] = make_float4(__uint_as_float(g[4 * i]), __uint_as_float(g[4 * i + 1]),
+                                                     __uint_as_float(g[4 * i + 2]), __uint_as_float(g[4 * i + 3]));
                         }
                     }
                 } else if constexpr (MODE == kDHid) {
@@ -441,17 +449,14 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         float r1[2], r3[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const float a1 = (&x1[i >> 1].x)[2 * (i & 1) + j];
-                            const float a3 = (&x3[i >> 1].x)[2 * (i & 1) + j];
                             const float gv = __uint_as_float(g[2 * i + j]);
-                            const float sg = act_sigmoid(a1, args.act);
-                            r1[j] = gv * a3 * act_grad(a1, sg, args.act);
-                            r3[j] = gv * (a1 * sg);
+                            r1[j] = gv * (&x1[i >> 1].x)[2 * (i & 1) + j];
+                            r3[j] = gv * (&x3[i >> 1].x)[2 * (i & 1) + j];
                         }
                         o1[i] = pack(r1[0], r1[1], f16);
                         o3[i] = pack(r3[0], r3[1], f16);
                     }
-                    load_pre(c + 1);
+                    load_factors(c + 1);
                     if (in) {
                         store_box(o1, x0, y0, &maps.o[0]);
                         store_box(o3, x0, y0, &maps.o[1]);
@@ -604,7 +609,7 @@ size_t ffn_dense_part_bytes() {
 }
 
 cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T, int d, int n,
-                            int act, bool f16, void *H, float *A1, float *A3, float4 *part,
+                            int act, bool f16, void *H, float *F1, float *F3, float4 *part,
                             uint32_t *ticket, uint32_t *err, cudaStream_t s) {
     Maps m{};
     if (!map_a(&m.a[0], f16, X, d, T) || !map_64(&m.b[0], f16, W1, n, d) ||
@@ -616,8 +621,8 @@ cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T
     a.kb = (d + BK - 1) / BK;
     a.f16 = f16;
     a.act = act;
-    a.a1 = A1;
-    a.a3 = A3;
+    a.f1 = F1;
+    a.f3 = F3;
     a.part = part;
     a.ticket = ticket;
     a.err = err;
@@ -642,8 +647,8 @@ cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, 
 }
 
 cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,
-                                const void *W2, const void *H, const float *A1, const float *A3,
-                                int T, int d, int n, int act, bool f16, void *dA1, void *dA3,
+                                const void *W2, const void *H, const float *F1, const float *F3,
+                                int T, int d, int n, bool f16, void *dA1, void *dA3,
                                 void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
                                 uint32_t *ticket, uint32_t *err, cudaStream_t s) {
     Maps m{};
@@ -655,9 +660,8 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
     a.cols[0] = n;
     a.kb = (d + BK - 1) / BK;
     a.f16 = f16;
-    a.act = act;
-    a.a1 = const_cast<float *>(A1);
-    a.a3 = const_cast<float *>(A3);
+    a.f1 = const_cast<float *>(F1);
+    a.f3 = const_cast<float *>(F3);
     a.part = part;
     a.ticket = ticket;
     a.err = err;

@@ -668,14 +668,14 @@ def moe_ffn(x, W1, W3, W2, act: str = "silu", ws=None, Y=None, stream=None):
 
 
 def moe_ffn_train(x, W1, W3, W2, act: str = "silu", ws=None, stream=None):
-    """(Y, H, A1, A3): moe_ffn's Y and what moe_ffn_backward takes (A1, A3: fp32 in the
+    """(Y, H, F1, F3): moe_ffn's Y and what moe_ffn_backward takes (F1, F3: fp32 in the
     blocks that moe.h describes). ws: ffn_workspace(..., train=True)."""
     return _native().ffn_train(x, W1, W3, W2, _act(act), _ffn_ws(ws, x, W1, True, stream), stream)
 
 
-def moe_ffn_backward(dY, x, W1, W3, W2, H, A1, A3, act: str = "silu", need_dx: bool = True,
+def moe_ffn_backward(dY, x, W1, W3, W2, H, F1, F3, act: str = "silu", need_dx: bool = True,
                      need_dw: bool = True, ws=None, stream=None):
     """(dX, dW1, dW3, dW2) of moe_ffn_train, all of x's type (None where not asked
     for). ws: ffn_workspace(..., train=True)."""
-    return _native().ffn_backward(dY, x, W1, W3, W2, H, A1, A3, _act(act), need_dx, need_dw,
+    return _native().ffn_backward(dY, x, W1, W3, W2, H, F1, F3, _act(act), need_dx, need_dw,
                                   _ffn_ws(ws, x, W1, True, stream), stream)
