@@ -186,3 +186,20 @@ def test_argument_checks():
         moe.moe_ffn(x, W1, W3, W2, "tanh")
     with pytest.raises(moe.MoeError):
         moe.moe_ffn(x, W1, W3, W2, ws=torch.zeros(1024, dtype=torch.uint8, device="cuda"))
+
+
+def test_one_workspace_for_cut_tiles_of_many_shapes():
+    # tiles that few pairs would take are cut; their join counters are back at zero after
+    # each call, also where the rows of some warps lie outside
+    ws = moe.ffn_workspace(2000, 1024, 4096, train=True)
+    for T, d, n in [(1906, 184, 1824), (66, 216, 4096), (300, 1024, 512), (130, 1024, 1024), (66, 216, 4096),
+                    (257, 520, 2056), (1906, 184, 1824)]:
+        x, W1, W3, W2, dY = make(T, d, n, BF, T)
+        want = None
+        for w in (None, ws, ws):
+            out = moe.moe_ffn_train(x, W1, W3, W2, "gelu", w)
+            got = (out[0], out[1]) + moe.moe_ffn_backward(dY, x, W1, W3, W2, *out[1:], "gelu", ws=w)
+            if want is None:
+                want = got
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (T, d, n)
+    assert moe.moe_sync_check(ws)[0] == 0

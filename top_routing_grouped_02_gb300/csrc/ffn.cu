@@ -37,6 +37,7 @@
 // bounded; a wait that gives up flags the error word, its role stops, and loads and
 // MMAs in flight are drained before the CTA leaves.
 #include <algorithm>
+#include <type_traits>
 
 #include "ffn.cuh"
 
@@ -84,6 +85,7 @@ enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4 };
 constexpr int BM = 128;  // rows per CTA
 constexpr int BK = 64;   // reduction depth per stage: 128 bytes of 16-bit elements
 constexpr int kEpiWarps = 8;
+constexpr int kShares = kEpiWarps / 4;  // warps of one quadrant share the columns
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = BM * BK * 2;  // 16 KB
 constexpr uint32_t kBox = 64 * 64 * 2;     // 8 KB: 64 x 64 elements
@@ -99,8 +101,13 @@ constexpr uint32_t kStageBytes = kABytes + kBoxes * kBox;
 constexpr int kStages = 6;                   // 192 KB
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes +
                          (size_t)kEpiWarps * kEpiBufs * kEpiBuf + 256;
-// Vectors (float4) of one warp's part: BN / 2 columns of 32 rows.
-constexpr int kPartVecs = BN / 2 * 32 / 4;
+// Vectors (float4) of one warp's part: its columns of 32 rows.
+constexpr int kPartVecs = BN / kShares * 32 / 4;
+
+// Up to this many segments a cut tile is joined in boxes of 32 columns, which leave by
+// TMA; more, four columns at a time, so that all holders have a share and eight segments
+// are in flight (24 segments, 66 tokens: 20.4 -> 14.8 us; three, 3133 tokens: 19.7 -> 25.4).
+constexpr int kFewSegments = 4;
 
 struct Maps {
     CUtensorMap a[3], b[3], o[3];
@@ -115,6 +122,7 @@ struct Args {
     int kb, kb_half;     // k-blocks; kDX: those of its first half
     uint32_t idesc;
     int f16, act;
+    void *out[3];        // the outputs of each problem (kDHid: both of its one)
     float *f1, *f3;      // the factors in blocks (saved_block): kGate stores them, or
                          // NULL; kDHid reads them
     float4 *part;        // [segment][CTA][warp][kPartVecs]
@@ -130,6 +138,29 @@ struct Args {
 __device__ __forceinline__ float4 *saved_block(float *a, int n, int row, int col, int lane) {
     const int64_t block = (int64_t)(row / 32) * ((n + 31) / 32) + col / 32;
     return reinterpret_cast<float4 *>(a) + block * 256 + lane;
+}
+
+// Two neighbouring words as a pair of fp32 values, and back.
+__device__ __forceinline__ f32x2 word_pair(const uint32_t *w) {
+    return pair(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
+__device__ __forceinline__ void put_pair(f32x2 p, uint32_t *w) {
+    float x, y;
+    unpair(p, x, y);
+    w[0] = __float_as_uint(x);
+    w[1] = __float_as_uint(y);
+}
+
+__device__ __forceinline__ f32x2 pair2(const float *f) { return pair(f[0], f[1]); }
+__device__ __forceinline__ float4 pairs_float4(f32x2 a, f32x2 b) {
+    float4 r;
+    unpair(a, r.x, r.y);
+    unpair(b, r.z, r.w);
+    return r;
+}
+__device__ __forceinline__ float4 words_float4(const uint32_t *w) {
+    return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]),
+                       __uint_as_float(w[3]));
 }
 
 struct Ctl {
@@ -310,13 +341,13 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         bounded_wait(ptx::smem_addr(&ctl->drain), 0, args.err);
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
-        const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+        const int ew = warp - 4, q = warp & 3, share = ew >> 2;
         const uint32_t buf0 = base + (uint32_t)S * kStageBytes + (uint32_t)ew * kEpiBufs * kEpiBuf;
         const uint32_t tempty0 = ptx::mapa(ptx::smem_addr(&ctl->tempty[0]), 0);
         const bool f16 = args.f16 != 0;
         uint32_t groups = 0, uc = 0;
-        // 32 rows x 64 bytes through a staging buffer (64-byte swizzle) and a TMA
-        // store at (x, y), skipped where the whole box lies outside
+        // 32 rows x 64 bytes through a staging buffer (64-byte swizzle) and a TMA store at
+        // (x, y)
         auto store_box = [&](const uint32_t (&v)[16], int x, int y, const CUtensorMap *map) {
             const uint32_t buf = buf0 + (groups % kEpiBufs) * kEpiBuf;
             if (lane == 0 && groups >= (uint32_t)kEpiBufs) ptx::bulk_wait_group_read<kEpiBufs - 1>();
@@ -334,38 +365,37 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             ++groups;
         };
         constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // output columns of a tile
-        constexpr int NC = kCols / 64;                      // 32-column chunks of a warp
-        const int c_lo = half * NC;
-        // this warp's part of pair p's segment, at this lane
+        constexpr int NC = kCols / kShares / 32;            // 32-column chunks of a warp
+        const int c_lo = share * NC;
+        // A cut tile. A warp's part is kPartVecs / 32 vectors of four columns x 32 rows; a
+        // unit of the join is such a vector (kGate: of W1's sums and of W3's). Each warp
+        // writes its part, but for the units that it joins itself: its pair's share, which
+        // goes round the warps where there are more segments than units.
+        constexpr int M = MODE == kGate ? 2 : 1, NU = kPartVecs / 32 / M;
         auto part_of = [&](int p) {
             return args.part + (((int64_t)p * 2 + rank) * kEpiWarps + ew) * kPartVecs + lane;
         };
-        // a part's vectors of 32 columns starting at block blk (of 32 columns)
-        auto put = [&](float4 *p, int blk, const uint32_t (&v)[32]) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                __stcg(p + (blk * 8 + i) * 32,
-                       make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                   __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+        // the accumulator's column of vector v of this warp's part
+        auto column = [&](int v) {
+            return MODE == kGate ? (v / NU) * (BN / 2) + share * NU * 4 + v % NU * 4 : share * NU * 4 + v * 4;
         };
-        // 32 columns of this pair's cut tile from its segments, in their order, this
-        // pair's own from its accumulator; blk: their block in the parts, col: in the
-        // accumulator
-        auto gather = [&](int blk, uint32_t taddr, int col, uint32_t (&v)[32]) {
+        // 32 columns of this pair's cut tile from its segments, in their order, this pair's
+        // own from its accumulator (column col); v0: their first vector in the parts
+        auto gather = [&](int v0, uint32_t taddr, int col, uint32_t (&v)[32]) {
             float s[32] = {};
             const int p0 = pair - pair % args.split;
 #pragma unroll 1
             for (int p = p0; p < p0 + args.split; ++p) {
                 if (p == pair) {
-                    ptx::tmem_ld32(taddr + col * 32, v);
+                    ptx::tmem_ld32(taddr + col, v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(v[i]);
                     continue;
                 }
-                const float4 *src = part_of(p);
+                const float4 *src = part_of(p) + v0 * 32;
                 float4 q[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q[i] = __ldcg(src + (blk * 8 + i) * 32);
+                for (int i = 0; i < 8; ++i) q[i] = __ldcg(src + i * 32);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     s[4 * i] += q[i].x;
@@ -379,16 +409,18 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         };
         // The chunks [lo, hi) of this warp's columns of a tile to the outputs: from the
         // accumulator at taddr alone, or joined from the tile's segments. ready(): waits for
-        // either. False if that gave up.
-        auto finish = [&](int u, int lo, int hi, uint32_t taddr, bool joined, auto ready) {
-            const Unit un = unit_at(u);
+        // either; release(): called after the last read of the accumulator.
+        auto finish = [&](const Unit &un, int lo, int hi, uint32_t taddr, bool joined, auto ready,
+                          auto release) {
             const int rows = args.rows[un.p], cols = args.cols[un.p];
             const int y0 = un.row0 + q * 32;
+            // chunks that are not all outside
+            hi = y0 < rows ? min(hi, (cols - un.nb * kCols + 31) / 32) : 0;
             // kDHid: this row's factors of a chunk, loaded while the one before is stored
             float4 x1[8] = {}, x3[8] = {};
             auto load_factors = [&](int c) {
+                if (c >= hi) return;
                 const int x0 = un.nb * kCols + c * 32;
-                if (c >= hi || y0 >= rows || x0 >= cols) return;
                 const float4 *p1 = saved_block(args.f1, cols, y0, x0, lane);
                 const float4 *p3 = saved_block(args.f3, cols, y0, x0, lane);
 #pragma unroll
@@ -399,38 +431,43 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
             };
             if constexpr (MODE == kDHid) load_factors(lo);
             if (!ready()) return false;
-            // blk: 32-column block of the tile as the accumulator holds it
-            auto load = [&](int blk, int own, uint32_t (&v)[32]) {
-                if (joined) gather(own, taddr, blk, v);
-                else ptx::tmem_ld32(taddr + blk * 32, v);
+            if (lo >= hi) release();
+            // m: W1's sums or (kGate) W3's
+            auto load = [&](int c, int m, uint32_t (&v)[32]) {
+                const int col = m * (BN / 2) + c * 32;
+                if (joined) gather(m * NU + (c - c_lo) * 8, taddr, col, v);
+                else ptx::tmem_ld32(taddr + col, v);
             };
 #pragma unroll 1
             for (int c = lo; c < hi; ++c) {
-                const int x0 = un.nb * kCols + c * 32, own = c - c_lo;
-                const bool in = y0 < rows && x0 < cols;
+                const int x0 = un.nb * kCols + c * 32;
                 if constexpr (MODE == kGate) {
                     uint32_t g[32], v[32], o[16];
-                    load(c, own, g);
-                    load(BN / 64 + c, NC + own, v);
+                    load(c, 0, g);
+                    load(c, 1, v);
+                    if (c == hi - 1) release();
                     const bool train = args.f1 != nullptr;
+                    auto chunk = [&](auto gelu, auto saves) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float h[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float a1 = __uint_as_float(g[2 * i + j]);
-                            const float a3 = __uint_as_float(v[2 * i + j]);
-                            const float sg = act_sigmoid(a1, args.act);
-                            h[j] = a1 * sg * a3;
-                            if (train) {  // v: F1, g: F3
-                                v[2 * i + j] = __float_as_uint(a3 * act_grad(a1, sg, args.act));
-                                g[2 * i + j] = __float_as_uint(a1 * sg);
+                        for (int i = 0; i < 16; ++i) {
+                            f32x2 h, f1 = 0, f3;
+                            activate<gelu(), saves()>(word_pair(g + 2 * i), word_pair(v + 2 * i), h, f1, f3);
+                            float x, y;
+                            unpair(h, x, y);
+                            o[i] = pack(x, y, f16);
+                            if (saves()) {
+                                put_pair(f1, v + 2 * i);
+                                put_pair(f3, g + 2 * i);
                             }
                         }
-                        o[i] = pack(h[0], h[1], f16);
-                    }
-                    if (in) store_box(o, x0, y0, &maps.o[0]);
-                    if (in && train) {
+                    };
+                    using yes = std::true_type;
+                    using no = std::false_type;
+                    if (args.act == MOE_ACT_SILU) train ? chunk(no(), yes()) : chunk(no(), no());
+                    else train ? chunk(yes(), yes()) : chunk(yes(), no());
+                    // v: F1, g: F3
+                    store_box(o, x0, y0, &maps.o[0]);
+                    if (train) {
                         float4 *p1 = saved_block(args.f1, cols, y0, x0, lane);
                         float4 *p3 = saved_block(args.f3, cols, y0, x0, lane);
 #pragma unroll
@@ -443,88 +480,194 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     }
                 } else if constexpr (MODE == kDHid) {
                     uint32_t g[32], o1[16], o3[16];
-                    load(c, own, g);
+                    load(c, 0, g);
+                    if (c == hi - 1) release();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float r1[2], r3[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float gv = __uint_as_float(g[2 * i + j]);
-                            r1[j] = gv * (&x1[i >> 1].x)[2 * (i & 1) + j];
-                            r3[j] = gv * (&x3[i >> 1].x)[2 * (i & 1) + j];
-                        }
-                        o1[i] = pack(r1[0], r1[1], f16);
-                        o3[i] = pack(r3[0], r3[1], f16);
+                        const float *r1 = &x1[i >> 1].x + 2 * (i & 1), *r3 = &x3[i >> 1].x + 2 * (i & 1);
+                        const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+                        o1[i] = pack(g0 * r1[0], g1 * r1[1], f16);
+                        o3[i] = pack(g0 * r3[0], g1 * r3[1], f16);
                     }
                     load_factors(c + 1);
-                    if (in) {
-                        store_box(o1, x0, y0, &maps.o[0]);
-                        store_box(o3, x0, y0, &maps.o[1]);
-                    }
+                    store_box(o1, x0, y0, &maps.o[0]);
+                    store_box(o3, x0, y0, &maps.o[1]);
                 } else {
                     uint32_t v[32], o[16];
-                    load(c, own, v);
+                    load(c, 0, v);
+                    if (c == hi - 1) release();
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         o[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
-                    if (in) store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
+                    store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
                 }
             }
             return true;
         };
 
+        // The join of many segments: units [lo, hi), one after the other, each the sum of its
+        // segments in their order, eight in flight.
+        auto join = [&](const Unit &un, uint32_t taddr, int lo, int hi) {
+            constexpr int U = 1, P = 8;
+            const int rows = args.rows[un.p], cols = args.cols[un.p];
+            const int y = un.row0 + q * 32, x_lo = un.nb * kCols + share * NU * 4;
+            const int p0 = pair - pair % args.split;
+            hi = min(hi, (cols - x_lo + 3) / 4);
+#pragma unroll 1
+            for (int u0 = lo; u0 < hi; u0 += U) {
+                [[maybe_unused]] float4 f1[U] = {}, f3[U] = {};
+                auto saved = [&](float *f, int u) {
+                    const int x = x_lo + u * 4;
+                    return saved_block(f, cols, y, x, lane) + (x & 31) / 4 * 32;
+                };
+                if constexpr (MODE == kDHid) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (u0 + u < hi) {
+                            f1[u] = __ldg(saved(args.f1, u0 + u));
+                            f3[u] = __ldg(saved(args.f3, u0 + u));
+                        }
+                }
+                float s[U][M][4] = {};
+#pragma unroll 1
+                for (int pb = 0; pb < args.split; pb += P) {
+                    float4 v[P][U][M];
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int m = 0; m < M; ++m)
+                                v[k][u][m] = pb + k < args.split && p0 + pb + k != pair && u0 + u < hi
+                                                 ? __ldcg(part_of(p0 + pb + k) + (m * NU + u0 + u) * 32)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int mine = pair - p0 - pb;
+                    if (mine >= 0 && mine < P) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int m = 0; m < M; ++m) {
+                                if (u0 + u >= hi) continue;
+                                uint32_t r[4];
+                                tmem_ld4(taddr + column(m * NU + u0 + u), r);
+#pragma unroll
+                                for (int k = 0; k < P; ++k)
+                                    if (k == mine) v[k][u][m] = words_float4(r);
+                            }
+                    }
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int m = 0; m < M; ++m) {
+                                s[u][m][0] += v[k][u][m].x;
+                                s[u][m][1] += v[k][u][m].y;
+                                s[u][m][2] += v[k][u][m].z;
+                                s[u][m][3] += v[k][u][m].w;
+                            }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u0 + u >= hi || y + lane >= rows) continue;
+                    const int64_t at = (int64_t)(y + lane) * cols + x_lo + (u0 + u) * 4;
+                    auto store = [&](int k, f32x2 lo2, f32x2 hi2) {
+                        float a, b, c, d;
+                        unpair(lo2, a, b);
+                        unpair(hi2, c, d);
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(args.out[k]) + at) =
+                            make_uint2(pack(a, b, f16), pack(c, d, f16));
+                    };
+                    f32x2 lo2 = pair2(s[u][0]), hi2 = pair2(s[u][0] + 2);
+                    if constexpr (MODE == kGate) {
+                        const f32x2 lo3 = pair2(s[u][1]), hi3 = pair2(s[u][1] + 2);
+                        f32x2 h[2], g1[2], g3[2];
+                        if (args.act == MOE_ACT_SILU) {
+                            activate<false, true>(lo2, lo3, h[0], g1[0], g3[0]);
+                            activate<false, true>(hi2, hi3, h[1], g1[1], g3[1]);
+                        } else {
+                            activate<true, true>(lo2, lo3, h[0], g1[0], g3[0]);
+                            activate<true, true>(hi2, hi3, h[1], g1[1], g3[1]);
+                        }
+                        store(0, h[0], h[1]);
+                        if (args.f1 != nullptr) {
+                            *saved(args.f1, u0 + u) = pairs_float4(g1[0], g1[1]);
+                            *saved(args.f3, u0 + u) = pairs_float4(g3[0], g3[1]);
+                        }
+                    } else if constexpr (MODE == kDHid) {
+                        store(0, mul2(lo2, pair2(&f1[u].x)), mul2(hi2, pair2(&f1[u].z)));
+                        store(1, mul2(lo2, pair2(&f3[u].x)), mul2(hi2, pair2(&f3[u].z)));
+                    } else {
+                        store(un.p, lo2, hi2);
+                    }
+                }
+                __syncwarp();
+            }
+        };
+
         // the pair's segment and its join, then the whole tiles
-        Work w(args, pair, pairs);
-        const int j = args.split > 0 ? pair % args.split : 0;
-        const int lo = args.split > 0 ? NC * j / args.split : 0;
-        const int hi = args.split > 0 ? NC * (j + 1) / args.split : 0;  // its share of a cut tile
-        while (w.step()) {
+        for (Work w(args, pair, pairs); w.step(); ++uc) {
             const uint32_t a = uc & 1u;
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * BN;
-            uint32_t *ticket = args.ticket + ((int64_t)w.u * 2 + rank) * kEpiWarps + ew;
+            const Unit un = unit_at(w.u);
             auto filled = [&] {
                 if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (uc >> 1) & 1u, args.err)) return false;
                 ptx::tc_fence_after();
                 return true;
             };
-            const bool joining = w.cut;
-            if (joining) {
-                if (!filled()) break;
-                float4 *p = part_of(pair);
-#pragma unroll 1
-                for (int c = 0; c < BN / 64; ++c) {
-                    const int own = MODE == kGate && c >= NC ? c - NC : c;
-                    if (own >= lo && own < hi) continue;
-                    uint32_t v[32];
-                    ptx::tmem_ld32(taddr + ((MODE == kGate && c >= NC ? BN / 64 : 0) + c_lo + own) * 32, v);
-                    put(p, c, v);
-                }
-                __threadfence();
+            auto release = [&] {
+                ptx::tc_fence_before();
                 __syncwarp();
-                // low half: parts written; high half: holders that need them no more (one
-                // with no share of the columns needs none of them)
-                if (lane == 0) atomicAdd(ticket, hi > lo ? 1u : 0x10001u);
+                if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
+            };
+            if (!w.cut) {
+                if (!finish(un, c_lo, c_lo + NC, taddr, false, filled, release)) break;
+                continue;
             }
-            if (!joining || hi > lo) {
-                auto ready = [&] {
-                    if (!joining) return filled();
+            if (!filled()) break;
+            uint32_t *ticket = args.ticket + ((int64_t)w.u * 2 + rank) * kEpiWarps + ew;
+            const int j = (pair + share) % args.split;
+            const bool few = args.split <= kFewSegments;
+            const int step = few ? 8 : 1;  // units of its share come in boxes of 8, or singly
+            const int lo = NU / step * j / args.split * step, hi = NU / step * (j + 1) / args.split * step;
+            float4 *mine = part_of(pair);
+            if (un.row0 + q * 32 >= args.rows[un.p]) {  // nothing to join, in any of its segments
+                release();
+                continue;
+            }
+#pragma unroll 1
+            for (int v0 = 0; v0 < M * NU; v0 += 8) {
+                uint32_t r[32];
+                ptx::tmem_ld32(taddr + column(v0), r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int u = (v0 + i) % NU;
+                    if (u < lo || u >= hi) __stcg(mine + (v0 + i) * 32, words_float4(r + 4 * i));
+                }
+            }
+            __threadfence();
+            __syncwarp();
+            // low half: parts written; high half: holders that need them no more (one with
+            // no units needs none of them)
+            if (lane == 0) atomicAdd(ticket, hi > lo ? 1u : 0x10001u);
+            if (hi > lo) {
+                auto joinable = [&] {
                     bool all = true;
                     if (lane == 0) all = word_wait(ticket, 0xffffu, (uint32_t)args.split, args.err);
                     return __shfl_sync(0xffffffffu, all, 0) != 0;
                 };
-                if (!finish(w.u, joining ? c_lo + lo : c_lo, joining ? c_lo + hi : c_lo + NC, taddr,
-                            joining, ready))
-                    break;
+                if (few) {
+                    if (!finish(un, c_lo + lo / 8, c_lo + hi / 8, taddr, true, joinable, [] {})) break;
+                } else {
+                    if (!joinable()) break;
+                    join(un, taddr, lo, hi);
+                }
                 // every lane has its parts; the last holder returns the ticket to zero
                 __syncwarp();
-                if (joining && lane == 0 &&
-                    atomicAdd(ticket, 0x10000u) >> 16 == (uint32_t)(args.split - 1))
+                if (lane == 0 && atomicAdd(ticket, 0x10000u) >> 16 == (uint32_t)(args.split - 1))
                     *ticket = 0;
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(tempty0 + a * (uint32_t)sizeof(uint64_t));
-            ++uc;
+            release();
         }
         if (lane == 0) ptx::bulk_wait_group<0>();
         __syncwarp();
@@ -621,6 +764,7 @@ cudaError_t launch_ffn_gate(const void *X, const void *W1, const void *W3, int T
     a.kb = (d + BK - 1) / BK;
     a.f16 = f16;
     a.act = act;
+    a.out[0] = H;
     a.f1 = F1;
     a.f3 = F3;
     a.part = part;
@@ -640,6 +784,7 @@ cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, 
     a.cols[0] = d;
     a.kb = (n + BK - 1) / BK;
     a.f16 = f16;
+    a.out[0] = Y;
     a.part = part;
     a.ticket = ticket;
     a.err = err;
@@ -660,6 +805,8 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
     a.cols[0] = n;
     a.kb = (d + BK - 1) / BK;
     a.f16 = f16;
+    a.out[0] = dA1;
+    a.out[1] = dA3;
     a.f1 = const_cast<float *>(F1);
     a.f3 = const_cast<float *>(F3);
     a.part = part;
@@ -675,6 +822,7 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
         a.cols[0] = d;
         a.kb_half = (n + BK - 1) / BK;
         a.kb = 2 * a.kb_half;
+        a.out[0] = dX;
         if ((e = launch<kDX>(m, a, s)) != cudaSuccess) return e;
     }
     if (dW1 == nullptr) return cudaSuccess;
@@ -687,6 +835,9 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
     a.rows[0] = a.rows[1] = a.cols[2] = d;
     a.cols[0] = a.cols[1] = a.rows[2] = n;
     a.kb = (T + BK - 1) / BK;
+    a.out[0] = dW1;
+    a.out[1] = dW3;
+    a.out[2] = dW2;
     return launch<kWGrad>(m, a, s);
 }
 

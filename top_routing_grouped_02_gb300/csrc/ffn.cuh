@@ -51,6 +51,16 @@ __device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint
     }
 }
 
+// Four columns.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Both activations are a * sigmoid(z(a)): SiLU with z = a, GELU's tanh form
 // 0.5 a (1 + tanh(u)) = a sigmoid(2 u) with z = 2 u = k (a + 0.044715 a^3),
 // k = 2 sqrt(2 / pi). sg: the sigmoid.
@@ -58,10 +68,41 @@ __device__ __forceinline__ float act_sigmoid(float a, int act) {
     const float z = act == MOE_ACT_SILU ? a : 1.5957691216f * fmaf(0.044715f * a * a, a, a);
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
-// Derivative sg + a sg (1 - sg) z'(a).
-__device__ __forceinline__ float act_grad(float a, float sg, int act) {
-    const float dz = act == MOE_ACT_SILU ? 1.0f : 1.5957691216f * fmaf(3.0f * 0.044715f * a, a, 1.0f);
-    return sg * fmaf(a * (1.0f - sg), dz, 1.0f);
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// For a pair of elements: h = act(a1) a3, f3 = act(a1) and (TRAIN) f1 = a3 act'(a1),
+//   act' = sg + a sg (1 - sg) z'(a).
+// Packed, with the sigmoid as 1 / (1 + 2^(-z log2 e)) and the branch on the activation
+// outside: an epilogue whose tile has a short reduction is bound by its instructions.
+template <bool GELU, bool TRAIN>
+__device__ __forceinline__ void activate(f32x2 a1, f32x2 a3, f32x2 &h, f32x2 &f1, f32x2 &f3) {
+    constexpr float kLog2e = 1.44269504f, kZ = 1.5957691216f, kCube = 0.044715f;
+    f32x2 t, sq = 0;
+    if (GELU) {
+        sq = mul2(a1, a1);
+        t = mul2(a1, fma2(sq, both(-kLog2e * kZ * kCube), both(-kLog2e * kZ)));
+    } else {
+        t = mul2(a1, both(-kLog2e));
+    }
+    float x, y;
+    unpair(t, x, y);
+    unpair(add2(pair(exp2_approx(x), exp2_approx(y)), both(1.f)), x, y);
+    const f32x2 sg = pair(rcp_approx(x), rcp_approx(y));
+    f3 = mul2(a1, sg);
+    h = mul2(f3, a3);
+    if (TRAIN) {
+        f32x2 u = fma2(sg, both(-1.f), both(1.f));
+        if (GELU) u = mul2(u, fma2(sq, both(3.f * kZ * kCube), both(kZ)));
+        f1 = mul2(a3, fma2(f3, u, sg));
+    }
 }
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi, bool f16) {
