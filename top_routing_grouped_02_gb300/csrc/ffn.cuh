@@ -35,20 +35,27 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
     }
 }
 
-// Polls a word in global memory (acquire) until (word & mask) == want, bounded like
-// bounded_wait.
-__device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint32_t want,
-                                          uint32_t *err) {
-    if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
+// Polls a word in global memory (acquire) until done(word), bounded like bounded_wait.
+template <typename Done>
+__device__ __forceinline__ bool poll_word(const uint32_t *w, uint32_t *err, Done done) {
+    if (done(ptx::ld_acquire_gpu(w))) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
     for (uint32_t spin = 1;; ++spin) {
         __nanosleep(32);
-        if ((ptx::ld_acquire_gpu(w) & mask) == want) return true;
+        if (done(ptx::ld_acquire_gpu(w))) return true;
         if ((spin & 15u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
             atomicOr(err, MOE_DEVERR_TIMEOUT);
             return false;
         }
     }
+}
+// Until (word & mask) == want; until word >= least.
+__device__ __forceinline__ bool word_wait(const uint32_t *w, uint32_t mask, uint32_t want,
+                                          uint32_t *err) {
+    return poll_word(w, err, [=](uint32_t v) { return (v & mask) == want; });
+}
+__device__ __forceinline__ bool word_wait_least(const uint32_t *w, uint32_t least, uint32_t *err) {
+    return poll_word(w, err, [=](uint32_t v) { return v >= least; });
 }
 
 // Four columns.

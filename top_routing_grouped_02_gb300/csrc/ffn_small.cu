@@ -17,8 +17,8 @@
 //
 // The down projection needs all of H: a grid-wide counter separates the products.
 // The rings of all SMs (about 200 KB each) meanwhile fill with W2, which does not
-// depend on H, so HBM stays busy through the joins and the barrier (asking for more
-// of it into L2 measured no faster). All CTAs are
+// depend on H, and once most CTAs are through with the first product, L2 fills with
+// more of it, so HBM stays busy through the joins and the barrier. All CTAs are
 // resident together (one per SM); every wait is bounded. The counters return to
 // zero with the launch.
 //
@@ -40,6 +40,10 @@ constexpr uint32_t kBox = 64 * 64 * 2;    // 8 KB: 64 columns x 64 rows of W
 constexpr uint32_t kMat = 2 * kBox;       // 128 columns
 constexpr uint32_t kWBytes = 2 * kMat;    // weights of one unit
 constexpr int kMaxStages = 6;
+// CTAs (in eighths) that have their part of H before W2 is fetched into L2 beyond the
+// rings, and how many units of it (one token, d = 4096, n = 14336: none 65.3 us, 8 units
+// 64.2, 12 or 16 63.4; the same 12 at six eighths 63.5, 8 at five eighths 64.5).
+constexpr int kAheadNum = 7, kAheadUnits = 12;
 // control words (behind the error word): grid arrivals, exits
 constexpr int kWordGrid = 8, kWordExit = 9;
 
@@ -352,6 +356,19 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
                     load_w((it0 + j) % S, tile, kb);
                     next(tile, kb);
                     ++it;
+                }
+                // Once most CTAs have their part of H, HBM is nearly idle until the last one
+                // has: it fetches the units behind the rings into L2 (earlier, the
+                // CTAs still in the first product lose what that takes).
+                ok = ok && word_wait_least(args.err + kWordGrid, gridDim.x * kAheadNum / 8, args.err);
+                int ptl = tile, pk = kb;
+                for (int j = ahead; j < min(count, ahead + kAheadUnits) && ok; ++j) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        ptx::tma_prefetch_2d(&maps.w[2], ptl * 128, (2 * pk + m) * BK);
+                        ptx::tma_prefetch_2d(&maps.w[2], ptl * 128 + 64, (2 * pk + m) * BK);
+                    }
+                    next(ptl, pk);
                 }
                 ok = ok && word_wait(args.err + kWordGrid, 0xffffffffu, gridDim.x, args.err);
                 ptx::fence_proxy_async_global();
