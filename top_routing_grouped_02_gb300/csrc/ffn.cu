@@ -684,9 +684,12 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
 
 // Which of `units` tiles of kb k-blocks are cut over `pairs` SM pairs: those past the
 // last whole wave, where that is worth a join (about 5 us, the time of kJoin k-blocks,
-// for the 256 x 256 sums of each pair to go through L2). At least kMinRun k-blocks a
-// segment.
-constexpr int kJoin = 14, kMinRun = 8;
+// for the 256 x 256 sums of each pair to go through L2 and for a launch that starts in
+// plain order). At least kMinRun k-blocks a segment. (Over 18 shapes of 66 to 2048
+// tokens, inference / training step: kJoin 8 30.7 / 88.6 us, 14 30.4 / 87.8, 18 29.8 /
+// 86.8, 26 and more slower again; nothing cut 32.7 / 94.7; a cost for each further
+// segment or another kMinRun gained on no average.)
+constexpr int kJoin = 18, kMinRun = 8;
 void split_work(int64_t units, int kb, int pairs, int *cut, int *split) {
     *cut = *split = 0;
     const int64_t rest = units % pairs;
