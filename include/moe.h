@@ -551,7 +551,7 @@ typedef enum {
 size_t moe_ffn_workspace_bytes(int T, int d, int n, int train);
 moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream);
 
-/* Y. Few tokens (up to 32, or 64 with 3 d n <= 2^26) one kernel, which streams the weights, each SM an equal share
+/* Y. Few tokens (up to 48, or 64 with 3 d n <= 2^27) one kernel, which streams the weights, each SM an equal share
  * of them, with H complete on all SMs before the down projection (bounded waits: a
  * CTA that never gets an SM sets MOE_DEVERR_TIMEOUT; initialise the workspace again
  * after that). Otherwise two: gate and up projections, activation and product in

@@ -229,15 +229,15 @@ cudaError_t launch_dropout(const void *x, int64_t ldx, const void *res, int64_t 
 // Dense gated feed-forward block (ffn.cu: tiled products; ffn_small.cu: few tokens,
 // which stream the weights). f16: fp16, else bf16. The factors F1, F3 of the gate product
 // may be NULL; dX may be NULL, and dW1, dW3, dW2 together.
-// The weight-streaming kernel takes up to 32 tokens, and up to 64 where the weights are
-// at most 2^26: it reads each token's values with every 128 columns of weights, which
+// The weight-streaming kernel takes up to 48 tokens, and up to 64 where the weights are
+// at most 2^27: it reads each token's values with every 128 columns of weights, which
 // costs large weights more of the SMs' intake than the tiled products' wider tiles.
-// Measured, streaming against tiled, in us: 4096 x 14336 17 tokens 71 / 75, 32: 76 / 75,
-// 48: 81 / 76, 64: 88 / 76; 7168 x 2048 32: 33 / 41, 64: 38 / 41, 96: 44 / 42; 1024 x 1024
-// 64: 16 / 20.
+// Measured, streaming against tiled, in us: 4096 x 14336 16 tokens 70 / 75, 40: 75 / 77,
+// 48: 76.5 / 76.6, 64: 80 / 77; 8192 x 4096 64: 54.4 / 54.9; 7168 x 2048 16: 31 / 37, 64:
+// 35 / 38; 1024 x 1024 64: 18.5 / 19.9.
 constexpr int kFfnStreamTokens = 64;
 inline bool ffn_streams(int T, int d, int n) {
-    return T <= 32 || (T <= kFfnStreamTokens && 3ll * d * n <= (1ll << 26));
+    return T <= 48 || (T <= kFfnStreamTokens && 3ll * d * n <= (1ll << 27));
 }
 constexpr int kFfnMaxCtas = 192;       // of one weight-streaming launch
 constexpr int kFfnMaxWidth = 1 << 20;  // of d and n
