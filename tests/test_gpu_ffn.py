@@ -203,3 +203,42 @@ def test_one_workspace_for_cut_tiles_of_many_shapes():
                 want = got
             assert all(torch.equal(a, b) for a, b in zip(got, want)), (T, d, n)
     assert moe.moe_sync_check(ws)[0] == 0
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,d,n", [(66, 4096, 256), (130, 4096, 200), (66, 216, 4096), (257, 136, 3000),
+                                   (2700, 200, 136), (1906, 184, 1824)])
+def test_tiles_of_many_segments(T, d, n, act, dt):
+    # one or a few tiles and long reductions: five and more segments a tile, in each of the
+    # products, with rows and columns past the tensors
+    x, W1, W3, W2, dY = make(T, d, n, dt, 3)
+    ws = moe.ffn_workspace(T, d, n, train=True)
+    Y, H, F1, F3 = moe.moe_ffn_train(x, W1, W3, W2, act, ws)
+    dX, dW1, dW3, dW2 = moe.moe_ffn_backward(dY, x, W1, W3, W2, H, F1, F3, act, ws=ws)
+    clean(ws)
+    ref = ffn(x, W1, W3, W2, act, dY)
+    for name, got in (("Y", Y), ("dX", dX), ("dW1", dW1), ("dW3", dW3), ("dW2", dW2)):
+        check_ffn(got, ref[name], name)
+    for _ in range(3):  # the order of arrival does not matter
+        again = moe.moe_ffn_backward(dY, x, W1, W3, W2, H, F1, F3, act, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(again, (dX, dW1, dW3, dW2)))
+        assert torch.equal(moe.moe_ffn(x, W1, W3, W2, act, ws), Y)
+
+
+@pytest.mark.parametrize("T", [48, 49, 64])
+def test_forward_at_the_switch_of_large_weights(T):
+    x, W1, W3, W2, _ = make(T, 4096, 11264, BF, 4)
+    Y = moe.moe_ffn(x, W1, W3, W2)
+    check_ffn(Y, ffn(x, W1, W3, W2, "silu")["Y"], "Y")
+
+
+@pytest.mark.parametrize("T,d,n", [(3, 8200, 6088), (40, 8136, 6136)])
+def test_few_tokens_with_ragged_large_weights(T, d, n):
+    # long runs whose last tiles and units end past the weights
+    x, W1, W3, W2, _ = make(T, d, n, BF, 5)
+    ws = moe.ffn_workspace(T, d, n)
+    Y = moe.moe_ffn(x, W1, W3, W2, "gelu", ws)
+    clean(ws)
+    check_ffn(Y, ffn(x, W1, W3, W2, "gelu")["Y"], "Y")
+    assert torch.equal(moe.moe_ffn(x, W1, W3, W2, "gelu", ws), Y)

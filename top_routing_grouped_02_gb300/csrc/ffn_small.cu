@@ -58,7 +58,7 @@ struct Geo {
 
 // One product: out[T, cols] from the reduction over K.
 struct Product {
-    int cols, kbs, tiles, ctas;  // kbs: units per tile
+    int cols, K, kbs, tiles, ctas;  // kbs: units per tile
     void *out;
 };
 
@@ -364,10 +364,11 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
                 int ptl = tile, pk = kb;
                 for (int j = ahead; j < min(count, ahead + kAheadUnits) && ok; ++j) {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        ptx::tma_prefetch_2d(&maps.w[2], ptl * 128, (2 * pk + m) * BK);
-                        ptx::tma_prefetch_2d(&maps.w[2], ptl * 128 + 64, (2 * pk + m) * BK);
-                    }
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int x = ptl * 128; x < ptl * 128 + 128; x += 64)
+                            if (x < p.cols && (2 * pk + m) * BK < p.K)
+                                ptx::tma_prefetch_2d(&maps.w[2], x, (2 * pk + m) * BK);
                     next(ptl, pk);
                 }
                 ok = ok && word_wait(args.err + kWordGrid, 0xffffffffu, gridDim.x, args.err);
@@ -494,6 +495,7 @@ int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 Product make_product(int cols, int K, int depth, int sms, void *out) {
     Product p;
     p.cols = cols;
+    p.K = K;
     p.kbs = (K + depth - 1) / depth;
     p.tiles = (cols + 127) / 128;
     p.ctas = (int)std::min<int64_t>(std::min(sms, kFfnMaxCtas),
