@@ -232,6 +232,7 @@ __device__ __forceinline__ uint32_t fetch_image(uint8_t *img, const T *base, int
     return bytes;
 }
 // The 16 bytes of vector v of a row whose image starts `shift` bytes into img.
+template <typename T>
 __device__ __forceinline__ uint4 image_vec(const uint8_t *img, int v, uint32_t shift) {
     const uint4 a = reinterpret_cast<const uint4 *>(img)[v], b = reinterpret_cast<const uint4 *>(img)[v + 1];
     uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x;
@@ -249,6 +250,7 @@ __device__ __forceinline__ uint4 image_vec(const uint8_t *img, int v, uint32_t s
         w3 = w4;
         w4 = shift & 8 ? b.w : b.y;
     }
+    if (sizeof(T) == 4) return make_uint4(w0, w1, w2, w3);
     const uint32_t bits = (shift & 2) * 8;
     return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits),
                       __funnelshift_r(w2, w3, bits), __funnelshift_r(w3, w4, bits));
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
         for (int i = 0; i < NV; ++i) {
             if constexpr (SHIFT) {
                 const int v = i * tpr + t;
-                uint4 q = ok[i] ? image_vec(stage, v, sx) : make_uint4(0, 0, 0, 0);
+                uint4 q = ok[i] ? image_vec<T>(stage, v, sx) : make_uint4(0, 0, 0, 0);
                 if ((v + 1) * V > a.d) q = first_elems<T>(q, a.d - v * V);
                 to_pairs<T, V>(q, f[i]);
             } else {
@@ -546,16 +548,18 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             return (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + row * ld) & 15;
         };
         const uint32_t sx = shift_of(a.x, a.ldx), sy = shift_of(a.dy, a.lddy), sr = shift_of(a.dres, a.lddres);
-        auto vec_x = [&](int i) { return SHIFT ? image_vec(stage, i * tpr + t, sx) : px[i * tpr]; };
-        auto vec_y = [&](int i) { return SHIFT ? image_vec(stage + row_bytes, i * tpr + t, sy) : py[i * tpr]; };
-        auto vec_r = [&](int i) { return SHIFT ? image_vec(stage + 2 * row_bytes, i * tpr + t, sr) : pr[i * tpr]; };
+        auto vec_x = [&](int i) { return SHIFT ? image_vec<T>(stage, i * tpr + t, sx) : px[i * tpr]; };
+        auto vec_y = [&](int i) { return SHIFT ? image_vec<T>(stage + row_bytes, i * tpr + t, sy) : py[i * tpr]; };
+        auto vec_r = [&](int i) { return SHIFT ? image_vec<T>(stage + 2 * row_bytes, i * tpr + t, sr) : pr[i * tpr]; };
         // xh = x r - m r
         const f32x2 r2 = both(rstd), shift = both(-mean * rstd);
         f32x2 p1 = 0, p2 = 0;
+        constexpr bool KEEP = sizeof(T) == 4;  // x and dy stay in registers (16 bits: too many)
+        f32x2 kx[KEEP ? NV : 1][P2], ky[KEEP ? NV : 1][P2];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!ok[i]) continue;
-            f32x2 x[P2], y[P2], g[P2];
+            f32x2 (&x)[P2] = kx[KEEP ? i : 0], (&y)[P2] = ky[KEEP ? i : 0], g[P2];
             uint4 qx = vec_x(i), qy = vec_y(i);
             if (SHIFT && (i * tpr + t + 1) * V > a.d) {  // what the last vector lacks adds nothing
                 qx = first_elems<T>(qx, a.d - (i * tpr + t) * V);
@@ -597,9 +601,11 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!ok[i]) continue;
-            f32x2 x[P2], y[P2], g[P2];
-            to_pairs<T, V>(vec_x(i), x);
-            to_pairs<T, V>(vec_y(i), y);
+            f32x2 (&x)[P2] = kx[KEEP ? i : 0], (&y)[P2] = ky[KEEP ? i : 0], g[P2];
+            if (!KEEP) {
+                to_pairs<T, V>(vec_x(i), x);
+                to_pairs<T, V>(vec_y(i), y);
+            }
             plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
             for (int j = 0; j < P2; ++j)
