@@ -219,3 +219,17 @@ def test_graph_replay():
     torch.cuda.synchronize()
     for a, b in zip((y, mean, rstd) + grads, want + wd):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,d,ld,dt,wt", [(800, 7167, 7167, BF, FP), (1400, 5001, 5003, HF, HF), (500, 8191, 8194, BF, BF),
+                                          (1200, 3001, 3001, FP, FP), (900, 4093, 4093, FP, FP)])
+def test_wide_unaligned_rows_many_a_group(T, d, ld, dt, wt):
+    # rings of one stage a group, which is used again and again
+    x, gamma, beta, dy, dres = make(T, d, ld, dt, wt, 5)
+    y, mean, rstd = moe.moe_layernorm(x, gamma, beta, EPS, stats=True)
+    check_forward(x, gamma, beta, y, mean, rstd)
+    for res in (None, dres):
+        dx, dgamma, dbeta = moe.moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=res)
+        check_backward(x, gamma, dy, res, dx, dgamma, dbeta)
+        again = moe.moe_layernorm_backward(dy, x, gamma, mean, rstd, dres=res)
+        assert all(torch.equal(a, b) for a, b in zip(again, (dx, dgamma, dbeta)))

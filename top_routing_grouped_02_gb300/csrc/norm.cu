@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             __syncwarp();
         }
         // every thread of the group is done with the previous row's stage
-        if (t < tensors && s_prev >= 0 && row + (S - 1) * stride < a.T)
+        if (!SHIFT && t < tensors && s_prev >= 0 && row + (S - 1) * stride < a.T)
             fetch(row + (S - 1) * stride, s_prev, t);
         if (a.wpr > 1) {
             const float2 o = lane < a.wpr ? ctl->stat[buf][w0 + lane] : make_float2(0.f, 0.f);
@@ -623,6 +623,8 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             ptx::fence_proxy_async_smem();
             if (a.wpr > 1) group_sync(1 + group, tpr);
             else __syncwarp();
+            // every thread of the group is done with this row's stage
+            if (t < tensors && row + S * stride < a.T) fetch(row + S * stride, s, t);
             send_image(image, drow, a.d, t, tpr);
         }
         s_prev = s;
@@ -811,17 +813,21 @@ int row_groups(int wpr, int threads) { return std::max(1, threads / (32 * wpr));
 
 // Row groups and ring stages of a block of at most max_threads threads (one block
 // per SM), with at most T / SMs rounded up groups so that few rows spread over the
-// SMs. False where two stages of one group do not fit the shared memory.
+// SMs. False where `least` stages of one group do not fit the shared memory. (SHIFT fetches
+// a group's next row as soon as all of its threads are done with the last, so one stage
+// will do, and more groups with one beat fewer with two: 8192 x 7167 bf16, one group with
+// two stages against two with one, backward 164 / 133 us; three against four groups,
+// forward 68 / 64. Otherwise a stage is free only at the next row's barrier.)
 constexpr size_t kRingSmem = 224 * 1024;
 // `fixed` bytes a block, `extra` a group, `stage` a stage.
 bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t extra, size_t stage,
-                int *groups) {
+                int least, int *groups) {
     a.wpr = (a.d + per_thread * 32 - 1) / (per_thread * 32);
     if (a.wpr * 32 > max_threads) return false;
     int g = std::min(row_groups(a.wpr, max_threads), a.wpr > 1 ? 15 : kMaxGroups);
     g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
-    while (g > 1 && fixed + g * (extra + 2 * stage) > kRingSmem) --g;
-    if (fixed + g * (extra + 2 * stage) > kRingSmem) return false;
+    while (g > 1 && fixed + g * (extra + least * stage) > kRingSmem) --g;
+    if (fixed + g * (extra + least * stage) > kRingSmem) return false;
     a.stages = (int)std::min<size_t>(((kRingSmem - fixed) / g - extra) / stage, kRingStages);
     *groups = g;
     return true;
@@ -836,7 +842,7 @@ cudaError_t forward_ring(LnArgs a, bool *fits, cudaStream_t s) {
     int groups;
     const size_t stage = SHIFT ? image_bytes(a.d, sizeof(T)) : (size_t)a.d * sizeof(T);
     const size_t fixed = kRingCtl + 2 * plane_bytes<V>(a.d);
-    *fits = ring_shape(a, V * NV, kFwdThreads, fixed, SHIFT ? stage : 0, stage, &groups);
+    *fits = ring_shape(a, V * NV, kFwdThreads, fixed, SHIFT ? stage : 0, stage, SHIFT ? 1 : 2, &groups);
     if (!*fits) return cudaSuccess;
     const cudaError_t e = ensure_dynamic_smem(
         reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV, SHIFT>), (int)kRingSmem);
@@ -851,14 +857,15 @@ cudaError_t backward_ring(LnArgs a, int *P, bool *fits, cudaStream_t s) {
     int groups;
     const size_t row = SHIFT ? image_bytes(a.d, sizeof(T)) : (size_t)a.d * sizeof(T);
     const size_t stage = row * (a.dres != nullptr ? 3 : 2), fixed = kRingCtl + plane_bytes<V>(a.d);
-    *fits = ring_shape(a, V * NV, kBwdRingThreads, fixed, SHIFT ? row : 0, stage, &groups);
+    // (a group's ring holds its [2][d] fp32 sums in the end)
+    const int least = SHIFT && stage + row >= 2 * plane_bytes<V>(a.d) ? 1 : 2;
+    *fits = ring_shape(a, V * NV, kBwdRingThreads, fixed, SHIFT ? row : 0, stage, least, &groups);
     if (!*fits) return cudaSuccess;
     const cudaError_t e = ensure_dynamic_smem(
         reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV, SHIFT>), (int)kRingSmem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(sm_count(), kLnPartials));
     *P = grid;
-    // (two stages of a group hold its [2][d] fp32 sums)
     return launch_k(ln_backward_ring_kernel<T, V, NV, SHIFT>, dim3(grid), dim3(groups * a.wpr * 32),
                     fixed + groups * (a.stages * stage + SHIFT * row), s, a);
 }
