@@ -22,6 +22,11 @@
 // resident together (one per SM); every wait is bounded. The counters return to
 // zero with the launch.
 //
+// Measured: one token, d = 4096, n = 14336 bf16 63.4 us (5.6 TB/s; a kernel that only loads
+// as much reaches 6.05); 48 tokens, 7168 x 2048 fp16 31.6 us, of which the loads need 15:
+// the first product's last sums are in the workspace at 16 us, H is complete at 19.5, the
+// second product's sums at 25 and joined at 29.
+//
 // Warps: 0 TMA producer, 1 MMA issuer, 2 TMEM allocation, 4-11 epilogue.
 #include <algorithm>
 

@@ -8,9 +8,13 @@
 // Both are bound by HBM: the forward reads x and writes y once, the backward
 // reads x, dy (and dres) and writes dx once. A group of warps takes a row at a time
 // from a ring of rows in shared memory, which is filled asynchronously ahead of it.
-// Row statistics: each warp takes the mean and
-// the squared deviations from its own mean of its elements, and the warps'
-// pairs are joined by
+// Measured, 8192 x 7168 bf16: forward 37 us (6.3 TB/s), backward with dres 84 us
+// (5.6 TB/s), the sum of the weights' partials 4.5 us; rows of 7167: 64 and 133 us (106
+// without dres), bound by the shifts' instructions; 4096 x 4096: 16.4, 22 and 4 us, of
+// which some 6, 7 and 3 us are the start and end of each kernel.
+//
+// Row statistics: each warp takes the mean and the squared deviations from its own mean
+// of its elements, and the warps' pairs are joined by
 //   m = sum n_w m_w / d,  M2 = sum (M2_w + n_w (m_w - m)^2),
 // one exchange through shared memory a row, with no subtraction of large equal
 // numbers: a row whose offset is far larger than its spread keeps its variance.
