@@ -513,97 +513,81 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         // The join of many segments: units [lo, hi), one after the other, each the sum of its
         // segments in their order, eight in flight.
         auto join = [&](const Unit &un, uint32_t taddr, int lo, int hi) {
-            constexpr int U = 1, P = 8;
+            constexpr int P = 8;
             const int rows = args.rows[un.p], cols = args.cols[un.p];
             const int y = un.row0 + q * 32, x_lo = un.nb * kCols + share * NU * 4;
             const int p0 = pair - pair % args.split;
             hi = min(hi, (cols - x_lo + 3) / 4);
 #pragma unroll 1
-            for (int u0 = lo; u0 < hi; u0 += U) {
-                [[maybe_unused]] float4 f1[U] = {}, f3[U] = {};
-                auto saved = [&](float *f, int u) {
-                    const int x = x_lo + u * 4;
+            for (int u = lo; u < hi; ++u) {
+                const int x = x_lo + u * 4;
+                auto saved = [&](float *f) {
                     return saved_block(f, cols, y, x, lane) + (x & 31) / 4 * 32;
                 };
+                [[maybe_unused]] float4 f1, f3;
                 if constexpr (MODE == kDHid) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (u0 + u < hi) {
-                            f1[u] = __ldg(saved(args.f1, u0 + u));
-                            f3[u] = __ldg(saved(args.f3, u0 + u));
-                        }
+                    f1 = __ldg(saved(args.f1));
+                    f3 = __ldg(saved(args.f3));
                 }
-                float s[U][M][4] = {};
+                float s[M][4] = {};
 #pragma unroll 1
                 for (int pb = 0; pb < args.split; pb += P) {
-                    float4 v[P][U][M];
+                    float4 v[P][M];
 #pragma unroll
                     for (int k = 0; k < P; ++k)
 #pragma unroll
-                        for (int u = 0; u < U; ++u)
-#pragma unroll
-                            for (int m = 0; m < M; ++m)
-                                v[k][u][m] = pb + k < args.split && p0 + pb + k != pair && u0 + u < hi
-                                                 ? __ldcg(part_of(p0 + pb + k) + (m * NU + u0 + u) * 32)
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-                    const int mine = pair - p0 - pb;
+                        for (int m = 0; m < M; ++m)
+                            v[k][m] = pb + k < args.split && p0 + pb + k != pair
+                                          ? __ldcg(part_of(p0 + pb + k) + (m * NU + u) * 32)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int mine = pair - p0 - pb;  // this pair's own comes from the accumulator
                     if (mine >= 0 && mine < P) {
 #pragma unroll
-                        for (int u = 0; u < U; ++u)
+                        for (int m = 0; m < M; ++m) {
+                            uint32_t r[4];
+                            tmem_ld4(taddr + column(m * NU + u), r);
 #pragma unroll
-                            for (int m = 0; m < M; ++m) {
-                                if (u0 + u >= hi) continue;
-                                uint32_t r[4];
-                                tmem_ld4(taddr + column(m * NU + u0 + u), r);
-#pragma unroll
-                                for (int k = 0; k < P; ++k)
-                                    if (k == mine) v[k][u][m] = words_float4(r);
-                            }
+                            for (int k = 0; k < P; ++k)
+                                if (k == mine) v[k][m] = words_float4(r);
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < P; ++k)
 #pragma unroll
-                        for (int u = 0; u < U; ++u)
-#pragma unroll
-                            for (int m = 0; m < M; ++m) {
-                                s[u][m][0] += v[k][u][m].x;
-                                s[u][m][1] += v[k][u][m].y;
-                                s[u][m][2] += v[k][u][m].z;
-                                s[u][m][3] += v[k][u][m].w;
-                            }
+                        for (int m = 0; m < M; ++m) {
+                            s[m][0] += v[k][m].x;
+                            s[m][1] += v[k][m].y;
+                            s[m][2] += v[k][m].z;
+                            s[m][3] += v[k][m].w;
+                        }
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (u0 + u >= hi || y + lane >= rows) continue;
-                    const int64_t at = (int64_t)(y + lane) * cols + x_lo + (u0 + u) * 4;
-                    auto store = [&](int k, f32x2 lo2, f32x2 hi2) {
-                        float a, b, c, d;
-                        unpair(lo2, a, b);
-                        unpair(hi2, c, d);
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(args.out[k]) + at) =
-                            make_uint2(pack(a, b, f16), pack(c, d, f16));
+                if (y + lane < rows) {
+                    auto store = [&](int k, f32x2 a, f32x2 b) {
+                        const float4 f = pairs_float4(a, b);
+                        uint16_t *out = static_cast<uint16_t *>(args.out[k]) + (int64_t)(y + lane) * cols + x;
+                        *reinterpret_cast<uint2 *>(out) = make_uint2(pack(f.x, f.y, f16), pack(f.z, f.w, f16));
                     };
-                    f32x2 lo2 = pair2(s[u][0]), hi2 = pair2(s[u][0] + 2);
+                    const f32x2 a = pair2(s[0]), b = pair2(s[0] + 2);
                     if constexpr (MODE == kGate) {
-                        const f32x2 lo3 = pair2(s[u][1]), hi3 = pair2(s[u][1] + 2);
+                        const f32x2 a3 = pair2(s[1]), b3 = pair2(s[1] + 2);
                         f32x2 h[2], g1[2], g3[2];
                         if (args.act == MOE_ACT_SILU) {
-                            activate<false, true>(lo2, lo3, h[0], g1[0], g3[0]);
-                            activate<false, true>(hi2, hi3, h[1], g1[1], g3[1]);
+                            activate<false, true>(a, a3, h[0], g1[0], g3[0]);
+                            activate<false, true>(b, b3, h[1], g1[1], g3[1]);
                         } else {
-                            activate<true, true>(lo2, lo3, h[0], g1[0], g3[0]);
-                            activate<true, true>(hi2, hi3, h[1], g1[1], g3[1]);
+                            activate<true, true>(a, a3, h[0], g1[0], g3[0]);
+                            activate<true, true>(b, b3, h[1], g1[1], g3[1]);
                         }
                         store(0, h[0], h[1]);
                         if (args.f1 != nullptr) {
-                            *saved(args.f1, u0 + u) = pairs_float4(g1[0], g1[1]);
-                            *saved(args.f3, u0 + u) = pairs_float4(g3[0], g3[1]);
+                            *saved(args.f1) = pairs_float4(g1[0], g1[1]);
+                            *saved(args.f3) = pairs_float4(g3[0], g3[1]);
                         }
                     } else if constexpr (MODE == kDHid) {
-                        store(0, mul2(lo2, pair2(&f1[u].x)), mul2(hi2, pair2(&f1[u].z)));
-                        store(1, mul2(lo2, pair2(&f3[u].x)), mul2(hi2, pair2(&f3[u].z)));
+                        store(0, mul2(a, pair2(&f1.x)), mul2(b, pair2(&f1.z)));
+                        store(1, mul2(a, pair2(&f3.x)), mul2(b, pair2(&f3.z)));
                     } else {
-                        store(un.p, lo2, hi2);
+                        store(un.p, a, b);
                     }
                 }
                 __syncwarp();
