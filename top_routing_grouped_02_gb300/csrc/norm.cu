@@ -555,10 +555,11 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
         auto vec_x = [&](int i) { return SHIFT ? image_vec<T>(stage, i * tpr + t, sx) : px[i * tpr]; };
         auto vec_y = [&](int i) { return SHIFT ? image_vec<T>(stage + row_bytes, i * tpr + t, sy) : py[i * tpr]; };
         auto vec_r = [&](int i) { return SHIFT ? image_vec<T>(stage + 2 * row_bytes, i * tpr + t, sr) : pr[i * tpr]; };
-        // xh = x r - m r
-        const f32x2 r2 = both(rstd), shift = both(-mean * rstd);
+        // xh = (x - m) r, the difference first: of x r and m r, both far larger where the
+        // row's offset is far above its spread, nothing but rounding would be left
+        const f32x2 r2 = both(rstd), shift = both(-mean);
         f32x2 p1 = 0, p2 = 0;
-        constexpr bool KEEP = sizeof(T) == 4;  // x and dy stay in registers (16 bits: too many)
+        constexpr bool KEEP = sizeof(T) == 4;  // xh and dy stay in registers (16 bits: too many)
         f32x2 kx[KEEP ? NV : 1][P2], ky[KEEP ? NV : 1][P2];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -574,11 +575,12 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
             for (int j = 0; j < P2; ++j) {
-                const f32x2 xh = fma2(x[j], r2, shift), gy = mul2(y[j], g[j]);
+                const f32x2 gy = mul2(y[j], g[j]);
+                x[j] = mul2(add2(x[j], shift), r2);
                 db[i][j] = add2(db[i][j], y[j]);
-                dg[i][j] = fma2(y[j], xh, dg[i][j]);
+                dg[i][j] = fma2(y[j], x[j], dg[i][j]);
                 p2 = add2(p2, gy);
-                p1 = fma2(gy, xh, p1);
+                p1 = fma2(gy, x[j], p1);
             }
         }
         float s1 = warp_sum(pair_sum(p1)), s2 = warp_sum(pair_sum(p2));
@@ -612,8 +614,10 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             }
             plane_pairs<V>(gamma, nvec, i * tpr + t, g);
 #pragma unroll
-            for (int j = 0; j < P2; ++j)
-                x[j] = fma2(fma2(x[j], r2, shift), k1, fma2(mul2(y[j], g[j]), r2, k2));
+            for (int j = 0; j < P2; ++j) {
+                if (!KEEP) x[j] = mul2(add2(x[j], shift), r2);
+                x[j] = fma2(x[j], k1, fma2(mul2(y[j], g[j]), r2, k2));
+            }
             if (has_res) {
                 to_pairs<T, V>(vec_r(i), y);
 #pragma unroll
