@@ -486,7 +486,10 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dt
  * gamma, beta [d] of wtype (x's type or MOE_DTYPE_F32) or NULL (1 and 0); y [T,d]
  * of x's type, row stride ldy; mean, rstd [T] fp32 or NULL (the backward takes
  * them). Statistics and arithmetic in fp32, y rounded once. y may be x (same
- * stride). T >= 0 (0: nothing is enqueued), d >= 1, eps >= 0. One kernel. */
+ * stride). T >= 0 (0: nothing is enqueued), d >= 1, eps >= 0. One kernel.
+ * Rows come through bounded waits: should a copy not arrive within about a second (a device
+ * that has stopped), the kernel ends and the rows that it did not get hold NaN, mean and
+ * rstd too (in the backward dx, dgamma and dbeta). */
 moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma,
                                    const void *beta, int64_t T, int d, float eps,
                                    moe_dtype_t type, moe_dtype_t wtype, void *y, int64_t ldy,
@@ -590,6 +593,13 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
  * error word and exits; moe_sync_check then returns MOE_ERR_DEVICE_TIMEOUT and
  * the context stays usable. ws: any workspace of >= 64 bytes. */
 moe_status_t moe_selftest_wait_timeout(void *ws, size_t ws_bytes, void *stream);
+
+/* The same for layer norm: the copies of row `row` in this thread's next layer norm call
+ * (forward or backward, of rows that its ring holds) are never issued, so the wait for them
+ * runs out after about 1 s. The call ends after 2 s with NaN in that row and in later rows of
+ * the same warps (backward: in dgamma and dbeta too); all other rows are as ever. row < 0:
+ * takes it back. */
+moe_status_t moe_selftest_layernorm_withhold(int64_t row);
 
 /* Wait for `stream`, read and clear the workspace's device error word.
  * Returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT or MOE_ERR_DEVICE_CHECK (or

@@ -51,6 +51,14 @@ moe_status_t drop(const void *x, int64_t ldx, const void *res, int64_t ldr, int6
                                     type, as_stream(stream)));
 }
 
+// The row that this thread's next layer norm withholds (moe_selftest_layernorm_withhold).
+thread_local int64_t t_withheld = -1;
+int64_t take_withheld() {
+    const int64_t row = t_withheld;
+    t_withheld = -1;
+    return row;
+}
+
 // ---- dense feed-forward block
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -118,7 +126,8 @@ moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma
     if (x == y && ldx != ldy && T > 1) return MOE_ERR_INVALID_ARG;
     if ((st = check_arch()) != MOE_OK) return st;
     return from_cuda(launch_layernorm_forward(x, ldx, gamma, beta, y, ldy, mean, rstd, T, d, eps,
-                                              type, wtype == MOE_DTYPE_F32, as_stream(stream)));
+                                              type, wtype == MOE_DTYPE_F32, take_withheld(),
+                                              as_stream(stream)));
 }
 
 size_t moe_layernorm_scratch_bytes(int64_t T, int d) {
@@ -161,7 +170,13 @@ moe_status_t moe_layernorm_backward(const void *dy, int64_t lddy, const void *x,
     return from_cuda(launch_layernorm_backward(dy, lddy, x, ldx, gamma, mean, rstd, dres, lddres,
                                                dx, lddx, dgamma, dbeta, T, d, type,
                                                wtype == MOE_DTYPE_F32,
-                                               static_cast<float *>(scratch), as_stream(stream)));
+                                               static_cast<float *>(scratch), take_withheld(),
+                                               as_stream(stream)));
+}
+
+moe_status_t moe_selftest_layernorm_withhold(int64_t row) {
+    t_withheld = row >= 0 ? row : -1;
+    return MOE_OK;
 }
 
 moe_status_t moe_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,

@@ -209,17 +209,20 @@ cudaError_t launch_combine_rows(const __nv_bfloat16 *Z, const int32_t *row_map,
                                 int d, int64_t rows_cap, __nv_bfloat16 *Y, cudaStream_t s);
 
 // Layer norm (norm.cu); w32: gamma, beta and their gradients are fp32, else of
-// `type`. part: ln_partials(T) * 2 * d floats of scratch.
+// `type`. part: ln_partials(T) * 2 * d floats of scratch. withheld: a row whose copies are
+// never issued (the self-test of the bounded waits), or -1.
 constexpr int kLnPartials = 384;
 int ln_partials(int64_t T);
 cudaError_t launch_layernorm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta,
                                      void *y, int64_t ldy, float *mean, float *rstd, int64_t T,
-                                     int d, float eps, moe_dtype_t type, bool w32, cudaStream_t s);
+                                     int d, float eps, moe_dtype_t type, bool w32, int64_t withheld,
+                                     cudaStream_t s);
 cudaError_t launch_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                       const void *gamma, const float *mean, const float *rstd,
                                       const void *dres, int64_t lddres, void *dx, int64_t lddx,
                                       void *dgamma, void *dbeta, int64_t T, int d,
-                                      moe_dtype_t type, bool w32, float *part, cudaStream_t s);
+                                      moe_dtype_t type, bool w32, float *part, int64_t withheld,
+                                      cudaStream_t s);
 // Residual dropout (dropout.cu); res may be NULL.
 cudaError_t launch_dropout(const void *x, int64_t ldx, const void *res, int64_t ldr, void *y,
                            int64_t ldy, int64_t T, int d, uint32_t thr, uint64_t seed,

@@ -60,6 +60,7 @@ struct LnArgs {
     float eps;
     int wpr;  // warps per row
     int stages;  // ring stages per row group
+    int64_t withheld;  // self-test: this row's copies are never issued (-1: none)
     // backward
     const void *dy, *dres;
     void *dx;
@@ -114,13 +115,29 @@ struct RingCtl {
 constexpr int kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
-// Waits for a stage; gives up after about a second (the copies were issued by this
-// block, so only a device that has stopped would get there).
-__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity) {
-    if (ptx::mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity))
-        if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) return;
+// Waits for stage s. A copy that has not arrived after about a second never will (it was
+// issued by this block: the device has stopped). Then false, and the caller's group gives
+// up: it issues no further copies, its rows' results and the block's sums become NaN. Copies
+// in flight land before the block leaves, as far as another limit allows (drain: the
+// threads that issue copies wait for them).
+__device__ __noinline__ bool ring_wait_long(uint32_t bar0, int stages, int s, uint32_t parity, bool drain) {
+    uint64_t t0 = ptx::globaltimer_ns();
+    for (;;) {
+        // the clock first: a block that was held up for longer looks once more
+        const bool late = ptx::globaltimer_ns() - t0 > kWaitLimitNs;
+        if (ptx::mbar_try_wait(bar0 + 8 * s, parity)) return true;
+        if (late) break;
+    }
+    t0 = ptx::globaltimer_ns();
+    for (int k = 0; drain && k < stages; ++k) {
+        const int at = s + k < stages ? s + k : s + k - stages;
+        while (!ptx::mbar_try_wait(bar0 + 8 * at, s + k < stages ? parity : parity ^ 1))
+            if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ bool ring_wait(uint32_t bar0, int stages, int s, uint32_t parity, bool drain) {
+    return ptx::mbar_try_wait(bar0 + 8 * s, parity) || ring_wait_long(bar0, stages, s, parity, drain);
 }
 
 // Weights of vector v from their planes.
@@ -156,11 +173,12 @@ __device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int 
                                                int t, const bool (&ok)[NV],
                                                const f32x2 (&dg)[NV][V / 2],
                                                const f32x2 (&db)[NV][V / 2], uint8_t *rings,
-                                               size_t ring_bytes) {
+                                               size_t ring_bytes, bool gave_up) {
     float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
     const int nvec = (a.d + V - 1) / V;
     constexpr int H = V / 4;
-    __syncthreads();  // every thread is done with the last rows
+    // every thread is done with the last rows
+    const bool lost = __syncthreads_or(gave_up);
     float4 *mine = reinterpret_cast<float4 *>(rings + group * ring_bytes);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -189,6 +207,7 @@ __device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int 
             x.z += q.z;
             x.w += q.w;
         }
+        if (lost) x.x = x.y = x.z = x.w = NAN;
         float *out = part + (int64_t)m * a.d + 4 * e;
         if ((a.d & 3) == 0) {
             *reinterpret_cast<float4 *>(out) = x;
@@ -346,6 +365,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
     pdl_wait();
     pdl_trigger();
     auto fetch = [&](int64_t r, int s) {
+        if (r == a.withheld) return;
         if constexpr (SHIFT) {
             const uint32_t bytes = fetch_image(ring + (size_t)s * row_bytes, static_cast<const T *>(a.x),
                                                a.ldx, r, a.T, a.d, bar0 + 8 * s);
@@ -376,14 +396,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
 
     int s = 0;
     uint32_t ph = 0;
+    bool alive = true;
     for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
-        ring_wait(bar0 + 8 * s, ph);
+        alive = alive && ring_wait(bar0, S, s, ph, t == 0);
         const uint8_t *stage = ring + (size_t)s * row_bytes;
         const uint4 *src = reinterpret_cast<const uint4 *>(stage) + t;
         const uint32_t sx = (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const T *>(a.x) + row * a.ldx) & 15;
         // f: the elements, then their distances from the warp's own mean (a thread past
         // the row's end holds zeros throughout)
-        f32x2 f[NV][P2], acc = 0;
+        f32x2 f[NV][P2], acc = alive ? 0 : both(NAN);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if constexpr (SHIFT) {
@@ -427,7 +448,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) ln_forward_ring_kernel(const L
             __syncwarp();
         }
         // every thread of the group has read the stage
-        if (t == 0 && row + S * stride < a.T) fetch(row + S * stride, s);
+        if (t == 0 && alive && row + S * stride < a.T) fetch(row + S * stride, s);
         if (++s == S) {
             s = 0;
             ph ^= 1;
@@ -500,6 +521,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
     pdl_trigger();
     // row r of tensor k (x, dy, dres) into stage s: a thread each
     auto fetch = [&](int64_t r, int s, int k) {
+        if (r == a.withheld) return;
         const uint32_t bar = bar0 + 8 * s;
         uint8_t *dst = ring + (size_t)s * stage_bytes + (size_t)k * row_bytes;
         const T *base = static_cast<const T *>(k == 0 ? a.x : k == 1 ? a.dy : a.dres);
@@ -537,13 +559,14 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
 
     int s = 0, s_prev = -1;
     uint32_t ph = 0;
+    bool alive = true;
     for (int buf = 0; row < a.T; row += stride, buf ^= 1) {
         const float mean = m_next, rstd = r_next;
         if (row + stride < a.T) {
             m_next = a.mean[row + stride];
             r_next = a.rstd[row + stride];
         }
-        ring_wait(bar0 + 8 * s, ph);
+        alive = alive && ring_wait(bar0, S, s, ph, t < tensors);
         const uint8_t *stage = ring + (size_t)s * stage_bytes;
         const uint4 *px = reinterpret_cast<const uint4 *>(stage) + t;
         const uint4 *py = px + nvec, *pr = py + nvec;
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
         // xh = (x - m) r, the difference first: of x r and m r, both far larger where the
         // row's offset is far above its spread, nothing but rounding would be left
         const f32x2 r2 = both(rstd), shift = both(-mean);
-        f32x2 p1 = 0, p2 = 0;
+        f32x2 p1 = 0, p2 = alive ? 0 : both(NAN);
         constexpr bool KEEP = sizeof(T) == 4;  // xh and dy stay in registers (16 bits: too many)
         f32x2 kx[KEEP ? NV : 1][P2], ky[KEEP ? NV : 1][P2];
 #pragma unroll
@@ -592,7 +615,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             __syncwarp();
         }
         // every thread of the group is done with the previous row's stage
-        if (!SHIFT && t < tensors && s_prev >= 0 && row + (S - 1) * stride < a.T)
+        if (!SHIFT && t < tensors && alive && s_prev >= 0 && row + (S - 1) * stride < a.T)
             fetch(row + (S - 1) * stride, s_prev, t);
         if (a.wpr > 1) {
             const float2 o = lane < a.wpr ? ctl->stat[buf][w0 + lane] : make_float2(0.f, 0.f);
@@ -632,7 +655,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
             if (a.wpr > 1) group_sync(1 + group, tpr);
             else __syncwarp();
             // every thread of the group is done with this row's stage
-            if (t < tensors && row + S * stride < a.T) fetch(row + S * stride, s, t);
+            if (t < tensors && alive && row + S * stride < a.T) fetch(row + S * stride, s, t);
             send_image(image, drow, a.d, t, tpr);
         }
         s_prev = s;
@@ -643,7 +666,8 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
     }
     if (SHIFT && t == 0) ptx::bulk_wait_group<0>();
     if (a.part == nullptr) return;
-    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, rings, S * stage_bytes + SHIFT * row_bytes);
+    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, rings, S * stage_bytes + SHIFT * row_bytes,
+                          !alive);
 }
 
 // dgamma[c], dbeta[c] = the sum of P partial rows, each thread row q of the block
@@ -940,7 +964,8 @@ int ln_partials(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(
 
 cudaError_t launch_layernorm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta,
                                      void *y, int64_t ldy, float *mean, float *rstd, int64_t T,
-                                     int d, float eps, moe_dtype_t type, bool w32, cudaStream_t s) {
+                                     int d, float eps, moe_dtype_t type, bool w32, int64_t withheld,
+                                     cudaStream_t s) {
     LnArgs a{};
     a.x = x;
     a.gamma = gamma;
@@ -953,6 +978,7 @@ cudaError_t launch_layernorm_forward(const void *x, int64_t ldx, const void *gam
     a.T = T;
     a.d = d;
     a.w32 = w32;
+    a.withheld = withheld;
     a.eps = eps;
     const int es = type == MOE_DTYPE_F32 ? 4 : 2;
     Align al;
@@ -969,7 +995,8 @@ cudaError_t launch_layernorm_backward(const void *dy, int64_t lddy, const void *
                                       const void *gamma, const float *mean, const float *rstd,
                                       const void *dres, int64_t lddres, void *dx, int64_t lddx,
                                       void *dgamma, void *dbeta, int64_t T, int d,
-                                      moe_dtype_t type, bool w32, float *part, cudaStream_t s) {
+                                      moe_dtype_t type, bool w32, float *part, int64_t withheld,
+                                      cudaStream_t s) {
     LnArgs a{};
     a.x = x;
     a.gamma = gamma;
@@ -985,6 +1012,7 @@ cudaError_t launch_layernorm_backward(const void *dy, int64_t lddy, const void *
     a.T = T;
     a.d = d;
     a.w32 = w32;
+    a.withheld = withheld;
     a.part = dgamma != nullptr || dbeta != nullptr ? part : nullptr;
     const int es = type == MOE_DTYPE_F32 ? 4 : 2;
     Align al;

@@ -85,6 +85,7 @@ _SIGS = {
                               _P]),
     "moe_sync_check": (_I, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_selftest_wait_timeout": (_I, [_P, _SZ, _P]),
+    "moe_selftest_layernorm_withhold": (_I, [_L]),
     "moe_forward_host_stream": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                      _I, _P, _SZ, _P, _P, _P]),
     "moe_layernorm_forward": (_I, [_P, _L, _P, _P, _L, _I, _F, _I, _I, _P, _L, _P, _P, _P]),
@@ -484,6 +485,11 @@ def moe_selftest_wait_timeout(ws, stream=None):
     """Enqueue the bounded-wait self-test (sets MOE_DEVERR_TIMEOUT after ~1 s)."""
     _check("moe_selftest_wait_timeout", lib().moe_selftest_wait_timeout(
         _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_selftest_layernorm_withhold(row: int):
+    """This thread's next layer norm call never gets row `row` (a wait of ~1 s runs out)."""
+    _check("moe_selftest_layernorm_withhold", lib().moe_selftest_layernorm_withhold(row))
 
 
 def moe_sync_check(ws, stream=None):
