@@ -225,7 +225,7 @@ __device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int 
 // Bytes of the image of a row: its blocks, wherever it starts, and one more that the
 // last vector's shift reads.
 __host__ __device__ constexpr uint32_t image_bytes(int d, int esize) {
-    return ((uint32_t)d * esize + 15) / 16 * 16 + 32;
+    return ((uint32_t)d * esize + 15) / 16 * 16 + 32;  // (d: of a row that fits the ring)
 }
 // One thread: the blocks of row r of a [T, d] tensor into img, announced on bar
 // (which the caller arrives on, with the bytes returned). Elements in blocks that reach
@@ -701,6 +701,9 @@ ln_weight_reduce_kernel(const float *__restrict__ part, int P, int d, int w32, v
 }
 
 // ---- rows too wide for a ring ------------------------------------------------
+//
+// Up to 2^31 - 1 elements: vectors are counted in 32 bits without a sign (a thread's step
+// past the last one stays above it), the two arrays of weight sums in 64.
 
 // Sum over the block, in a fixed order.
 __device__ __forceinline__ float block_sum(float v, float *sh) {
@@ -717,26 +720,26 @@ __global__ void __launch_bounds__(1024) ln_forward_wide_kernel(const LnArgs a) {
     __shared__ float sh[32];
     pdl_wait();
     pdl_trigger();
-    const int nvec = a.d / V;
+    const uint32_t nvec = a.d / V;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         const Raw<T, V> *xp =
             reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.x) + row * a.ldx);
         Raw<T, V> *yp = reinterpret_cast<Raw<T, V> *>(static_cast<T *>(a.y) + row * a.ldy);
         float s = 0.f, f[V];
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        for (uint32_t v = threadIdx.x; v < nvec; v += blockDim.x) {
             to_f32<T, V>(xp[v], f);
 #pragma unroll
             for (int j = 0; j < V; ++j) s += f[j];
         }
         const float mean = block_sum(s, sh) / (float)a.d;
         s = 0.f;
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        for (uint32_t v = threadIdx.x; v < nvec; v += blockDim.x) {
             to_f32<T, V>(xp[v], f);
 #pragma unroll
             for (int j = 0; j < V; ++j) s = fmaf(f[j] - mean, f[j] - mean, s);
         }
         const float rstd = __frsqrt_rn(block_sum(s, sh) / (float)a.d + a.eps);
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        for (uint32_t v = threadIdx.x; v < nvec; v += blockDim.x) {
             to_f32<T, V>(xp[v], f);
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(1024) ln_backward_wide_kernel(const LnArgs a) 
     __shared__ float sh[32];
     pdl_wait();
     pdl_trigger();
-    const int nvec = a.d / V;
+    const uint32_t nvec = a.d / V;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         const Raw<T, V> *xp =
             reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(a.x) + row * a.ldx);
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(1024) ln_backward_wide_kernel(const LnArgs a) 
         Raw<T, V> *op = reinterpret_cast<Raw<T, V> *>(static_cast<T *>(a.dx) + row * a.lddx);
         const float mean = a.mean[row], rstd = a.rstd[row];
         float s1 = 0.f, s2 = 0.f, x[V], g[V];
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        for (uint32_t v = threadIdx.x; v < nvec; v += blockDim.x) {
             to_f32<T, V>(xp[v], x);
             to_f32<T, V>(yp[v], g);
 #pragma unroll
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(1024) ln_backward_wide_kernel(const LnArgs a) 
         }
         const float c1 = block_sum(s1, sh) / (float)a.d;
         const float c2 = block_sum(s2, sh) / (float)a.d;
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        for (uint32_t v = threadIdx.x; v < nvec; v += blockDim.x) {
             to_f32<T, V>(xp[v], x);
             to_f32<T, V>(yp[v], g);
 #pragma unroll
@@ -803,8 +806,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int v = blockIdx.x * 256 + threadIdx.x;
-    if (v >= a.d / V) return;
+    const uint32_t v = blockIdx.x * 256 + threadIdx.x;
+    if (v >= (uint32_t)(a.d / V)) return;
     float dg[V], db[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) dg[j] = db[j] = 0.f;
@@ -819,11 +822,11 @@ __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
             dg[j] = fmaf(g[j], (x[j] - mean) * rstd, dg[j]);
         }
     }
-    float *part = a.part + (int64_t)blockIdx.y * 2 * a.d;
+    float *part = a.part + (int64_t)blockIdx.y * 2 * a.d + (int64_t)v * V;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        part[v * V + j] = dg[j];
-        part[a.d + v * V + j] = db[j];
+        part[j] = dg[j];
+        part[a.d + (int64_t)j] = db[j];
     }
 }
 
@@ -854,8 +857,8 @@ constexpr size_t kRingSmem = 224 * 1024;
 // `fixed` bytes a block, `extra` a group, `stage` a stage.
 bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t extra, size_t stage,
                 int least, int *groups) {
+    if (a.d > max_threads * per_thread) return false;
     a.wpr = (a.d + per_thread * 32 - 1) / (per_thread * 32);
-    if (a.wpr * 32 > max_threads) return false;
     int g = std::min(row_groups(a.wpr, max_threads), a.wpr > 1 ? 15 : kMaxGroups);
     g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
     while (g > 1 && fixed + g * (extra + least * stage) > kRingSmem) --g;
@@ -867,7 +870,7 @@ bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t
 
 // Bytes of the fp32 planes of one weight vector.
 template <int V>
-size_t plane_bytes(int d) { return (size_t)(d + V - 1) / V * V * sizeof(float); }
+size_t plane_bytes(int d) { return ((size_t)d + V - 1) / V * V * sizeof(float); }
 
 template <typename T, int V, int NV, bool SHIFT>
 cudaError_t forward_ring(LnArgs a, bool *fits, cudaStream_t s) {
@@ -945,7 +948,7 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
         if (a.part != nullptr) {
             P = ln_partials(a.T);
             const int v = al.fits(16) ? W : 1;
-            const dim3 g((a.d / v + 255) / 256, P);
+            const dim3 g((a.d / v + 255u) / 256, P);
             e = al.fits(16) ? launch_k(ln_weight_wide_kernel<T, W>, g, dim3(256), 0, s, a)
                             : launch_k(ln_weight_wide_kernel<T, 1>, g, dim3(256), 0, s, a);
             if (e != cudaSuccess) return e;
@@ -954,7 +957,7 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
                         : launch_k(ln_backward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
     }
     if (e != cudaSuccess || a.part == nullptr) return e;
-    return launch_k(ln_weight_reduce_kernel<T>, dim3((2 * a.d + 31) / 32), dim3(512), 0, s,
+    return launch_k(ln_weight_reduce_kernel<T>, dim3((unsigned)((2ll * a.d + 31) / 32)), dim3(512), 0, s,
                     static_cast<const float *>(a.part), P, a.d, a.w32, dgamma, dbeta);
 }
 
