@@ -500,7 +500,7 @@ moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma
  *   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
  * dy, x, dx [T,d] of `type` with their row strides; dres [T,d] or NULL: a gradient
  * that reaches x by another branch (the residual), added to dx. dx may be dy or
- * dres. dgamma, dbeta [d] of wtype, each may be NULL; summed in fp32 in a fixed
+ * dres (same stride). dgamma, dbeta [d] of wtype, each may be NULL; summed in fp32 in a fixed
  * order (deterministic), 0 for T = 0. scratch: moe_layernorm_scratch_bytes(T, d)
  * bytes, 256-byte aligned, needed with dgamma or dbeta; its content on entry does
  * not matter. Two kernels (one without dgamma and dbeta; d > 8192: one more). */
@@ -523,14 +523,14 @@ moe_status_t moe_layernorm_backward(const void *dy, int64_t lddy, const void *x,
  * counter that the kernel adds to `offset`, or NULL (a captured graph draws anew
  * in each replay when the caller advances it). The mask is stored nowhere: the
  * backward draws it again. x, residual, y [T,d] of `type`, row strides in
- * elements; y may be x or residual. A dropped element does not read into y
+ * elements; y may be x or residual (same stride). A dropped element does not read into y
  * whatever x holds (infinities and NaN too). T >= 0, 0 <= p <= 1. One kernel. */
 moe_status_t moe_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,
                          int64_t T, int d, double p, uint64_t seed, uint64_t offset,
                          const uint64_t *offset_dev, moe_dtype_t type, void *y, int64_t ldy,
                          void *stream);
 /* dx = kept ? dy * 65536 / (65536 - thr) : 0 for the same p, seed and offset (the
- * residual's gradient is dy itself). dx may be dy. One kernel. */
+ * residual's gradient is dy itself). dx may be dy (same stride). One kernel. */
 moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d, double p,
                                   uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                                   moe_dtype_t type, void *dx, int64_t lddx, void *stream);

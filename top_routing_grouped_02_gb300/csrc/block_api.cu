@@ -35,6 +35,12 @@ moe_status_t check_shape(int64_t T, int d, moe_dtype_t t) {
     return MOE_OK;
 }
 
+// An output in the place of an operand has its row stride: with another one, rows would be
+// overwritten before they are read.
+bool strides_clash(const void *in, int64_t ldin, const void *out, int64_t ldout, int64_t T) {
+    return in == out && ldin != ldout && T > 1;
+}
+
 moe_status_t drop(const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t T, int d,
                   double p, uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                   moe_dtype_t type, void *y, int64_t ldy, void *stream) {
@@ -45,6 +51,7 @@ moe_status_t drop(const void *x, int64_t ldx, const void *res, int64_t ldr, int6
     if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
     if ((st = check_matrix(y, ldy, T, d, type)) != MOE_OK) return st;
     if (res != nullptr && (st = check_matrix(res, ldr, T, d, type)) != MOE_OK) return st;
+    if (strides_clash(x, ldx, y, ldy, T) || strides_clash(res, ldr, y, ldy, T)) return MOE_ERR_INVALID_ARG;
     if ((st = check_arch()) != MOE_OK) return st;
     const uint32_t thr = (uint32_t)floor(p * 65536.0 + 0.5);
     return from_cuda(launch_dropout(x, ldx, res, ldr, y, ldy, T, d, thr, seed, offset, offset_dev,
@@ -123,7 +130,7 @@ moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma
     if (T == 0) return MOE_OK;
     if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
     if ((st = check_matrix(y, ldy, T, d, type)) != MOE_OK) return st;
-    if (x == y && ldx != ldy && T > 1) return MOE_ERR_INVALID_ARG;
+    if (strides_clash(x, ldx, y, ldy, T)) return MOE_ERR_INVALID_ARG;
     if ((st = check_arch()) != MOE_OK) return st;
     return from_cuda(launch_layernorm_forward(x, ldx, gamma, beta, y, ldy, mean, rstd, T, d, eps,
                                               type, wtype == MOE_DTYPE_F32, take_withheld(),
@@ -154,6 +161,9 @@ moe_status_t moe_layernorm_backward(const void *dy, int64_t lddy, const void *x,
         if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
         if ((st = check_matrix(dx, lddx, T, d, type)) != MOE_OK) return st;
         if (dres != nullptr && (st = check_matrix(dres, lddres, T, d, type)) != MOE_OK) return st;
+        if (strides_clash(dy, lddy, dx, lddx, T) || strides_clash(x, ldx, dx, lddx, T) ||
+            strides_clash(dres, lddres, dx, lddx, T))
+            return MOE_ERR_INVALID_ARG;
         if (dgamma != nullptr || dbeta != nullptr) {
             if (scratch == nullptr || !aligned(scratch, 256)) return MOE_ERR_INVALID_ARG;
             if (scratch_bytes < moe_layernorm_scratch_bytes(T, d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
