@@ -11,6 +11,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <optional>
 
 #include "moe.h"
@@ -58,16 +59,39 @@ int type_of(const at::Tensor &t) {
     }
 }
 
-// The call's stream, and torch's current one while the call lasts: what the call
-// allocates (outputs, scratch) then comes from this stream's memory, which no pending
-// work of another stream still uses or will be given before the call's kernels are done.
+// Every operand and the given stream belong to the first tensor's device.
+struct Named {
+    const at::Tensor &t;
+    const char *name;
+};
+void one_device(const Named &first, std::initializer_list<Named> others, PyObject *stream) {
+    if (!first.t.is_cuda()) refuse(PyExc_ValueError, "%s must be a CUDA tensor", first.name);
+    const int device = first.t.get_device();
+    for (const Named &o : others)
+        if (o.t.defined() && (!o.t.is_cuda() || o.t.get_device() != device))
+            refuse(PyExc_ValueError, "%s must lie on the first tensor's device", o.name);
+    if (stream == Py_None) return;
+    PyObject *v = PyObject_GetAttrString(stream, "device_index");
+    if (v == nullptr) {  // a bare handle: the caller's word for it
+        PyErr_Clear();
+        return;
+    }
+    const long index = PyLong_AsLong(v);
+    Py_DECREF(v);
+    if (index == -1 && PyErr_Occurred()) throw Refused();
+    if (index != device) refuse(PyExc_ValueError, "%s must belong to the first tensor's device", "stream");
+}
+
+// The call's device and stream, torch's current ones while the call lasts: its kernels are
+// launched on that device, and what it allocates (outputs, scratch) comes from that
+// stream's memory, which no pending work of another stream still uses or will be given
+// before the call's kernels are done.
 struct OnStream {
+    c10::cuda::CUDAGuard device;
     std::optional<c10::cuda::CUDAStreamGuard> guard;
     cudaStream_t s;
-    OnStream(PyObject *o, const at::Tensor &t) {
-        if (!t.is_cuda()) refuse(PyExc_ValueError, "%s must be a CUDA tensor", "the first tensor");
-        const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(t.get_device());
-        s = now.stream();
+    OnStream(PyObject *o, const at::Tensor &t) : device(t.device()) {
+        s = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
         if (o == Py_None) return;
         PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
         if (v == nullptr) throw Refused();
@@ -112,9 +136,9 @@ Rows rows_of(const at::Tensor &t, const char *name, const at::Tensor *like = nul
     r.T = t.size(0);
     return r;
 }
-// An output: `o`, or a new contiguous tensor like x.
-at::Tensor output(PyObject *o, const at::Tensor &x, const char *name) {
-    return o == Py_None ? fresh(x.sizes(), x.scalar_type(), x) : tensor(o, name);
+// An output: `given`, or a new contiguous tensor like x.
+at::Tensor output(const at::Tensor &given, const at::Tensor &x) {
+    return given.defined() ? given : fresh(x.sizes(), x.scalar_type(), x);
 }
 void *vec_of(const at::Tensor &t, int64_t d, const at::Tensor &x, const char *name) {
     if (!t.defined()) return nullptr;
@@ -173,7 +197,9 @@ PyObject *wrap_all(const Ts &...ts) {
 PyObject *layernorm(PyObject *const *a, Py_ssize_t n) {
     expect(n, 7);
     const at::Tensor x = tensor(a[0], "x");
-    const at::Tensor gamma = optional_tensor(a[1], "gamma"), beta = optional_tensor(a[2], "beta");
+    const at::Tensor gamma = optional_tensor(a[1], "gamma"), beta = optional_tensor(a[2], "beta"),
+                     given = optional_tensor(a[5], "y");
+    one_device({x, "x"}, {{gamma, "gamma"}, {beta, "beta"}, {given, "y"}}, a[6]);
     const Rows rx = rows_of(x, "x");
     const OnStream stream(a[6], x);
     const double eps = number(a[3]);
@@ -181,7 +207,7 @@ PyObject *layernorm(PyObject *const *a, Py_ssize_t n) {
     void *pg = vec_of(gamma, rx.d, x, "gamma"), *pb = vec_of(beta, rx.d, x, "beta");
     if (pg != nullptr && pb != nullptr && gamma.scalar_type() != beta.scalar_type())
         refuse(PyExc_TypeError, "gamma and %s must have one type", "beta");
-    const at::Tensor y = output(a[5], x, "y");
+    const at::Tensor y = output(given, x);
     const Rows ry = rows_of(y, "y", &x);
     at::Tensor mean, rstd;
     if (stats) {
@@ -203,14 +229,19 @@ PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
     expect(n, 10);
     const at::Tensor dy = tensor(a[0], "dy"), x = tensor(a[1], "x");
     const at::Tensor gamma = optional_tensor(a[2], "gamma"), mean = tensor(a[3], "mean"),
-                     rstd = tensor(a[4], "rstd"), dres = optional_tensor(a[5], "dres");
+                     rstd = tensor(a[4], "rstd"), dres = optional_tensor(a[5], "dres"),
+                     given = optional_tensor(a[7], "dx"), memory = optional_tensor(a[8], "scratch");
+    one_device({x, "x"},
+               {{dy, "dy"}, {gamma, "gamma"}, {mean, "mean"}, {rstd, "rstd"}, {dres, "dres"}, {given, "dx"},
+                {memory, "scratch"}},
+               a[9]);
     const Rows rx = rows_of(x, "x"), rdy = rows_of(dy, "dy", &x);
     const OnStream stream(a[9], x);
     Rows rr{};
     if (dres.defined()) rr = rows_of(dres, "dres", &x);
     void *pg = vec_of(gamma, rx.d, x, "gamma");
     float *pm = stat_of(mean, rx.T, "mean"), *pr = stat_of(rstd, rx.T, "rstd");
-    const at::Tensor dx = output(a[7], x, "dx");
+    const at::Tensor dx = output(given, x);
     const Rows rdx = rows_of(dx, "dx", &x);
     const at::ScalarType wt = gamma.defined()               ? gamma.scalar_type()
                               : PyObject_IsTrue(a[6]) == 1 ? at::kFloat
@@ -218,10 +249,9 @@ PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor dgamma = fresh({rx.d}, wt, x);
     const at::Tensor dbeta = fresh({rx.d}, wt, x);
     const at::Tensor scratch =
-        a[8] != Py_None ? tensor(a[8], "scratch")
-                        : fresh({(int64_t)moe_layernorm_scratch_bytes(rx.T, (int)rx.d)}, at::kByte, x);
-    if (!scratch.is_cuda() || !scratch.is_contiguous())
-        refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor", "scratch");
+        memory.defined() ? memory
+                         : fresh({(int64_t)moe_layernorm_scratch_bytes(rx.T, (int)rx.d)}, at::kByte, x);
+    if (!scratch.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", "scratch");
     check("moe_layernorm_backward",
           moe_layernorm_backward(rdy.p, rdy.ld, rx.p, rx.ld, pg, pm, pr, rr.p, rr.ld, rx.T, (int)rx.d,
                                  dtype(x), dtype(dgamma), rdx.p, rdx.ld, dgamma.data_ptr(),
@@ -234,7 +264,8 @@ PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
 PyObject *dropout(PyObject *const *a, Py_ssize_t n) {
     expect(n, 8);
     const at::Tensor x = tensor(a[0], "x"), res = optional_tensor(a[4], "residual"),
-                     ctr = optional_tensor(a[5], "offset_dev");
+                     ctr = optional_tensor(a[5], "offset_dev"), given = optional_tensor(a[6], "y");
+    one_device({x, "x"}, {{res, "residual"}, {ctr, "offset_dev"}, {given, "y"}}, a[7]);
     const Rows rx = rows_of(x, "x");
     const OnStream stream(a[7], x);
     const double p = number(a[1]);
@@ -242,7 +273,7 @@ PyObject *dropout(PyObject *const *a, Py_ssize_t n) {
     Rows rr{};
     if (res.defined()) rr = rows_of(res, "residual", &x);
     const uint64_t *pc = counter_of(ctr);
-    const at::Tensor y = output(a[6], x, "y");
+    const at::Tensor y = output(given, x);
     const Rows ry = rows_of(y, "y", &x);
     check("moe_dropout", moe_dropout(rx.p, rx.ld, rr.p, rr.ld, rx.T, (int)rx.d, p, seed, offset, pc,
                                      dtype(x), ry.p, ry.ld, stream));
@@ -252,13 +283,15 @@ PyObject *dropout(PyObject *const *a, Py_ssize_t n) {
 // dy, p, seed, offset, offset_dev, dx, stream
 PyObject *dropout_backward(PyObject *const *a, Py_ssize_t n) {
     expect(n, 7);
-    const at::Tensor dy = tensor(a[0], "dy"), ctr = optional_tensor(a[4], "offset_dev");
+    const at::Tensor dy = tensor(a[0], "dy"), ctr = optional_tensor(a[4], "offset_dev"),
+                     given = optional_tensor(a[5], "dx");
+    one_device({dy, "dy"}, {{ctr, "offset_dev"}, {given, "dx"}}, a[6]);
     const Rows r = rows_of(dy, "dy");
     const OnStream stream(a[6], dy);
     const double p = number(a[1]);
     const uint64_t seed = word(a[2]), offset = word(a[3]);
     const uint64_t *pc = counter_of(ctr);
-    const at::Tensor dx = output(a[5], dy, "dx");
+    const at::Tensor dx = output(given, dy);
     const Rows rdx = rows_of(dx, "dx", &dy);
     check("moe_dropout_backward",
           moe_dropout_backward(r.p, r.ld, r.T, (int)r.d, p, seed, offset, pc, dtype(dy), rdx.p, rdx.ld,
@@ -273,8 +306,9 @@ struct Ffn {
     void *px, *p1, *p3, *p2, *pws;
     at::ScalarType type;
 };
-Ffn ffn_args(PyObject *x, PyObject *W1, PyObject *W3, PyObject *W2, PyObject *ws) {
+Ffn ffn_args(PyObject *x, PyObject *W1, PyObject *W3, PyObject *W2, PyObject *ws, PyObject *stream) {
     Ffn f{tensor(x, "x"), tensor(W1, "W1"), tensor(W3, "W3"), tensor(W2, "W2"), tensor(ws, "ws")};
+    one_device({f.x, "x"}, {{f.W1, "W1"}, {f.W3, "W3"}, {f.W2, "W2"}, {f.ws, "ws"}}, stream);
     if (f.x.dim() < 1 || f.W1.dim() != 2 || f.x.size(-1) != f.W1.size(0))
         refuse(PyExc_ValueError, "%s must be [..., d] and W1 [d, n]", "x");
     f.type = f.x.scalar_type();
@@ -287,8 +321,7 @@ Ffn ffn_args(PyObject *x, PyObject *W1, PyObject *W3, PyObject *W2, PyObject *ws
     f.p1 = dense(f.W1, {d, n}, f.type, "W1");
     f.p3 = dense(f.W3, {d, n}, f.type, "W3");
     f.p2 = dense(f.W2, {n, d}, f.type, "W2");
-    if (!f.ws.is_cuda() || !f.ws.is_contiguous())
-        refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor", "ws");
+    if (!f.ws.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", "ws");
     f.pws = f.ws.data_ptr();
     f.T = (int)T;
     f.d = (int)d;
@@ -299,9 +332,11 @@ Ffn ffn_args(PyObject *x, PyObject *W1, PyObject *W3, PyObject *W2, PyObject *ws
 // x, W1, W3, W2, act, ws, Y, stream
 PyObject *ffn(PyObject *const *a, Py_ssize_t n) {
     expect(n, 8);
-    const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5]);
+    const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5], a[7]);
+    const at::Tensor given = optional_tensor(a[6], "Y");
+    one_device({f.x, "x"}, {{given, "Y"}}, Py_None);
     const OnStream stream(a[7], f.x);
-    const at::Tensor Y = output(a[6], f.x, "Y");
+    const at::Tensor Y = output(given, f.x);
     void *py = dense(Y, f.x.sizes(), f.type, "Y");
     check("moe_ffn_forward",
           moe_ffn_forward(f.px, f.p1, f.p3, f.p2, f.T, f.d, f.n, (moe_act_t)integer(a[4]), dtype(f.x), py,
@@ -312,7 +347,7 @@ PyObject *ffn(PyObject *const *a, Py_ssize_t n) {
 // x, W1, W3, W2, act, ws, stream
 PyObject *ffn_train(PyObject *const *a, Py_ssize_t n) {
     expect(n, 7);
-    const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5]);
+    const Ffn f = ffn_args(a[0], a[1], a[2], a[3], a[5], a[6]);
     const OnStream stream(a[6], f.x);
     const at::Tensor Y = fresh(f.x.sizes(), f.type, f.x);
     const at::Tensor H = fresh({f.T, f.n}, f.type, f.x);
@@ -330,10 +365,11 @@ PyObject *ffn_train(PyObject *const *a, Py_ssize_t n) {
 // dY, x, W1, W3, W2, H, F1, F3, act, need_dx, need_dw, ws, stream
 PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
     expect(n, 13);
-    const Ffn f = ffn_args(a[1], a[2], a[3], a[4], a[11]);
-    const OnStream stream(a[12], f.x);
+    const Ffn f = ffn_args(a[1], a[2], a[3], a[4], a[11], a[12]);
     const at::Tensor dY = tensor(a[0], "dY"), H = tensor(a[5], "H"), F1 = tensor(a[6], "F1"),
                      F3 = tensor(a[7], "F3");
+    one_device({f.x, "x"}, {{dY, "dY"}, {H, "H"}, {F1, "F1"}, {F3, "F3"}}, Py_None);
+    const OnStream stream(a[12], f.x);
     const int64_t saved = (int64_t)moe_ffn_saved_floats(f.T, f.n);
     void *pdy = dense(dY, f.x.sizes(), f.type, "dY"), *ph = dense(H, {f.T, f.n}, f.type, "H");
     const float *pf1 = static_cast<float *>(dense(F1, {saved}, at::kFloat, "F1"));

@@ -639,16 +639,22 @@ ACTS = {"silu": 0, "gelu": 1}
 
 def ffn_workspace(T: int, d: int, n: int, train: bool = False, device=None, stream=None):
     """A workspace (uint8, control words zeroed) of the dense block's calls for up to
-    T tokens; train: of moe_ffn_train and moe_ffn_backward too."""
+    T tokens; train: of moe_ffn_train and moe_ffn_backward too. It lies on `device`
+    (default: the given stream's, else the current one)."""
     nbytes = int(lib().moe_ffn_workspace_bytes(T, d, n, int(train)))
     if nbytes == 0:
         raise ValueError("invalid feed-forward shape")
-    if device is not None and torch.device(device).type != "cuda":
-        raise ValueError("the workspace lies on a CUDA device")
-    with torch.cuda.stream(stream):  # its memory, as a temporary's reuse follows that order
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
-    _check("moe_ffn_workspace_init", lib().moe_ffn_workspace_init(
-        ws.data_ptr(), nbytes, _stream(stream)))
+    device = None if device is None else torch.device(device)
+    if device is not None:
+        if device.type != "cuda":
+            raise ValueError("the workspace lies on a CUDA device")
+        if stream is not None and device.index not in (None, stream.device_index):
+            raise ValueError("stream must belong to the workspace's device")
+    # its memory is the stream's, as a temporary's reuse follows that order
+    with torch.cuda.device(device if stream is None else stream.device), torch.cuda.stream(stream):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        _check("moe_ffn_workspace_init", lib().moe_ffn_workspace_init(
+            ws.data_ptr(), nbytes, _stream(stream)))
     return ws
 
 
