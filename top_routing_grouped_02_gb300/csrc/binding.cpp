@@ -44,6 +44,11 @@ long integer(PyObject *o) {
     if (v == -1 && PyErr_Occurred()) throw Refused();
     return v;
 }
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused();
+    return v != 0;
+}
 uint64_t word(PyObject *o) {
     const uint64_t v = PyLong_AsUnsignedLongLongMask(o);
     if (v == (uint64_t)-1 && PyErr_Occurred()) throw Refused();
@@ -203,7 +208,7 @@ PyObject *layernorm(PyObject *const *a, Py_ssize_t n) {
     const Rows rx = rows_of(x, "x");
     const OnStream stream(a[6], x);
     const double eps = number(a[3]);
-    const bool stats = PyObject_IsTrue(a[4]) == 1;
+    const bool stats = truth(a[4]);
     void *pg = vec_of(gamma, rx.d, x, "gamma"), *pb = vec_of(beta, rx.d, x, "beta");
     if (pg != nullptr && pb != nullptr && gamma.scalar_type() != beta.scalar_type())
         refuse(PyExc_TypeError, "gamma and %s must have one type", "beta");
@@ -244,7 +249,7 @@ PyObject *layernorm_backward(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor dx = output(given, x);
     const Rows rdx = rows_of(dx, "dx", &x);
     const at::ScalarType wt = gamma.defined()               ? gamma.scalar_type()
-                              : PyObject_IsTrue(a[6]) == 1 ? at::kFloat
+                              : truth(a[6]) ? at::kFloat
                                                             : x.scalar_type();
     const at::Tensor dgamma = fresh({rx.d}, wt, x);
     const at::Tensor dbeta = fresh({rx.d}, wt, x);
@@ -375,8 +380,8 @@ PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
     const float *pf1 = static_cast<float *>(dense(F1, {saved}, at::kFloat, "F1"));
     const float *pf3 = static_cast<float *>(dense(F3, {saved}, at::kFloat, "F3"));
     at::Tensor dX, dW1, dW3, dW2;
-    if (PyObject_IsTrue(a[9]) == 1) dX = fresh(f.x.sizes(), f.type, f.x);
-    const bool dw = PyObject_IsTrue(a[10]) == 1;
+    if (truth(a[9])) dX = fresh(f.x.sizes(), f.type, f.x);
+    const bool dw = truth(a[10]);
     if (dw) {
         dW1 = fresh({f.d, f.n}, f.type, f.x);
         dW3 = fresh({f.d, f.n}, f.type, f.x);
