@@ -643,7 +643,9 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 auto joinable = [&] {
                     bool all = true;
                     if (lane == 0) all = word_wait(ticket, 0xffffu, (uint32_t)args.split, args.err);
-                    return __shfl_sync(0xffffffffu, all, 0) != 0;
+                    all = __shfl_sync(0xffffffffu, all, 0) != 0;
+                    __syncwarp();  // lane 0's acquire comes before every lane's loads (a shuffle orders none)
+                    return all;
                 };
                 if (few) {
                     if (!finish(un, c_lo + lo / 8, c_lo + hi / 8, taddr, true, joinable, [] {})) break;

@@ -225,6 +225,7 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
             ok = word_wait(ticket + x.tile * 4 + q, 0xffffu, (uint32_t)(x.P * kSets), args.err);
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
     }
+    __syncwarp();  // lane 0's acquires come before every lane's loads (a shuffle orders none)
     constexpr int kBatch = MATS == 2 ? 10 : 16;  // parts in flight
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
