@@ -22,13 +22,15 @@ inline CUtensorMapDataType map_type(bool f16) {
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // Polls a barrier of this CTA; after about one second it sets MOE_DEVERR_TIMEOUT
-// and gives up.
+// and gives up. (The clock comes before the last look: a block that was itself held up for
+// longer does not give up on what has arrived meanwhile.)
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint32_t *err) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
     for (uint32_t spin = 1;; ++spin) {
+        const bool late = (spin & 63u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs;
         if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((spin & 63u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (late) {
             atomicOr(err, MOE_DEVERR_TIMEOUT);
             return false;
         }
@@ -42,8 +44,9 @@ __device__ __forceinline__ bool poll_word(const uint32_t *w, uint32_t *err, Done
     const uint64_t t0 = ptx::globaltimer_ns();
     for (uint32_t spin = 1;; ++spin) {
         __nanosleep(32);
+        const bool late = (spin & 15u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs;
         if (done(ptx::ld_acquire_gpu(w))) return true;
-        if ((spin & 15u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (late) {
             atomicOr(err, MOE_DEVERR_TIMEOUT);
             return false;
         }
