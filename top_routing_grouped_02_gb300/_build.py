@@ -40,10 +40,23 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _torch_dirs():
     import importlib.util
     base = os.path.dirname(importlib.util.find_spec("torch").origin)
     return os.path.join(base, "include"), os.path.join(base, "lib")
+
+
+def _native_stamp(commands) -> str:
+    """What _native.so is made with: it belongs to one torch."""
+    with open(os.path.join(os.path.dirname(_torch_dirs()[0]), "version.py")) as f:
+        return "\n".join([*(" ".join(c) for c in commands), f.read()])
 
 
 def _native_compile(src: str, obj: str) -> list[str]:
@@ -76,8 +89,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             jobs.append(cmd)
     native_src = os.path.join(CSRC, "binding.cpp")
     native_obj = os.path.join(BUILD, "binding.o")
-    if force or _stale(native_obj, [native_src, headers[-1]]):
-        jobs.append(_native_compile(native_src, native_obj))
+    native_cmds = [_native_compile(native_src, native_obj), _native_link(native_obj, NATIVE)]
+    stamp, stamp_file = _native_stamp(native_cmds), os.path.join(BUILD, "native.stamp")
+    native_old = _stale(native_obj, [native_src, headers[-1]]) or _read(stamp_file) != stamp
+    if force or native_old:
+        jobs.append(native_cmds[0])
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
     for cmd, r in zip(jobs, results):
@@ -95,7 +111,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link of libmoe.so failed")
         os.replace(tmp, LIB)
-    if force or _stale(NATIVE, [native_obj]):
+    if force or native_old or _stale(NATIVE, [native_obj]):
         tmp = NATIVE + f".tmp{os.getpid()}"
         cmd = _native_link(native_obj, tmp)
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -104,6 +120,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link of _native.so failed")
         os.replace(tmp, NATIVE)
+        with open(stamp_file, "w") as f:
+            f.write(stamp)
     return LIB
 
 
