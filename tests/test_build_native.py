@@ -60,3 +60,49 @@ def test_another_torch_makes_it_anew(tools):
     assert tools.take() == [("g++", "binding.o"), ("g++", "_native.so")]
     _build.build()
     assert tools.take() == []
+
+
+@pytest.mark.parametrize("error", [FileNotFoundError("no g++"), "Python.h: No such file or directory"])
+@pytest.mark.parametrize("output", ["binding.o", "_native.so"])
+def test_the_layer_is_built_without_it(tools, capsys, error, output):
+    tools.fail = lambda cmd: error if cmd[0] == "g++" and output in cmd[cmd.index("-o") + 1] else None
+    assert _build.build() == _build.LIB
+    assert os.path.exists(_build.LIB) and not os.path.exists(_build.NATIVE)
+    assert "_native.so was not built" in capsys.readouterr().out
+    # once the tools are there
+    tools.fail = lambda cmd: None
+    tools.take()
+    _build.build()
+    assert ("g++", "_native.so") in tools.take() and os.path.exists(_build.NATIVE)
+
+
+def test_an_old_one_is_not_left_behind(tools):
+    _build.build()
+    tools.fail = lambda cmd: "error" if cmd[0] == "g++" else None
+    (tools.torch / "version.py").write_text("__version__ = '2'\n")
+    _build.build()
+    assert not os.path.exists(_build.NATIVE)
+
+
+def test_failures_of_nvcc_stop_the_build(tools):
+    tools.fail = lambda cmd: "error" if cmd[0].endswith("nvcc") else None
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        _build.build()
+
+
+def test_the_loaders_message_is_passed_on(monkeypatch):
+    from top_routing_grouped_02_gb300 import moe
+    import builtins
+
+    real = builtins.__import__
+
+    def fake(name, globals=None, locals=None, fromlist=(), level=0):
+        if "_native" in (fromlist or ()):
+            raise ImportError("undefined symbol: of another torch")
+        return real(name, globals, locals, fromlist, level)
+
+    monkeypatch.setattr(moe, "_nat", None)
+    monkeypatch.setattr(moe, "lib", lambda: None)
+    monkeypatch.setattr(builtins, "__import__", fake)
+    with pytest.raises(RuntimeError, match="undefined symbol: of another torch"):
+        moe._native()

@@ -40,6 +40,10 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _stamp_file() -> str:
+    return os.path.join(BUILD, "native.stamp")
+
+
 def _read(path: str) -> str | None:
     if not os.path.exists(path):
         return None
@@ -49,7 +53,10 @@ def _read(path: str) -> str | None:
 
 def _torch_dirs():
     import importlib.util
-    base = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    base = os.path.dirname(spec.origin)
     return os.path.join(base, "include"), os.path.join(base, "lib")
 
 
@@ -75,6 +82,9 @@ def _native_link(obj: str, out: str) -> list[str]:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Builds both libraries and returns libmoe.so's path. Where _native.so cannot be made (no
+    g++, no Python or torch headers) it says why and leaves none: the layer's calls need
+    libmoe.so alone, and the sub-block's calls raise."""
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
@@ -87,21 +97,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(obj, [src] + headers):
             cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
             jobs.append(cmd)
-    native_src = os.path.join(CSRC, "binding.cpp")
-    native_obj = os.path.join(BUILD, "binding.o")
-    native_cmds = [_native_compile(native_src, native_obj), _native_link(native_obj, NATIVE)]
-    stamp, stamp_file = _native_stamp(native_cmds), os.path.join(BUILD, "native.stamp")
-    native_old = _stale(native_obj, [native_src, headers[-1]]) or _read(stamp_file) != stamp
-    if force or native_old:
-        jobs.append(native_cmds[0])
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        native = ex.submit(_native_object, headers[-1], force, verbose)
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
     for cmd, r in zip(jobs, results):
         if verbose or r.returncode != 0:
             print(" ".join(cmd))
             print(r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}")
+            raise RuntimeError(f"nvcc failed for {cmd[-3]}")
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
@@ -111,18 +115,48 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link of libmoe.so failed")
         os.replace(tmp, LIB)
-    if force or native_old or _stale(NATIVE, [native_obj]):
-        tmp = NATIVE + f".tmp{os.getpid()}"
-        cmd = _native_link(native_obj, tmp)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            print(" ".join(cmd))
-            print(r.stdout + r.stderr)
-            raise RuntimeError("link of _native.so failed")
-        os.replace(tmp, NATIVE)
-        with open(stamp_file, "w") as f:
-            f.write(stamp)
+    try:
+        _native_finish(native.result())
+    except (OSError, RuntimeError) as e:
+        print(f"_native.so was not built, the sub-block's calls will raise: {e}")
+        if os.path.exists(NATIVE):
+            os.remove(NATIVE)
     return LIB
+
+
+def _run_native(cmd, verbose: bool = False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        print(" ".join(cmd))
+        print(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {cmd[-1]}")
+
+
+def _native_object(header: str, force: bool, verbose: bool):
+    """Compiles the binding if it is out of date; what _native_finish links, or the error."""
+    try:
+        src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+        compile_cmd, link_cmd = _native_compile(src, obj), _native_link(obj, NATIVE)
+        stamp = _native_stamp([compile_cmd, link_cmd])
+        old = force or _stale(obj, [src, header]) or _read(_stamp_file()) != stamp
+        if old:
+            _run_native(compile_cmd, verbose)
+        return obj, stamp, old
+    except (OSError, RuntimeError) as e:
+        return e
+
+
+def _native_finish(made):
+    if isinstance(made, Exception):
+        raise made
+    obj, stamp, old = made
+    if old or _stale(NATIVE, [obj]):
+        tmp = NATIVE + f".tmp{os.getpid()}"
+        _run_native(_native_link(obj, tmp))
+        os.replace(tmp, NATIVE)
+        with open(_stamp_file(), "w") as f:
+            f.write(stamp)
 
 
 if __name__ == "__main__":

@@ -596,7 +596,8 @@ def _native():
         try:
             from . import _native as nat
         except ImportError as e:
-            raise RuntimeError("_native.so not built; run __graft_entry__.build()") from e
+            raise RuntimeError(f"_native.so is not built or cannot be loaded ({e}); run "
+                               "__graft_entry__.build()") from e
         nat.set_error(MoeError)
         _nat = nat
     return _nat
