@@ -20,7 +20,7 @@ namespace {
 
 PyObject *g_error = nullptr;  // moe.MoeError
 
-struct Refused {};  // a Python exception is set
+using Refused = python_error;  // a Python exception is set
 
 [[noreturn]] void refuse(PyObject *type, const char *format, const char *name) {
     PyErr_Format(type, format, name);
@@ -403,16 +403,12 @@ PyObject *set_error(PyObject *const *a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// No C++ exception leaves an entry point: refusals have set theirs, torch's are
-// translated.
+// No C++ exception leaves an entry point: torch's macros translate them (a refusal's Python
+// exception is set already) and give torch's pending warnings first.
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    try {
-        return F(args, n);
-    } catch (const Refused &) {
-        return nullptr;
-    }
+    return F(args, n);
     END_HANDLE_TH_ERRORS
 }
 
