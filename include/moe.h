@@ -503,7 +503,8 @@ moe_status_t moe_layernorm_forward(const void *x, int64_t ldx, const void *gamma
  * dres (same stride). dgamma, dbeta [d] of wtype, each may be NULL; summed in fp32 in a fixed
  * order (deterministic), 0 for T = 0. scratch: moe_layernorm_scratch_bytes(T, d)
  * bytes, 256-byte aligned, needed with dgamma or dbeta; its content on entry does
- * not matter. Two kernels (one without dgamma and dbeta; d > 8192: one more). */
+ * not matter. Two kernels (one without dgamma and dbeta; rows that no ring in shared memory
+ * holds, past some 14000 elements of 16 bits or 8000 of 32: one more). */
 size_t moe_layernorm_scratch_bytes(int64_t T, int d);
 moe_status_t moe_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                     const void *gamma, const float *mean, const float *rstd,
@@ -547,18 +548,21 @@ typedef enum {
 } moe_act_t;
 
 /* Workspace of the calls below for up to T tokens (train: of the training forward
- * and the backward too; else of moe_ffn_forward), 256-byte aligned; 0 for an invalid shape. Its control words (the device error word of
+ * and the backward too; else of moe_ffn_forward), 256-byte aligned; 0 for an invalid shape.
+ * Its control words (the device error word of
  * moe_sync_check and join counters) start at zero, once before the first use
  * (moe_ffn_workspace_init), and every call leaves the counters so. It serves any
  * shape that needs no more bytes. Calls that overlap on the GPU need one each. */
 size_t moe_ffn_workspace_bytes(int T, int d, int n, int train);
 moe_status_t moe_ffn_workspace_init(void *ws, size_t ws_bytes, void *stream);
 
-/* Y. Few tokens (up to 48, or 64 with 3 d n <= 2^27) one kernel, which streams the weights, each SM an equal share
- * of them, with H complete on all SMs before the down projection (bounded waits: a
- * CTA that never gets an SM sets MOE_DEVERR_TIMEOUT; initialise the workspace again
- * after that). Otherwise two: gate and up projections, activation and product in
- * one, the down projection in the other. */
+/* Y. Few tokens (up to 48, or 64 with 3 d n <= 2^27) one kernel, which streams the weights,
+ * each SM an equal share of them, with H complete on all SMs before the down projection.
+ * Otherwise two: gate and up projections, activation and product in one, the down
+ * projection in the other. CTAs that wait on one another, here and in the calls below, are
+ * launched cooperatively (all resident, or none), and every wait is bounded: one that runs
+ * out (about a second: a device that has stopped) sets MOE_DEVERR_TIMEOUT in the workspace,
+ * which is to be initialised again after that. */
 moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, const void *W2, int T,
                              int d, int n, moe_act_t act, moe_dtype_t type, void *Y, void *ws,
                              size_t ws_bytes, void *stream);
@@ -567,8 +571,9 @@ moe_status_t moe_ffn_forward(const void *X, const void *W1, const void *W3, cons
  * F1 = A3 act'(A1) and F3 = act(A1) in fp32, each a buffer of moe_ffn_saved_floats(T, n)
  * floats (16-byte aligned) in blocks of 32 tokens x 32 columns: element (t, j) lies at float
  *   ((t / 32) * ceil(n / 32) + j / 32) * 1024 + (j % 32) / 4 * 128 + (t % 32) * 4 + j % 4
- * (what lies in the blocks past T and n is not defined). ws: a workspace for training.
- * Two kernels. */
+ * (what lies in the blocks past T and n is not defined). The factors take four times H's
+ * memory (470 MB for 4096 tokens, n = 14336) until the backward; in 16 bits dA1 and dA3 would
+ * be rounded twice. ws: a workspace for training. Two kernels. */
 size_t moe_ffn_saved_floats(int T, int n);
 moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3, const void *W2,
                                    int T, int d, int n, moe_act_t act, moe_dtype_t type, void *Y,
@@ -578,7 +583,8 @@ moe_status_t moe_ffn_forward_train(const void *X, const void *W1, const void *W3
 /* The gradients, with G = dY W2^T, dA1 = G F1, dA3 = G F3:
  *   dX = dA1 W1^T + dA3 W3^T, dW1 = X^T dA1, dW3 = X^T dA3, dW2 = H^T dY
  * all of `type`, each rounded once after an fp32 sum (dA1 and dA3 are rounded to
- * `type` as operands). dX may be NULL; dW1, dW3 and dW2 are all given or all NULL.
+ * `type` as operands; in fp16, values of theirs below 2^-14 lose bits, as any fp16 gradient's
+ * do, and a scaled loss keeps them). dX may be NULL; dW1, dW3 and dW2 are all given or all NULL.
  * act: the forward's (F1 and F3 hold it). T = 0 gives zero weight gradients. ws: a workspace for training. Three kernels
  * (one fewer without dX, or without the weight gradients). Deterministic. */
 moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,

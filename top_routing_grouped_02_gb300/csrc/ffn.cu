@@ -26,9 +26,10 @@
 // reduction, 746 against 571 us for dX of 4096 tokens, d = 4096, n = 14336.)
 // Measured, 4096 tokens, d = 4096, n = 14336 bf16 under the power cap: gate/up 570-600 us
 // (1.6-1.7 PFLOP/s), down 270-280, dA1 and dA3 300-310, dX 530-550, weight gradients
-// 770-800. 777 tokens, 1000 x 2728: 24.5, 15, 16.5, 19 and 19.5 us with 5 us of MMAs each;
-// the rest is the start (1 us), the ring's fill (2-3), the last epilogue (1.5-4) or the join
-// (5), and the end (1.5).
+// 770-800. 777 tokens, 1000 x 2728: 24.5, 15, 16.5, 19 and 19.5 us, of which a pair's longest
+// run of k-blocks (32, 11, 16, 22 and 26, at 0.33 us each; gate and the weight gradients are
+// two waves) takes 10.7, 3.7, 5.3, 7.3 and 8.7; the rest is the start (1 us), the ring's fill
+// (2-3), the last epilogue (1.5-4) or the join (5), and the end (1.5).
 // All tails (T, d, n need not be multiples of a tile) are left to TMA: loads
 // outside a tensor give zeros, which add nothing, and stores outside write nothing.
 //

@@ -8,16 +8,17 @@
 // Both are bound by HBM: the forward reads x and writes y once, the backward
 // reads x, dy (and dres) and writes dx once. A group of warps takes a row at a time
 // from a ring of rows in shared memory, which is filled asynchronously ahead of it.
-// Measured, 8192 x 7168 bf16: forward 37 us (6.3 TB/s), backward with dres 84 us
-// (5.6 TB/s), the sum of the weights' partials 4.5 us; rows of 7167: 64 and 133 us (106
-// without dres), bound by the shifts' instructions; 4096 x 4096: 16.4, 22 and 4 us, of
-// which some 6, 7 and 3 us are the start and end of each kernel.
+// Measured, calls back to back, 8192 x 7168 bf16: forward 40 us (5.9 TB/s), backward with
+// dres and the sum of the weights' partials 87 us (5.4 TB/s); rows of 7167: 65 and 141 us
+// (109 without dres), bound by the shifts' instructions; 4096 x 4096: 15 and 28 us, of
+// which some 6 and 10 are the starts and ends of the kernels. The partials' sum takes 4.
 //
 // Row statistics: each warp takes the mean and the squared deviations from its own mean
 // of its elements, and the warps' pairs are joined by
 //   m = sum n_w m_w / d,  M2 = sum (M2_w + n_w (m_w - m)^2),
 // one exchange through shared memory a row, with no subtraction of large equal
-// numbers: a row whose offset is far larger than its spread keeps its variance.
+// numbers: a row whose offset is far larger than its spread keeps its variance. The
+// backward takes x - m before it scales, for the same reason.
 //
 // Weight gradients: each thread owns its columns and sums them over the rows of
 // its group in fp32 registers; the groups of a block are added in a fixed order
@@ -579,7 +580,8 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
         auto vec_y = [&](int i) { return SHIFT ? image_vec<T>(stage + row_bytes, i * tpr + t, sy) : py[i * tpr]; };
         auto vec_r = [&](int i) { return SHIFT ? image_vec<T>(stage + 2 * row_bytes, i * tpr + t, sr) : pr[i * tpr]; };
         // xh = (x - m) r, the difference first: of x r and m r, both far larger where the
-        // row's offset is far above its spread, nothing but rounding would be left
+        // row's offset is far above its spread, nothing but rounding would be left (one
+        // operation a pair and pass: 8192 x 7168 bf16 86.1 -> 86.5 us, 7167 137 -> 141)
         const f32x2 r2 = both(rstd), shift = both(-mean);
         f32x2 p1 = 0, p2 = alive ? 0 : both(NAN);
         constexpr bool KEEP = sizeof(T) == 4;  // xh and dy stay in registers (16 bits: too many)
@@ -851,8 +853,8 @@ int row_groups(int wpr, int threads) { return std::max(1, threads / (32 * wpr));
 // SMs. False where `least` stages of one group do not fit the shared memory. (SHIFT fetches
 // a group's next row as soon as all of its threads are done with the last, so one stage
 // will do, and more groups with one beat fewer with two: 8192 x 7167 bf16, one group with
-// two stages against two with one, backward 164 / 133 us; three against four groups,
-// forward 68 / 64. Otherwise a stage is free only at the next row's barrier.)
+// two stages against two with one, backward 174 / 141 us; three against four groups,
+// forward 69 / 65. Otherwise a stage is free only at the next row's barrier.)
 constexpr size_t kRingSmem = 224 * 1024;
 // `fixed` bytes a block, `extra` a group, `stage` a stage.
 bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t extra, size_t stage,
