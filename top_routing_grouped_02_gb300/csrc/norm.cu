@@ -17,7 +17,8 @@
 // of its elements, and the warps' pairs are joined by
 //   m = sum n_w m_w / d,  M2 = sum (M2_w + n_w (m_w - m)^2),
 // one exchange through shared memory a row, with no subtraction of large equal
-// numbers: a row whose offset is far larger than its spread keeps its variance. The
+// numbers: a row whose offset is far larger than its spread keeps its variance (to within
+// 2^-24 of their ratio: the warps' means are rounded; y is off by as much through m). The
 // backward takes x - m before it scales, for the same reason.
 //
 // Weight gradients: each thread owns its columns and sums them over the rows of
