@@ -593,6 +593,35 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
                               void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
                               void *stream);
 
+/* ---- Token rows to the rows sorted by expert and back, for experts of any kind (the layer's
+ * own GEMMs gather their rows and apply the weights themselves). row_of_slot [T*K] int32 as
+ * moe_permute writes it: the sorted row of slot t*K+k, distinct for distinct slots; a value
+ * outside [0, rows) is a slot without a row. Matrices of `type` with row strides in elements
+ * (any alignment of a whole element); 1 <= K <= 8, T*K < 2^31, T >= 0 (0: nothing is
+ * enqueued). Sums in fp32, k ascending, one rounding; no atomics. One kernel each.
+ *
+ * Dispatch: xg[row_of_slot[t*K+k],:] = x[t,:]. x [T,d], xg [rows,d]; rows of xg that no slot
+ * names are left as they were. */
+moe_status_t moe_dispatch(const void *x, int64_t ldx, const int32_t *row_of_slot, int64_t T, int K,
+                          int d, moe_dtype_t type, void *xg, int64_t ldxg, int64_t rows,
+                          void *stream);
+/* Combine: y[t,:] = sum_k w[t*K+k] z[row_of_slot[t*K+k],:] (+ residual[t,:]) over the slots
+ * that have a row. z [rows,d]; w [T*K] fp32, or NULL for ones: the sum is then the gradient of
+ * moe_dispatch (z: the gradient of xg, residual: a gradient that reaches x by another branch).
+ * residual, y [T,d]; y may be residual (same stride). */
+moe_status_t moe_combine_weighted(const void *z, int64_t ldz, int64_t rows,
+                                  const int32_t *row_of_slot, const float *w, const void *residual,
+                                  int64_t ldr, int64_t T, int K, int d, moe_dtype_t type, void *y,
+                                  int64_t ldy, void *stream);
+/* Its gradients: dz[row_of_slot[t*K+k],:] = w[t*K+k] dy[t,:] and dw[t*K+k] = the dot product of
+ * dy[t,:] and z[row_of_slot[t*K+k],:], 0 for a slot without a row (the residual's gradient is
+ * dy). dz [rows,d]: rows that no slot names are left as they were; it may be z (same stride).
+ * dw [T*K] fp32. */
+moe_status_t moe_combine_weighted_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                                           int64_t rows, const int32_t *row_of_slot, const float *w,
+                                           int64_t T, int K, int d, moe_dtype_t type, void *dz,
+                                           int64_t lddz, float *dw, void *stream);
+
 /* Failure-detection self-test: enqueues one CTA that waits, through the same
  * bounded wait as the GEMM pipelines, on a barrier nothing arrives at. After
  * the wait limit (about 1 s) it sets MOE_DEVERR_TIMEOUT in the workspace's

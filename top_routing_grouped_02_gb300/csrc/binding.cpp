@@ -304,6 +304,95 @@ PyObject *dropout_backward(PyObject *const *a, Py_ssize_t n) {
     return wrap(dx);
 }
 
+// The map of slots onto sorted rows.
+const int32_t *slots_of(const at::Tensor &t, int64_t slots) {
+    if (!t.is_cuda() || t.scalar_type() != at::kInt || !t.is_contiguous() || t.numel() != slots)
+        refuse(PyExc_ValueError, "%s must hold one contiguous int32 value a slot", "row_of_slot");
+    return static_cast<const int32_t *>(t.data_ptr());
+}
+// Rows in another order than the first tensor's: as long and of its type.
+Rows sorted_rows(const at::Tensor &t, const at::Tensor &like, int64_t d, const char *name) {
+    const Rows r = rows_of(t, name);
+    if (t.dim() != 2 || r.d != d || t.scalar_type() != like.scalar_type())
+        refuse(PyExc_ValueError, "%s must be a matrix of rows of the call's length and type", name);
+    return r;
+}
+int slots_a_token(int64_t K) {
+    if (K < 1 || K > INT32_MAX) refuse(PyExc_ValueError, "%s must be positive", "K");
+    return (int)K;
+}
+
+// x, row_of_slot, K, xg, stream
+PyObject *dispatch(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 5);
+    const at::Tensor x = tensor(a[0], "x"), map = tensor(a[1], "row_of_slot"), given = optional_tensor(a[3], "xg");
+    one_device({x, "x"}, {{map, "row_of_slot"}, {given, "xg"}}, a[4]);
+    const Rows rx = rows_of(x, "x");
+    const int K = slots_a_token(integer(a[2]));
+    const int32_t *pm = slots_of(map, rx.T * K);
+    const OnStream stream(a[4], x);
+    const at::Tensor xg = given.defined() ? given : fresh({rx.T * K, rx.d}, x.scalar_type(), x);
+    const Rows rg = sorted_rows(xg, x, rx.d, "xg");
+    check("moe_dispatch", moe_dispatch(rx.p, rx.ld, pm, rx.T, K, (int)rx.d, dtype(x), rg.p, rg.ld, rg.T, stream));
+    return wrap(xg);
+}
+
+// z, row_of_slot, w or the slots a token, residual, y, stream
+PyObject *combine_weighted(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 6);
+    const at::Tensor z = tensor(a[0], "z"), map = tensor(a[1], "row_of_slot"),
+                     res = optional_tensor(a[3], "residual"), given = optional_tensor(a[4], "y");
+    at::Tensor w;
+    int K;
+    if (PyLong_Check(a[2])) {
+        K = slots_a_token(integer(a[2]));
+    } else {
+        w = tensor(a[2], "w");
+        if (w.dim() != 2) refuse(PyExc_ValueError, "%s must be [T, K]", "w");
+        K = slots_a_token(w.size(1));
+    }
+    one_device({z, "z"}, {{map, "row_of_slot"}, {w, "w"}, {res, "residual"}, {given, "y"}}, a[5]);
+    const Rows rz = rows_of(z, "z");
+    sorted_rows(z, z, rz.d, "z");
+    const int64_t T = map.numel() / K;
+    const int32_t *pm = slots_of(map, T * K);
+    const float *pw = w.defined() ? stat_of(w, T * K, "w") : nullptr;
+    const OnStream stream(a[5], z);
+    Rows rr{};
+    if (res.defined()) rr = sorted_rows(res, z, rz.d, "residual");
+    const at::Tensor y = given.defined() ? given : fresh({T, rz.d}, z.scalar_type(), z);
+    const Rows ry = sorted_rows(y, z, rz.d, "y");
+    if (ry.T != T || (res.defined() && rr.T != T))
+        refuse(PyExc_ValueError, "%s must have one row a token", ry.T != T ? "y" : "residual");
+    check("moe_combine_weighted",
+          moe_combine_weighted(rz.p, rz.ld, rz.T, pm, pw, rr.p, rr.ld, T, K, (int)rz.d, dtype(z), ry.p, ry.ld,
+                               stream));
+    return wrap(y);
+}
+
+// dy, z, row_of_slot, w, dz, stream
+PyObject *combine_weighted_backward(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 6);
+    const at::Tensor dy = tensor(a[0], "dy"), z = tensor(a[1], "z"), map = tensor(a[2], "row_of_slot"),
+                     w = tensor(a[3], "w"), given = optional_tensor(a[4], "dz");
+    one_device({dy, "dy"}, {{z, "z"}, {map, "row_of_slot"}, {w, "w"}, {given, "dz"}}, a[5]);
+    if (w.dim() != 2) refuse(PyExc_ValueError, "%s must be [T, K]", "w");
+    const int K = slots_a_token(w.size(1));
+    const Rows rdy = rows_of(dy, "dy"), rz = sorted_rows(z, dy, rdy.d, "z");
+    const int64_t T = rdy.T;
+    const int32_t *pm = slots_of(map, T * K);
+    const float *pw = stat_of(w, T * K, "w");
+    const OnStream stream(a[5], dy);
+    const at::Tensor dz = given.defined() ? given : fresh({rz.T, rz.d}, z.scalar_type(), z);
+    const Rows rdz = sorted_rows(dz, dy, rdy.d, "dz");
+    if (rdz.T != rz.T) refuse(PyExc_ValueError, "%s must have z's shape", "dz");
+    const at::Tensor dw = fresh({T, K}, at::kFloat, dy);
+    check("moe_combine_weighted_backward",
+          moe_combine_weighted_backward(rdy.p, rdy.ld, rz.p, rz.ld, rz.T, pm, pw, T, K, (int)rz.d, dtype(z),
+                                        rdz.p, rdz.ld, static_cast<float *>(dw.data_ptr()), stream));
+    return wrap_all(dz, dw);
+}
+
 // The feed-forward block's operands.
 struct Ffn {
     at::Tensor x, W1, W3, W2, ws;
@@ -415,7 +504,9 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define MOE_ENTRY(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MOE_ENTRY(layernorm), MOE_ENTRY(layernorm_backward), MOE_ENTRY(dropout),
                            MOE_ENTRY(dropout_backward), MOE_ENTRY(ffn), MOE_ENTRY(ffn_train),
-                           MOE_ENTRY(ffn_backward), MOE_ENTRY(set_error),
+                           MOE_ENTRY(ffn_backward), MOE_ENTRY(dispatch),
+                           MOE_ENTRY(combine_weighted), MOE_ENTRY(combine_weighted_backward),
+                           MOE_ENTRY(set_error),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

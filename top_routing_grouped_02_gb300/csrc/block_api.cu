@@ -58,6 +58,21 @@ moe_status_t drop(const void *x, int64_t ldx, const void *res, int64_t ldr, int6
                                     type, as_stream(stream)));
 }
 
+// The shape of a map of T x K slots onto `rows` sorted rows of d elements.
+moe_status_t check_slots(const int32_t *row_of_slot, int64_t T, int K, int d, int64_t rows,
+                         moe_dtype_t type) {
+    moe_status_t st = check_shape(T, d, type);
+    if (st != MOE_OK) return st;
+    if (K < 1 || rows < 0 || !aligned(row_of_slot, 4) || (row_of_slot == nullptr && T > 0))
+        return MOE_ERR_INVALID_ARG;
+    if (K > kMaxK || T > INT32_MAX / K) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+// A matrix of sorted rows; there may be none of them.
+moe_status_t check_sorted(const void *p, int64_t ld, int64_t rows, int d, moe_dtype_t type) {
+    return rows == 0 ? MOE_OK : check_matrix(p, ld, rows, d, type);
+}
+
 // The row that this thread's next layer norm withholds (moe_selftest_layernorm_withhold).
 thread_local int64_t t_withheld = -1;
 int64_t take_withheld() {
@@ -200,6 +215,86 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
                                   uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                                   moe_dtype_t type, void *dx, int64_t lddx, void *stream) {
     return drop(dy, lddy, nullptr, 0, T, d, p, seed, offset, offset_dev, type, dx, lddx, stream);
+}
+
+moe_status_t moe_dispatch(const void *x, int64_t ldx, const int32_t *row_of_slot, int64_t T, int K,
+                          int d, moe_dtype_t type, void *xg, int64_t ldxg, int64_t rows,
+                          void *stream) {
+    moe_status_t st = check_slots(row_of_slot, T, K, d, rows, type);
+    if (st != MOE_OK || T == 0) return st;
+    if ((st = check_matrix(x, ldx, T, d, type)) != MOE_OK) return st;
+    if ((st = check_sorted(xg, ldxg, rows, d, type)) != MOE_OK) return st;
+    if (x == xg) return MOE_ERR_INVALID_ARG;
+    if ((st = check_arch()) != MOE_OK || rows == 0) return st;
+    RowArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.row_of_slot = row_of_slot;
+    a.out = xg;
+    a.ldo = ldxg;
+    a.T = T;
+    a.rows = rows;
+    a.K = K;
+    a.d = d;
+    return from_cuda(launch_dispatch(a, type, as_stream(stream)));
+}
+
+moe_status_t moe_combine_weighted(const void *z, int64_t ldz, int64_t rows,
+                                  const int32_t *row_of_slot, const float *w, const void *residual,
+                                  int64_t ldr, int64_t T, int K, int d, moe_dtype_t type, void *y,
+                                  int64_t ldy, void *stream) {
+    moe_status_t st = check_slots(row_of_slot, T, K, d, rows, type);
+    if (st != MOE_OK) return st;
+    if (!aligned(w, 4)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((st = check_sorted(z, ldz, rows, d, type)) != MOE_OK) return st;
+    if ((st = check_matrix(y, ldy, T, d, type)) != MOE_OK) return st;
+    if (residual != nullptr && (st = check_matrix(residual, ldr, T, d, type)) != MOE_OK) return st;
+    if (z == y || strides_clash(residual, ldr, y, ldy, T)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_arch()) != MOE_OK) return st;
+    RowArgs a{};
+    a.z = z;
+    a.ldz = ldz;
+    a.rows = rows;
+    a.row_of_slot = row_of_slot;
+    a.w = w;
+    a.res = residual;
+    a.ldr = ldr;
+    a.out = y;
+    a.ldo = ldy;
+    a.T = T;
+    a.K = K;
+    a.d = d;
+    return from_cuda(launch_sum_rows(a, type, as_stream(stream)));
+}
+
+moe_status_t moe_combine_weighted_backward(const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                                           int64_t rows, const int32_t *row_of_slot, const float *w,
+                                           int64_t T, int K, int d, moe_dtype_t type, void *dz,
+                                           int64_t lddz, float *dw, void *stream) {
+    moe_status_t st = check_slots(row_of_slot, T, K, d, rows, type);
+    if (st != MOE_OK || T == 0) return st;
+    if (w == nullptr || dw == nullptr || !aligned(w, 4) || !aligned(dw, 4)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_matrix(dy, lddy, T, d, type)) != MOE_OK) return st;
+    if ((st = check_sorted(z, ldz, rows, d, type)) != MOE_OK) return st;
+    if ((st = check_sorted(dz, lddz, rows, d, type)) != MOE_OK) return st;
+    if (dy == dz || strides_clash(z, ldz, dz, lddz, rows)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_arch()) != MOE_OK) return st;
+    RowArgs a{};
+    a.x = dy;
+    a.ldx = lddy;
+    a.z = z;
+    a.ldz = ldz;
+    a.rows = rows;
+    a.row_of_slot = row_of_slot;
+    a.w = w;
+    a.out = dz;
+    a.ldo = lddz;
+    a.dw = dw;
+    a.T = T;
+    a.K = K;
+    a.d = d;
+    return from_cuda(launch_combine_backward(a, type, as_stream(stream)));
 }
 
 size_t moe_ffn_workspace_bytes(int T, int d, int n, int train) {

@@ -265,6 +265,24 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
                                 void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
                                 uint32_t *ticket, uint32_t *err, cudaStream_t s);
 
+// Token rows and rows sorted by expert (dispatch.cu). x: by token (the dispatch's input, the
+// combine's gradient); z: by sorted row; out: by sorted row, or (x NULL) by token; res, w may
+// be NULL.
+struct RowArgs {
+    const void *x, *z, *res;
+    const int32_t *row_of_slot;
+    const float *w;
+    void *out;
+    float *dw;
+    int64_t ldx, ldz, ldr, ldo;
+    int64_t T, rows;
+    int K, d;
+    int split;  // warps a token
+};
+cudaError_t launch_dispatch(const RowArgs &a, moe_dtype_t type, cudaStream_t s);
+cudaError_t launch_sum_rows(const RowArgs &a, moe_dtype_t type, cudaStream_t s);
+cudaError_t launch_combine_backward(const RowArgs &a, moe_dtype_t type, cudaStream_t s);
+
 // One CTA whose pipeline wait on a barrier nothing arrives at runs out after the
 // wait limit (about 1 s) and sets MOE_DEVERR_TIMEOUT in *err.
 cudaError_t launch_wait_timeout_selftest(uint32_t *err, cudaStream_t s);

@@ -13,6 +13,8 @@ struct RawOf;
 template <>
 struct RawOf<16> { using type = uint4; };
 template <>
+struct RawOf<8> { using type = uint2; };
+template <>
 struct RawOf<4> { using type = uint32_t; };
 template <>
 struct RawOf<2> { using type = uint16_t; };
@@ -57,6 +59,9 @@ __device__ __forceinline__ void to_f32(const Raw<T, V> &r, float *f) {
             f[1] = __uint_as_float(r.y);
             f[2] = __uint_as_float(r.z);
             f[3] = __uint_as_float(r.w);
+        } else if constexpr (V == 2) {
+            f[0] = __uint_as_float(r.x);
+            f[1] = __uint_as_float(r.y);
         } else {
             f[0] = __uint_as_float(r);
         }
@@ -65,6 +70,9 @@ __device__ __forceinline__ void to_f32(const Raw<T, V> &r, float *f) {
         unpack2<T>(r.y, f[2], f[3]);
         unpack2<T>(r.z, f[4], f[5]);
         unpack2<T>(r.w, f[6], f[7]);
+    } else if constexpr (V == 4) {
+        unpack2<T>(r.x, f[0], f[1]);
+        unpack2<T>(r.y, f[2], f[3]);
     } else if constexpr (V == 2) {
         unpack2<T>(r, f[0], f[1]);
     } else {
@@ -78,11 +86,15 @@ __device__ __forceinline__ Raw<T, V> from_f32(const float *f) {
         if constexpr (V == 4)
             return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                               __float_as_uint(f[3]));
+        else if constexpr (V == 2)
+            return make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
         else
             return __float_as_uint(f[0]);
     } else if constexpr (V == 8) {
         return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
                           pack2<T>(f[6], f[7]));
+    } else if constexpr (V == 4) {
+        return make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
     } else if constexpr (V == 2) {
         return pack2<T>(f[0], f[1]);
     } else {

@@ -32,7 +32,8 @@ LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_g
             "moe_backward_router": 5, "moe_backward_dw": 5,
             "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1,
             "moe_layernorm": 1, "moe_layernorm_backward": 2, "moe_dropout": 1,
-            "moe_dropout_backward": 1, "moe_ffn": 2, "moe_ffn_train": 2, "moe_ffn_backward": 3}
+            "moe_dropout_backward": 1, "moe_ffn": 2, "moe_ffn_train": 2, "moe_ffn_backward": 3,
+            "moe_dispatch": 1, "moe_combine_weighted": 1, "moe_combine_weighted_backward": 1}
 TILE_M = 128
 
 
@@ -102,6 +103,10 @@ _SIGS = {
                                    _P]),
     "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
                               _P, _SZ, _P]),
+    "moe_dispatch": (_I, [_P, _L, _P, _L, _I, _I, _I, _P, _L, _L, _P]),
+    "moe_combine_weighted": (_I, [_P, _L, _L, _P, _P, _P, _L, _L, _I, _I, _I, _P, _L, _P]),
+    "moe_combine_weighted_backward": (_I, [_P, _L, _P, _L, _L, _P, _P, _L, _I, _I, _I, _P, _L, _P,
+                                           _P]),
     "moe_round_capacity": (ctypes.c_int64, [_I, _I, _I, _I]),
     "moe_round_workspace_bytes": (_SZ, [_I, _I]),
     "moe_round_routing": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
@@ -692,3 +697,32 @@ def moe_ffn_backward(dY, x, W1, W3, W2, H, F1, F3, act: str = "silu", need_dx: b
     for). ws: ffn_workspace(..., train=True)."""
     return _native().ffn_backward(dY, x, W1, W3, W2, H, F1, F3, _act(act), need_dx, need_dw,
                                   _ffn_ws(ws, x, W1, True, stream), stream)
+
+# ------------------------- rows sorted by expert and back, for experts of any kind
+
+
+def moe_dispatch(x, row_of_slot, K: int, xg=None, stream=None):
+    """xg [T*K, d]: every token's row of x [..., d] at the rows of its K slots, with
+    row_of_slot as moe_permute gives it (a value outside xg's rows: no row). Rows that no
+    slot names are left as they were: not defined in a new xg."""
+    return _native().dispatch(x, row_of_slot, K, xg, stream)
+
+
+def moe_dispatch_backward(dxg, row_of_slot, K: int, residual=None, dx=None, stream=None):
+    """dx [T, d]: the sum of dxg over each token's rows (+ residual, a gradient that reaches
+    x by another branch)."""
+    return _native().combine_weighted(dxg, row_of_slot, int(K), residual, dx, stream)
+
+
+def moe_combine_weighted(z, row_of_slot, w, residual=None, y=None, stream=None):
+    """y [T, d] = sum over k of w[t, k] times the row of slot (t, k) of z [rows, d]
+    (+ residual); w [T, K] fp32 as moe_route gives it. y may be residual."""
+    if not torch.is_tensor(w):
+        raise TypeError("w must be a tensor")
+    return _native().combine_weighted(z, row_of_slot, w, residual, y, stream)
+
+
+def moe_combine_weighted_backward(dy, z, row_of_slot, w, dz=None, stream=None):
+    """(dz [rows, d], dw [T, K] fp32) of moe_combine_weighted (the residual's gradient is
+    dy). Rows of dz that no slot names are left as they were: not defined in a new dz."""
+    return _native().combine_weighted_backward(dy, z, row_of_slot, w, dz, stream)
