@@ -593,6 +593,51 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
                               void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
                               void *stream);
 
+/* ---- The norms around a block, with its gate and the residual scale, in one pass over the
+ * stream: behind a block whose output is b, and in front of the next one,
+ *   n = post bh,            bh = b / sqrt(mean(b^2) + eps)   (MOE_NORM_POST; else bh = b)
+ *   y = scale x + g n,      g = sigmoid(gate), or 1
+ *   u = pre yh,             yh = y / sqrt(mean(y^2) + eps)   (MOE_NORM_PRE; else no u)
+ * means over the row. With b NULL: u = pre yh of y = x alone, an RMS norm (then no gate, no
+ * post, no y, MOE_NORM_PRE and scale 1).
+ * x, b, y, u [T,d] of `type`, row strides in elements (any alignment of a whole element);
+ * post, pre [d] of wtype (type or MOE_DTYPE_F32) or NULL (ones; without MOE_NORM_POST, post
+ * scales the channels of b). gate: MOE_GATE_ROW one fp32 value a row; MOE_GATE_FULL [T,d] of
+ * `type`. Arithmetic and statistics in fp32; y and u are rounded once each, u from the fp32 y.
+ * rstd_post, rstd_pre [T] fp32 or NULL: 1 / sqrt(mean + eps), which the backward takes.
+ * T >= 0 (0: nothing is enqueued), 1 <= d <= 16384, eps >= 0. y and u may each be one of x, b
+ * and the full gate (same stride). One kernel. Rows come through waits bounded as layer norm's. */
+enum { MOE_NORM_POST = 1, MOE_NORM_PRE = 2 };
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_ROW = 1, MOE_GATE_FULL = 2 } moe_gate_t;
+moe_status_t moe_block_norm_forward(const void *x, int64_t ldx, const void *b, int64_t ldb,
+                                    const void *gate, int64_t ldgate, moe_gate_t gate_kind,
+                                    const void *post, const void *pre, float scale, int norms,
+                                    int64_t T, int d, float eps, moe_dtype_t type,
+                                    moe_dtype_t wtype, void *y, int64_t ldy, void *u, int64_t ldu,
+                                    float *rstd_post, float *rstd_pre, void *stream);
+
+/* Its gradients. dy: the gradient that reaches y by the stream (NULL: none; then
+ * MOE_NORM_PRE); du: that of u (with MOE_NORM_PRE, else NULL). With e = pre du,
+ *   dY = dy + r_pre (e - yh mean(e yh)),  f = g dY post
+ *   dx = scale dY,  db = r_post (f - bh mean(f bh)),  dgate = f bh (1 - g)
+ *   dpost = sum over rows of g dY bh,  dpre = sum over rows of du yh
+ * (a row's dgate summed over the row). rstd_post, rstd_pre as the forward gave them (those of
+ * its norms). dx, db [T,d], dgate like the gate (those of the operands that there are); dpost,
+ * dpre [d] of wtype, each may be NULL: summed in fp32 in a fixed order, 0 for T = 0. dx, db
+ * and a full dgate may each be one of the call's matrices (same stride). scratch:
+ * moe_block_norm_scratch_bytes(T, d) bytes, 256-byte aligned, needed with dpost or dpre; its
+ * content on entry does not matter. Two kernels (one without dpost and dpre). */
+size_t moe_block_norm_scratch_bytes(int64_t T, int d);
+moe_status_t moe_block_norm_backward(const void *dy, int64_t lddy, const void *du, int64_t lddu,
+                                     const void *x, int64_t ldx, const void *b, int64_t ldb,
+                                     const void *gate, int64_t ldgate, moe_gate_t gate_kind,
+                                     const void *post, const void *pre, float scale, int norms,
+                                     const float *rstd_post, const float *rstd_pre, int64_t T, int d,
+                                     moe_dtype_t type, moe_dtype_t wtype, void *dx, int64_t lddx,
+                                     void *db, int64_t lddb, void *dgate, int64_t lddgate,
+                                     void *dpost, void *dpre, void *scratch, size_t scratch_bytes,
+                                     void *stream);
+
 /* ---- Token rows to the rows sorted by expert and back, for experts of any kind (the layer's
  * own GEMMs gather their rows and apply the weights themselves). row_of_slot [T*K] int32 as
  * moe_permute writes it: the sorted row of slot t*K+k, distinct for distinct slots; a value

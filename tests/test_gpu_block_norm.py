@@ -1,0 +1,267 @@
+"""The norms around a block, and their gradients, against the 64-bit formulas."""
+import pytest
+import torch
+
+import norms_common as plain
+from block_common import assert_close, matrix
+from top_routing_grouped_02_gb300 import moe
+
+pytestmark = pytest.mark.gpu
+
+BF, FP16, F32 = torch.bfloat16, torch.float16, torch.float32
+EPS = 1e-6
+
+# T, d, type, weights' type, gate, (post norm, pre norm), scale, row stride
+CASES = [
+    (1, 1, F32, F32, "row", (1, 1), 1.0, None), (3, 2, BF, BF, None, (1, 1), 1.0, None),
+    (5, 7, FP16, F32, "full", (1, 1), 0.5, None), (4, 8, BF, F32, "full", (1, 1), 1.0, None),
+    (33, 31, F32, F32, "row", (1, 1), -2.0, 33), (70, 33, BF, BF, "full", (1, 1), 1.0, None),
+    (9, 255, FP16, FP16, None, (1, 1), 2.5, 258), (300, 256, BF, BF, "full", (1, 1), 1.0, None),
+    (300, 520, FP16, F32, "row", (1, 1), 1.0, 528), (2000, 64, BF, F32, "full", (1, 1), 1.0, None),
+    (64, 1000, BF, BF, "full", (1, 0), 1.0, None), (64, 1000, FP16, FP16, "row", (0, 1), 0.7, None),
+    (40, 1000, BF, F32, None, (0, 0), 1.0, None), (40, 96, F32, F32, "full", (0, 1), 1.0, 100),
+    (257, 1023, F32, F32, "row", (1, 1), 0.5, None), (31, 1536, BF, BF, "full", (1, 1), 1.0, 1600),
+    (5, 2047, BF, BF, "row", (1, 1), 1.0, 2049), (5, 2049, FP16, F32, "full", (1, 1), 1.0, None),
+    (170, 4096, BF, BF, "row", (1, 1), 1.0, None), (4, 4096, F32, F32, "full", (1, 1), 1.0, None),
+    (160, 7168, BF, BF, "full", (1, 1), 1.0, None), (160, 7168, FP16, F32, "full", (1, 1), 1.0, None),
+    (3, 7167, BF, BF, "full", (1, 1), 1.0, None), (310, 8192, BF, F32, "row", (1, 1), 1.0, None),
+    (2, 16384, F32, F32, "full", (1, 1), 1.0, None), (2, 16384, BF, BF, "full", (1, 1), 1.0, None),
+    (2, 16381, BF, F32, "row", (1, 1), 1.0, None), (3, 12000, BF, BF, "full", (1, 1), 1.0, None),
+]
+IDS = [f"T{c[0]}d{c[1]}-{str(c[2])[6:]}-{c[4]}-{c[5][0]}{c[5][1]}-ld{c[7] or c[1]}" for c in CASES]
+
+
+def inputs(case):
+    T, d, dt, wt, gate, _, _, ld = case
+    gen = torch.Generator().manual_seed(T * 100003 + d)
+    m = {k: matrix(T, d, dt, gen, ld, scale=s) for k, s in (("x", 2.0), ("b", 0.7), ("dy", 1.0), ("du", 1.0))}
+    m["gate"] = None
+    if gate == "full":
+        m["gate"] = matrix(T, d, dt, gen, ld, scale=2.0)
+    elif gate == "row":
+        m["gate"] = matrix(T, 1, F32, gen, scale=2.0)[:, 0].contiguous()
+    m["post"], m["pre"] = ((1 + 0.3 * torch.randn(d, generator=gen)).to(wt).cuda() for _ in range(2))
+    return m
+
+
+def cpu(m, *names):
+    return [None if m[k] is None else m[k].cpu() for k in names]
+
+
+def check(got, ref, T, zmax, what=""):
+    for name, value in got.items():
+        if value is None:
+            assert name not in ref, name
+            continue
+        want, size = ref[name]
+        c = plain.C[name] + 2 * zmax + (T if name in ("dpost", "dpre") else 0)
+        assert_close(value, want, size, c, what + name)
+
+
+def steepest(gate):
+    """|z| of the gates: what an approximate 2^(z log2 e) may be off by."""
+    return 0.0 if gate is None or gate.numel() == 0 else float(gate.float().abs().max())
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward_and_backward(case):
+    T, d, dt, wt, _, (post_norm, pre_norm), scale, _ = case
+    m = inputs(case)
+    kw = dict(gate=m["gate"], scale=scale)
+    y, u, r_post, r_pre = moe.moe_block_norm(m["x"], m["b"], m["post"], m["pre"] if pre_norm else None, eps=EPS,
+                                             post_norm=bool(post_norm), pre_norm=bool(pre_norm), stats=True, **kw)
+    x, b, post, pre, gate, dy, du = cpu(m, "x", "b", "post", "pre", "gate", "dy", "du")
+    args = (x, b, post, pre, gate, scale, EPS, post_norm, pre_norm)
+    o, z = plain.forward(*args), steepest(gate)
+    assert_close(y, o["y"], o["Y"], plain.C["y"] + 2 * z, "y")
+    assert (r_post is None) == (not post_norm) and (u is None) == (r_pre is None) == (not pre_norm)
+    if post_norm:
+        assert_close(r_post, o["r_post"][:, 0], o["r_post"][:, 0], 20, "rstd_post")
+    if pre_norm:
+        assert_close(u, o["u"], o["U"], plain.C["u"] + 2 * z, "u")
+        assert_close(r_pre, o["r_pre"][:, 0], (o["r_pre"] * o["rho"])[:, 0], plain.C["u"] + 2 * z, "rstd_pre")
+    y2, u2 = moe.moe_block_norm(m["x"], m["b"], m["post"], m["pre"] if pre_norm else None, eps=EPS,
+                                post_norm=bool(post_norm), pre_norm=bool(pre_norm), **kw)
+    assert torch.equal(y2, y) and (u is None or torch.equal(u2, u))
+    names = ("dx", "db", "dgate", "dpost", "dpre")
+    got = moe.moe_block_norm_backward(m["dy"], m["du"] if pre_norm else None, m["x"], m["b"], m["post"],
+                                      m["pre"] if pre_norm else None, r_post, r_pre, **kw)
+    assert got[3].dtype == wt and (got[4] is None or got[4].dtype == wt)
+    check(dict(zip(names, got)), plain.backward(dy, du, *args), T, z)
+    if pre_norm:  # no gradient by the stream
+        alone = moe.moe_block_norm_backward(None, m["du"], m["x"], m["b"], m["post"], m["pre"], r_post, r_pre, **kw)
+        check(dict(zip(names, alone)), plain.backward(None, du, *args), T, z, "alone ")
+    # results in the places of inputs
+    again = moe.moe_block_norm_backward(m["dy"], m["du"] if pre_norm else None, m["x"], m["b"], m["post"],
+                                        m["pre"] if pre_norm else None, r_post, r_pre, dx=m["dy"], db=m["b"], **kw)
+    assert all(p is q is None or torch.equal(p, q) for p, q in zip(got, again))
+    assert again[0].data_ptr() == m["dy"].data_ptr() and again[1].data_ptr() == m["b"].data_ptr()
+    m = inputs(case)
+    y2, u2 = moe.moe_block_norm(m["x"], m["b"], m["post"], m["pre"] if pre_norm else None, eps=EPS, y=m["x"],
+                                post_norm=bool(post_norm), pre_norm=bool(pre_norm), gate=m["gate"], scale=scale,
+                                u=m["b"] if pre_norm else None)
+    assert y2.data_ptr() == m["x"].data_ptr() and torch.equal(y2, y) and (u is None or torch.equal(u2, u))
+
+
+@pytest.mark.parametrize("case", [c for c in CASES if c[4] is None or c[1] in (1, 7, 1023, 2049, 7168, 16384)], ids=str)
+def test_rmsnorm(case):
+    T, d, dt, wt = case[:4]
+    m = inputs(case)
+    x, pre, dy, du = cpu(m, "x", "pre", "dy", "du")
+    u, rstd = moe.moe_rmsnorm(m["x"], m["pre"], EPS, stats=True)
+    o = plain.forward(x, None, None, pre, None, 1.0, EPS)
+    assert_close(u, o["u"], o["U"], plain.C["u"], "y")
+    assert_close(rstd, o["r_pre"][:, 0], o["r_pre"][:, 0], 20, "rstd")
+    assert torch.equal(moe.moe_rmsnorm(m["x"], m["pre"], EPS), u)
+    for res in (None, dy):
+        dx, dgamma = moe.moe_rmsnorm_backward(m["du"], m["x"], m["pre"], rstd, dres=None if res is None else m["dy"])
+        check({"dx": dx, "dpre": dgamma}, plain.backward(res, du, x, None, None, pre, None, 1.0, EPS), T, 0)
+    again, _ = moe.moe_rmsnorm_backward(m["du"], m["x"], m["pre"], rstd, dres=m["dy"], dx=m["du"])
+    assert torch.equal(again, dx)
+    assert torch.equal(moe.moe_rmsnorm(m["x"], m["pre"], EPS, y=m["x"]), u)
+
+
+def test_without_weights():
+    T, d = 37, 200
+    gen = torch.Generator().manual_seed(4)
+    x, b, dy, du = (matrix(T, d, BF, gen) for _ in range(4))
+    y, u, rp, rq = moe.moe_block_norm(x, b, stats=True)
+    o = plain.forward(x.cpu(), b.cpu(), None, None, None, 1.0, EPS)
+    assert_close(y, o["y"], o["Y"], plain.C["y"], "y")
+    assert_close(u, o["u"], o["U"], plain.C["u"], "u")
+    ref = plain.backward(dy.cpu(), du.cpu(), x.cpu(), b.cpu(), None, None, None, 1.0, EPS)
+    for wdtype in (None, BF):
+        dx, db, dgate, dpost, dpre = moe.moe_block_norm_backward(dy, du, x, b, None, None, rp, rq, wdtype=wdtype)
+        assert dpost.dtype == dpre.dtype == (wdtype or F32)
+        check(dict(dx=dx, db=db, dgate=dgate, dpost=dpost, dpre=dpre), ref, T, 0)
+
+
+@pytest.mark.parametrize("d,ld", [(256, 256), (1023, 1023), (7168, 7168)])
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+def test_zero_rows_and_steep_gates(d, ld, dt):
+    """Rows of zeros (the root of eps alone), gates that are shut, open or infinite."""
+    T = 8
+    gen = torch.Generator().manual_seed(d)
+    x, b, dy, du = (matrix(T, d, dt, gen) for _ in range(4))
+    b[0], x[1], b[2], x[2] = 0, 0, 0, 0
+    z = torch.zeros(T, device="cuda")
+    z[3], z[4], z[5], z[6] = float("-inf"), float("inf"), -200.0, 90.0
+    for gate in (z, z[:, None].expand(T, d).to(dt).contiguous()):
+        y, u, rp, rq = moe.moe_block_norm(x, b, gate=gate, eps=EPS, stats=True)
+        got = moe.moe_block_norm_backward(dy, du, x, b, None, None, rp, rq, gate=gate)
+        args = (x.cpu(), b.cpu(), None, None, gate.cpu(), 1.0, EPS)
+        o = plain.forward(*args)
+        assert_close(y, o["y"], o["Y"], 250, "y")
+        assert_close(u, o["u"], o["U"], 300, "u")
+        check(dict(zip(("dx", "db", "dgate", "dpost", "dpre"), got)), plain.backward(dy.cpu(), du.cpu(), *args), T, 200)
+
+
+def test_not_a_number_stays_in_its_row():
+    T, d = 40, 512
+    gen = torch.Generator().manual_seed(2)
+    x, b, gate, dy, du = (matrix(T, d, BF, gen) for _ in range(5))
+    clean = moe.moe_block_norm(x, b, gate=gate)
+    for t, m in ((3, x), (5, b), (7, gate)):
+        m[t, 100] = float("nan")
+    b[9, 0] = float("inf")
+    y, u, rp, rq = moe.moe_block_norm(x, b, gate=gate, stats=True)
+    rows = torch.ones(T, dtype=torch.bool)
+    rows[[3, 5, 7, 9]] = False
+    assert torch.equal(y[rows], clean[0][rows]) and torch.equal(u[rows], clean[1][rows])
+    for t in (3, 5, 7, 9):
+        assert u[t].isnan().all() and y[t].isnan().any()
+    dx, db, dgate, _, _ = moe.moe_block_norm_backward(dy, du, x, b, None, None, rp, rq, gate=gate)
+    for g in (dx, db, dgate):
+        assert g[rows].isfinite().all() and g[3].isnan().all() and g[9].isnan().any()
+
+
+def test_gradients_by_differences():
+    T, d = 6, 72
+    gen = torch.Generator().manual_seed(8)
+    v = {k: torch.randn(T, d, generator=gen).cuda() for k in ("x", "b", "gate")}
+    v |= {k: 1 + 0.2 * torch.randn(d, generator=gen).cuda() for k in ("post", "pre")}
+    dy, du = (torch.randn(T, d, generator=gen).cuda() for _ in range(2))
+
+    def loss(v):
+        y, u = moe.moe_block_norm(**v, scale=0.5)
+        return float((y.double() * dy.double()).sum() + (u.double() * du.double()).sum())
+
+    _, _, rp, rq = moe.moe_block_norm(**v, scale=0.5, stats=True)
+    dx, db, dgate, dpost, dpre = moe.moe_block_norm_backward(dy, du, v["x"], v["b"], v["post"], v["pre"], rp, rq,
+                                                             gate=v["gate"], scale=0.5)
+    for name, grad in dict(x=dx, b=db, gate=dgate, post=dpost, pre=dpre).items():
+        step = torch.randn(grad.shape, generator=gen).cuda()
+        step /= step.norm()
+        h = 2.0 ** -6
+        plus, minus = (loss(v | {name: v[name] + s * step}) for s in (h, -h))
+        want = float((grad.double() * step.double()).sum())
+        # the difference's own error: h^2 / 6 times a third derivative of order 10 per unit
+        # step and output (2 T d outputs of order 1), and fp32 roundings of the outputs over h
+        slack = h * h / 6 * 10 * (2 * T * d) ** 0.5 + 2.0 ** -20 * (2 * T * d) ** 0.5 / h
+        assert abs((plus - minus) / (2 * h) - want) <= slack, (name, (plus - minus) / (2 * h), want)
+
+
+def test_no_rows():
+    x = torch.empty(0, 64, dtype=BF, device="cuda")
+    y, u, rp, rq = moe.moe_block_norm(x, x, gate=x, stats=True)
+    assert y.shape == u.shape == (0, 64) and rp.shape == (0,)
+    out = moe.moe_block_norm_backward(x, x, x, x, None, None, rp, rq, gate=x)
+    assert out[0].shape == out[1].shape == out[2].shape == (0, 64)
+    assert not out[3].any() and not out[4].any() and out[3].shape == (64,)
+
+
+def test_leading_dimensions():
+    gen = torch.Generator().manual_seed(1)
+    x, b = (torch.randn(3, 5, 72, generator=gen).cuda() for _ in range(2))
+    gate = torch.randn(3, 5, generator=gen).cuda()
+    y, u, rp, rq = moe.moe_block_norm(x, b, gate=gate, stats=True)
+    assert y.shape == x.shape and rp.shape == (3, 5)
+    flat = moe.moe_block_norm(x.view(15, 72), b.view(15, 72), gate=gate.view(15))
+    assert torch.equal(y.view(15, 72), flat[0]) and torch.equal(u.view(15, 72), flat[1])
+    dx, db, dgate, _, _ = moe.moe_block_norm_backward(y, u, x, b, None, None, rp, rq, gate=gate)
+    assert dx.shape == db.shape == x.shape and dgate.shape == (3, 5)
+    one = moe.moe_block_norm(x[0, 0], b[0, 0])
+    assert one[0].shape == (72,)
+
+
+def test_offsets_past_32_bits():
+    """Rows more than 2^31 elements into their buffers."""
+    T, d, ld = 35, 64, 1 << 26
+    gen = torch.Generator().manual_seed(6)
+    x, b = (torch.empty(T * ld, dtype=FP16, device="cuda").view(T, ld)[:, :d] for _ in range(2))
+    x.copy_(torch.randn(T, d, generator=gen)), b.copy_(torch.randn(T, d, generator=gen))
+    want = moe.moe_block_norm(x.contiguous(), b.contiguous(), gate=b.contiguous(), stats=True)
+    y, u, rp, rq = moe.moe_block_norm(x, b, gate=b, stats=True, y=torch.empty_like(want[0]))
+    assert torch.equal(y, want[0]) and torch.equal(u, want[1])
+    want = moe.moe_block_norm_backward(y, u, x.contiguous(), b.contiguous(), None, None, rp, rq, gate=b.contiguous())
+    got = moe.moe_block_norm_backward(y, u, x, b, None, None, rp, rq, gate=b, dx=x)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_captured_calls_and_streams():
+    T, d = 300, 1024
+    gen = torch.Generator().manual_seed(11)
+    x, b, gate, dy = (matrix(T, d, BF, gen) for _ in range(4))
+
+    def step():
+        y, u, rp, rq = moe.moe_block_norm(x, b, gate=gate, stats=True)
+        return y, u, *moe.moe_block_norm_backward(dy, u, x, b, None, None, rp, rq, gate=gate)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(2):
+        x.copy_(torch.randn(T, d, generator=gen))
+        graph.replay()
+        for p, q in zip(out, step()):
+            assert torch.equal(p, q)
+    want = moe.moe_block_norm(x, b, gate=gate)
+    side.wait_stream(torch.cuda.current_stream())
+    got = moe.moe_block_norm(x, b, gate=gate, stream=side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))

@@ -304,6 +304,115 @@ PyObject *dropout_backward(PyObject *const *a, Py_ssize_t n) {
     return wrap(dx);
 }
 
+// A block's gate: a matrix like x, or one fp32 value a row.
+struct Gate {
+    moe_gate_t kind = MOE_GATE_NONE;
+    void *p = nullptr;
+    int64_t ld = 0;
+};
+Gate gate_of(const at::Tensor &t, const at::Tensor &x, const Rows &rx, const char *name) {
+    Gate g;
+    if (!t.defined()) return g;
+    if (t.dim() == x.dim()) {
+        const Rows r = rows_of(t, name, &x);
+        g.kind = MOE_GATE_FULL;
+        g.p = r.p;
+        g.ld = r.ld;
+        return g;
+    }
+    if (t.sizes() != x.sizes().slice(0, x.dim() - 1))
+        refuse(PyExc_ValueError, "%s must have x's shape, or that of its rows", name);
+    g.kind = MOE_GATE_ROW;
+    g.p = stat_of(t, rx.T, name);
+    return g;
+}
+Rows rows_if(const at::Tensor &t, const char *name, const at::Tensor &like) {
+    return t.defined() ? rows_of(t, name, &like) : Rows{};
+}
+moe_dtype_t weight_type(const at::Tensor &post, const at::Tensor &pre, const at::Tensor &x) {
+    if (post.defined() && pre.defined() && post.scalar_type() != pre.scalar_type())
+        refuse(PyExc_TypeError, "post and %s must have one type", "pre");
+    return dtype(post.defined() ? post : pre.defined() ? pre : x);
+}
+int norms_of(bool post, bool pre) { return (post ? MOE_NORM_POST : 0) | (pre ? MOE_NORM_PRE : 0); }
+
+// x, b, post, pre, gate, scale, eps, post_norm, pre_norm, stats, y, u, stream
+PyObject *block_norm(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 13);
+    const at::Tensor x = tensor(a[0], "x"), b = optional_tensor(a[1], "b"), post = optional_tensor(a[2], "post"),
+                     pre = optional_tensor(a[3], "pre"), gate = optional_tensor(a[4], "gate"),
+                     given_y = optional_tensor(a[10], "y"), given_u = optional_tensor(a[11], "u");
+    one_device({x, "x"},
+               {{b, "b"}, {post, "post"}, {pre, "pre"}, {gate, "gate"}, {given_y, "y"}, {given_u, "u"}}, a[12]);
+    const Rows rx = rows_of(x, "x"), rb = rows_if(b, "b", x);
+    const OnStream stream(a[12], x);
+    const double scale = number(a[5]), eps = number(a[6]);
+    const bool post_norm = truth(a[7]), pre_norm = truth(a[8]), stats = truth(a[9]);
+    void *pp = vec_of(post, rx.d, x, "post"), *pq = vec_of(pre, rx.d, x, "pre");
+    const moe_dtype_t wt = weight_type(post, pre, x);
+    const Gate g = gate_of(gate, x, rx, "gate");
+    at::Tensor y, u, r_post, r_pre;
+    if (b.defined()) y = output(given_y, x);
+    else if (given_y.defined()) refuse(PyExc_ValueError, "without a block there is no %s", "y");
+    if (pre_norm) u = output(given_u, x);
+    else if (given_u.defined()) refuse(PyExc_ValueError, "without the pre norm there is no %s", "u");
+    const Rows ry = rows_if(y, "y", x), ru = rows_if(u, "u", x);
+    const auto sizes = x.sizes().slice(0, x.dim() - 1);
+    if (stats && post_norm) r_post = fresh(sizes, at::kFloat, x);
+    if (stats && pre_norm) r_pre = fresh(sizes, at::kFloat, x);
+    auto floats = [](const at::Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; };
+    check("moe_block_norm_forward",
+          moe_block_norm_forward(rx.p, rx.ld, rb.p, rb.ld, g.p, g.ld, g.kind, pp, pq, (float)scale,
+                                 norms_of(post_norm, pre_norm), rx.T, (int)rx.d, (float)eps, dtype(x), wt, ry.p,
+                                 ry.ld, ru.p, ru.ld, floats(r_post), floats(r_pre), stream));
+    return wrap_all(y, u, r_post, r_pre);
+}
+
+// dy, du, x, b, post, pre, rstd_post, rstd_pre, gate, scale, fp32 weight gradients without
+// weights, dx, db, scratch, stream
+PyObject *block_norm_backward(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 15);
+    const at::Tensor dy = optional_tensor(a[0], "dy"), du = optional_tensor(a[1], "du"), x = tensor(a[2], "x"),
+                     b = optional_tensor(a[3], "b"), post = optional_tensor(a[4], "post"),
+                     pre = optional_tensor(a[5], "pre"), r_post = optional_tensor(a[6], "rstd_post"),
+                     r_pre = optional_tensor(a[7], "rstd_pre"), gate = optional_tensor(a[8], "gate"),
+                     given_dx = optional_tensor(a[11], "dx"), given_db = optional_tensor(a[12], "db"),
+                     memory = optional_tensor(a[13], "scratch");
+    one_device({x, "x"},
+               {{dy, "dy"}, {du, "du"}, {b, "b"}, {post, "post"}, {pre, "pre"}, {r_post, "rstd_post"},
+                {r_pre, "rstd_pre"}, {gate, "gate"}, {given_dx, "dx"}, {given_db, "db"}, {memory, "scratch"}},
+               a[14]);
+    const Rows rx = rows_of(x, "x"), rb = rows_if(b, "b", x), rdy = rows_if(dy, "dy", x), rdu = rows_if(du, "du", x);
+    const OnStream stream(a[14], x);
+    const double scale = number(a[9]);
+    void *pp = vec_of(post, rx.d, x, "post"), *pq = vec_of(pre, rx.d, x, "pre");
+    moe_dtype_t wt = weight_type(post, pre, x);
+    if (pp == nullptr && pq == nullptr && truth(a[10])) wt = MOE_DTYPE_F32;
+    const Gate g = gate_of(gate, x, rx, "gate");
+    const float *pr = r_post.defined() ? stat_of(r_post, rx.T, "rstd_post") : nullptr;
+    const float *qr = r_pre.defined() ? stat_of(r_pre, rx.T, "rstd_pre") : nullptr;
+    const at::Tensor dx = output(given_dx, x);
+    at::Tensor db, dgate, dpost, dpre;
+    if (b.defined()) db = output(given_db, x);
+    else if (given_db.defined()) refuse(PyExc_ValueError, "without a block there is no %s", "db");
+    if (gate.defined()) dgate = fresh(gate.sizes(), gate.scalar_type(), x);
+    const at::ScalarType wtype = wt == MOE_DTYPE_F32 ? at::kFloat : x.scalar_type();
+    if (b.defined()) dpost = fresh({rx.d}, wtype, x);
+    if (r_pre.defined()) dpre = fresh({rx.d}, wtype, x);
+    const at::Tensor scratch =
+        memory.defined() ? memory
+                         : fresh({(int64_t)moe_block_norm_scratch_bytes(rx.T, (int)rx.d)}, at::kByte, x);
+    if (!scratch.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", "scratch");
+    const Rows rdx = rows_of(dx, "dx", &x), rdb = rows_if(db, "db", x);
+    auto data = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+    check("moe_block_norm_backward",
+          moe_block_norm_backward(rdy.p, rdy.ld, rdu.p, rdu.ld, rx.p, rx.ld, rb.p, rb.ld, g.p, g.ld, g.kind, pp, pq,
+                                  (float)scale, norms_of(r_post.defined(), r_pre.defined()), pr, qr, rx.T,
+                                  (int)rx.d, dtype(x), wt, rdx.p, rdx.ld, rdb.p, rdb.ld, data(dgate), rx.d,
+                                  data(dpost), data(dpre), scratch.data_ptr(), scratch.nbytes(), stream));
+    return wrap_all(dx, db, dgate, dpost, dpre);
+}
+
 // The map of slots onto sorted rows.
 const int32_t *slots_of(const at::Tensor &t, int64_t slots) {
     if (!t.is_cuda() || t.scalar_type() != at::kInt || !t.is_contiguous() || t.numel() != slots)
@@ -504,7 +613,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define MOE_ENTRY(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MOE_ENTRY(layernorm), MOE_ENTRY(layernorm_backward), MOE_ENTRY(dropout),
                            MOE_ENTRY(dropout_backward), MOE_ENTRY(ffn), MOE_ENTRY(ffn_train),
-                           MOE_ENTRY(ffn_backward), MOE_ENTRY(dispatch),
+                           MOE_ENTRY(ffn_backward), MOE_ENTRY(block_norm),
+                           MOE_ENTRY(block_norm_backward), MOE_ENTRY(dispatch),
                            MOE_ENTRY(combine_weighted), MOE_ENTRY(combine_weighted_backward),
                            MOE_ENTRY(set_error),
                            {nullptr, nullptr, 0, nullptr}};

@@ -81,6 +81,45 @@ int64_t take_withheld() {
     return row;
 }
 
+// ---- norms around a block
+
+// What forward and backward refuse alike of the operands that both have.
+moe_status_t check_block_norm(const BlockNormCall &c, moe_gate_t kind, int norms, moe_dtype_t wtype) {
+    const moe_status_t st = check_shape(c.T, c.d, c.type);
+    if (st != MOE_OK) return st;
+    if (c.d > kBlockNormMaxWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if ((wtype != c.type && wtype != MOE_DTYPE_F32) || (norms & ~(MOE_NORM_POST | MOE_NORM_PRE)) != 0 ||
+        (kind != MOE_GATE_NONE && kind != MOE_GATE_ROW && kind != MOE_GATE_FULL) ||
+        (kind == MOE_GATE_NONE && c.gate.p != nullptr) || !(c.scale == c.scale))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(c.post, size_of(wtype)) || !aligned(c.pre, size_of(wtype)) || !aligned(c.r_post, 4) ||
+        !aligned(c.r_pre, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!c.pre_norm && c.pre != nullptr) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+bool plain_norm(const BlockNormCall &c, moe_gate_t kind) {
+    return kind == MOE_GATE_NONE && !c.post_norm && c.pre_norm && c.post == nullptr && c.scale == 1.f;
+}
+// The call's matrices: each one there, and no output with another stride in an input's place
+// or in another output's.
+moe_status_t check_matrices(const BlockNormCall &c, std::initializer_list<Matrix> in,
+                            std::initializer_list<Matrix> out) {
+    moe_status_t st;
+    for (const Matrix &m : in)
+        if ((st = check_matrix(m.p, m.ld, c.T, c.d, c.type)) != MOE_OK) return st;
+    for (const Matrix *o = out.begin(); o != out.end(); ++o) {
+        if ((st = check_matrix(o->p, o->ld, c.T, c.d, c.type)) != MOE_OK) return st;
+        for (const Matrix &m : in)
+            if (strides_clash(m.p, m.ld, o->p, o->ld, c.T)) return MOE_ERR_INVALID_ARG;
+        for (const Matrix *q = out.begin(); q != o; ++q)
+            if (q->p == o->p) return MOE_ERR_INVALID_ARG;
+    }
+    return MOE_OK;
+}
+// Matrix `m` if the call has one, else another that is checked all the same.
+Matrix if_any(bool has, const Matrix &m, const Matrix &other) { return has ? m : other; }
+
 // ---- dense feed-forward block
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -215,6 +254,123 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
                                   uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                                   moe_dtype_t type, void *dx, int64_t lddx, void *stream) {
     return drop(dy, lddy, nullptr, 0, T, d, p, seed, offset, offset_dev, type, dx, lddx, stream);
+}
+
+size_t moe_block_norm_scratch_bytes(int64_t T, int d) { return moe_layernorm_scratch_bytes(T, d); }
+
+moe_status_t moe_block_norm_forward(const void *x, int64_t ldx, const void *b, int64_t ldb,
+                                    const void *gate, int64_t ldgate, moe_gate_t gate_kind,
+                                    const void *post, const void *pre, float scale, int norms,
+                                    int64_t T, int d, float eps, moe_dtype_t type,
+                                    moe_dtype_t wtype, void *y, int64_t ldy, void *u, int64_t ldu,
+                                    float *rstd_post, float *rstd_pre, void *stream) {
+    BlockNormCall c{};
+    c.x = {x, ldx};
+    c.b = {b, ldb};
+    c.gate = {gate, ldgate};
+    c.y = {y, ldy};
+    c.u = {u, ldu};
+    c.post = post;
+    c.pre = pre;
+    c.r_post = rstd_post;
+    c.r_pre = rstd_pre;
+    c.T = T;
+    c.d = d;
+    c.type = type;
+    c.w32 = wtype == MOE_DTYPE_F32;
+    c.gate_rows = gate_kind == MOE_GATE_FULL;
+    c.post_norm = (norms & MOE_NORM_POST) != 0;
+    c.pre_norm = (norms & MOE_NORM_PRE) != 0;
+    c.scale = scale;
+    c.eps = eps;
+    moe_status_t st = check_block_norm(c, gate_kind, norms, wtype);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.f) || (!c.pre_norm && u != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    const bool full = gate_kind == MOE_GATE_FULL;
+    if (b == nullptr) {
+        if (!plain_norm(c, gate_kind) || y != nullptr) return MOE_ERR_INVALID_ARG;
+        st = check_matrices(c, {c.x}, {c.u});
+    } else {
+        if (gate_kind == MOE_GATE_ROW && (gate == nullptr || !aligned(gate, 4))) return MOE_ERR_INVALID_ARG;
+        const std::initializer_list<Matrix> in = {c.x, c.b, if_any(full, c.gate, c.x)};
+        st = c.pre_norm ? check_matrices(c, in, {c.y, c.u}) : check_matrices(c, in, {c.y});
+    }
+    if (st != MOE_OK || (st = check_arch()) != MOE_OK) return st;
+    return from_cuda(launch_block_norm_forward(c, take_withheld(), as_stream(stream)));
+}
+
+moe_status_t moe_block_norm_backward(const void *dy, int64_t lddy, const void *du, int64_t lddu,
+                                     const void *x, int64_t ldx, const void *b, int64_t ldb,
+                                     const void *gate, int64_t ldgate, moe_gate_t gate_kind,
+                                     const void *post, const void *pre, float scale, int norms,
+                                     const float *rstd_post, const float *rstd_pre, int64_t T, int d,
+                                     moe_dtype_t type, moe_dtype_t wtype, void *dx, int64_t lddx,
+                                     void *db, int64_t lddb, void *dgate, int64_t lddgate,
+                                     void *dpost, void *dpre, void *scratch, size_t scratch_bytes,
+                                     void *stream) {
+    BlockNormCall c{};
+    c.x = {x, ldx};
+    c.b = {b, ldb};
+    c.gate = {gate, ldgate};
+    c.post = post;
+    c.pre = pre;
+    c.r_post = const_cast<float *>(rstd_post);
+    c.r_pre = const_cast<float *>(rstd_pre);
+    c.T = T;
+    c.d = d;
+    c.type = type;
+    c.w32 = wtype == MOE_DTYPE_F32;
+    c.gate_rows = gate_kind == MOE_GATE_FULL;
+    c.post_norm = (norms & MOE_NORM_POST) != 0;
+    c.pre_norm = (norms & MOE_NORM_PRE) != 0;
+    c.scale = scale;
+    c.dy = {dy, lddy};
+    c.du = {du, lddu};
+    c.dx = {dx, lddx};
+    c.db = {db, lddb};
+    c.dgate = {dgate, lddgate};
+    c.dpost = dpost;
+    c.dpre = dpre;
+    c.part = static_cast<float *>(scratch);
+    moe_status_t st = check_block_norm(c, gate_kind, norms, wtype);
+    if (st != MOE_OK) return st;
+    const int ws = size_of(wtype);
+    if (!aligned(dpost, ws) || !aligned(dpre, ws) || (!c.pre_norm && (du != nullptr || dpre != nullptr)))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        const bool full = gate_kind == MOE_GATE_FULL;
+        if ((dy == nullptr && !c.pre_norm) || (c.post_norm && rstd_post == nullptr) ||
+            (c.pre_norm && rstd_pre == nullptr))
+            return MOE_ERR_INVALID_ARG;
+        const Matrix g = if_any(full, c.gate, c.x), u = if_any(c.pre_norm, c.du, c.x),
+                     s = if_any(dy != nullptr, c.dy, c.x);
+        if (b == nullptr) {
+            if (!plain_norm(c, gate_kind) || db != nullptr || dgate != nullptr || dpost != nullptr)
+                return MOE_ERR_INVALID_ARG;
+            st = check_matrices(c, {c.x, u, s}, {c.dx});
+        } else {
+            if (gate_kind == MOE_GATE_ROW &&
+                (gate == nullptr || dgate == nullptr || !aligned(gate, 4) || !aligned(dgate, 4)))
+                return MOE_ERR_INVALID_ARG;
+            if (gate_kind == MOE_GATE_NONE && dgate != nullptr) return MOE_ERR_INVALID_ARG;
+            const std::initializer_list<Matrix> in = {c.x, c.b, g, u, s};
+            st = full ? check_matrices(c, in, {c.dx, c.db, c.dgate}) : check_matrices(c, in, {c.dx, c.db});
+        }
+        if (st != MOE_OK) return st;
+        if (dpost != nullptr || dpre != nullptr) {
+            if (scratch == nullptr || !aligned(scratch, 256)) return MOE_ERR_INVALID_ARG;
+            if (scratch_bytes < moe_block_norm_scratch_bytes(T, d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+        }
+    }
+    if ((st = check_arch()) != MOE_OK) return st;
+    if (T == 0) {  // sums over no rows
+        cudaError_t e = cudaSuccess;
+        for (void *p : {dpost, dpre})
+            if (p != nullptr && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)d * ws, as_stream(stream));
+        return from_cuda(e);
+    }
+    return from_cuda(launch_block_norm_backward(c, take_withheld(), as_stream(stream)));
 }
 
 moe_status_t moe_dispatch(const void *x, int64_t ldx, const int32_t *row_of_slot, int64_t T, int K,

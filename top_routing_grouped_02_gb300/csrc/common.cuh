@@ -265,6 +265,33 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
                                 void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
                                 uint32_t *ticket, uint32_t *err, cudaStream_t s);
 
+// The norms around a block (block_norm.cu, block_norm_backward.cu); w32: post, pre and their
+// gradients are fp32. gate_rows: gate and dgate are [T,d] of `type`, else fp32, one a row.
+constexpr int kBlockNormMaxWidth = 16384;
+struct Matrix {
+    const void *p;
+    int64_t ld;
+};
+struct BlockNormCall {
+    Matrix x, b, gate, y, u;
+    const void *post, *pre;
+    float *r_post, *r_pre;
+    int64_t T;
+    int d;
+    moe_dtype_t type;
+    bool w32, gate_rows, post_norm, pre_norm;
+    float scale, eps;
+    // backward (r_post and r_pre are inputs then); part: ln_partials(T) * 2 * d floats
+    Matrix dy, du, dx, db, dgate;
+    void *dpost, *dpre;
+    float *part;
+};
+cudaError_t launch_block_norm_forward(const BlockNormCall &c, int64_t withheld, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const BlockNormCall &c, int64_t withheld, cudaStream_t s);
+// first, second [d] of wtype (each may be NULL) = the sums of P rows of part [P][2][d].
+cudaError_t launch_weight_reduce(const float *part, int P, int d, moe_dtype_t wtype, void *first,
+                                 void *second, cudaStream_t s);
+
 // Token rows and rows sorted by expert (dispatch.cu). x: by token (the dispatch's input, the
 // combine's gradient); z: by sorted row; out: by sorted row, or (x NULL) by token; res, w may
 // be NULL.

@@ -34,18 +34,10 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace moe {
 namespace {
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 // Threads of a ring block: 72 registers a thread forward, 128 backward, where the
 // column sums take 64.
@@ -69,12 +61,6 @@ struct LnArgs {
     int64_t lddy, lddres, lddx;
     float *part;       // [blocks][2][d] partial sums (dgamma, dbeta), or NULL
 };
-
-template <typename T>
-__device__ __forceinline__ float load_w(const void *w, int w32, int c, float none) {
-    if (w == nullptr) return none;
-    return w32 ? static_cast<const float *>(w)[c] : load_f32(static_cast<const T *>(w) + c);
-}
 
 // Elements of a row that warp w of `tpr` threads holds, NV vectors of V each thread.
 template <int V, int NV>
@@ -115,56 +101,6 @@ struct RingCtl {
     uint4 zero;  // what a thread past the row's end reads
 };
 constexpr int kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
-
-// Waits for stage s. A copy that has not arrived after about a second never will (it was
-// issued by this block: the device has stopped). Then false, and the caller's group gives
-// up: it issues no further copies, its rows' results and the block's sums become NaN. Copies
-// in flight land before the block leaves, as far as another limit allows (drain: the
-// threads that issue copies wait for them).
-__device__ __noinline__ bool ring_wait_long(uint32_t bar0, int stages, int s, uint32_t parity, bool drain) {
-    uint64_t t0 = ptx::globaltimer_ns();
-    for (;;) {
-        // the clock first: a block that was held up for longer looks once more
-        const bool late = ptx::globaltimer_ns() - t0 > kWaitLimitNs;
-        if (ptx::mbar_try_wait(bar0 + 8 * s, parity)) return true;
-        if (late) break;
-    }
-    t0 = ptx::globaltimer_ns();
-    for (int k = 0; drain && k < stages; ++k) {
-        const int at = s + k < stages ? s + k : s + k - stages;
-        while (!ptx::mbar_try_wait(bar0 + 8 * at, s + k < stages ? parity : parity ^ 1))
-            if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    }
-    return false;
-}
-__device__ __forceinline__ bool ring_wait(uint32_t bar0, int stages, int s, uint32_t parity, bool drain) {
-    return ptx::mbar_try_wait(bar0 + 8 * s, parity) || ring_wait_long(bar0, stages, s, parity, drain);
-}
-
-// Weights of vector v from their planes.
-template <int V>
-__device__ __forceinline__ void plane_pairs(const float *planes, int nvec, int v, f32x2 (&g)[V / 2]) {
-#pragma unroll
-    for (int h = 0; h < V / 4; ++h) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(planes + (h * nvec + v) * 4);
-        g[2 * h] = q.x;
-        g[2 * h + 1] = q.y;
-    }
-}
-template <typename T, int V>
-__device__ __forceinline__ void fill_planes(float *planes, const void *w, int w32, int d, float none) {
-    const int nvec = (d + V - 1) / V;
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-        float f[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = v * V + j < d ? load_w<T>(w, w32, v * V + j, none) : 0.f;
-#pragma unroll
-        for (int h = 0; h < V / 4; ++h)
-            *reinterpret_cast<float4 *>(planes + (h * nvec + v) * 4) =
-                make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
-    }
-}
 
 // A block's partial sums dgamma, dbeta: each group puts its own into its ring (as planes,
 // [2][d rounded up to V]), and the block adds the groups' in order, four columns a
@@ -837,16 +773,6 @@ __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
 
 // Vector length (elements) that divides d and every row stride and suits the
 // pointers' alignment.
-struct Align {
-    uint64_t bits = 0;
-    void add(const void *p, int64_t ld, int d, int esize, int64_t T) {
-        if (p == nullptr) return;
-        bits |= reinterpret_cast<uintptr_t>(p) | (uint64_t)d * esize;
-        if (T > 1) bits |= (uint64_t)ld * esize;
-    }
-    bool fits(int bytes) const { return (bits & (bytes - 1)) == 0; }
-};
-
 int row_groups(int wpr, int threads) { return std::max(1, threads / (32 * wpr)); }
 
 // Row groups and ring stages of a block of at most max_threads threads (one block
@@ -925,6 +851,13 @@ cudaError_t backward_rows(const LnArgs &a, int *P, bool *fits, cudaStream_t s) {
 }
 
 template <typename T>
+cudaError_t weight_reduce(const float *part, int P, int d, int w32, void *dgamma, void *dbeta,
+                          cudaStream_t s) {
+    return launch_k(ln_weight_reduce_kernel<T>, dim3((unsigned)((2ll * d + 31) / 32)), dim3(512), 0, s,
+                    part, P, d, w32, dgamma, dbeta);
+}
+
+template <typename T>
 cudaError_t forward_type(const LnArgs &a, const Align &al, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);  // elements of a 16-byte vector
     bool fits = false;
@@ -960,11 +893,19 @@ cudaError_t backward_type(const LnArgs &a, const Align &al, void *dgamma, void *
                         : launch_k(ln_backward_wide_kernel<T, 1>, dim3(grid), dim3(1024), 0, s, a);
     }
     if (e != cudaSuccess || a.part == nullptr) return e;
-    return launch_k(ln_weight_reduce_kernel<T>, dim3((unsigned)((2ll * a.d + 31) / 32)), dim3(512), 0, s,
-                    static_cast<const float *>(a.part), P, a.d, a.w32, dgamma, dbeta);
+    return weight_reduce<T>(a.part, P, a.d, a.w32, dgamma, dbeta, s);
 }
 
 }  // namespace
+
+cudaError_t launch_weight_reduce(const float *part, int P, int d, moe_dtype_t wtype, void *first,
+                                 void *second, cudaStream_t s) {
+    switch (wtype) {
+        case MOE_DTYPE_BF16: return weight_reduce<__nv_bfloat16>(part, P, d, 0, first, second, s);
+        case MOE_DTYPE_F16: return weight_reduce<__half>(part, P, d, 0, first, second, s);
+        default: return weight_reduce<float>(part, P, d, 1, first, second, s);
+    }
+}
 
 int ln_partials(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(T, kLnPartials)); }
 

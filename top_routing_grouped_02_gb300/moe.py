@@ -33,7 +33,8 @@ LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_g
             "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1,
             "moe_layernorm": 1, "moe_layernorm_backward": 2, "moe_dropout": 1,
             "moe_dropout_backward": 1, "moe_ffn": 2, "moe_ffn_train": 2, "moe_ffn_backward": 3,
-            "moe_dispatch": 1, "moe_combine_weighted": 1, "moe_combine_weighted_backward": 1}
+            "moe_block_norm": 1, "moe_block_norm_backward": 2, "moe_rmsnorm": 1,
+            "moe_rmsnorm_backward": 2, "moe_dispatch": 1, "moe_combine_weighted": 1, "moe_combine_weighted_backward": 1}
 TILE_M = 128
 
 
@@ -103,6 +104,12 @@ _SIGS = {
                                    _P]),
     "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
                               _P, _SZ, _P]),
+    "moe_block_norm_forward": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _I, _L, _I, _F, _I, _I,
+                                    _P, _L, _P, _L, _P, _P, _P]),
+    "moe_block_norm_scratch_bytes": (_SZ, [_L, _I]),
+    "moe_block_norm_backward": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _I, _P,
+                                     _P, _L, _I, _I, _I, _P, _L, _P, _L, _P, _L, _P, _P, _P, _SZ,
+                                     _P]),
     "moe_dispatch": (_I, [_P, _L, _P, _L, _I, _I, _I, _P, _L, _L, _P]),
     "moe_combine_weighted": (_I, [_P, _L, _L, _P, _P, _P, _L, _L, _I, _I, _I, _P, _L, _P]),
     "moe_combine_weighted_backward": (_I, [_P, _L, _P, _L, _L, _P, _P, _L, _I, _I, _I, _P, _L, _P,
@@ -697,6 +704,63 @@ def moe_ffn_backward(dY, x, W1, W3, W2, H, F1, F3, act: str = "silu", need_dx: b
     for). ws: ffn_workspace(..., train=True)."""
     return _native().ffn_backward(dY, x, W1, W3, W2, H, F1, F3, _act(act), need_dx, need_dw,
                                   _ffn_ws(ws, x, W1, True, stream), stream)
+
+# --------------------------------------------------- the norms around a block
+
+
+def moe_block_norm(x, b, post=None, pre=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
+                   post_norm: bool = True, pre_norm: bool = True, stats: bool = False, y=None, u=None,
+                   stream=None):
+    """(y, u): y = scale x + sigmoid(gate) post rms(b), the stream behind a block whose output
+    is b, and u = pre rms(y), the input of the next one (None without pre_norm; without
+    post_norm, post scales b itself). gate: like x, or one fp32 value a row, or None (no gate);
+    post, pre [d] of x's type or fp32, or None. stats=True: (y, u, rstd_post, rstd_pre), the
+    fp32 row statistics that the backward takes. y may be x."""
+    out = _native().block_norm(x, _block(b), post, pre, gate, scale, eps, post_norm, pre_norm, stats,
+                               y, u, stream)
+    return out if stats else out[:2]
+
+
+def moe_block_norm_backward(dy, du, x, b, post, pre, rstd_post, rstd_pre, gate=None,
+                            scale: float = 1.0, wdtype=None, dx=None, db=None, scratch=None,
+                            stream=None):
+    """(dx, db, dgate, dpost, dpre) of moe_block_norm, with dy the gradient that reaches y by the
+    stream (or None) and du that of u; rstd_post and rstd_pre are None where the forward had no
+    such norm. dgate is None without a gate, dpre without the pre norm. dpost and dpre have the
+    weights' type, or wdtype (default fp32) without weights."""
+    if post is None and pre is None and wdtype not in (None, torch.float32, x.dtype):
+        raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wdtype}")
+    return _native().block_norm_backward(dy, du, x, _block(b), post, pre, rstd_post, rstd_pre, gate,
+                                         scale, wdtype is not x.dtype, dx, db, scratch, stream)
+
+
+def _block(b):
+    if b is None:
+        raise TypeError("b must be a tensor (moe_rmsnorm is the norm alone)")
+    return b
+
+
+def moe_rmsnorm(x, gamma=None, eps: float = 1e-6, stats: bool = False, y=None, stream=None):
+    """y = gamma x / sqrt(mean(x^2) + eps) along the last dimension (gamma: [d] of x's type or
+    fp32, or None); stats=True: (y, rstd), the fp32 row statistics that the backward takes."""
+    _, out, _, rstd = _native().block_norm(x, None, None, gamma, None, 1.0, eps, False, True, stats, None,
+                                           y, stream)
+    return (out, rstd) if stats else out
+
+
+def moe_rmsnorm_backward(dy, x, gamma, rstd, dres=None, wdtype=None, dx=None, scratch=None,
+                         stream=None):
+    """(dx, dgamma) of moe_rmsnorm, with `dres` (the gradient that reaches x by the residual
+    branch) added to dx when given. dgamma has gamma's type, or wdtype (default fp32) without
+    gamma."""
+    if gamma is None and wdtype not in (None, torch.float32, x.dtype):
+        raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wdtype}")
+    if not torch.is_tensor(dy) or not torch.is_tensor(rstd):
+        raise TypeError("dy and rstd must be tensors")
+    out = _native().block_norm_backward(dres, dy, x, None, None, gamma, None, rstd, None, 1.0,
+                                        wdtype is not x.dtype, dx, None, scratch, stream)
+    return out[0], out[4]
+
 
 # ------------------------- rows sorted by expert and back, for experts of any kind
 
