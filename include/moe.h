@@ -544,7 +544,8 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
  * `type` between the two products, Y once. act: */
 typedef enum {
     MOE_ACT_SILU = 0,      /* a sigmoid(a) */
-    MOE_ACT_GELU_TANH = 1  /* 0.5 a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) */
+    MOE_ACT_GELU_TANH = 1, /* 0.5 a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) */
+    MOE_ACT_NONE = 2       /* a (moe_linear_* alone) */
 } moe_act_t;
 
 /* Workspace of the calls below for up to T tokens (train: of the training forward
@@ -592,6 +593,38 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
                               int T, int d, int n, moe_act_t act, moe_dtype_t type, void *dX,
                               void *dW1, void *dW3, void *dW2, void *ws, size_t ws_bytes,
                               void *stream);
+
+/* ---- A dense projection with its epilogue:
+ *   A = X W + bias,  Y = act(A) + residual
+ * X [T,k], W [k,n], residual, Y [T,n] of `type` (MOE_DTYPE_BF16 or MOE_DTYPE_F16), bias [n] of
+ * btype (type or MOE_DTYPE_F32); bias and residual may be NULL. Dense, row-major and 16-byte
+ * aligned; k and n multiples of 8 up to 2^20, any T >= 0 (0: nothing is enqueued). Sums and
+ * the epilogue in fp32, Y rounded once. Y may be residual. Few tokens (up to 48) take a kernel
+ * that streams the weights, more a tiled one: one kernel either way. The workspace is of
+ * moe_linear_workspace_bytes(T, k, n, train) bytes, initialised by moe_ffn_workspace_init and
+ * kept as those of the feed-forward calls are (either kind of call may use it, if it is large
+ * enough); waits are bounded as theirs. */
+size_t moe_linear_workspace_bytes(int T, int k, int n, int train);
+moe_status_t moe_linear_forward(const void *X, const void *W, const void *bias,
+                                const void *residual, int T, int k, int n, moe_act_t act,
+                                moe_dtype_t type, moe_dtype_t btype, void *Y, void *ws,
+                                size_t ws_bytes, void *stream);
+/* Y and F = act'(A) in fp32, which the backward takes: moe_ffn_saved_floats(T, n) floats in the
+ * blocks of moe_ffn_forward_train's factors (NULL with MOE_ACT_NONE, where it is 1). In 16
+ * bits it would round dA = dY F twice, and dbias at all. ws: a workspace for training. */
+moe_status_t moe_linear_forward_train(const void *X, const void *W, const void *bias,
+                                      const void *residual, int T, int k, int n, moe_act_t act,
+                                      moe_dtype_t type, moe_dtype_t btype, void *Y, float *F,
+                                      void *ws, size_t ws_bytes, void *stream);
+/* The gradients, with dA = dY F (dY itself without F), rounded to `type` as an operand:
+ *   dX = dA W^T, dW = X^T dA, dbias = the sums over rows of dY F (before that rounding)
+ * dX, dW of `type`, dbias of btype, each rounded once after an fp32 sum and each may be NULL
+ * (the residual's gradient is dY). T = 0 gives a zero dW and dbias. ws: a workspace for
+ * training. Up to four kernels: dA with the blocks' sums, the sum of those, dX, dW.
+ * Deterministic. */
+moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, const float *F, int T,
+                                 int k, int n, moe_dtype_t type, moe_dtype_t btype, void *dX,
+                                 void *dW, void *dbias, void *ws, size_t ws_bytes, void *stream);
 
 /* ---- The norms around a block, with its gate and the residual scale, in one pass over the
  * stream: behind a block whose output is b, and in front of the next one,

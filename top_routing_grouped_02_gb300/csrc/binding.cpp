@@ -13,6 +13,7 @@
 
 #include <initializer_list>
 #include <optional>
+#include <vector>
 
 #include "moe.h"
 
@@ -593,6 +594,93 @@ PyObject *ffn_backward(PyObject *const *a, Py_ssize_t n) {
     return wrap_all(dX, dW1, dW3, dW2);
 }
 
+// A projection's operands.
+struct Linear {
+    at::Tensor x, W, bias, res, ws;
+    int T, k, n;
+    void *px, *pw, *pb, *pws;
+    at::ScalarType type;
+    std::vector<int64_t> out;  // the result's shape
+};
+Linear linear_args(PyObject *x, PyObject *W, PyObject *bias, PyObject *res, PyObject *ws, PyObject *stream) {
+    Linear f{tensor(x, "x"), tensor(W, "W"), optional_tensor(bias, "bias"), optional_tensor(res, "residual"),
+             tensor(ws, "ws")};
+    one_device({f.x, "x"}, {{f.W, "W"}, {f.bias, "bias"}, {f.res, "residual"}, {f.ws, "ws"}}, stream);
+    if (f.x.dim() < 1 || f.W.dim() != 2 || f.x.size(-1) != f.W.size(0))
+        refuse(PyExc_ValueError, "%s must be [..., k] and W [k, n]", "x");
+    f.type = f.x.scalar_type();
+    if (f.type != at::kBFloat16 && f.type != at::kHalf)
+        refuse(PyExc_TypeError, "a projection takes bf16 or fp16 %s", "x");
+    const int64_t k = f.W.size(0), n = f.W.size(1), T = k > 0 ? f.x.numel() / k : 0;
+    if (T > INT32_MAX || k > INT32_MAX || n > INT32_MAX) refuse(PyExc_ValueError, "%s is too large", "x");
+    f.px = dense(f.x, f.x.sizes(), f.type, "x");
+    f.pw = dense(f.W, {k, n}, f.type, "W");
+    f.pb = vec_of(f.bias, n, f.x, "bias");
+    if (!f.ws.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", "ws");
+    f.pws = f.ws.data_ptr();
+    f.T = (int)T;
+    f.k = (int)k;
+    f.n = (int)n;
+    f.out = f.x.sizes().vec();
+    f.out.back() = n;
+    return f;
+}
+moe_dtype_t bias_type(const Linear &f) { return dtype(f.bias.defined() ? f.bias : f.x); }
+
+// x, W, bias, act, residual, ws, Y, stream
+PyObject *linear(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 8);
+    const Linear f = linear_args(a[0], a[1], a[2], a[4], a[5], a[7]);
+    const at::Tensor given = optional_tensor(a[6], "Y");
+    one_device({f.x, "x"}, {{given, "Y"}}, Py_None);
+    const OnStream stream(a[7], f.x);
+    const at::Tensor Y = given.defined() ? given : fresh(f.out, f.type, f.x);
+    void *py = dense(Y, f.out, f.type, "Y"), *pr = f.res.defined() ? dense(f.res, f.out, f.type, "residual") : nullptr;
+    check("moe_linear_forward",
+          moe_linear_forward(f.px, f.pw, f.pb, pr, f.T, f.k, f.n, (moe_act_t)integer(a[3]), dtype(f.x), bias_type(f),
+                             py, f.pws, f.ws.nbytes(), stream));
+    return wrap(Y);
+}
+
+// x, W, bias, act, residual, ws, stream
+PyObject *linear_train(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 7);
+    const Linear f = linear_args(a[0], a[1], a[2], a[4], a[5], a[6]);
+    const OnStream stream(a[6], f.x);
+    const moe_act_t act = (moe_act_t)integer(a[3]);
+    void *pr = f.res.defined() ? dense(f.res, f.out, f.type, "residual") : nullptr;
+    const at::Tensor Y = fresh(f.out, f.type, f.x);
+    at::Tensor F;
+    if (act != MOE_ACT_NONE) F = fresh({(int64_t)moe_ffn_saved_floats(f.T, f.n)}, at::kFloat, f.x);
+    check("moe_linear_forward_train",
+          moe_linear_forward_train(f.px, f.pw, f.pb, pr, f.T, f.k, f.n, act, dtype(f.x), bias_type(f), Y.data_ptr(),
+                                   F.defined() ? static_cast<float *>(F.data_ptr()) : nullptr, f.pws, f.ws.nbytes(), stream));
+    return wrap_all(Y, F);
+}
+
+// dY, x, W, F, fp32 bias gradient or not (None: no bias gradient), need_dx, need_dw, ws, stream
+PyObject *linear_backward(PyObject *const *a, Py_ssize_t n) {
+    expect(n, 9);
+    const Linear f = linear_args(a[1], a[2], Py_None, Py_None, a[7], a[8]);
+    const at::Tensor dY = tensor(a[0], "dY"), F = optional_tensor(a[3], "F");
+    one_device({f.x, "x"}, {{dY, "dY"}, {F, "F"}}, Py_None);
+    const OnStream stream(a[8], f.x);
+    void *pdy = dense(dY, f.out, f.type, "dY");
+    const float *pf = F.defined() ? static_cast<const float *>(
+                                        dense(F, {(int64_t)moe_ffn_saved_floats(f.T, f.n)}, at::kFloat, "F"))
+                                  : nullptr;
+    const bool db = a[4] != Py_None, b32 = db && truth(a[4]);
+    at::Tensor dX, dW, dbias;
+    if (truth(a[5])) dX = fresh(f.x.sizes(), f.type, f.x);
+    if (truth(a[6])) dW = fresh({f.k, f.n}, f.type, f.x);
+    if (db) dbias = fresh({f.n}, b32 ? at::kFloat : f.type, f.x);
+    auto data = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+    check("moe_linear_backward",
+          moe_linear_backward(pdy, f.px, f.pw, pf, f.T, f.k, f.n, dtype(f.x), b32 ? MOE_DTYPE_F32 : dtype(f.x),
+                              data(dX), data(dW), data(dbias), f.pws, f.ws.nbytes(), stream));
+    return wrap_all(dX, dW, dbias);
+}
+
 // error class
 PyObject *set_error(PyObject *const *a, Py_ssize_t n) {
     expect(n, 1);
@@ -613,7 +701,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define MOE_ENTRY(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MOE_ENTRY(layernorm), MOE_ENTRY(layernorm_backward), MOE_ENTRY(dropout),
                            MOE_ENTRY(dropout_backward), MOE_ENTRY(ffn), MOE_ENTRY(ffn_train),
-                           MOE_ENTRY(ffn_backward), MOE_ENTRY(block_norm),
+                           MOE_ENTRY(ffn_backward), MOE_ENTRY(linear), MOE_ENTRY(linear_train),
+                           MOE_ENTRY(linear_backward), MOE_ENTRY(block_norm),
                            MOE_ENTRY(block_norm_backward), MOE_ENTRY(dispatch),
                            MOE_ENTRY(combine_weighted), MOE_ENTRY(combine_weighted_backward),
                            MOE_ENTRY(set_error),

@@ -154,6 +154,33 @@ FfnWs ffn_ws(int T, int d, int n, bool train) {
                                     align256(ffn_stream_part_bytes(few, d, n)));
     return w;
 }
+// The same for projections: the training's dA, the sums of its bias' gradient, then the parts.
+struct LinearWs {
+    size_t da, sums, part, total;
+};
+LinearWs linear_ws(int T, int k, int n, bool train) {
+    LinearWs w;
+    w.da = align256(kFfnControlBytes);
+    w.sums = w.da + (train ? align256((size_t)T * n * 2) : 0);
+    w.part = w.sums + (train ? align256(linear_sums_floats(T, n) * sizeof(float)) : 0);
+    const bool tiled = train || !linear_streams(T, k, n);
+    w.total = w.part + (tiled ? align256(ffn_dense_part_bytes()) : 0);
+    // a workspace for T tokens serves fewer, whichever kernel they take
+    const int few = std::min(T, kFfnStreamTokens);
+    w.total = std::max(w.total, w.part + align256(linear_stream_part_bytes(few, k, n)));
+    return w;
+}
+moe_status_t check_linear(int T, int k, int n, moe_act_t act, moe_dtype_t type, moe_dtype_t btype) {
+    const moe_status_t st =
+        check_ffn(T, k, n, act == MOE_ACT_NONE ? MOE_ACT_SILU : act, type);
+    if (st != MOE_OK) return st;
+    return btype == type || btype == MOE_DTYPE_F32 ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+moe_status_t check_linear_ws(void *ws, size_t ws_bytes, int T, int k, int n, bool train) {
+    if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    return ws_bytes < linear_ws(T, k, n, train).total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
 
 bool all_aligned16(std::initializer_list<const void *> ps) {
@@ -254,6 +281,83 @@ moe_status_t moe_dropout_backward(const void *dy, int64_t lddy, int64_t T, int d
                                   uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
                                   moe_dtype_t type, void *dx, int64_t lddx, void *stream) {
     return drop(dy, lddy, nullptr, 0, T, d, p, seed, offset, offset_dev, type, dx, lddx, stream);
+}
+
+size_t moe_linear_workspace_bytes(int T, int k, int n, int train) {
+    if (check_linear(T, k, n, MOE_ACT_NONE, MOE_DTYPE_BF16, MOE_DTYPE_BF16) != MOE_OK) return 0;
+    return linear_ws(T, k, n, train != 0).total;
+}
+
+static moe_status_t linear_forward(const void *X, const void *W, const void *bias, const void *residual,
+                                   int T, int k, int n, moe_act_t act, moe_dtype_t type,
+                                   moe_dtype_t btype, void *Y, float *F, bool train, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    moe_status_t st = check_linear(T, k, n, act, type, btype);
+    if (st != MOE_OK || T == 0) return st;
+    if (!all_aligned16({X, W, Y}) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(F, 16) ||
+        (train && (F != nullptr) != (act != MOE_ACT_NONE)) || Y == X || Y == F)
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_linear_ws(ws, ws_bytes, T, k, n, train)) != MOE_OK) return st;
+    if ((st = check_arch()) != MOE_OK) return st;
+    const LinearCall c{X, W, bias, residual, Y, T, k, n, act, type == MOE_DTYPE_F16, btype == MOE_DTYPE_F32};
+    void *part = at(ws, linear_ws(T, k, n, train).part);
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset));
+    uint32_t *err = static_cast<uint32_t *>(ws);
+    cudaStream_t s = as_stream(stream);
+    if (F == nullptr && linear_streams(T, k, n))
+        return from_cuda(launch_linear_stream(c, static_cast<float *>(part), ticket, err, s));
+    return from_cuda(launch_linear_tiled(c, F, static_cast<float4 *>(part), ticket, err, s));
+}
+
+moe_status_t moe_linear_forward(const void *X, const void *W, const void *bias,
+                                const void *residual, int T, int k, int n, moe_act_t act,
+                                moe_dtype_t type, moe_dtype_t btype, void *Y, void *ws,
+                                size_t ws_bytes, void *stream) {
+    return linear_forward(X, W, bias, residual, T, k, n, act, type, btype, Y, nullptr, false, ws, ws_bytes,
+                          stream);
+}
+
+moe_status_t moe_linear_forward_train(const void *X, const void *W, const void *bias,
+                                      const void *residual, int T, int k, int n, moe_act_t act,
+                                      moe_dtype_t type, moe_dtype_t btype, void *Y, float *F,
+                                      void *ws, size_t ws_bytes, void *stream) {
+    return linear_forward(X, W, bias, residual, T, k, n, act, type, btype, Y, F, true, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, const float *F, int T,
+                                 int k, int n, moe_dtype_t type, moe_dtype_t btype, void *dX,
+                                 void *dW, void *dbias, void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t st = check_linear(T, k, n, MOE_ACT_NONE, type, btype);
+    if (st != MOE_OK) return st;
+    if (!aligned(dX, 16) || !aligned(dW, 16) || !aligned(dbias, size_of(btype))) return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!all_aligned16({dY}) || !aligned(F, 16) || (dX != nullptr && !all_aligned16({W})) ||
+            (dW != nullptr && !all_aligned16({X})))
+            return MOE_ERR_INVALID_ARG;
+        for (const void *out : {dX, dW, dbias})
+            if (out != nullptr && (out == dY || out == X || out == W || out == F)) return MOE_ERR_INVALID_ARG;
+        if ((st = check_linear_ws(ws, ws_bytes, T, k, n, true)) != MOE_OK) return st;
+    }
+    if ((st = check_arch()) != MOE_OK) return st;
+    cudaStream_t s = as_stream(stream);
+    if (T == 0) {  // sums over no tokens
+        cudaError_t e = cudaSuccess;
+        if (dW != nullptr) e = cudaMemsetAsync(dW, 0, (size_t)k * n * 2, s);
+        if (dbias != nullptr && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, (size_t)n * size_of(btype), s);
+        return from_cuda(e);
+    }
+    const LinearWs w = linear_ws(T, k, n, true);
+    const bool f16 = type == MOE_DTYPE_F16;
+    const bool products = dX != nullptr || dW != nullptr;
+    void *dA = F != nullptr ? at(ws, w.da) : const_cast<void *>(dY);
+    if (!products && dbias == nullptr) return MOE_OK;
+    cudaError_t e = launch_linear_grad(dY, F, T, n, f16, dA, dbias, btype == MOE_DTYPE_F32,
+                                       reinterpret_cast<float *>(at(ws, w.sums)), s);
+    if (e == cudaSuccess)
+        e = launch_linear_products(dA, X, W, T, k, n, f16, dX, dW, reinterpret_cast<float4 *>(at(ws, w.part)),
+                                   reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),
+                                   static_cast<uint32_t *>(ws), s);
+    return from_cuda(e);
 }
 
 size_t moe_block_norm_scratch_bytes(int64_t T, int d) { return moe_layernorm_scratch_bytes(T, d); }

@@ -265,6 +265,31 @@ cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, c
                                 void *dX, void *dW1, void *dW3, void *dW2, float4 *part,
                                 uint32_t *ticket, uint32_t *err, cudaStream_t s);
 
+// A projection, Y = act(X W + bias) + residual (ffn.cu, ffn_small.cu), and what its gradients
+// take beside the products (linear.cu). bias, res may be NULL; act: moe_act_t. Y may be res.
+struct LinearCall {
+    const void *X, *W, *bias, *res;
+    void *Y;
+    int T, k, n, act;
+    bool f16, bias32;
+};
+inline bool linear_streams(int T, int k, int n) { return T <= 48; }
+size_t linear_stream_part_bytes(int T, int k, int n);
+cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *ticket, uint32_t *err,
+                                 cudaStream_t s);
+// F: act'(X W + bias) in blocks of 32 x 32 (moe_ffn_forward_train), or NULL.
+cudaError_t launch_linear_tiled(const LinearCall &c, float *F, float4 *part, uint32_t *ticket, uint32_t *err,
+                                cudaStream_t s);
+// dX = dA W^T, dW = X^T dA; either may be NULL.
+cudaError_t launch_linear_products(const void *dA, const void *X, const void *W, int T, int k, int n, bool f16,
+                                   void *dX, void *dW, float4 *part, uint32_t *ticket, uint32_t *err,
+                                   cudaStream_t s);
+// dA = dY F (F NULL: dY itself, nothing is written) and, with dbias, its column sums (fp32, then
+// of the 16-bit type or fp32) by way of sums: linear_sums_floats(T, n) floats.
+size_t linear_sums_floats(int T, int n);
+cudaError_t launch_linear_grad(const void *dY, const float *F, int T, int n, bool f16, void *dA, void *dbias,
+                               bool bias32, float *sums, cudaStream_t s);
+
 // The norms around a block (block_norm.cu, block_norm_backward.cu); w32: post, pre and their
 // gradients are fp32. gate_rows: gate and dgate are [T,d] of `type`, else fp32, one a row.
 constexpr int kBlockNormMaxWidth = 16384;

@@ -86,7 +86,9 @@ namespace {
 // kDHid: dA1, dA3 from dY, W2 (K-major: its rows are the output columns) and F1,
 // F3. kDX: dX, one reduction over dA1 W1^T then dA3 W3^T (K-major weights).
 // kWGrad: dW1, dW3, dW2 in one launch, both operands MN-major, reduction over T.
-enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4 };
+// kLinear: a projection, Y = act(X W + bias) + residual, and (training) F = act'(X W + bias);
+// its gradients are products of the modes kDX, with no second half, and kWGrad, with one problem.
+enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4, kLinear = 5 };
 
 constexpr int BM = 128;  // rows per CTA
 constexpr int BK = 64;   // reduction depth per stage: 128 bytes of 16-bit elements
@@ -129,8 +131,11 @@ struct Args {
     uint32_t idesc;
     int f16, act;
     void *out[3];        // the outputs of each problem (kDHid: both of its one)
+    const void *bias;    // kLinear: [cols] of 16 bits or (bias32) fp32, or NULL
+    int bias32;
+    const void *res;     // kLinear: [rows, cols] of 16 bits, or NULL; out[0] may be it
     float *f1, *f3;      // the factors in blocks (saved_block): kGate stores them, or
-                         // NULL; kDHid reads them
+                         // NULL; kDHid reads them; kLinear stores F in f1, or NULL
     float4 *part;        // [segment][CTA][warp][kPartVecs]
     uint32_t *ticket;    // [cut][CTA][warp]
     uint32_t *err;
@@ -385,6 +390,38 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         auto column = [&](int v) {
             return MODE == kGate ? (v / NU) * (BN / 2) + share * NU * 4 + v % NU * 4 : share * NU * 4 + v * 4;
         };
+        // kLinear: the bias of four columns; a call with the activation and whether its
+        // derivative is wanted, known at compile time
+        auto bias_pairs = [&](int x, f32x2 (&b)[2]) {
+            if (args.bias32) {
+                const float4 q = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(args.bias) + x));
+                b[0] = moe::pair(q.x, q.y);
+                b[1] = moe::pair(q.z, q.w);
+                return;
+            }
+            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(args.bias) + x));
+            float f[4];
+            if (f16) {
+                unpack2<__half>(q.x, f[0], f[1]);
+                unpack2<__half>(q.y, f[2], f[3]);
+            } else {
+                unpack2<__nv_bfloat16>(q.x, f[0], f[1]);
+                unpack2<__nv_bfloat16>(q.y, f[2], f[3]);
+            }
+            b[0] = pair2(f);
+            b[1] = pair2(f + 2);
+        };
+        auto with_act = [&](auto &&call) {
+            using yes = std::true_type;
+            using no = std::false_type;
+            if (args.act == kNoAct) call(std::integral_constant<int, kNoAct>(), no());
+            else if (args.act == MOE_ACT_SILU)
+                args.f1 != nullptr ? call(std::integral_constant<int, MOE_ACT_SILU>(), yes())
+                                   : call(std::integral_constant<int, MOE_ACT_SILU>(), no());
+            else
+                args.f1 != nullptr ? call(std::integral_constant<int, MOE_ACT_GELU_TANH>(), yes())
+                                   : call(std::integral_constant<int, MOE_ACT_GELU_TANH>(), no());
+        };
         // 32 columns of this pair's cut tile from its segments, in their order, this pair's
         // own from its accumulator (column col); v0: their first vector in the parts
         auto gather = [&](int v0, uint32_t taddr, int col, uint32_t (&v)[32]) {
@@ -435,7 +472,19 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     x3[i] = __ldg(p3 + i * 32);
                 }
             };
+            // kLinear: this row's residual of a chunk, likewise
+            [[maybe_unused]] uint4 rr[4] = {};
+            auto load_residual = [&](int c) {
+                if (args.res == nullptr || c >= hi || y0 + lane >= rows) return;
+                const int x0 = un.nb * kCols + c * 32;
+                const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(args.res) +
+                                                                 (int64_t)(y0 + lane) * cols + x0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (x0 + 8 * i < cols) rr[i] = p[i];
+            };
             if constexpr (MODE == kDHid) load_factors(lo);
+            if constexpr (MODE == kLinear) load_residual(lo);
             if (!ready()) return false;
             if (lo >= hi) release();
             // m: W1's sums or (kGate) W3's
@@ -498,6 +547,47 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     load_factors(c + 1);
                     store_box(o1, x0, y0, &maps.o[0]);
                     store_box(o3, x0, y0, &maps.o[1]);
+                } else if constexpr (MODE == kLinear) {
+                    uint32_t v[32], o[16];
+                    load(c, 0, v);
+                    if (c == hi - 1) release();
+                    if (args.bias != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (x0 + 8 * i < cols)
+#pragma unroll
+                                for (int j = 0; j < 8; j += 4) {
+                                    f32x2 b[2];
+                                    bias_pairs(x0 + 8 * i + j, b);
+                                    put_pair(add2(word_pair(v + 8 * i + j), b[0]), v + 8 * i + j);
+                                    put_pair(add2(word_pair(v + 8 * i + j + 2), b[1]), v + 8 * i + j + 2);
+                                }
+                    }
+                    auto chunk = [&](auto act, auto saves) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f32x2 f, df = 0;
+                            activate_one<act(), saves()>(word_pair(v + 2 * i), f, df);
+                            float x, y;
+                            if (args.res != nullptr) {
+                                const uint32_t w = (&rr[i >> 2].x)[i & 3];
+                                if (f16) unpack2<__half>(w, x, y);
+                                else unpack2<__nv_bfloat16>(w, x, y);
+                                f = add2(f, moe::pair(x, y));
+                            }
+                            unpair(f, x, y);
+                            o[i] = pack(x, y, f16);
+                            if (saves()) put_pair(df, v + 2 * i);
+                        }
+                    };
+                    with_act(chunk);
+                    load_residual(c + 1);
+                    store_box(o, x0, y0, &maps.o[0]);
+                    if (args.f1 != nullptr) {
+                        float4 *p = saved_block(args.f1, cols, y0, x0, lane);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) p[i * 32] = words_float4(v + 4 * i);
+                    }
                 } else {
                     uint32_t v[32], o[16];
                     load(c, 0, v);
@@ -587,6 +677,30 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     } else if constexpr (MODE == kDHid) {
                         store(0, mul2(a, pair2(&f1.x)), mul2(b, pair2(&f1.z)));
                         store(1, mul2(a, pair2(&f3.x)), mul2(b, pair2(&f3.z)));
+                    } else if constexpr (MODE == kLinear) {
+                        f32x2 bias[2] = {0, 0}, r[2] = {0, 0};
+                        if (args.bias != nullptr) bias_pairs(x, bias);
+                        if (args.res != nullptr) {
+                            const uint2 q = *reinterpret_cast<const uint2 *>(
+                                static_cast<const uint16_t *>(args.res) + (int64_t)(y + lane) * cols + x);
+                            float e[4];
+                            if (f16) {
+                                unpack2<__half>(q.x, e[0], e[1]);
+                                unpack2<__half>(q.y, e[2], e[3]);
+                            } else {
+                                unpack2<__nv_bfloat16>(q.x, e[0], e[1]);
+                                unpack2<__nv_bfloat16>(q.y, e[2], e[3]);
+                            }
+                            r[0] = pair2(e);
+                            r[1] = pair2(e + 2);
+                        }
+                        with_act([&](auto act, auto saves) {
+                            f32x2 f[2], df[2];
+                            activate_one<act(), saves()>(add2(a, bias[0]), f[0], df[0]);
+                            activate_one<act(), saves()>(add2(b, bias[1]), f[1], df[1]);
+                            store(0, add2(f[0], r[0]), add2(f[1], r[1]));
+                            if (saves()) *saved(args.f1) = pairs_float4(df[0], df[1]);
+                        });
                     } else {
                         store(un.p, a, b);
                     }
@@ -784,6 +898,65 @@ cudaError_t launch_ffn_down(const void *H, const void *W2, int T, int d, int n, 
     a.ticket = ticket;
     a.err = err;
     return launch<kDown>(m, a, s);
+}
+
+cudaError_t launch_linear_tiled(const LinearCall &c, float *F, float4 *part, uint32_t *ticket, uint32_t *err,
+                                cudaStream_t s) {
+    Maps m{};
+    if (!map_a(&m.a[0], c.f16, c.X, c.k, c.T) || !map_64(&m.b[0], c.f16, c.W, c.n, c.k) ||
+        !map_out(&m.o[0], c.f16, c.Y, c.n, c.T))
+        return cudaErrorInvalidValue;
+    Args a{};
+    a.rows[0] = c.T;
+    a.cols[0] = c.n;
+    a.kb = (c.k + BK - 1) / BK;
+    a.f16 = c.f16;
+    a.act = c.act;
+    a.bias = c.bias;
+    a.bias32 = c.bias32;
+    a.res = c.res;
+    a.f1 = F;
+    a.out[0] = c.Y;
+    a.part = part;
+    a.ticket = ticket;
+    a.err = err;
+    return launch<kLinear>(m, a, s);
+}
+
+cudaError_t launch_linear_products(const void *dA, const void *X, const void *W, int T, int k, int n, bool f16,
+                                   void *dX, void *dW, float4 *part, uint32_t *ticket, uint32_t *err,
+                                   cudaStream_t s) {
+    Maps m{};
+    Args a{};
+    a.f16 = f16;
+    a.part = part;
+    a.ticket = ticket;
+    a.err = err;
+    if (dX != nullptr) {
+        if (!map_a(&m.a[0], f16, dA, n, T) || !map_64(&m.b[0], f16, W, n, k) || !map_out(&m.o[0], f16, dX, k, T))
+            return cudaErrorInvalidValue;
+        m.a[1] = m.a[0];
+        m.b[1] = m.b[0];
+        a.rows[0] = T;
+        a.cols[0] = k;
+        a.kb = a.kb_half = (n + BK - 1) / BK;
+        a.out[0] = dX;
+        const cudaError_t e = launch<kDX>(m, a, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (dW == nullptr) return cudaSuccess;
+    if (!map_64(&m.a[0], f16, X, k, T) || !map_64(&m.b[0], f16, dA, n, T) || !map_out(&m.o[0], f16, dW, n, k))
+        return cudaErrorInvalidValue;
+    for (int i = 1; i < 3; ++i) {  // one problem of three
+        m.a[i] = m.a[0];
+        m.b[i] = m.b[0];
+        m.o[i] = m.o[0];
+    }
+    a.rows[0] = k;
+    a.cols[0] = n;
+    a.kb = (T + BK - 1) / BK;
+    a.out[0] = dW;
+    return launch<kWGrad>(m, a, s);
 }
 
 cudaError_t launch_ffn_backward(const void *dY, const void *X, const void *W1, const void *W3,

@@ -115,11 +115,34 @@ __device__ __forceinline__ void activate(f32x2 a1, f32x2 a3, f32x2 &h, f32x2 &f1
     }
 }
 
+// A projection's activation of a pair, f = act(a), and (TRAIN) df = act'(a). ACT: moe_act_t, or
+// kNoAct: f = a.
+constexpr int kNoAct = MOE_ACT_NONE;
+template <int ACT, bool TRAIN>
+__device__ __forceinline__ void activate_one(f32x2 a, f32x2 &f, f32x2 &df) {
+    if constexpr (ACT == kNoAct) {
+        f = a;
+        if (TRAIN) df = both(1.f);
+    } else {
+        f32x2 h;
+        activate<ACT == MOE_ACT_GELU_TANH, TRAIN>(a, both(1.f), h, df, f);
+    }
+}
+
 __device__ __forceinline__ uint32_t pack(float lo, float hi, bool f16) {
     return f16 ? pack2<__half>(lo, hi) : pack2<__nv_bfloat16>(lo, hi);
 }
 __device__ __forceinline__ uint16_t round16(float v, bool f16) {
     return (uint16_t)(pack(v, 0.f, f16) & 0xffffu);
+}
+
+// Element i of a 16-bit vector.
+__device__ __forceinline__ float load16(const void *p, int64_t i, bool f16) {
+    const uint32_t w = static_cast<const uint16_t *>(p)[i];
+    float x, unused;
+    if (f16) unpack2<__half>(w, x, unused);
+    else unpack2<__nv_bfloat16>(w, x, unused);
+    return x;
 }
 
 // Instruction descriptor: fp32 accumulator, A and B both bf16 or both fp16.

@@ -73,6 +73,8 @@ struct SmallMaps {
 
 struct SmallArgs {
     Product p[2];
+    const void *bias, *res;  // a projection's, or NULL
+    int bias32;
     int T, act, f16;
     uint32_t idesc;
     float *part;       // [CTA][2][matrices][T / 4][128][4]
@@ -124,7 +126,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 // writes and reads 16 bytes at a time.
 // joined() is called once the CTA's outputs are stored, before the tickets are
 // released.
-template <int MATS, int NT, typename Joined>
+// LINEAR: the sums of a projection, out = act(sums + bias) + residual.
+template <int MATS, int NT, bool LINEAR, typename Joined>
 __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p, uint32_t *ticket,
                                          SmallCtl *ctl, uint32_t tmem_base, int &seg, Joined joined) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, T = args.T;
@@ -139,8 +142,15 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
     const int first_tile = (int)(begin / p.kbs), last_tile = (int)((end - 1) / p.kbs);
     auto emit = [&](int tile, int t, float s0, float s1) {
         const int col = tile * 128 + q * 32 + lane;
-        const float v = MATS == 2 ? s0 * act_sigmoid(s0, args.act) * s1 : s0;
-        if (col < p.cols) out[(int64_t)t * p.cols + col] = round16(v, f16);
+        if (col >= p.cols) return;
+        float v = MATS == 2 ? s0 * act_sigmoid(s0, args.act) * s1 : s0;
+        if constexpr (LINEAR) {
+            if (args.bias != nullptr)
+                v += args.bias32 ? __ldg(static_cast<const float *>(args.bias) + col) : load16(args.bias, col, f16);
+            if (args.act != kNoAct) v *= act_sigmoid(v, args.act);
+            if (args.res != nullptr) v += load16(args.res, (int64_t)t * p.cols + col, f16);
+        }
+        out[(int64_t)t * p.cols + col] = round16(v, f16);
     };
     auto is_cut = [&](int tile) {
         return begin > (int64_t)tile * p.kbs || end < (int64_t)(tile + 1) * p.kbs;
@@ -274,11 +284,12 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
     return true;
 }
 
-template <int NT>
+// LINEAR: the second product alone, a projection.
+template <int NT, bool LINEAR>
 __global__ void __launch_bounds__(kThreads, 1)
 stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant__ SmallArgs args) {
     using G = Geo<NT>;
-    constexpr int S = G::kStages;
+    constexpr int S = G::kStages, FIRST = LINEAR ? 1 : 0;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -314,7 +325,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
         uint32_t it = 0;
         bool ok = true;
 #pragma unroll
-        for (int ph = 0; ph < 2; ++ph) {
+        for (int ph = FIRST; ph < 2; ++ph) {
             const Product &p = args.p[ph];
             const Runs run(p);
             const int64_t begin = run.start(blockIdx.x);
@@ -351,7 +362,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
                 return bounded_wait(ptx::smem_addr(&ctl->empty[i % S]), ((i / S) & 1u) ^ 1u, args.err);
             };
             int done = 0;
-            if (ph == 1 && ok && count > 0) {
+            if (!LINEAR && ph == 1 && ok && count > 0) {
                 // a ring full of weights, then (once H is complete) its rows
                 const int ahead = min(count, S);
                 const uint32_t it0 = it;
@@ -408,7 +419,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
         int seg = 0;
         bool ok = true;
 #pragma unroll
-        for (int ph = 0; ph < 2; ++ph) {
+        for (int ph = FIRST; ph < 2; ++ph) {
             const Product &p = args.p[ph];
             const Runs run(p);
             const int64_t begin = run.start(blockIdx.x);
@@ -463,18 +474,21 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
             asm volatile("bar.sync 1, %0;" ::"n"(128 * kSets) : "memory");
             if (warp == 4 && lane == 0) atomicAdd(args.err + kWordGrid, 1u);
         };
-        const bool ok = epilogue<2, NT>(args, args.p[0], args.ticket, ctl, tmem_base, seg, arrive);
-        arrive();  // (without a cut tile, or after a wait that gave up)
+        bool ok = true;
+        if constexpr (!LINEAR) {
+            ok = epilogue<2, NT, false>(args, args.p[0], args.ticket, ctl, tmem_base, seg, arrive);
+            arrive();  // (without a cut tile, or after a wait that gave up)
+        }
         if (ok)
-            epilogue<1, NT>(args, args.p[1], args.ticket + 4 * args.p[0].tiles, ctl, tmem_base, seg,
-                            [] {});
+            epilogue<1, NT, LINEAR>(args, args.p[1], args.ticket + 4 * args.p[0].tiles, ctl, tmem_base, seg,
+                                    [] {});
     }
 
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 2) ptx::tmem_dealloc(tmem_base, G::kTmem);
-    if (tid == 0) {
+    if (!LINEAR && tid == 0) {
         // the last CTA to leave returns the grid's counters to zero
         __threadfence();
         if (atomicAdd(args.err + kWordExit, 1u) == gridDim.x - 1) {
@@ -484,14 +498,14 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
     }
 }
 
-template <int NT>
+template <int NT, bool LINEAR>
 cudaError_t launch_nt(const SmallMaps &maps, SmallArgs args, int grid, cudaStream_t s) {
     constexpr size_t kSmem = Geo<NT>::kSmem;
     args.idesc = idesc(args.f16 != 0, 128, NT, true, false);
     const cudaError_t e =
-        ensure_dynamic_smem(reinterpret_cast<const void *>(stream_ffn_kernel<NT>), (int)kSmem);
+        ensure_dynamic_smem(reinterpret_cast<const void *>(stream_ffn_kernel<NT, LINEAR>), (int)kSmem);
     if (e != cudaSuccess) return e;
-    return launch_together(stream_ffn_kernel<NT>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
+    return launch_together(stream_ffn_kernel<NT, LINEAR>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
 }
 
 int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
@@ -544,9 +558,40 @@ cudaError_t launch_ffn_stream(const void *X, const void *W1, const void *W3, con
     a.err = err;
     const int grid = std::max(a.p[0].ctas, a.p[1].ctas);
     switch (nt) {
-        case 16: return launch_nt<16>(m, a, grid, s);
-        case 32: return launch_nt<32>(m, a, grid, s);
-        default: return launch_nt<64>(m, a, grid, s);
+        case 16: return launch_nt<16, false>(m, a, grid, s);
+        case 32: return launch_nt<32, false>(m, a, grid, s);
+        default: return launch_nt<64, false>(m, a, grid, s);
+    }
+}
+
+size_t linear_stream_part_bytes(int T, int k, int n) {
+    const size_t ctas = make_product(n, k, 2 * BK, kFfnMaxCtas, nullptr).ctas;
+    return ctas * 2 * ((T + 3) / 4) * 128 * 4 * sizeof(float);
+}
+
+cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *ticket, uint32_t *err, cudaStream_t s) {
+    const int nt = padded_tokens(c.T);
+    SmallMaps m{};
+    const CUtensorMapDataType ty = map_type(c.f16);
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_map(&m.w[2], ty, c.W, c.n, c.k, 64, BK, sw) || !make_map(&m.h, ty, c.X, c.k, c.T, 64, nt, sw))
+        return cudaErrorInvalidValue;
+    SmallArgs a{};
+    a.p[1] = make_product(c.n, c.k, 2 * BK, sm_count(), c.Y);
+    a.bias = c.bias;
+    a.bias32 = c.bias32;
+    a.res = c.res;
+    a.T = c.T;
+    a.act = c.act;
+    a.f16 = c.f16;
+    a.part = part;
+    a.ticket = ticket;
+    a.err = err;
+    const int grid = a.p[1].ctas;
+    switch (nt) {
+        case 16: return launch_nt<16, true>(m, a, grid, s);
+        case 32: return launch_nt<32, true>(m, a, grid, s);
+        default: return launch_nt<64, true>(m, a, grid, s);
     }
 }
 

@@ -33,6 +33,7 @@ LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_g
             "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1,
             "moe_layernorm": 1, "moe_layernorm_backward": 2, "moe_dropout": 1,
             "moe_dropout_backward": 1, "moe_ffn": 2, "moe_ffn_train": 2, "moe_ffn_backward": 3,
+            "moe_linear": 1, "moe_linear_train": 1, "moe_linear_backward": 4,
             "moe_block_norm": 1, "moe_block_norm_backward": 2, "moe_rmsnorm": 1,
             "moe_rmsnorm_backward": 2, "moe_dispatch": 1, "moe_combine_weighted": 1, "moe_combine_weighted_backward": 1}
 TILE_M = 128
@@ -104,6 +105,10 @@ _SIGS = {
                                    _P]),
     "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
                               _P, _SZ, _P]),
+    "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_linear_forward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_linear_forward_train": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_linear_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_block_norm_forward": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _I, _L, _I, _F, _I, _I,
                                     _P, _L, _P, _L, _P, _P, _P]),
     "moe_block_norm_scratch_bytes": (_SZ, [_L, _I]),
@@ -657,6 +662,10 @@ def ffn_workspace(T: int, d: int, n: int, train: bool = False, device=None, stre
     nbytes = int(lib().moe_ffn_workspace_bytes(T, d, n, int(train)))
     if nbytes == 0:
         raise ValueError("invalid feed-forward shape")
+    return _control_workspace(nbytes, device, stream)
+
+
+def _control_workspace(nbytes: int, device, stream):
     device = None if device is None else torch.device(device)
     if device is not None:
         if device.type != "cuda":
@@ -704,6 +713,57 @@ def moe_ffn_backward(dY, x, W1, W3, W2, H, F1, F3, act: str = "silu", need_dx: b
     for). ws: ffn_workspace(..., train=True)."""
     return _native().ffn_backward(dY, x, W1, W3, W2, H, F1, F3, _act(act), need_dx, need_dw,
                                   _ffn_ws(ws, x, W1, True, stream), stream)
+
+# ------------------------------------------- a dense projection with its epilogue
+
+
+def linear_workspace(T: int, k: int, n: int, train: bool = False, device=None, stream=None):
+    """A workspace (uint8, control words zeroed) of the projection calls for up to T tokens;
+    train: of moe_linear_train and moe_linear_backward too. Where it lies: as ffn_workspace."""
+    nbytes = int(lib().moe_linear_workspace_bytes(T, k, n, int(train)))
+    if nbytes == 0:
+        raise ValueError("invalid projection shape")
+    return _control_workspace(nbytes, device, stream)
+
+
+def _linear_act(act) -> int:
+    return 2 if act is None else _act(act)
+
+
+def _linear_ws(ws, x, W, train, stream):
+    if ws is not None:
+        return ws
+    if not x.is_cuda or x.dim() < 1 or W.dim() != 2 or W.numel() == 0:
+        raise ValueError("x must be a CUDA tensor [..., k] and W [k, n]")
+    k, n = W.shape
+    return linear_workspace(x.numel() // k, k, n, train, x.device, stream)
+
+
+def moe_linear(x, W, bias=None, act=None, residual=None, ws=None, Y=None, stream=None):
+    """Y = act(x W + bias) + residual of x [..., k] (bf16 or fp16); act None, "silu" or "gelu"
+    (the tanh form), bias [n] of x's type or fp32. Y may be residual. ws: linear_workspace, kept
+    between calls."""
+    return _native().linear(x, W, bias, _linear_act(act), residual, _linear_ws(ws, x, W, False, stream), Y,
+                            stream)
+
+
+def moe_linear_train(x, W, bias=None, act=None, residual=None, ws=None, stream=None):
+    """(Y, F): moe_linear's Y and F = act'(x W + bias), which moe_linear_backward takes (fp32 in
+    the blocks that moe.h describes; None without an activation). ws: linear_workspace(..., train=True)."""
+    return _native().linear_train(x, W, bias, _linear_act(act), residual, _linear_ws(ws, x, W, True, stream),
+                                  stream)
+
+
+def moe_linear_backward(dY, x, W, F, bias_dtype=None, need_dx: bool = True, need_dw: bool = True, ws=None,
+                        stream=None):
+    """(dX, dW, dbias) of moe_linear_train, of x's type, dbias of bias_dtype (x's type or fp32;
+    None: there was no bias); None where not asked for. The residual's gradient is dY. ws:
+    linear_workspace(..., train=True)."""
+    if bias_dtype not in (None, torch.float32, x.dtype):
+        raise TypeError(f"the bias' gradient is {x.dtype} or fp32, got {bias_dtype}")
+    return _native().linear_backward(dY, x, W, F, None if bias_dtype is None else bias_dtype is not x.dtype,
+                                     need_dx, need_dw, _linear_ws(ws, x, W, True, stream), stream)
+
 
 # --------------------------------------------------- the norms around a block
 
