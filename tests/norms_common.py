@@ -71,6 +71,10 @@ def backward(dy, du, x, b, post, pre, gate, scale, eps, post_norm=True, pre_norm
         out["dgate"] = (o["h"] * fb, o["h"] * Fb)
         if gate.dim() < x.dim():
             out["dgate"] = tuple(v.sum(-1) for v in out["dgate"])
+        else:
+            # for 16-bit results 2^x flushes what is under 2^-126: 1 - g is off by that much at
+            # most, which is 2^-102 in units of 2^-24
+            out["dgate"] = (out["dgate"][0], out["dgate"][1] + 2.0 ** -102 * Fb / C["dgate"])
     out["dpost"] = ((o["g"] * dY * bh).flatten(0, -2).sum(0), (o["g"] * D * bh.abs()).flatten(0, -2).sum(0))
     return out
 

@@ -25,6 +25,11 @@ CASES = [
     (170, 4096, BF, BF, "row", (1, 1), 1.0, None), (4, 4096, F32, F32, "full", (1, 1), 1.0, None),
     (160, 7168, BF, BF, "full", (1, 1), 1.0, None), (160, 7168, FP16, F32, "full", (1, 1), 1.0, None),
     (3, 7167, BF, BF, "full", (1, 1), 1.0, None), (310, 8192, BF, F32, "row", (1, 1), 1.0, None),
+    # rows that start anywhere: every place of 16 bytes, whole warps of vectors and one more
+    (41, 512, BF, F32, "full", (1, 1), 1.0, 513), (23, 1024, FP16, FP16, "row", (1, 1), 1.0, 1027),
+    (19, 256, F32, F32, "full", (1, 1), 0.5, 257), (30, 9, BF, BF, "full", (1, 1), 1.0, 10),
+    (700, 515, BF, BF, "full", (1, 1), 1.0, None), (333, 4099, FP16, F32, "full", (1, 1), 1.0, 4101),
+    (7, 130, BF, BF, "full", (0, 1), 1.0, 131), (7, 1, BF, BF, "full", (1, 0), 1.0, 3),
     (2, 16384, F32, F32, "full", (1, 1), 1.0, None), (2, 16384, BF, BF, "full", (1, 1), 1.0, None),
     (2, 16381, BF, F32, "row", (1, 1), 1.0, None), (3, 12000, BF, BF, "full", (1, 1), 1.0, None),
 ]
@@ -94,13 +99,17 @@ def test_forward_and_backward(case):
     # results in the places of inputs
     again = moe.moe_block_norm_backward(m["dy"], m["du"] if pre_norm else None, m["x"], m["b"], m["post"],
                                         m["pre"] if pre_norm else None, r_post, r_pre, dx=m["dy"], db=m["b"], **kw)
-    assert all(p is q is None or torch.equal(p, q) for p, q in zip(got, again))
+    # (the order of sums may go with where the first output's rows start)
+    check(dict(zip(names, again)), plain.backward(dy, du, *args), T, z, "in place ")
     assert again[0].data_ptr() == m["dy"].data_ptr() and again[1].data_ptr() == m["b"].data_ptr()
     m = inputs(case)
     y2, u2 = moe.moe_block_norm(m["x"], m["b"], m["post"], m["pre"] if pre_norm else None, eps=EPS, y=m["x"],
                                 post_norm=bool(post_norm), pre_norm=bool(pre_norm), gate=m["gate"], scale=scale,
                                 u=m["b"] if pre_norm else None)
-    assert y2.data_ptr() == m["x"].data_ptr() and torch.equal(y2, y) and (u is None or torch.equal(u2, u))
+    assert y2.data_ptr() == m["x"].data_ptr()
+    assert_close(y2, o["y"], o["Y"], plain.C["y"] + 2 * z, "y in place")
+    if pre_norm:
+        assert_close(u2, o["u"], o["U"], plain.C["u"] + 2 * z, "u in place")
 
 
 @pytest.mark.parametrize("case", [c for c in CASES if c[4] is None or c[1] in (1, 7, 1023, 2049, 7168, 16384)], ids=str)
@@ -116,9 +125,10 @@ def test_rmsnorm(case):
     for res in (None, dy):
         dx, dgamma = moe.moe_rmsnorm_backward(m["du"], m["x"], m["pre"], rstd, dres=None if res is None else m["dy"])
         check({"dx": dx, "dpre": dgamma}, plain.backward(res, du, x, None, None, pre, None, 1.0, EPS), T, 0)
+    ref = plain.backward(dy, du, x, None, None, pre, None, 1.0, EPS)
     again, _ = moe.moe_rmsnorm_backward(m["du"], m["x"], m["pre"], rstd, dres=m["dy"], dx=m["du"])
-    assert torch.equal(again, dx)
-    assert torch.equal(moe.moe_rmsnorm(m["x"], m["pre"], EPS, y=m["x"]), u)
+    check({"dx": again, "dpre": dgamma}, ref, T, 0, "in place ")
+    assert_close(moe.moe_rmsnorm(m["x"], m["pre"], EPS, y=m["x"]), o["u"], o["U"], plain.C["u"], "y in place")
 
 
 def test_without_weights():
@@ -154,6 +164,43 @@ def test_zero_rows_and_steep_gates(d, ld, dt):
         assert_close(y, o["y"], o["Y"], 250, "y")
         assert_close(u, o["u"], o["U"], 300, "u")
         check(dict(zip(("dx", "db", "dgate", "dpost", "dpre"), got)), plain.backward(dy.cpu(), du.cpu(), *args), T, 200)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+def test_operands_that_start_at_different_places(dt):
+    """Each operand in a buffer of its own stride and start."""
+    T, d = 45, 300
+    gen = torch.Generator().manual_seed(17)
+
+    def mat(ld, start):
+        v = torch.randn(T * ld + start + d, generator=gen).to(dt).cuda()
+        return torch.as_strided(v, (T, d), (ld, 1), start)
+
+    x, b, gate, dy, du = mat(301, 0), mat(303, 1), mat(300, 3), mat(307, 2), mat(302, 5)
+    y, u, dx, db = mat(305, 4), mat(300, 0), mat(309, 7), mat(304, 1)
+    w = torch.randn(d, generator=gen).to(dt).cuda()
+    _, _, rp, rq = moe.moe_block_norm(x, b, w, w, gate=gate, stats=True, y=y, u=u)
+    args = (x.cpu(), b.cpu(), w.cpu(), w.cpu(), gate.cpu(), 1.0, EPS)
+    o, z = plain.forward(*args), steepest(gate)
+    assert_close(y, o["y"], o["Y"], plain.C["y"] + 2 * z, "y")
+    assert_close(u, o["u"], o["U"], plain.C["u"] + 2 * z, "u")
+    got = moe.moe_block_norm_backward(dy, du, x, b, w, w, rp, rq, gate=gate, dx=dx, db=db)
+    check(dict(zip(("dx", "db", "dgate", "dpost", "dpre"), got)), plain.backward(dy.cpu(), du.cpu(), *args), T, z)
+
+
+def test_writes_nothing_else():
+    """What lies around the rows of the outputs stays as it was."""
+    T, d, ld = 37, 203, 210
+    gen = torch.Generator().manual_seed(18)
+    x, b, gate, dy, du = (matrix(T, d, BF, gen, 205) for _ in range(5))
+    bufs = [torch.full((T + 2, ld), 7.0, device="cuda", dtype=BF) for _ in range(4)]
+    y, u, dx, db = (v[1:-1, 3:3 + d] for v in bufs)
+    _, _, rp, rq = moe.moe_block_norm(x, b, gate=gate, stats=True, y=y, u=u)
+    moe.moe_block_norm_backward(dy, du, x, b, None, None, rp, rq, gate=gate, dx=dx, db=db)
+    for v, inner in zip(bufs, (y, u, dx, db)):
+        assert not (inner == 7.0).all()
+        inner.fill_(7.0)
+        assert (v == 7.0).all()
 
 
 def test_not_a_number_stays_in_its_row():
@@ -234,7 +281,7 @@ def test_offsets_past_32_bits():
     y, u, rp, rq = moe.moe_block_norm(x, b, gate=b, stats=True, y=torch.empty_like(want[0]))
     assert torch.equal(y, want[0]) and torch.equal(u, want[1])
     want = moe.moe_block_norm_backward(y, u, x.contiguous(), b.contiguous(), None, None, rp, rq, gate=b.contiguous())
-    got = moe.moe_block_norm_backward(y, u, x, b, None, None, rp, rq, gate=b, dx=x)
+    got = moe.moe_block_norm_backward(y, u, x, b, None, None, rp, rq, gate=b, dx=x)  # (all rows start on 16 bytes)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 

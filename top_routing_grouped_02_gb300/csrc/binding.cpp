@@ -366,7 +366,7 @@ PyObject *block_norm(PyObject *const *a, Py_ssize_t n) {
           moe_block_norm_forward(rx.p, rx.ld, rb.p, rb.ld, g.p, g.ld, g.kind, pp, pq, (float)scale,
                                  norms_of(post_norm, pre_norm), rx.T, (int)rx.d, (float)eps, dtype(x), wt, ry.p,
                                  ry.ld, ru.p, ru.ld, floats(r_post), floats(r_pre), stream));
-    return wrap_all(y, u, r_post, r_pre);
+    return stats ? wrap_all(y, u, r_post, r_pre) : wrap_all(y, u);
 }
 
 // dy, du, x, b, post, pre, rstd_post, rstd_pre, gate, scale, fp32 weight gradients without

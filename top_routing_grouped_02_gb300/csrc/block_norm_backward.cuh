@@ -1,0 +1,446 @@
+// The norms around a block (block_norm.cuh), gradients, for one element type: with e = pre du,
+//   dY   = dy + r_pre (e - yh mean(e yh))          the whole gradient of y
+//   f    = g dY post                               the gradient of bh
+//   dx   = scale dY,   db = r_post (f - bh mean(f bh))
+//   dgate = dY n g (1 - g) = f bh (1 - g), of a row's gate summed over the row
+//   dpost = sum over rows of g dY bh,   dpre = sum over rows of du yh
+// y is formed again from x, b and the gate, in fp32, as in the forward (reading the rounded y
+// instead would cost as much and lose the rounded bits).
+//
+// Bound by HBM: x, b, the gate, dy and du are read once, dx, db and dgate written once. Two
+// sums over a row: e yh before dY, f bh before db (a row's dgate is (1 - g) times the
+// second). Each thread owns its columns and sums dpost and dpre over its group's rows in
+// registers; a block's groups are added in order through shared memory, the blocks' partial
+// rows by a second kernel, in order: no atomics, the result does not depend on timing.
+#pragma once
+
+#include <algorithm>
+
+#include "block_norm.cuh"
+
+namespace moe {
+namespace bn {
+namespace {
+
+constexpr int kBwdThreads = 512, kBwdFewThreads = 448;  // most of a block with a ring
+
+// A block's row of partial sums from its groups' [groups][2][n], in order; the columns lie `lead`
+// elements on.
+__device__ __forceinline__ void add_groups(const Args &a, const float *sums, int n, int lead, int groups, bool lost) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) {
+        const float *at = sums + (c < a.d ? lead + c : n + lead + c - a.d);
+        float s = lost ? NAN : at[0];
+        for (int k = 1; k < groups; ++k) s += at[(size_t)2 * k * n];
+        a.part[(size_t)blockIdx.x * 2 * a.d + c] = s;
+    }
+}
+
+// Rows that no ring holds, straight from global memory: each pass forms again what it needs,
+// from L1 or L2. All results are written by the last pass, after the thread's last read, so
+// that they may replace inputs.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(1024) backward_rows_kernel(const Args a) {
+    extern __shared__ float sums[];  // [groups][2][d]
+    __shared__ float slots[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int tpr = a.wpr * 32, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+    const int groups = blockDim.x / tpr, nvec = a.d / V;
+    const float inv_d = 1.f / (float)a.d;
+    GroupSum sum{slots, group * a.wpr, a.wpr, 1 + group};
+    float dpost[NV][V], dpre[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) dpost[i][j] = dpre[i][j] = 0.f;
+    for (int64_t row = (int64_t)blockIdx.x * groups + group; row < a.T; row += (int64_t)gridDim.x * groups) {
+        const float r_post = a.post_norm ? a.r_post[row] : 1.f, r_pre = a.pre_norm ? a.r_pre[row] : 0.f;
+        float g_row = 1.f, h_row = 0.f;
+        if (a.gate != nullptr && !a.full) sigmoid(static_cast<const float *>(a.gate)[row], g_row, h_row);
+        // of a vector: yh, bh, g and 1 - g, du and dy
+        float yh[V], bh[V], g[V], h[V], du[V], dy[V];
+        auto form = [&](int v) {
+            float x[V], z[V];
+            load_row<T, V>(a.x, a.ldx, row, v, x);
+            if (a.b != nullptr) load_row<T, V>(a.b, a.ldb, row, v, bh);
+            if (a.full) load_row<T, V>(a.gate, a.ldg, row, v, z);
+            if (a.pre_norm) load_row<T, V>(a.du, a.lddu, row, v, du);
+            if (a.dy != nullptr) load_row<T, V>(a.dy, a.lddy, row, v, dy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                g[j] = g_row;
+                h[j] = h_row;
+                if (a.full) sigmoid(z[j], g[j], h[j]);
+                float y = x[j];
+                if (a.b != nullptr) {
+                    bh[j] *= r_post;
+                    y = fmaf(a.scale, y, g[j] * (bh[j] * load_w<T>(a.post, a.w32, v * V + j, 1.f)));
+                } else {
+                    bh[j] = 0.f;
+                }
+                yh[j] = y * r_pre;
+                if (!a.pre_norm) du[j] = 0.f;
+                if (a.dy == nullptr) dy[j] = 0.f;
+            }
+        };
+        auto weight = [&](const void *w, int v, int j) { return load_w<T>(w, a.w32, v * V + j, 1.f); };
+        float s = 0.f;
+        if (a.pre_norm) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = i * tpr + t;
+                if (v >= nvec) continue;
+                form(v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) s = fmaf(du[j] * weight(a.pre, v, j), yh[j], s);
+            }
+        }
+        const float c1 = a.pre_norm ? sum(s) * inv_d : 0.f;
+        // dY of element j of vector v
+        auto grad_y = [&](int v, int j) {
+            return fmaf(r_pre, fmaf(-c1, yh[j], du[j] * weight(a.pre, v, j)), dy[j]);
+        };
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            if (v >= nvec) continue;
+            form(v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float gd = g[j] * grad_y(v, j) * bh[j];
+                dpost[i][j] += gd;
+                dpre[i][j] = fmaf(du[j], yh[j], dpre[i][j]);
+                s = fmaf(gd, weight(a.post, v, j), s);
+            }
+        }
+        if (a.b != nullptr) s = sum(s);
+        const float c2 = a.post_norm ? s * inv_d : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            if (v >= nvec) continue;
+            form(v);
+            float dx[V], db[V], dz[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float gy = grad_y(v, j), f = g[j] * gy * weight(a.post, v, j);
+                dx[j] = a.b != nullptr ? a.scale * gy : gy;
+                dz[j] = f * bh[j] * h[j];
+                db[j] = r_post * fmaf(-c2, bh[j], f);
+            }
+            store_row<T, V>(a.dx, a.lddx, row, v, dx);
+            if (a.b != nullptr) store_row<T, V>(a.db, a.lddb, row, v, db);
+            if (a.full) store_row<T, V>(a.dgate, a.lddg, row, v, dz);
+        }
+        if (t == 0 && a.gate != nullptr && !a.full) static_cast<float *>(a.dgate)[row] = h_row * s;
+    }
+    if (a.part == nullptr) return;
+    // the groups' sums in order
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * tpr + t;
+        if (v >= nvec) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            sums[(size_t)(2 * group) * a.d + v * V + j] = dpost[i][j];
+            sums[(size_t)(2 * group + 1) * a.d + v * V + j] = dpre[i][j];
+        }
+    }
+    add_groups(a, sums, a.d, 0, groups, false);
+}
+
+template <typename T, int V, int NV>
+cudaError_t backward_rows(Args a, int *P, cudaStream_t s) {
+    RowShape r = row_shape(a, V * NV);
+    r.grid = std::min(r.grid, kLnPartials);
+    *P = r.grid;
+    const size_t smem = a.part != nullptr ? (size_t)r.groups * 2 * a.d * sizeof(float) : 0;
+    const cudaError_t e = ensure_dynamic_smem(
+        reinterpret_cast<const void *>(backward_rows_kernel<T, V, NV>), (int)(2 * kBlockNormMaxWidth * sizeof(float)));
+    if (e != cudaSuccess) return e;
+    return launch_k(backward_rows_kernel<T, V, NV>, dim3(r.grid), dim3(r.groups * a.wpr * 32), smem, s, a);
+}
+
+// Rows through a ring, as the forward's. A stage holds x, b (MODE 1, 2) and the gate (MODE 2),
+// then du and dy, where the call has them. MT: most threads.
+template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW, int MT>
+__global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
+    extern __shared__ __align__(128) uint8_t ring_sh[];
+    RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
+    using Wt = Weights<T, V, SHIFT, RAW>;
+    constexpr int P2 = V / 2;
+    const int tpr = a.wpr * 32, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+    const int groups = blockDim.x / tpr, S = a.stages;
+    const bool has_du = a.pre_norm, has_dy = a.dy != nullptr;
+    const int K = MODE + 1 + has_du + has_dy;
+    const uint32_t row_bytes = ring_row_bytes<T, SHIFT>(a.d);
+    const uint32_t stage_bytes = K * row_bytes, w_bytes = Wt::bytes(a.d);
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    if (SHIFT) row = blockIdx.x % kPhases + (int64_t)kPhases * (blockIdx.x / kPhases * groups + group);
+    // (the rows of a block start at the same place: its first row's, there or not)
+    const Part<T, V, SHIFT> part(tpr, t, a.d, static_cast<T *>(a.dx) + blockIdx.x % kPhases * a.lddx);
+    uint8_t *post = ring_sh + kRingCtl, *pre = post + (MODE > 0 ? w_bytes : 0), *rings = pre + w_bytes;
+    uint8_t *ring = rings + (size_t)group * S * stage_bytes;
+    const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, K);
+        ptx::fence_barrier_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    // row r of the stage's tensor k into stage s: a thread each
+    auto fetch = [&](int64_t r, int s, int k) {
+        if (r == a.withheld) return;
+        const void *p = a.x;
+        int64_t ld = a.ldx;
+        if (MODE > 0 && k == 1) p = a.b, ld = a.ldb;
+        if (MODE > 1 && k == 2) p = a.gate, ld = a.ldg;
+        if (k > MODE) {
+            const bool u = has_du && k == MODE + 1;
+            p = u ? a.du : a.dy;
+            ld = u ? a.lddu : a.lddy;
+        }
+        fetch_row<T, SHIFT>(ring + (size_t)s * stage_bytes + (size_t)k * row_bytes, p, ld, r, a.T, a.d, bar0 + 8 * s);
+    };
+    __syncwarp();
+    if (t < S * K && row + t / K * stride < a.T) fetch(row + t / K * stride, t / K, t % K);
+    if (MODE > 0) Wt::fill(post, a.post, a.w32, part);
+    Wt::fill(pre, a.pre, a.w32, part);
+    __syncthreads();
+
+    f32x2 dpost[NV][P2], dpre[NV][P2];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P2; ++j) dpost[i][j] = dpre[i][j] = 0;
+    auto off = [&](const void *p, int64_t ld) { return part.off(static_cast<const T *>(p) + blockIdx.x % kPhases * ld); };
+    const int ox = off(a.x, a.ldx), ob = MODE > 0 ? off(a.b, a.ldb) : 0, oz = MODE > 1 ? off(a.gate, a.ldg) : 0;
+    const int ou = has_du ? off(a.du, a.lddu) : 0, oy = has_dy ? off(a.dy, a.lddy) : 0;
+    const int odx = 0, odb = MODE > 0 ? off(a.db, a.lddb) : 0, odz = MODE > 1 ? off(a.dgate, a.lddg) : 0;
+    const float inv_d = 1.f / (float)a.d;
+    GroupSum sum{ctl->slots, group * a.wpr, a.wpr, 1 + group};
+    int s = 0;
+    uint32_t ph = 0;
+    bool alive = true;
+    for (; row < a.T; row += stride) {
+        float g_row = 1.f, h_row = 0.f;
+        if (MODE == 1 && a.gate != nullptr) sigmoid(static_cast<const float *>(a.gate)[row], g_row, h_row);
+        const float r_post = MODE > 0 && a.post_norm ? a.r_post[row] : 1.f, r_pre = has_du ? a.r_pre[row] : 0.f;
+        alive = alive && ring_wait(bar0, S, s, ph, t < K);
+        const uint8_t *stage = ring + (size_t)s * stage_bytes;
+        const uint8_t *px = stage + image_at<T, SHIFT>(a.x, a.ldx, row);
+        const uint8_t *pb = stage + row_bytes + (MODE > 0 ? image_at<T, SHIFT>(a.b, a.ldb, row) : 0);
+        const uint8_t *pz = stage + 2 * row_bytes + (MODE > 1 ? image_at<T, SHIFT>(a.gate, a.ldg, row) : 0);
+        const uint8_t *pu = stage + (MODE + 1) * row_bytes + image_at<T, SHIFT>(a.du, a.lddu, row);
+        const uint8_t *py = stage + (MODE + 1 + has_du) * row_bytes + image_at<T, SHIFT>(a.dy, a.lddy, row);
+        // (a row that did not come: NaN)
+        const f32x2 scale = both(alive ? a.scale : NAN), rp = both(alive ? r_post : NAN), rq = both(r_pre);
+        // yh, then f; g and 1 - g, then bh
+        f32x2 yh[NV][P2], g[NV][P2], h[MODE == 2 ? NV : 1][P2], q = alive ? 0 : both(NAN);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!part.has(i)) continue;
+            f32x2 w[P2], du[P2];
+            part.load(px, ox, i, yh[i]);
+            if (MODE > 0) {
+                f32x2 b[P2];
+                part.load(pb, ob, i, b);
+                Wt::load(part, post, i, w);
+                if (MODE == 2) {
+                    f32x2 z[P2];
+                    part.load(pz, oz, i, z);
+#pragma unroll
+                    for (int j = 0; j < P2; ++j) sigmoid2<T, true>(z[j], g[i][j], h[i][j]);
+                }
+#pragma unroll
+                for (int j = 0; j < P2; ++j)
+                    yh[i][j] = fma2(scale, yh[i][j], mul2(mul2(mul2(b[j], rp), w[j]), MODE == 2 ? g[i][j] : both(g_row)));
+            }
+            if (has_du) {
+                part.load(pu, ou, i, du);
+                Wt::load(part, pre, i, w);
+#pragma unroll
+                for (int j = 0; j < P2; ++j) {
+                    yh[i][j] = mul2(yh[i][j], rq);
+                    dpre[i][j] = fma2(du[j], yh[i][j], dpre[i][j]);
+                    q = fma2(mul2(du[j], w[j]), yh[i][j], q);
+                }
+            }
+        }
+        const f32x2 c1 = both(has_du ? -sum(pair_sum(q)) * inv_d : 0.f);
+        q = alive ? 0 : both(NAN);
+        T *xrow = static_cast<T *>(a.dx) + row * a.lddx, *brow = static_cast<T *>(a.db) + row * a.lddb;
+        T *zrow = static_cast<T *>(a.dgate) + row * a.lddg;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!part.has(i)) continue;
+            f32x2 w[P2], d[P2];
+            // dY
+#pragma unroll
+            for (int j = 0; j < P2; ++j) d[j] = 0;
+            if (has_dy) part.load(py, oy, i, d);
+            if (has_du) {
+                f32x2 du[P2];
+                part.load(pu, ou, i, du);
+                Wt::load(part, pre, i, w);
+#pragma unroll
+                for (int j = 0; j < P2; ++j) d[j] = fma2(rq, fma2(yh[i][j], c1, mul2(du[j], w[j])), d[j]);
+            }
+            if (MODE == 0) {
+                part.store(xrow, odx, i, d);
+                continue;
+            }
+            f32x2 b[P2], o[P2];
+            part.load(pb, ob, i, b);
+            Wt::load(part, post, i, w);
+#pragma unroll
+            for (int j = 0; j < P2; ++j) {
+                o[j] = mul2(scale, d[j]);
+                d[j] = mul2(d[j], MODE == 2 ? g[i][j] : both(g_row));
+                b[j] = mul2(b[j], rp);
+                dpost[i][j] = fma2(d[j], b[j], dpost[i][j]);
+                d[j] = mul2(d[j], w[j]);  // f
+            }
+            part.store(xrow, odx, i, o);
+#pragma unroll
+            for (int j = 0; j < P2; ++j) {
+                const f32x2 fb = mul2(d[j], b[j]);
+                q = add2(q, fb);
+                if (MODE == 2) o[j] = mul2(fb, h[i][j]);
+                yh[i][j] = d[j];
+                g[i][j] = b[j];
+            }
+            if (MODE == 2) part.store(zrow, odz, i, o);
+        }
+        float ss = 0.f;
+        if (MODE > 0) ss = sum(pair_sum(q));
+        else if (a.wpr > 1) group_sync(1 + group, tpr);
+        if (a.wpr == 1) __syncwarp();
+        // every thread of the group is done with the stage
+        if (t < K && alive && row + S * stride < a.T) fetch(row + S * stride, s, t);
+        if (MODE > 0) {
+            if (MODE == 1 && t == 0 && a.gate != nullptr) static_cast<float *>(a.dgate)[row] = h_row * ss;
+            const f32x2 c2 = both(a.post_norm ? -ss * inv_d : 0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!part.has(i)) continue;
+                f32x2 o[P2];
+#pragma unroll
+                for (int j = 0; j < P2; ++j) o[j] = mul2(rp, fma2(g[i][j], c2, yh[i][j]));
+                part.store(brow, odb, i, o);
+            }
+        }
+        if (++s == S) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+    if (a.part == nullptr) return;
+    if constexpr (!SHIFT) {
+        bool ok[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) ok[i] = part.has(i);
+        store_partials<V, NV>(a.part, a.d, groups, group, tpr, t, ok, dpost, dpre, rings, (size_t)S * stage_bytes, !alive);
+    } else {
+        // every thread is done with the last rows
+        const bool lost = __syncthreads_or(!alive);
+        float *sums = reinterpret_cast<float *>(rings);  // [groups][2][nvec V], `lead` columns on
+        const int n = part.nvec * V;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!part.has(i)) continue;
+            f32x2 *at = reinterpret_cast<f32x2 *>(sums + (size_t)2 * group * n + (i * tpr + t) * V);
+#pragma unroll
+            for (int j = 0; j < P2; ++j) {
+                at[j] = dpost[i][j];
+                at[n / 2 + j] = dpre[i][j];
+            }
+        }
+        add_groups(a, sums, n, part.lead, groups, lost);
+    }
+}
+
+template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
+    const size_t stage = (MODE + 1 + a.pre_norm + (a.dy != nullptr)) * ring_row_bytes<T, SHIFT>(a.d);
+    const size_t fixed = kRingCtl + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(a.d);
+    // (a group's ring holds its fp32 sums in the end, [2][d] and up to two vectors more)
+    const size_t sums = 2 * ((size_t)a.d + 2 * V) * sizeof(float);
+    if (!ring_shape(a, ring_cols<V, SHIFT>(a.d), V * NV, threads, fixed, stage, sums, groups) ||
+        a.stages * stage < sums)
+        return false;
+    *smem = fixed + *groups * a.stages * stage;
+    return true;
+}
+// The block of at most 448 threads is compiled for as many registers as that of 512 (128), but
+// runs 8 to 10 % faster where both have the same groups, or nearly (8192 x 7168 bf16 180 / 200
+// us, 4096 x 1024 19.7 / 21.4; 4096 x 4096, one group against two, 77 / 58).
+template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+bool backward_best(Args &a, int *threads, int *groups, size_t *smem) {
+    Args few = a;
+    int g = 0;
+    size_t m = 0;
+    *threads = kBwdThreads;
+    const bool fits = backward_shape<T, V, NV, MODE, SHIFT, RAW>(a, kBwdThreads, groups, smem);
+    if (fits && backward_shape<T, V, NV, MODE, SHIFT, RAW>(few, kBwdFewThreads, &g, &m) && 5 * g >= 4 * *groups) {
+        a = few;
+        *threads = kBwdFewThreads;
+        *groups = g;
+        *smem = m;
+    }
+    return fits;
+}
+template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+cudaError_t backward_launch(const Args &a, int threads, int groups, size_t smem, int *P, cudaStream_t s) {
+    const auto kernel = threads == kBwdFewThreads
+                            ? backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdFewThreads>
+                            : backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdThreads>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)kRingSmem);
+    if (e != cudaSuccess) return e;
+    *P = ring_grid<SHIFT>(a.T, groups, std::min(sm_count(), kLnPartials));
+    return launch_k(kernel, dim3(*P), dim3(groups * a.wpr * 32), smem, s, a);
+}
+// (weights as in the forward)
+template <typename T, int MODE, bool SHIFT>
+cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T), NV = 16 / V;  // 16 elements a thread
+    Args planes = a;
+    int groups = 0, threads = 0;
+    size_t smem = 0;
+    *fits = backward_best<T, V, NV, MODE, SHIFT, false>(planes, &threads, &groups, &smem);
+    if constexpr (sizeof(T) == 2) {
+        Args raw = a;
+        int more = 0, t = 0;
+        size_t less = 0;
+        if (!a.w32 && backward_best<T, V, NV, MODE, SHIFT, true>(raw, &t, &more, &less) &&
+            (!*fits || rows_ahead(raw, more) > rows_ahead(planes, groups))) {
+            *fits = true;
+            return backward_launch<T, V, NV, MODE, SHIFT, true>(raw, t, more, less, P, s);
+        }
+    }
+    return *fits ? backward_launch<T, V, NV, MODE, SHIFT, false>(planes, threads, groups, smem, P, s) : cudaSuccess;
+}
+template <typename T, bool SHIFT>
+cudaError_t backward_rings(const Args &a, int *P, bool *fits, cudaStream_t s) {
+    return a.b == nullptr ? backward_ring<T, 0, SHIFT>(a, P, fits, s)
+           : !a.full      ? backward_ring<T, 1, SHIFT>(a, P, fits, s)
+                          : backward_ring<T, 2, SHIFT>(a, P, fits, s);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t backward_type(const Args &a, const Align &al, int *P, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T);
+    bool fits = false;
+    const cudaError_t e =
+        al.fits(16) ? backward_rings<T, false>(a, P, &fits, s) : backward_rings<T, true>(a, P, &fits, s);
+    if (e != cudaSuccess || fits) return e;
+    return al.fits(16) ? backward_rows<T, W, 16 / W>(a, P, s) : backward_rows<T, 1, 16>(a, P, s);
+}
+
+}  // namespace bn
+}  // namespace moe

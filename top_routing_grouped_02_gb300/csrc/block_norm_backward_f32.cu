@@ -1,0 +1,7 @@
+#include "block_norm_backward.cuh"
+
+namespace moe {
+namespace bn {
+template cudaError_t backward_type<float>(const Args &, const Align &, int *, cudaStream_t);
+}  // namespace bn
+}  // namespace moe

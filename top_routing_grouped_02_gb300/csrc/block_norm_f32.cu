@@ -1,0 +1,7 @@
+#include "block_norm_forward.cuh"
+
+namespace moe {
+namespace bn {
+template cudaError_t forward_type<float>(const Args &, const Align &, cudaStream_t);
+}  // namespace bn
+}  // namespace moe

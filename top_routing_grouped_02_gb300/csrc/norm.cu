@@ -102,120 +102,8 @@ struct RingCtl {
 };
 constexpr int kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
 
-// A block's partial sums dgamma, dbeta: each group puts its own into its ring (as planes,
-// [2][d rounded up to V]), and the block adds the groups' in order, four columns a
-// thread. (One group after the other through one copy took 3.5 us for 4 groups of d =
-// 4096.)
-template <int V, int NV>
-__device__ __forceinline__ void store_partials(const LnArgs &a, int groups, int group, int tpr,
-                                               int t, const bool (&ok)[NV],
-                                               const f32x2 (&dg)[NV][V / 2],
-                                               const f32x2 (&db)[NV][V / 2], uint8_t *rings,
-                                               size_t ring_bytes, bool gave_up) {
-    float *part = a.part + (int64_t)blockIdx.x * 2 * a.d;
-    const int nvec = (a.d + V - 1) / V;
-    constexpr int H = V / 4;
-    // every thread is done with the last rows
-    const bool lost = __syncthreads_or(gave_up);
-    float4 *mine = reinterpret_cast<float4 *>(rings + group * ring_bytes);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (ok[i])
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const f32x2 *p = m == 0 ? &dg[i][2 * h] : &db[i][2 * h];
-                    float4 q;
-                    unpair(p[0], q.x, q.y);
-                    unpair(p[1], q.z, q.w);
-                    mine[(m * H + h) * nvec + i * tpr + t] = q;
-                }
-    __syncthreads();
-    const int quads = nvec * H;  // of one array
-    for (int c = threadIdx.x; c < 2 * quads; c += blockDim.x) {
-        const int m = c >= quads, e = c - m * quads, v = e / H, h = e % H;
-        if (4 * e >= a.d) continue;  // the last vector may reach past the row
-        const uint8_t *at = rings + (size_t)((m * H + h) * nvec + v) * sizeof(float4);
-        float4 x = *reinterpret_cast<const float4 *>(at);
-        for (int k = 1; k < groups; ++k) {
-            const float4 q = *reinterpret_cast<const float4 *>(at + k * ring_bytes);
-            x.x += q.x;
-            x.y += q.y;
-            x.z += q.z;
-            x.w += q.w;
-        }
-        if (lost) x.x = x.y = x.z = x.w = NAN;
-        float *out = part + (int64_t)m * a.d + 4 * e;
-        if ((a.d & 3) == 0) {
-            *reinterpret_cast<float4 *>(out) = x;
-        } else {
-            const float f[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * e + j < a.d) out[j] = f[j];
-        }
-    }
-}
-
 // ---- SHIFT helpers
 
-// Bytes of the image of a row: its blocks, wherever it starts, and one more that the
-// last vector's shift reads.
-__host__ __device__ constexpr uint32_t image_bytes(int d, int esize) {
-    return ((uint32_t)d * esize + 15) / 16 * 16 + 32;  // (d: of a row that fits the ring)
-}
-// One thread: the blocks of row r of a [T, d] tensor into img, announced on bar
-// (which the caller arrives on, with the bytes returned). Elements in blocks that reach
-// out of the tensor are copied one by one.
-template <typename T>
-__device__ __forceinline__ uint32_t fetch_image(uint8_t *img, const T *base, int64_t ld, int64_t r,
-                                                int64_t rows, int d, uint32_t bar) {
-    const uintptr_t b0 = reinterpret_cast<uintptr_t>(base);
-    const uintptr_t b1 = reinterpret_cast<uintptr_t>(base + (rows - 1) * ld + d);
-    const T *row = base + r * ld;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row), end = reinterpret_cast<uintptr_t>(row + d);
-    const uintptr_t origin = at & ~(uintptr_t)15;
-    uintptr_t lo = origin, hi = (end + 15) & ~(uintptr_t)15;
-    if (lo < b0) lo += 16;
-    if (hi > b1) hi -= 16;
-    uint32_t bytes = 0;
-    if (hi > lo) {
-        bytes = (uint32_t)(hi - lo);
-        ptx::bulk_load(ptx::smem_addr(img + (lo - origin)), reinterpret_cast<const void *>(lo), bytes, bar);
-    } else {
-        lo = hi = end;  // no whole block: every element by itself
-    }
-    T *to = reinterpret_cast<T *>(img + (at - origin));
-    for (const T *p = row; reinterpret_cast<uintptr_t>(p) < lo; ++p) to[p - row] = *p;
-    if (hi < end)
-        for (const T *p = reinterpret_cast<const T *>(hi); p < row + d; ++p) to[p - row] = *p;
-    return bytes;
-}
-// The 16 bytes of vector v of a row whose image starts `shift` bytes into img.
-template <typename T>
-__device__ __forceinline__ uint4 image_vec(const uint8_t *img, int v, uint32_t shift) {
-    const uint4 a = reinterpret_cast<const uint4 *>(img)[v], b = reinterpret_cast<const uint4 *>(img)[v + 1];
-    uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x;
-    if (shift & 8) {
-        w0 = a.z;
-        w1 = a.w;
-        w2 = b.x;
-        w3 = b.y;
-        w4 = b.z;
-    }
-    if (shift & 4) {
-        w0 = w1;
-        w1 = w2;
-        w2 = w3;
-        w3 = w4;
-        w4 = shift & 8 ? b.w : b.y;
-    }
-    if (sizeof(T) == 4) return make_uint4(w0, w1, w2, w3);
-    const uint32_t bits = (shift & 2) * 8;
-    return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits),
-                      __funnelshift_r(w2, w3, bits), __funnelshift_r(w3, w4, bits));
-}
 // v's first n elements (of 16 bytes), zeros after them.
 template <typename T>
 __device__ __forceinline__ uint4 first_elems(uint4 v, int n) {
@@ -605,7 +493,7 @@ __global__ void __launch_bounds__(kBwdRingThreads, 1) ln_backward_ring_kernel(co
     }
     if (SHIFT && t == 0) ptx::bulk_wait_group<0>();
     if (a.part == nullptr) return;
-    store_partials<V, NV>(a, groups, group, tpr, t, ok, dg, db, rings, S * stage_bytes + SHIFT * row_bytes,
+    store_partials<V, NV>(a.part, a.d, groups, group, tpr, t, ok, dg, db, rings, S * stage_bytes + SHIFT * row_bytes,
                           !alive);
 }
 

@@ -776,9 +776,9 @@ def moe_block_norm(x, b, post=None, pre=None, gate=None, scale: float = 1.0, eps
     post_norm, post scales b itself). gate: like x, or one fp32 value a row, or None (no gate);
     post, pre [d] of x's type or fp32, or None. stats=True: (y, u, rstd_post, rstd_pre), the
     fp32 row statistics that the backward takes. y may be x."""
-    out = _native().block_norm(x, _block(b), post, pre, gate, scale, eps, post_norm, pre_norm, stats,
-                               y, u, stream)
-    return out if stats else out[:2]
+    if b is None:
+        raise TypeError("b must be a tensor (moe_rmsnorm is the norm alone)")
+    return _native().block_norm(x, b, post, pre, gate, scale, eps, post_norm, pre_norm, stats, y, u, stream)
 
 
 def moe_block_norm_backward(dy, du, x, b, post, pre, rstd_post, rstd_pre, gate=None,
@@ -790,22 +790,17 @@ def moe_block_norm_backward(dy, du, x, b, post, pre, rstd_post, rstd_pre, gate=N
     weights' type, or wdtype (default fp32) without weights."""
     if post is None and pre is None and wdtype not in (None, torch.float32, x.dtype):
         raise TypeError(f"weight gradients are {x.dtype} or fp32, got {wdtype}")
-    return _native().block_norm_backward(dy, du, x, _block(b), post, pre, rstd_post, rstd_pre, gate,
-                                         scale, wdtype is not x.dtype, dx, db, scratch, stream)
-
-
-def _block(b):
     if b is None:
-        raise TypeError("b must be a tensor (moe_rmsnorm is the norm alone)")
-    return b
+        raise TypeError("b must be a tensor (moe_rmsnorm_backward is the norm alone)")
+    return _native().block_norm_backward(dy, du, x, b, post, pre, rstd_post, rstd_pre, gate,
+                                         scale, wdtype is not x.dtype, dx, db, scratch, stream)
 
 
 def moe_rmsnorm(x, gamma=None, eps: float = 1e-6, stats: bool = False, y=None, stream=None):
     """y = gamma x / sqrt(mean(x^2) + eps) along the last dimension (gamma: [d] of x's type or
     fp32, or None); stats=True: (y, rstd), the fp32 row statistics that the backward takes."""
-    _, out, _, rstd = _native().block_norm(x, None, None, gamma, None, 1.0, eps, False, True, stats, None,
-                                           y, stream)
-    return (out, rstd) if stats else out
+    out = _native().block_norm(x, None, None, gamma, None, 1.0, eps, False, True, stats, None, y, stream)
+    return (out[1], out[3]) if stats else out[1]
 
 
 def moe_rmsnorm_backward(dy, x, gamma, rstd, dres=None, wdtype=None, dx=None, scratch=None,
