@@ -163,7 +163,7 @@ LinearWs linear_ws(int T, int k, int n, bool train) {
     w.da = align256(kFfnControlBytes);
     w.sums = w.da + (train ? align256((size_t)T * n * 2) : 0);
     w.part = w.sums + (train ? align256(linear_sums_floats(T, n) * sizeof(float)) : 0);
-    const bool tiled = train || !linear_streams(T, k, n);
+    const bool tiled = train || !linear_streams(T, n);
     w.total = w.part + (tiled ? align256(ffn_dense_part_bytes()) : 0);
     // a workspace for T tokens serves fewer, whichever kernel they take
     const int few = std::min(T, kFfnStreamTokens);
@@ -304,7 +304,7 @@ static moe_status_t linear_forward(const void *X, const void *W, const void *bia
     uint32_t *ticket = reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset));
     uint32_t *err = static_cast<uint32_t *>(ws);
     cudaStream_t s = as_stream(stream);
-    if (F == nullptr && linear_streams(T, k, n))
+    if (F == nullptr && linear_streams(T, n))
         return from_cuda(launch_linear_stream(c, static_cast<float *>(part), ticket, err, s));
     return from_cuda(launch_linear_tiled(c, F, static_cast<float4 *>(part), ticket, err, s));
 }

@@ -472,9 +472,12 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     x3[i] = __ldg(p3 + i * 32);
                 }
             };
-            // kLinear: this row's residual of a chunk, likewise
-            [[maybe_unused]] uint4 rr[4] = {};
-            auto load_residual = [&](int c) {
+            // kLinear: this row's residual of a chunk, loaded a chunk ahead, and the bias of four of
+            // the warp's columns, which a shuffle hands out (777 x 1000 x 2728: loads where they
+            // are used cost 1.7 and 3.7 of 18.2 us)
+            [[maybe_unused]] uint4 rr[4] = {}, ahead[4] = {};
+            [[maybe_unused]] f32x2 bias4[2] = {0, 0};
+            auto load_residual = [&](int c, uint4 (&rr)[4]) {
                 if (args.res == nullptr || c >= hi || y0 + lane >= rows) return;
                 const int x0 = un.nb * kCols + c * 32;
                 const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(args.res) +
@@ -484,7 +487,11 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     if (x0 + 8 * i < cols) rr[i] = p[i];
             };
             if constexpr (MODE == kDHid) load_factors(lo);
-            if constexpr (MODE == kLinear) load_residual(lo);
+            if constexpr (MODE == kLinear) {
+                const int x = un.nb * kCols + c_lo * 32 + lane * 4;
+                if (args.bias != nullptr && x < cols) bias_pairs(x, bias4);
+                load_residual(lo, rr);
+            }
             if (!ready()) return false;
             if (lo >= hi) release();
             // m: W1's sums or (kGate) W3's
@@ -549,19 +556,15 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     store_box(o3, x0, y0, &maps.o[1]);
                 } else if constexpr (MODE == kLinear) {
                     uint32_t v[32], o[16];
+                    load_residual(c + 1, ahead);
                     load(c, 0, v);
                     if (c == hi - 1) release();
                     if (args.bias != nullptr) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (x0 + 8 * i < cols)
-#pragma unroll
-                                for (int j = 0; j < 8; j += 4) {
-                                    f32x2 b[2];
-                                    bias_pairs(x0 + 8 * i + j, b);
-                                    put_pair(add2(word_pair(v + 8 * i + j), b[0]), v + 8 * i + j);
-                                    put_pair(add2(word_pair(v + 8 * i + j + 2), b[1]), v + 8 * i + j + 2);
-                                }
+                        for (int i = 0; i < 16; ++i) {
+                            const f32x2 b = __shfl_sync(0xffffffffu, bias4[i & 1], (c - c_lo) * 8 + (i >> 1));
+                            put_pair(add2(word_pair(v + 2 * i), b), v + 2 * i);
+                        }
                     }
                     auto chunk = [&](auto act, auto saves) {
 #pragma unroll
@@ -581,7 +584,8 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         }
                     };
                     with_act(chunk);
-                    load_residual(c + 1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rr[i] = ahead[i];
                     store_box(o, x0, y0, &maps.o[0]);
                     if (args.f1 != nullptr) {
                         float4 *p = saved_block(args.f1, cols, y0, x0, lane);
@@ -616,6 +620,14 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                     return saved_block(f, cols, y, x, lane) + (x & 31) / 4 * 32;
                 };
                 [[maybe_unused]] float4 f1, f3;
+                [[maybe_unused]] f32x2 bias[2] = {0, 0};
+                [[maybe_unused]] uint2 res = {0, 0};
+                if constexpr (MODE == kLinear) {
+                    if (args.bias != nullptr) bias_pairs(x, bias);
+                    if (args.res != nullptr && y + lane < rows)
+                        res = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(args.res) +
+                                                               (int64_t)(y + lane) * cols + x);
+                }
                 if constexpr (MODE == kDHid) {
                     f1 = __ldg(saved(args.f1));
                     f3 = __ldg(saved(args.f3));
@@ -678,22 +690,15 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                         store(0, mul2(a, pair2(&f1.x)), mul2(b, pair2(&f1.z)));
                         store(1, mul2(a, pair2(&f3.x)), mul2(b, pair2(&f3.z)));
                     } else if constexpr (MODE == kLinear) {
-                        f32x2 bias[2] = {0, 0}, r[2] = {0, 0};
-                        if (args.bias != nullptr) bias_pairs(x, bias);
-                        if (args.res != nullptr) {
-                            const uint2 q = *reinterpret_cast<const uint2 *>(
-                                static_cast<const uint16_t *>(args.res) + (int64_t)(y + lane) * cols + x);
-                            float e[4];
-                            if (f16) {
-                                unpack2<__half>(q.x, e[0], e[1]);
-                                unpack2<__half>(q.y, e[2], e[3]);
-                            } else {
-                                unpack2<__nv_bfloat16>(q.x, e[0], e[1]);
-                                unpack2<__nv_bfloat16>(q.y, e[2], e[3]);
-                            }
-                            r[0] = pair2(e);
-                            r[1] = pair2(e + 2);
+                        float e[4];  // (no residual: zeros)
+                        if (f16) {
+                            unpack2<__half>(res.x, e[0], e[1]);
+                            unpack2<__half>(res.y, e[2], e[3]);
+                        } else {
+                            unpack2<__nv_bfloat16>(res.x, e[0], e[1]);
+                            unpack2<__nv_bfloat16>(res.y, e[2], e[3]);
                         }
+                        const f32x2 r[2] = {pair2(e), pair2(e + 2)};
                         with_act([&](auto act, auto saves) {
                             f32x2 f[2], df[2];
                             activate_one<act(), saves()>(add2(a, bias[0]), f[0], df[0]);
