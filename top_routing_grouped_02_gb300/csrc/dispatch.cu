@@ -12,7 +12,7 @@
 // warps write the same element, and every sum has a fixed order: no atomics.
 //
 // A warp takes a token's elements in chunks of 32 x U vectors, with the loads of all K rows
-// in flight at once (U K = 8 vectors a lane). Short batches spread a token's chunks over
+// in flight at once. Short batches spread a token's chunks over
 // more warps; the gradient, whose dot products run along the row, over the 8 warps of one
 // block, which join their sums through shared memory.
 // Vectors are as wide as the alignment of all operands' rows allows; the elements behind
@@ -58,6 +58,20 @@ __device__ __forceinline__ Raw<T, V> *row_out(void *p, int64_t ld, int64_t t) {
     return reinterpret_cast<Raw<T, V> *>(static_cast<T *>(p) + t * ld);
 }
 
+// Vectors of a row in flight a lane: 8 of 16 or 8 bytes over all rows, more of narrower ones,
+// four times as many with eight rows and twice with fewer (bf16 rows of 7167, K = 8, without
+// and with: sum 177 / 119 us, gradient 416 / 281; rows of 4097, K = 2, twice and four times: sum
+// 24.4 / 26.2, gradient 38.5 / 43.0; the dispatch, whose loads are one row's, four times with 2
+// to 8 rows: 148 / 112, and twice with one).
+template <typename T, int V, int KU>
+constexpr int flight() {
+    return 8 / KU * (V * (int)sizeof(T) >= 8 ? 1 : KU == 8 ? 4 : 2);
+}
+template <typename T, int V, int KU>
+constexpr int dispatch_flight() {
+    return (KU == 1 ? 8 : 4) * std::min<int>(KU == 1 ? 2 : 4, 16 / (V * (int)sizeof(T)));
+}
+
 // This warp's token and its part of the token's chunks.
 struct Share {
     int64_t t;
@@ -72,7 +86,7 @@ struct Share {
 
 template <typename T, int V, int KU>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowArgs a) {
-    constexpr int U = KU == 1 ? 8 : 4;
+    constexpr int U = dispatch_flight<T, V, KU>();
     pdl_wait();
     pdl_trigger();
     const Share s(a);
@@ -106,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowArgs a) {
 
 template <typename T, int V, int KU>
 __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const RowArgs a) {
-    constexpr int U = 8 / KU;
+    constexpr int U = flight<T, V, KU>();
     pdl_wait();
     pdl_trigger();
     const Share s(a);
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const RowArgs a) {
 // (a.split divides the block's warps: a token's warps are of one block)
 template <typename T, int V, int KU>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowArgs a) {
-    constexpr int U = 8 / KU;
+    constexpr int U = flight<T, V, KU>();
     __shared__ float part[kWarps][KU];
     pdl_wait();
     pdl_trigger();
@@ -255,7 +269,7 @@ enum class Op { kDispatch, kSum, kBackward };
 
 template <Op OP, typename T, int V, int KU>
 cudaError_t launch_one(RowArgs a, cudaStream_t s) {
-    constexpr int U = OP == Op::kDispatch ? (KU == 1 ? 8 : 4) : 8 / KU;
+    constexpr int U = OP == Op::kDispatch ? dispatch_flight<T, V, KU>() : flight<T, V, KU>();
     // warps a token: enough of them to fill the device
     const int chunks = std::max(1, (a.d / V + 32 * U - 1) / (32 * U));
     const int64_t want = ((int64_t)sm_count() * kTargetWarps + a.T - 1) / a.T;
