@@ -638,7 +638,8 @@ moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, c
  * scales the channels of b). gate: MOE_GATE_ROW one fp32 value a row; MOE_GATE_FULL [T,d] of
  * `type`. Arithmetic and statistics in fp32; y and u are rounded once each, u from the fp32 y.
  * rstd_post, rstd_pre [T] fp32 or NULL: 1 / sqrt(mean + eps), which the backward takes.
- * T >= 0 (0: nothing is enqueued), 1 <= d <= 16384, eps >= 0. y and u may each be one of x, b
+ * T >= 0 (0: nothing is enqueued), 1 <= d <= 16384, eps >= 0 (0: a row of zeros gives NaN;
+ * squares past the range of fp32, of elements beyond 1e19, give zeros). y and u may each be one of x, b
  * and the full gate (same stride). One kernel. Rows come through waits bounded as layer norm's. */
 enum { MOE_NORM_POST = 1, MOE_NORM_PRE = 2 };
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_ROW = 1, MOE_GATE_FULL = 2 } moe_gate_t;
@@ -675,8 +676,8 @@ moe_status_t moe_block_norm_backward(const void *dy, int64_t lddy, const void *d
  * own GEMMs gather their rows and apply the weights themselves). row_of_slot [T*K] int32 as
  * moe_permute writes it: the sorted row of slot t*K+k, distinct for distinct slots; a value
  * outside [0, rows) is a slot without a row. Matrices of `type` with row strides in elements
- * (any alignment of a whole element); 1 <= K <= 8, T*K < 2^31, T >= 0 (0: nothing is
- * enqueued). Sums in fp32, k ascending, one rounding; no atomics. One kernel each.
+ * (any alignment of a whole element); 1 <= d <= 2^28, 1 <= K <= 8, T*K < 2^31, T >= 0 (0:
+ * nothing is enqueued). Sums in fp32, k ascending, one rounding; no atomics. One kernel each.
  *
  * Dispatch: xg[row_of_slot[t*K+k],:] = x[t,:]. x [T,d], xg [rows,d]; rows of xg that no slot
  * names are left as they were. */
@@ -707,10 +708,10 @@ moe_status_t moe_combine_weighted_backward(const void *dy, int64_t lddy, const v
  * the context stays usable. ws: any workspace of >= 64 bytes. */
 moe_status_t moe_selftest_wait_timeout(void *ws, size_t ws_bytes, void *stream);
 
-/* The same for layer norm: the copies of row `row` in this thread's next layer norm call
- * (forward or backward, of rows that its ring holds) are never issued, so the wait for them
+/* The same for the norms: the copies of row `row` in this thread's next layer norm or block
+ * norm call (forward or backward, of rows that its ring holds) are never issued, so the wait for them
  * runs out after about 1 s. The call ends after 2 s with NaN in that row and in later rows of
- * the same warps (backward: in dgamma and dbeta too); all other rows are as ever. row < 0:
+ * the same warps (backward: in the weights' gradients too); all other rows are as ever. row < 0:
  * takes it back. */
 moe_status_t moe_selftest_layernorm_withhold(int64_t row);
 

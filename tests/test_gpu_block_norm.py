@@ -203,6 +203,20 @@ def test_writes_nothing_else():
         assert (v == 7.0).all()
 
 
+@pytest.mark.parametrize("T,d,ld", [(1, 7, 7), (3, 1001, 1001), (9, 130, 131), (17, 64, 64), (40, 7, 9), (500, 33, 33)])
+def test_scratch_of_the_stated_size(T, d, ld):
+    """The partial weight sums stay inside moe_block_norm_scratch_bytes."""
+    gen = torch.Generator().manual_seed(T)
+    x, b, dy, du = (matrix(T, d, BF, gen, ld) for _ in range(4))
+    _, _, rp, rq = moe.moe_block_norm(x, b, stats=True)
+    want = moe.moe_block_norm_backward(dy, du, x, b, None, None, rp, rq)
+    nbytes = int(moe.lib().moe_block_norm_scratch_bytes(T, d))
+    buf = torch.full((nbytes + (1 << 20),), 113, dtype=torch.uint8, device="cuda")
+    got = moe.moe_block_norm_backward(dy, du, x, b, None, None, rp, rq, scratch=buf[:nbytes])
+    assert (buf[nbytes:] == 113).all()
+    assert all(p is q is None or torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_not_a_number_stays_in_its_row():
     T, d = 40, 512
     gen = torch.Generator().manual_seed(2)

@@ -65,7 +65,8 @@ moe_status_t check_slots(const int32_t *row_of_slot, int64_t T, int K, int d, in
     if (st != MOE_OK) return st;
     if (K < 1 || rows < 0 || !aligned(row_of_slot, 4) || (row_of_slot == nullptr && T > 0))
         return MOE_ERR_INVALID_ARG;
-    if (K > kMaxK || T > INT32_MAX / K) return MOE_ERR_UNSUPPORTED_SHAPE;
+    // (columns are counted in 32 bits, a step past the last one too)
+    if (K > kMaxK || T > INT32_MAX / K || d > kMaxRowWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
 // A matrix of sorted rows; there may be none of them.
@@ -360,7 +361,10 @@ moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, c
     return from_cuda(e);
 }
 
-size_t moe_block_norm_scratch_bytes(int64_t T, int d) { return moe_layernorm_scratch_bytes(T, d); }
+size_t moe_block_norm_scratch_bytes(int64_t T, int d) {
+    if (T < 0 || d < 1) return 0;
+    return align256((size_t)block_norm_partials(T) * 2 * (size_t)d * sizeof(float));
+}
 
 moe_status_t moe_block_norm_forward(const void *x, int64_t ldx, const void *b, int64_t ldb,
                                     const void *gate, int64_t ldgate, moe_gate_t gate_kind,

@@ -36,6 +36,10 @@ RowShape row_shape(Args &a, int per_thread) {
 
 using namespace bn;
 
+int block_norm_partials(int64_t T) {
+    return (int)std::min<int64_t>((T + kPhases - 1) / kPhases * kPhases, kLnPartials);
+}
+
 cudaError_t launch_block_norm_forward(const BlockNormCall &c, int64_t withheld, cudaStream_t s) {
     Args a{};
     Align al;

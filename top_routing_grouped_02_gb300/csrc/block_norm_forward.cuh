@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(1024) forward_rows_kernel(const Args a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) s = fmaf(y[i][j], y[i][j], s);
         }
-        if (t == 0 && a.r_post != nullptr) a.r_post[row] = r_post;
+        if (t == 0 && a.post_norm && a.r_post != nullptr) a.r_post[row] = r_post;
         if (!a.pre_norm) continue;
         const float r_pre = __frsqrt_rn(sum(s) * inv_d + a.eps);
         if (t == 0 && a.r_pre != nullptr) a.r_pre[row] = r_pre;

@@ -311,17 +311,21 @@ struct BlockNormCall {
     moe_dtype_t type;
     bool w32, gate_rows, post_norm, pre_norm;
     float scale, eps;
-    // backward (r_post and r_pre are inputs then); part: ln_partials(T) * 2 * d floats
+    // backward (r_post and r_pre are inputs then); part: block_norm_partials(T) * 2 * d floats
     Matrix dy, du, dx, db, dgate;
     void *dpost, *dpre;
     float *part;
 };
+// Rows of partial weight sums: one of each block, and blocks come by eights where rows start
+// anywhere.
+int block_norm_partials(int64_t T);
 cudaError_t launch_block_norm_forward(const BlockNormCall &c, int64_t withheld, cudaStream_t s);
 cudaError_t launch_block_norm_backward(const BlockNormCall &c, int64_t withheld, cudaStream_t s);
 // first, second [d] of wtype (each may be NULL) = the sums of P rows of part [P][2][d].
 cudaError_t launch_weight_reduce(const float *part, int P, int d, moe_dtype_t wtype, void *first,
                                  void *second, cudaStream_t s);
 
+constexpr int kMaxRowWidth = 1 << 28;
 // Token rows and rows sorted by expert (dispatch.cu). x: by token (the dispatch's input, the
 // combine's gradient); z: by sorted row; out: by sorted row, or (x NULL) by token; res, w may
 // be NULL.

@@ -505,7 +505,7 @@ def moe_selftest_wait_timeout(ws, stream=None):
 
 
 def moe_selftest_layernorm_withhold(row: int):
-    """This thread's next layer norm call never gets row `row` (a wait of ~1 s runs out)."""
+    """This thread's next layer or block norm call never gets row `row` (a wait of ~1 s runs out)."""
     _check("moe_selftest_layernorm_withhold", lib().moe_selftest_layernorm_withhold(row))
 
 
