@@ -78,6 +78,9 @@ def test_forward_and_backward(case):
     assert all(p is q is None or torch.equal(p, q) for p, q in zip((dX, dW, db), again))
     one = moe.moe_linear_backward(m["dY"], m["x"], m["W"], f, need_dw=False, ws=ws)
     assert torch.equal(one[0], dX) and one[1] is None and one[2] is None
+    if bt is not None:  # the bias' gradient alone takes a kernel of its own
+        check(moe.moe_linear_backward(m["dY"], m["x"], m["W"], f, bias_dtype=bt, need_dx=False, need_dw=False, ws=ws)[2],
+              ref["dbias"], "dbias alone")
     one = moe.moe_linear_backward(m["dY"], m["x"], m["W"], f, need_dx=False, ws=ws)
     assert one[0] is None and torch.equal(one[1], dW)
     # onto the residual, with a workspace of more tokens

@@ -163,7 +163,7 @@ LinearWs linear_ws(int T, int k, int n, bool train) {
     LinearWs w;
     w.da = align256(kFfnControlBytes);
     w.sums = w.da + (train ? align256((size_t)T * n * 2) : 0);
-    w.part = w.sums + (train ? align256(linear_sums_floats(T, n) * sizeof(float)) : 0);
+    w.part = w.sums + (train ? align256((size_t)linear_sum_rows(T, n) * n * sizeof(float)) : 0);
     const bool tiled = train || !linear_streams(T, n);
     w.total = w.part + (tiled ? align256(ffn_dense_part_bytes()) : 0);
     // a workspace for T tokens serves fewer, whichever kernel they take
@@ -352,10 +352,14 @@ moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, c
     const bool products = dX != nullptr || dW != nullptr;
     void *dA = F != nullptr ? at(ws, w.da) : const_cast<void *>(dY);
     if (!products && dbias == nullptr) return MOE_OK;
-    cudaError_t e = launch_linear_grad(dY, F, T, n, f16, dA, dbias, btype == MOE_DTYPE_F32,
-                                       reinterpret_cast<float *>(at(ws, w.sums)), s);
+    float *sums = dbias != nullptr ? reinterpret_cast<float *>(at(ws, w.sums)) : nullptr;
+    const bool b32 = btype == MOE_DTYPE_F32;
+    cudaError_t e = launch_linear_grad(dY, F, T, n, f16, dA, sums, s);
+    if (e == cudaSuccess && dbias != nullptr && dW == nullptr)
+        e = launch_linear_bias(sums, T, n, f16, dbias, b32, s);
     if (e == cudaSuccess)
-        e = launch_linear_products(dA, X, W, T, k, n, f16, dX, dW, reinterpret_cast<float4 *>(at(ws, w.part)),
+        e = launch_linear_products(dA, X, W, T, k, n, f16, dX, dW, dbias, b32, sums,
+                                   reinterpret_cast<float4 *>(at(ws, w.part)),
                                    reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),
                                    static_cast<uint32_t *>(ws), s);
     return from_cuda(e);

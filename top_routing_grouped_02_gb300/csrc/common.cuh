@@ -285,15 +285,19 @@ cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *tic
 // F: act'(X W + bias) in blocks of 32 x 32 (moe_ffn_forward_train), or NULL.
 cudaError_t launch_linear_tiled(const LinearCall &c, float *F, float4 *part, uint32_t *ticket, uint32_t *err,
                                 cudaStream_t s);
-// dX = dA W^T, dW = X^T dA; either may be NULL.
+// dX = dA W^T, dW = X^T dA; either may be NULL. With dW, dbias may be given: the sums of
+// launch_linear_grad's rows, beside the products.
 cudaError_t launch_linear_products(const void *dA, const void *X, const void *W, int T, int k, int n, bool f16,
-                                   void *dX, void *dW, float4 *part, uint32_t *ticket, uint32_t *err,
-                                   cudaStream_t s);
-// dA = dY F (F NULL: dY itself, nothing is written) and, with dbias, its column sums (fp32, then
-// of the 16-bit type or fp32) by way of sums: linear_sums_floats(T, n) floats.
-size_t linear_sums_floats(int T, int n);
-cudaError_t launch_linear_grad(const void *dY, const float *F, int T, int n, bool f16, void *dA, void *dbias,
-                               bool bias32, float *sums, cudaStream_t s);
+                                   void *dX, void *dW, void *dbias, bool bias32, const float *sums,
+                                   float4 *part, uint32_t *ticket, uint32_t *err, cudaStream_t s);
+// dA = dY F (F NULL: dY itself, nothing is written) and, unless sums is NULL, the column sums of
+// dY F over runs of rows: sums [linear_sum_rows(T, n)][n]. And the sums of those rows alone, of the
+// 16-bit type or fp32.
+int linear_sum_rows(int T, int n);
+cudaError_t launch_linear_grad(const void *dY, const float *F, int T, int n, bool f16, void *dA, float *sums,
+                               cudaStream_t s);
+cudaError_t launch_linear_bias(const float *sums, int T, int n, bool f16, void *dbias, bool bias32,
+                               cudaStream_t s);
 
 // The norms around a block (block_norm.cu, block_norm_backward.cu); w32: post, pre and their
 // gradients are fp32. gate_rows: gate and dgate are [T,d] of `type`, else fp32, one a row.

@@ -134,6 +134,11 @@ struct Args {
     const void *bias;    // kLinear: [cols] of 16 bits or (bias32) fp32, or NULL
     int bias32;
     const void *res;     // kLinear: [rows, cols] of 16 bits, or NULL; out[0] may be it
+    // kWGrad of a projection: its bias' gradient [sum_n] (of 16 bits or (bias32) fp32, or NULL),
+    // the sums of sum_rows rows of sums [.][sum_n]
+    void *dbias;
+    const float *sums;
+    int sum_rows, sum_n;
     float *f1, *f3;      // the factors in blocks (saved_block): kGate stores them, or
                          // NULL; kDHid reads them; kLinear stores F in f1, or NULL
     float4 *part;        // [segment][CTA][warp][kPartVecs]
@@ -350,6 +355,17 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         }
         ptx::tc_commit_pair(ptx::smem_addr(&ctl->drain), 0x1);
         bounded_wait(ptx::smem_addr(&ctl->drain), 0, args.err);
+    } else if (MODE == kWGrad && warp == 3) {
+        // the bias' gradient beside the products: a launch of its own took 2 us of a short
+        // training step's 55
+        if (args.dbias != nullptr)
+            for (int c = blockIdx.x * 32 + lane; c < args.sum_n; c += gridDim.x * 32) {
+                float v = 0.f;
+#pragma unroll 8
+                for (int p = 0; p < args.sum_rows; ++p) v += __ldg(args.sums + (int64_t)p * args.sum_n + c);
+                if (args.bias32) static_cast<float *>(args.dbias)[c] = v;
+                else static_cast<uint16_t *>(args.dbias)[c] = round16(v, args.f16 != 0);
+            }
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
         const int ew = warp - 4, q = warp & 3, share = ew >> 2;
@@ -929,8 +945,8 @@ cudaError_t launch_linear_tiled(const LinearCall &c, float *F, float4 *part, uin
 }
 
 cudaError_t launch_linear_products(const void *dA, const void *X, const void *W, int T, int k, int n, bool f16,
-                                   void *dX, void *dW, float4 *part, uint32_t *ticket, uint32_t *err,
-                                   cudaStream_t s) {
+                                   void *dX, void *dW, void *dbias, bool bias32, const float *sums,
+                                   float4 *part, uint32_t *ticket, uint32_t *err, cudaStream_t s) {
     Maps m{};
     Args a{};
     a.f16 = f16;
@@ -957,6 +973,11 @@ cudaError_t launch_linear_products(const void *dA, const void *X, const void *W,
         m.b[i] = m.b[0];
         m.o[i] = m.o[0];
     }
+    a.dbias = dbias;
+    a.bias32 = bias32;
+    a.sums = sums;
+    a.sum_rows = linear_sum_rows(T, n);
+    a.sum_n = n;
     a.rows[0] = k;
     a.cols[0] = n;
     a.kb = (T + BK - 1) / BK;

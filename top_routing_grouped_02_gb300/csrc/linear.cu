@@ -8,7 +8,8 @@
 // rows x 4 groups of 8 columns: its loads of F are 128 consecutive bytes for each group, those
 // of dY 64 for each row, and the neighbouring warps take the rest of the rows' lines. Each
 // thread sums its columns over its rows, the 8 lanes of a column are added by shuffles and the
-// blocks' partial rows in order by a second kernel: the result does not depend on timing.
+// blocks' partial rows in order by the weight gradient's launch or (without it) a kernel of their
+// own: the result does not depend on timing.
 #include <algorithm>
 
 #include "common.cuh"
@@ -20,13 +21,7 @@ namespace {
 constexpr int kWarps = 8, kCols = 32 * kWarps;  // of a block
 constexpr int kRows = 32;                       // at a time: four of each lane's in flight
 
-// Blocks over the rows: as many as make eight for each SM of the device (a constant: a
-// workspace's size does not depend on the device at hand).
 constexpr int kBlocks = 8 * 152;
-int row_blocks(int T, int n) {
-    const int64_t across = (n + kCols - 1) / kCols, most = ((int64_t)T + kRows - 1) / kRows;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(most, kBlocks / across));
-}
 
 template <typename T, bool FACTOR>
 __global__ void __launch_bounds__(32 * kWarps)
@@ -84,9 +79,8 @@ linear_grad_kernel(const T *dY, const float *F, int rows, int n, T *dA, float *s
 }
 
 template <typename T>
-cudaError_t launch_grad(const void *dY, const float *F, int rows, int n, void *dA, float *sums, int blocks,
-                        cudaStream_t s) {
-    const dim3 grid((n + kCols - 1) / kCols, blocks), block(32 * kWarps);
+cudaError_t launch_grad(const void *dY, const float *F, int rows, int n, void *dA, float *sums, cudaStream_t s) {
+    const dim3 grid((n + kCols - 1) / kCols, linear_sum_rows(rows, n)), block(32 * kWarps);
     const T *y = static_cast<const T *>(dY);
     return F != nullptr ? launch_k(linear_grad_kernel<T, true>, grid, block, 0, s, y, F, rows, n,
                                    static_cast<T *>(dA), sums)
@@ -96,19 +90,23 @@ cudaError_t launch_grad(const void *dY, const float *F, int rows, int n, void *d
 
 }  // namespace
 
-size_t linear_sums_floats(int T, int n) { return (size_t)row_blocks(T, n) * n; }
+// Blocks over the rows: as many as make eight for each SM of the device (a constant: a
+// workspace's size does not depend on the device at hand).
+int linear_sum_rows(int T, int n) {
+    const int64_t across = (n + kCols - 1) / kCols, most = ((int64_t)T + kRows - 1) / kRows;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, kBlocks / across));
+}
 
-cudaError_t launch_linear_grad(const void *dY, const float *F, int T, int n, bool f16, void *dA, void *dbias,
-                               bool bias32, float *sums, cudaStream_t s) {
-    if (F == nullptr && dbias == nullptr) return cudaSuccess;
-    const int blocks = row_blocks(T, n);
-    float *part = dbias != nullptr ? sums : nullptr;
-    const cudaError_t e = f16 ? launch_grad<__half>(dY, F, T, n, dA, part, blocks, s)
-                              : launch_grad<__nv_bfloat16>(dY, F, T, n, dA, part, blocks, s);
-    if (e != cudaSuccess || dbias == nullptr) return e;
-    // (n is even: the row of sums is two halves, as the reduction takes them)
+cudaError_t launch_linear_grad(const void *dY, const float *F, int T, int n, bool f16, void *dA, float *sums,
+                               cudaStream_t s) {
+    if (F == nullptr && sums == nullptr) return cudaSuccess;
+    return f16 ? launch_grad<__half>(dY, F, T, n, dA, sums, s) : launch_grad<__nv_bfloat16>(dY, F, T, n, dA, sums, s);
+}
+
+cudaError_t launch_linear_bias(const float *sums, int T, int n, bool f16, void *dbias, bool bias32, cudaStream_t s) {
+    // (n is even: a row of sums is two halves, as the reduction takes them)
     const moe_dtype_t wt = bias32 ? MOE_DTYPE_F32 : f16 ? MOE_DTYPE_F16 : MOE_DTYPE_BF16;
-    return launch_weight_reduce(sums, blocks, n / 2, wt, dbias,
+    return launch_weight_reduce(sums, linear_sum_rows(T, n), n / 2, wt, dbias,
                                 static_cast<char *>(dbias) + (size_t)(n / 2) * (bias32 ? 4 : 2), s);
 }
 

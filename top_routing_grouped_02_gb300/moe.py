@@ -33,7 +33,7 @@ LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_g
             "moe_gemm_down": 1, "moe_combine": 1, "moe_round_routing": 3, "moe_combine_rows": 1,
             "moe_layernorm": 1, "moe_layernorm_backward": 2, "moe_dropout": 1,
             "moe_dropout_backward": 1, "moe_ffn": 2, "moe_ffn_train": 2, "moe_ffn_backward": 3,
-            "moe_linear": 1, "moe_linear_train": 1, "moe_linear_backward": 4,
+            "moe_linear": 1, "moe_linear_train": 1, "moe_linear_backward": 3,
             "moe_block_norm": 1, "moe_block_norm_backward": 2, "moe_rmsnorm": 1,
             "moe_rmsnorm_backward": 2, "moe_dispatch": 1, "moe_combine_weighted": 1, "moe_combine_weighted_backward": 1}
 TILE_M = 128
