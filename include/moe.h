@@ -620,8 +620,9 @@ moe_status_t moe_linear_forward_train(const void *X, const void *W, const void *
  *   dX = dA W^T, dW = X^T dA, dbias = the sums over rows of dY F (before that rounding)
  * dX, dW of `type`, dbias of btype, each rounded once after an fp32 sum and each may be NULL
  * (the residual's gradient is dY). T = 0 gives a zero dW and dbias. ws: a workspace for
- * training. Three kernels, dA, dX and dW with
- * dbias (fewer where there is less to do; one more for dbias without dW). Deterministic. */
+ * training. Three kernels: dA, dX, dW with dbias
+ * (dX and dW in one where both are small; fewer where there is less to do; one more for dbias
+ * without dW). Deterministic, but dX may differ in its last bit with and without dW. */
 moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, const float *F, int T,
                                  int k, int n, moe_dtype_t type, moe_dtype_t btype, void *dX,
                                  void *dW, void *dbias, void *ws, size_t ws_bytes, void *stream);

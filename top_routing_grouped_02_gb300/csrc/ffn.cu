@@ -87,8 +87,9 @@ namespace {
 // F3. kDX: dX, one reduction over dA1 W1^T then dA3 W3^T (K-major weights).
 // kWGrad: dW1, dW3, dW2 in one launch, both operands MN-major, reduction over T.
 // kLinear: a projection, Y = act(X W + bias) + residual, and (training) F = act'(X W + bias);
-// its gradients are products of the modes kDX, with no second half, and kWGrad, with one problem.
-enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4, kLinear = 5 };
+// its gradients are products of the modes kDX, with no second half, and kWGrad, with one problem,
+// or both in one launch (kBoth: problem 0 is dX, problem 1 is dW) where both are small.
+enum Mode : int { kGate = 0, kDown = 1, kDHid = 2, kDX = 3, kWGrad = 4, kLinear = 5, kBoth = 6 };
 
 constexpr int BM = 128;  // rows per CTA
 constexpr int BK = 64;   // reduction depth per stage: 128 bytes of 16-bit elements
@@ -128,13 +129,14 @@ struct Args {
     int mt[3], nb[3];    // row-tile pairs, column blocks
     int rows[3], cols[3];// of the outputs
     int kb, kb_half;     // k-blocks; kDX: those of its first half
-    uint32_t idesc;
+    int kb_dw;           // kBoth: those of problem 1
+    uint32_t idesc, idesc_dw;
     int f16, act;
     void *out[3];        // the outputs of each problem (kDHid: both of its one)
     const void *bias;    // kLinear: [cols] of 16 bits or (bias32) fp32, or NULL
     int bias32;
     const void *res;     // kLinear: [rows, cols] of 16 bits, or NULL; out[0] may be it
-    // kWGrad of a projection: its bias' gradient [sum_n] (of 16 bits or (bias32) fp32, or NULL),
+    // kWGrad and kBoth of a projection: its bias' gradient [sum_n] (of 16 bits or (bias32) fp32, or NULL),
     // the sums of sum_rows rows of sums [.][sum_n]
     void *dbias;
     const float *sums;
@@ -189,10 +191,11 @@ static_assert(sizeof(Ctl) <= 256, "control block");
 // segment), then whole tiles.
 struct Work {
     int pairs, units, kb, next;
+    int dw, kb_dw;    // kBoth: problem 1's first tile, its k-blocks
     int u, kb0, kb1;  // current: tile, its k-blocks
     bool cut;         // a segment
     __device__ __forceinline__ Work(const Args &a, int pair, int pairs_)
-        : pairs(pairs_), units(a.units), kb(a.kb), next(a.cut + pair), cut(false) {
+        : pairs(pairs_), units(a.units), kb(a.kb), next(a.cut + pair), dw(a.first[1]), kb_dw(a.kb_dw), cut(false) {
         if (pair < a.cut * a.split) {
             u = pair / a.split;
             const int j = pair - u * a.split;
@@ -209,7 +212,7 @@ struct Work {
         u = next;
         next += pairs;
         kb0 = 0;
-        kb1 = kb;
+        kb1 = kb_dw > 0 && u >= dw ? kb_dw : kb;
         return true;
     }
 };
@@ -218,8 +221,9 @@ template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args args) {
     constexpr int S = kStages;
-    constexpr bool A_MN = MODE == kWGrad;
-    constexpr bool B_K = MODE == kDHid || MODE == kDX;
+    // whether A's tiles have the rows as the contiguous dimension, and B's the reduction
+    auto a_mn = [](int p) { return MODE == kWGrad || (MODE == kBoth && p == 1); };
+    auto b_k = [](int p) { return MODE == kDHid || MODE == kDX || (MODE == kBoth && p == 0); };
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -244,9 +248,9 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         ptx::fence_barrier_init();
     }
     if (warp == 3 && lane < 9) {  // the descriptors of this mode's tensors
-        constexpr int nA = MODE == kWGrad ? 3 : MODE == kDX ? 2 : 1;
-        constexpr int nB = MODE == kWGrad ? 3 : MODE == kDX || MODE == kGate ? 2 : 1;
-        constexpr int nO = MODE == kWGrad ? 3 : MODE == kDHid ? 2 : 1;
+        constexpr int nA = MODE == kWGrad ? 3 : MODE == kDX || MODE == kBoth ? 2 : 1;
+        constexpr int nB = MODE == kWGrad ? 3 : MODE == kDX || MODE == kGate || MODE == kBoth ? 2 : 1;
+        constexpr int nO = MODE == kWGrad ? 3 : MODE == kDHid || MODE == kBoth ? 2 : 1;
         const int k = lane % 3;
         if (lane < 3 ? k < nA : lane < 6 ? k < nB : k < nO)
             ptx::prefetch_tensormap(lane < 3 ? &maps.a[k] : lane < 6 ? &maps.b[k] : &maps.o[k]);
@@ -270,6 +274,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         Unit x;
         x.p = 0;
         if (MODE == kWGrad) x.p = u >= args.first[2] ? 2 : u >= args.first[1] ? 1 : 0;
+        if (MODE == kBoth) x.p = u >= args.first[1] ? 1 : 0;
         u -= args.first[x.p];
         const int mt = args.mt[x.p], per = kGroup * args.nb[x.p];
         const int k = u / per, gs = min(kGroup, mt - k * kGroup), r = u - k * per;
@@ -298,11 +303,11 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 const uint32_t sA = base + s * kStageBytes, sB = sA + kABytes;
                 const bool second = MODE == kDX && kb >= args.kb_half;
                 const int k0 = (second ? kb - args.kb_half : kb) * BK;
-                const int ai = MODE == kWGrad ? un.p : second ? 1 : 0;
-                const int bi = MODE == kWGrad ? un.p
+                const int ai = MODE == kWGrad || MODE == kBoth ? un.p : second ? 1 : 0;
+                const int bi = MODE == kWGrad || MODE == kBoth ? un.p
                                : MODE == kGate ? (int)rank
                                : second ? 1 : 0;
-                if (A_MN) {
+                if (a_mn(un.p)) {
                     ptx::tma_load_2d_pair(sA, &maps.a[ai], bar, un.row0, k0);
                     ptx::tma_load_2d_pair(sA + kBox, &maps.a[ai], bar, un.row0 + 64, k0);
                 } else {
@@ -312,7 +317,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 const int c0 = MODE == kGate ? un.nb * (BN / 2) : un.nb * BN + (int)rank * (BN / 2);
 #pragma unroll
                 for (int q = 0; q < kBoxes; ++q) {
-                    if (B_K) ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, k0, c0 + q * 64);
+                    if (b_k(un.p)) ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, k0, c0 + q * 64);
                     else ptx::tma_load_2d_pair(sB + q * kBox, &maps.b[bi], bar, c0 + q * 64, k0);
                 }
             }
@@ -328,6 +333,8 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         bool ok = true;
         for (Work w(args, pair, pairs); ok && w.step(); ++uc) {
             const uint32_t a = uc & 1u;
+            const int prob = MODE == kBoth && w.u >= args.first[1] ? 1 : 0;
+            const uint32_t idesc = prob == 1 ? args.idesc_dw : args.idesc;
             if (!bounded_wait(ptx::smem_addr(&ctl->tempty[a]), ((uc >> 1) & 1u) ^ 1u, args.err)) break;
             ptx::tc_fence_after();
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
@@ -342,11 +349,11 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
                 for (int k = 0; k < BK / 16; ++k) {
                     // K-major: the next 16 of the reduction are 32 bytes on; MN-major:
                     // 16 rows of 128 bytes, 64-column slabs 8 KB apart
-                    const uint64_t ad = A_MN ? ptx::desc_sw128(sA + k * 2048, kBox, 1024)
+                    const uint64_t ad = a_mn(prob) ? ptx::desc_sw128(sA + k * 2048, kBox, 1024)
                                              : ptx::desc_sw128(sA + k * 32, 16, 1024);
-                    const uint64_t bd = B_K ? ptx::desc_sw128(sB + k * 32, 16, 1024)
+                    const uint64_t bd = b_k(prob) ? ptx::desc_sw128(sB + k * 32, 16, 1024)
                                             : ptx::desc_sw128(sB + k * 2048, kBox, 1024);
-                    ptx::tc_mma_f16_pair(tmem_base + a * BN, ad, bd, args.idesc, kb != w.kb0 || k != 0);
+                    ptx::tc_mma_f16_pair(tmem_base + a * BN, ad, bd, idesc, kb != w.kb0 || k != 0);
                 }
                 ptx::tc_commit_pair(ptx::smem_addr(&ctl->empty[s]), 0x3);
             }
@@ -355,7 +362,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
         }
         ptx::tc_commit_pair(ptx::smem_addr(&ctl->drain), 0x1);
         bounded_wait(ptx::smem_addr(&ctl->drain), 0, args.err);
-    } else if (MODE == kWGrad && warp == 3) {
+    } else if ((MODE == kWGrad || MODE == kBoth) && warp == 3) {
         // the bias' gradient beside the products: a launch of its own took 2 us of a short
         // training step's 55
         if (args.dbias != nullptr)
@@ -615,7 +622,7 @@ dense_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Arg
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         o[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
-                    store_box(o, x0, y0, &maps.o[MODE == kWGrad ? un.p : 0]);
+                    store_box(o, x0, y0, &maps.o[MODE == kWGrad || MODE == kBoth ? un.p : 0]);
                 }
             }
             return true;
@@ -834,7 +841,7 @@ int64_t tiles_of(int rows, int cols, bool gate) {
 
 template <int MODE>
 cudaError_t launch(const Maps &maps, Args args, cudaStream_t s) {
-    const int problems = MODE == kWGrad ? 3 : 1;
+    const int problems = MODE == kWGrad ? 3 : MODE == kBoth ? 2 : 1;
     int64_t units = 0;
     for (int p = 0; p < 3; ++p) {
         args.first[p] = (int)units;
@@ -847,15 +854,35 @@ cudaError_t launch(const Maps &maps, Args args, cudaStream_t s) {
     if (units > (1 << 30)) return cudaErrorInvalidValue;
     args.units = (int)units;
     const int all = std::max(1, std::min(sm_count(), kFfnMaxCtas) / 2);
-    split_work(units, args.kb, all, &args.cut, &args.split);
+    if (MODE != kBoth) split_work(units, args.kb, all, &args.cut, &args.split);
     const int pairs = (int)std::min<int64_t>(all, std::max<int64_t>(units, args.cut * args.split));
-    args.idesc = idesc(args.f16 != 0, 2 * BM, BN, MODE == kWGrad, !(MODE == kDHid || MODE == kDX));
+    args.idesc = idesc(args.f16 != 0, 2 * BM, BN, MODE == kWGrad, !(MODE == kDHid || MODE == kDX || MODE == kBoth));
+    args.idesc_dw = idesc(args.f16 != 0, 2 * BM, BN, true, true);
     const cudaError_t e =
         ensure_dynamic_smem(reinterpret_cast<const void *>(dense_gemm_kernel<MODE>), (int)kSmem);
     if (e != cudaSuccess) return e;
     if (args.cut > 0)
         return launch_together(dense_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
     return launch_k(dense_gemm_kernel<MODE>, dim3(2 * pairs), dim3(kThreads), kSmem, s, maps, args);
+}
+
+// Whether dX [T,k] and dW [k,n] of a projection run in one launch: where their tiles fit the
+// SM pairs together and the longer reduction takes less than both launches (in k-blocks, with a
+// launch's start, fill and end as kStart). The whole backward, two launches against one: 777 x
+// 1000 x 2728 35.0 / 27.0 us, 2432 x 560 x 256 24.7 / 22.2, 375 x 424 x 656 19.0 / 12.3; where the
+// reductions are too long for tiles that are not cut, and two launches stay: 70 x 576 x 3864 26.3 /
+// 29.7, 256 x 256 x 8192 28.8 / 56.3.
+constexpr int kStart = 18;
+int64_t launch_blocks(int64_t units, int kb, int pairs) {
+    int cut, split;
+    split_work(units, kb, pairs, &cut, &split);
+    const int64_t whole = (units - cut + pairs - 1) / pairs * kb;
+    return kStart + std::max<int64_t>(whole, cut > 0 ? (kb + split - 1) / split + kJoin : 0);
+}
+bool both_in_one(int T, int k, int n, int pairs) {
+    const int64_t x = tiles_of(T, k, false), w = tiles_of(k, n, false);
+    const int kx = (n + BK - 1) / BK, kw = (T + BK - 1) / BK;
+    return x + w <= pairs && kStart + std::max(kx, kw) < launch_blocks(x, kx, pairs) + launch_blocks(w, kw, pairs);
 }
 
 constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B, kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;
@@ -953,6 +980,25 @@ cudaError_t launch_linear_products(const void *dA, const void *X, const void *W,
     a.part = part;
     a.ticket = ticket;
     a.err = err;
+    a.dbias = dbias;
+    a.bias32 = bias32;
+    a.sums = sums;
+    a.sum_rows = linear_sum_rows(T, n);
+    a.sum_n = n;
+    const int kx = (n + BK - 1) / BK, kw = (T + BK - 1) / BK;
+    if (dX != nullptr && dW != nullptr && both_in_one(T, k, n, sm_count() / 2)) {
+        if (!map_a(&m.a[0], f16, dA, n, T) || !map_64(&m.b[0], f16, W, n, k) || !map_out(&m.o[0], f16, dX, k, T) ||
+            !map_64(&m.a[1], f16, X, k, T) || !map_64(&m.b[1], f16, dA, n, T) || !map_out(&m.o[1], f16, dW, n, k))
+            return cudaErrorInvalidValue;
+        a.rows[0] = T;
+        a.cols[0] = a.rows[1] = k;
+        a.cols[1] = n;
+        a.kb = kx;
+        a.kb_dw = kw;
+        a.out[0] = dX;
+        a.out[1] = dW;
+        return launch<kBoth>(m, a, s);
+    }
     if (dX != nullptr) {
         if (!map_a(&m.a[0], f16, dA, n, T) || !map_64(&m.b[0], f16, W, n, k) || !map_out(&m.o[0], f16, dX, k, T))
             return cudaErrorInvalidValue;
@@ -960,7 +1006,7 @@ cudaError_t launch_linear_products(const void *dA, const void *X, const void *W,
         m.b[1] = m.b[0];
         a.rows[0] = T;
         a.cols[0] = k;
-        a.kb = a.kb_half = (n + BK - 1) / BK;
+        a.kb = a.kb_half = kx;
         a.out[0] = dX;
         const cudaError_t e = launch<kDX>(m, a, s);
         if (e != cudaSuccess) return e;
@@ -973,14 +1019,9 @@ cudaError_t launch_linear_products(const void *dA, const void *X, const void *W,
         m.b[i] = m.b[0];
         m.o[i] = m.o[0];
     }
-    a.dbias = dbias;
-    a.bias32 = bias32;
-    a.sums = sums;
-    a.sum_rows = linear_sum_rows(T, n);
-    a.sum_n = n;
     a.rows[0] = k;
     a.cols[0] = n;
-    a.kb = (T + BK - 1) / BK;
+    a.kb = kw;
     a.out[0] = dW;
     return launch<kWGrad>(m, a, s);
 }
