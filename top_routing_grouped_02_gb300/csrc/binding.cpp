@@ -1,5 +1,5 @@
-// Python entry points of the sub-block calls (layer norm, residual dropout, dense
-// feed-forward block): argument checks, output allocation and one call into
+// Python entry points of the sub-block calls (layer norm, residual dropout, dense feed-forward
+// block, projections, norms around a block, dispatch and combine): argument checks, output allocation and one call into
 // libmoe.so each. They do what the ctypes functions of moe.py do for the other calls;
 // these run at sizes where a call's host time is several times its GPU time, and from
 // Python it was (12 us of host time for a 2 us kernel).

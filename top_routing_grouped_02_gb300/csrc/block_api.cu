@@ -1,6 +1,6 @@
-// C ABI of the sub-block operators around the layer (layer norm, residual
-// dropout, dense gated feed-forward block): argument checks and launches. Errors are returned before anything
-// is enqueued.
+// C ABI of the sub-block operators around the layer (layer norm, residual dropout, dense gated
+// feed-forward block, projections, norms around a block, dispatch and combine): argument checks
+// and launches. Errors are returned before anything is enqueued.
 #include <math.h>
 
 #include <algorithm>

@@ -30,6 +30,10 @@
 // run of k-blocks (32, 11, 16, 22 and 26, at 0.33 us each; gate and the weight gradients are
 // two waves) takes 10.7, 3.7, 5.3, 7.3 and 8.7; the rest is the start (1 us), the ring's fill
 // (2-3), the last epilogue (1.5-4) or the join (5), and the end (1.5).
+// The projections (kLinear and the products of its gradients): 4096 tokens, 4096 x 14336 bf16 with
+// F 285 us (1.69 PFLOP/s), dX 256 (1.88), dW 248 (1.94); 777 tokens, 1000 x 2728: 19 us with F, bias,
+// gelu and residual (12.4 with none of them), dX and dW together 20; 512 tokens, 7168 x 2048 fp16:
+// 24 us.
 // All tails (T, d, n need not be multiples of a tile) are left to TMA: loads
 // outside a tensor give zeros, which add nothing, and stores outside write nothing.
 //

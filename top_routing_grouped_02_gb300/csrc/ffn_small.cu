@@ -27,6 +27,10 @@
 // the first product's last sums are in the workspace at 16 us, H is complete at 19.5, the
 // second product's sums at 25 and joined at 29.
 //
+// LINEAR: a projection for few tokens, the second product alone with bias, activation and residual
+// in its epilogue: one token, 14336 x 4096 bf16 25.9 us (4.5 TB/s), 16 tokens 30.2; 7168 x 2048, 64
+// tokens 20.6.
+//
 // Warps: 0 TMA producer, 1 MMA issuer, 2 TMEM allocation, 4-11 epilogue.
 #include <algorithm>
 
