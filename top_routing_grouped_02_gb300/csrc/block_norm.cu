@@ -42,10 +42,10 @@ int block_norm_partials(int64_t T) {
 
 cudaError_t launch_block_norm_forward(const BlockNormCall &c, int64_t withheld, cudaStream_t s) {
     Args a{};
-    Align al;
+    Places places;
     const int es = c.type == MOE_DTYPE_F32 ? 4 : 2;
     auto in = [&](const Matrix &m) {
-        al.add(m.p, m.ld, c.d, es, c.T);
+        places.add(m.p, m.ld, c.d, es, c.T);
         return m.p;
     };
     a.x = in(c.x);
@@ -72,18 +72,18 @@ cudaError_t launch_block_norm_forward(const BlockNormCall &c, int64_t withheld, 
     a.eps = c.eps;
     a.withheld = withheld;
     switch (c.type) {
-        case MOE_DTYPE_BF16: return forward_type<__nv_bfloat16>(a, al, s);
-        case MOE_DTYPE_F16: return forward_type<__half>(a, al, s);
-        default: return forward_type<float>(a, al, s);
+        case MOE_DTYPE_BF16: return forward_type<__nv_bfloat16>(a, places.shift(), s);
+        case MOE_DTYPE_F16: return forward_type<__half>(a, places.shift(), s);
+        default: return forward_type<float>(a, places.shift(), s);
     }
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormCall &c, int64_t withheld, cudaStream_t s) {
     Args a{};
-    Align al;
+    Places places;
     const int es = c.type == MOE_DTYPE_F32 ? 4 : 2;
     auto in = [&](const Matrix &m) {
-        al.add(m.p, m.ld, c.d, es, c.T);
+        places.add(m.p, m.ld, c.d, es, c.T);
         return m.p;
     };
     auto out = [&](const Matrix &m) { return const_cast<void *>(in(m)); };
@@ -117,9 +117,9 @@ cudaError_t launch_block_norm_backward(const BlockNormCall &c, int64_t withheld,
     a.withheld = withheld;
     a.part = c.dpost != nullptr || c.dpre != nullptr ? c.part : nullptr;
     int P = 0;
-    const cudaError_t e = c.type == MOE_DTYPE_BF16  ? backward_type<__nv_bfloat16>(a, al, &P, s)
-                          : c.type == MOE_DTYPE_F16 ? backward_type<__half>(a, al, &P, s)
-                                                    : backward_type<float>(a, al, &P, s);
+    const cudaError_t e = c.type == MOE_DTYPE_BF16  ? backward_type<__nv_bfloat16>(a, places.shift(), &P, s)
+                          : c.type == MOE_DTYPE_F16 ? backward_type<__half>(a, places.shift(), &P, s)
+                                                    : backward_type<float>(a, places.shift(), &P, s);
     if (e != cudaSuccess || a.part == nullptr) return e;
     return launch_weight_reduce(a.part, P, a.d, a.w32 ? MOE_DTYPE_F32 : c.type, c.dpost, c.dpre, s);
 }

@@ -112,9 +112,9 @@ __device__ __forceinline__ void sigmoid2(f32x2 z, f32x2 &g, f32x2 &h) {
 // at the same place of its 16 bytes again, whatever the stride. So a thread's vectors are the
 // image's blocks, with the same columns in all of its rows, and nothing is shifted but the
 // weights, once; the elements of the first and the last block that are not the row's are set to
-// zero. The place is that of the first output's rows; where an operand's rows start elsewhere
-// its vectors are shifted out of two neighbouring blocks, and another output's elements are
-// stored one by one.
+// zero. The place is that of the first output's rows; where (SHIFT 2) an operand's rows start
+// elsewhere its vectors are shifted out of two neighbouring blocks, and another output's elements
+// are stored one by one.
 constexpr int kRingStages = 4, kMaxGroups = 28, kPhases = 8;
 constexpr size_t kRingSmem = 224 * 1024;
 struct RingCtl {
@@ -132,7 +132,7 @@ bool ring_shape(Args &a, int cols, int per_thread, int max_threads, size_t fixed
 // Rows of a block in hand: a group with one stage fetches its next row late, with two it need not.
 inline int rows_ahead(const Args &a, int groups) { return groups * std::min(a.stages, 2); }
 // Blocks of a launch of rows in `groups` a block.
-template <bool SHIFT>
+template <int SHIFT>
 int ring_grid(int64_t T, int groups, int sms) {
     if (!SHIFT) return (int)std::min<int64_t>((T + groups - 1) / groups, sms);
     const int64_t of_phase = (T + kPhases - 1) / kPhases;
@@ -140,9 +140,9 @@ int ring_grid(int64_t T, int groups, int sms) {
 }
 // Columns that a row's vectors may reach over; bytes of a row in a stage. (A vector that is
 // shifted out of two blocks may reach a block past the image, or lie one in front of it.)
-template <int V, bool SHIFT>
+template <int V, int SHIFT>
 __host__ __device__ constexpr int ring_cols(int d) { return SHIFT ? d + V - 1 : d; }
-template <typename T, bool SHIFT>
+template <typename T, int SHIFT>
 __host__ __device__ uint32_t ring_row_bytes(int d) {
     return SHIFT ? (image_bytes(d, sizeof(T)) + 16 + 112 + 127) / 128 * 128 : (uint32_t)(d * sizeof(T));
 }
@@ -164,7 +164,7 @@ __device__ __forceinline__ uint4 elements_inside(uint4 q, int first, int end) {
 }
 
 // A thread's vectors of V elements of a row: vector v holds the columns v V - lead and on.
-template <typename T, int V, bool SHIFT>
+template <typename T, int V, int SHIFT>
 struct Part {
     int tpr, t, d, nvec;
     int lead;  // elements of the first block in front of the row
@@ -176,7 +176,7 @@ struct Part {
     __device__ __forceinline__ bool has(int i) const { return i * tpr + t < nvec; }
     // a row's start in global memory, against the output's place
     __device__ __forceinline__ int off(const T *row) const {
-        return SHIFT ? (int)(reinterpret_cast<uintptr_t>(row) & 15) - lead * (int)sizeof(T) : 0;
+        return SHIFT == 2 ? (int)(reinterpret_cast<uintptr_t>(row) & 15) - lead * (int)sizeof(T) : 0;
     }
     // vector i of the row at `image`, which starts `off` bytes off that place
     __device__ __forceinline__ void load(const uint8_t *image, int off, int i, f32x2 (&p)[V / 2]) const {
@@ -184,7 +184,8 @@ struct Part {
         if constexpr (!SHIFT) {
             to_pairs<T, V>(reinterpret_cast<const uint4 *>(image)[v], p);
         } else {
-            uint4 q = off == 0 ? reinterpret_cast<const uint4 *>(image)[v]
+            uint4 q = SHIFT == 1 || off == 0
+                               ? reinterpret_cast<const uint4 *>(image)[v]
                                : image_vec<T>(image - (off < 0 ? 16 : 0), v, (uint32_t)off & 15);
             if (v == 0 || v == nvec - 1) q = elements_inside<T>(q, lead - v * V, d + lead - v * V);
             to_pairs<T, V>(q, p);
@@ -196,7 +197,7 @@ struct Part {
         const uint4 q = from_pairs<T, V>(p);
         if constexpr (!SHIFT) {
             reinterpret_cast<uint4 *>(row)[v] = q;
-        } else if (off == 0 && v > 0 && v < nvec - 1) {
+        } else if ((SHIFT == 1 || off == 0) && v > 0 && v < nvec - 1) {
             *reinterpret_cast<uint4 *>(row + (v * V - lead)) = q;
         } else {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -213,7 +214,7 @@ struct Part {
 // A weight vector in shared memory, `lead` elements on: in fp32 as planes of four elements of
 // every vector, or (RAW) of 16 bits as it is. Both are read without bank conflicts; planes need
 // no conversion, RAW half the memory.
-template <typename T, int V, bool SHIFT, bool RAW>
+template <typename T, int V, int SHIFT, bool RAW>
 struct Weights {
     static __host__ __device__ uint32_t bytes(int d) {
         const uint32_t n = (uint32_t)((ring_cols<V, SHIFT>(d) + V - 1) / V * V) * (RAW ? sizeof(T) : sizeof(float));
@@ -245,12 +246,12 @@ struct Weights {
 };
 // Where the image of a row lies in its place of a stage: as far from a 128-byte line of shared
 // memory as the row is from one of global memory, so that a bulk copy moves whole lines.
-template <typename T, bool SHIFT>
+template <typename T, int SHIFT>
 __device__ __forceinline__ uint32_t image_at(const void *p, int64_t ld, int64_t r) {
     return SHIFT ? (uint32_t)reinterpret_cast<uintptr_t>(static_cast<const T *>(p) + r * ld) & 112 : 0;
 }
 // One thread: row r of a [rows, d] tensor into dst, arriving on bar.
-template <typename T, bool SHIFT>
+template <typename T, int SHIFT>
 __device__ __forceinline__ void fetch_row(uint8_t *dst, const void *p, int64_t ld, int64_t r, int64_t rows, int d,
                                           uint32_t bar) {
     const T *base = static_cast<const T *>(p);
@@ -269,11 +270,27 @@ struct RowShape {
 };
 RowShape row_shape(Args &a, int per_thread);
 
+// How the rows of a call's matrices start: 0 all on 16 bytes, 1 all at the same places, 2 anywhere.
+struct Places {
+    Align al;
+    uint64_t first = 0, other = 0;
+    bool any = false;
+    void add(const void *p, int64_t ld, int d, int esize, int64_t T) {
+        if (p == nullptr) return;
+        al.add(p, ld, d, esize, T);
+        const uint64_t at = (reinterpret_cast<uintptr_t>(p) & 15) | (T > 1 ? ((uint64_t)ld * esize & 15) << 4 : 0);
+        if (!any) first = at;
+        any = true;
+        other |= at ^ first;
+    }
+    int shift() const { return al.fits(16) ? 0 : other == 0 ? 1 : 2; }
+};
+
 // The launches for one element type (block_norm_*.cu).
 template <typename T>
-cudaError_t forward_type(const Args &a, const Align &al, cudaStream_t s);
+cudaError_t forward_type(const Args &a, int shift, cudaStream_t s);
 template <typename T>
-cudaError_t backward_type(const Args &a, const Align &al, int *P, cudaStream_t s);
+cudaError_t backward_type(const Args &a, int shift, int *P, cudaStream_t s);
 
 }  // namespace bn
 }  // namespace moe

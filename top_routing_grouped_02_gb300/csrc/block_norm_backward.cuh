@@ -15,7 +15,7 @@
 //
 // Measured, with the second kernel: 8192 x 7168 bf16 with a full gate 180 us (5.2 TB/s), 4096 x
 // 4096 bf16 with a row's gate 58 us, 8192 x 4096 fp32 without one 136 us (5.9 TB/s); rows of 7167
-// bf16, 354 us. One row group of 14 warps is all that the registers (the column sums and five values
+// bf16, 315 us. One row group of 14 warps is all that the registers (the column sums and five values
 // an element between the sums) let an SM hold of 7168 columns, and it waits twice a row for a sum.
 #pragma once
 
@@ -170,7 +170,7 @@ cudaError_t backward_rows(Args a, int *P, cudaStream_t s) {
 
 // Rows through a ring, as the forward's. A stage holds x, b (MODE 1, 2) and the gate (MODE 2),
 // then du and dy, where the call has them. MT: most threads.
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW, int MT>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW, int MT>
 __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     }
 }
 
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
     const size_t stage = (MODE + 1 + a.pre_norm + (a.dy != nullptr)) * ring_row_bytes<T, SHIFT>(a.d);
     const size_t fixed = kRingCtl + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(a.d);
@@ -383,7 +383,7 @@ bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
 // The block of at most 448 threads is compiled for as many registers as that of 512 (128), but
 // runs 8 to 10 % faster where both have the same groups, or nearly (8192 x 7168 bf16 180 / 200
 // us, 4096 x 1024 19.7 / 21.4; 4096 x 4096, one group against two, 77 / 58).
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 bool backward_best(Args &a, int *threads, int *groups, size_t *smem) {
     Args few = a;
     int g = 0;
@@ -398,7 +398,7 @@ bool backward_best(Args &a, int *threads, int *groups, size_t *smem) {
     }
     return fits;
 }
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 cudaError_t backward_launch(const Args &a, int threads, int groups, size_t smem, int *P, cudaStream_t s) {
     const auto kernel = threads == kBwdFewThreads
                             ? backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdFewThreads>
@@ -409,7 +409,7 @@ cudaError_t backward_launch(const Args &a, int threads, int groups, size_t smem,
     return launch_k(kernel, dim3(*P), dim3(groups * a.wpr * 32), smem, s, a);
 }
 // (weights as in the forward)
-template <typename T, int MODE, bool SHIFT>
+template <typename T, int MODE, int SHIFT>
 cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T), NV = 16 / V;  // 16 elements a thread
     Args planes = a;
@@ -428,7 +428,7 @@ cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
     }
     return *fits ? backward_launch<T, V, NV, MODE, SHIFT, false>(planes, threads, groups, smem, P, s) : cudaSuccess;
 }
-template <typename T, bool SHIFT>
+template <typename T, int SHIFT>
 cudaError_t backward_rings(const Args &a, int *P, bool *fits, cudaStream_t s) {
     return a.b == nullptr ? backward_ring<T, 0, SHIFT>(a, P, fits, s)
            : !a.full      ? backward_ring<T, 1, SHIFT>(a, P, fits, s)
@@ -438,13 +438,14 @@ cudaError_t backward_rings(const Args &a, int *P, bool *fits, cudaStream_t s) {
 }  // namespace
 
 template <typename T>
-cudaError_t backward_type(const Args &a, const Align &al, int *P, cudaStream_t s) {
+cudaError_t backward_type(const Args &a, int shift, int *P, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
     bool fits = false;
-    const cudaError_t e =
-        al.fits(16) ? backward_rings<T, false>(a, P, &fits, s) : backward_rings<T, true>(a, P, &fits, s);
+    const cudaError_t e = shift == 0   ? backward_rings<T, 0>(a, P, &fits, s)
+                          : shift == 1 ? backward_rings<T, 1>(a, P, &fits, s)
+                                       : backward_rings<T, 2>(a, P, &fits, s);
     if (e != cudaSuccess || fits) return e;
-    return al.fits(16) ? backward_rows<T, W, 16 / W>(a, P, s) : backward_rows<T, 1, 16>(a, P, s);
+    return shift == 0 ? backward_rows<T, W, 16 / W>(a, P, s) : backward_rows<T, 1, 16>(a, P, s);
 }
 
 }  // namespace bn

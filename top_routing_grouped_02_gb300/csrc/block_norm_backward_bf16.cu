@@ -2,6 +2,6 @@
 
 namespace moe {
 namespace bn {
-template cudaError_t backward_type<__nv_bfloat16>(const Args &, const Align &, int *, cudaStream_t);
+template cudaError_t backward_type<__nv_bfloat16>(const Args &, int, int *, cudaStream_t);
 }  // namespace bn
 }  // namespace moe

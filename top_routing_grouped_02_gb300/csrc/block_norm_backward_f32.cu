@@ -2,6 +2,6 @@
 
 namespace moe {
 namespace bn {
-template cudaError_t backward_type<float>(const Args &, const Align &, int *, cudaStream_t);
+template cudaError_t backward_type<float>(const Args &, int, int *, cudaStream_t);
 }  // namespace bn
 }  // namespace moe

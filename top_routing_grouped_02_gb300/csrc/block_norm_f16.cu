@@ -2,6 +2,6 @@
 
 namespace moe {
 namespace bn {
-template cudaError_t forward_type<__half>(const Args &, const Align &, cudaStream_t);
+template cudaError_t forward_type<__half>(const Args &, int, cudaStream_t);
 }  // namespace bn
 }  // namespace moe

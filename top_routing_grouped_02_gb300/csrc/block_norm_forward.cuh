@@ -6,8 +6,8 @@
 // end.
 //
 // Measured, calls back to back: 8192 x 7168 bf16 with a full gate 103 us (5.7 TB/s), 4096 x 4096
-// bf16 with a row's gate 27 us (5.0 TB/s), 8192 x 4097 fp32 92 us (5.9 TB/s); rows of 7167 bf16,
-// 138 us.
+// bf16 with a row's gate 27 us (5.0 TB/s), 8192 x 4097 fp32 89 us (6.1 TB/s); rows of 7167 bf16
+// 113 us, of 7168 with inputs that start elsewhere than outputs 153 us.
 #pragma once
 
 #include <algorithm>
@@ -89,7 +89,7 @@ cudaError_t forward_rows(Args a, cudaStream_t s) {
 // Rows through a ring. MODE: 0 x alone, 1 x and b (a gate is the row's), 2 x, b and the gate.
 // The arithmetic is packed.
 constexpr int kFwdThreads = 896, kFwdWideThreads = 640;  // most of a block; with 32 elements a thread
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 __global__ void __launch_bounds__(V * NV == 32 ? kFwdWideThreads : kFwdThreads, 1) forward_ring_kernel(const Args a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(V * NV == 32 ? kFwdWideThreads : kFwdThreads, 
     }
 }
 
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 bool forward_shape(Args &a, int *groups, size_t *smem) {
     const size_t stage = (MODE + 1) * ring_row_bytes<T, SHIFT>(a.d);
     const size_t fixed = kRingCtl + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(a.d);
@@ -219,7 +219,7 @@ bool forward_shape(Args &a, int *groups, size_t *smem) {
     *smem = fixed + *groups * a.stages * stage;
     return true;
 }
-template <typename T, int V, int NV, int MODE, bool SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 cudaError_t forward_launch(const Args &a, int groups, size_t smem, cudaStream_t s) {
     const auto kernel = forward_ring_kernel<T, V, NV, MODE, SHIFT, RAW>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)kRingSmem);
@@ -229,7 +229,7 @@ cudaError_t forward_launch(const Args &a, int groups, size_t smem, cudaStream_t 
 // 16-bit weights as they are where their planes leave room for fewer rows at a time (8192 x 7168
 // bf16 with a full gate, two groups with a stage each against two: 112 / 103 us; 4096 x 4096
 // with a row's gate, alike either way: 29.4 with planes, 32.6).
-template <typename T, int NV, int MODE, bool SHIFT>
+template <typename T, int NV, int MODE, int SHIFT>
 cudaError_t forward_ring(const Args &a, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     Args planes = a;
@@ -250,14 +250,14 @@ cudaError_t forward_ring(const Args &a, bool *fits, cudaStream_t s) {
 }
 // 16 elements a thread, 32 of long 16-bit rows (4096 x 4096 bf16 with a row's gate 29.4 / 27.1 us,
 // 8192 x 7167 with a full one 153 / 132; 4096 x 1024 7.3 / 8.0; fp32 4096 x 4096 62 / 73).
-template <typename T, int MODE, bool SHIFT>
+template <typename T, int MODE, int SHIFT>
 cudaError_t forward_length(const Args &a, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     if constexpr (sizeof(T) == 2)
         if (a.d >= 2048) return forward_ring<T, 32 / V, MODE, SHIFT>(a, fits, s);
     return forward_ring<T, 16 / V, MODE, SHIFT>(a, fits, s);
 }
-template <typename T, bool SHIFT>
+template <typename T, int SHIFT>
 cudaError_t forward_rings(const Args &a, bool *fits, cudaStream_t s) {
     return a.b == nullptr ? forward_length<T, 0, SHIFT>(a, fits, s)
            : !a.full      ? forward_length<T, 1, SHIFT>(a, fits, s)
@@ -267,13 +267,14 @@ cudaError_t forward_rings(const Args &a, bool *fits, cudaStream_t s) {
 }  // namespace
 
 template <typename T>
-cudaError_t forward_type(const Args &a, const Align &al, cudaStream_t s) {
+cudaError_t forward_type(const Args &a, int shift, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
     bool fits = false;
-    const cudaError_t e =
-        al.fits(16) ? forward_rings<T, false>(a, &fits, s) : forward_rings<T, true>(a, &fits, s);
+    const cudaError_t e = shift == 0   ? forward_rings<T, 0>(a, &fits, s)
+                          : shift == 1 ? forward_rings<T, 1>(a, &fits, s)
+                                       : forward_rings<T, 2>(a, &fits, s);
     if (e != cudaSuccess || fits) return e;
-    return al.fits(16) ? forward_rows<T, W, 16 / W>(a, s) : forward_rows<T, 1, 16>(a, s);
+    return shift == 0 ? forward_rows<T, W, 16 / W>(a, s) : forward_rows<T, 1, 16>(a, s);
 }
 
 }  // namespace bn
