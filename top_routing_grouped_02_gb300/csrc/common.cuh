@@ -275,9 +275,9 @@ struct LinearCall {
 };
 // Few tokens stream the weights: up to 16, or 64 where n <= 2048 leaves the tiles so few that they
 // are cut into many segments. Measured, streaming against tiled, in us: 14336 x 4096 16 tokens
-// 30.2 / 30.9, 32: 33.0 / 31.0, 64: 36.6 / 31.7; 4096 x 4096 32: 20.6 / 18.6; 4096 x 8192 32:
-// 27.8 / 24.8; 7168 x 2048 16: 16.5 / 20.8, 64: 20.6 / 22.7; 8192 x 1024 64: 16.6 / 18.3; 4096 x
-// 128 64: 10.3 / 15.8.
+// 28.9 / 30.9, 32: 30.9 / 30.9, 64: 33.1 / 31.3; 4096 x 4096 32: 18.6 / 18.5, 64: 20.8 / 18.6; 4096
+// x 8192 32: 24.7 / 23.4; 2048 x 2728 64: 18.2 / 15.7; 7168 x 2048 16: 14.6 / 20.8, 64: 18.8 / 22.7;
+// 8192 x 1024 64: 14.9 / 18.6; 4096 x 128 64: 10.3 / 15.2.
 inline bool linear_streams(int T, int n) { return T <= 16 || (T <= kFfnStreamTokens && n <= 2048); }
 size_t linear_stream_part_bytes(int T, int k, int n);
 cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *ticket, uint32_t *err,

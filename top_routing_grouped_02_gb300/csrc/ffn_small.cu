@@ -28,8 +28,8 @@
 // second product's sums at 25 and joined at 29.
 //
 // LINEAR: a projection for few tokens, the second product alone with bias, activation and residual
-// in its epilogue: one token, 14336 x 4096 bf16 25.9 us (4.5 TB/s), 16 tokens 30.2; 7168 x 2048, 64
-// tokens 20.6.
+// in its epilogue: one token, 14336 x 4096 bf16 24.9 us (4.7 TB/s), 16 tokens 28.9; 7168 x 2048, 64
+// tokens 18.8.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 TMEM allocation, 4-11 epilogue.
 #include <algorithm>
@@ -130,8 +130,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 // writes and reads 16 bytes at a time.
 // joined() is called once the CTA's outputs are stored, before the tickets are
 // released.
-// LINEAR: the sums of a projection, out = act(sums + bias) + residual. LAST: a cut tile is
-// joined by the warp whose part is the last one there, and no CTA waits for another.
+// LINEAR: the sums of a projection, out = act(sums + bias) + residual. LAST (of up to four
+// tokens): a cut tile is joined by the warp whose part is the last one there, and no CTA waits
+// for another.
 template <int MATS, int NT, bool LINEAR, bool LAST, typename Joined>
 __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p, uint32_t *ticket,
                                          SmallCtl *ctl, uint32_t tmem_base, int &seg, Joined joined) {
@@ -145,15 +146,31 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
     const int TG = (T + 3) / 4;
     const int64_t part_ld = (int64_t)MATS * TG * 128;  // vectors of one part
     const int first_tile = (int)(begin / p.kbs), last_tile = (int)((end - 1) / p.kbs);
-    auto emit = [&](int tile, int t, float s0, float s1) {
+    // LINEAR: the bias and up to four tokens' residuals of this lane's column of a tile, loaded
+    // before their sums are there (one token, 14336 x 4096: 25.9 us with loads behind the sums,
+    // 24.9)
+    struct Ends {
+        float bias, res[4];
+    };
+    auto load_ends = [&](int tile, int t0) {
+        Ends e = {};
+        const int col = tile * 128 + q * 32 + lane;
+        if (!LINEAR || col >= p.cols) return e;
+        if (args.bias != nullptr)
+            e.bias = args.bias32 ? __ldg(static_cast<const float *>(args.bias) + col) : load16(args.bias, col, f16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (args.res != nullptr && t0 + j < T) e.res[j] = load16(args.res, (int64_t)(t0 + j) * p.cols + col, f16);
+        return e;
+    };
+    auto emit = [&](int tile, int t, float s0, float s1, float bias, float res) {
         const int col = tile * 128 + q * 32 + lane;
         if (col >= p.cols) return;
         float v = MATS == 2 ? s0 * act_sigmoid(s0, args.act) * s1 : s0;
         if constexpr (LINEAR) {
-            if (args.bias != nullptr)
-                v += args.bias32 ? __ldg(static_cast<const float *>(args.bias) + col) : load16(args.bias, col, f16);
+            v += bias;
             if (args.act != kNoAct) v *= act_sigmoid(v, args.act);
-            if (args.res != nullptr) v += load16(args.res, (int64_t)t * p.cols + col, f16);
+            v += res;
         }
         out[(int64_t)t * p.cols + col] = round16(v, f16);
     };
@@ -192,7 +209,7 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
 
     // vector g of a cut tile's tokens: its parts in order, then the outputs
     constexpr int kBatch = MATS == 2 ? 10 : 16;  // parts in flight
-    auto add_parts = [&](const Cut &x, int g) {
+    auto add_parts = [&](const Cut &x, int g, const Ends &e) {
         float sum[MATS][4] = {};
 #pragma unroll 1
         for (int c = 0; c < x.P; c += kBatch) {
@@ -216,12 +233,14 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (4 * g + j < T) emit(x.tile, 4 * g + j, sum[0][j], sum[MATS - 1][j]);
+            if (4 * g + j < T) emit(x.tile, 4 * g + j, sum[0][j], sum[MATS - 1][j], e.bias, e.res[j]);
     };
 
     for (int tile = first_tile; tile <= last_tile; ++tile, ++seg) {
         const bool cut = is_cut(tile);
         const int a = seg & 1;
+        Ends ends;
+        if constexpr (LAST) ends = load_ends(tile, 0);
         if (!bounded_wait(ptx::smem_addr(&ctl->tfull[a]), (seg >> 1) & 1, args.err)) return false;
         ptx::tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 2 * NT;
@@ -233,9 +252,15 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
             for (int m = 0; m < MATS; ++m) tmem_ld16(taddr + m * NT + c, r[m]);
             if (!cut) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + j < T)
-                        emit(tile, c + j, __uint_as_float(r[0][j]), __uint_as_float(r[MATS - 1][j]));
+                for (int j = 0; j < 16; j += 4) {
+                    if (c + j >= T) break;
+                    if constexpr (!LAST) ends = load_ends(tile, c + j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c + j + k < T)
+                            emit(tile, c + j + k, __uint_as_float(r[0][j + k]), __uint_as_float(r[MATS - 1][j + k]),
+                                 ends.bias, ends.res[k]);
+                }
                 continue;
             }
 #pragma unroll
@@ -259,7 +284,7 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
             if (!__shfl_sync(0xffffffffu, last, 0)) continue;
             __threadfence();  // the parts' loads come after the ticket
             __syncwarp();
-            for (int g = 0; g < TG; ++g) add_parts(x, g);
+            add_parts(x, 0, ends);
             if (lane == 0) ticket[tile * 4 + q] = 0;
         } else if (cut) {
             // low half: warps whose parts are written; high half: that need them no more
@@ -286,7 +311,7 @@ __device__ __forceinline__ bool epilogue(const SmallArgs &args, const Product &p
         const Cut x = i == 0 ? cuts[0] : cuts[1];
         if (x.tile < 0) continue;
 #pragma unroll 1
-        for (int g = x.lo; g < x.hi; g += kSets) add_parts(x, g);
+        for (int g = x.lo; g < x.hi; g += kSets) add_parts(x, g, load_ends(x.tile, 4 * g));
     }
     __syncwarp();  // every lane has its parts
     // this warp's shares are done; the last one of a tile returns its ticket to zero
@@ -327,6 +352,15 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
         }
         ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
         ptx::fence_barrier_init();
+    }
+    if (warp == 3 && lane == 0) {
+        if (!LINEAR) {
+            ptx::prefetch_tensormap(&maps.w[0]);
+            ptx::prefetch_tensormap(&maps.w[1]);
+            ptx::prefetch_tensormap(&maps.x);
+        }
+        ptx::prefetch_tensormap(&maps.w[2]);
+        ptx::prefetch_tensormap(&maps.h);
     }
     if (warp == 2) {
         ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), G::kTmem);
@@ -612,7 +646,7 @@ cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *tic
     // Up to four tokens' parts are added by the last of their warps, if they are few (a tile's
     // parts are one round trip, then): a launch that need not be cooperative starts earlier.
     // Measured, against joins that the CTAs share: 14336 x 4096, one token 25.9 / 27.6 us, 1024 x
-    // 1024 6.4 / 8.3; eight tokens, two round trips, 4096 x 4096 21.1 / 16.5.
+    // 1024 6.4 / 8.3 (24.9 and 5.8 since); eight tokens, two round trips, 4096 x 4096 21.1 / 16.5.
     constexpr int kLastTokens = 4;
     const int parts = (grid + a.p[1].tiles - 1) / a.p[1].tiles + 1;
     const bool last = c.T <= kLastTokens && parts <= 16;
