@@ -32,6 +32,12 @@ CASES = [
     (7, 130, BF, BF, "full", (0, 1), 1.0, 131), (7, 1, BF, BF, "full", (1, 0), 1.0, 3),
     (2, 16384, F32, F32, "full", (1, 1), 1.0, None), (2, 16384, BF, BF, "full", (1, 1), 1.0, None),
     (2, 16381, BF, F32, "row", (1, 1), 1.0, None), (3, 12000, BF, BF, "full", (1, 1), 1.0, None),
+    # long rows: halves of them, of the same and of different sizes
+    (400, 14336, BF, BF, "row", (1, 1), 1.0, None), (170, 8200, FP16, F32, "full", (1, 1), 0.5, 8216),
+    (1, 8196, F32, F32, None, (1, 1), 1.0, None), (79, 16384, F32, F32, None, (1, 1), 1.0, None),
+    (160, 10248, BF, BF, "full", (1, 0), 1.0, None), (77, 16376, FP16, FP16, "row", (0, 1), 1.0, None),
+    (333, 14335, BF, BF, "row", (1, 1), 1.0, None), (40, 9001, FP16, F32, "full", (1, 1), 1.0, 9003),
+    (20, 12301, F32, F32, None, (1, 1), 1.0, None), (18, 9217, BF, BF, None, (1, 1), 1.0, 9218),
 ]
 IDS = [f"T{c[0]}d{c[1]}-{str(c[2])[6:]}-{c[4]}-{c[5][0]}{c[5][1]}-ld{c[7] or c[1]}" for c in CASES]
 
@@ -166,18 +172,17 @@ def test_zero_rows_and_steep_gates(d, ld, dt):
         check(dict(zip(("dx", "db", "dgate", "dpost", "dpre"), got)), plain.backward(dy.cpu(), du.cpu(), *args), T, 200)
 
 
-@pytest.mark.parametrize("dt", [BF, F32], ids=str)
-def test_operands_that_start_at_different_places(dt):
+@pytest.mark.parametrize("T,d,dt", [(45, 300, BF), (45, 300, F32), (91, 9000, BF), (20, 8501, F32)], ids=str)
+def test_operands_that_start_at_different_places(T, d, dt):
     """Each operand in a buffer of its own stride and start."""
-    T, d = 45, 300
     gen = torch.Generator().manual_seed(17)
 
     def mat(ld, start):
         v = torch.randn(T * ld + start + d, generator=gen).to(dt).cuda()
         return torch.as_strided(v, (T, d), (ld, 1), start)
 
-    x, b, gate, dy, du = mat(301, 0), mat(303, 1), mat(300, 3), mat(307, 2), mat(302, 5)
-    y, u, dx, db = mat(305, 4), mat(300, 0), mat(309, 7), mat(304, 1)
+    x, b, gate, dy, du = mat(d + 1, 0), mat(d + 3, 1), mat(d, 3), mat(d + 7, 2), mat(d + 2, 5)
+    y, u, dx, db = mat(d + 5, 4), mat(d, 0), mat(d + 9, 7), mat(d + 4, 1)
     w = torch.randn(d, generator=gen).to(dt).cuda()
     _, _, rp, rq = moe.moe_block_norm(x, b, w, w, gate=gate, stats=True, y=y, u=u)
     args = (x.cpu(), b.cpu(), w.cpu(), w.cpu(), gate.cpu(), 1.0, EPS)
@@ -188,11 +193,12 @@ def test_operands_that_start_at_different_places(dt):
     check(dict(zip(("dx", "db", "dgate", "dpost", "dpre"), got)), plain.backward(dy.cpu(), du.cpu(), *args), T, z)
 
 
-def test_writes_nothing_else():
+@pytest.mark.parametrize("d", [203, 9003])
+def test_writes_nothing_else(d):
     """What lies around the rows of the outputs stays as it was."""
-    T, d, ld = 37, 203, 210
+    T, ld = 37, d + 7
     gen = torch.Generator().manual_seed(18)
-    x, b, gate, dy, du = (matrix(T, d, BF, gen, 205) for _ in range(5))
+    x, b, gate, dy, du = (matrix(T, d, BF, gen, d + 2) for _ in range(5))
     bufs = [torch.full((T + 2, ld), 7.0, device="cuda", dtype=BF) for _ in range(4)]
     y, u, dx, db = (v[1:-1, 3:3 + d] for v in bufs)
     _, _, rp, rq = moe.moe_block_norm(x, b, gate=gate, stats=True, y=y, u=u)

@@ -21,7 +21,8 @@ def rows_apart(got, want, row):
 
 @pytest.mark.parametrize("T,d,ld,dt,gate,norms,row", [
     (1500, 200, 200, BF, "full", (1, 1), 700), (700, 4096, 4096, BF, "row", (1, 1), 0), (700, 2048, 2048, FP, None, (1, 0), 699),
-    (1400, 1001, 1003, BF, "full", (1, 1), 700), (1000, 7167, 7167, BF, "full", (0, 1), 40)])
+    (1400, 1001, 1003, BF, "full", (1, 1), 700), (1000, 7167, 7167, BF, "full", (0, 1), 40),
+    (900, 12296, 12304, BF, "row", (1, 1), 899), (900, 12299, 12301, BF, "row", (1, 1), 8)])
 def test_a_row_that_never_comes(T, d, ld, dt, gate, norms, row):
     g = torch.Generator().manual_seed(d)
     x, b, dy, du = (matrix(T, d, dt, g, ld) for _ in range(4))

@@ -6,12 +6,12 @@
 namespace moe {
 namespace bn {
 
-bool ring_shape(Args &a, int cols, int per_thread, int max_threads, size_t fixed, size_t stage, size_t least,
-                int *groups) {
+bool ring_shape(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
+                size_t least, int *groups) {
     if (cols > max_threads * per_thread) return false;
     a.wpr = (cols + per_thread * 32 - 1) / (per_thread * 32);
     int g = std::min(std::max(1, max_threads / (32 * a.wpr)), a.wpr > 1 ? 15 : kMaxGroups);
-    g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
+    g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sms - 1) / sms));
     // as many groups as have a stage each, rather than fewer with two: they overlap as well
     // (4096 x 4096 fp32 with a full gate, one group of 14 KB rows against two: forward 79 / 58 us)
     const size_t most = std::max(least, stage);

@@ -69,6 +69,45 @@ struct GroupSum {
     }
 };
 
+// The same over the warps of a row group of both CTAs of a pair, which hold half of the row each: a
+// warp gives its value to both CTAs and arrives on both barriers (of 2 wpr arrivals), two of
+// each in turn. A wait that runs out (after the limits of the waits for rows, which the other
+// CTA may be in: its device has stopped) gives NaN, and no later one waits.
+struct PairCtl {
+    uint64_t bar[16][2];
+    float slots[16][2][32];
+};
+struct PairSum {
+    PairCtl *ctl;
+    int group, wg, wpr;
+    uint32_t rank;
+    int count = 0;
+    bool dead = false;
+    __device__ __forceinline__ float operator()(float v) {
+        const int lane = threadIdx.x & 31, k = count & 1;
+        const uint32_t parity = (count >> 1) & 1;
+        ++count;
+        v = warp_sum(v);
+        const uint32_t bar = ptx::smem_addr(&ctl->bar[group][k]);
+        if (lane < 2) {
+            const uint32_t to = ptx::smem_addr(&ctl->slots[group][k][rank * wpr + wg]);
+            ptx::st_cluster_f32(ptx::mapa(to, lane), v);
+            ptx::mbar_arrive_cluster(ptx::mapa(bar, lane));
+        }
+        if (!dead && !ptx::mbar_try_wait_cluster(bar, parity)) dead = !wait_long(bar, parity);
+        if (dead) return NAN;
+        return warp_sum(lane < 2 * wpr ? ctl->slots[group][k][lane] : 0.f);
+    }
+    static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        for (;;) {
+            const bool late = ptx::globaltimer_ns() - t0 > 4 * kWaitLimitNs;
+            if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+            if (late) return false;
+        }
+    }
+};
+
 // Packed sigmoid g of z, and h = 1 - g, for 16-bit results: with t = 2^(-z log2 e), g = 1 / (1 + t)
 // and h = t g, which does not cancel. (t infinite: g is 0, and the minimum with 1 takes the
 // place of infinity times 0. Where 1 + t is past 2^126, z < -87.3, g is 0.) The exponent's own
@@ -124,11 +163,11 @@ struct RingCtl {
 constexpr size_t kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
 
 // Warps a row, row groups (at most T / SMs rounded up, so that few rows spread over the SMs)
-// and ring stages of a block of at most max_threads; false where a stage of one group does not
-// fit. cols: columns that a row's vectors may reach over; `fixed` bytes a block, `stage` a
+// and ring stages of a block of at most max_threads, one of `sms`; false where a stage of one
+// group does not fit. cols: columns that a row's vectors may reach over; `fixed` bytes a block, `stage` a
 // stage, `least` a group's stages together.
-bool ring_shape(Args &a, int cols, int per_thread, int max_threads, size_t fixed, size_t stage, size_t least,
-                int *groups);
+bool ring_shape(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
+                size_t least, int *groups);
 // Rows of a block in hand: a group with one stage fetches its next row late, with two it need not.
 inline int rows_ahead(const Args &a, int groups) { return groups * std::min(a.stages, 2); }
 // Blocks of a launch of rows in `groups` a block.
@@ -220,13 +259,15 @@ struct Weights {
         const uint32_t n = (uint32_t)((ring_cols<V, SHIFT>(d) + V - 1) / V * V) * (RAW ? sizeof(T) : sizeof(float));
         return SHIFT ? (n + 127) / 128 * 128 : n;
     }
-    static __device__ __forceinline__ void fill(uint8_t *to, const void *w, int w32, const Part<T, V, SHIFT> &part) {
+    // (first: the column that the part starts with)
+    static __device__ __forceinline__ void fill(uint8_t *to, const void *w, int w32, const Part<T, V, SHIFT> &part,
+                                                int first = 0) {
         for (int v = threadIdx.x; v < part.nvec; v += blockDim.x) {
             float f[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = v * V + j - part.lead;
-                f[j] = c >= 0 && c < part.d ? load_w<T>(w, w32, c, 1.f) : 0.f;
+                f[j] = c >= 0 && c < part.d ? load_w<T>(w, w32, first + c, 1.f) : 0.f;
             }
             if constexpr (RAW) {
                 reinterpret_cast<uint4 *>(to)[v] = from_f32<T, V>(f);

@@ -15,11 +15,13 @@
 //
 // Measured, with the second kernel: 8192 x 7168 bf16 with a full gate 180 us (5.2 TB/s), 4096 x
 // 4096 bf16 with a row's gate 58 us, 8192 x 4096 fp32 without one 136 us (5.9 TB/s); rows of 7167
-// bf16, 315 us. One row group of 14 warps is all that the registers (the column sums and five values
-// an element between the sums) let an SM hold of 7168 columns, and it waits twice a row for a sum.
+// bf16, 315 us; 8192 x 14336 bf16 with a row's gate (pairs) 428 us (3.3 TB/s). One row group of
+// 14 warps is all that the registers (the column sums and five values an element between the sums)
+// let an SM hold of 7168 columns, and it waits twice a row for a sum.
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block_norm.cuh"
 
@@ -28,16 +30,25 @@ namespace bn {
 namespace {
 
 constexpr int kBwdThreads = 512, kBwdFewThreads = 448;  // most of a block with a ring
+constexpr size_t kPairCtl = (sizeof(PairCtl) + 127) / 128 * 128;
+// Columns of the first CTA of a pair: half of the row's vectors, rounded up (so that the second
+// half starts at the same place of 16 bytes as the row).
+template <int V>
+__host__ __device__ constexpr int half_columns(int d) { return ((d + V - 1) / V + 1) / 2 * V; }
+__device__ __forceinline__ bool sum_lost(const GroupSum &) { return false; }
+__device__ __forceinline__ bool sum_lost(const PairSum &s) { return s.dead; }
 
-// A block's row of partial sums from its groups' [groups][2][n], in order; the columns lie `lead`
-// elements on.
-__device__ __forceinline__ void add_groups(const Args &a, const float *sums, int n, int lead, int groups, bool lost) {
+// Row `row` of the partial sums from a block's groups' [groups][2][n], in order: columns at .. at +
+// cols - 1, which lie `lead` elements on.
+__device__ __forceinline__ void add_groups(const Args &a, const float *sums, int n, int lead, int cols, int at,
+                                           int row, int groups, bool lost) {
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) {
-        const float *at = sums + (c < a.d ? lead + c : n + lead + c - a.d);
-        float s = lost ? NAN : at[0];
-        for (int k = 1; k < groups; ++k) s += at[(size_t)2 * k * n];
-        a.part[(size_t)blockIdx.x * 2 * a.d + c] = s;
+    for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) {
+        const int m = c >= cols, i = c - m * cols;
+        const float *from = sums + m * n + lead + i;
+        float s = lost ? NAN : from[0];
+        for (int k = 1; k < groups; ++k) s += from[(size_t)2 * k * n];
+        a.part[((size_t)row * 2 + m) * a.d + at + i] = s;
     }
 }
 
@@ -153,7 +164,7 @@ __global__ void __launch_bounds__(1024) backward_rows_kernel(const Args a) {
             sums[(size_t)(2 * group + 1) * a.d + v * V + j] = dpre[i][j];
         }
     }
-    add_groups(a, sums, a.d, 0, groups, false);
+    add_groups(a, sums, a.d, 0, a.d, 0, blockIdx.x, groups, false);
 }
 
 template <typename T, int V, int NV>
@@ -169,8 +180,9 @@ cudaError_t backward_rows(Args a, int *P, cudaStream_t s) {
 }
 
 // Rows through a ring, as the forward's. A stage holds x, b (MODE 1, 2) and the gate (MODE 2),
-// then du and dy, where the call has them. MT: most threads.
-template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW, int MT>
+// then du and dy, where the call has them. MT: most threads. CTAS 2: a row is
+// halved over a pair of CTAs, each with half of its threads and memory.
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW, int MT, int CTAS>
 __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
@@ -178,20 +190,28 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     constexpr int P2 = V / 2;
     const int tpr = a.wpr * 32, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
     const int groups = blockDim.x / tpr, S = a.stages;
+    const uint32_t rank = CTAS == 2 ? ptx::cluster_ctarank() : 0;
+    const int unit = blockIdx.x / CTAS;
     const bool has_du = a.pre_norm, has_dy = a.dy != nullptr;
     const int K = MODE + 1 + has_du + has_dy;
-    const uint32_t row_bytes = ring_row_bytes<T, SHIFT>(a.d);
-    const uint32_t stage_bytes = K * row_bytes, w_bytes = Wt::bytes(a.d);
-    const int64_t stride = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + group;
-    if (SHIFT) row = blockIdx.x % kPhases + (int64_t)kPhases * (blockIdx.x / kPhases * groups + group);
+    // the columns of this CTA's part: the first or the second half of the vectors, or all
+    const int most = CTAS == 2 ? half_columns<V>(a.d) : a.d, first = rank * most, own = min(most, a.d - first);
+    const uint32_t row_bytes = ring_row_bytes<T, SHIFT>(most);
+    const uint32_t stage_bytes = K * row_bytes, w_bytes = Wt::bytes(most);
+    const int64_t stride = (int64_t)(gridDim.x / CTAS) * groups;
+    int64_t row = (int64_t)unit * groups + group;
+    if (SHIFT) row = unit % kPhases + (int64_t)kPhases * (unit / kPhases * groups + group);
     // (the rows of a block start at the same place: its first row's, there or not)
-    const Part<T, V, SHIFT> part(tpr, t, a.d, static_cast<T *>(a.dx) + blockIdx.x % kPhases * a.lddx);
-    uint8_t *post = ring_sh + kRingCtl, *pre = post + (MODE > 0 ? w_bytes : 0), *rings = pre + w_bytes;
+    const Part<T, V, SHIFT> part(tpr, t, own, static_cast<T *>(a.dx) + unit % kPhases * a.lddx);
+    PairCtl *pairs = reinterpret_cast<PairCtl *>(ring_sh + kRingCtl);
+    uint8_t *post = ring_sh + kRingCtl + (CTAS == 2 ? kPairCtl : 0), *pre = post + (MODE > 0 ? w_bytes : 0);
+    uint8_t *rings = pre + w_bytes;
     uint8_t *ring = rings + (size_t)group * S * stage_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, K);
+        if (CTAS == 2)
+            for (int k = 0; k < 2; ++k) ptx::mbar_init(ptx::smem_addr(&pairs->bar[group][k]), 2 * a.wpr);
         ptx::fence_barrier_init();
     }
     pdl_wait();
@@ -208,25 +228,31 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
             p = u ? a.du : a.dy;
             ld = u ? a.lddu : a.lddy;
         }
-        fetch_row<T, SHIFT>(ring + (size_t)s * stage_bytes + (size_t)k * row_bytes, p, ld, r, a.T, a.d, bar0 + 8 * s);
+        fetch_row<T, SHIFT>(ring + (size_t)s * stage_bytes + (size_t)k * row_bytes, static_cast<const T *>(p) + first,
+                            ld, r, a.T, own, bar0 + 8 * s);
     };
     __syncwarp();
     if (t < S * K && row + t / K * stride < a.T) fetch(row + t / K * stride, t / K, t % K);
-    if (MODE > 0) Wt::fill(post, a.post, a.w32, part);
-    Wt::fill(pre, a.pre, a.w32, part);
+    if (MODE > 0) Wt::fill(post, a.post, a.w32, part, first);
+    Wt::fill(pre, a.pre, a.w32, part, first);
     __syncthreads();
+    if (CTAS == 2) ptx::cluster_sync();  // both CTAs' barriers are there
 
     f32x2 dpost[NV][P2], dpre[NV][P2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < P2; ++j) dpost[i][j] = dpre[i][j] = 0;
-    auto off = [&](const void *p, int64_t ld) { return part.off(static_cast<const T *>(p) + blockIdx.x % kPhases * ld); };
+    auto off = [&](const void *p, int64_t ld) { return part.off(static_cast<const T *>(p) + unit % kPhases * ld); };
     const int ox = off(a.x, a.ldx), ob = MODE > 0 ? off(a.b, a.ldb) : 0, oz = MODE > 1 ? off(a.gate, a.ldg) : 0;
     const int ou = has_du ? off(a.du, a.lddu) : 0, oy = has_dy ? off(a.dy, a.lddy) : 0;
     const int odx = 0, odb = MODE > 0 ? off(a.db, a.lddb) : 0, odz = MODE > 1 ? off(a.dgate, a.lddg) : 0;
     const float inv_d = 1.f / (float)a.d;
-    GroupSum sum{ctl->slots, group * a.wpr, a.wpr, 1 + group};
+    using Sum = typename std::conditional<CTAS == 2, PairSum, GroupSum>::type;
+    Sum sum = [&] {
+        if constexpr (CTAS == 2) return PairSum{pairs, group, (int)(threadIdx.x >> 5) - group * a.wpr, a.wpr, rank};
+        else return GroupSum{ctl->slots, group * a.wpr, a.wpr, 1 + group};
+    }();
     int s = 0;
     uint32_t ph = 0;
     bool alive = true;
@@ -236,11 +262,14 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
         const float r_post = MODE > 0 && a.post_norm ? a.r_post[row] : 1.f, r_pre = has_du ? a.r_pre[row] : 0.f;
         alive = alive && ring_wait(bar0, S, s, ph, t < K);
         const uint8_t *stage = ring + (size_t)s * stage_bytes;
-        const uint8_t *px = stage + image_at<T, SHIFT>(a.x, a.ldx, row);
-        const uint8_t *pb = stage + row_bytes + (MODE > 0 ? image_at<T, SHIFT>(a.b, a.ldb, row) : 0);
-        const uint8_t *pz = stage + 2 * row_bytes + (MODE > 1 ? image_at<T, SHIFT>(a.gate, a.ldg, row) : 0);
-        const uint8_t *pu = stage + (MODE + 1) * row_bytes + image_at<T, SHIFT>(a.du, a.lddu, row);
-        const uint8_t *py = stage + (MODE + 1 + has_du) * row_bytes + image_at<T, SHIFT>(a.dy, a.lddy, row);
+        auto image = [&](const void *p, int64_t ld) {
+            return image_at<T, SHIFT>(static_cast<const T *>(p) + first, ld, row);
+        };
+        const uint8_t *px = stage + image(a.x, a.ldx);
+        const uint8_t *pb = stage + row_bytes + (MODE > 0 ? image(a.b, a.ldb) : 0);
+        const uint8_t *pz = stage + 2 * row_bytes + (MODE > 1 ? image(a.gate, a.ldg) : 0);
+        const uint8_t *pu = stage + (MODE + 1) * row_bytes + image(a.du, a.lddu);
+        const uint8_t *py = stage + (MODE + 1 + has_du) * row_bytes + image(a.dy, a.lddy);
         // (a row that did not come: NaN)
         const f32x2 scale = both(alive ? a.scale : NAN), rp = both(alive ? r_post : NAN), rq = both(r_pre);
         // yh, then f; g and 1 - g, then bh
@@ -277,8 +306,9 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
         }
         const f32x2 c1 = both(has_du ? -sum(pair_sum(q)) * inv_d : 0.f);
         q = alive ? 0 : both(NAN);
-        T *xrow = static_cast<T *>(a.dx) + row * a.lddx, *brow = static_cast<T *>(a.db) + row * a.lddb;
-        T *zrow = static_cast<T *>(a.dgate) + row * a.lddg;
+        T *xrow = static_cast<T *>(a.dx) + row * a.lddx + first;
+        T *brow = static_cast<T *>(a.db) + row * a.lddb + first;
+        T *zrow = static_cast<T *>(a.dgate) + row * a.lddg + first;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!part.has(i)) continue;
@@ -327,7 +357,7 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
         // every thread of the group is done with the stage
         if (t < K && alive && row + S * stride < a.T) fetch(row + S * stride, s, t);
         if (MODE > 0) {
-            if (MODE == 1 && t == 0 && a.gate != nullptr) static_cast<float *>(a.dgate)[row] = h_row * ss;
+            if (MODE == 1 && t == 0 && rank == 0 && a.gate != nullptr) static_cast<float *>(a.dgate)[row] = h_row * ss;
             const f32x2 c2 = both(a.post_norm ? -ss * inv_d : 0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -343,15 +373,19 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
             ph ^= 1;
         }
     }
+    if (CTAS == 2) {  // nothing of this CTA is on its way to the other, or back
+        __syncwarp();
+        ptx::cluster_sync();
+    }
     if (a.part == nullptr) return;
-    if constexpr (!SHIFT) {
+    if constexpr (!SHIFT && CTAS == 1) {
         bool ok[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) ok[i] = part.has(i);
         store_partials<V, NV>(a.part, a.d, groups, group, tpr, t, ok, dpost, dpre, rings, (size_t)S * stage_bytes, !alive);
     } else {
         // every thread is done with the last rows
-        const bool lost = __syncthreads_or(!alive);
+        const bool lost = __syncthreads_or(!alive || sum_lost(sum));
         float *sums = reinterpret_cast<float *>(rings);  // [groups][2][nvec V], `lead` columns on
         const int n = part.nvec * V;
 #pragma unroll
@@ -364,17 +398,19 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
                 at[n / 2 + j] = dpre[i][j];
             }
         }
-        add_groups(a, sums, n, part.lead, groups, lost);
+        add_groups(a, sums, n, part.lead, part.d, first, unit, groups, lost);
     }
 }
 
-template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
+template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW, int CTAS>
 bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
-    const size_t stage = (MODE + 1 + a.pre_norm + (a.dy != nullptr)) * ring_row_bytes<T, SHIFT>(a.d);
-    const size_t fixed = kRingCtl + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(a.d);
+    const int cols = CTAS == 2 ? half_columns<V>(a.d) : a.d;
+    const size_t stage = (MODE + 1 + a.pre_norm + (a.dy != nullptr)) * ring_row_bytes<T, SHIFT>(cols);
+    const size_t fixed =
+        kRingCtl + (CTAS == 2 ? kPairCtl : 0) + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(cols);
     // (a group's ring holds its fp32 sums in the end, [2][d] and up to two vectors more)
-    const size_t sums = 2 * ((size_t)a.d + 2 * V) * sizeof(float);
-    if (!ring_shape(a, ring_cols<V, SHIFT>(a.d), V * NV, threads, fixed, stage, sums, groups) ||
+    const size_t sums = 2 * ((size_t)cols + 2 * V) * sizeof(float);
+    if (!ring_shape(a, ring_cols<V, SHIFT>(cols), V * NV, threads, sm_count() / CTAS, fixed, stage, sums, groups) ||
         a.stages * stage < sums)
         return false;
     *smem = fixed + *groups * a.stages * stage;
@@ -389,8 +425,8 @@ bool backward_best(Args &a, int *threads, int *groups, size_t *smem) {
     int g = 0;
     size_t m = 0;
     *threads = kBwdThreads;
-    const bool fits = backward_shape<T, V, NV, MODE, SHIFT, RAW>(a, kBwdThreads, groups, smem);
-    if (fits && backward_shape<T, V, NV, MODE, SHIFT, RAW>(few, kBwdFewThreads, &g, &m) && 5 * g >= 4 * *groups) {
+    const bool fits = backward_shape<T, V, NV, MODE, SHIFT, RAW, 1>(a, kBwdThreads, groups, smem);
+    if (fits && backward_shape<T, V, NV, MODE, SHIFT, RAW, 1>(few, kBwdFewThreads, &g, &m) && 5 * g >= 4 * *groups) {
         a = few;
         *threads = kBwdFewThreads;
         *groups = g;
@@ -401,8 +437,8 @@ bool backward_best(Args &a, int *threads, int *groups, size_t *smem) {
 template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 cudaError_t backward_launch(const Args &a, int threads, int groups, size_t smem, int *P, cudaStream_t s) {
     const auto kernel = threads == kBwdFewThreads
-                            ? backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdFewThreads>
-                            : backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdThreads>;
+                            ? backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdFewThreads, 1>
+                            : backward_ring_kernel<T, V, NV, MODE, SHIFT, RAW, kBwdThreads, 1>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)kRingSmem);
     if (e != cudaSuccess) return e;
     *P = ring_grid<SHIFT>(a.T, groups, std::min(sm_count(), kLnPartials));
@@ -426,7 +462,18 @@ cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
             return backward_launch<T, V, NV, MODE, SHIFT, true>(raw, t, more, less, P, s);
         }
     }
-    return *fits ? backward_launch<T, V, NV, MODE, SHIFT, false>(planes, threads, groups, smem, P, s) : cudaSuccess;
+    if (*fits) return backward_launch<T, V, NV, MODE, SHIFT, false>(planes, threads, groups, smem, P, s);
+    // Rows that no SM holds: halves, over pairs of CTAs (8192 x 14336 bf16 with a row's gate
+    // 1580 / 428 us without and with, of 4096 x 14335 1849 / 265; where an SM holds one row, two
+    // halves of two rows in its place are slower: 8192 x 7168 bf16 with a full gate 180 / 235).
+    Args pair = a;
+    if (!backward_shape<T, V, NV, MODE, SHIFT, false, 2>(pair, kBwdThreads, &groups, &smem)) return cudaSuccess;
+    *fits = true;
+    const auto kernel = backward_ring_kernel<T, V, NV, MODE, SHIFT, false, kBwdThreads, 2>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)kRingSmem);
+    if (e != cudaSuccess) return e;
+    *P = ring_grid<SHIFT>(a.T, groups, std::min(sm_count() / 2, kLnPartials));
+    return launch_pairs(kernel, dim3(2 * *P), dim3(groups * pair.wpr * 32), smem, s, pair);
 }
 template <typename T, int SHIFT>
 cudaError_t backward_rings(const Args &a, int *P, bool *fits, cudaStream_t s) {
