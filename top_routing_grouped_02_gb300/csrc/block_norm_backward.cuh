@@ -14,8 +14,8 @@
 // rows by a second kernel, in order: no atomics, the result does not depend on timing.
 //
 // Measured, with the second kernel: 8192 x 7168 bf16 with a full gate 180 us (5.2 TB/s), 4096 x
-// 4096 bf16 with a row's gate 58 us, 8192 x 4096 fp32 without one 136 us (5.9 TB/s); rows of 7167
-// bf16, 315 us; 8192 x 14336 bf16 with a row's gate (pairs) 428 us (3.3 TB/s). One row group of
+// 4096 bf16 with a row's gate 45 us, 8192 x 4096 fp32 without one 138 us (5.8 TB/s); rows of 7167
+// bf16, 327 us; 8192 x 14336 bf16 with a row's gate (pairs) 393 us (3.6 TB/s). One row group of
 // 14 warps is all that the registers (the column sums and five values an element between the sums)
 // let an SM hold of 7168 columns, and it waits twice a row for a sum.
 #pragma once
@@ -209,16 +209,21 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     uint8_t *ring = rings + (size_t)group * S * stage_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
-        for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, K);
+        for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, K + 1);
         if (CTAS == 2)
             for (int k = 0; k < 2; ++k) ptx::mbar_init(ptx::smem_addr(&pairs->bar[group][k]), 2 * a.wpr);
         ptx::fence_barrier_init();
     }
     pdl_wait();
     pdl_trigger();
-    // row r of the stage's tensor k into stage s: a thread each
+    // row r of the stage's tensor k into stage s, or (k = K) its scalars: a thread each
     auto fetch = [&](int64_t r, int s, int k) {
         if (r == a.withheld) return;
+        if (k == K) {
+            fetch_scalars(ctl->scalars[group][s], has_du ? a.r_pre : nullptr,
+                          MODE > 0 && a.post_norm ? a.r_post : nullptr, MODE == 1 ? static_cast<const float *>(a.gate) : nullptr, r, bar0 + 8 * s);
+            return;
+        }
         const void *p = a.x;
         int64_t ld = a.ldx;
         if (MODE > 0 && k == 1) p = a.b, ld = a.ldb;
@@ -232,7 +237,8 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
                             ld, r, a.T, own, bar0 + 8 * s);
     };
     __syncwarp();
-    if (t < S * K && row + t / K * stride < a.T) fetch(row + t / K * stride, t / K, t % K);
+    if (t < S * (K + 1) && row + t / (K + 1) * stride < a.T)
+        fetch(row + t / (K + 1) * stride, t / (K + 1), t % (K + 1));
     if (MODE > 0) Wt::fill(post, a.post, a.w32, part, first);
     Wt::fill(pre, a.pre, a.w32, part, first);
     __syncthreads();
@@ -257,10 +263,11 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     uint32_t ph = 0;
     bool alive = true;
     for (; row < a.T; row += stride) {
+        alive = alive && ring_wait(bar0, S, s, ph, t <= K);
+        const float *scalars = ctl->scalars[group][s];
         float g_row = 1.f, h_row = 0.f;
-        if (MODE == 1 && a.gate != nullptr) sigmoid(static_cast<const float *>(a.gate)[row], g_row, h_row);
-        const float r_post = MODE > 0 && a.post_norm ? a.r_post[row] : 1.f, r_pre = has_du ? a.r_pre[row] : 0.f;
-        alive = alive && ring_wait(bar0, S, s, ph, t < K);
+        if (MODE == 1 && a.gate != nullptr) sigmoid(scalars[2], g_row, h_row);
+        const float r_post = MODE > 0 && a.post_norm ? scalars[1] : 1.f, r_pre = has_du ? scalars[0] : 0.f;
         const uint8_t *stage = ring + (size_t)s * stage_bytes;
         auto image = [&](const void *p, int64_t ld) {
             return image_at<T, SHIFT>(static_cast<const T *>(p) + first, ld, row);
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
         else if (a.wpr > 1) group_sync(1 + group, tpr);
         if (a.wpr == 1) __syncwarp();
         // every thread of the group is done with the stage
-        if (t < K && alive && row + S * stride < a.T) fetch(row + S * stride, s, t);
+        if (t <= K && alive && row + S * stride < a.T) fetch(row + S * stride, s, t);
         if (MODE > 0) {
             if (MODE == 1 && t == 0 && rank == 0 && a.gate != nullptr) static_cast<float *>(a.dgate)[row] = h_row * ss;
             const f32x2 c2 = both(a.post_norm ? -ss * inv_d : 0.f);

@@ -6,7 +6,7 @@
 // end.
 //
 // Measured, calls back to back: 8192 x 7168 bf16 with a full gate 103 us (5.7 TB/s), 4096 x 4096
-// bf16 with a row's gate 27 us (5.0 TB/s), 8192 x 4097 fp32 89 us (6.1 TB/s); rows of 7167 bf16
+// bf16 with a row's gate 24 us (5.5 TB/s), 8192 x 4097 fp32 89 us (6.1 TB/s); rows of 7167 bf16
 // 113 us, of 7168 with inputs that start elsewhere than outputs 153 us.
 #pragma once
 
@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(V * NV == 32 ? kFwdWideThreads : kFwdThreads, 
     extern __shared__ __align__(128) uint8_t ring_sh[];
     RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_sh);
     using Wt = Weights<T, V, SHIFT, RAW>;
-    constexpr int P2 = V / 2, K = MODE + 1;
+    constexpr int P2 = V / 2, K = MODE + 1 + (MODE == 1);  // (a stage's tensors, and a row's gate)
     const int tpr = a.wpr * 32, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
     const int groups = blockDim.x / tpr, S = a.stages;
     const uint32_t row_bytes = ring_row_bytes<T, SHIFT>(a.d);
-    const uint32_t stage_bytes = K * row_bytes, w_bytes = Wt::bytes(a.d);
+    const uint32_t stage_bytes = (MODE + 1) * row_bytes, w_bytes = Wt::bytes(a.d);
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + group;
     if (SHIFT) row = blockIdx.x % kPhases + (int64_t)kPhases * (blockIdx.x / kPhases * groups + group);
@@ -116,6 +116,10 @@ __global__ void __launch_bounds__(V * NV == 32 ? kFwdWideThreads : kFwdThreads, 
     // row r of tensor k (x, b, gate) into stage s: a thread each
     auto fetch = [&](int64_t r, int s, int k) {
         if (r == a.withheld) return;
+        if (MODE == 1 && k == 2) {
+            fetch_scalars(ctl->scalars[group][s], nullptr, nullptr, static_cast<const float *>(a.gate), r, bar0 + 8 * s);
+            return;
+        }
         fetch_row<T, SHIFT>(ring + (size_t)s * stage_bytes + (size_t)k * row_bytes, k == 0 ? a.x : k == 1 ? a.b : a.gate,
                             k == 0 ? a.ldx : k == 1 ? a.ldb : a.ldg, r, a.T, a.d, bar0 + 8 * s);
     };
@@ -134,9 +138,9 @@ __global__ void __launch_bounds__(V * NV == 32 ? kFwdWideThreads : kFwdThreads, 
     uint32_t ph = 0;
     bool alive = true;
     for (; row < a.T; row += stride) {
-        float g_row = 1.f, h_row;
-        if (MODE == 1 && a.gate != nullptr) sigmoid(static_cast<const float *>(a.gate)[row], g_row, h_row);
         alive = alive && ring_wait(bar0, S, s, ph, t < K);
+        float g_row = 1.f, h_row;
+        if (MODE == 1 && a.gate != nullptr) sigmoid(ctl->scalars[group][s][2], g_row, h_row);
         const uint8_t *stage = ring + (size_t)s * stage_bytes;
         const uint8_t *px = stage + image_at<T, SHIFT>(a.x, a.ldx, row);
         const uint8_t *pb = stage + row_bytes + (MODE > 0 ? image_at<T, SHIFT>(a.b, a.ldb, row) : 0);
