@@ -424,8 +424,9 @@ bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
     return true;
 }
 // The block of at most 448 threads is compiled for as many registers as that of 512 (128), but
-// runs 8 to 10 % faster where both have the same groups, or nearly (8192 x 7168 bf16 180 / 200
-// us, 4096 x 1024 19.7 / 21.4; 4096 x 4096, one group against two, 77 / 58).
+// runs up to 6 % faster where both have the same groups, or nearly (8192 x 7168 bf16 with a row's
+// gate 137 / 145 us, with a full one 182 / 179, 4096 x 1024 21.6 / 22.7; 4096 x 4096 with a row's,
+// one group against two, 58 / 45).
 template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 bool backward_best(Args &a, int *threads, int *groups, size_t *smem) {
     Args few = a;

@@ -6,7 +6,7 @@
 // end.
 //
 // Measured, calls back to back: 8192 x 7168 bf16 with a full gate 103 us (5.7 TB/s), 4096 x 4096
-// bf16 with a row's gate 24 us (5.5 TB/s), 8192 x 4097 fp32 89 us (6.1 TB/s); rows of 7167 bf16
+// bf16 with a row's gate 25 us (5.3 TB/s), 8192 x 4097 fp32 89 us (6.0 TB/s); rows of 7167 bf16
 // 113 us, of 7168 with inputs that start elsewhere than outputs 153 us.
 #pragma once
 
@@ -232,8 +232,7 @@ cudaError_t forward_launch(const Args &a, int groups, size_t smem, cudaStream_t 
     return launch_k(kernel, dim3(ring_grid<SHIFT>(a.T, groups, sm_count())), dim3(groups * a.wpr * 32), smem, s, a);
 }
 // 16-bit weights as they are where their planes leave room for fewer rows at a time (8192 x 7168
-// bf16 with a full gate, two groups with a stage each against two: 112 / 103 us; 4096 x 4096
-// with a row's gate, alike either way: 29.4 with planes, 32.6).
+// bf16 with a full gate, 113 / 103 us; 8192 x 2048 fp16, where both leave the same, 31.8 with planes, 32.2).
 template <typename T, int NV, int MODE, int SHIFT>
 cudaError_t forward_ring(const Args &a, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
@@ -253,14 +252,20 @@ cudaError_t forward_ring(const Args &a, bool *fits, cudaStream_t s) {
     }
     return *fits ? forward_launch<T, V, NV, MODE, SHIFT, false>(planes, groups, smem, s) : cudaSuccess;
 }
-// 16 elements a thread, 32 of long 16-bit rows (4096 x 4096 bf16 with a row's gate 29.4 / 27.1 us,
-// 8192 x 7167 with a full one 153 / 132; 4096 x 1024 7.3 / 8.0; fp32 4096 x 4096 62 / 73).
+// 16 elements a thread, or 32 (16-bit types): of long rows that start anywhere (8192 x 7167 bf16 with a
+// full gate 149 / 113 us, 8192 x 4097 with a row's 61 / 54; inputs that start elsewhere than
+// outputs, 8192 x 7168 with a full gate 179 / 153, 8192 x 4096 with a row's 70 / 77), and of rows
+// that 16 do not reach over. Aligned rows: 8192 x 2048 28.5 / 31.7 us, 4096 x 4096 28.5 / 32.3,
+// 8192 x 6144 with a row's gate 66 / 74 (4096 x 4096, 25.5 / 24.5).
 template <typename T, int MODE, int SHIFT>
 cudaError_t forward_length(const Args &a, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    if constexpr (sizeof(T) == 2)
-        if (a.d >= 2048) return forward_ring<T, 32 / V, MODE, SHIFT>(a, fits, s);
-    return forward_ring<T, 16 / V, MODE, SHIFT>(a, fits, s);
+    if (sizeof(T) == 4 || SHIFT == 0 || a.d < 2048) {
+        const cudaError_t e = forward_ring<T, 16 / V, MODE, SHIFT>(a, fits, s);
+        if (sizeof(T) == 4 || e != cudaSuccess || *fits) return e;
+    }
+    if constexpr (sizeof(T) == 2) return forward_ring<T, 32 / V, MODE, SHIFT>(a, fits, s);
+    return cudaSuccess;
 }
 template <typename T, int SHIFT>
 cudaError_t forward_rings(const Args &a, bool *fits, cudaStream_t s) {
