@@ -15,7 +15,7 @@
 //
 // Measured, with the second kernel: 8192 x 7168 bf16 with a full gate 180 us (5.2 TB/s), 4096 x
 // 4096 bf16 with a row's gate 45 us, 8192 x 4096 fp32 without one 138 us (5.8 TB/s); rows of 7167
-// bf16, 327 us; 8192 x 14336 bf16 with a row's gate (pairs) 393 us (3.6 TB/s). One row group of
+// bf16, 300 us; 8192 x 14336 bf16 with a row's gate (pairs) 393 us (3.6 TB/s). One row group of
 // 14 warps is all that the registers (the column sums and five values an element between the sums)
 // let an SM hold of 7168 columns, and it waits twice a row for a sum.
 #pragma once
@@ -452,7 +452,9 @@ cudaError_t backward_launch(const Args &a, int threads, int groups, size_t smem,
     *P = ring_grid<SHIFT>(a.T, groups, std::min(sm_count(), kLnPartials));
     return launch_k(kernel, dim3(*P), dim3(groups * a.wpr * 32), smem, s, a);
 }
-// (weights as in the forward)
+// Weights as in the forward; the fullest form of rows that start anywhere spills less without planes
+// (8192 x 7167 bf16 with a full gate 326 us with, 300 without, 4096 x 5001 135 / 129; with a
+// row's gate 214 / 220).
 template <typename T, int MODE, int SHIFT>
 cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T), NV = 16 / V;  // 16 elements a thread
@@ -465,7 +467,7 @@ cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
         int more = 0, t = 0;
         size_t less = 0;
         if (!a.w32 && backward_best<T, V, NV, MODE, SHIFT, true>(raw, &t, &more, &less) &&
-            (!*fits || rows_ahead(raw, more) > rows_ahead(planes, groups))) {
+            (!*fits || rows_ahead(raw, more) + (SHIFT && MODE == 2) > rows_ahead(planes, groups))) {
             *fits = true;
             return backward_launch<T, V, NV, MODE, SHIFT, true>(raw, t, more, less, P, s);
         }
