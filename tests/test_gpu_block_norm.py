@@ -305,8 +305,8 @@ def test_offsets_past_32_bits():
     assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
-def test_captured_calls_and_streams():
-    T, d = 300, 1024
+@pytest.mark.parametrize("T,d", [(300, 1024), (200, 9000), (90, 9001)])
+def test_captured_calls_and_streams(T, d):
     gen = torch.Generator().manual_seed(11)
     x, b, gate, dy = (matrix(T, d, BF, gen) for _ in range(4))
 
@@ -332,3 +332,26 @@ def test_captured_calls_and_streams():
     got = moe.moe_block_norm(x, b, gate=gate, stream=side)
     side.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_backward_passes_at_once():
+    """Calls on two streams, whose kernels run side by side."""
+    gen = torch.Generator().manual_seed(12)
+    sets = [[matrix(T, d, BF, gen) for _ in range(4)] for T, d in ((600, 12000), (700, 8960))]
+    stats = [moe.moe_block_norm(x, b, stats=True)[2:] for x, b, _, _ in sets]
+
+    def back(k):
+        x, b, dy, du = sets[k]
+        return moe.moe_block_norm_backward(dy, du, x, b, None, None, *stats[k])
+
+    want = [back(0), back(1)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((k, back(k)))
+    torch.cuda.synchronize()
+    assert all(p is q is None or torch.equal(p, q) for k, out in got for p, q in zip(out, want[k]))

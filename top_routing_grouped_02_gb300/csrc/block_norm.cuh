@@ -87,7 +87,8 @@ struct PairSum {
         const int lane = threadIdx.x & 31, k = count & 1;
         const uint32_t parity = (count >> 1) & 1;
         ++count;
-        v = warp_sum(v);
+        // (a warp that no longer waits may arrive early: with NaN, so that no sum it is in has a value)
+        v = warp_sum(dead ? NAN : v);
         const uint32_t bar = ptx::smem_addr(&ctl->bar[group][k]);
         if (lane < 2) {
             const uint32_t to = ptx::smem_addr(&ctl->slots[group][k][rank * wpr + wg]);
