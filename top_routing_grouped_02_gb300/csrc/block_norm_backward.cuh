@@ -15,7 +15,7 @@
 //
 // Measured, with the second kernel: 8192 x 7168 bf16 with a full gate 180 us (5.2 TB/s), 4096 x
 // 4096 bf16 with a row's gate 45 us, 8192 x 4096 fp32 without one 138 us (5.8 TB/s); rows of 7167
-// bf16, 300 us; 8192 x 14336 bf16 with a row's gate (pairs) 393 us (3.6 TB/s). One row group of
+// bf16, 300 us; 8192 x 14336 bf16 with a row's gate (pairs) 387 us (3.6 TB/s). One row group of
 // 14 warps is all that the registers (the column sums and five values an element between the sums)
 // let an SM hold of 7168 columns, and it waits twice a row for a sum.
 #pragma once
@@ -474,7 +474,7 @@ cudaError_t backward_ring(const Args &a, int *P, bool *fits, cudaStream_t s) {
     }
     if (*fits) return backward_launch<T, V, NV, MODE, SHIFT, false>(planes, threads, groups, smem, P, s);
     // Rows that no SM holds: halves, over pairs of CTAs (8192 x 14336 bf16 with a row's gate
-    // 1580 / 428 us without and with, of 4096 x 14335 1849 / 265; where an SM holds one row, two
+    // 1580 / 387 us without and with, 4096 x 14335 1849 / 260; where an SM holds one row, two
     // halves of two rows in its place are slower: 8192 x 7168 bf16 with a full gate 180 / 235).
     Args pair = a;
     if (!backward_shape<T, V, NV, MODE, SHIFT, false, 2>(pair, kBwdThreads, &groups, &smem)) return cudaSuccess;
