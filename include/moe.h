@@ -599,7 +599,8 @@ moe_status_t moe_ffn_backward(const void *dY, const void *X, const void *W1, con
  * X [T,k], W [k,n], residual, Y [T,n] of `type` (MOE_DTYPE_BF16 or MOE_DTYPE_F16), bias [n] of
  * btype (type or MOE_DTYPE_F32); bias and residual may be NULL. Dense, row-major and 16-byte
  * aligned; k and n multiples of 8 up to 2^20, any T >= 0 (0: nothing is enqueued). Sums and
- * the epilogue in fp32, Y rounded once. Y may be residual. Few tokens (up to 16, or 64 with n <= 2048)
+ * the epilogue in fp32, Y rounded once. Y may be residual; otherwise no output (Y, F; dX, dW, dbias
+ * below) shares memory with an operand or another output. Few tokens (up to 16, or 64 with n <= 2048)
  * take a kernel that streams the weights, more a tiled one: one kernel either way. The workspace is of
  * moe_linear_workspace_bytes(T, k, n, train) bytes, initialised by moe_ffn_workspace_init and
  * kept as those of the feed-forward calls are (either kind of call may use it, if it is large

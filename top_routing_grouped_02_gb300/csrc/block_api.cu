@@ -184,6 +184,24 @@ moe_status_t check_linear_ws(void *ws, size_t ws_bytes, int T, int k, int n, boo
 
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
 
+// A dense operand's bytes; none where p is NULL.
+struct Span {
+    uintptr_t at, end;
+    Span(const void *p, size_t bytes)
+        : at(reinterpret_cast<uintptr_t>(p)), end(p == nullptr ? at : at + bytes) {}
+};
+// Whether one of the outputs shares bytes with an operand or with another output.
+bool overlaps(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+    auto shares = [](const Span &a, const Span &b) { return a.at < b.end && b.at < a.end; };
+    for (const Span *o = out.begin(); o != out.end(); ++o) {
+        for (const Span &i : in)
+            if (shares(i, *o)) return true;
+        for (const Span *q = out.begin(); q != o; ++q)
+            if (shares(*q, *o)) return true;
+    }
+    return false;
+}
+
 bool all_aligned16(std::initializer_list<const void *> ps) {
     for (const void *p : ps)
         if (p == nullptr || !aligned(p, 16)) return false;
@@ -296,7 +314,14 @@ static moe_status_t linear_forward(const void *X, const void *W, const void *bia
     moe_status_t st = check_linear(T, k, n, act, type, btype);
     if (st != MOE_OK || T == 0) return st;
     if (!all_aligned16({X, W, Y}) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(F, 16) ||
-        (train && (F != nullptr) != (act != MOE_ACT_NONE)) || Y == X || Y == F)
+        (train && (F != nullptr) != (act != MOE_ACT_NONE)))
+        return MOE_ERR_INVALID_ARG;
+    // Y and F are stored while other tiles read their operands: of all of them, only the residual is
+    // read where it is overwritten
+    const size_t rows = T;
+    const Span y(Y, rows * n * 2), f(F, moe_ffn_saved_floats(T, n) * sizeof(float)), x(X, rows * k * 2),
+        w(W, (size_t)k * n * 2), b(bias, (size_t)n * size_of(btype)), r(residual, rows * n * 2);
+    if (overlaps({x, w, b}, {y, f}) || overlaps({r}, {f}) || (residual != Y && overlaps({r}, {y})))
         return MOE_ERR_INVALID_ARG;
     if ((st = check_linear_ws(ws, ws_bytes, T, k, n, train)) != MOE_OK) return st;
     if ((st = check_arch()) != MOE_OK) return st;
@@ -335,8 +360,11 @@ moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, c
         if (!all_aligned16({dY}) || !aligned(F, 16) || (dX != nullptr && !all_aligned16({W})) ||
             (dW != nullptr && !all_aligned16({X})))
             return MOE_ERR_INVALID_ARG;
-        for (const void *out : {dX, dW, dbias})
-            if (out != nullptr && (out == dY || out == X || out == W || out == F)) return MOE_ERR_INVALID_ARG;
+        const size_t rows = T;
+        const Span dy(dY, rows * n * 2), f(F, moe_ffn_saved_floats(T, n) * sizeof(float)), x(X, rows * k * 2),
+            wt(W, (size_t)k * n * 2), dx(dX, rows * k * 2), dw(dW, (size_t)k * n * 2),
+            db(dbias, (size_t)n * size_of(btype));
+        if (overlaps({dy, f, x, wt}, {dx, dw, db})) return MOE_ERR_INVALID_ARG;
         if ((st = check_linear_ws(ws, ws_bytes, T, k, n, true)) != MOE_OK) return st;
     }
     if ((st = check_arch()) != MOE_OK) return st;
