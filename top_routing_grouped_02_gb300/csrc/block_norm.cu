@@ -18,6 +18,7 @@ bool ring_shape(Args &a, int cols, int per_thread, int max_threads, int sms, siz
     while (g > 1 && fixed + g * most > kRingSmem) --g;
     if (fixed + g * most > kRingSmem) return false;
     a.stages = (int)std::min<size_t>((kRingSmem - fixed) / g / stage, kRingStages);
+    a.group_bytes = (uint32_t)std::max(least, a.stages * stage);
     *groups = g;
     return true;
 }

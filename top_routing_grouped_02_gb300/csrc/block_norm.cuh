@@ -27,6 +27,7 @@ struct Args {
     int post_norm, pre_norm;
     float scale, eps;
     int wpr, stages; // warps per row; ring stages per row group
+    uint32_t group_bytes;  // of a row group's ring
     int64_t withheld;  // self-test: this row's copies are never issued (-1: none)
     // backward
     const void *dy, *du;
@@ -167,7 +168,7 @@ constexpr size_t kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
 // Warps a row, row groups (at most T / SMs rounded up, so that few rows spread over the SMs)
 // and ring stages of a block of at most max_threads, one of `sms`; false where a stage of one
 // group does not fit. cols: columns that a row's vectors may reach over; `fixed` bytes a block, `stage` a
-// stage, `least` a group's stages together.
+// stage, `least` a group's ring (which stages alone may leave smaller).
 bool ring_shape(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
                 size_t least, int *groups);
 // Rows of a block in hand: a group with one stage fetches its next row late, with two it need not.

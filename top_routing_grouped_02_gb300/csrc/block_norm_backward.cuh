@@ -15,8 +15,9 @@
 //
 // Measured, with the second kernel: 8192 x 7168 bf16 with a full gate 180 us (5.2 TB/s), 4096 x
 // 4096 bf16 with a row's gate 45 us, 8192 x 4096 fp32 without one 138 us (5.8 TB/s); rows of 7167
-// bf16, 300 us; 8192 x 14336 bf16 with a row's gate (pairs) 387 us (3.6 TB/s). One row group of
-// 14 warps is all that the registers (the column sums and five values an element between the sums)
+// bf16, 300 us; 8192 x 14336 bf16 with a row's gate (pairs) 387 us (3.6 TB/s). The norm
+// alone, 8192 x 7168 bf16: 77 us (4.6 TB/s), with the residual's gradient 86 (5.4); 4096 x 4096 27 and 30.
+// One row group of 14 warps is all that the registers (the column sums and five values an element between the sums)
 // let an SM hold of 7168 columns, and it waits twice a row for a sum.
 #pragma once
 
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
     PairCtl *pairs = reinterpret_cast<PairCtl *>(ring_sh + kRingCtl);
     uint8_t *post = ring_sh + kRingCtl + (CTAS == 2 ? kPairCtl : 0), *pre = post + (MODE > 0 ? w_bytes : 0);
     uint8_t *rings = pre + w_bytes;
-    uint8_t *ring = rings + (size_t)group * S * stage_bytes;
+    uint8_t *ring = rings + (size_t)group * a.group_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, K + 1);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(MT, 1) backward_ring_kernel(const Args a) {
         bool ok[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) ok[i] = part.has(i);
-        store_partials<V, NV>(a.part, a.d, groups, group, tpr, t, ok, dpost, dpre, rings, (size_t)S * stage_bytes, !alive);
+        store_partials<V, NV>(a.part, a.d, groups, group, tpr, t, ok, dpost, dpre, rings, a.group_bytes, !alive);
     } else {
         // every thread is done with the last rows
         const bool lost = __syncthreads_or(!alive || sum_lost(sum));
@@ -415,12 +416,13 @@ bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
     const size_t stage = (MODE + 1 + a.pre_norm + (a.dy != nullptr)) * ring_row_bytes<T, SHIFT>(cols);
     const size_t fixed =
         kRingCtl + (CTAS == 2 ? kPairCtl : 0) + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(cols);
-    // (a group's ring holds its fp32 sums in the end, [2][d] and up to two vectors more)
-    const size_t sums = 2 * ((size_t)cols + 2 * V) * sizeof(float);
-    if (!ring_shape(a, ring_cols<V, SHIFT>(cols), V * NV, threads, sm_count() / CTAS, fixed, stage, sums, groups) ||
-        a.stages * stage < sums)
+    // (a group's ring holds its fp32 sums in the end, [2][d] and up to two vectors more, in whole
+    // lines: 128 bytes more than two stages of two 16-bit tensors, those of the norm alone. A rule that
+    // had the stages hold them sent its aligned rows past the ring: 8192 x 7168 bf16 615 / 77 us)
+    const size_t sums = (2 * ((size_t)cols + 2 * V) * sizeof(float) + 127) / 128 * 128;
+    if (!ring_shape(a, ring_cols<V, SHIFT>(cols), V * NV, threads, sm_count() / CTAS, fixed, stage, sums, groups))
         return false;
-    *smem = fixed + *groups * a.stages * stage;
+    *smem = fixed + (size_t)*groups * a.group_bytes;
     return true;
 }
 // The block of at most 448 threads is compiled for as many registers as that of 512 (128), but

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(V * NV == 32 ? kFwdWideThreads : kFwdThreads, 
     // (the rows of a block start at the same place: its first row's, there or not)
     const Part<T, V, SHIFT> part(tpr, t, a.d, static_cast<T *>(MODE > 0 ? a.y : a.u) + blockIdx.x % kPhases * (MODE > 0 ? a.ldy : a.ldu));
     uint8_t *post = ring_sh + kRingCtl, *pre = post + (MODE > 0 ? w_bytes : 0);
-    uint8_t *ring = pre + w_bytes + (size_t)group * S * stage_bytes;
+    uint8_t *ring = pre + w_bytes + (size_t)group * a.group_bytes;
     const uint32_t bar0 = ptx::smem_addr(&ctl->full[group][0]);
     if (t == 0) {
         for (int s = 0; s < S; ++s) ptx::mbar_init(bar0 + 8 * s, K);
@@ -221,7 +221,7 @@ bool forward_shape(Args &a, int *groups, size_t *smem) {
     const size_t fixed = kRingCtl + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(a.d);
     if (!ring_shape(a, ring_cols<V, SHIFT>(a.d), V * NV, V * NV == 32 ? kFwdWideThreads : kFwdThreads, sm_count(),
                     fixed, stage, stage, groups)) return false;
-    *smem = fixed + *groups * a.stages * stage;
+    *smem = fixed + (size_t)*groups * a.group_bytes;
     return true;
 }
 template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
