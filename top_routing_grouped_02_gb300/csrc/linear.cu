@@ -1,6 +1,8 @@
 // What a projection's gradients need beside the products of ffn.cu: dA = dY F, F = act'(A),
 // rounded to 16 bits as the tensor cores' operand, and the bias' gradient, the sums over rows
-// of dY F before that rounding.
+// of dY F before that rounding. The rounding is all that dX and dW lose but for their own: for bf16
+// they are 2.35e-3 off in the 2-norm where one rounding is 1.66e-3. (dA as the sum of two 16-bit
+// matrices would keep them at that, for twice the products: 504 us more of a 970 us step at 4096 x 4096 x 14336.)
 //
 // Bound by HBM: dY (16 bits) and F (fp32, in blocks of 32 x 32, the columns by fours: see
 // moe_ffn_forward_train) are read once and dA is written once, in the same pass as the sums. A
