@@ -623,7 +623,7 @@ moe_status_t moe_linear_forward_train(const void *X, const void *W, const void *
  * (the residual's gradient is dY). T = 0 gives a zero dW and dbias. ws: a workspace for
  * training. Three kernels: dA, dX, dW with dbias
  * (dX and dW in one where both are small; fewer where there is less to do; one more for dbias
- * without dW). Deterministic, but dX may differ in its last bit with and without dW. */
+ * without dW, or with T > 10240 and n <= 768). Deterministic, but dX may differ in its last bit with and without dW. */
 moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, const float *F, int T,
                                  int k, int n, moe_dtype_t type, moe_dtype_t btype, void *dX,
                                  void *dW, void *dbias, void *ws, size_t ws_bytes, void *stream);

@@ -383,10 +383,11 @@ moe_status_t moe_linear_backward(const void *dY, const void *X, const void *W, c
     float *sums = dbias != nullptr ? reinterpret_cast<float *>(at(ws, w.sums)) : nullptr;
     const bool b32 = btype == MOE_DTYPE_F32;
     cudaError_t e = launch_linear_grad(dY, F, T, n, f16, dA, sums, s);
-    if (e == cudaSuccess && dbias != nullptr && dW == nullptr)
+    const bool beside = dW != nullptr && linear_sum_rows(T, n) <= kLinearSumsBeside;
+    if (e == cudaSuccess && dbias != nullptr && !beside)
         e = launch_linear_bias(sums, T, n, f16, dbias, b32, s);
     if (e == cudaSuccess)
-        e = launch_linear_products(dA, X, W, T, k, n, f16, dX, dW, dbias, b32, sums,
+        e = launch_linear_products(dA, X, W, T, k, n, f16, dX, dW, beside ? dbias : nullptr, b32, sums,
                                    reinterpret_cast<float4 *>(at(ws, w.part)),
                                    reinterpret_cast<uint32_t *>(at(ws, kFfnTicketOffset)),
                                    static_cast<uint32_t *>(ws), s);

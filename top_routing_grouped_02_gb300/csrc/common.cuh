@@ -286,7 +286,13 @@ cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *tic
 cudaError_t launch_linear_tiled(const LinearCall &c, float *F, float4 *part, uint32_t *ticket, uint32_t *err,
                                 cudaStream_t s);
 // dX = dA W^T, dW = X^T dA; either may be NULL. With dW, dbias may be given: the sums of
-// launch_linear_grad's rows, beside the products.
+// launch_linear_grad's rows, beside the products: up to 320 rows of them. One warp a CTA adds a column's
+// rows one after the other, and with more it ends behind the products: launch_linear_bias takes them.
+// The whole backward, beside / by a kernel of its own, in us: 4096 x 1024 x 512 (128 rows) 33.1 / 37.1,
+// 8192 x 1024 x 256 (256) 37.1 / 40.0, 16384 x 1024 x 1024 (304) 94.5 / 98.2, 11000 x 1024 x 256 (344)
+// 47.9 / 49.2 and x 256 x 256 35.5 / 35.2, 13000 x 1024 x 256 (407) 57.1 / 51.7, 16384 x 2048 x 512 (512)
+// 100.7 / 87.6, 40000 x 256 x 256 (1216) 121 / 70.
+constexpr int kLinearSumsBeside = 320;
 cudaError_t launch_linear_products(const void *dA, const void *X, const void *W, int T, int k, int n, bool f16,
                                    void *dX, void *dW, void *dbias, bool bias32, const float *sums,
                                    float4 *part, uint32_t *ticket, uint32_t *err, cudaStream_t s);

@@ -10,8 +10,8 @@
 // rows x 4 groups of 8 columns: its loads of F are 128 consecutive bytes for each group, those
 // of dY 64 for each row, and the neighbouring warps take the rest of the rows' lines. Each
 // thread sums its columns over its rows, the 8 lanes of a column are added by shuffles and the
-// blocks' partial rows in order by the weight gradient's launch or (without it) a kernel of their
-// own: the result does not depend on timing.
+// blocks' partial rows in order by the weight gradient's launch or (without it, or many of them) a kernel
+// of their own: the result does not depend on timing.
 // Measured: 4096 x 14336 bf16 71 us (6.6 TB/s), 777 x 2728 6 us.
 #include <algorithm>
 

@@ -25,8 +25,8 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
 # Kernels each call enqueues; the gate/up GEMM launches one more (a row gather)
 # when it runs on CTA pairs, the router's backward one fewer when T is too
 # short to split into chunks, moe_ffn one for few tokens, moe_permute one kernel instead of three for
-# T <= 65536, and the whole-layer calls depend on the shape
-# (forward_launches).
+# T <= 65536, moe_linear_backward one to four (moe.h), the norms' backward one without weights'
+# gradients, and the whole-layer calls depend on the shape (forward_launches).
 LAUNCHES = {"moe_route": 2, "moe_route_logits": 1, "moe_permute": 3, "moe_gemm_gate_up": 1,
             "moe_gemm_gate_up_train": 1, "moe_backward_dh": 2, "moe_backward_dx": 2,
             "moe_backward_router": 5, "moe_backward_dw": 5,
