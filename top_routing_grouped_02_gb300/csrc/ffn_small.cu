@@ -553,6 +553,7 @@ stream_ffn_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant_
 
 template <int NT, bool LINEAR, bool LAST>
 cudaError_t launch_nt(const SmallMaps &maps, SmallArgs args, int grid, cudaStream_t s) {
+    static_assert(!LAST || (LINEAR && NT == 16), "the last warp joins a few tokens' projection alone");
     constexpr size_t kSmem = Geo<NT>::kSmem;
     args.idesc = idesc(args.f16 != 0, 128, NT, true, false);
     const cudaError_t e =
@@ -563,7 +564,7 @@ cudaError_t launch_nt(const SmallMaps &maps, SmallArgs args, int grid, cudaStrea
     return launch_together(stream_ffn_kernel<NT, LINEAR, LAST>, dim3(grid), dim3(kThreads), kSmem, s, maps, args);
 }
 
-int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+constexpr int padded_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 // A product whose units are 32 KB of weights, on one CTA per SM, fewer where a run
 // would be under two units (then the joining costs more than the shorter runs save).
@@ -649,11 +650,12 @@ cudaError_t launch_linear_stream(const LinearCall &c, float *part, uint32_t *tic
     // 1024 6.4 / 8.3 (24.9 and 5.8 since); eight tokens, two round trips, 4096 x 4096 21.1 / 16.5.
     constexpr int kLastTokens = 4;
     const int parts = (grid + a.p[1].tiles - 1) / a.p[1].tiles + 1;
-    const bool last = c.T <= kLastTokens && parts <= 16;
+    static_assert(padded_tokens(kLastTokens) == 16, "");
+    if (c.T <= kLastTokens && parts <= 16) return launch_nt<16, true, true>(m, a, grid, s);
     switch (nt) {
-        case 16: return last ? launch_nt<16, true, true>(m, a, grid, s) : launch_nt<16, true, false>(m, a, grid, s);
-        case 32: return last ? launch_nt<32, true, true>(m, a, grid, s) : launch_nt<32, true, false>(m, a, grid, s);
-        default: return last ? launch_nt<64, true, true>(m, a, grid, s) : launch_nt<64, true, false>(m, a, grid, s);
+        case 16: return launch_nt<16, true, false>(m, a, grid, s);
+        case 32: return launch_nt<32, true, false>(m, a, grid, s);
+        default: return launch_nt<64, true, false>(m, a, grid, s);
     }
 }
 
