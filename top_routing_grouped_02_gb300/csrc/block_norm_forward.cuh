@@ -253,14 +253,17 @@ cudaError_t forward_ring(const Args &a, bool *fits, cudaStream_t s) {
     return *fits ? forward_launch<T, V, NV, MODE, SHIFT, false>(planes, groups, smem, s) : cudaSuccess;
 }
 // 16 elements a thread, or 32 (16-bit types): of long rows that start anywhere (8192 x 7167 bf16 with a
-// full gate 149 / 113 us, 8192 x 4097 with a row's 61 / 54; inputs that start elsewhere than
-// outputs, 8192 x 7168 with a full gate 179 / 153, 8192 x 4096 with a row's 70 / 77), and of rows
-// that 16 do not reach over. Aligned rows: 8192 x 2048 28.5 / 31.7 us, 4096 x 4096 28.5 / 32.3,
-// 8192 x 6144 with a row's gate 66 / 74 (4096 x 4096, 25.5 / 24.5).
+// full gate 149 / 113 us, 8192 x 4097 with a row's 61 / 54), and of rows that 16 do not reach over.
+// Where inputs start elsewhere than outputs behind a block, 16 as long as a block holds two rows so
+// (8192 x 2048 with a row's gate 43.7 / 43.2, 8192 x 4096 70 / 77, with a full one 76 / 91, 4096 x 6144
+// 56 / 67 and 61 / 69; 4096 x 7168, one row, 87 / 71 and 93 / 85, 8192 x 7168 179 / 153; the norm
+// alone, 8192 x 2560, 25.6 / 22.5, 4096 x 7168 42.5 / 30.1). Aligned rows: 8192 x 2048 28.5 / 31.7 us,
+// 4096 x 4096 28.5 / 32.3, 8192 x 6144 with a row's gate 66 / 74 (4096 x 4096, 25.5 / 24.5).
 template <typename T, int MODE, int SHIFT>
 cudaError_t forward_length(const Args &a, bool *fits, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    if (sizeof(T) == 4 || SHIFT == 0 || a.d < 2048) {
+    const bool two_rows = SHIFT == 2 && MODE > 0 && 2 * ring_cols<V, SHIFT>(a.d) <= kFwdThreads * 16;
+    if (sizeof(T) == 4 || SHIFT == 0 || a.d < 2048 || two_rows) {
         const cudaError_t e = forward_ring<T, 16 / V, MODE, SHIFT>(a, fits, s);
         if (sizeof(T) == 4 || e != cudaSuccess || *fits) return e;
     }
