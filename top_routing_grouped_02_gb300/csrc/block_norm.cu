@@ -6,20 +6,18 @@
 namespace moe {
 namespace bn {
 
-bool ring_shape(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
-                size_t least, int *groups) {
-    if (cols > max_threads * per_thread) return false;
-    a.wpr = (cols + per_thread * 32 - 1) / (per_thread * 32);
-    int g = std::min(std::max(1, max_threads / (32 * a.wpr)), a.wpr > 1 ? 15 : kMaxGroups);
-    g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sms - 1) / sms));
+bool shape_of(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
+              size_t least, int *groups) {
     // as many groups as have a stage each, rather than fewer with two: they overlap as well
     // (4096 x 4096 fp32 with a full gate, one group of 14 KB rows against two: forward 79 / 58 us)
-    const size_t most = std::max(least, stage);
-    while (g > 1 && fixed + g * most > kRingSmem) --g;
-    if (fixed + g * most > kRingSmem) return false;
-    a.stages = (int)std::min<size_t>((kRingSmem - fixed) / g / stage, kRingStages);
-    a.group_bytes = (uint32_t)std::max(least, a.stages * stage);
-    *groups = g;
+    Ring r;
+    if (!ring_shape({a.T, cols, per_thread, max_threads, kMaxGroups, kRingStages, sms, fixed, 0, stage,
+                     std::max(least, stage)}, &r))
+        return false;
+    a.wpr = r.wpr;
+    a.stages = r.stages;
+    a.group_bytes = (uint32_t)std::max(least, r.stages * stage);
+    *groups = r.groups;
     return true;
 }
 

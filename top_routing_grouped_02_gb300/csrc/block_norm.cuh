@@ -1,5 +1,5 @@
-// The norms around a block in one pass over the stream (block_norm.cu, its gradients in
-// block_norm_backward.cu). For a row of d elements,
+// The norms around a block in one pass over the stream (block_norm_forward.cuh, its gradients in
+// block_norm_backward.cuh). For a row of d elements,
 //   bh = b r_post,  r_post = 1 / sqrt(mean(b^2) + eps)   (1 without the post norm)
 //   n  = post bh
 //   y  = scale x + g n,   g = sigmoid(gate) of the row or the element, or 1
@@ -157,7 +157,6 @@ __device__ __forceinline__ void sigmoid2(f32x2 z, f32x2 &g, f32x2 &h) {
 // elsewhere its vectors are shifted out of two neighbouring blocks, and another output's elements
 // are stored one by one.
 constexpr int kRingStages = 2, kMaxGroups = 28, kPhases = 8;
-constexpr size_t kRingSmem = 224 * 1024;
 struct RingCtl {
     uint64_t full[kMaxGroups][kRingStages];
     float slots[2][32];
@@ -165,12 +164,11 @@ struct RingCtl {
 };
 constexpr size_t kRingCtl = (sizeof(RingCtl) + 127) / 128 * 128;
 
-// Warps a row, row groups (at most T / SMs rounded up, so that few rows spread over the SMs)
-// and ring stages of a block of at most max_threads, one of `sms`; false where a stage of one
-// group does not fit. cols: columns that a row's vectors may reach over; `fixed` bytes a block, `stage` a
-// stage, `least` a group's ring (which stages alone may leave smaller).
-bool ring_shape(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
-                size_t least, int *groups);
+// Warps a row, row groups and ring stages of a block of at most max_threads, one of `sms`; false
+// where a stage of one group does not fit. cols: columns that a row's vectors may reach over; `fixed` bytes
+// a block, `stage` a stage, `least` a group's ring (which stages alone may leave smaller).
+bool shape_of(Args &a, int cols, int per_thread, int max_threads, int sms, size_t fixed, size_t stage,
+              size_t least, int *groups);
 // Rows of a block in hand: a group with one stage fetches its next row late, with two it need not.
 inline int rows_ahead(const Args &a, int groups) { return groups * std::min(a.stages, 2); }
 // Blocks of a launch of rows in `groups` a block.

@@ -420,7 +420,7 @@ bool backward_shape(Args &a, int threads, int *groups, size_t *smem) {
     // lines: 128 bytes more than two stages of two 16-bit tensors, those of the norm alone. A rule that
     // had the stages hold them sent its aligned rows past the ring: 8192 x 7168 bf16 615 / 77 us)
     const size_t sums = (2 * ((size_t)cols + 2 * V) * sizeof(float) + 127) / 128 * 128;
-    if (!ring_shape(a, ring_cols<V, SHIFT>(cols), V * NV, threads, sm_count() / CTAS, fixed, stage, sums, groups))
+    if (!shape_of(a, ring_cols<V, SHIFT>(cols), V * NV, threads, sm_count() / CTAS, fixed, stage, sums, groups))
         return false;
     *smem = fixed + (size_t)*groups * a.group_bytes;
     return true;

@@ -219,7 +219,7 @@ template <typename T, int V, int NV, int MODE, int SHIFT, bool RAW>
 bool forward_shape(Args &a, int *groups, size_t *smem) {
     const size_t stage = (MODE + 1) * ring_row_bytes<T, SHIFT>(a.d);
     const size_t fixed = kRingCtl + (MODE > 0 ? 2 : 1) * Weights<T, V, SHIFT, RAW>::bytes(a.d);
-    if (!ring_shape(a, ring_cols<V, SHIFT>(a.d), V * NV, V * NV == 32 ? kFwdWideThreads : kFwdThreads, sm_count(),
+    if (!shape_of(a, ring_cols<V, SHIFT>(a.d), V * NV, V * NV == 32 ? kFwdWideThreads : kFwdThreads, sm_count(),
                     fixed, stage, stage, groups)) return false;
     *smem = fixed + (size_t)*groups * a.group_bytes;
     return true;

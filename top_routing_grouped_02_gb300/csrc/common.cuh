@@ -305,7 +305,7 @@ cudaError_t launch_linear_grad(const void *dY, const float *F, int T, int n, boo
 cudaError_t launch_linear_bias(const float *sums, int T, int n, bool f16, void *dbias, bool bias32,
                                cudaStream_t s);
 
-// The norms around a block (block_norm.cu, block_norm_backward.cu); w32: post, pre and their
+// The norms around a block (block_norm.cu, block_norm_forward.cuh, block_norm_backward.cuh); w32: post, pre and their
 // gradients are fp32. gate_rows: gate and dgate are [T,d] of `type`, else fp32, one a row.
 constexpr int kBlockNormMaxWidth = 16384;
 struct Matrix {

@@ -24,8 +24,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
-#include "elem.cuh"
+#include "rows.cuh"
 
 namespace moe {
 namespace {
@@ -33,12 +32,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTargetWarps = 48;  // an SM
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 
 // The rows of a token's slots: every lane has all of them, -1 where a slot has none.
 template <int KU>

@@ -1,5 +1,5 @@
-// Element types of the row-wise operators (layer norm, dropout): vectors of V
-// elements as one raw register value, converted to and from fp32.
+// Element types of the sub-block operators (norms, dropout, dispatch and combine, dense block and
+// projections): packed pairs and vectors of V elements as one raw register value, converted to and from fp32.
 #pragma once
 
 #include <cuda_bf16.h>

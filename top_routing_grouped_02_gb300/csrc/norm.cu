@@ -659,29 +659,20 @@ __global__ void __launch_bounds__(256) ln_weight_wide_kernel(const LnArgs a) {
 
 // ------------------------------------------------------------ host side --
 
-// Vector length (elements) that divides d and every row stride and suits the
-// pointers' alignment.
-int row_groups(int wpr, int threads) { return std::max(1, threads / (32 * wpr)); }
-
-// Row groups and ring stages of a block of at most max_threads threads (one block
-// per SM), with at most T / SMs rounded up groups so that few rows spread over the
-// SMs. False where `least` stages of one group do not fit the shared memory. (SHIFT fetches
-// a group's next row as soon as all of its threads are done with the last, so one stage
-// will do, and more groups with one beat fewer with two: 8192 x 7167 bf16, one group with
-// two stages against two with one, backward 174 / 141 us; three against four groups,
-// forward 69 / 65. Otherwise a stage is free only at the next row's barrier.)
-constexpr size_t kRingSmem = 224 * 1024;
-// `fixed` bytes a block, `extra` a group, `stage` a stage.
-bool ring_shape(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t extra, size_t stage,
-                int least, int *groups) {
-    if (a.d > max_threads * per_thread) return false;
-    a.wpr = (a.d + per_thread * 32 - 1) / (per_thread * 32);
-    int g = std::min(row_groups(a.wpr, max_threads), a.wpr > 1 ? 15 : kMaxGroups);
-    g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (a.T + sm_count() - 1) / sm_count()));
-    while (g > 1 && fixed + g * (extra + least * stage) > kRingSmem) --g;
-    if (fixed + g * (extra + least * stage) > kRingSmem) return false;
-    a.stages = (int)std::min<size_t>(((kRingSmem - fixed) / g - extra) / stage, kRingStages);
-    *groups = g;
+// False where `least` stages of one group do not fit the shared memory. (SHIFT fetches a group's next
+// row as soon as all of its threads are done with the last, so one stage will do, and more
+// groups with one beat fewer with two: 8192 x 7167 bf16, one group with two stages against
+// two with one, backward 174 / 141 us; three against four groups, forward 69 / 65. Otherwise a
+// stage is free only at the next row's barrier.) `fixed` bytes a block, `extra` a group, `stage` a stage.
+bool shape_of(LnArgs &a, int per_thread, int max_threads, size_t fixed, size_t extra, size_t stage,
+              int least, int *groups) {
+    Ring r;
+    if (!ring_shape({a.T, a.d, per_thread, max_threads, kMaxGroups, kRingStages, sm_count(), fixed, extra, stage,
+                     least * stage}, &r))
+        return false;
+    a.wpr = r.wpr;
+    a.stages = r.stages;
+    *groups = r.groups;
     return true;
 }
 
@@ -694,7 +685,7 @@ cudaError_t forward_ring(LnArgs a, bool *fits, cudaStream_t s) {
     int groups;
     const size_t stage = SHIFT ? image_bytes(a.d, sizeof(T)) : (size_t)a.d * sizeof(T);
     const size_t fixed = kRingCtl + 2 * plane_bytes<V>(a.d);
-    *fits = ring_shape(a, V * NV, kFwdThreads, fixed, SHIFT ? stage : 0, stage, SHIFT ? 1 : 2, &groups);
+    *fits = shape_of(a, V * NV, kFwdThreads, fixed, SHIFT ? stage : 0, stage, SHIFT ? 1 : 2, &groups);
     if (!*fits) return cudaSuccess;
     const cudaError_t e = ensure_dynamic_smem(
         reinterpret_cast<const void *>(ln_forward_ring_kernel<T, V, NV, SHIFT>), (int)kRingSmem);
@@ -711,7 +702,7 @@ cudaError_t backward_ring(LnArgs a, int *P, bool *fits, cudaStream_t s) {
     const size_t stage = row * (a.dres != nullptr ? 3 : 2), fixed = kRingCtl + plane_bytes<V>(a.d);
     // (a group's ring holds its [2][d] fp32 sums in the end)
     const int least = SHIFT && stage + row >= 2 * plane_bytes<V>(a.d) ? 1 : 2;
-    *fits = ring_shape(a, V * NV, kBwdRingThreads, fixed, SHIFT ? row : 0, stage, least, &groups);
+    *fits = shape_of(a, V * NV, kBwdRingThreads, fixed, SHIFT ? row : 0, stage, least, &groups);
     if (!*fits) return cudaSuccess;
     const cudaError_t e = ensure_dynamic_smem(
         reinterpret_cast<const void *>(ln_backward_ring_kernel<T, V, NV, SHIFT>), (int)kRingSmem);

@@ -2,6 +2,8 @@
 // warps, weights, rings of rows in shared memory and the alignment of operands.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "elem.cuh"
 #include "ptx.cuh"
@@ -25,6 +27,33 @@ __device__ __forceinline__ float load_w(const void *w, int w32, int c, float non
 }
 
 // ---- rings of rows, filled by bulk copies
+
+// The shape of a block with one ring for each of its row groups, one block per SM.
+struct Ring {
+    int wpr, groups, stages;  // warps a row; row groups; stages of each
+};
+struct RingNeeds {
+    int64_t T;
+    int cols, per_thread;  // columns that a row's vectors may reach over; elements a thread
+    int max_threads, max_groups, max_stages, sms;
+    size_t fixed, extra;   // bytes a block; bytes a group beside its ring
+    size_t stage, least;   // bytes a stage; of a group's ring at least (one stage or more)
+};
+constexpr size_t kRingSmem = 224 * 1024;
+// As many groups as have `least` each, at most T / SMs rounded up, so that few rows spread over the
+// SMs; then as many stages as there is room for. False where one group does not fit.
+inline bool ring_shape(const RingNeeds &n, Ring *r) {
+    if (n.cols > n.max_threads * n.per_thread) return false;
+    r->wpr = (n.cols + n.per_thread * 32 - 1) / (n.per_thread * 32);
+    // (named barriers: 15)
+    int g = std::min(std::max(1, n.max_threads / (32 * r->wpr)), r->wpr > 1 ? 15 : n.max_groups);
+    g = (int)std::min<int64_t>(g, std::max<int64_t>(1, (n.T + n.sms - 1) / n.sms));
+    while (g > 1 && n.fixed + g * (n.extra + n.least) > kRingSmem) --g;
+    if (n.fixed + g * (n.extra + n.least) > kRingSmem) return false;
+    r->groups = g;
+    r->stages = (int)std::min<size_t>(((kRingSmem - n.fixed) / g - n.extra) / n.stage, n.max_stages);
+    return true;
+}
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
