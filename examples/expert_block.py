@@ -7,7 +7,8 @@
 i.e. the experts are two projections with biases each (moe_linear), their rows come sorted by
 expert (moe_route, moe_permute, moe_dispatch), go back weighted (moe_combine_weighted), and one
 pass adds them to the stream behind a norm and a gate of the row and makes the next block's
-input (moe_block_norm). `forward` and `backward` are a training step of it.
+input (moe_block_norm). `forward` and `backward` are a training step of it, for some tens of experts: each
+one's projections are launches of their own, over runs of rows that the host reads.
 
     python examples/expert_block.py [--tokens 1024] [--steps 5]
 """
