@@ -11,7 +11,7 @@ class _Params(ctypes.Structure):
 
 
 def _ok(status):
-    assert status == 0, f"driver status {status}"
+    assert status == 0, f"CUDA status {status}"
 
 
 def kernels(call, stream):
